@@ -339,6 +339,14 @@ nq_status nq_ste_set_params(nq_ste_t h, const float* U, const float* V, const fl
 nq_status nq_ste_step(nq_ste_t h, const float* X, int64_t ldx, const float* Y, int64_t ldy,
                       const int32_t* rows, int64_t T, float lr, void* stream);
 
+/* nq_ste_step with the inputs given as their 8-bit checkpoint (see
+ * nq_act8_quantize: codes with row stride ldc >= n, exps with lde >=
+ * ceil(n/32)): the same step, bit for bit, as on the float32 values that the
+ * checkpoint stands for. */
+nq_status nq_ste_step_act8(nq_ste_t h, const int8_t* codes, int64_t ldc, const uint8_t* exps,
+                           int64_t lde, const float* Y, int64_t ldy, const int32_t* rows,
+                           int64_t T, float lr, void* stream);
+
 /* The loss of the last step's batch before its update (host double); waits
  * for `stream`. */
 nq_status nq_ste_last_loss(nq_ste_t h, double* loss, void* stream);
@@ -347,6 +355,106 @@ nq_status nq_ste_last_loss(nq_ste_t h, double* loss, void* stream);
  * Their signs packed by nq_pack_signs are the refined binary factors. */
 nq_status nq_ste_get_params(nq_ste_t h, float* U, float* V, float* s1, float* s2, void* stream);
 nq_status nq_ste_destroy(nq_ste_t h);
+
+/* ---- tuning a packed model ----
+ * The digest's stage 3 (方法步骤详情) freezes the binary factors and tunes the
+ * scales of the whole model against a loss on its outputs. What follows is
+ * what one layer of that needs beside nq_binary_matmul: its input kept in 8
+ * bits for the backward pass, and its gradient from there. */
+
+/* Element types of tensors that are not always float32. */
+typedef enum nq_dtype { NQ_F32 = 0, NQ_BF16 = 1, NQ_F16 = 2 } nq_dtype;
+
+/* 8-bit checkpoint of X (device, rows x cols of type `dtype`, row stride
+ * ldx >= cols elements): in each row, 32 consecutive columns (fewer at the
+ * end) share the step 2^e, e the least integer with max|x| <= 127 2^e,
+ * clamped to -126 .. 121 (to at most 9 for NQ_F16: the values stay finite in
+ * X's type);
+ *   codes (rows x cols int8, row stride ldc >= cols) = x / 2^e rounded to
+ *     even, in -127 .. 127;
+ *   exps (rows x ceil(cols/32) uint8, row stride lde) = e + 127.
+ * A group holding a NaN or an infinity gets exps 255 and codes 0. One kernel,
+ * no allocation; rows == 0 or cols == 0 is a no-op. */
+nq_status nq_act8_quantize(const void* X, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx,
+                           int8_t* codes, int64_t ldc, uint8_t* exps, int64_t lde, void* stream);
+
+/* X (device, rows x cols of `dtype`, row stride ldx) = codes 2^(exps - 127),
+ * NaN where exps is 255. Exact in float32 and bfloat16; rounded to even in
+ * float16 (exact for a checkpoint of float16 values). */
+nq_status nq_act8_dequantize(const int8_t* codes, int64_t ldc, const uint8_t* exps, int64_t lde,
+                             int64_t rows, int64_t cols, void* X, int32_t dtype, int64_t ldx,
+                             void* stream);
+
+/* steps (device, rows x groups float32, row stride lds) = 2^(exps - 127), NaN
+ * where exps is 255. */
+nq_status nq_act8_steps(const uint8_t* exps, int64_t lde, int64_t rows, int64_t groups,
+                        float* steps, int64_t lds, void* stream);
+
+/* Gradient of nq_binary_matmul's layer Y = X W^T, W = diag(s1) S_U S_V^T
+ * diag(s2), with respect to X, s1 and s2, the signs held. X is given as its
+ * 8-bit checkpoint (T x n; codes, ldc, exps, lde as above), and with
+ * a = s2 * x, p = S_V^T a, q = S_U p per token:
+ *   ds1 (m) = sum_t dY_t * q_t,
+ *   dX (T x n, row stride lddx, dY's type; nullable) = s2 * da,
+ *   ds2 (n) = sum_t da_t * x_t,   da = S_V (S_U^T (s1 * dY_t)).
+ * dY (device): T x m of `dtype`, row stride lddy >= m. Signs (device, uint32
+ * words): U_bits m x ldu, Ut_bits r x ldut (its transpose), V_bits n x ldv,
+ * Vt_bits r x ldvt, each as nq_lbadmm_run and nq_transpose_signs write them.
+ * ds1, ds2 float32, written (not added to). T == 0 writes zeros there.
+ * The left factors of the products are taken in fixed point, 24 bits of each
+ * row's largest value, and summed exactly; a row of X or dY with a NaN or an
+ * infinity gives NaN. Results do not depend on any order of summing but that
+ * of ds1 and ds2 over tokens, which is fixed. All on `stream`, no allocation;
+ * work: nq_binary_matmul_backward_work_bytes(T, m, n, r) bytes of device
+ * scratch, 16-byte aligned. m, n, r in 1 .. 2^21. */
+nq_status nq_binary_matmul_backward(const uint32_t* U_bits, int64_t ldu, const uint32_t* Ut_bits,
+                                    int64_t ldut, const uint32_t* V_bits, int64_t ldv,
+                                    const uint32_t* Vt_bits, int64_t ldvt, int64_t m, int64_t n,
+                                    int64_t r, const float* s1, const float* s2,
+                                    const int8_t* codes, int64_t ldc, const uint8_t* exps,
+                                    int64_t lde, int64_t T, const void* dY, int32_t dtype,
+                                    int64_t lddy, void* dX, int64_t lddx, float* ds1, float* ds2,
+                                    void* work, void* stream);
+
+/* Bytes of `work` for the call above (host only; -1 for sizes out of range). */
+int64_t nq_binary_matmul_backward_work_bytes(int64_t T, int64_t m, int64_t n, int64_t r);
+
+/* Softmax cross entropy over a large vocabulary (the loss of a tuned model's
+ * outputs), the T x V logits never kept. For hidden states H (T x d, row
+ * stride ldh) and the vocabulary's weights W (V x d, row stride ldw), both
+ * device, of type `dtype`, with z = scale H W^T (scale: one over the softmax
+ * temperature):
+ *   lse_t = log sum_v exp z_tv,   loss_t = lse_t - z_t,labels[t]
+ * (device float32, T each). A negative label is ignored: its loss and lse are
+ * 0 and its row of H is not used (it may hold anything); a label >= V gives
+ * NaN (the library does not read labels on the host). A NaN or an infinity in
+ * a row of H gives NaN in its loss, in W in every loss it takes part in.
+ * work: nq_vocab_loss_work_bytes(T, V, d, dtype, 0) bytes of device scratch,
+ * 16-byte aligned. All on `stream`, no allocation; sums run in a fixed order.
+ * T == 0 is a no-op. T <= 2^20, V <= 2^24, d <= 2^18, strides <= 2^21. */
+nq_status nq_vocab_loss(const void* H, int64_t ldh, const void* W, int64_t ldw, int32_t dtype,
+                        int64_t T, int64_t V, int64_t d, const int32_t* labels, float scale,
+                        float* loss, float* lse, void* work, void* stream);
+
+/* Gradient of sum_t dloss_t loss_t from the lse of nq_vocab_loss on the same
+ * H, W, labels and scale: with
+ *   G_tv = (exp(z_tv - lse_t) - [v == labels[t]]) dloss_t scale,
+ *   dH (T x d, row stride lddh) = G W,   dW (V x d, row stride lddw) = G^T H
+ * in H's type, written (not added to); one of them may be NULL. The logits are
+ * computed again, a piece of the vocabulary at a time; G is rounded once to
+ * H's type (float32: kept whole). Ignored tokens get zero rows of dH and add
+ * nothing to dW, whatever their dloss; a label >= V gives NaN in its row of
+ * dH and in dW. work: nq_vocab_loss_work_bytes(T, V, d, dtype, 1) bytes,
+ * 16-byte aligned. T == 0 is a no-op with dW == NULL and an error with it. */
+nq_status nq_vocab_loss_backward(const void* H, int64_t ldh, const void* W, int64_t ldw,
+                                 int32_t dtype, int64_t T, int64_t V, int64_t d,
+                                 const int32_t* labels, float scale, const float* lse,
+                                 const float* dloss, void* dH, int64_t lddh, void* dW,
+                                 int64_t lddw, void* work, void* stream);
+
+/* Bytes of `work` for the two calls above (grad: 0 for the loss, 1 for its
+ * gradient). Host only; -1 for sizes out of range. */
+int64_t nq_vocab_loss_work_bytes(int64_t T, int64_t V, int64_t d, int32_t dtype, int32_t grad);
 
 /* ---- building blocks (the same kernels the run uses; for tests and tools) ----
  * These take caller buffers of any shape, copy into zero-padded temporaries

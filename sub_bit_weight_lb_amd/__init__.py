@@ -10,7 +10,8 @@ Functions mirror the C names without the ``nq_`` prefix:
     lbadmm_create / lbadmm_run / lbadmm_query / lbadmm_get_state /
     lbadmm_destroy / lbadmm_workspace_bytes / pack_signs /
     transpose_signs / binary_matmul / binary_matmul_noalloc / lw_* (LedoitWolf) /
-    ste_* (STERefiner) /
+    ste_* (STERefiner) / act8_quantize / act8_dequantize / act8_steps (Act8) /
+    binary_matmul_backward / vocab_loss / vocab_loss_backward /
     op_precondition / op_gram / op_gemm_rhs / op_cholesky_inverse / op_svid
 plus the conveniences ``LBADMM`` (a handle object) and ``lbadmm`` (one call).
 """
@@ -29,6 +30,9 @@ __all__ = [
     "NQError", "lbadmm_create", "lbadmm_run", "lbadmm_query", "lbadmm_get_state",
     "lbadmm_destroy", "lbadmm_profile", "lbadmm_workspace_bytes", "pack_signs", "transpose_signs",
     "binary_matmul", "binary_matmul_noalloc", "binary_matmul_work_floats", "LedoitWolf", "ledoit_wolf_diag",
+    "Act8", "ACT8_GROUP", "act8_quantize", "act8_dequantize", "act8_steps",
+    "binary_matmul_backward", "binary_matmul_backward_work_bytes",
+    "vocab_loss", "vocab_loss_backward", "vocab_loss_work_bytes",
     "preconditioners", "STERefiner", "cosine_lr", "op_precondition", "op_gram",
     "op_gemm_rhs", "op_sign_gemm", "op_cholesky_inverse", "op_svid", "LBADMM", "lbadmm", "Result",
     "status_string", "version",
@@ -318,6 +322,306 @@ def _binmm_out(Y, B, m, vec, device):
     return Y2
 
 
+# ---------------------------------------------------------------- tuning a packed model
+
+# consecutive columns of a row that share one exponent of an 8-bit checkpoint
+ACT8_GROUP = 32
+
+
+@dataclass
+class Act8:
+    """8-bit checkpoint of a rows x cols activation matrix: codes (rows x cols
+    int8) and exps (rows x ceil(cols/32) uint8); the value of a code is
+    code * 2^(exps - 127), NaN in a group whose exps is 255. dtype is the type
+    of the activations it was made from (what act8_dequantize returns)."""
+    codes: "object"
+    exps: "object"
+    dtype: "object" = None
+
+    @property
+    def shape(self):
+        return tuple(self.codes.shape)
+
+
+def _dtype_code(dtype, name):
+    torch = _torch()
+    codes = {torch.float32: _lib.NQ_F32, torch.bfloat16: _lib.NQ_BF16, torch.float16: _lib.NQ_F16}
+    if dtype not in codes:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {dtype}")
+    return codes[dtype]
+
+
+def _matrix(t, name, rows=None, cols=None, dtype=None):
+    """Checks that t is a 2-D tensor with unit column stride and rows that do
+    not overlap (of the given size and type where given)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must be {'any' if rows is None else rows} x "
+                         f"{'any' if cols is None else cols}, got {tuple(t.shape)}")
+    if t.numel() == 0:
+        return
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}'s rows overlap (row stride {t.stride(0)})")
+
+
+def _vector(t, name, n, dtype):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {n} values")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _ld(t):
+    """Row stride of a 2-D tensor (a single row's is not what it says)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _on_device(named):
+    """Checks that every tensor of {name: tensor or None} lies on one GPU and
+    returns a context in which that GPU is the current one."""
+    import contextlib
+    torch = _torch()
+    dev, first = None, None
+    for name, t in named.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+        if dev is None:
+            dev, first = t.device, name
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, {first} on {dev}")
+    if dev is None or dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _p(t):
+    return None if t is None else C.c_void_p(t.data_ptr())
+
+
+def _workspace(work, need, device):
+    """The workspace of a call: a new one, or the caller's after a check."""
+    torch = _torch()
+    if work is None:
+        return torch.empty((max(need, 1),), dtype=torch.uint8, device=device)
+    if not isinstance(work, torch.Tensor) or not work.is_contiguous():
+        raise ValueError("work must be a contiguous tensor")
+    if work.numel() * work.element_size() < need:
+        raise ValueError(f"work holds {work.numel() * work.element_size()} bytes, needs {need}")
+    if work.data_ptr() % 16:
+        raise ValueError("work must be 16-byte aligned")
+    return work
+
+
+def _act8(q, name, rows=None, cols=None):
+    torch = _torch()
+    if not isinstance(q, Act8):
+        raise TypeError(f"{name} must be an Act8")
+    _matrix(q.codes, f"{name}.codes", rows, cols, torch.int8)
+    _matrix(q.exps, f"{name}.exps", q.codes.shape[0], -(-q.codes.shape[1] // ACT8_GROUP),
+            torch.uint8)
+
+
+def act8_quantize(X, q=None, stream=None):
+    """8-bit checkpoint of X (rows x cols float32, bfloat16 or float16, unit
+    column stride): 32 consecutive columns of a row share a power-of-two step,
+    the least with max|x| <= 127 steps. q, if given, is an Act8 of that shape
+    to fill. A group with a NaN or an infinity reads back as NaN."""
+    torch = _torch()
+    _matrix(X, "X")
+    code = _dtype_code(X.dtype, "X")
+    rows, cols = X.shape
+    if q is None:
+        q = Act8(torch.empty((rows, cols), dtype=torch.int8, device=X.device),
+                 torch.empty((rows, -(-cols // ACT8_GROUP)), dtype=torch.uint8, device=X.device))
+    else:
+        _act8(q, "q", rows, cols)
+    q.dtype = X.dtype
+    with _on_device(dict(X=X, codes=q.codes, exps=q.exps)):
+        _check(_lib.load().nq_act8_quantize(_p(X), code, rows, cols, _ld(X), _p(q.codes),
+                                            _ld(q.codes), _p(q.exps), _ld(q.exps),
+                                            _stream(stream)), "nq_act8_quantize")
+    return q
+
+
+def act8_dequantize(q, out=None, dtype=None, stream=None):
+    """The activations of a checkpoint, in dtype (default: the type they had,
+    float32 when q does not say), or into out."""
+    torch = _torch()
+    _act8(q, "q")
+    rows, cols = q.shape
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype or q.dtype or torch.float32,
+                          device=q.codes.device)
+    else:
+        _matrix(out, "out", rows, cols, dtype)
+    code = _dtype_code(out.dtype, "out")
+    with _on_device(dict(codes=q.codes, exps=q.exps, out=out)):
+        _check(_lib.load().nq_act8_dequantize(_p(q.codes), _ld(q.codes), _p(q.exps), _ld(q.exps),
+                                              rows, cols, _p(out), code, _ld(out),
+                                              _stream(stream)), "nq_act8_dequantize")
+    return out
+
+
+def act8_steps(q, stream=None):
+    """The step of each group of a checkpoint (rows x ceil(cols/32) float32,
+    powers of two, NaN for a group that was not finite)."""
+    torch = _torch()
+    _act8(q, "q")
+    rows, groups = q.exps.shape
+    steps = torch.empty((rows, groups), dtype=torch.float32, device=q.exps.device)
+    with _on_device(dict(exps=q.exps)):
+        _check(_lib.load().nq_act8_steps(_p(q.exps), _ld(q.exps), rows, groups, _p(steps),
+                                         max(groups, 1), _stream(stream)), "nq_act8_steps")
+    return steps
+
+
+def binary_matmul_backward_work_bytes(T, m, n, r):
+    """Bytes of workspace binary_matmul_backward needs for T tokens."""
+    return int(_lib.load().nq_binary_matmul_backward_work_bytes(int(T), int(m), int(n), int(r)))
+
+
+def binary_matmul_backward(U_bits, Ut_bits, V_bits, Vt_bits, s1, s2, X, dY, r, want_dX=True,
+                           dX=None, ds1=None, ds2=None, work=None, stream=None):
+    """Gradient of binary_matmul's layer Y = X W^T, W = diag(s1) S_U S_V^T
+    diag(s2), with the signs held: returns (dX, ds1, ds2) for dY = dL/dY
+    (T x m float32, bfloat16 or float16) from the 8-bit checkpoint X (an Act8,
+    T x n) of the layer's input. U_bits (m x ceil(r/32) int32 words) and V_bits
+    (n x ceil(r/32)) as lbadmm_run returns them, Ut_bits (r x ceil(m/32)) and
+    Vt_bits (r x ceil(n/32)) their transposes (transpose_signs). dX (T x n) has
+    dY's type (None with want_dX=False); ds1 (m) and ds2 (n) are float32 sums
+    over the tokens. work, if given, holds
+    binary_matmul_backward_work_bytes(T, m, n, r) bytes, 16-byte aligned."""
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
+    _act8(X, "X")
+    T, n = X.shape
+    for t, name in ((U_bits, "U_bits"), (Ut_bits, "Ut_bits"), (V_bits, "V_bits"),
+                    (Vt_bits, "Vt_bits")):
+        _matrix(t, name, dtype=i32)
+    m, r = U_bits.shape[0], int(r)
+    for t, name, rows, cols in ((U_bits, "U_bits", m, r), (Ut_bits, "Ut_bits", r, m),
+                                (V_bits, "V_bits", n, r), (Vt_bits, "Vt_bits", r, n)):
+        if t.shape[0] != rows or t.shape[1] < (cols + 31) // 32:
+            raise ValueError(f"{name} must be {rows} x (>= {(cols + 31) // 32}) words, "
+                             f"got {tuple(t.shape)}")
+    _vector(s1, "s1", m, f32)
+    _vector(s2, "s2", n, f32)
+    _matrix(dY, "dY", T, m)
+    code = _dtype_code(dY.dtype, "dY")
+    if dX is not None:
+        _matrix(dX, "dX", T, n, dY.dtype)
+    elif want_dX:
+        dX = torch.empty((T, n), dtype=dY.dtype, device=dY.device)
+    if ds1 is None:
+        ds1 = torch.empty(m, dtype=f32, device=dY.device)
+    if ds2 is None:
+        ds2 = torch.empty(n, dtype=f32, device=dY.device)
+    _vector(ds1, "ds1", m, f32)
+    _vector(ds2, "ds2", n, f32)
+    if min(m, n, r) < 1:
+        raise ValueError("m, n and r must be >= 1")
+    with _on_device(dict(U_bits=U_bits, Ut_bits=Ut_bits, V_bits=V_bits, Vt_bits=Vt_bits, s1=s1,
+                         s2=s2, codes=X.codes, exps=X.exps, dY=dY, dX=dX, ds1=ds1, ds2=ds2,
+                         work=work)):
+        work = _workspace(work, binary_matmul_backward_work_bytes(T, m, n, r), dY.device)
+        _check(_lib.load().nq_binary_matmul_backward(
+            _p(U_bits), _ld(U_bits), _p(Ut_bits), _ld(Ut_bits), _p(V_bits), _ld(V_bits),
+            _p(Vt_bits), _ld(Vt_bits), m, n, r, _p(s1), _p(s2), _p(X.codes), _ld(X.codes),
+            _p(X.exps), _ld(X.exps), T, _p(dY), code, _ld(dY), _p(dX),
+            _ld(dX) if dX is not None else 0, _p(ds1), _p(ds2), _p(work), _stream(stream)),
+            "nq_binary_matmul_backward")
+    return dX, ds1, ds2
+
+
+def vocab_loss_work_bytes(T, V, d, dtype, grad=False):
+    """Bytes of workspace vocab_loss (or, with grad, vocab_loss_backward)
+    needs for T tokens, V words, hidden size d and H, W of dtype."""
+    return int(_lib.load().nq_vocab_loss_work_bytes(int(T), int(V), int(d),
+                                                    _dtype_code(dtype, "dtype"), int(bool(grad))))
+
+
+def _vocab_args(H, W, labels):
+    torch = _torch()
+    _matrix(H, "H")
+    T, d = H.shape
+    _matrix(W, "W", None, d, H.dtype)
+    code = _dtype_code(H.dtype, "H")
+    _vector(labels, "labels", T, torch.int32)
+    if W.shape[0] < 1 or d < 1:
+        raise ValueError("the vocabulary and the hidden size must be >= 1")
+    return T, W.shape[0], d, code
+
+
+def vocab_loss(H, W, labels, scale=1.0, loss=None, lse=None, work=None, stream=None):
+    """Softmax cross entropy of logits z = scale H W^T, which are never kept:
+    H (T x d) and W (V x d) float32, bfloat16 or float16 with unit column
+    stride, labels (T) int32. Returns (loss, lse), T float32 each:
+    lse = log sum exp z, loss = lse - z[label]. A negative label is ignored
+    (loss and lse 0, its row of H is not used); a label >= V gives NaN. work,
+    if given, holds vocab_loss_work_bytes(T, V, d, H.dtype) bytes."""
+    torch = _torch()
+    T, V, d, code = _vocab_args(H, W, labels)
+    if loss is None:
+        loss = torch.empty(T, dtype=torch.float32, device=H.device)
+    if lse is None:
+        lse = torch.empty(T, dtype=torch.float32, device=H.device)
+    _vector(loss, "loss", T, torch.float32)
+    _vector(lse, "lse", T, torch.float32)
+    with _on_device(dict(H=H, W=W, labels=labels, loss=loss, lse=lse, work=work)):
+        need = _lib.load().nq_vocab_loss_work_bytes(T, V, d, code, 0)
+        work = _workspace(work, need, H.device)
+        _check(_lib.load().nq_vocab_loss(_p(H), _ld(H), _p(W), _ld(W), code, T, V, d, _p(labels),
+                                         float(scale), _p(loss), _p(lse), _p(work),
+                                         _stream(stream)), "nq_vocab_loss")
+    return loss, lse
+
+
+def vocab_loss_backward(H, W, labels, lse, dloss, scale=1.0, want_dH=True, want_dW=True, dH=None,
+                        dW=None, work=None, stream=None):
+    """Gradient of sum(dloss * loss) for vocab_loss(H, W, labels, scale), from
+    its lse: returns (dH, dW) in H's type (None where not wanted). lse and
+    dloss are T float32. The logits are computed again in pieces of the
+    vocabulary. Ignored tokens (negative labels) get zero rows of dH and add
+    nothing to dW. work, if given, holds
+    vocab_loss_work_bytes(T, V, d, H.dtype, grad=True) bytes."""
+    torch = _torch()
+    T, V, d, code = _vocab_args(H, W, labels)
+    _vector(lse, "lse", T, torch.float32)
+    _vector(dloss, "dloss", T, torch.float32)
+    if dH is not None:
+        _matrix(dH, "dH", T, d, H.dtype)
+    elif want_dH:
+        dH = torch.empty((T, d), dtype=H.dtype, device=H.device)
+    if dW is not None:
+        _matrix(dW, "dW", V, d, H.dtype)
+    elif want_dW:
+        dW = torch.empty((V, d), dtype=H.dtype, device=H.device)
+    if dH is None and dW is None:
+        raise ValueError("neither dH nor dW is wanted")
+    with _on_device(dict(H=H, W=W, labels=labels, lse=lse, dloss=dloss, dH=dH, dW=dW, work=work)):
+        if T == 0:
+            if dW is not None:
+                dW.zero_()
+            return dH, dW
+        need = _lib.load().nq_vocab_loss_work_bytes(T, V, d, code, 1)
+        work = _workspace(work, need, H.device)
+        _check(_lib.load().nq_vocab_loss_backward(
+            _p(H), _ld(H), _p(W), _ld(W), code, T, V, d, _p(labels), float(scale), _p(lse),
+            _p(dloss), _p(dH), _ld(dH) if dH is not None else 0, _p(dW),
+            _ld(dW) if dW is not None else 0, _p(work), _stream(stream)),
+            "nq_vocab_loss_backward")
+    return dH, dW
+
+
 class LedoitWolf:
     """Running Ledoit-Wolf statistics of activation samples with p features
     (nq_lw_*): accumulate() chunks of tokens x p float32 samples, then
@@ -393,7 +697,8 @@ def cosine_lr(t, K, lr_max=1e-4, lr_min=1e-6):
 
 class STERefiner:
     """STE refinement of one factorised layer (nq_ste_*): set_params() from
-    a run's U, V, s1, s2, then step() per batch (X, Y = X W^T device float32;
+    a run's U, V, s1, s2, then step() per batch (X, Y = X W^T device float32,
+    X also as its 8-bit checkpoint, an Act8;
     rows: an int32 device index vector or None), or refine() over a list of
     batches with the cosine schedule."""
 
@@ -419,7 +724,9 @@ class STERefiner:
         (a device read and a wait; the library cannot see X's length)."""
         torch = _torch()
         f32 = torch.float32
-        if X.dim() != 2 or X.shape[1] != self.n or X.stride(1) != 1:
+        if isinstance(X, Act8):
+            _act8(X, "X", None, self.n)
+        elif X.dim() != 2 or X.shape[1] != self.n or X.stride(1) != 1:
             raise ValueError(f"X must be tokens x {self.n} with unit column stride")
         if Y.dim() != 2 or Y.shape[1] != self.m or Y.stride(1) != 1 or Y.shape[0] != X.shape[0]:
             raise ValueError(f"Y must be tokens x {self.m}, as many rows as X")
@@ -435,6 +742,13 @@ class STERefiner:
                 raise ValueError("rows holds an index outside X")
         if not 1 <= T <= self.max_tokens:
             raise ValueError(f"a batch holds 1 .. {self.max_tokens} tokens")
+        if isinstance(X, Act8):
+            with _on_device(dict(codes=X.codes, exps=X.exps, Y=Y, rows=rows)):
+                _check(_lib.load().nq_ste_step_act8(
+                    C.c_void_p(self.handle), _p(X.codes), _ld(X.codes), _p(X.exps), _ld(X.exps),
+                    _ptr(Y, "Y", f32, 2, need_contig=False), _ld(Y), rp, T, float(lr),
+                    _stream(stream)), "nq_ste_step_act8")
+            return
         _check(_lib.load().nq_ste_step(
             C.c_void_p(self.handle), _ptr(X, "X", f32, 2, need_contig=False), X.stride(0),
             _ptr(Y, "Y", f32, 2, need_contig=False), Y.stride(0), rp, T, float(lr),

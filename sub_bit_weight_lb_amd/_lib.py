@@ -25,6 +25,10 @@ NQ_FLAG_PROFILE_RHS_ONLY = 0x20
 NQ_FLAG_SOLVE_CG = 0x40
 NQ_FLAG_SOLVE_GD = 0x80
 
+NQ_F32 = 0
+NQ_BF16 = 1
+NQ_F16 = 2
+
 PHASES = ["gemm_rhs", "gemm_solve", "chain", "svid", "prep", "finish"]
 
 
@@ -44,6 +48,7 @@ class Stats(C.Structure):
 
 P = C.c_void_p
 I64 = C.c_int64
+I32 = C.c_int32
 F32 = C.c_float
 ST = C.c_int
 
@@ -70,9 +75,20 @@ SIGNATURES = {
     "nq_ste_create": (ST, [I64, I64, I64, I64, C.POINTER(P)]),
     "nq_ste_set_params": (ST, [P, P, P, P, P, P]),
     "nq_ste_step": (ST, [P, P, I64, P, I64, P, I64, C.c_float, P]),
+    "nq_ste_step_act8": (ST, [P, P, I64, P, I64, P, I64, P, I64, C.c_float, P]),
     "nq_ste_last_loss": (ST, [P, C.POINTER(C.c_double), P]),
     "nq_ste_get_params": (ST, [P, P, P, P, P, P]),
     "nq_ste_destroy": (ST, [P]),
+    "nq_act8_quantize": (ST, [P, I32, I64, I64, I64, P, I64, P, I64, P]),
+    "nq_act8_dequantize": (ST, [P, I64, P, I64, I64, I64, P, I32, I64, P]),
+    "nq_act8_steps": (ST, [P, I64, I64, I64, P, I64, P]),
+    "nq_binary_matmul_backward": (ST, [P, I64, P, I64, P, I64, P, I64, I64, I64, I64, P, P, P, I64,
+                                       P, I64, I64, P, I32, I64, P, I64, P, P, P, P]),
+    "nq_binary_matmul_backward_work_bytes": (I64, [I64, I64, I64, I64]),
+    "nq_vocab_loss": (ST, [P, I64, P, I64, I32, I64, I64, I64, P, F32, P, P, P, P]),
+    "nq_vocab_loss_backward": (ST, [P, I64, P, I64, I32, I64, I64, I64, P, F32, P, P, P, I64, P,
+                                    I64, P, P]),
+    "nq_vocab_loss_work_bytes": (I64, [I64, I64, I64, I32, I32]),
     "nq_op_precondition": (ST, [P, I64, I64, I64, P, P, P, I64, P]),
     "nq_op_gram": (ST, [P, I64, I64, I64, F32, P, I64, P]),
     "nq_op_gemm_rhs": (ST, [P, I64, P, I64, P, I64, F32, P, I64, I64, I64, I64, P]),

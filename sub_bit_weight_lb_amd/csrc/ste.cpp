@@ -9,27 +9,9 @@
 #include <string>
 
 #include "abi.h"
-#include "common.h"
+#include "ste.h"
 
 using namespace nq;
-
-namespace nq {
-hipError_t launch_ste_signs(const float* F, int64_t rows, int64_t r, int64_t rp, int64_t rows_pad,
-                            float* S, float* St, hipStream_t s);
-hipError_t launch_ste_stage(const float* X, int64_t ldx, const int32_t* idx, int64_t T, int64_t n,
-                            const float* s2, int64_t np_, int64_t tp, float* A, float* At,
-                            hipStream_t s);
-hipError_t launch_ste_loss(const float* Q, const float* Y, int64_t ldy, const int32_t* idx,
-                           int64_t T, int64_t m, const float* s1, int64_t mp, int64_t tp,
-                           float* dQ, float* dQt, float* ds1p, double* lossp, float* ds1,
-                           double* loss, hipStream_t s);
-hipError_t launch_ste_ds2(const float* dA, const float* X, int64_t ldx, const int32_t* idx,
-                          int64_t T, int64_t n, int64_t np_, int64_t tp, float* ds2p, float* ds2,
-                          hipStream_t s);
-hipError_t launch_ste_adam(float* p, const float* g, float* m, float* v, int64_t rows,
-                           int64_t cols, int64_t ld, float lr, float b1, float b2, float c1,
-                           float c2, float eps, hipStream_t s);
-}  // namespace nq
 
 struct nq_ste {
   int64_t m = 0, n = 0, r = 0, tmax = 0, mp = 0, np_ = 0, rp = 0, tp = 0;
@@ -111,6 +93,49 @@ hipError_t stage_in(const float* src, int64_t rows, int64_t cols, int64_t lds, f
                           sizeof(float) * cols, rows, hipMemcpyDeviceToDevice, s);
 }
 
+nq_status check_step(nq_ste_t h, bool have_x, const float* Y, int64_t T, float lr) {
+  if (!h) return set_error(NQ_ERR_INVALID_ARG, "handle is NULL");
+  if (!h->has_params) return set_error(NQ_ERR_INVALID_ARG, "nq_ste_set_params has not run");
+  if (!have_x || !Y) return set_error(NQ_ERR_INVALID_ARG, "X and Y are required");
+  if (T < 1 || T > h->tmax) return set_error(NQ_ERR_INVALID_ARG, "T must be in [1, max_tokens]");
+  if (!(lr >= 0.0f) || !std::isfinite(lr))
+    return set_error(NQ_ERR_INVALID_ARG, "lr must be finite and >= 0");
+  return NQ_OK;
+}
+
+// One step on the rows of X (SteFloat or Act8) and Y
+template <class Src>
+nq_status step(nq_ste_t h, const Src& X, const float* Y, int64_t ldy, const int32_t* rows,
+               int64_t T, float lr, hipStream_t s) {
+  const int64_t mp = h->mp, np_ = h->np_, rp = h->rp, tp = round_up(T, 256);
+  // forward
+  NQ_HIPCHK(launch_ste_stage(X, rows, T, h->n, h->s2, np_, tp, h->A, h->At, s));
+  // (the four products with a sign factor run on the bf16 matrix cores,
+  // exactly: launch_sign_gemm)
+  NQ_HIPCHK(launch_sign_gemm(h->A, np_, h->SVt, np_, h->P, rp, h->Pt, tp, (int)tp, (int)rp, (int)np_, s));
+  NQ_HIPCHK(launch_sign_gemm(h->P, rp, h->SU, rp, h->Q, mp, nullptr, 0, (int)tp, (int)mp, (int)rp, s));
+  // loss, dL/dYq, ds1, dQ
+  NQ_HIPCHK(launch_ste_loss(h->Q, Y, ldy, rows, T, h->m, h->s1, mp, tp, h->dQ, h->dQt, h->ds1p,
+                            h->lossp, h->ds1, h->loss, s));
+  // backward through the two sign products
+  NQ_HIPCHK(gemm(h->dQt, tp, h->Pt, tp, h->dU, rp, mp, rp, tp, nullptr, 0, s));
+  NQ_HIPCHK(launch_sign_gemm(h->dQ, mp, h->SUt, mp, h->dP, rp, h->dPt, tp, (int)tp, (int)rp, (int)mp, s));
+  NQ_HIPCHK(gemm(h->At, tp, h->dPt, tp, h->dV, rp, np_, rp, tp, nullptr, 0, s));
+  NQ_HIPCHK(launch_sign_gemm(h->dP, rp, h->SV, rp, h->dA, np_, nullptr, 0, (int)tp, (int)np_, (int)rp, s));
+  NQ_HIPCHK(launch_ste_ds2(h->dA, X, rows, T, h->n, np_, tp, h->ds2p, h->ds2, s));
+  // Adam, then the signs of the moved latents
+  h->t += 1;
+  const float c1 = (float)(1.0 - std::pow((double)kB1, h->t));
+  const float c2 = (float)(1.0 - std::pow((double)kB2, h->t));
+  NQ_HIPCHK(launch_ste_adam(h->U, h->dU, h->mU, h->vU, h->m, h->r, rp, lr, kB1, kB2, c1, c2, kEps, s));
+  NQ_HIPCHK(launch_ste_adam(h->V, h->dV, h->mV, h->vV, h->n, h->r, rp, lr, kB1, kB2, c1, c2, kEps, s));
+  NQ_HIPCHK(launch_ste_adam(h->s1, h->ds1, h->ms1, h->vs1, 1, h->m, h->m, lr, kB1, kB2, c1, c2, kEps, s));
+  NQ_HIPCHK(launch_ste_adam(h->s2, h->ds2, h->ms2, h->vs2, 1, h->n, h->n, lr, kB1, kB2, c1, c2, kEps, s));
+  NQ_HIPCHK(launch_ste_signs(h->U, h->m, h->r, rp, mp, h->SU, h->SUt, s));
+  NQ_HIPCHK(launch_ste_signs(h->V, h->n, h->r, rp, np_, h->SV, h->SVt, s));
+  return NQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -160,41 +185,21 @@ nq_status nq_ste_set_params(nq_ste_t h, const float* U, const float* V, const fl
 
 nq_status nq_ste_step(nq_ste_t h, const float* X, int64_t ldx, const float* Y, int64_t ldy,
                       const int32_t* rows, int64_t T, float lr, void* stream) {
-  if (!h) return set_error(NQ_ERR_INVALID_ARG, "handle is NULL");
-  if (!h->has_params) return set_error(NQ_ERR_INVALID_ARG, "nq_ste_set_params has not run");
-  if (!X || !Y) return set_error(NQ_ERR_INVALID_ARG, "X and Y are required");
-  if (T < 1 || T > h->tmax) return set_error(NQ_ERR_INVALID_ARG, "T must be in [1, max_tokens]");
+  const nq_status st = check_step(h, X != nullptr, Y, T, lr);
+  if (st != NQ_OK) return st;
   if (ldx < h->n || ldy < h->m) return set_error(NQ_ERR_INVALID_ARG, "ldx < n or ldy < m");
-  if (!(lr >= 0.0f) || !std::isfinite(lr))
-    return set_error(NQ_ERR_INVALID_ARG, "lr must be finite and >= 0");
-  hipStream_t s = (hipStream_t)stream;
-  const int64_t mp = h->mp, np_ = h->np_, rp = h->rp, tp = round_up(T, 256);
-  // forward
-  NQ_HIPCHK(launch_ste_stage(X, ldx, rows, T, h->n, h->s2, np_, tp, h->A, h->At, s));
-  // (the four products with a sign factor run on the bf16 matrix cores,
-  // exactly: launch_sign_gemm)
-  NQ_HIPCHK(launch_sign_gemm(h->A, np_, h->SVt, np_, h->P, rp, h->Pt, tp, (int)tp, (int)rp, (int)np_, s));
-  NQ_HIPCHK(launch_sign_gemm(h->P, rp, h->SU, rp, h->Q, mp, nullptr, 0, (int)tp, (int)mp, (int)rp, s));
-  // loss, dL/dYq, ds1, dQ
-  NQ_HIPCHK(launch_ste_loss(h->Q, Y, ldy, rows, T, h->m, h->s1, mp, tp, h->dQ, h->dQt, h->ds1p,
-                            h->lossp, h->ds1, h->loss, s));
-  // backward through the two sign products
-  NQ_HIPCHK(gemm(h->dQt, tp, h->Pt, tp, h->dU, rp, mp, rp, tp, nullptr, 0, s));
-  NQ_HIPCHK(launch_sign_gemm(h->dQ, mp, h->SUt, mp, h->dP, rp, h->dPt, tp, (int)tp, (int)rp, (int)mp, s));
-  NQ_HIPCHK(gemm(h->At, tp, h->dPt, tp, h->dV, rp, np_, rp, tp, nullptr, 0, s));
-  NQ_HIPCHK(launch_sign_gemm(h->dP, rp, h->SV, rp, h->dA, np_, nullptr, 0, (int)tp, (int)np_, (int)rp, s));
-  NQ_HIPCHK(launch_ste_ds2(h->dA, X, ldx, rows, T, h->n, np_, tp, h->ds2p, h->ds2, s));
-  // Adam, then the signs of the moved latents
-  h->t += 1;
-  const float c1 = (float)(1.0 - std::pow((double)kB1, h->t));
-  const float c2 = (float)(1.0 - std::pow((double)kB2, h->t));
-  NQ_HIPCHK(launch_ste_adam(h->U, h->dU, h->mU, h->vU, h->m, h->r, rp, lr, kB1, kB2, c1, c2, kEps, s));
-  NQ_HIPCHK(launch_ste_adam(h->V, h->dV, h->mV, h->vV, h->n, h->r, rp, lr, kB1, kB2, c1, c2, kEps, s));
-  NQ_HIPCHK(launch_ste_adam(h->s1, h->ds1, h->ms1, h->vs1, 1, h->m, h->m, lr, kB1, kB2, c1, c2, kEps, s));
-  NQ_HIPCHK(launch_ste_adam(h->s2, h->ds2, h->ms2, h->vs2, 1, h->n, h->n, lr, kB1, kB2, c1, c2, kEps, s));
-  NQ_HIPCHK(launch_ste_signs(h->U, h->m, h->r, rp, mp, h->SU, h->SUt, s));
-  NQ_HIPCHK(launch_ste_signs(h->V, h->n, h->r, rp, np_, h->SV, h->SVt, s));
-  return NQ_OK;
+  return step(h, SteFloat{X, ldx}, Y, ldy, rows, T, lr, (hipStream_t)stream);
+}
+
+nq_status nq_ste_step_act8(nq_ste_t h, const int8_t* codes, int64_t ldc, const uint8_t* exps,
+                           int64_t lde, const float* Y, int64_t ldy, const int32_t* rows,
+                           int64_t T, float lr, void* stream) {
+  const nq_status st = check_step(h, codes && exps, Y, T, lr);
+  if (st != NQ_OK) return st;
+  if (ldc < h->n || ldy < h->m) return set_error(NQ_ERR_INVALID_ARG, "ldc < n or ldy < m");
+  if (lde < (h->n + kActGroup - 1) / kActGroup)
+    return set_error(NQ_ERR_INVALID_ARG, "lde < ceil(n/32)");
+  return step(h, Act8{codes, ldc, exps, lde}, Y, ldy, rows, T, lr, (hipStream_t)stream);
 }
 
 nq_status nq_ste_last_loss(nq_ste_t h, double* loss, void* stream) {

@@ -23,12 +23,20 @@
 // exact bf16 terms (every product exact, fp32 accumulation), the two
 // without on the fp32 matrix-core GEMM of the ADMM path. Every reduction
 // runs in a fixed order.
-#include "common.h"
+#include "ste.h"
 
 #include <algorithm>
 
 namespace nq {
 namespace {
+
+// Element (row, j) of the inputs: float32, or an 8-bit checkpoint of them.
+__device__ __forceinline__ float ste_input(const SteFloat& x, int64_t row, int64_t j) {
+  return x.X[row * x.ldx + j];
+}
+__device__ __forceinline__ float ste_input(const Act8& x, int64_t row, int64_t j) {
+  return (float)x.codes[row * x.ldc + j] * act8_step(x.exps[row * x.lde + j / kActGroup]);
+}
 
 // S (rows_pad x rp) = sign(F) for i < rows, k < r, else 0; St = S^T
 // (rp x rows_pad). 32 x 32 tiles, grid (rp / 32, rows_pad / 32).
@@ -52,8 +60,9 @@ __global__ __launch_bounds__(256) void ste_signs_kernel(const float* __restrict_
 }
 
 // A (tp x np) = X[idx[t]] * s2 for t < T, j < n, else 0; At = A^T (np x tp)
-__global__ __launch_bounds__(256) void ste_stage_kernel(const float* __restrict__ X, int64_t ldx,
-                                                        const int32_t* __restrict__ idx, int64_t T,
+template <class Src>
+__global__ __launch_bounds__(256) void ste_stage_kernel(Src X, const int32_t* __restrict__ idx,
+                                                        int64_t T,
                                                         int64_t n, const float* __restrict__ s2,
                                                         int64_t np_, int64_t tp,
                                                         float* __restrict__ A,
@@ -67,7 +76,7 @@ __global__ __launch_bounds__(256) void ste_stage_kernel(const float* __restrict_
     float v = 0.0f;
     if (t < T && j < n) {
       const int64_t row = idx ? (int64_t)idx[t] : t;
-      v = X[row * ldx + j] * s2[j];
+      v = ste_input(X, row, j) * s2[j];
     }
     A[t * np_ + j] = v;
     tile[ty + 8 * q][tx] = v;
@@ -131,8 +140,8 @@ __global__ __launch_bounds__(256) void ste_loss_kernel(
 }
 
 // ds2p[tile row][j] = sum over the tile's 32 rows t < T of dA_tj X[idx t]_j
-__global__ __launch_bounds__(256) void ste_ds2_kernel(const float* __restrict__ dA,
-                                                      const float* __restrict__ X, int64_t ldx,
+template <class Src>
+__global__ __launch_bounds__(256) void ste_ds2_kernel(const float* __restrict__ dA, Src X,
                                                       const int32_t* __restrict__ idx, int64_t T,
                                                       int64_t n, int64_t np_,
                                                       float* __restrict__ ds2p) {
@@ -145,7 +154,7 @@ __global__ __launch_bounds__(256) void ste_ds2_kernel(const float* __restrict__ 
     const int64_t t = t0 + 4 * ty + q;
     if (t < T && j < n) {
       const int64_t row = idx ? (int64_t)idx[t] : t;
-      c += dA[t * np_ + j] * X[row * ldx + j];
+      c += dA[t * np_ + j] * ste_input(X, row, j);
     }
   }
   cs[ty][tx] = c;
@@ -232,14 +241,19 @@ hipError_t launch_ste_signs(const float* F, int64_t rows, int64_t r, int64_t rp,
   return hipGetLastError();
 }
 
-hipError_t launch_ste_stage(const float* X, int64_t ldx, const int32_t* idx, int64_t T, int64_t n,
+template <class Src>
+hipError_t launch_ste_stage(const Src& X, const int32_t* idx, int64_t T, int64_t n,
                             const float* s2, int64_t np_, int64_t tp, float* A, float* At,
                             hipStream_t s) {
   if (np_ % 32 || tp % 32 || tp / 32 > 65535) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(ste_stage_kernel, dim3((unsigned)(np_ / 32), (unsigned)(tp / 32)), dim3(256),
-                     0, s, X, ldx, idx, T, n, s2, np_, tp, A, At);
+  hipLaunchKernelGGL(ste_stage_kernel<Src>, dim3((unsigned)(np_ / 32), (unsigned)(tp / 32)),
+                     dim3(256), 0, s, X, idx, T, n, s2, np_, tp, A, At);
   return hipGetLastError();
 }
+template hipError_t launch_ste_stage(const SteFloat&, const int32_t*, int64_t, int64_t,
+                                     const float*, int64_t, int64_t, float*, float*, hipStream_t);
+template hipError_t launch_ste_stage(const Act8&, const int32_t*, int64_t, int64_t, const float*,
+                                     int64_t, int64_t, float*, float*, hipStream_t);
 
 hipError_t launch_ste_loss(const float* Q, const float* Y, int64_t ldy, const int32_t* idx,
                            int64_t T, int64_t m, const float* s1, int64_t mp, int64_t tp,
@@ -256,16 +270,20 @@ hipError_t launch_ste_loss(const float* Q, const float* Y, int64_t ldy, const in
   return hipGetLastError();
 }
 
-hipError_t launch_ste_ds2(const float* dA, const float* X, int64_t ldx, const int32_t* idx,
-                          int64_t T, int64_t n, int64_t np_, int64_t tp, float* ds2p, float* ds2,
-                          hipStream_t s) {
+template <class Src>
+hipError_t launch_ste_ds2(const float* dA, const Src& X, const int32_t* idx, int64_t T, int64_t n,
+                          int64_t np_, int64_t tp, float* ds2p, float* ds2, hipStream_t s) {
   if (np_ % 32 || tp % 32 || tp / 32 > 65535) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(ste_ds2_kernel, dim3((unsigned)(np_ / 32), (unsigned)(tp / 32)), dim3(256), 0,
-                     s, dA, X, ldx, idx, T, n, np_, ds2p);
+  hipLaunchKernelGGL(ste_ds2_kernel<Src>, dim3((unsigned)(np_ / 32), (unsigned)(tp / 32)),
+                     dim3(256), 0, s, dA, X, idx, T, n, np_, ds2p);
   hipLaunchKernelGGL(ste_colsum_kernel, dim3((unsigned)(np_ / 32)), dim3(256), 0, s, ds2p,
                      (int)(tp / 32), np_, ds2);
   return hipGetLastError();
 }
+template hipError_t launch_ste_ds2(const float*, const SteFloat&, const int32_t*, int64_t, int64_t,
+                                   int64_t, int64_t, float*, float*, hipStream_t);
+template hipError_t launch_ste_ds2(const float*, const Act8&, const int32_t*, int64_t, int64_t,
+                                   int64_t, int64_t, float*, float*, hipStream_t);
 
 hipError_t launch_ste_adam(float* p, const float* g, float* m, float* v, int64_t rows,
                            int64_t cols, int64_t ld, float lr, float b1, float b2, float c1,
