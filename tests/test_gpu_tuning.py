@@ -6,11 +6,15 @@ With u = 2^-24 (half a unit of fp32) and h(t) half a unit of the output type
 (torch.finfo(t).eps / 2: fp32 u, bf16 2^-8, fp16 2^-11):
 
 checkpoint   nothing rounds but the codes: equal to the oracle.
-layer        a and s1 dy: one fp32 rounding each (u), then fixed point, 2^-31
-             of the row's largest; sums are exact; p, dp: one rounding (u),
-             then 2^-23 of the row's largest; q, da: one rounding (u). So with
-             A = sum_c |a_c| over a row: |dp| <= u A + K 2^-31 max|a| + u |p|,
-             |dq| <= sum_k |dp_k| + r 2^-23 max|p| + u |q|. dx adds u and h(t);
+layer        a and s1 dy: two fp32 roundings each at most (2 u), then fixed
+             point, 2^-31 of the row's largest; sums of digits are exact and
+             joined by ND - 1 fp32 multiply-adds and a conversion each (ND = 4,
+             then 3), whose roundings are u of the partial results, at most
+             |p| plus the lower digits' sums, K 2^-8 max|a| together; p, dp:
+             fixed point, 2^-23 of the row's largest. So with A = sum_c |a_c|
+             over a row: |dp| <= 2 u A + K 2^-31 max|a| + 8 u (|p| + K 2^-7
+             max|a|), |dq| <= sum_k |dp_k| + r 2^-23 max|p| + 6 u (|q| + r 2^-7
+             max|p|). dx adds u and h(t);
              ds1, ds2 sum at most 24 rounded fp32 terms in a row before fp64
              takes over (16 in a lane, 4 lanes, 2 halves, the product).
 loss         z: an fp32 sum of d exact products, (d + 2) u sum |h_k w_k|, for
@@ -169,9 +173,12 @@ class Layer:
         def chain(a, S, S2):
             """(values, bounds) of the product a S S2^T"""
             p = a @ S
-            ep = (U * np.abs(a).sum(1) + a.shape[1] * 2.0 ** -31 * np.abs(a).max(1))[:, None] + U * np.abs(p)
-            q = p @ S2.T
-            eq = (ep.sum(1) + r * 2.0 ** -23 * (np.abs(p) + ep).max(1))[:, None] + U * np.abs(q)
+            K, big = a.shape[1], np.abs(a).max(1)
+            ep = (2 * U * np.abs(a).sum(1) + K * 2.0 ** -31 * big)[:, None]
+            ep = ep + 8 * U * (np.abs(p) + (K * 2.0 ** -7 * big)[:, None])
+            q, big = p @ S2.T, (np.abs(p) + ep).max(1)
+            eq = (ep.sum(1) + r * 2.0 ** -23 * big)[:, None]
+            eq = eq + 6 * U * (np.abs(q) + (r * 2.0 ** -7 * big)[:, None])
             return q, eq
 
         q, eq = chain(x * s2, self.SV, self.SU)
