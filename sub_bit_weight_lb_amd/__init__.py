@@ -53,9 +53,15 @@ def _check(status: int, where: str):
         raise NQError(status, where)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t, name, dtype=None, ndim=None, allow_none=False, need_contig=True):
@@ -78,7 +84,9 @@ def _ptr(t, name, dtype=None, ndim=None, allow_none=False, need_contig=True):
 def _stream(stream):
     if stream is not None:
         return C.c_void_p(int(stream))
-    return C.c_void_p(_torch().cuda.current_stream().cuda_stream)
+    # the current stream's handle without a Stream object (2.7 us of every call)
+    torch = _torch()
+    return C.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def status_string(status: int) -> str:
@@ -343,31 +351,42 @@ class Act8:
         return tuple(self.codes.shape)
 
 
+_DTYPES = {}   # torch type -> nq_dtype, filled on first use
+
+
 def _dtype_code(dtype, name):
-    torch = _torch()
-    codes = {torch.float32: _lib.NQ_F32, torch.bfloat16: _lib.NQ_BF16, torch.float16: _lib.NQ_F16}
-    if dtype not in codes:
+    if not _DTYPES:
+        torch = _torch()
+        _DTYPES.update({torch.float32: _lib.NQ_F32, torch.bfloat16: _lib.NQ_BF16,
+                        torch.float16: _lib.NQ_F16})
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {dtype}")
-    return codes[dtype]
+    return code
 
 
 def _matrix(t, name, rows=None, cols=None, dtype=None):
     """Checks that t is a 2-D tensor with unit column stride and rows that do
-    not overlap (of the given size and type where given)."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+    not overlap (of the given size and type where given); returns its rows,
+    columns and row stride (a single row's is not what it says)."""
+    if not isinstance(t, _torch().Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+    nr, nc = t.shape
+    if (rows is not None and nr != rows) or (cols is not None and nc != cols):
         raise ValueError(f"{name} must be {'any' if rows is None else rows} x "
-                         f"{'any' if cols is None else cols}, got {tuple(t.shape)}")
-    if t.numel() == 0:
-        return
-    if t.shape[1] > 1 and t.stride(1) != 1:
+                         f"{'any' if cols is None else cols}, got {nr} x {nc}")
+    ld, step = t.stride()
+    if nr == 0 or nc == 0:
+        return nr, nc, max(nc, 1)
+    if nc > 1 and step != 1:
         raise ValueError(f"{name} must have unit column stride")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}'s rows overlap (row stride {t.stride(0)})")
+    if nr == 1:
+        return nr, nc, nc
+    if ld < nc:
+        raise ValueError(f"{name}'s rows overlap (row stride {ld})")
+    return nr, nc, ld
 
 
 def _vector(t, name, n, dtype):
@@ -378,33 +397,43 @@ def _vector(t, name, n, dtype):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
-def _ld(t):
-    """Row stride of a 2-D tensor (a single row's is not what it says)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+class _OnDevice:
+    """Makes `index` the current GPU for a block (nothing when it is)."""
+
+    def __init__(self, index):
+        self.index, self.previous = index, None
+
+    def __enter__(self):
+        cuda = _torch().cuda
+        now = cuda.current_device()
+        if now != self.index:
+            cuda.set_device(self.index)
+            self.previous = now
+
+    def __exit__(self, *exc):
+        if self.previous is not None:
+            _torch().cuda.set_device(self.previous)
 
 
-def _on_device(named):
-    """Checks that every tensor of {name: tensor or None} lies on one GPU and
-    returns a context in which that GPU is the current one."""
-    import contextlib
-    torch = _torch()
-    dev, first = None, None
-    for name, t in named.items():
+def _on_device(names, *tensors):
+    """Checks that every tensor (or None) lies on one GPU and returns a context
+    in which that GPU is the current one; names: theirs, separated by spaces."""
+    dev = None
+    for i, t in enumerate(tensors):
         if t is None:
             continue
-        if not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+        d = t.device
         if dev is None:
-            dev, first = t.device, name
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, {first} on {dev}")
-    if dev is None or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+            dev = d
+            if d.type != "cuda":
+                raise TypeError(f"{names.split()[i]} must be a CUDA (HIP) tensor")
+        elif d != dev:
+            raise ValueError(f"{names.split()[i]} is on {d}, the others on {dev}")
+    return _OnDevice(dev.index)
 
 
 def _p(t):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _workspace(work, need, device):
@@ -422,12 +451,14 @@ def _workspace(work, need, device):
 
 
 def _act8(q, name, rows=None, cols=None):
+    """Checks a checkpoint; returns its rows, columns and the row strides of
+    its codes and exponents."""
     torch = _torch()
     if not isinstance(q, Act8):
         raise TypeError(f"{name} must be an Act8")
-    _matrix(q.codes, f"{name}.codes", rows, cols, torch.int8)
-    _matrix(q.exps, f"{name}.exps", q.codes.shape[0], -(-q.codes.shape[1] // ACT8_GROUP),
-            torch.uint8)
+    rows, cols, ldc = _matrix(q.codes, f"{name}.codes", rows, cols, torch.int8)
+    _, _, lde = _matrix(q.exps, f"{name}.exps", rows, -(-cols // ACT8_GROUP), torch.uint8)
+    return rows, cols, ldc, lde
 
 
 def act8_quantize(X, q=None, stream=None):
@@ -436,19 +467,19 @@ def act8_quantize(X, q=None, stream=None):
     the least with max|x| <= 127 steps. q, if given, is an Act8 of that shape
     to fill. A group with a NaN or an infinity reads back as NaN."""
     torch = _torch()
-    _matrix(X, "X")
+    rows, cols, ldx = _matrix(X, "X")
     code = _dtype_code(X.dtype, "X")
-    rows, cols = X.shape
     if q is None:
+        groups = -(-cols // ACT8_GROUP)
         q = Act8(torch.empty((rows, cols), dtype=torch.int8, device=X.device),
-                 torch.empty((rows, -(-cols // ACT8_GROUP)), dtype=torch.uint8, device=X.device))
+                 torch.empty((rows, groups), dtype=torch.uint8, device=X.device))
+        ldc, lde = max(cols, 1), max(groups, 1)
     else:
-        _act8(q, "q", rows, cols)
+        _, _, ldc, lde = _act8(q, "q", rows, cols)
     q.dtype = X.dtype
-    with _on_device(dict(X=X, codes=q.codes, exps=q.exps)):
-        _check(_lib.load().nq_act8_quantize(_p(X), code, rows, cols, _ld(X), _p(q.codes),
-                                            _ld(q.codes), _p(q.exps), _ld(q.exps),
-                                            _stream(stream)), "nq_act8_quantize")
+    with _on_device("X codes exps", X, q.codes, q.exps):
+        _check(_lib.load().nq_act8_quantize(_p(X), code, rows, cols, ldx, _p(q.codes), ldc,
+                                            _p(q.exps), lde, _stream(stream)), "nq_act8_quantize")
     return q
 
 
@@ -456,18 +487,18 @@ def act8_dequantize(q, out=None, dtype=None, stream=None):
     """The activations of a checkpoint, in dtype (default: the type they had,
     float32 when q does not say), or into out."""
     torch = _torch()
-    _act8(q, "q")
-    rows, cols = q.shape
+    rows, cols, ldc, lde = _act8(q, "q")
     if out is None:
         out = torch.empty((rows, cols), dtype=dtype or q.dtype or torch.float32,
                           device=q.codes.device)
+        ldo = max(cols, 1)
     else:
-        _matrix(out, "out", rows, cols, dtype)
+        _, _, ldo = _matrix(out, "out", rows, cols, dtype)
     code = _dtype_code(out.dtype, "out")
-    with _on_device(dict(codes=q.codes, exps=q.exps, out=out)):
-        _check(_lib.load().nq_act8_dequantize(_p(q.codes), _ld(q.codes), _p(q.exps), _ld(q.exps),
-                                              rows, cols, _p(out), code, _ld(out),
-                                              _stream(stream)), "nq_act8_dequantize")
+    with _on_device("codes exps out", q.codes, q.exps, out):
+        _check(_lib.load().nq_act8_dequantize(_p(q.codes), ldc, _p(q.exps), lde, rows, cols,
+                                              _p(out), code, ldo, _stream(stream)),
+               "nq_act8_dequantize")
     return out
 
 
@@ -475,11 +506,11 @@ def act8_steps(q, stream=None):
     """The step of each group of a checkpoint (rows x ceil(cols/32) float32,
     powers of two, NaN for a group that was not finite)."""
     torch = _torch()
-    _act8(q, "q")
+    _, _, _, lde = _act8(q, "q")
     rows, groups = q.exps.shape
     steps = torch.empty((rows, groups), dtype=torch.float32, device=q.exps.device)
-    with _on_device(dict(exps=q.exps)):
-        _check(_lib.load().nq_act8_steps(_p(q.exps), _ld(q.exps), rows, groups, _p(steps),
+    with _on_device("exps", q.exps):
+        _check(_lib.load().nq_act8_steps(_p(q.exps), lde, rows, groups, _p(steps),
                                          max(groups, 1), _stream(stream)), "nq_act8_steps")
     return steps
 
@@ -502,43 +533,46 @@ def binary_matmul_backward(U_bits, Ut_bits, V_bits, Vt_bits, s1, s2, X, dY, r, w
     binary_matmul_backward_work_bytes(T, m, n, r) bytes, 16-byte aligned."""
     torch = _torch()
     f32, i32 = torch.float32, torch.int32
-    _act8(X, "X")
-    T, n = X.shape
-    for t, name in ((U_bits, "U_bits"), (Ut_bits, "Ut_bits"), (V_bits, "V_bits"),
-                    (Vt_bits, "Vt_bits")):
-        _matrix(t, name, dtype=i32)
-    m, r = U_bits.shape[0], int(r)
-    for t, name, rows, cols in ((U_bits, "U_bits", m, r), (Ut_bits, "Ut_bits", r, m),
-                                (V_bits, "V_bits", n, r), (Vt_bits, "Vt_bits", r, n)):
-        if t.shape[0] != rows or t.shape[1] < (cols + 31) // 32:
+    T, n, ldc, lde = _act8(X, "X")
+    r = int(r)
+    m, words, ldu = _matrix(U_bits, "U_bits", dtype=i32)
+    got = [(m, words), None, None, None]
+    lds = [ldu, 0, 0, 0]
+    for k, (t, name) in enumerate(((Ut_bits, "Ut_bits"), (V_bits, "V_bits"), (Vt_bits, "Vt_bits"))):
+        nr, nc, lds[k + 1] = _matrix(t, name, dtype=i32)
+        got[k + 1] = (nr, nc)
+    for (nr, nc), name, rows, cols in zip(got, ("U_bits", "Ut_bits", "V_bits", "Vt_bits"),
+                                          (m, r, n, r), (r, m, r, n)):
+        if nr != rows or nc < (cols + 31) // 32:
             raise ValueError(f"{name} must be {rows} x (>= {(cols + 31) // 32}) words, "
-                             f"got {tuple(t.shape)}")
+                             f"got {nr} x {nc}")
     _vector(s1, "s1", m, f32)
     _vector(s2, "s2", n, f32)
-    _matrix(dY, "dY", T, m)
+    _, _, lddy = _matrix(dY, "dY", T, m)
     code = _dtype_code(dY.dtype, "dY")
+    lddx = 0
     if dX is not None:
-        _matrix(dX, "dX", T, n, dY.dtype)
+        _, _, lddx = _matrix(dX, "dX", T, n, dY.dtype)
     elif want_dX:
-        dX = torch.empty((T, n), dtype=dY.dtype, device=dY.device)
+        dX, lddx = torch.empty((T, n), dtype=dY.dtype, device=dY.device), max(n, 1)
     if ds1 is None:
         ds1 = torch.empty(m, dtype=f32, device=dY.device)
+    else:
+        _vector(ds1, "ds1", m, f32)
     if ds2 is None:
         ds2 = torch.empty(n, dtype=f32, device=dY.device)
-    _vector(ds1, "ds1", m, f32)
-    _vector(ds2, "ds2", n, f32)
+    else:
+        _vector(ds2, "ds2", n, f32)
     if min(m, n, r) < 1:
         raise ValueError("m, n and r must be >= 1")
-    with _on_device(dict(U_bits=U_bits, Ut_bits=Ut_bits, V_bits=V_bits, Vt_bits=Vt_bits, s1=s1,
-                         s2=s2, codes=X.codes, exps=X.exps, dY=dY, dX=dX, ds1=ds1, ds2=ds2,
-                         work=work)):
-        work = _workspace(work, binary_matmul_backward_work_bytes(T, m, n, r), dY.device)
-        _check(_lib.load().nq_binary_matmul_backward(
-            _p(U_bits), _ld(U_bits), _p(Ut_bits), _ld(Ut_bits), _p(V_bits), _ld(V_bits),
-            _p(Vt_bits), _ld(Vt_bits), m, n, r, _p(s1), _p(s2), _p(X.codes), _ld(X.codes),
-            _p(X.exps), _ld(X.exps), T, _p(dY), code, _ld(dY), _p(dX),
-            _ld(dX) if dX is not None else 0, _p(ds1), _p(ds2), _p(work), _stream(stream)),
-            "nq_binary_matmul_backward")
+    with _on_device("U_bits Ut_bits V_bits Vt_bits s1 s2 codes exps dY dX ds1 ds2 work", U_bits,
+                    Ut_bits, V_bits, Vt_bits, s1, s2, X.codes, X.exps, dY, dX, ds1, ds2, work):
+        lib = _lib.load()
+        work = _workspace(work, lib.nq_binary_matmul_backward_work_bytes(T, m, n, r), dY.device)
+        _check(lib.nq_binary_matmul_backward(
+            _p(U_bits), lds[0], _p(Ut_bits), lds[1], _p(V_bits), lds[2], _p(Vt_bits), lds[3], m, n,
+            r, _p(s1), _p(s2), _p(X.codes), ldc, _p(X.exps), lde, T, _p(dY), code, lddy, _p(dX),
+            lddx, _p(ds1), _p(ds2), _p(work), _stream(stream)), "nq_binary_matmul_backward")
     return dX, ds1, ds2
 
 
@@ -551,14 +585,13 @@ def vocab_loss_work_bytes(T, V, d, dtype, grad=False):
 
 def _vocab_args(H, W, labels):
     torch = _torch()
-    _matrix(H, "H")
-    T, d = H.shape
-    _matrix(W, "W", None, d, H.dtype)
+    T, d, ldh = _matrix(H, "H")
+    V, _, ldw = _matrix(W, "W", None, d, H.dtype)
     code = _dtype_code(H.dtype, "H")
     _vector(labels, "labels", T, torch.int32)
-    if W.shape[0] < 1 or d < 1:
+    if V < 1 or d < 1:
         raise ValueError("the vocabulary and the hidden size must be >= 1")
-    return T, W.shape[0], d, code
+    return T, V, d, code, ldh, ldw
 
 
 def vocab_loss(H, W, labels, scale=1.0, loss=None, lse=None, work=None, stream=None):
@@ -569,19 +602,21 @@ def vocab_loss(H, W, labels, scale=1.0, loss=None, lse=None, work=None, stream=N
     (loss and lse 0, its row of H is not used); a label >= V gives NaN. work,
     if given, holds vocab_loss_work_bytes(T, V, d, H.dtype) bytes."""
     torch = _torch()
-    T, V, d, code = _vocab_args(H, W, labels)
+    f32 = torch.float32
+    T, V, d, code, ldh, ldw = _vocab_args(H, W, labels)
     if loss is None:
-        loss = torch.empty(T, dtype=torch.float32, device=H.device)
+        loss = torch.empty(T, dtype=f32, device=H.device)
+    else:
+        _vector(loss, "loss", T, f32)
     if lse is None:
-        lse = torch.empty(T, dtype=torch.float32, device=H.device)
-    _vector(loss, "loss", T, torch.float32)
-    _vector(lse, "lse", T, torch.float32)
-    with _on_device(dict(H=H, W=W, labels=labels, loss=loss, lse=lse, work=work)):
-        need = _lib.load().nq_vocab_loss_work_bytes(T, V, d, code, 0)
-        work = _workspace(work, need, H.device)
-        _check(_lib.load().nq_vocab_loss(_p(H), _ld(H), _p(W), _ld(W), code, T, V, d, _p(labels),
-                                         float(scale), _p(loss), _p(lse), _p(work),
-                                         _stream(stream)), "nq_vocab_loss")
+        lse = torch.empty(T, dtype=f32, device=H.device)
+    else:
+        _vector(lse, "lse", T, f32)
+    with _on_device("H W labels loss lse work", H, W, labels, loss, lse, work):
+        lib = _lib.load()
+        work = _workspace(work, lib.nq_vocab_loss_work_bytes(T, V, d, code, 0), H.device)
+        _check(lib.nq_vocab_loss(_p(H), ldh, _p(W), ldw, code, T, V, d, _p(labels), float(scale),
+                                 _p(loss), _p(lse), _p(work), _stream(stream)), "nq_vocab_loss")
     return loss, lse
 
 
@@ -594,31 +629,30 @@ def vocab_loss_backward(H, W, labels, lse, dloss, scale=1.0, want_dH=True, want_
     nothing to dW. work, if given, holds
     vocab_loss_work_bytes(T, V, d, H.dtype, grad=True) bytes."""
     torch = _torch()
-    T, V, d, code = _vocab_args(H, W, labels)
+    T, V, d, code, ldh, ldw = _vocab_args(H, W, labels)
     _vector(lse, "lse", T, torch.float32)
     _vector(dloss, "dloss", T, torch.float32)
+    lddh = lddw = 0
     if dH is not None:
-        _matrix(dH, "dH", T, d, H.dtype)
+        _, _, lddh = _matrix(dH, "dH", T, d, H.dtype)
     elif want_dH:
-        dH = torch.empty((T, d), dtype=H.dtype, device=H.device)
+        dH, lddh = torch.empty((T, d), dtype=H.dtype, device=H.device), d
     if dW is not None:
-        _matrix(dW, "dW", V, d, H.dtype)
+        _, _, lddw = _matrix(dW, "dW", V, d, H.dtype)
     elif want_dW:
-        dW = torch.empty((V, d), dtype=H.dtype, device=H.device)
+        dW, lddw = torch.empty((V, d), dtype=H.dtype, device=H.device), d
     if dH is None and dW is None:
         raise ValueError("neither dH nor dW is wanted")
-    with _on_device(dict(H=H, W=W, labels=labels, lse=lse, dloss=dloss, dH=dH, dW=dW, work=work)):
+    with _on_device("H W labels lse dloss dH dW work", H, W, labels, lse, dloss, dH, dW, work):
         if T == 0:
             if dW is not None:
                 dW.zero_()
             return dH, dW
-        need = _lib.load().nq_vocab_loss_work_bytes(T, V, d, code, 1)
-        work = _workspace(work, need, H.device)
-        _check(_lib.load().nq_vocab_loss_backward(
-            _p(H), _ld(H), _p(W), _ld(W), code, T, V, d, _p(labels), float(scale), _p(lse),
-            _p(dloss), _p(dH), _ld(dH) if dH is not None else 0, _p(dW),
-            _ld(dW) if dW is not None else 0, _p(work), _stream(stream)),
-            "nq_vocab_loss_backward")
+        lib = _lib.load()
+        work = _workspace(work, lib.nq_vocab_loss_work_bytes(T, V, d, code, 1), H.device)
+        _check(lib.nq_vocab_loss_backward(
+            _p(H), ldh, _p(W), ldw, code, T, V, d, _p(labels), float(scale), _p(lse), _p(dloss),
+            _p(dH), lddh, _p(dW), lddw, _p(work), _stream(stream)), "nq_vocab_loss_backward")
     return dH, dW
 
 
@@ -725,7 +759,7 @@ class STERefiner:
         torch = _torch()
         f32 = torch.float32
         if isinstance(X, Act8):
-            _act8(X, "X", None, self.n)
+            _, _, ldc, lde = _act8(X, "X", None, self.n)
         elif X.dim() != 2 or X.shape[1] != self.n or X.stride(1) != 1:
             raise ValueError(f"X must be tokens x {self.n} with unit column stride")
         if Y.dim() != 2 or Y.shape[1] != self.m or Y.stride(1) != 1 or Y.shape[0] != X.shape[0]:
@@ -743,10 +777,10 @@ class STERefiner:
         if not 1 <= T <= self.max_tokens:
             raise ValueError(f"a batch holds 1 .. {self.max_tokens} tokens")
         if isinstance(X, Act8):
-            with _on_device(dict(codes=X.codes, exps=X.exps, Y=Y, rows=rows)):
+            with _on_device("codes exps Y rows", X.codes, X.exps, Y, rows):
                 _check(_lib.load().nq_ste_step_act8(
-                    C.c_void_p(self.handle), _p(X.codes), _ld(X.codes), _p(X.exps), _ld(X.exps),
-                    _ptr(Y, "Y", f32, 2, need_contig=False), _ld(Y), rp, T, float(lr),
+                    C.c_void_p(self.handle), _p(X.codes), ldc, _p(X.exps), lde,
+                    _ptr(Y, "Y", f32, 2, need_contig=False), _matrix(Y, "Y")[2], rp, T, float(lr),
                     _stream(stream)), "nq_ste_step_act8")
             return
         _check(_lib.load().nq_ste_step(

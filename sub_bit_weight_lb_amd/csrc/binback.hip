@@ -27,23 +27,25 @@
 // and an fp32 sum over r terms lose.
 //
 // Digit layout, written by rows_kernel: per 16 rows and 128 columns a block
-// of 2048 ND bytes, [digit][s][lane][16]: lane (li, g) = row li, word g of the
-// block's four 32-column words; byte 4 d + b of half s is column 8 b + 4 s + d
-// of the word, so that (w >> (4 s + d)) & 0x01010101 is dword d of the signs'
-// operand, one shift and one and for four columns. The signs go from memory
-// to registers and never to LDS.
+// of 2048 ND bytes, [digit][s][lane][16]: lane (li, g) = row li, a 32-column
+// word per lane group g; byte 4 d + b of half s is column 8 b + 4 s + d of the
+// word, so that (w >> (4 s + d)) & 0x01010101 is dword d of the signs'
+// operand, one shift and one and for four columns. Four blocks share 512
+// columns, 16 words: block k takes words 4 g + k, so that a lane's signs for
+// all four are 16 consecutive bytes.
 //
 // The two chains a -> p -> q and s1 dy -> dp -> da do not depend on each
-// other: each launch takes a step of both (grid z, or y).
+// other: each launch takes a step of both (grid z, or y), the one with more
+// columns first.
 //
 // wide_kernel (more than kThinMax rows): 256 threads, 2 x 2 waves of 16 MI
-// rows x 64 signs (MI = 4 for three digits, 2 for four: 192 and 128 registers
-// of sums). The digits of 64 columns are copied straight to LDS, double
-// buffered; the lanes' fragments are consecutive, so reads have no bank
-// conflicts. The digits share one expansion of the signs (32 vector
-// instructions against 4 MI ND products per wave and stage). Workgroup b runs
-// on XCD b % 8, and an XCD takes consecutive tiles, which share their rows'
-// digits in its L2.
+// rows x 16 NJ signs. A wave loads its digits from memory to registers two
+// steps of 64 columns ahead (a fragment is 1 KB in a row; the two waves of a
+// row share it in the L1), without a barrier. The signs of 512 columns are
+// copied to LDS as they are, double buffered, one barrier per eight steps;
+// the digits share one expansion of them (8 NJ vector instructions against
+// MI NJ ND products per step). Workgroup b runs on XCD b % 8, and an XCD takes
+// consecutive tiles, which share their rows' digits in its L2.
 // thin_kernel (few rows): a workgroup takes all rows and 16 signs' rows, its
 // waves split the columns and add up through LDS.
 #include "tune.h"
@@ -57,7 +59,6 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 constexpr int kDigit = 2048;      // bytes of a digit per 16 rows and 128 columns
-constexpr int kTile = 128;        // signs of a wide tile; its rows with three digits
 constexpr int kThinMax = 64;      // rows of a thin launch
 constexpr int kThinWaves = 8;
 constexpr int kMaxSplit = 8;      // slices of the columns (wide, few tiles)
@@ -154,11 +155,14 @@ __device__ __forceinline__ void to_digits(const float (&x)[4], float inv, uint32
   out[3] = __builtin_amdgcn_perm(e, d, 0x07060302u);
 }
 
+// 128-column blocks of a row of digits: whole groups of four
+__host__ __device__ __forceinline__ int64_t blocks(int64_t cols) { return (cols + 511) / 512 * 4; }
+
 // Eight rows per workgroup, a wave each (lane = word (lane / 8) of 256
 // columns, byte position lane % 8 in it), the digits of 256 columns exchanged
 // through LDS so that whole 128-byte lines are stored. TEAM: one row per
 // workgroup, its waves taking 256 columns in turn (few rows). blockIdx.y picks
-// one of two jobs. Columns past the end up to a multiple of 128 get zeros.
+// one of two jobs. Columns past the end up to a multiple of 512 get zeros.
 template <int ND, bool TEAM, class S0, class S1>
 __global__ __launch_bounds__(512) void rows_kernel(S0 s0, S1 s1, int64_t T, Digits o0, Digits o1) {
   constexpr int kRun = 8 * 16 + 16;   // eight rows of 16 bytes, padded against bank conflicts
@@ -172,7 +176,7 @@ __global__ __launch_bounds__(512) void rows_kernel(S0 s0, S1 s1, int64_t T, Digi
   const int64_t cols = job ? s1.cols : s0.cols;
   const Digits o = job ? o1 : o0;
   const bool in = row < T;
-  const int64_t nkb = (cols + 127) / 128, nch = (nkb + 1) / 2;
+  const int64_t nkb = blocks(cols), nch = nkb / 2;
   const int64_t first = TEAM ? wave : 0, stride = TEAM ? 8 : 1;
   const int w8 = lane >> 3, sd = lane & 7;
   auto load = [&](int64_t ch, float (&x)[4]) {
@@ -186,11 +190,24 @@ __global__ __launch_bounds__(512) void rows_kernel(S0 s0, S1 s1, int64_t T, Digi
     }
   };
   uint32_t mx = 0;
-  for (int64_t ch = first; ch < nch; ch += stride) {
-    float x[4];
-    load(ch, x);
+  auto look = [&](const float (&x)[4]) {
 #pragma unroll
     for (int b = 0; b < 4; ++b) mx = max(mx, __float_as_uint(x[b]) & 0x7fffffffu);
+  };
+  // the first runs of 256 columns stay in registers (4096 columns), the rest
+  // are read a second time
+  constexpr int kKeep = TEAM ? 2 : 16;
+  float keep[kKeep][4];
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k)
+    if (first + k * stride < nch) load(first + k * stride, keep[k]);
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k)
+    if (first + k * stride < nch) look(keep[k]);
+  for (int64_t ch = first + kKeep * stride; ch < nch; ch += stride) {
+    float x[4];
+    load(ch, x);
+    look(x);
   }
 #pragma unroll
   for (int q = 32; q > 0; q >>= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, q));
@@ -207,40 +224,44 @@ __global__ __launch_bounds__(512) void rows_kernel(S0 s0, S1 s1, int64_t T, Digi
 #pragma unroll
   for (int p = 0; p < ND; ++p) sum[p] = 0;
   uint8_t* block = o.planes + (row >> 4) * nkb * (ND * kDigit);
-  for (int64_t ch = first; ch < nch; ch += stride) {
-    float x[4];
-    load(ch, x);
+  auto write = [&](int64_t ch, float (&x)[4]) {
     if (bad) x[0] = x[1] = x[2] = x[3] = 0.0f;
     uint32_t dig[4];
     to_digits<ND>(x, inv, dig);
 #pragma unroll
     for (int p = 0; p < ND; ++p) sum[p] = __builtin_amdgcn_sdot4((int)dig[p], 0x01010101, sum[p], false);
+    // word w8 of these 256 columns: block w8 % 4 of the 512's four, lane group
+    // w8 / 4, plus two in the second half
     if (TEAM) {
-      const int64_t kb = 2 * ch + (w8 >> 2);
-      if (kb < nkb) {
-        uint8_t* dst = block + kb * (ND * kDigit) + (sd >> 2) * 1024 +
-                       ((w8 & 3) * 16 + (int)(row & 15)) * 16 + 4 * (sd & 3);
+      uint8_t* dst = block + ((ch >> 1) * 4 + (w8 & 3)) * (ND * kDigit) + (sd >> 2) * 1024 +
+                     (((w8 >> 2) + 2 * (int)(ch & 1)) * 16 + (int)(row & 15)) * 16 + 4 * (sd & 3);
 #pragma unroll
-        for (int p = 0; p < ND; ++p) *(uint32_t*)(dst + p * kDigit) = dig[p];
-      }
+      for (int p = 0; p < ND; ++p) *(uint32_t*)(dst + p * kDigit) = dig[p];
     } else {
-      // run (kb, digit, s, g) of eight rows, the row's 16 bytes
+      // run (block, digit, s, g) of eight rows, the row's 16 bytes
       uint8_t* b = buf[ch & 1];
 #pragma unroll
       for (int p = 0; p < ND; ++p)
-        *(uint32_t*)(b + ((((w8 >> 2) * ND + p) * 2 + (sd >> 2)) * 4 + (w8 & 3)) * kRun + wave * 16 +
+        *(uint32_t*)(b + ((((w8 & 3) * ND + p) * 2 + (sd >> 2)) * 2 + (w8 >> 2)) * kRun + wave * 16 +
                      4 * (sd & 3)) = dig[p];
       __syncthreads();   // (the other buffer is free: its readers passed this barrier)
       const int t = threadIdx.x;
       if (t < ND * 128) {
-        const int run = t >> 3, g = run & 3, s = (run >> 2) & 1, q = run >> 3;
-        const int64_t kb = 2 * ch + q / ND;
-        if (kb < nkb)
-          *(u32x4*)(o.planes + (((int64_t)blockIdx.x >> 1) * nkb + kb) * (ND * kDigit) +
-                    (q % ND) * kDigit + s * 1024 + (g * 16 + (blockIdx.x & 1) * 8 + (t & 7)) * 16) =
-              *(const u32x4*)(b + run * kRun + (t & 7) * 16);
+        const int run = t >> 3, g = (run & 1) + 2 * (int)(ch & 1), s = (run >> 1) & 1, q = run >> 2;
+        const int64_t kb = (ch >> 1) * 4 + q / ND;
+        *(u32x4*)(o.planes + (((int64_t)blockIdx.x >> 1) * nkb + kb) * (ND * kDigit) +
+                  (q % ND) * kDigit + s * 1024 + (g * 16 + (blockIdx.x & 1) * 8 + (t & 7)) * 16) =
+            *(const u32x4*)(b + run * kRun + (t & 7) * 16);
       }
     }
+  };
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k)
+    if (first + k * stride < nch) write(first + k * stride, keep[k]);
+  for (int64_t ch = first + kKeep * stride; ch < nch; ch += stride) {
+    float x[4];
+    load(ch, x);
+    write(ch, x);
   }
 #pragma unroll
   for (int p = 0; p < ND; ++p)
@@ -272,7 +293,10 @@ enum Epi : int {
   kGrad = 1,   // column sums of dy q; or dx = s2 da and column sums of da x^
 };
 constexpr int digits(int epi) { return epi == kProj ? 4 : 3; }
-constexpr int row_tiles(int epi) { return epi == kProj ? 2 : 4; }   // 16-row tiles per wave
+// A wide wave's tile in units of 16 rows and 16 signs: 128 and 144 registers
+// of sums
+constexpr int row_tiles(int epi) { return epi == kProj ? 1 : 2; }
+constexpr int sign_tiles(int epi) { return epi == kProj ? 8 : 6; }
 struct Prod {
   Digits a;                   // T rows, K columns
   const uint32_t* bits;       // N x K signs
@@ -281,7 +305,7 @@ struct Prod {
   void* P;
   int64_t ldp, slice;
   int split;
-  int64_t kbs;                // 128-column blocks per slice
+  int64_t kbs;                // blocks per slice, a multiple of 4
   // kGrad
   float* colp;                // row tiles x N partial column sums
   const void* dY;             // null: the second chain
@@ -302,30 +326,86 @@ __device__ __forceinline__ float value(float step, const i32x4& sum, const int (
   for (int p = ND - 2; p >= 0; --p) r = fmaf(r, 256.0f, (float)(2 * acc[p] - sum[p]));
   return r * step;
 }
-// What the sums acc of row t (step, sum) and sign row n give: stored, or
-// returned as a share of the column sum.
-template <int EPI, int D>
-__device__ __forceinline__ float finish(const Prod& a, int64_t t, int64_t n, float step,
-                                        const i32x4& sum, const int (&acc)[digits(EPI)], int z) {
+// The end of a wave's MI x NJ tiles from row t0 and sign row n0: acc[p][i][j]
+// of lane (g, li), element v is row 16 i + 4 g + v, sign row 16 j + li. Stores
+// kProj's values or dx, and adds the wave's share of the column sums to cs.
+// Loads are clamped to the last row and column and what they give dropped, so
+// that a row's loads go out together.
+template <int EPI, int D, int MI, int NJ>
+__device__ __forceinline__ void finish(const Prod& a, int64_t t0, int64_t n0, int g, int li, int z,
+                                       const i32x4 (&acc)[digits(EPI)][MI][NJ], float (&cs)[NJ]) {
   typedef typename Elem<D>::type E;
   constexpr int ND = digits(EPI);
-  if (t >= a.T || n >= a.N) return 0.0f;
-  if (EPI == kProj) {
-    if (a.split == 1) {
-      ((float*)a.P)[t * a.ldp + n] = value<ND>(step, sum, acc);
-    } else {   // a slice's share, exact; the first takes the digit sums
-      double r = 0.0;
+  int64_t n[NJ];
+  bool in[NJ];
+  float s2[NJ];
 #pragma unroll
-      for (int p = ND - 1; p >= 0; --p)
-        r = fma(r, 256.0, 2.0 * (double)acc[p] - (z == 0 ? (double)sum[p] : 0.0));
-      ((double*)a.P)[z * a.slice + t * a.ldp + n] = r * (double)step;
-    }
-    return 0.0f;
+  for (int j = 0; j < NJ; ++j) {
+    in[j] = n0 + 16 * j + li < a.N;
+    n[j] = in[j] ? n0 + 16 * j + li : a.N - 1;
+    s2[j] = EPI == kGrad && !a.dY ? a.s2[n[j]] : 0.0f;
   }
-  const float v = value<ND>(step, sum, acc);
-  if (a.dY) return Elem<D>::to(((const E*)a.dY)[t * a.lddy + n]) * v;
-  if (a.dX) ((E*)a.dX)[t * a.lddx + n] = Elem<D>::from(a.s2[n] * v);
-  return v * ((float)a.x.codes[t * a.x.ldc + n] * act8_step(a.x.exps[t * a.x.lde + (n >> 5)]));
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const bool row = t0 + 16 * i + 4 * g + v < a.T;
+      const int64_t t = row ? t0 + 16 * i + 4 * g + v : a.T - 1;
+      const float step = a.a.steps[t];
+      const i32x4 sum = a.a.sums[t];
+      float val[NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        int d[ND];
+#pragma unroll
+        for (int p = 0; p < ND; ++p) d[p] = acc[p][i][j][v];
+        val[j] = value<ND>(step, sum, d);
+      }
+      if (EPI == kProj) {
+        if (a.split == 1) {
+          float* out = (float*)a.P + t * a.ldp;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            if (row && in[j]) out[n[j]] = val[j];
+        } else {   // a slice's share, exact; the first takes the digit sums
+          double* out = (double*)a.P + z * a.slice + t * a.ldp;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            double r = 0.0;
+#pragma unroll
+            for (int p = ND - 1; p >= 0; --p)
+              r = fma(r, 256.0, 2.0 * (double)acc[p][i][j][v] - (z == 0 ? (double)sum[p] : 0.0));
+            if (row && in[j]) out[n[j]] = r * (double)step;
+          }
+        }
+      } else if (a.dY) {
+        const E* y = (const E*)a.dY + t * a.lddy;
+        E e[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) e[j] = y[n[j]];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) cs[j] += row && in[j] ? Elem<D>::to(e[j]) * val[j] : 0.0f;
+      } else {
+        const int8_t* c = a.x.codes + t * a.x.ldc;
+        const uint8_t* x = a.x.exps + t * a.x.lde;
+        int code[NJ];
+        uint32_t ex[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          code[j] = c[n[j]];
+          ex[j] = x[n[j] >> 5];
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          cs[j] += row && in[j] ? val[j] * ((float)code[j] * act8_step(ex[j])) : 0.0f;
+        if (a.dX) {
+          E* out = (E*)a.dX + t * a.lddx;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            if (row && in[j]) out[n[j]] = Elem<D>::from(s2[j] * val[j]);
+        }
+      }
+    }
 }
 // dwords of the signs' operand, half s of word w
 __device__ __forceinline__ i32x4 spread(uint32_t w, int s) {
@@ -337,121 +417,119 @@ __device__ __forceinline__ i32x4 spread(uint32_t w, int s) {
 
 template <int EPI, int D>
 __global__ __launch_bounds__(256, 2) void wide_kernel(Prod a0, Prod a1) {
-  constexpr int ND = digits(EPI), MI = row_tiles(EPI);
-  constexpr int kBlock = ND * kDigit, kRows = 32 * MI;
-  constexpr int kStage = 2 * MI * ND * 1024;   // 32 MI rows, 64 columns
-  __shared__ __align__(16) uint8_t lds[2 * kStage];
+  constexpr int ND = digits(EPI), MI = row_tiles(EPI), NJ = sign_tiles(EPI);
+  constexpr int kBlock = ND * kDigit, kRows = 32 * MI, kSigns = 32 * NJ;
+  __shared__ uint32_t lds[2][kSigns][16];   // signs of 512 columns
   const Prod& a = blockIdx.z ? a1 : a0;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, li = lane & 15;
   const int wm = wave >> 1, wn = wave & 1;
-  const int64_t ntn = (a.N + kTile - 1) / kTile, ntm = (a.T + kRows - 1) / kRows;
+  const int64_t ntn = (a.N + kSigns - 1) / kSigns, ntm = (a.T + kRows - 1) / kRows;
   const int64_t per = (ntn * ntm + 7) / 8;
   const int64_t tile = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
   const int z = blockIdx.y;
   if ((int64_t)(blockIdx.x >> 3) >= per || tile >= ntn * ntm || z >= a.split) return;
   const int64_t tm = tile / ntn, tn = tile - tm * ntn;
-  const int64_t nkb = (a.K + 127) / 128, nw = (a.K + 31) / 32;
+  const int64_t nkb = blocks(a.K), nw = (a.K + 31) / 32;
   const int64_t kb0 = z * a.kbs, kb1 = min(nkb, kb0 + a.kbs);
-  // this tile's digits: 2 MI blocks of 16 rows, nkb blocks apart (rows past
-  // T hold no digits of the call: whatever they give is dropped at the end)
-  const __amdgpu_buffer_rsrc_t pr = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(a.a.planes + tm * 2 * MI * nkb * kBlock), (short)0, (int)(2 * MI * nkb * kBlock),
+  // signs of the tile: rows past N are clamped (dropped at the end), words
+  // past a row's last read what follows, or 0 past the last row's: they meet
+  // zero digits
+  const int64_t rows = min<int64_t>(kSigns, a.N - tn * kSigns);
+  const __amdgpu_buffer_rsrc_t br = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(a.bits + tn * kSigns * a.ldb), (short)0, (int)(((rows - 1) * a.ldb + nw) * 4),
       0x00020000);
-  auto copy = [&](int stage, int64_t kb, int s) {
-    constexpr int C = 2 * MI * ND / 4;   // copies of 1 KB per wave
+  // a copy takes 4 rows x 16 words; row r keeps words 4 q .. 4 q + 3 in slot
+  // q ^ ((r >> 2) & 3)
+  auto signs = [&](int64_t sb) {
+    uint32_t* st = &lds[sb & 1][0][0];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int i = wave * C + c, rt = i / ND, p = i - ND * rt;
+    for (int c = 0; c < kSigns / 16; ++c) {
+      const int r0 = (wave * (kSigns / 16) + c) * 4, r = r0 + (lane >> 4);
+      const int w = ((((lane >> 2) & 3) ^ ((r >> 2) & 3)) << 2) | (lane & 3);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          pr, (lds_ptr_t)(lds + stage * kStage + i * 1024), 16, lane * 16,
-          (int)((rt * nkb + kb) * kBlock) + p * kDigit + s * 1024, 0, 0);
+          br, (lds_ptr_t)(st + r0 * 16), 4, (int)((min<int64_t>(r, rows - 1) * a.ldb + w) * 4),
+          (int)(sb * 64), 0, 0);
     }
   };
-  // the lane's sign rows (clamped: rows past N are dropped at the end; words
-  // past a row's last meet zero digits)
-  const uint32_t* bp[4];
+  // the wave's digits: MI rows of blocks, nkb blocks apart (rows past T hold no
+  // digits of the call: whatever they give is dropped at the end)
+  const uint8_t* dp = a.a.planes + (tm * 2 + wm) * MI * nkb * kBlock + lane * 16;
+  i32x4 fr[2][MI][ND];
+  auto digits_of = [&](int64_t kb, int s) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    bp[j] = a.bits + min<int64_t>(tn * kTile + wn * 64 + j * 16 + li, a.N - 1) * a.ldb;
-  uint32_t word[4], next[4];
-  auto words = [&](uint32_t (&w)[4], int64_t kb) {
-    const int64_t at = min<int64_t>(4 * kb + g, nw - 1);
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = bp[j][at];
+      for (int p = 0; p < ND; ++p)
+        fr[s][i][p] = *(const i32x4*)(dp + (i * nkb + kb) * kBlock + p * kDigit + s * 1024);
   };
-  i32x4 acc[ND][MI][4];
+  i32x4 acc[ND][MI][NJ];
 #pragma unroll
   for (int p = 0; p < ND; ++p)
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[p][i][j] = i32x4{0, 0, 0, 0};
-  auto mult = [&](int stage, int s) {
-    i32x4 b[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = spread(word[j], s);
-    const uint8_t* st = lds + stage * kStage + lane * 16;
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int p = 0; p < ND; ++p) {
-        const i32x4 f = *(const i32x4*)(st + ((wm * MI + i) * ND + p) * 1024);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[p][i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f, b[j], acc[p][i][j], 0, 0, 0);
-      }
-  };
-  // each wave waits for its own copies and reads, then for the other waves
-  auto sync = [&]() {
-    __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
-    asm volatile("s_barrier" ::: "memory");
-  };
-  copy(0, kb0, 0);
-  words(word, kb0);
+      for (int j = 0; j < NJ; ++j) acc[p][i][j] = i32x4{0, 0, 0, 0};
+  digits_of(kb0, 0);
+  digits_of(kb0, 1);
+  signs(kb0 >> 2);
+  const int at = (wn * 16 * NJ + li) * 16 + ((g ^ (li >> 2)) << 2);
   for (int64_t kb = kb0; kb < kb1; ++kb) {
-    sync();   // stage 0 holds (kb, 0); everyone is done with stage 1
-    copy(1, kb, 1);
-    words(next, kb + 1);
-    mult(0, 0);
-    sync();   // stage 1 holds (kb, 1); everyone is done with stage 0
-    if (kb + 1 < kb1) copy(0, kb + 1, 0);
-    mult(1, 1);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) word[j] = next[j];
-  }
-  const int64_t t0 = tm * kRows + wm * 16 * MI, n0 = tn * kTile + wn * 64;
-  float cs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int64_t t = t0 + 16 * i + 4 * g + v;
-      const float step = a.a.steps[min(t, a.T - 1)];
-      const i32x4 sum = a.a.sums[min(t, a.T - 1)];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        int d[ND];
-#pragma unroll
-        for (int p = 0; p < ND; ++p) d[p] = acc[p][i][j][v];
-        cs[j] += finish<EPI, D>(a, t, n0 + 16 * j + li, step, sum, d, z);
-      }
+    if ((kb & 3) == 0) {
+      // the copies of this 512 have landed, everyone is done with the last
+      __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
+      asm volatile("s_barrier" ::: "memory");
+      if (kb + 4 < kb1) signs((kb >> 2) + 1);
     }
+    const uint32_t* st = &lds[(kb >> 2) & 1][0][0] + at + (kb & 3);
+    uint32_t word[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) word[j] = st[j * 256];
+    const int64_t ahead = min(kb + 1, kb1 - 1);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      i32x4 b = spread(word[0], s);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const i32x4 nb = spread(word[j + 1 < NJ ? j + 1 : j], s);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int p = 0; p < ND; ++p)
+            acc[p][i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fr[s][i][p], b, acc[p][i][j], 0, 0, 0);
+        // the next signs are spread between the products
+#pragma unroll
+        for (int q = 0; q < MI * ND; ++q) {
+          __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x2, 2, 0);
+        }
+        b = nb;
+      }
+      // (kept here: the next step's products must not move above these loads)
+      digits_of(ahead, s);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  float cs[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) cs[j] = 0.0f;
+  finish<EPI, D, MI, NJ>(a, tm * kRows + wm * 16 * MI, tn * kSigns + wn * 16 * NJ, g, li, z, acc, cs);
   if (EPI == kProj) return;
   // the tile's column sums: the rows of a lane, then the four lanes of a
   // column, then the two row halves, each in a fixed order
   __syncthreads();
-  float* half = (float*)lds;   // [wm][128]
+  float* half = (float*)lds;   // [wm][kSigns]
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < NJ; ++j) {
     cs[j] += __shfl_xor(cs[j], 16);
     cs[j] += __shfl_xor(cs[j], 32);
-    if (g == 0) half[wm * 128 + wn * 64 + 16 * j + li] = cs[j];
+    if (g == 0) half[wm * kSigns + wn * 16 * NJ + 16 * j + li] = cs[j];
   }
   __syncthreads();
   const int c = threadIdx.x;
-  if (c < 128 && tn * kTile + c < a.N) a.colp[tm * a.N + tn * kTile + c] = half[c] + half[128 + c];
+  if (c < kSigns && tn * kSigns + c < a.N)
+    a.colp[tm * a.N + tn * kSigns + c] = half[c] + half[kSigns + c];
 }
 
 // All T <= 16 MT rows and 16 sign rows per workgroup; wave w takes the
@@ -465,15 +543,15 @@ __global__ __launch_bounds__(64 * kThinWaves) void thin_kernel(Prod a0, Prod a1)
   const int g = lane >> 4, li = lane & 15;
   const int64_t n0 = (int64_t)blockIdx.x * 16;
   if (n0 >= a.N) return;
-  const int64_t nkb = (a.K + 127) / 128, nw = (a.K + 31) / 32;
+  const int64_t nkb = blocks(a.K), nw = (a.K + 31) / 32;
   const uint32_t* bp = a.bits + min<int64_t>(n0 + li, a.N - 1) * a.ldb;
-  i32x4 acc[ND][MT];
+  i32x4 acc[ND][MT][1];
 #pragma unroll
   for (int p = 0; p < ND; ++p)
 #pragma unroll
-    for (int i = 0; i < MT; ++i) acc[p][i] = i32x4{0, 0, 0, 0};
+    for (int i = 0; i < MT; ++i) acc[p][i][0] = i32x4{0, 0, 0, 0};
   for (int64_t kb = wave; kb < nkb; kb += kThinWaves) {
-    const uint32_t w = bp[min<int64_t>(4 * kb + g, nw - 1)];
+    const uint32_t w = bp[min<int64_t>((kb >> 2) * 16 + 4 * g + (kb & 3), nw - 1)];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const i32x4 b = spread(w, s);
@@ -483,7 +561,7 @@ __global__ __launch_bounds__(64 * kThinWaves) void thin_kernel(Prod a0, Prod a1)
         for (int p = 0; p < ND; ++p) {
           const i32x4 f = *(const i32x4*)(a.a.planes + (i * nkb + kb) * kBlock + p * kDigit +
                                           s * 1024 + lane * 16);
-          acc[p][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f, b, acc[p][i], 0, 0, 0);
+          acc[p][i][0] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f, b, acc[p][i][0], 0, 0, 0);
         }
     }
   }
@@ -492,31 +570,22 @@ __global__ __launch_bounds__(64 * kThinWaves) void thin_kernel(Prod a0, Prod a1)
   for (int p = 0; p < ND; ++p) {
     if (p) __syncthreads();
 #pragma unroll
-    for (int i = 0; i < MT; ++i) red[wave][i][lane] = acc[p][i];
+    for (int i = 0; i < MT; ++i) red[wave][i][lane] = acc[p][i][0];
     __syncthreads();
     if (wave == 0) {
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int w = 1; w < kThinWaves; ++w) acc[p][i] += red[w][i][lane];
+        for (int w = 1; w < kThinWaves; ++w) acc[p][i][0] += red[w][i][lane];
     }
   }
   if (wave) return;
-  float cs = 0.0f;
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int64_t t = 16 * i + 4 * g + v;
-      int d[ND];
-#pragma unroll
-      for (int p = 0; p < ND; ++p) d[p] = acc[p][i][v];
-      cs += finish<EPI, D>(a, t, n0 + li, a.a.steps[min(t, a.T - 1)], a.a.sums[min(t, a.T - 1)], d, 0);
-    }
+  float cs[1] = {0.0f};
+  finish<EPI, D, MT, 1>(a, 0, n0, g, li, 0, acc, cs);
   if (EPI == kProj) return;
-  cs += __shfl_xor(cs, 16);
-  cs += __shfl_xor(cs, 32);
-  if (g == 0 && n0 + li < a.N) a.colp[n0 + li] = cs;
+  cs[0] += __shfl_xor(cs[0], 16);
+  cs[0] += __shfl_xor(cs[0], 32);
+  if (g == 0 && n0 + li < a.N) a.colp[n0 + li] = cs[0];
 }
 
 // ds1 and ds2 from the partial column sums of nt row tiles, in fp64: thread
@@ -555,14 +624,18 @@ struct Work {
 };
 // Slices of the columns of a chain's first product: enough tiles for two
 // workgroups on each of the 256 CUs (the two chains run together), at least
-// four blocks of 128 each.
+// 512 columns each.
+constexpr int64_t tiles_of(int epi, int64_t T, int64_t N) {
+  const int64_t rows = 32 * row_tiles(epi), signs = 32 * sign_tiles(epi);
+  return ((T + rows - 1) / rows) * ((N + signs - 1) / signs);
+}
 int proj_split(int64_t T, int64_t r, int64_t K) {
   if (T <= kThinMax) return 1;
-  const int64_t rows = 32 * row_tiles(kProj);
-  const int64_t tiles = 2 * ((T + rows - 1) / rows) * ((r + kTile - 1) / kTile);
-  const int64_t nkb = (K + 127) / 128;
-  return (int)std::max<int64_t>(1, std::min({(int64_t)kMaxSplit, 512 / tiles, nkb / 4}));
+  const int64_t tiles = 2 * tiles_of(kProj, T, r);
+  return (int)std::max<int64_t>(1, std::min({(int64_t)kMaxSplit, 512 / tiles, blocks(K) / 4}));
 }
+// rows per partial column sum
+constexpr int64_t kSumRows = 32 * row_tiles(kGrad);
 Work carve(char* base, int64_t m, int64_t n, int64_t r, int64_t T) {
   Work w{};
   int64_t off = 0;
@@ -571,11 +644,11 @@ Work carve(char* base, int64_t m, int64_t n, int64_t r, int64_t T) {
     off += (bytes + 255) / 256 * 256;
     return p;
   };
-  const int64_t Tp = round_up(T, T <= kThinMax ? 16 : kTile), nt = (T + kTile - 1) / kTile;
+  const int64_t Tp = round_up(T, T <= kThinMax ? 16 : kSumRows), nt = (T + kSumRows - 1) / kSumRows;
   for (int c = 0; c < 2; ++c) {
     const int64_t K = c ? m : n;
     const int sp = proj_split(T, r, K);
-    w.d[c].planes = (uint8_t*)take(Tp * std::max(4 * round_up(K, 128), 3 * round_up(r, 128)));
+    w.d[c].planes = (uint8_t*)take(Tp * 128 * std::max(4 * blocks(K), 3 * blocks(r)));
     w.d[c].steps = (float*)take(4 * T);
     w.d[c].sums = (i32x4*)take(16 * T);
     w.P[c] = take(sp == 1 ? 4 * T * r : 8 * T * r * sp);
@@ -609,10 +682,13 @@ hipError_t products(const Prod& a, const Prod& b, hipStream_t s) {
       hipLaunchKernelGGL((thin_kernel<EPI, D, 4>), grid, block, 0, s, a, b);
     return hipGetLastError();
   }
-  const int64_t rows = 32 * row_tiles(EPI);
-  const int64_t tiles = ((a.T + rows - 1) / rows) * ((N + kTile - 1) / kTile);
+  const int64_t tiles = tiles_of(EPI, a.T, N);
   const dim3 grid((unsigned)((tiles + 7) / 8 * 8), (unsigned)std::max(a.split, b.split), 2);
-  hipLaunchKernelGGL((wide_kernel<EPI, D>), grid, dim3(256), 0, s, a, b);
+  // the longer chain's tiles start first
+  if (a.K >= b.K)
+    hipLaunchKernelGGL((wide_kernel<EPI, D>), grid, dim3(256), 0, s, a, b);
+  else
+    hipLaunchKernelGGL((wide_kernel<EPI, D>), grid, dim3(256), 0, s, b, a);
   return hipGetLastError();
 }
 
@@ -620,7 +696,7 @@ template <int D>
 hipError_t run(const BinBack& a, hipStream_t s) {
   typedef typename Elem<D>::type E;
   const Work w = carve((char*)a.work, a.m, a.n, a.r, a.T);
-  const bool one = a.T <= kTile;   // a single row tile: its column sums are the result
+  const bool one = a.T <= kSumRows;   // a single row tile: its column sums are the result
   hipError_t e;
   // a and s1 dy, then p and dp
   if ((e = rows<digits(kProj)>(SrcAct{a.x, a.s2, a.n},
@@ -628,14 +704,14 @@ hipError_t run(const BinBack& a, hipStream_t s) {
     return e;
   Prod p[2]{};
   for (int c = 0; c < 2; ++c) {
-    const int64_t K = c ? a.m : a.n, nkb = (K + 127) / 128;
+    const int64_t K = c ? a.m : a.n, nkb = blocks(K);
     p[c].a = w.d[c];
     p[c].bits = c ? a.ut : a.vt;
     p[c].ldb = c ? a.ldut : a.ldvt;
     p[c].T = a.T; p[c].N = a.r; p[c].K = K;
     p[c].P = w.P[c]; p[c].ldp = a.r; p[c].slice = a.T * a.r;
     p[c].split = proj_split(a.T, a.r, K);
-    p[c].kbs = (nkb + p[c].split - 1) / p[c].split;
+    p[c].kbs = round_up((nkb + p[c].split - 1) / p[c].split, 4);
     p[c].split = (int)((nkb + p[c].kbs - 1) / p[c].kbs);   // (no empty slice)
   }
   if ((e = products<kProj, D>(p[0], p[1], s)) != hipSuccess) return e;
@@ -644,7 +720,7 @@ hipError_t run(const BinBack& a, hipStream_t s) {
                                SrcProj{w.P[1], a.r, a.T * a.r, p[1].split, a.r}, a.T, w, s)) != hipSuccess)
     return e;
   for (int c = 0; c < 2; ++c) {
-    p[c].K = a.r; p[c].split = 1; p[c].kbs = (a.r + 127) / 128;
+    p[c].K = a.r; p[c].split = 1; p[c].kbs = blocks(a.r);
   }
   p[0].bits = a.u; p[0].ldb = a.ldu; p[0].N = a.m;
   p[0].dY = a.dY; p[0].lddy = a.lddy;
@@ -655,7 +731,7 @@ hipError_t run(const BinBack& a, hipStream_t s) {
   if ((e = products<kGrad, D>(p[0], p[1], s)) != hipSuccess) return e;
   if (one) return hipSuccess;
   hipLaunchKernelGGL(colsum_kernel, dim3((unsigned)((a.m + a.n + 31) / 32)), dim3(256), 0, s,
-                     w.cp1, a.m, a.ds1, w.cp2, a.n, a.ds2, (a.T + kTile - 1) / kTile);
+                     w.cp1, a.m, a.ds1, w.cp2, a.n, a.ds2, (a.T + kSumRows - 1) / kSumRows);
   return hipGetLastError();
 }
 

@@ -3,6 +3,7 @@
 // such a checkpoint (binback.hip) and the loss over a large vocabulary with its
 // gradient (vocab.hip). Each call only checks its arguments and enqueues
 // kernels on the caller's stream: no allocation, no wait.
+#include <algorithm>
 #include <cmath>
 #include <string>
 
@@ -136,6 +137,8 @@ nq_status nq_binary_matmul_backward(const uint32_t* U_bits, int64_t ldu, const u
   if (ldut < mw) return bad("ldut < ceil(m/32)");
   if (ldv < rw) return bad("ldv < ceil(r/32)");
   if (ldvt < nw) return bad("ldvt < ceil(n/32)");
+  if (std::max(std::max(ldu, ldut), std::max(ldv, ldvt)) > kMaxDim)
+    return bad("the signs' row strides must be <= 2^21 words");
   const nq_status st = check_act8(codes, ldc, exps, lde, n);
   if (st != NQ_OK) return st;
   if (lddy < m) return bad("lddy < m");

@@ -149,11 +149,11 @@ def test_loss_refuses_outputs_of_another_shape(no_library):
 def test_tensors_must_share_a_gpu():
     class Fake:
         def __init__(self, index):
-            self.is_cuda, self.device = True, torch.device("cuda", index)
-    with pytest.raises(ValueError, match="cuda:1"):
-        nq._on_device(dict(a=Fake(0), b=None, c=Fake(1)))
-    with pytest.raises(TypeError, match="CUDA"):
-        nq._on_device(dict(a=torch.zeros(1)))
+            self.device = torch.device("cuda", index)
+    with pytest.raises(ValueError, match="c is on cuda:1"):
+        nq._on_device("a b c", Fake(0), None, Fake(1))
+    with pytest.raises(TypeError, match="b must be a CUDA"):
+        nq._on_device("a b", None, torch.zeros(1))
 
 
 # ---------------------------------------------------------------- C ABI
