@@ -10,27 +10,32 @@
 // A negative label is ignored: loss 0, lse 0, no gradient, and its row of H
 // is never used (it may hold NaN).
 //
-// All products run on the bf16 or fp16 matrix cores as C = A B^T with both
-// operands k-contiguous, from one kernel (mma_kernel) with an epilogue each:
-//   kStat  z of 256 words x 256 tokens -> per token the largest and the sum
+// All products run on the bf16 or fp16 matrix cores from one kernel
+// (mma_kernel) with an epilogue each, a piece of the vocabulary at a time:
+//   kStat  z of a tile of words x tokens -> per token the largest and the sum
 //          of exponentials over each half of the tile; stat_kernel joins them;
 //   kGrad  z again, G = exp(z - lse) - [label] rounded to the operands' type,
-//          written both ways (G and G^T) for a piece of the vocabulary;
+//          [token][word];
 //   kDh    dH += G W over the piece (fp32 sums, slices of the piece when
 //          there are few tiles; dh_kernel adds the slices at the end);
 //   kDw    dW = G^T H, the piece's rows.
 // 8 T V d operations in place of the 6 T V d that keeping T V logits would
-// need. W^T of the piece and H^T are laid out by transposing copies.
+// need. Each of H, W and G is read in the one layout it has: an operand whose
+// k runs down the rows (W in kDh, H and G in kDw) is transposed on its way from
+// LDS to the registers, by ds_read_b64_tr_b16.
 //
 // Types: bf16 and fp16 operands are exact and sums are fp32; G is rounded to
 // the operands' type once (half a unit, like the results). fp16's G is scaled
 // to 2^15 at its largest, so that probabilities down to 2^-29 keep all their
-// bits. fp32 operands are split into three bf16 terms x = h + m + l (exact)
-// and multiplied as h h + h m + m h + h l + l h + m m, six passes over k: what
-// is left out is below 2^-24 of a product.
+// bits. fp32 operands are scaled by a power of two each (H, W and G to 2^15 at
+// their largest) and split into two fp16 terms x = h + l, which hold x to
+// 2^-24 of itself or 2^-39 of the largest; x y = h h + h l + l h, three passes
+// over k, leaves out l l, at most 2^-24 of the product. (Three bf16 terms and
+// six passes measured 1.9 times the time at no smaller error.)
 //
 // Few tokens (up to 64, the loss alone): score_kernel streams W once, 64 words
-// per workgroup, its waves sharing the columns; fp32 is split in registers.
+// per workgroup, its waves sharing the columns; fp32 is split in registers,
+// into three bf16 terms and six products, which need no scale.
 #include "tune.h"
 
 #include <algorithm>
@@ -40,17 +45,19 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
+typedef __attribute__((address_space(3))) s16x4* lds_tr_t;
 
-constexpr int BK = 64;            // k per stage: 128-byte rows in LDS
+constexpr int BK = 64;            // k per stage
 constexpr int kScoreMax = 64;     // tokens of score_kernel
 constexpr float kNegInf = -__builtin_inff();
+constexpr float kTop16 = 32768.0f;   // what fp16 terms are scaled to
 
-// one 16 x 16 x 32 product; D says how the 16-bit operands read (fp32 tensors
-// come as bf16 terms)
-template <int D>
+// one 16 x 16 x 32 product of 16-bit operands
+template <bool F16>
 __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
-  if constexpr (D == kF16)
+  if constexpr (F16)
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
   else
@@ -58,62 +65,56 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// Terms of an operand of type D: one, or three for fp32.
-constexpr int terms(int D) { return D == kF32 ? 3 : 1; }
-constexpr int passes(int D) { return D == kF32 ? 6 : 1; }
-// term of A and of B in pass s (2 bits each)
-__device__ __forceinline__ int term_a(int s) { return (0x250 >> (2 * s)) & 3; }   // 0 0 1 1 2 0
-__device__ __forceinline__ int term_b(int s) { return (0x844 >> (2 * s)) & 3; }   // 0 1 0 1 0 2
+// 16-bit terms of an operand of type D, and passes over k
+constexpr int terms(int D) { return D == kF32 ? 2 : 1; }
+constexpr int passes(int D) { return D == kF32 ? 3 : 1; }
 
-// x as its 16-bit terms of type D. Not finite: the first term alone.
+// x (already scaled) as its terms of type D. Not finite: the first term alone.
 template <int D>
 __device__ __forceinline__ void split(float x, uint16_t (&t)[terms(D)]) {
   if constexpr (D == kF32) {
-    t[0] = Elem<kBF16>::from(x);
-    const float r = x - Elem<kBF16>::to(t[0]);
+    const _Float16 h = (_Float16)x;
+    const float r = x - (float)h;
     const bool fin = (__float_as_uint(r) & 0x7fffffffu) < 0x7f800000u;
-    t[1] = fin ? Elem<kBF16>::from(r) : (uint16_t)0;
-    t[2] = fin ? Elem<kBF16>::from(r - Elem<kBF16>::to(t[1])) : (uint16_t)0;
+    t[0] = __builtin_bit_cast(uint16_t, h);
+    t[1] = fin ? __builtin_bit_cast(uint16_t, (_Float16)r) : (uint16_t)0;
   } else {
     t[0] = __builtin_bit_cast(uint16_t, Elem<D>::from(x));
   }
 }
-// an element's own bits as terms (16-bit types pass through)
-template <int D>
-__device__ __forceinline__ void split_elem(typename Elem<D>::type x, uint16_t (&t)[terms(D)]) {
-  if constexpr (D == kF32)
-    split<D>(x, t);
-  else
-    t[0] = __builtin_bit_cast(uint16_t, x);
-}
 
-// A k-contiguous operand: `rows` rows of 16-bit values, `ld` apart, whose
-// terms are `plane` apart within a row.
+// A 16-bit operand of the products, `ld` apart, its terms `plane` apart within
+// a row. k-contiguous: `rows` rows of k values. k-major: k runs down the rows
+// and `rows` counts the columns. kv: the k that exist (past them a
+// k-contiguous operand reads zeros, a k-major one its last row, which meets
+// zeros of the other).
 struct Opnd {
   const uint16_t* p;
-  int64_t ld, plane, rows;
+  int64_t ld, plane, rows, kv;
 };
 
 enum Epi : int { kStat = 0, kGrad = 1, kDh = 2, kDw = 3 };
 struct Mma {
-  Opnd A, B;                // C (M x N) = A B^T; M = A.rows, N = B.rows
+  Opnd A, B;                // C (M x N), M = A.rows, N = B.rows
   int64_t K;                // a multiple of 64
   int64_t k_slice;          // k per slice (grid y), a multiple of 64
-  float scale;
+  const float* zs;          // kStat, kGrad: the factor of the products (one float)
   // kStat, kGrad: rows are words v0 .., columns tokens
   int64_t v0;
   const int32_t* labels;
-  float *top, *sum, *hit;   // kStat: partials [2 ceil(M / 256)][N], target logits
+  float *top, *sum, *hit;   // kStat: partials [half tiles of words][N], target logits
   const float *lse, *wn;    // kGrad: lse and normalised dloss per token
-  uint16_t *G, *Gt;         // kGrad: G [token][term][gld], Gt [word][term][gtld]
-  int64_t gld, gtld;
+  uint16_t* G;              // kGrad: [token][term][gld]
+  int64_t gld;
   // kDh, kDw: rows are the d columns, columns tokens or words
   float* part;              // kDh: slices of N x ldo fp32
   int64_t slice, ldo;
   int add;                  // kDh: add to what part holds
-  const float* post;        // kDw: the factor taken out of wn (one float)
+  const float* post;        // kDw: the factor of the results (one float)
   void* out;                // kDw
 };
+constexpr bool a_major(int epi) { return epi == kDh || epi == kDw; }
+constexpr bool b_major(int epi) { return epi == kDw; }
 
 // Tile order: workgroup b runs on XCD b % 8, which takes consecutive indices;
 // indices run down bands of 4 tile rows, so that the 32 tiles an XCD holds at
@@ -129,16 +130,114 @@ __device__ __forceinline__ bool tile_of(int64_t ntm, int64_t ntn, int64_t& tm, i
   return true;
 }
 
-// 512 threads, WM x WN waves of 16 MI x 16 NI. Rows of 64 k (128 bytes, eight
-// 16-byte slots) go straight from memory to LDS, double buffered; row r keeps
-// k-octet q in slot q ^ ((r >> 1) & 7), so that the 16 lanes that read one
-// octet of 16 consecutive rows hit distinct banks.
+// One operand's tile: R rows (k-contiguous) or columns (k-major) of 64 k, R *
+// 128 bytes per stage, brought from memory to LDS by NC copies of 1 KB per
+// wave.
+//   k-contiguous: LDS rows of 64 k (128 bytes, eight 16-byte slots); row r
+//   keeps k-octet q in slot q ^ ((r >> 1) & 7), so that the 16 lanes that read
+//   one octet of 16 consecutive rows hit distinct banks.
+//   k-major: LDS rows of R columns (2 R bytes, 32-byte chunks); row k keeps
+//   chunk c in place c ^ ((k & 3) + 4 ((k >> 3) & 1)), so that the eight rows
+//   that half a wave reads at once hit distinct banks.
+// A fragment is 16 rows or columns of 32 k: lane (li, g) holds row li, k 8 g ..
+// 8 g + 7. In the k-major form two transposing reads of 4 k each fill it: in
+// each 16 lanes, lane i addresses row i / 4, columns 4 (i % 4) .., and receives
+// column i.
+template <int R, int NC, bool MAJOR>
+struct Tile {
+  const uint16_t* base;
+  int64_t ld, kv;
+  uint32_t off[NC];       // byte offset of the lane in each copy
+  int32_t krow[MAJOR ? NC : 1];
+  int koct[2];            // k-contiguous: the lane's octet in even and odd copies
+
+  __device__ __forceinline__ void init(const Opnd& o, int64_t r0, int wave, int lane) {
+    ld = o.ld;
+    kv = o.kv;
+    if constexpr (MAJOR) {
+      base = o.p + r0;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int pos = (wave * NC + c) * 1024 + lane * 16, k = pos / (2 * R);
+        const int slot = (pos - k * 2 * R) >> 4;
+        const int chunk = (slot >> 1) ^ ((k & 3) + 4 * ((k >> 3) & 1));
+        // (columns past the last octet are clamped: what they give is dropped)
+        const int64_t col = min<int64_t>(16 * chunk + 8 * (slot & 1), ((o.rows + 7) / 8 - 1) * 8 - r0);
+        krow[c] = k;
+        off[c] = (uint32_t)(col * 2);
+      }
+    } else {
+      base = o.p + r0 * o.ld;
+      koct[0] = (lane & 7) ^ (lane >> 4);
+      koct[1] = (lane & 7) ^ (4 + (lane >> 4));
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int cc = wave * NC + c, r = cc * 8 + (lane >> 3);
+        // (rows past the last are clamped: what they give is dropped)
+        off[c] = (uint32_t)((min<int64_t>(r, o.rows - 1 - r0) * o.ld + 8 * koct[cc & 1]) * 2);
+      }
+    }
+  }
+  // the 64 k from k on, of the term `plane` elements into the rows
+  __device__ __forceinline__ void copy(uint8_t* st, int wave, int64_t k, int64_t plane) const {
+    const uint16_t* p = base + (MAJOR ? k * ld : k) + plane;
+    const __amdgpu_buffer_rsrc_t rs =
+        __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, 0x7fffffff, 0x00020000);
+    const bool tail = k + BK > kv;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      uint32_t o = off[c];
+      if constexpr (MAJOR) {
+        const int64_t row = tail ? min<int64_t>(krow[c], kv - 1 - k) : krow[c];
+        o += (uint32_t)(row * ld * 2);
+      } else {
+        // past the descriptor's range: zeros
+        if (tail && k + 8 * koct[(wave * NC + c) & 1] >= kv) o = 0x80000000u;
+      }
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(st + (wave * NC + c) * 1024), 16,
+                                               (int)o, 0, 0, 0);
+    }
+  }
+};
+// Fragments of the N 16-row groups from group g0 on, half h (32 k) of a stage.
+template <int R, int N, bool MAJOR>
+struct Reader {
+  int at[MAJOR ? N : 2];
+
+  __device__ __forceinline__ void init(int g0, int g, int li) {
+    if constexpr (MAJOR) {
+      const int f = (li >> 2) + 4 * (g & 1);
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        at[j] = (8 * g + (li >> 2)) * 2 * R + (((g0 + j) ^ f) << 5) + (li & 3) * 8;
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) at[h] = (g0 * 16 + li) * 128 + (((4 * h + g) ^ (li >> 1)) << 4);
+    }
+  }
+  __device__ __forceinline__ u32x4 read(uint8_t* st, int j, int h) const {
+    if constexpr (MAJOR) {
+      uint8_t* p = st + at[j] + 32 * h * 2 * R;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_tr_t)p);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_tr_t)(p + 4 * 2 * R));
+      const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
+      return u32x4{a[0], a[1], b[0], b[1]};
+    } else {
+      return *(const u32x4*)(st + at[h] + j * 2048);
+    }
+  }
+};
+
+// WM x WN waves of 16 MI x 16 NI. Two stages of 64 k in LDS; the copies of a
+// stage go out two half-stages before its first fragments are read, and each
+// half's fragments are read while the half before it multiplies.
 template <int D, int EPI, int WM, int WN, int MI, int NI>
 __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
   constexpr int BM = 16 * MI * WM, BN = 16 * NI * WN, W = WM * WN;
   constexpr int kStage = (BM + BN) * 128;
-  constexpr int CA = BM / 8 / W, CB = BN / 8 / W;   // copies of 8 rows per wave and stage
+  constexpr int CA = BM / 8 / W, CB = BN / 8 / W;
   static_assert(CA * 8 * W == BM && CB * 8 * W == BN, "copies");
+  constexpr bool AM = a_major(EPI), BM_ = b_major(EPI), F16 = D != kBF16;
   __shared__ __align__(16) uint8_t lds[2 * kStage];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -152,87 +251,69 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
   const int nk = (int)((min(a.K, k_lo + a.k_slice) - k_lo) / BK);
   const int steps = nk * passes(D);
 
-  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(a.A.p + m0 * a.A.ld), (short)0, 0x7fffffff, 0x00020000);
-  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(a.B.p + n0 * a.B.ld), (short)0, 0x7fffffff, 0x00020000);
-  // lane -> row lane / 8 of a copy, slot lane % 8; rows past the end are
-  // clamped (what they give is dropped)
-  uint32_t oa[CA], ob[CB];
-#pragma unroll
-  for (int c = 0; c < CA; ++c) {
-    const int r = (wave * CA + c) * 8 + (lane >> 3);
-    const int q = (lane & 7) ^ ((r >> 1) & 7);
-    oa[c] = (uint32_t)((min<int64_t>(r, M - 1 - m0) * a.A.ld + 8 * q) * 2);
-  }
-#pragma unroll
-  for (int c = 0; c < CB; ++c) {
-    const int r = (wave * CB + c) * 8 + (lane >> 3);
-    const int q = (lane & 7) ^ ((r >> 1) & 7);
-    ob[c] = (uint32_t)((min<int64_t>(r, N - 1 - n0) * a.B.ld + 8 * q) * 2);
-  }
-  auto copy = [&](int stage, int pass, int kt) {
+  Tile<BM, CA, AM> ta;
+  Tile<BN, CB, BM_> tb;
+  ta.init(a.A, m0, wave, lane);
+  tb.init(a.B, n0, wave, lane);
+  Reader<BM, MI, AM> ra;
+  Reader<BN, NI, BM_> rb;
+  ra.init(wm * MI, g, li);
+  rb.init(wn * NI, g, li);
+  // passes: h h, h l, l h
+  int pass = 0, kt = 0;
+  auto copy = [&](int stage) {
     uint8_t* st = lds + stage * kStage;
     const int64_t k = k_lo + (int64_t)kt * BK;
-    const int ka = (int)((k + (D == kF32 ? term_a(pass) * a.A.plane : 0)) * 2);
-    const int kb = (int)((k + (D == kF32 ? term_b(pass) * a.B.plane : 0)) * 2);
-#pragma unroll
-    for (int c = 0; c < CA; ++c)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(st + (wave * CA + c) * 1024), 16,
-                                               (int)oa[c], ka, 0, 0);
-#pragma unroll
-    for (int c = 0; c < CB; ++c)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rb, (lds_ptr_t)(st + BM * 128 + (wave * CB + c) * 1024), 16, (int)ob[c], kb, 0, 0);
+    ta.copy(st, wave, k, D == kF32 && pass == 2 ? a.A.plane : 0);
+    tb.copy(st + BM * 128, wave, k, D == kF32 && pass == 1 ? a.B.plane : 0);
+    if (++kt == nk) {
+      kt = 0;
+      ++pass;
+    }
   };
   f32x4 acc[MI][NI];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int fa = (wm * MI * 16 + li) * 128, fb = BM * 128 + (wn * NI * 16 + li) * 128;
-  auto mult = [&](int stage) {
-    const uint8_t* st = lds + stage * kStage;
+  u32x4 fa[2][MI], fb[2][NI];
+  auto read = [&](int stage, int h) {
+    uint8_t* st = lds + stage * kStage;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int slot = ((4 * h + g) ^ (li >> 1)) * 16;
-      u32x4 b[NI];
+    for (int j = 0; j < NI; ++j) fb[h][j] = rb.read(st + BM * 128, j, h);
 #pragma unroll
-      for (int j = 0; j < NI; ++j) b[j] = *(const u32x4*)(st + fb + slot + j * 2048);
+    for (int i = 0; i < MI; ++i) fa[h][i] = ra.read(st, i, h);
+  };
+  auto mult = [&](int h) {
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const u32x4 f = *(const u32x4*)(st + fa + slot + i * 2048);
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < NI; ++j) acc[i][j] = mma<D>(f, b[j], acc[i][j]);
-      }
-    }
+      for (int j = 0; j < NI; ++j) acc[i][j] = mma<F16>(fa[h][i], fb[h][j], acc[i][j]);
   };
   // each wave waits for its own copies and reads, then for the other waves
   auto sync = [&]() {
     __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
     asm volatile("s_barrier" ::: "memory");
   };
-  int pass = 0, kt = 0;
-  auto advance = [&]() {
-    if (++kt == nk) {
-      kt = 0;
-      ++pass;
-    }
-  };
-  copy(0, 0, 0);
-  advance();
+  copy(0);
+  sync();
+  if (steps > 1) copy(1);
+  read(0, 0);
   for (int s = 0; s < steps; ++s) {
-    sync();   // stage s & 1 has landed; everyone is done with the other
-    if (s + 1 < steps) {
-      copy((s & 1) ^ 1, pass, kt);
-      advance();
-    }
-    mult(s & 1);
+    const int cur = s & 1;
+    read(cur, 1);
+    mult(0);
+    sync();   // the other stage has landed; everyone has read this one
+    if (s + 2 < steps) copy(cur);
+    if (s + 1 < steps) read(cur ^ 1, 0);
+    mult(1);
   }
 
   // lane (g, li), element v of tile (i, j): row 16 i + 4 g + v, column 16 j + li
   const int64_t r0 = m0 + wm * MI * 16 + 4 * g, c0 = n0 + wn * NI * 16 + li;
   if constexpr (EPI == kStat) {
+    const float zs = *a.zs;
+    const int64_t half = a.v0 / (16 * MI) + tm * WM + wm;
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const int64_t t = c0 + 16 * j;
@@ -243,7 +324,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const int64_t w = r0 + 16 * i + v;
-          const float z = a.scale * acc[i][j][v];
+          const float z = zs * acc[i][j][v];
           acc[i][j][v] = z;
           if (w < M) top = fmaxf(top, z);
           if (w < M && w + a.v0 == label) a.hit[t] = z;
@@ -259,38 +340,35 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
       sum += __shfl_xor(sum, 16);
       sum += __shfl_xor(sum, 32);
       if (g == 0 && t < N) {
-        a.top[(tm * WM + wm) * N + t] = top;
-        a.sum[(tm * WM + wm) * N + t] = sum;
+        a.top[half * N + t] = top;
+        a.sum[half * N + t] = sum;
       }
     }
   } else if constexpr (EPI == kGrad) {
+    const float zs = *a.zs;
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const int64_t t = c0 + 16 * j;
       const int32_t label = t < N ? a.labels[t] : -1;
       const float lse = label >= 0 ? a.lse[t] : 0.0f, wn_t = label >= 0 ? a.wn[t] : 0.0f;
+      uint16_t* row = a.G + t * a.gld * terms(D);
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         uint16_t q[4][terms(D)];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const int64_t w = r0 + 16 * i + v;
-          const float y = a.scale * acc[i][j][v] - lse;
+          const float y = zs * acc[i][j][v] - lse;
           float x = D == kF32 ? expf(y) : __expf(y);
           if (w + a.v0 == label) x -= 1.0f;
           x = label >= 0 && w < M ? x * wn_t : 0.0f;
           split<D>(x, q[v]);
         }
-        const int64_t w = r0 + 16 * i;
 #pragma unroll
-        for (int p = 0; p < terms(D); ++p) {
-          *(u32x2*)(a.G + t * a.gld * terms(D) + p * a.gld + w) =
+        for (int p = 0; p < terms(D); ++p)
+          *(u32x2*)(row + p * a.gld + r0 + 16 * i) =
               u32x2{(uint32_t)q[0][p] | (uint32_t)q[1][p] << 16,
                     (uint32_t)q[2][p] | (uint32_t)q[3][p] << 16};
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            a.Gt[(w + v) * a.gtld * terms(D) + p * a.gtld + t] = q[v][p];
-        }
       }
     }
   } else if constexpr (EPI == kDh) {
@@ -336,42 +414,60 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
 }
 
 // ---------------------------------------------------------------- few tokens
-// 64 words and all T <= 16 NT tokens per workgroup; wave w takes the columns
-// 128 w .. 128 w + 127 of every 512. Rows are 16-byte aligned and d % 8 == 0
-// (VEC), or elements are loaded one by one.
+// 64 words and all T <= 16 NT tokens per workgroup; the four waves take runs
+// of 32 S columns in turn, the next run's loads in flight while one multiplies.
+// Rows are 16-byte aligned and d % 8 == 0 (VEC), or elements are loaded one by
+// one.
 template <int D>
-struct Frag {
-  u32x4 t[terms(D)];
+struct Raw8 {
+  typename Elem<D>::type e[8];
 };
 template <int D, bool VEC>
-__device__ __forceinline__ Frag<D> load_frag(const typename Elem<D>::type* row, int64_t k,
-                                             int64_t d) {
+__device__ __forceinline__ Raw8<D> load8(const typename Elem<D>::type* row, int64_t k, int64_t d) {
   typedef typename Elem<D>::type E;
-  E e[8];
+  Raw8<D> r;
   if constexpr (VEC) {
-    if (k < d)
-      __builtin_memcpy(e, __builtin_assume_aligned(row + k, 16), sizeof(e));
-    else
-      __builtin_memset(e, 0, sizeof(e));
+    __builtin_memcpy(r.e, __builtin_assume_aligned(row + min(k, d - 8), 16), sizeof(r.e));
+    if (k >= d) __builtin_memset(r.e, 0, sizeof(r.e));
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = k + i < d ? row[k + i] : (E)0;
+    for (int i = 0; i < 8; ++i) r.e[i] = k + i < d ? row[k + i] : (E)0;
   }
+  return r;
+}
+// x = h + m + l in bf16, exact; not finite: the first term alone
+__device__ __forceinline__ void split3(float x, uint16_t (&t)[3]) {
+  t[0] = Elem<kBF16>::from(x);
+  const float r = x - Elem<kBF16>::to(t[0]);
+  const bool fin = (__float_as_uint(r) & 0x7fffffffu) < 0x7f800000u;
+  t[1] = fin ? Elem<kBF16>::from(r) : (uint16_t)0;
+  t[2] = fin ? Elem<kBF16>::from(r - Elem<kBF16>::to(t[1])) : (uint16_t)0;
+}
+constexpr int score_terms(int D) { return D == kF32 ? 3 : 1; }
+template <int D>
+struct Frag {
+  u32x4 t[score_terms(D)];
+};
+template <int D>
+__device__ __forceinline__ Frag<D> frag_of(const Raw8<D>& r) {
   Frag<D> f;
   if constexpr (D == kF32) {
     uint16_t q[8][3];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) split<kF32>(e[i], q[i]);
+    for (int i = 0; i < 8; ++i) split3(r.e[i], q[i]);
 #pragma unroll
     for (int p = 0; p < 3; ++p)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         f.t[p][i] = (uint32_t)q[2 * i][p] | (uint32_t)q[2 * i + 1][p] << 16;
   } else {
-    __builtin_memcpy(&f.t[0], e, 16);
+    __builtin_memcpy(&f.t[0], r.e, 16);
   }
   return f;
 }
+// the six products of bf16 terms: term of A and of B (2 bits each)
+__device__ __forceinline__ int term_a(int s) { return (0x250 >> (2 * s)) & 3; }   // 0 0 1 1 2 0
+__device__ __forceinline__ int term_b(int s) { return (0x844 >> (2 * s)) & 3; }   // 0 1 0 1 0 2
 
 template <int D, int NT, bool VEC>
 __global__ __launch_bounds__(256) void score_kernel(const typename Elem<D>::type* __restrict__ H,
@@ -382,6 +478,7 @@ __global__ __launch_bounds__(256) void score_kernel(const typename Elem<D>::type
                                                     float scale, float* __restrict__ top,
                                                     float* __restrict__ sum,
                                                     float* __restrict__ hit) {
+  constexpr int S = !VEC ? 1 : D == kF32 ? (NT == 4 ? 1 : 2) : (NT == 4 ? 2 : 4);
   __shared__ f32x4 red[4][4 * NT][64];
   __shared__ float st[2][4][16 * NT];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -397,24 +494,47 @@ __global__ __launch_bounds__(256) void score_kernel(const typename Elem<D>::type
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t k0 = wave * 128; k0 < d; k0 += 512) {
+  struct Run {
+    Raw8<D> w[S][4], h[S][NT];
+  };
+  auto load = [&](Run& r, int64_t k0) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < S; ++s) {
       const int64_t k = k0 + 32 * s + 8 * g;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.w[s][i] = load8<D, VEC>(wr[i], k, d);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) r.h[s][j] = load8<D, VEC>(hr[j], k, d);
+    }
+  };
+  auto mult = [&](const Run& r) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
       Frag<D> b[NT];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) b[j] = load_frag<D, VEC>(hr[j], k, d);
+      for (int j = 0; j < NT; ++j) b[j] = frag_of<D>(r.h[s][j]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const Frag<D> f = load_frag<D, VEC>(wr[i], k, d);
+        const Frag<D> f = frag_of<D>(r.w[s][i]);
 #pragma unroll
-        for (int q = 0; q < passes(D); ++q)
+        for (int q = 0; q < (D == kF32 ? 6 : 1); ++q)
 #pragma unroll
           for (int j = 0; j < NT; ++j)
-            acc[i][j] = mma<D>(f.t[D == kF32 ? term_a(q) : 0], b[j].t[D == kF32 ? term_b(q) : 0],
-                               acc[i][j]);
+            acc[i][j] = mma<D == kF16>(f.t[D == kF32 ? term_a(q) : 0],
+                                       b[j].t[D == kF32 ? term_b(q) : 0], acc[i][j]);
       }
     }
+  };
+  // (runs past d load and add zeros)
+  Run r0, r1;
+  load(r0, wave * 32 * S);
+  for (int64_t k0 = wave * 32 * S; k0 < d; k0 += 256 * S) {
+    load(r1, k0 + 128 * S);
+    __builtin_amdgcn_sched_barrier(0);
+    mult(r0);
+    load(r0, k0 + 256 * S);
+    __builtin_amdgcn_sched_barrier(0);
+    mult(r1);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -503,30 +623,88 @@ __global__ __launch_bounds__(1024) void stat_kernel(const float* __restrict__ to
   loss[t] = label < 0 ? 0.0f : l - h;
 }
 
-// wn[t] = dloss[t] / max|dloss| times gs (0 for an ignored token, NaN for a
-// label at or past V); post = max|dloss| scale / gs. One workgroup.
-__global__ __launch_bounds__(1024) void weight_kernel(const float* __restrict__ dloss,
-                                                      const int32_t* __restrict__ labels,
-                                                      int64_t T, int64_t V, float gs, float scale,
-                                                      float* __restrict__ wn,
-                                                      float* __restrict__ post) {
-  __shared__ float sm[1024];
+// Factors of a call, read by the kernels that follow.
+struct Factors {
+  float mh, mw;          // powers of two that H and W are scaled by (fp32, else 1)
+  float zs;              // scale / (mh mw)
+  float post_h, post_w;  // of dH and dW
+};
+constexpr int kAmaxParts = 512;
+// parts[y][x] = the largest finite magnitude of a share of H (y = 0) or W
+__global__ __launch_bounds__(256) void amax_kernel(const float* __restrict__ H, int64_t T,
+                                                   int64_t ldh, const float* __restrict__ W,
+                                                   int64_t V, int64_t ldw, int64_t d,
+                                                   const int32_t* __restrict__ labels,
+                                                   float* __restrict__ parts) {
+  __shared__ float sm[256];
+  const bool w = blockIdx.y;
+  const float* X = w ? W : H;
+  const int64_t rows = w ? V : T, ld = w ? ldw : ldh;
   float m = 0.0f;
-  for (int64_t t = threadIdx.x; t < T; t += 1024)
-    if (labels[t] >= 0) m = fmaxf(m, fabsf(dloss[t]));
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    if (!w && labels[r] < 0) continue;
+    const float* x = X + r * ld;
+#pragma unroll 4
+    for (int64_t c = threadIdx.x; c < d; c += 256) {
+      const float v = fabsf(x[c]);
+      m = v < __builtin_inff() ? fmaxf(m, v) : m;
+    }
+  }
   sm[threadIdx.x] = m;
+  __syncthreads();
+  for (int o = 128; o > 0; o >>= 1) {
+    if ((int)threadIdx.x < o) sm[threadIdx.x] = fmaxf(sm[threadIdx.x], sm[threadIdx.x + o]);
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) parts[blockIdx.y * gridDim.x + blockIdx.x] = sm[0];
+}
+// the largest of v over the workgroup's 1024 threads
+__device__ __forceinline__ float max_of(float v, float* sm) {
+  __syncthreads();
+  sm[threadIdx.x] = v;
   __syncthreads();
   for (int o = 512; o > 0; o >>= 1) {
     if ((int)threadIdx.x < o) sm[threadIdx.x] = fmaxf(sm[threadIdx.x], sm[threadIdx.x + o]);
     __syncthreads();
   }
-  m = sm[0];
-  for (int64_t t = threadIdx.x; t < T; t += 1024) {
-    const int32_t label = labels[t];
-    const float w = m == 0.0f ? dloss[t] : dloss[t] / m * gs;   // (all zero, or NaN)
-    wn[t] = label < 0 ? 0.0f : label < V ? w : __uint_as_float(0x7fc00000u);
+  return sm[0];
+}
+// 2^e with m 2^e in (2^14, 2^15], e in -126 .. 126
+__device__ __forceinline__ float power_for(float m) {
+  const uint32_t b = __float_as_uint(m);
+  const int e = 14 - ((int)(b >> 23) - 127) + ((b & 0x7fffffu) == 0);
+  return m > 0.0f ? __uint_as_float((uint32_t)(min(max(e, -126), 126) + 127) << 23) : 1.0f;
+}
+// The factors, and with dloss the normalised weights: wn[t] = dloss[t] /
+// max|dloss| times gs (0 for an ignored token, NaN for a label at or past V).
+// parts (fp32 operands): the maxima of H and W. One workgroup.
+__global__ __launch_bounds__(1024) void factors_kernel(const float* __restrict__ parts,
+                                                       const float* __restrict__ dloss,
+                                                       const int32_t* __restrict__ labels,
+                                                       int64_t T, int64_t V, float gs, float scale,
+                                                       float* __restrict__ wn,
+                                                       Factors* __restrict__ out) {
+  __shared__ float sm[1024];
+  float mh = 1.0f, mw = 1.0f, m = 0.0f;
+  if (parts) {
+    const int t = threadIdx.x;
+    mh = power_for(max_of(t < kAmaxParts ? parts[t] : 0.0f, sm));
+    mw = power_for(max_of(t < kAmaxParts ? parts[kAmaxParts + t] : 0.0f, sm));
   }
-  if (threadIdx.x == 0) *post = (m == 0.0f ? 1.0f : m) * scale / gs;
+  if (dloss) {
+    for (int64_t t = threadIdx.x; t < T; t += 1024)
+      if (labels[t] >= 0) m = fmaxf(m, fabsf(dloss[t]));
+    m = max_of(m, sm);
+    for (int64_t t = threadIdx.x; t < T; t += 1024) {
+      const int32_t label = labels[t];
+      const float w = m == 0.0f ? dloss[t] : dloss[t] / m * gs;   // (all zero, or NaN)
+      wn[t] = label < 0 ? 0.0f : label < V ? w : __uint_as_float(0x7fc00000u);
+    }
+  }
+  if (threadIdx.x == 0) {
+    const double f = (m == 0.0f ? 1.0 : (double)m) * (double)scale / (double)gs;
+    *out = Factors{mh, mw, (float)((double)scale / mh / mw), (float)(f / mw), (float)(f / mh)};
+  }
 }
 
 // dH = post times the sum of nz slices (in order)
@@ -549,25 +727,37 @@ __global__ __launch_bounds__(256) void dh_kernel(const float* __restrict__ part,
 }
 
 // ---------------------------------------------------------------- layout
-// out [row][term][kp] = X (rows x k), zero from k to kp
+// out [row][term][kp] = the terms of X (rows x k) times *mul (fp32), zero from
+// k to kp, for rows past the last up to rp, and for rows whose label is
+// negative (labels nullable).
 template <int D>
 __global__ __launch_bounds__(256) void pack_kernel(const typename Elem<D>::type* __restrict__ X,
                                                    int64_t rows, int64_t k, int64_t ld,
-                                                   uint16_t* __restrict__ out, int64_t kp) {
+                                                   const int32_t* __restrict__ labels,
+                                                   const float* __restrict__ mul,
+                                                   uint16_t* __restrict__ out, int64_t rp,
+                                                   int64_t kp) {
   typedef typename Elem<D>::type E;
   const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
   if (c >= kp) return;
-  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+  const float f = D == kF32 ? *mul : 1.0f;
+  for (int64_t r = blockIdx.y; r < rp; r += gridDim.y) {
     E e[8];
-    if (c + 8 <= k) {
+    const bool row = r < rows && (!labels || labels[r] >= 0);
+    if (row && c + 8 <= k) {
       __builtin_memcpy(e, X + r * ld + c, sizeof(e));
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = c + i < k ? X[r * ld + c + i] : (E)0;
+      for (int i = 0; i < 8; ++i) e[i] = row && c + i < k ? X[r * ld + c + i] : (E)0;
     }
     uint16_t q[8][terms(D)];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) split_elem<D>(e[i], q[i]);
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (D == kF32)
+        split<D>(e[i] * f, q[i]);
+      else
+        q[i][0] = __builtin_bit_cast(uint16_t, e[i]);
+    }
 #pragma unroll
     for (int p = 0; p < terms(D); ++p) {
       u32x4 w;
@@ -578,98 +768,69 @@ __global__ __launch_bounds__(256) void pack_kernel(const typename Elem<D>::type*
   }
 }
 
-// out [col][term][rp] = X^T (X rows x cols), zero from rows to rp and for rows
-// whose label is negative (labels nullable). 64 x 64 tiles through LDS.
-template <int D>
-__global__ __launch_bounds__(256) void pack_t_kernel(const typename Elem<D>::type* __restrict__ X,
-                                                     int64_t rows, int64_t cols, int64_t ld,
-                                                     const int32_t* __restrict__ labels,
-                                                     uint16_t* __restrict__ out, int64_t rp) {
-  typedef typename Elem<D>::type E;
-  __shared__ E tile[64][64 + (D == kF32 ? 1 : 2)];
-  const int64_t c0 = (int64_t)blockIdx.x * 64;
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-  for (int64_t r0 = (int64_t)blockIdx.y * 64; r0 < rp; r0 += (int64_t)gridDim.y * 64) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int64_t r = r0 + ty + 4 * i, c = c0 + tx;
-      const bool ok = r < rows && c < cols && (!labels || labels[r] >= 0);
-      tile[ty + 4 * i][tx] = ok ? X[r * ld + c] : (E)0;
-    }
-    __syncthreads();
-    // thread -> column threadIdx / 8 (+ 32), rows 8 (threadIdx % 8) ..
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = (threadIdx.x >> 3) + 32 * h, r = 8 * (threadIdx.x & 7);
-      if (c0 + c >= cols) continue;
-      uint16_t q[8][terms(D)];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) split_elem<D>(tile[r + i][c], q[i]);
-#pragma unroll
-      for (int p = 0; p < terms(D); ++p) {
-        u32x4 w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = (uint32_t)q[2 * i][p] | (uint32_t)q[2 * i + 1][p] << 16;
-        *(u32x4*)(out + ((c0 + c) * terms(D) + p) * rp + r0 + r) = w;
-      }
-    }
-  }
-}
-
 // ---------------------------------------------------------------- plan
-// Whether X's rows can be copied as they are (16-byte aligned, k % 64 == 0).
+// Whether X's rows can be copied as they are: 16-bit, 16-byte aligned.
 bool direct(const void* X, int64_t ld, int64_t k, int dtype) {
-  return dtype != kF32 && k % BK == 0 && ld % 8 == 0 && (uintptr_t)X % 16 == 0;
+  return dtype != kF32 && k % 8 == 0 && ld % 8 == 0 && (uintptr_t)X % 16 == 0;
 }
 
 struct Plan {
   int64_t dp, tp;              // d to 64, T to 256
-  int64_t piece, pp, npieces;  // words of a piece, to 256; pieces
-  int64_t np;                  // partials per token
+  int64_t piece, npieces;      // words of a piece, to 256; pieces
   int nz;                      // slices of dH
   // byte offsets
-  int64_t hp, wp, top, sum, hit, wn, post, ht, wt, G, Gt, part, bytes;
+  int64_t hp, wp, top, sum, hit, wn, fac, amax, G, part, bytes;
 };
-// Words per piece: G and W^T of a piece hold at most 2^26 values each (two
-// thousand words at least), which leaves the fp32 sums of dH, read and written
-// once per piece, a few percent of the piece's products.
+// Tiles of 256 x 256 (one workgroup of four waves per CU) or of 128 x 128 (two
+// per CU, which lose about a fifth of the rate to twice the copies): whichever
+// needs less time in whole rounds over the 256 CUs.
+bool big_tiles(int64_t M, int64_t N, int64_t slices) {
+  const int64_t big = ((M + 255) / 256) * ((N + 255) / 256) * slices;
+  const int64_t small = ((M + 127) / 128) * ((N + 127) / 128) * slices;
+  return (big + 255) / 256 * 4.0 <= (small + 255) / 256 * 1.25;
+}
+// Slices of the contraction of dH: a workgroup for every CU, 256 words at
+// least.
+int dh_slices(int64_t T, int64_t d, int64_t piece) {
+  const int64_t tiles = ((d + 127) / 128) * ((T + 127) / 128);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, piece / 256, 64}));
+}
+// Words per piece: G, and a copy of W's piece where one is needed, hold at most
+// 2^26 values each (two thousand words at least), which leaves the fp32 sums of
+// dH, read and written once per piece, a few percent of the piece's products.
 Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad) {
   Plan p{};
   const int nt = terms(dtype);
   p.dp = round_up(d, BK);
   p.tp = round_up(T, 256);
+  const int64_t most = std::max<int64_t>(2048, (int64_t(1) << 26) / std::max(T, d) / 256 * 256);
+  p.npieces = (V + most - 1) / most;
+  p.piece = round_up((V + p.npieces - 1) / p.npieces, 256);
+  p.npieces = (V + p.piece - 1) / p.piece;
   int64_t off = 0;
   auto take = [&](int64_t bytes) {
     const int64_t at = off;
     off += round_up(bytes, 256);
     return at;
   };
-  const bool score = !grad && T <= kScoreMax;
-  p.np = score ? (V + 63) / 64 : 2 * ((V + 255) / 256);
   if (!grad) {
-    p.top = take(4 * p.np * T);
-    p.sum = take(4 * p.np * T);
+    const int64_t np = (V + 63) / 64 + 4;
+    p.top = take(4 * np * T);
+    p.sum = take(4 * np * T);
     p.hit = take(4 * T);
+    if (T <= kScoreMax) {
+      p.bytes = off;
+      return p;
+    }
   }
-  if (!score) {
-    p.hp = take(2 * nt * T * p.dp);
-    p.wp = take(2 * nt * V * p.dp);
-  }
+  p.fac = take(sizeof(Factors));
+  p.amax = take(4 * 2 * kAmaxParts);
+  p.hp = take(2 * nt * p.tp * p.dp);
+  p.wp = take(2 * nt * p.piece * p.dp);
   if (grad) {
-    const int64_t most = std::max<int64_t>(2048, (int64_t(1) << 26) / std::max(T, d) / 256 * 256);
-    p.npieces = (V + most - 1) / most;
-    p.piece = round_up((V + p.npieces - 1) / p.npieces, 256);
-    p.npieces = (V + p.piece - 1) / p.piece;
-    p.pp = p.piece;
-    const int64_t tiles = ((d + 255) / 256) * ((T + 255) / 256);
-    p.nz = (int)std::max<int64_t>(1, std::min<int64_t>({256 / tiles, p.pp / 512, 64}));
+    p.nz = dh_slices(T, d, p.piece);
     p.wn = take(4 * T);
-    p.post = take(4);
-    p.ht = take(2 * nt * d * p.tp);
-    p.wt = take(2 * nt * d * p.pp);
-    p.G = take(2 * nt * p.tp * p.pp);
-    p.Gt = take(2 * nt * p.tp * p.pp);
+    p.G = take(2 * nt * p.tp * p.piece);
     p.part = take(4 * p.nz * T * round_up(d, 4));
   }
   p.bytes = off;
@@ -677,41 +838,60 @@ Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad) {
 }
 
 template <int D, int EPI>
-hipError_t mma_launch(const Mma& a, int slices, hipStream_t s) {
-  const int64_t tiles = ((a.A.rows + 255) / 256) * ((a.B.rows + 255) / 256);
-  hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 4, 8, 4>),
-                     dim3((unsigned)((tiles + 7) / 8 * 8), (unsigned)slices), dim3(512), 0, s, a);
+hipError_t mma_launch(const Mma& a, bool big, int slices, hipStream_t s) {
+  const int64_t t = big ? 256 : 128;
+  const int64_t tiles = ((a.A.rows + t - 1) / t) * ((a.B.rows + t - 1) / t);
+  const dim3 grid((unsigned)((tiles + 7) / 8 * 8), (unsigned)slices);
+  if (big)
+    hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 4, 8, 4>), grid, dim3(512), 0, s, a);
+  else
+    hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 2, 4, 4>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 template <int D>
-hipError_t pack(const void* X, int64_t rows, int64_t k, int64_t ld, uint16_t* out, int64_t kp,
-                hipStream_t s) {
-  const dim3 grid((unsigned)((kp / 8 + 255) / 256), (unsigned)std::min<int64_t>(rows, 16384));
+hipError_t pack(const void* X, int64_t rows, int64_t k, int64_t ld, const int32_t* labels,
+                const float* mul, uint16_t* out, int64_t rp, int64_t kp, hipStream_t s) {
+  const dim3 grid((unsigned)((kp / 8 + 255) / 256), (unsigned)std::min<int64_t>(rp, 16384));
   hipLaunchKernelGGL(pack_kernel<D>, grid, dim3(256), 0, s, (const typename Elem<D>::type*)X, rows,
-                     k, ld, out, kp);
-  return hipGetLastError();
-}
-template <int D>
-hipError_t pack_t(const void* X, int64_t rows, int64_t cols, int64_t ld, const int32_t* labels,
-                  uint16_t* out, int64_t rp, hipStream_t s) {
-  const dim3 grid((unsigned)((cols + 63) / 64), (unsigned)std::min<int64_t>(rp / 64, 65535));
-  hipLaunchKernelGGL(pack_t_kernel<D>, grid, dim3(256), 0, s, (const typename Elem<D>::type*)X,
-                     rows, cols, ld, labels, out, rp);
+                     k, ld, labels, mul, out, rp, kp);
   return hipGetLastError();
 }
 
-// H or W as a k-contiguous operand: in place, or a copy in the workspace
+// The factors of a call (and wn with dloss), and H's rows with those of
+// ignored tokens zeroed.
 template <int D>
-hipError_t operand(const void* X, int64_t rows, int64_t ld, const Vocab& a, const Plan& p,
-                   int64_t at, Opnd* o, hipStream_t s) {
-  if (direct(X, ld, a.d, D)) {
-    *o = Opnd{(const uint16_t*)X, ld, 0, rows};
+hipError_t begin(const Vocab& a, const Plan& p, const float* dloss, Opnd* H, hipStream_t s) {
+  char* w = (char*)a.work;
+  Factors* fac = (Factors*)(w + p.fac);
+  float* amax = (float*)(w + p.amax);
+  hipError_t e;
+  if (D == kF32) {
+    hipLaunchKernelGGL(amax_kernel, dim3(kAmaxParts, 2), dim3(256), 0, s, (const float*)a.H, a.T,
+                       a.ldh, (const float*)a.W, a.V, a.ldw, a.d, a.labels, amax);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(factors_kernel, dim3(1), dim3(1024), 0, s, D == kF32 ? amax : nullptr, dloss,
+                     a.labels, a.T, a.V, D == kBF16 ? 1.0f : kTop16, a.scale, (float*)(w + p.wn),
+                     fac);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  uint16_t* out = (uint16_t*)(w + p.hp);
+  *H = Opnd{out, p.dp * terms(D), p.dp, a.T, p.dp};
+  return pack<D>(a.H, a.T, a.d, a.ldh, a.labels, &fac->mh, out, p.tp, p.dp, s);
+}
+// nv words of W from v0: in place, or a copy in the workspace
+template <int D>
+hipError_t words(const Vocab& a, const Plan& p, int64_t v0, int64_t nv, Opnd* o, hipStream_t s) {
+  typedef typename Elem<D>::type E;
+  const E* W = (const E*)a.W + v0 * a.ldw;
+  if (direct(a.W, a.ldw, a.d, D)) {
+    *o = Opnd{(const uint16_t*)W, a.ldw, 0, nv, a.d};
     return hipSuccess;
   }
-  uint16_t* out = (uint16_t*)((char*)a.work + at);
-  *o = Opnd{out, p.dp * terms(D), p.dp, rows};
-  return pack<D>(X, rows, a.d, ld, out, p.dp, s);
+  char* w = (char*)a.work;
+  uint16_t* out = (uint16_t*)(w + p.wp);
+  *o = Opnd{out, p.dp * terms(D), p.dp, nv, p.dp};
+  return pack<D>(W, nv, a.d, a.ldw, nullptr, &((Factors*)(w + p.fac))->mw, out, nv, p.dp, s);
 }
 
 template <int D, int NT>
@@ -720,7 +900,7 @@ void score(const Vocab& a, const Plan& p, hipStream_t s) {
   char* w = (char*)a.work;
   const bool vec = a.d % 8 == 0 && a.ldh * sizeof(E) % 16 == 0 && a.ldw * sizeof(E) % 16 == 0 &&
                    ((uintptr_t)a.H | (uintptr_t)a.W) % 16 == 0;
-  const dim3 grid((unsigned)p.np);
+  const dim3 grid((unsigned)((a.V + 63) / 64));
   if (vec)
     hipLaunchKernelGGL((score_kernel<D, NT, true>), grid, dim3(256), 0, s, (const E*)a.H, a.ldh,
                        (const E*)a.W, a.ldw, a.T, a.V, a.d, a.labels, a.scale,
@@ -736,24 +916,33 @@ hipError_t loss(const Vocab& a, hipStream_t s) {
   const Plan p = plan_for(a.T, a.V, a.d, D, false);
   char* w = (char*)a.work;
   hipError_t e;
+  int64_t np;   // partials per token
   if (a.T <= kScoreMax) {
+    np = (a.V + 63) / 64;
     if (a.T <= 16) score<D, 1>(a, p, s);
     else if (a.T <= 32) score<D, 2>(a, p, s);
     else score<D, 4>(a, p, s);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   } else {
     Mma m{};
-    if ((e = operand<D>(a.W, a.V, a.ldw, a, p, p.wp, &m.A, s)) != hipSuccess) return e;
-    if ((e = operand<D>(a.H, a.T, a.ldh, a, p, p.hp, &m.B, s)) != hipSuccess) return e;
+    if ((e = begin<D>(a, p, nullptr, &m.B, s)) != hipSuccess) return e;
     m.K = m.k_slice = p.dp;
-    m.scale = a.scale;
+    m.zs = &((Factors*)(w + p.fac))->zs;
     m.labels = a.labels;
     m.top = (float*)(w + p.top); m.sum = (float*)(w + p.sum); m.hit = (float*)(w + p.hit);
-    if ((e = mma_launch<D, kStat>(m, 1, s)) != hipSuccess) return e;
+    // all words at once where W is used in place
+    const int64_t piece = direct(a.W, a.ldw, a.d, D) ? a.V : p.piece;
+    const bool big = big_tiles(piece, a.T, 1);
+    np = big ? 2 * ((a.V + 255) / 256) : 2 * ((a.V + 127) / 128);
+    for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
+      m.v0 = v0;
+      if ((e = words<D>(a, p, v0, std::min(piece, a.V - v0), &m.A, s)) != hipSuccess) return e;
+      if ((e = mma_launch<D, kStat>(m, big, 1, s)) != hipSuccess) return e;
+    }
   }
   hipLaunchKernelGGL(stat_kernel, dim3((unsigned)((a.T + 15) / 16)), dim3(1024), 0, s,
-                     (const float*)(w + p.top), (const float*)(w + p.sum), p.np, a.T, a.V,
-                     a.labels, (const float*)(w + p.hit), a.loss, a.lse);
+                     (const float*)(w + p.top), (const float*)(w + p.sum), np, a.T, a.V, a.labels,
+                     (const float*)(w + p.hit), a.loss, a.lse);
   return hipGetLastError();
 }
 
@@ -762,62 +951,52 @@ hipError_t backward(const Vocab& a, hipStream_t s) {
   typedef typename Elem<D>::type E;
   const Plan p = plan_for(a.T, a.V, a.d, D, true);
   char* w = (char*)a.work;
-  float *wn = (float*)(w + p.wn), *post = (float*)(w + p.post);
-  const float gs = D == kF16 ? 32768.0f : 1.0f;
-  hipError_t e;
-  hipLaunchKernelGGL(weight_kernel, dim3(1), dim3(1024), 0, s, a.dloss, a.labels, a.T, a.V, gs,
-                     a.scale, wn, post);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  Opnd H, W;
-  if ((e = operand<D>(a.W, a.V, a.ldw, a, p, p.wp, &W, s)) != hipSuccess) return e;
-  if ((e = operand<D>(a.H, a.T, a.ldh, a, p, p.hp, &H, s)) != hipSuccess) return e;
-  uint16_t *Ht = (uint16_t*)(w + p.ht), *Wt = (uint16_t*)(w + p.wt);
-  uint16_t *G = (uint16_t*)(w + p.G), *Gt = (uint16_t*)(w + p.Gt);
+  Factors* fac = (Factors*)(w + p.fac);
+  uint16_t* G = (uint16_t*)(w + p.G);
   constexpr int NTm = terms(D);
-  if (a.dW && (e = pack_t<D>(a.H, a.T, a.d, a.ldh, a.labels, Ht, p.tp, s)) != hipSuccess) return e;
   const int64_t ldp = round_up(a.d, 4), slice = a.T * ldp;
-  int64_t kz = 0;
-  for (int64_t q = 0; q < p.npieces; ++q) {
-    const int64_t v0 = q * p.piece, nv = std::min(p.piece, a.V - v0);
-    const int64_t nvp = round_up(nv, 256);
+  hipError_t e;
+  Opnd H, W;
+  if ((e = begin<D>(a, p, a.dloss, &H, s)) != hipSuccess) return e;
+  // every piece uses the same slices of its words for dH (the last may leave
+  // some without a share: those are not launched)
+  const int64_t kz = round_up((p.piece + p.nz - 1) / p.nz, BK);
+  const int nz = (int)((p.piece + kz - 1) / kz);
+  for (int64_t v0 = 0; v0 < a.V; v0 += p.piece) {
+    const int64_t nv = std::min(p.piece, a.V - v0), nvp = round_up(nv, 256);
+    if ((e = words<D>(a, p, v0, nv, &W, s)) != hipSuccess) return e;
     Mma m{};
-    m.A = Opnd{W.p + v0 * W.ld, W.ld, W.plane, nv};
-    m.B = H;
+    m.A = W; m.B = H;
     m.K = m.k_slice = p.dp;
-    m.scale = a.scale;
-    m.v0 = v0; m.labels = a.labels; m.lse = a.lse; m.wn = wn;
-    m.G = G; m.Gt = Gt; m.gld = p.pp; m.gtld = p.tp;
-    if ((e = mma_launch<D, kGrad>(m, 1, s)) != hipSuccess) return e;
+    m.zs = &fac->zs;
+    m.v0 = v0; m.labels = a.labels; m.lse = a.lse; m.wn = (float*)(w + p.wn);
+    m.G = G; m.gld = p.piece;
+    if ((e = mma_launch<D, kGrad>(m, big_tiles(nv, a.T, 1), 1, s)) != hipSuccess) return e;
+    // (G is zero for words past nv and tokens past T, to the tile's end)
     if (a.dH) {
-      if ((e = pack_t<D>((const E*)a.W + v0 * a.ldw, nv, a.d, a.ldw, nullptr, Wt, p.pp, s)) != hipSuccess)
-        return e;
       Mma h{};
-      h.A = Opnd{Wt, p.pp * NTm, p.pp, a.d};
-      h.B = Opnd{G, p.pp * NTm, p.pp, a.T};
-      h.K = nvp;
-      // every piece uses the same slices (the last may leave some of them
-      // without a share of its own: those are not launched)
-      h.k_slice = kz ? kz : round_up((nvp + p.nz - 1) / p.nz, BK);
-      kz = h.k_slice;
-      h.part = (float*)(w + p.part); h.slice = slice; h.ldo = ldp; h.add = q > 0;
-      if ((e = mma_launch<D, kDh>(h, (int)((nvp + kz - 1) / kz), s)) != hipSuccess) return e;
+      h.A = Opnd{W.p, W.ld, W.plane, a.d, nv};
+      h.B = Opnd{G, p.piece * NTm, p.piece, a.T, nvp};
+      h.K = round_up(nv, BK);
+      h.k_slice = kz;
+      h.part = (float*)(w + p.part); h.slice = slice; h.ldo = ldp; h.add = v0 > 0;
+      const int n = (int)((h.K + kz - 1) / kz);
+      if ((e = mma_launch<D, kDh>(h, big_tiles(a.d, a.T, nz), n, s)) != hipSuccess) return e;
     }
     if (a.dW) {
       Mma x{};
-      x.A = Opnd{Ht, p.tp * NTm, p.tp, a.d};
-      x.B = Opnd{Gt, p.tp * NTm, p.tp, nv};
+      x.A = Opnd{H.p, H.ld, H.plane, a.d, p.tp};
+      x.B = Opnd{G, p.piece * NTm, p.piece, nv, p.tp};
       x.K = x.k_slice = round_up(a.T, BK);
-      x.post = post;
+      x.post = &fac->post_w;
       x.out = (E*)a.dW + v0 * a.lddw; x.ldo = a.lddw;
-      if ((e = mma_launch<D, kDw>(x, 1, s)) != hipSuccess) return e;
+      if ((e = mma_launch<D, kDw>(x, big_tiles(a.d, nv, 1), 1, s)) != hipSuccess) return e;
     }
   }
   if (a.dH) {
-    const int64_t first = round_up(std::min(p.piece, a.V), 256);
-    const int nz = (int)((first + kz - 1) / kz);
     const dim3 grid((unsigned)((a.d + 1023) / 1024), (unsigned)std::min<int64_t>(a.T, 16384));
     hipLaunchKernelGGL(dh_kernel<D>, grid, dim3(256), 0, s, (const float*)(w + p.part), nz, slice,
-                       ldp, a.T, a.d, post, (E*)a.dH, a.lddh);
+                       ldp, a.T, a.d, &fac->post_h, (E*)a.dH, a.lddh);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return hipSuccess;

@@ -18,7 +18,9 @@ layer        a and s1 dy: two fp32 roundings each at most (2 u), then fixed
              ds1, ds2 sum at most 24 rounded fp32 terms in a row before fp64
              takes over (16 in a lane, 4 lanes, 2 halves, the product).
 loss         z: an fp32 sum of d exact products, (d + 2) u sum |h_k w_k|, for
-             fp32 operands 2^-23 more of it for the products left out; exp and
+             fp32 operands (two fp16 terms: a value to 2^-24 of itself or
+             2^-39 of the largest, the product of the second terms left out,
+             2^-24) 2^-22 more of it and d 2^-38 of the largest product; exp and
              log within 4 units; sums of V positive terms V u. G is rounded
              once, h(t); dH and dW sum V and T rounded terms in fp32.
 """
@@ -285,8 +287,9 @@ class Head:
     def zbound(self):
         Hh, W = np.abs(H(self.H)), np.abs(H(self.W))
         Hh[self.labels.cpu().numpy() < 0] = 0
-        extra = 2.0 ** -23 if self.name == "float32" else 0.0
-        return abs(self.scale) * ((Hh.shape[1] + 2) * U + extra) * (Hh @ W.T)
+        d, fp32 = Hh.shape[1], self.name == "float32"
+        tiny = d * 2.0 ** -38 * Hh.max() * W.max() if fp32 else 0.0
+        return abs(self.scale) * (((d + 2) * U + (2.0 ** -22 if fp32 else 0.0)) * (Hh @ W.T) + tiny)
 
     def check_loss(self, loss, lse):
         V = self.W.shape[0]
@@ -315,12 +318,16 @@ class Head:
         big = np.abs(dl[use]).max() if use.any() else 0.0
         eg = (p * (np.expm1(ee) + 8 * U)) * np.abs(dl[use])[:, None] * abs(self.scale)
         eg += (h + 4 * U) * np.abs(G)
-        if self.name == "float16":
+        if self.name != "bfloat16":
+            # (fp16's subnormals; fp32's second term, and the terms left out)
             eg += 2.0 ** -25 / 2 ** 15 * big * abs(self.scale)
         sumH = (np.abs(G) + eg) @ np.abs(W)
         sumW = (np.abs(G) + eg).T @ np.abs(Hh[use])
-        tH = eg @ np.abs(W) + ((V + 40) * U + (2.0 ** -23 if self.name == "float32" else 0)) * sumH
-        tW = eg.T @ np.abs(Hh[use]) + ((T + 40) * U + (2.0 ** -23 if self.name == "float32" else 0)) * sumW
+        tH = eg @ np.abs(W) + ((V + 40) * U + (2.0 ** -22 if self.name == "float32" else 0)) * sumH
+        tW = eg.T @ np.abs(Hh[use]) + ((T + 40) * U + (2.0 ** -22 if self.name == "float32" else 0)) * sumW
+        if self.name == "float32":   # operands to 2^-39 of the largest, V or T of them
+            tH += V * 2.0 ** -38 * (np.abs(G).max() if G.size else 0.0) * np.abs(W).max()
+            tW += T * 2.0 ** -38 * (np.abs(G).max() if G.size else 0.0) * np.abs(Hh).max()
         if dH is not None:
             np.testing.assert_array_less(np.abs(H(dH)[use] - wantH[use]),
                                          1.01 * tH + h * np.abs(wantH[use]) + least(self.name))
