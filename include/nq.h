@@ -407,7 +407,7 @@ nq_status nq_act8_steps(const uint8_t* exps, int64_t lde, int64_t rows, int64_t 
  * of ds1 and ds2 over tokens, which is fixed. All on `stream`, no allocation;
  * work: nq_binary_matmul_backward_work_bytes(T, m, n, r) bytes of device
  * scratch, 16-byte aligned. m, n, r in 1 .. 2^21, the signs' row strides at most
- * 2^21 words. */
+ * 2^20 words. */
 nq_status nq_binary_matmul_backward(const uint32_t* U_bits, int64_t ldu, const uint32_t* Ut_bits,
                                     int64_t ldut, const uint32_t* V_bits, int64_t ldv,
                                     const uint32_t* Vt_bits, int64_t ldvt, int64_t m, int64_t n,

@@ -432,11 +432,12 @@ __global__ __launch_bounds__(256, 2) void wide_kernel(Prod a0, Prod a1) {
   if ((int64_t)(blockIdx.x >> 3) >= per || tile >= ntn * ntm || z >= a.split) return;
   const int64_t tm = tile / ntn, tn = tile - tm * ntn;
   const int64_t nkb = blocks(a.K), nw = (a.K + 31) / 32;
-  const int64_t kb0 = z * a.kbs, kb1 = min(nkb, kb0 + a.kbs);
+  const int64_t kb0 = z * a.kbs, kb1 = lmin(nkb, kb0 + a.kbs);
   // signs of the tile: rows past N are clamped (dropped at the end), words
-  // past a row's last read what follows, or 0 past the last row's: they meet
-  // zero digits
-  const int64_t rows = min<int64_t>(kSigns, a.N - tn * kSigns);
+  // past a row's last read what follows, or nothing past the last row's (the
+  // descriptor's range, which counts the vector offset alone): they meet zero
+  // digits
+  const int64_t rows = lmin(kSigns, a.N - tn * kSigns);
   const __amdgpu_buffer_rsrc_t br = __builtin_amdgcn_make_buffer_rsrc(
       (void*)(a.bits + tn * kSigns * a.ldb), (short)0, (int)(((rows - 1) * a.ldb + nw) * 4),
       0x00020000);
@@ -449,8 +450,8 @@ __global__ __launch_bounds__(256, 2) void wide_kernel(Prod a0, Prod a1) {
       const int r0 = (wave * (kSigns / 16) + c) * 4, r = r0 + (lane >> 4);
       const int w = ((((lane >> 2) & 3) ^ ((r >> 2) & 3)) << 2) | (lane & 3);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          br, (lds_ptr_t)(st + r0 * 16), 4, (int)((min<int64_t>(r, rows - 1) * a.ldb + w) * 4),
-          (int)(sb * 64), 0, 0);
+          br, (lds_ptr_t)(st + r0 * 16), 4, (int)((lmin(r, rows - 1) * a.ldb + sb * 16 + w) * 4), 0,
+          0, 0);
     }
   };
   // the wave's digits: MI rows of blocks, nkb blocks apart (rows past T hold no
@@ -486,7 +487,7 @@ __global__ __launch_bounds__(256, 2) void wide_kernel(Prod a0, Prod a1) {
     uint32_t word[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) word[j] = st[j * 256];
-    const int64_t ahead = min(kb + 1, kb1 - 1);
+    const int64_t ahead = lmin(kb + 1, kb1 - 1);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       i32x4 b = spread(word[0], s);
@@ -544,14 +545,14 @@ __global__ __launch_bounds__(64 * kThinWaves) void thin_kernel(Prod a0, Prod a1)
   const int64_t n0 = (int64_t)blockIdx.x * 16;
   if (n0 >= a.N) return;
   const int64_t nkb = blocks(a.K), nw = (a.K + 31) / 32;
-  const uint32_t* bp = a.bits + min<int64_t>(n0 + li, a.N - 1) * a.ldb;
+  const uint32_t* bp = a.bits + lmin(n0 + li, a.N - 1) * a.ldb;
   i32x4 acc[ND][MT][1];
 #pragma unroll
   for (int p = 0; p < ND; ++p)
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[p][i][0] = i32x4{0, 0, 0, 0};
   for (int64_t kb = wave; kb < nkb; kb += kThinWaves) {
-    const uint32_t w = bp[min<int64_t>((kb >> 2) * 16 + 4 * g + (kb & 3), nw - 1)];
+    const uint32_t w = bp[lmin((kb >> 2) * 16 + 4 * g + (kb & 3), nw - 1)];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const i32x4 b = spread(w, s);

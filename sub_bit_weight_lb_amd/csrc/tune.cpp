@@ -16,6 +16,7 @@ namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 21;    // layer sizes
 constexpr int64_t kMaxRows = int64_t(1) << 31;   // tokens
+constexpr int64_t kMaxWords = int64_t(1) << 20;  // of a row of signs: 256 rows stay below 2^31 bytes
 
 bool dtype_ok(int32_t t) { return t == NQ_F32 || t == NQ_BF16 || t == NQ_F16; }
 static_assert((int)NQ_F32 == kF32 && (int)NQ_BF16 == kBF16 && (int)NQ_F16 == kF16, "nq_dtype");
@@ -137,8 +138,8 @@ nq_status nq_binary_matmul_backward(const uint32_t* U_bits, int64_t ldu, const u
   if (ldut < mw) return bad("ldut < ceil(m/32)");
   if (ldv < rw) return bad("ldv < ceil(r/32)");
   if (ldvt < nw) return bad("ldvt < ceil(n/32)");
-  if (std::max(std::max(ldu, ldut), std::max(ldv, ldvt)) > kMaxDim)
-    return bad("the signs' row strides must be <= 2^21 words");
+  if (std::max(std::max(ldu, ldut), std::max(ldv, ldvt)) > kMaxWords)
+    return bad("the signs' row strides must be <= 2^20 words");
   const nq_status st = check_act8(codes, ldc, exps, lde, n);
   if (st != NQ_OK) return st;
   if (lddy < m) return bad("lddy < m");

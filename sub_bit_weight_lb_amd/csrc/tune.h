@@ -14,6 +14,11 @@ inline int64_t dtype_bytes(int t) { return t == kF32 ? 4 : 2; }
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
+// (the device's own min and max take two 64-bit integers of different
+// spellings to double)
+__device__ __forceinline__ int64_t lmin(int64_t a, int64_t b) { return a < b ? a : b; }
+__device__ __forceinline__ int64_t lmax(int64_t a, int64_t b) { return a > b ? a : b; }
+
 // One element of type D as the caller stores it, and its conversions; from()
 // rounds to nearest even.
 template <int D> struct Elem;

@@ -39,6 +39,7 @@
 #include "tune.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace nq {
 namespace {
@@ -124,10 +125,18 @@ __device__ __forceinline__ bool tile_of(int64_t ntm, int64_t ntn, int64_t& tm, i
   const int64_t t = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
   if ((int64_t)(blockIdx.x >> 3) >= per || t >= nt) return false;
   const int64_t band = t / (4 * ntn), idx = t - band * 4 * ntn;
-  const int64_t h = min<int64_t>(4, ntm - 4 * band);
+  const int64_t h = lmin(4, ntm - 4 * band);
   tm = 4 * band + idx % h;
   tn = idx / h;
   return true;
+}
+
+// A uniform value in a scalar register, for the copies below: read from a vector
+// register that the compiler cannot see through (it drops a v_readfirstlane of
+// what it knows to be uniform, and may then hand them a vector register).
+__device__ __forceinline__ int scalar(int x) {
+  asm("" : "+v"(x));
+  return __builtin_amdgcn_readfirstlane(x);
 }
 
 // One operand's tile: R rows (k-contiguous) or columns (k-major) of 64 k, R *
@@ -145,58 +154,85 @@ __device__ __forceinline__ bool tile_of(int64_t ntm, int64_t ntn, int64_t& tm, i
 // column i.
 template <int R, int NC, bool MAJOR>
 struct Tile {
+  static constexpr int kRowsPer = MAJOR ? 512 / R : 8;   // LDS rows per copy
   const uint16_t* base;
-  int64_t ld, kv;
-  uint32_t off[NC];       // byte offset of the lane in each copy
-  int32_t krow[MAJOR ? NC : 1];
-  int koct[2];            // k-contiguous: the lane's octet in even and odd copies
+  int64_t ld, kv, left;   // left: bytes from base to the operand's end
+  // Copies c of a wave come in two kinds, by the swizzle of their rows: even
+  // and odd ones, or (k-major, four rows each) the first and the last two.
+  static constexpr int kind(int c) { return MAJOR && R == 128 ? c >> 1 : c & 1; }
+  static constexpr int first(int q) { return MAJOR && R == 128 ? 2 * q : q; }
+  uint32_t off[2];        // byte offset of the lane in the copies of a kind, from their first row
+  int koct[2];            // k-contiguous: the lane's octet in them
 
   __device__ __forceinline__ void init(const Opnd& o, int64_t r0, int wave, int lane) {
     ld = o.ld;
     kv = o.kv;
+    const int64_t end = o.plane ? o.ld : MAJOR ? (o.rows + 7) / 8 * 8 : o.kv;   // of the last row
     if constexpr (MAJOR) {
-      base = o.p + r0;
+      static_assert(NC % 2 == 0 && NC * kRowsPer % 8 == 0, "rows of a wave");
+      const int k0 = wave * NC * kRowsPer;
+      base = o.p + r0 + k0 * o.ld;
+      left = ((o.kv - 1 - k0) * o.ld + end - r0) * 2;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int pos = (wave * NC + c) * 1024 + lane * 16, k = pos / (2 * R);
-        const int slot = (pos - k * 2 * R) >> 4;
+      for (int c = 0; c < 2; ++c) {
+        const int k = k0 + first(c) * kRowsPer + lane * 16 / (2 * R), slot = lane * 16 % (2 * R) / 16;
         const int chunk = (slot >> 1) ^ ((k & 3) + 4 * ((k >> 3) & 1));
-        // (columns past the last octet are clamped: what they give is dropped)
-        const int64_t col = min<int64_t>(16 * chunk + 8 * (slot & 1), ((o.rows + 7) / 8 - 1) * 8 - r0);
-        krow[c] = k;
-        off[c] = (uint32_t)(col * 2);
+        off[c] = (uint32_t)(((int64_t)(lane * 16 / (2 * R)) * o.ld + 16 * chunk + 8 * (slot & 1)) * 2);
       }
     } else {
-      base = o.p + r0 * o.ld;
-      koct[0] = (lane & 7) ^ (lane >> 4);
-      koct[1] = (lane & 7) ^ (4 + (lane >> 4));
+      const int64_t r = r0 + wave * NC * 8;
+      base = o.p + r * o.ld;
+      left = ((o.rows - 1 - r) * o.ld + end) * 2;
+      static_assert(NC % 2 == 0, "copies in pairs");
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int cc = wave * NC + c, r = cc * 8 + (lane >> 3);
-        // (rows past the last are clamped: what they give is dropped)
-        off[c] = (uint32_t)((min<int64_t>(r, o.rows - 1 - r0) * o.ld + 8 * koct[cc & 1]) * 2);
+      for (int c = 0; c < 2; ++c) {
+        koct[c] = (lane & 7) ^ (4 * c + (lane >> 4));
+        off[c] = (uint32_t)(((lane >> 3) * o.ld + 8 * koct[c]) * 2);
       }
     }
   }
-  // the 64 k from k on, of the term `plane` elements into the rows
-  __device__ __forceinline__ void copy(uint8_t* st, int wave, int64_t k, int64_t plane) const {
-    const uint16_t* p = base + (MAJOR ? k * ld : k) + plane;
-    const __amdgpu_buffer_rsrc_t rs =
-        __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, 0x7fffffff, 0x00020000);
-    const bool tail = k + BK > kv;
+  // The 64 k from k on, of the term `plane` elements into the rows. What lies
+  // past the operand's end reads as zero (the descriptor's range, which counts
+  // the vector offset alone: all of an address below its base is in it). The
+  // copies
+  // are written out: a builtin's would make every transposing read wait for
+  // the copies of the next stage. They write no register, and sync() waits.
+  __device__ __forceinline__ void copy(uint32_t st, int wave, int64_t k, int64_t plane) const {
+    const int64_t skip = (MAJOR ? k * ld : k) + plane;
+    const uint64_t p = (uint64_t)(uintptr_t)(base + skip);
+    const int64_t n = lmin(lmax(left - 2 * skip, 0), 0x7fffffff);
+    uint32_t o[2] = {off[0], off[1]};
+    if constexpr (!MAJOR) {
+      if (k + BK > kv) {
+        // octets past kv: past any descriptor's range
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      uint32_t o = off[c];
-      if constexpr (MAJOR) {
-        const int64_t row = tail ? min<int64_t>(krow[c], kv - 1 - k) : krow[c];
-        o += (uint32_t)(row * ld * 2);
-      } else {
-        // past the descriptor's range: zeros
-        if (tail && k + 8 * koct[(wave * NC + c) & 1] >= kv) o = 0x80000000u;
+        for (int c = 0; c < 2; ++c) o[c] = k + 8 * koct[c] >= kv ? 0x80000000u : o[c];
       }
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(st + (wave * NC + c) * 1024), 16,
-                                               (int)o, 0, 0, 0);
     }
+    static_assert(NC == 4, "the copies below");
+    const uint32_t step = (uint32_t)(kRowsPer * ld * 2);
+    asm volatile(
+        "s_mov_b32 s92, %0\n\t"
+        "s_mov_b32 s93, %1\n\t"
+        "s_mov_b32 s94, %2\n\t"
+        "s_mov_b32 s95, 0x20000\n\t"
+        "s_mov_b32 m0, %3\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %4, s[92:95], 0 offen lds\n\t"
+        "s_add_u32 m0, m0, 0x400\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %5, s[92:95], 0 offen lds\n\t"
+        "s_add_u32 m0, m0, 0x400\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %6, s[92:95], 0 offen lds\n\t"
+        "s_add_u32 m0, m0, 0x400\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %7, s[92:95], 0 offen lds"
+        :
+        : "s"(scalar((int)p)), "s"(scalar((int)(p >> 32) & 0xffff)), "s"(scalar((int)n)),
+          "s"(scalar((int)(st + wave * NC * 1024))), "v"(o[kind(0)]),
+          "v"(o[kind(1)] + step), "v"(o[kind(2)] + 2 * step), "v"(o[kind(3)] + 3 * step)
+        : "s92", "s93", "s94", "s95", "scc", "memory");
   }
 };
 // Fragments of the N 16-row groups from group g0 on, half h (32 k) of a stage.
@@ -228,9 +264,9 @@ struct Reader {
   }
 };
 
-// WM x WN waves of 16 MI x 16 NI. Two stages of 64 k in LDS; the copies of a
-// stage go out two half-stages before its first fragments are read, and each
-// half's fragments are read while the half before it multiplies.
+// WM x WN waves of 16 MI x 16 NI (MI >= NI). Two stages of 64 k in LDS; a
+// stage's copies go out as soon as everyone has read the stage that they
+// replace, a half-stage of products and more before they are waited for.
 template <int D, int EPI, int WM, int WN, int MI, int NI>
 __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
   constexpr int BM = 16 * MI * WM, BN = 16 * NI * WN, W = WM * WN;
@@ -248,7 +284,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
   if (!tile_of((M + BM - 1) / BM, (N + BN - 1) / BN, tm, tn)) return;
   const int64_t m0 = tm * BM, n0 = tn * BN;
   const int64_t k_lo = (int64_t)blockIdx.y * a.k_slice;
-  const int nk = (int)((min(a.K, k_lo + a.k_slice) - k_lo) / BK);
+  const int nk = (int)((lmin(a.K, k_lo + a.k_slice) - k_lo) / BK);
   const int steps = nk * passes(D);
 
   Tile<BM, CA, AM> ta;
@@ -261,8 +297,9 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
   rb.init(wn * NI, g, li);
   // passes: h h, h l, l h
   int pass = 0, kt = 0;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   auto copy = [&](int stage) {
-    uint8_t* st = lds + stage * kStage;
+    const uint32_t st = lds0 + stage * kStage;
     const int64_t k = k_lo + (int64_t)kt * BK;
     ta.copy(st, wave, k, D == kF32 && pass == 2 ? a.A.plane : 0);
     tb.copy(st + BM * 128, wave, k, D == kF32 && pass == 1 ? a.B.plane : 0);
@@ -277,36 +314,45 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   u32x4 fa[2][MI], fb[2][NI];
-  auto read = [&](int stage, int h) {
-    uint8_t* st = lds + stage * kStage;
+  // Multiplies half h while the other half's fragments come from stage st: a
+  // read between products, one at a time.
+  auto phase = [&](auto half, uint8_t* st) {
+    constexpr int h = decltype(half)::value;
 #pragma unroll
-    for (int j = 0; j < NI; ++j) fb[h][j] = rb.read(st + BM * 128, j, h);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) fa[h][i] = ra.read(st, i, h);
-  };
-  auto mult = [&](int h) {
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
+    for (int i = 0; i < MI; ++i) {
+      if (i < NI) fb[h ^ 1][i] = rb.read(st + BM * 128, i, h ^ 1);
+      fa[h ^ 1][i] = ra.read(st, i, h ^ 1);
 #pragma unroll
       for (int j = 0; j < NI; ++j) acc[i][j] = mma<F16>(fa[h][i], fb[h][j], acc[i][j]);
+    }
+    constexpr int kReads = MI * (AM ? 2 : 1) + NI * (BM_ ? 2 : 1), kRest = MI * NI - kReads;
+#pragma unroll
+    for (int q = 0; q < kReads; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // a read from LDS
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);     // a product
+    }
+    __builtin_amdgcn_sched_group_barrier(0x8, kRest, 0);
   };
   // each wave waits for its own copies and reads, then for the other waves
   auto sync = [&]() {
-    __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
-    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);    // (products before it stay before it)
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
   };
   copy(0);
   sync();
   if (steps > 1) copy(1);
-  read(0, 0);
+#pragma unroll
+  for (int j = 0; j < NI; ++j) fb[0][j] = rb.read(lds + BM * 128, j, 0);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) fa[0][i] = ra.read(lds, i, 0);
   for (int s = 0; s < steps; ++s) {
     const int cur = s & 1;
-    read(cur, 1);
-    mult(0);
+    phase(std::integral_constant<int, 0>{}, lds + cur * kStage);
     sync();   // the other stage has landed; everyone has read this one
     if (s + 2 < steps) copy(cur);
-    if (s + 1 < steps) read(cur ^ 1, 0);
-    mult(1);
+    // (after the last stage these read what is left there, for nothing)
+    phase(std::integral_constant<int, 1>{}, lds + (cur ^ 1) * kStage);
   }
 
   // lane (g, li), element v of tile (i, j): row 16 i + 4 g + v, column 16 j + li
@@ -427,7 +473,7 @@ __device__ __forceinline__ Raw8<D> load8(const typename Elem<D>::type* row, int6
   typedef typename Elem<D>::type E;
   Raw8<D> r;
   if constexpr (VEC) {
-    __builtin_memcpy(r.e, __builtin_assume_aligned(row + min(k, d - 8), 16), sizeof(r.e));
+    __builtin_memcpy(r.e, __builtin_assume_aligned(row + lmin(k, d - 8), 16), sizeof(r.e));
     if (k >= d) __builtin_memset(r.e, 0, sizeof(r.e));
   } else {
 #pragma unroll
@@ -486,9 +532,9 @@ __global__ __launch_bounds__(256) void score_kernel(const typename Elem<D>::type
   const int64_t v0 = (int64_t)blockIdx.x * 64;
   const typename Elem<D>::type *wr[4], *hr[NT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) wr[i] = W + min<int64_t>(v0 + 16 * i + li, V - 1) * ldw;
+  for (int i = 0; i < 4; ++i) wr[i] = W + lmin(v0 + 16 * i + li, V - 1) * ldw;
 #pragma unroll
-  for (int j = 0; j < NT; ++j) hr[j] = H + min<int64_t>(16 * j + li, T - 1) * ldh;
+  for (int j = 0; j < NT; ++j) hr[j] = H + lmin(16 * j + li, T - 1) * ldh;
   f32x4 acc[4][NT];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
