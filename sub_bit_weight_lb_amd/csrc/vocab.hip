@@ -191,17 +191,23 @@ struct Tile {
       }
     }
   }
-  // The 64 k from k on, of the term `plane` elements into the rows. What lies
-  // past the operand's end reads as zero (the descriptor's range, which counts
-  // the vector offset alone: all of an address below its base is in it). The
-  // copies
-  // are written out: a builtin's would make every transposing read wait for
-  // the copies of the next stage. They write no register, and sync() waits.
-  __device__ __forceinline__ void copy(uint32_t st, int wave, int64_t k, int64_t plane) const {
+  // The copies of the 64 k from k on, of the term `plane` elements into the
+  // rows, to LDS offset st: made ready here, sent one at a time by put(). What
+  // lies past the operand's end reads as zero (the descriptor's range, which
+  // counts the vector offset alone: all of an address below its base is in it).
+  int lo, hi, n, to;
+  uint32_t o[2], step;
+  // (!live: copies of zeros, which read nothing.)
+  __device__ __forceinline__ void aim(bool live, uint32_t st, int wave, int64_t k, int64_t plane) {
     const int64_t skip = (MAJOR ? k * ld : k) + plane;
     const uint64_t p = (uint64_t)(uintptr_t)(base + skip);
-    const int64_t n = lmin(lmax(left - 2 * skip, 0), 0x7fffffff);
-    uint32_t o[2] = {off[0], off[1]};
+    lo = scalar((int)p);
+    hi = scalar((int)(p >> 32) & 0xffff);
+    n = scalar(live ? (int)lmin(lmax(left - 2 * skip, 0), 0x7fffffff) : 0);
+    to = scalar((int)(st + wave * NC * 1024));
+    step = (uint32_t)(kRowsPer * ld * 2);
+    o[0] = off[0];
+    o[1] = off[1];
     if constexpr (!MAJOR) {
       if (k + BK > kv) {
         // octets past kv: past any descriptor's range
@@ -209,30 +215,22 @@ struct Tile {
         for (int c = 0; c < 2; ++c) o[c] = k + 8 * koct[c] >= kv ? 0x80000000u : o[c];
       }
     }
-    static_assert(NC == 4, "the copies below");
-    const uint32_t step = (uint32_t)(kRowsPer * ld * 2);
+  }
+  // Copy c. Written out: after a builtin's every transposing read would wait
+  // for it, though it is for the next stage. It writes no register, sync()
+  // waits for it, and it keeps its place among the reads and sync()s.
+  __device__ __forceinline__ void put(int c) const {
     asm volatile(
         "s_mov_b32 s92, %0\n\t"
         "s_mov_b32 s93, %1\n\t"
         "s_mov_b32 s94, %2\n\t"
         "s_mov_b32 s95, 0x20000\n\t"
-        "s_mov_b32 m0, %3\n\t"
+        "s_add_u32 m0, %3, %4\n\t"
         "s_nop 0\n\t"
-        "buffer_load_dwordx4 %4, s[92:95], 0 offen lds\n\t"
-        "s_add_u32 m0, m0, 0x400\n\t"
-        "s_nop 0\n\t"
-        "buffer_load_dwordx4 %5, s[92:95], 0 offen lds\n\t"
-        "s_add_u32 m0, m0, 0x400\n\t"
-        "s_nop 0\n\t"
-        "buffer_load_dwordx4 %6, s[92:95], 0 offen lds\n\t"
-        "s_add_u32 m0, m0, 0x400\n\t"
-        "s_nop 0\n\t"
-        "buffer_load_dwordx4 %7, s[92:95], 0 offen lds"
+        "buffer_load_dwordx4 %5, s[92:95], 0 offen lds"
         :
-        : "s"(scalar((int)p)), "s"(scalar((int)(p >> 32) & 0xffff)), "s"(scalar((int)n)),
-          "s"(scalar((int)(st + wave * NC * 1024))), "v"(o[kind(0)]),
-          "v"(o[kind(1)] + step), "v"(o[kind(2)] + 2 * step), "v"(o[kind(3)] + 3 * step)
-        : "s92", "s93", "s94", "s95", "scc", "memory");
+        : "s"(lo), "s"(hi), "s"(n), "s"(to), "i"(c * 1024), "v"(o[kind(c)] + c * step)
+        : "s92", "s93", "s94", "s95", "scc");
   }
 };
 // Fragments of the N 16-row groups from group g0 on, half h (32 k) of a stage.
@@ -298,15 +296,23 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
   // passes: h h, h l, l h
   int pass = 0, kt = 0;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-  auto copy = [&](int stage) {
+  // the next stage's copies, ready to go to `stage`
+  auto aim = [&](int stage, bool live) {
     const uint32_t st = lds0 + stage * kStage;
     const int64_t k = k_lo + (int64_t)kt * BK;
-    ta.copy(st, wave, k, D == kF32 && pass == 2 ? a.A.plane : 0);
-    tb.copy(st + BM * 128, wave, k, D == kF32 && pass == 1 ? a.B.plane : 0);
+    ta.aim(live, st, wave, k, D == kF32 && pass == 2 ? a.A.plane : 0);
+    tb.aim(live, st + BM * 128, wave, k, D == kF32 && pass == 1 ? a.B.plane : 0);
     if (++kt == nk) {
       kt = 0;
       ++pass;
     }
+  };
+  auto copy = [&](int stage) {
+    aim(stage, true);
+#pragma unroll
+    for (int c = 0; c < CA; ++c) ta.put(c);
+#pragma unroll
+    for (int c = 0; c < CB; ++c) tb.put(c);
   };
   f32x4 acc[MI][NI];
 #pragma unroll
@@ -314,24 +320,29 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   u32x4 fa[2][MI], fb[2][NI];
-  // Multiplies half h while the other half's fragments come from stage st: a
-  // read between products, one at a time.
-  auto phase = [&](auto half, uint8_t* st) {
+  // Multiplies half h while the other half's fragments come from stage st, and
+  // with COPY the copies made ready go out: a row of products, its reads and
+  // copies at a time (a run of copies would hold up the products behind it).
+  auto phase = [&](auto half, auto copies, uint8_t* st) {
     constexpr int h = decltype(half)::value;
+    constexpr bool COPY = decltype(copies)::value;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       if (i < NI) fb[h ^ 1][i] = rb.read(st + BM * 128, i, h ^ 1);
       fa[h ^ 1][i] = ra.read(st, i, h ^ 1);
 #pragma unroll
       for (int j = 0; j < NI; ++j) acc[i][j] = mma<F16>(fa[h][i], fb[h][j], acc[i][j]);
-    }
-    constexpr int kReads = MI * (AM ? 2 : 1) + NI * (BM_ ? 2 : 1), kRest = MI * NI - kReads;
+      if constexpr (COPY) {
 #pragma unroll
-    for (int q = 0; q < kReads; ++q) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // a read from LDS
-      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);     // a product
+        for (int c = i * (CA + CB) / MI; c < (i + 1) * (CA + CB) / MI; ++c) {
+          if (c < CA)
+            ta.put(c);
+          else
+            tb.put(c - CA);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_sched_group_barrier(0x8, kRest, 0);
   };
   // each wave waits for its own copies and reads, then for the other waves
   auto sync = [&]() {
@@ -346,14 +357,19 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
   for (int j = 0; j < NI; ++j) fb[0][j] = rb.read(lds + BM * 128, j, 0);
 #pragma unroll
   for (int i = 0; i < MI; ++i) fa[0][i] = ra.read(lds, i, 0);
+  typedef std::integral_constant<int, 0> H0;
+  typedef std::integral_constant<int, 1> H1;
   for (int s = 0; s < steps; ++s) {
     const int cur = s & 1;
-    phase(std::integral_constant<int, 0>{}, lds + cur * kStage);
+    phase(H0{}, std::false_type{}, lds + cur * kStage);
     sync();   // the other stage has landed; everyone has read this one
-    if (s + 2 < steps) copy(cur);
-    // (after the last stage these read what is left there, for nothing)
-    phase(std::integral_constant<int, 1>{}, lds + (cur ^ 1) * kStage);
+    // (no branch around the last two stages' copies: they bring zeros; after
+    // the last stage this reads what is left there, for nothing)
+    aim(cur, s + 2 < steps);
+    phase(H1{}, std::true_type{}, lds + (cur ^ 1) * kStage);
   }
+  // the last copies must land before this workgroup's LDS is given away
+  sync();
 
   // lane (g, li), element v of tile (i, j): row 16 i + 4 g + v, column 16 j + li
   const int64_t r0 = m0 + wm * MI * 16 + 4 * g, c0 = n0 + wn * NI * 16 + li;
