@@ -124,6 +124,22 @@ def test_checkpoint_of_hard_values(gpu, name):
 
 
 @pytest.mark.parametrize("name", TYPES)
+def test_checkpoint_of_values_past_the_last_level_cache(gpu, name):
+    """Above 256 MB of values the accesses change; nothing else does."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    rows, cols = 9001, 7501 if name == "float32" else 15001
+    X = torch.randn(rows, cols, device=gpu).mul_(3).to(dt(name))
+    assert X.numel() * X.element_size() > 256 << 20
+    q = nq.act8_quantize(X)
+    got = nq.act8_dequantize(q)
+    for r in (slice(0, 4500), slice(4500, rows)):
+        part = nq.act8_quantize(X[r])
+        assert torch.equal(part.codes, q.codes[r]) and torch.equal(part.exps, q.exps[r])
+        assert torch.equal(nq.act8_dequantize(part), got[r])
+
+
+@pytest.mark.parametrize("name", TYPES)
 @pytest.mark.parametrize("cols, extra, lead", [(33, 5, 1), (64, 1, 3), (1000, 7, 1), (4096, 9, 0)])
 def test_checkpoint_of_views_writes_nothing_else(gpu, name, cols, extra, lead):
     import torch
@@ -354,6 +370,16 @@ def test_loss_and_gradient_match_oracle(gpu, name, T, V, d):
     l2, s2 = nq.vocab_loss(L.H, L.W, L.labels)
     h2, w2 = nq.vocab_loss_backward(L.H, L.W, L.labels, s2, L.dl)
     assert (l2 == loss).all() and (h2 == dH).all() and (w2 == dW).all()
+
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("T, d", [(15, 200), (16, 72), (31, 136), (32, 1000), (33, 129), (48, 64),
+                                  (63, 40), (64, 515)])
+def test_loss_of_few_tokens(gpu, name, T, d):
+    import sub_bit_weight_lb_amd as nq
+    print(f"case T={T} d={d} {name}", flush=True)
+    L = Head(T + d, T, 1500 + T, d, name, gpu)
+    L.check_loss(*nq.vocab_loss(L.H, L.W, L.labels))
 
 
 @pytest.mark.parametrize("name", TYPES)
