@@ -33,9 +33,9 @@
 // over k, leaves out l l, at most 2^-24 of the product. (Three bf16 terms and
 // six passes measured 1.9 times the time at no smaller error.)
 //
-// Few tokens (up to 64, the loss alone): score_kernel streams W once, 64 words
-// per workgroup, its waves sharing the columns; fp32 is split in registers,
-// into three bf16 terms and six products, which need no scale.
+// Few tokens (up to 32, fp32 up to 64, the loss alone): score_kernel streams W
+// once, 64 words per workgroup, its waves sharing the columns; fp32 is split in
+// registers, into three bf16 terms and six products, which need no scale.
 #include "tune.h"
 
 #include <algorithm>
@@ -51,7 +51,11 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 typedef __attribute__((address_space(3))) s16x4* lds_tr_t;
 
 constexpr int BK = 64;            // k per stage
-constexpr int kScoreMax = 64;     // tokens of score_kernel
+// Tokens of score_kernel. Above, mma_kernel reads W at a higher rate although
+// half of a tile is empty (4096 x 32000 bf16, 64 tokens: 94 us, score_kernel
+// 104; 32 tokens: 72 in score_kernel), but fp32 would be copied for it (2048 x
+// 32000, 64 tokens: 309 us, score_kernel 90).
+constexpr int score_max(int dtype) { return dtype == kF32 ? 64 : 32; }
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kTop16 = 32768.0f;   // what fp16 terms are scaled to
 
@@ -476,10 +480,13 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
 }
 
 // ---------------------------------------------------------------- few tokens
-// 64 words and all T <= 16 NT tokens per workgroup; the four waves take runs
-// of 32 S columns in turn, the next run's loads in flight while one multiplies.
-// Rows are 16-byte aligned and d % 8 == 0 (VEC), or elements are loaded one by
-// one.
+// 64 words and all T <= 16 NT tokens per workgroup of 16 / NT waves, which take
+// 32 columns each in turn: neighbours read neighbouring 64 bytes of a row, and
+// many waves with one load per row each keep HBM busiest (4096 x 32000 bf16, 16
+// tokens, in us with the join: 16 waves 59 (4.4 TB/s), 8 waves 63, 4 waves 96;
+// 8 waves of 64 columns 71, 4 waves of 128 columns 80, of two such runs in
+// registers 84). Rows are 16-byte aligned and d % 8 == 0 (VEC), or elements are
+// loaded one by one.
 template <int D>
 struct Raw8 {
   typename Elem<D>::type e[8];
@@ -531,8 +538,10 @@ __device__ __forceinline__ Frag<D> frag_of(const Raw8<D>& r) {
 __device__ __forceinline__ int term_a(int s) { return (0x250 >> (2 * s)) & 3; }   // 0 0 1 1 2 0
 __device__ __forceinline__ int term_b(int s) { return (0x844 >> (2 * s)) & 3; }   // 0 1 0 1 0 2
 
+// (64 registers or fewer: two workgroups of 1024 threads per CU)
 template <int D, int NT, bool VEC>
-__global__ __launch_bounds__(256) void score_kernel(const typename Elem<D>::type* __restrict__ H,
+__global__ __launch_bounds__(1024 / NT)
+    __attribute__((amdgpu_waves_per_eu(D != kF32 && VEC && NT == 1 ? 8 : 1))) void score_kernel(const typename Elem<D>::type* __restrict__ H,
                                                     int64_t ldh,
                                                     const typename Elem<D>::type* __restrict__ W,
                                                     int64_t ldw, int64_t T, int64_t V, int64_t d,
@@ -540,8 +549,8 @@ __global__ __launch_bounds__(256) void score_kernel(const typename Elem<D>::type
                                                     float scale, float* __restrict__ top,
                                                     float* __restrict__ sum,
                                                     float* __restrict__ hit) {
-  constexpr int S = !VEC ? 1 : D == kF32 ? (NT == 4 ? 1 : 2) : (NT == 4 ? 2 : 4);
-  __shared__ f32x4 red[4][4 * NT][64];
+  constexpr int NW = 16 / NT;
+  __shared__ f32x4 red[NW][4 * NT][64];
   __shared__ float st[2][4][16 * NT];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, li = lane & 15;
@@ -556,47 +565,26 @@ __global__ __launch_bounds__(256) void score_kernel(const typename Elem<D>::type
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  struct Run {
-    Raw8<D> w[S][4], h[S][NT];
-  };
-  auto load = [&](Run& r, int64_t k0) {
+  for (int64_t k0 = wave * 32; k0 < d; k0 += 32 * NW) {
+    Raw8<D> w[4], h[NT];
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const int64_t k = k0 + 32 * s + 8 * g;
+    for (int i = 0; i < 4; ++i) w[i] = load8<D, VEC>(wr[i], k0 + 8 * g, d);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r.w[s][i] = load8<D, VEC>(wr[i], k, d);
+    for (int j = 0; j < NT; ++j) h[j] = load8<D, VEC>(hr[j], k0 + 8 * g, d);
+    __builtin_amdgcn_sched_barrier(0);   // (all loads before the first product)
+    Frag<D> b[NT];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) r.h[s][j] = load8<D, VEC>(hr[j], k, d);
+    for (int j = 0; j < NT; ++j) b[j] = frag_of<D>(h[j]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const Frag<D> f = frag_of<D>(w[i]);
+#pragma unroll
+      for (int q = 0; q < (D == kF32 ? 6 : 1); ++q)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          acc[i][j] = mma<D == kF16>(f.t[D == kF32 ? term_a(q) : 0],
+                                     b[j].t[D == kF32 ? term_b(q) : 0], acc[i][j]);
     }
-  };
-  auto mult = [&](const Run& r) {
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      Frag<D> b[NT];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) b[j] = frag_of<D>(r.h[s][j]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const Frag<D> f = frag_of<D>(r.w[s][i]);
-#pragma unroll
-        for (int q = 0; q < (D == kF32 ? 6 : 1); ++q)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-            acc[i][j] = mma<D == kF16>(f.t[D == kF32 ? term_a(q) : 0],
-                                       b[j].t[D == kF32 ? term_b(q) : 0], acc[i][j]);
-      }
-    }
-  };
-  // (runs past d load and add zeros)
-  Run r0, r1;
-  load(r0, wave * 32 * S);
-  for (int64_t k0 = wave * 32 * S; k0 < d; k0 += 256 * S) {
-    load(r1, k0 + 128 * S);
-    __builtin_amdgcn_sched_barrier(0);
-    mult(r0);
-    load(r0, k0 + 256 * S);
-    __builtin_amdgcn_sched_barrier(0);
-    mult(r1);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -606,8 +594,11 @@ __global__ __launch_bounds__(256) void score_kernel(const typename Elem<D>::type
   // wave i joins the 16 words of row tile i
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
+    if (wave >= 4) break;
     const int e = wave * NT + j;
-    const f32x4 z = ((red[0][e][lane] + red[1][e][lane]) + red[2][e][lane]) + red[3][e][lane];
+    f32x4 z = red[0][e][lane];
+#pragma unroll
+    for (int n = 1; n < NW; ++n) z += red[n][e][lane];
     const int64_t t = 16 * j + li, w = v0 + 16 * wave + 4 * g;
     const int32_t label = t < T ? labels[t] : -1;
     float m = kNegInf, x[4];
@@ -691,7 +682,7 @@ struct Factors {
   float zs;              // scale / (mh mw)
   float post_h, post_w;  // of dH and dW
 };
-constexpr int kAmaxParts = 512;
+constexpr int kAmaxParts = 1024;
 // parts[y][x] = the largest finite magnitude of a share of H (y = 0) or W
 __global__ __launch_bounds__(256) void amax_kernel(const float* __restrict__ H, int64_t T,
                                                    int64_t ldh, const float* __restrict__ W,
@@ -706,8 +697,19 @@ __global__ __launch_bounds__(256) void amax_kernel(const float* __restrict__ H, 
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     if (!w && labels[r] < 0) continue;
     const float* x = X + r * ld;
+    // (16 bytes at a time, which may start at any element)
+    int64_t c = 4 * threadIdx.x;
 #pragma unroll 4
-    for (int64_t c = threadIdx.x; c < d; c += 256) {
+    for (; c + 4 <= d; c += 1024) {
+      struct __attribute__((packed)) { float v[4]; } q;
+      __builtin_memcpy(&q, x + c, 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float v = fabsf(q.v[i]);
+        m = v < __builtin_inff() ? fmaxf(m, v) : m;
+      }
+    }
+    for (; c < d; ++c) {
       const float v = fabsf(x[c]);
       m = v < __builtin_inff() ? fmaxf(m, v) : m;
     }
@@ -750,8 +752,8 @@ __global__ __launch_bounds__(1024) void factors_kernel(const float* __restrict__
   float mh = 1.0f, mw = 1.0f, m = 0.0f;
   if (parts) {
     const int t = threadIdx.x;
-    mh = power_for(max_of(t < kAmaxParts ? parts[t] : 0.0f, sm));
-    mw = power_for(max_of(t < kAmaxParts ? parts[kAmaxParts + t] : 0.0f, sm));
+    mh = power_for(max_of(parts[t], sm));
+    mw = power_for(max_of(parts[kAmaxParts + t], sm));
   }
   if (dloss) {
     for (int64_t t = threadIdx.x; t < T; t += 1024)
@@ -851,11 +853,15 @@ bool big_tiles(int64_t M, int64_t N, int64_t slices) {
   const int64_t small = ((M + 127) / 128) * ((N + 127) / 128) * slices;
   return (big + 255) / 256 * 4.0 <= (small + 255) / 256 * 1.25;
 }
-// Slices of the contraction of dH: a workgroup for every CU, 256 words at
-// least.
+// Slices of the contraction of dH: a workgroup for every CU, in big tiles where
+// those are enough for most of the CUs, 256 words at least.
 int dh_slices(int64_t T, int64_t d, int64_t piece) {
-  const int64_t tiles = ((d + 127) / 128) * ((T + 127) / 128);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, piece / 256, 64}));
+  const int64_t big = ((d + 255) / 256) * ((T + 255) / 256);
+  const int64_t small = ((d + 127) / 128) * ((T + 127) / 128);
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(piece / 256, 64));
+  const int64_t nb = std::max<int64_t>(1, std::min(256 / big, most));
+  if (big * nb >= 192) return (int)nb;
+  return (int)std::max<int64_t>(1, std::min(512 / small, most));
 }
 // Words per piece: G, and a copy of W's piece where one is needed, hold at most
 // 2^26 values each (two thousand words at least), which leaves the fp32 sums of
@@ -880,7 +886,7 @@ Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad) {
     p.top = take(4 * np * T);
     p.sum = take(4 * np * T);
     p.hit = take(4 * T);
-    if (T <= kScoreMax) {
+    if (T <= score_max(dtype)) {
       p.bytes = off;
       return p;
     }
@@ -964,11 +970,11 @@ void score(const Vocab& a, const Plan& p, hipStream_t s) {
                    ((uintptr_t)a.H | (uintptr_t)a.W) % 16 == 0;
   const dim3 grid((unsigned)((a.V + 63) / 64));
   if (vec)
-    hipLaunchKernelGGL((score_kernel<D, NT, true>), grid, dim3(256), 0, s, (const E*)a.H, a.ldh,
+    hipLaunchKernelGGL((score_kernel<D, NT, true>), grid, dim3(1024 / NT), 0, s, (const E*)a.H, a.ldh,
                        (const E*)a.W, a.ldw, a.T, a.V, a.d, a.labels, a.scale,
                        (float*)(w + p.top), (float*)(w + p.sum), (float*)(w + p.hit));
   else
-    hipLaunchKernelGGL((score_kernel<D, NT, false>), grid, dim3(256), 0, s, (const E*)a.H, a.ldh,
+    hipLaunchKernelGGL((score_kernel<D, NT, false>), grid, dim3(1024 / NT), 0, s, (const E*)a.H, a.ldh,
                        (const E*)a.W, a.ldw, a.T, a.V, a.d, a.labels, a.scale,
                        (float*)(w + p.top), (float*)(w + p.sum), (float*)(w + p.hit));
 }
@@ -979,11 +985,15 @@ hipError_t loss(const Vocab& a, hipStream_t s) {
   char* w = (char*)a.work;
   hipError_t e;
   int64_t np;   // partials per token
-  if (a.T <= kScoreMax) {
+  if (a.T <= score_max(D)) {
     np = (a.V + 63) / 64;
-    if (a.T <= 16) score<D, 1>(a, p, s);
-    else if (a.T <= 32) score<D, 2>(a, p, s);
-    else score<D, 4>(a, p, s);
+    if (a.T <= 16) {
+      score<D, 1>(a, p, s);
+    } else if (D != kF32 || a.T <= 32) {
+      score<D, 2>(a, p, s);
+    } else if constexpr (D == kF32) {
+      score<D, 4>(a, p, s);
+    }
     if ((e = hipGetLastError()) != hipSuccess) return e;
   } else {
     Mma m{};
