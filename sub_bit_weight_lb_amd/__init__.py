@@ -398,26 +398,31 @@ def _vector(t, name, n, dtype):
 
 
 class _OnDevice:
-    """Makes `index` the current GPU for a block (nothing when it is)."""
+    """The GPU `index`, and calls on it."""
 
     def __init__(self, index):
-        self.index, self.previous = index, None
+        self.index = index
 
-    def __enter__(self):
-        cuda = _torch().cuda
-        now = cuda.current_device()
-        if now != self.index:
-            cuda.set_device(self.index)
-            self.previous = now
-
-    def __exit__(self, *exc):
-        if self.previous is not None:
-            _torch().cuda.set_device(self.previous)
+    def call(self, stream, f):
+        """f(handle) with this GPU the current one, and with `stream`, if one
+        is given, the current stream: what f allocates belongs to the stream
+        that uses it."""
+        torch = _torch()
+        cuda = torch.cuda
+        if stream is None and cuda.current_device() == self.index:
+            return f(torch._C._cuda_getCurrentRawStream(self.index))
+        with cuda.device(self.index):
+            if stream is None:
+                return f(torch._C._cuda_getCurrentRawStream(self.index))
+            stream = int(stream)
+            with cuda.stream(cuda.ExternalStream(stream, self.index) if stream
+                             else cuda.default_stream(self.index)):
+                return f(stream)
 
 
 def _on_device(names, *tensors):
-    """Checks that every tensor (or None) lies on one GPU and returns a context
-    in which that GPU is the current one; names: theirs, separated by spaces."""
+    """Checks that every tensor (or None) lies on one GPU and returns it as an
+    _OnDevice; names: the tensors', separated by spaces."""
     dev = None
     for i, t in enumerate(tensors):
         if t is None:
@@ -469,18 +474,24 @@ def act8_quantize(X, q=None, stream=None):
     torch = _torch()
     rows, cols, ldx = _matrix(X, "X")
     code = _dtype_code(X.dtype, "X")
-    if q is None:
-        groups = -(-cols // ACT8_GROUP)
-        q = Act8(torch.empty((rows, cols), dtype=torch.int8, device=X.device),
-                 torch.empty((rows, groups), dtype=torch.uint8, device=X.device))
-        ldc, lde = max(cols, 1), max(groups, 1)
-    else:
+    groups = -(-cols // ACT8_GROUP)
+    ldc, lde = max(cols, 1), max(groups, 1)
+    if q is not None:
         _, _, ldc, lde = _act8(q, "q", rows, cols)
-    q.dtype = X.dtype
-    with _on_device("X codes exps", X, q.codes, q.exps):
-        _check(_lib.load().nq_act8_quantize(_p(X), code, rows, cols, ldx, _p(q.codes), ldc,
-                                            _p(q.exps), lde, _stream(stream)), "nq_act8_quantize")
-    return q
+        on = _on_device("X codes exps", X, q.codes, q.exps)
+    else:
+        on = _on_device("X", X)
+
+    def run(handle):
+        o = q
+        if o is None:
+            o = Act8(torch.empty((rows, cols), dtype=torch.int8, device=X.device),
+                     torch.empty((rows, groups), dtype=torch.uint8, device=X.device))
+        o.dtype = X.dtype
+        _check(_lib.load().nq_act8_quantize(_p(X), code, rows, cols, ldx, _p(o.codes), ldc,
+                                            _p(o.exps), lde, handle), "nq_act8_quantize")
+        return o
+    return on.call(stream, run)
 
 
 def act8_dequantize(q, out=None, dtype=None, stream=None):
@@ -488,18 +499,22 @@ def act8_dequantize(q, out=None, dtype=None, stream=None):
     float32 when q does not say), or into out."""
     torch = _torch()
     rows, cols, ldc, lde = _act8(q, "q")
-    if out is None:
-        out = torch.empty((rows, cols), dtype=dtype or q.dtype or torch.float32,
-                          device=q.codes.device)
-        ldo = max(cols, 1)
-    else:
+    if out is not None:
         _, _, ldo = _matrix(out, "out", rows, cols, dtype)
-    code = _dtype_code(out.dtype, "out")
-    with _on_device("codes exps out", q.codes, q.exps, out):
+        dtype = out.dtype
+    else:
+        dtype, ldo = dtype or q.dtype or torch.float32, max(cols, 1)
+    code = _dtype_code(dtype, "out")
+    on = _on_device("codes exps out", q.codes, q.exps, out)
+
+    def run(handle):
+        o = out
+        if o is None:
+            o = torch.empty((rows, cols), dtype=dtype, device=q.codes.device)
         _check(_lib.load().nq_act8_dequantize(_p(q.codes), ldc, _p(q.exps), lde, rows, cols,
-                                              _p(out), code, ldo, _stream(stream)),
-               "nq_act8_dequantize")
-    return out
+                                              _p(o), code, ldo, handle), "nq_act8_dequantize")
+        return o
+    return on.call(stream, run)
 
 
 def act8_steps(q, stream=None):
@@ -508,11 +523,13 @@ def act8_steps(q, stream=None):
     torch = _torch()
     _, _, _, lde = _act8(q, "q")
     rows, groups = q.exps.shape
-    steps = torch.empty((rows, groups), dtype=torch.float32, device=q.exps.device)
-    with _on_device("exps", q.exps):
+
+    def run(handle):
+        steps = torch.empty((rows, groups), dtype=torch.float32, device=q.exps.device)
         _check(_lib.load().nq_act8_steps(_p(q.exps), lde, rows, groups, _p(steps),
-                                         max(groups, 1), _stream(stream)), "nq_act8_steps")
-    return steps
+                                         max(groups, 1), handle), "nq_act8_steps")
+        return steps
+    return _on_device("exps", q.exps).call(stream, run)
 
 
 def binary_matmul_backward_work_bytes(T, m, n, r):
@@ -550,30 +567,32 @@ def binary_matmul_backward(U_bits, Ut_bits, V_bits, Vt_bits, s1, s2, X, dY, r, w
     _vector(s2, "s2", n, f32)
     _, _, lddy = _matrix(dY, "dY", T, m)
     code = _dtype_code(dY.dtype, "dY")
-    lddx = 0
     if dX is not None:
         _, _, lddx = _matrix(dX, "dX", T, n, dY.dtype)
-    elif want_dX:
-        dX, lddx = torch.empty((T, n), dtype=dY.dtype, device=dY.device), max(n, 1)
-    if ds1 is None:
-        ds1 = torch.empty(m, dtype=f32, device=dY.device)
     else:
+        lddx = max(n, 1)
+    if ds1 is not None:
         _vector(ds1, "ds1", m, f32)
-    if ds2 is None:
-        ds2 = torch.empty(n, dtype=f32, device=dY.device)
-    else:
+    if ds2 is not None:
         _vector(ds2, "ds2", n, f32)
     if min(m, n, r) < 1:
         raise ValueError("m, n and r must be >= 1")
-    with _on_device("U_bits Ut_bits V_bits Vt_bits s1 s2 codes exps dY dX ds1 ds2 work", U_bits,
-                    Ut_bits, V_bits, Vt_bits, s1, s2, X.codes, X.exps, dY, dX, ds1, ds2, work):
+    on = _on_device("U_bits Ut_bits V_bits Vt_bits s1 s2 codes exps dY dX ds1 ds2 work", U_bits,
+                    Ut_bits, V_bits, Vt_bits, s1, s2, X.codes, X.exps, dY, dX, ds1, ds2, work)
+
+    def run(handle):
+        def out(t, shape, dtype):
+            return torch.empty(shape, dtype=dtype, device=dY.device) if t is None else t
+        x = out(dX, (T, n), dY.dtype) if want_dX or dX is not None else None
+        g1, g2 = out(ds1, m, f32), out(ds2, n, f32)
         lib = _lib.load()
-        work = _workspace(work, lib.nq_binary_matmul_backward_work_bytes(T, m, n, r), dY.device)
+        w = _workspace(work, lib.nq_binary_matmul_backward_work_bytes(T, m, n, r), dY.device)
         _check(lib.nq_binary_matmul_backward(
             _p(U_bits), lds[0], _p(Ut_bits), lds[1], _p(V_bits), lds[2], _p(Vt_bits), lds[3], m, n,
-            r, _p(s1), _p(s2), _p(X.codes), ldc, _p(X.exps), lde, T, _p(dY), code, lddy, _p(dX),
-            lddx, _p(ds1), _p(ds2), _p(work), _stream(stream)), "nq_binary_matmul_backward")
-    return dX, ds1, ds2
+            r, _p(s1), _p(s2), _p(X.codes), ldc, _p(X.exps), lde, T, _p(dY), code, lddy, _p(x),
+            lddx, _p(g1), _p(g2), _p(w), handle), "nq_binary_matmul_backward")
+        return x, g1, g2
+    return on.call(stream, run)
 
 
 def vocab_loss_work_bytes(T, V, d, dtype, grad=False):
@@ -604,20 +623,21 @@ def vocab_loss(H, W, labels, scale=1.0, loss=None, lse=None, work=None, stream=N
     torch = _torch()
     f32 = torch.float32
     T, V, d, code, ldh, ldw = _vocab_args(H, W, labels)
-    if loss is None:
-        loss = torch.empty(T, dtype=f32, device=H.device)
-    else:
+    if loss is not None:
         _vector(loss, "loss", T, f32)
-    if lse is None:
-        lse = torch.empty(T, dtype=f32, device=H.device)
-    else:
+    if lse is not None:
         _vector(lse, "lse", T, f32)
-    with _on_device("H W labels loss lse work", H, W, labels, loss, lse, work):
+    on = _on_device("H W labels loss lse work", H, W, labels, loss, lse, work)
+
+    def run(handle):
+        a = torch.empty(T, dtype=f32, device=H.device) if loss is None else loss
+        b = torch.empty(T, dtype=f32, device=H.device) if lse is None else lse
         lib = _lib.load()
-        work = _workspace(work, lib.nq_vocab_loss_work_bytes(T, V, d, code, 0), H.device)
+        w = _workspace(work, lib.nq_vocab_loss_work_bytes(T, V, d, code, 0), H.device)
         _check(lib.nq_vocab_loss(_p(H), ldh, _p(W), ldw, code, T, V, d, _p(labels), float(scale),
-                                 _p(loss), _p(lse), _p(work), _stream(stream)), "nq_vocab_loss")
-    return loss, lse
+                                 _p(a), _p(b), _p(w), handle), "nq_vocab_loss")
+        return a, b
+    return on.call(stream, run)
 
 
 def vocab_loss_backward(H, W, labels, lse, dloss, scale=1.0, want_dH=True, want_dW=True, dH=None,
@@ -632,28 +652,33 @@ def vocab_loss_backward(H, W, labels, lse, dloss, scale=1.0, want_dH=True, want_
     T, V, d, code, ldh, ldw = _vocab_args(H, W, labels)
     _vector(lse, "lse", T, torch.float32)
     _vector(dloss, "dloss", T, torch.float32)
-    lddh = lddw = 0
+    lddh = lddw = d
     if dH is not None:
         _, _, lddh = _matrix(dH, "dH", T, d, H.dtype)
-    elif want_dH:
-        dH, lddh = torch.empty((T, d), dtype=H.dtype, device=H.device), d
     if dW is not None:
         _, _, lddw = _matrix(dW, "dW", V, d, H.dtype)
-    elif want_dW:
-        dW, lddw = torch.empty((V, d), dtype=H.dtype, device=H.device), d
-    if dH is None and dW is None:
+    want_dH, want_dW = want_dH or dH is not None, want_dW or dW is not None
+    if not (want_dH or want_dW):
         raise ValueError("neither dH nor dW is wanted")
-    with _on_device("H W labels lse dloss dH dW work", H, W, labels, lse, dloss, dH, dW, work):
+    on = _on_device("H W labels lse dloss dH dW work", H, W, labels, lse, dloss, dH, dW, work)
+
+    def run(handle):
+        gH, gW = dH, dW
+        if want_dH and gH is None:
+            gH = torch.empty((T, d), dtype=H.dtype, device=H.device)
+        if want_dW and gW is None:
+            gW = torch.empty((V, d), dtype=H.dtype, device=H.device)
         if T == 0:
-            if dW is not None:
-                dW.zero_()
-            return dH, dW
+            if gW is not None:
+                gW.zero_()
+            return gH, gW
         lib = _lib.load()
-        work = _workspace(work, lib.nq_vocab_loss_work_bytes(T, V, d, code, 1), H.device)
+        w = _workspace(work, lib.nq_vocab_loss_work_bytes(T, V, d, code, 1), H.device)
         _check(lib.nq_vocab_loss_backward(
             _p(H), ldh, _p(W), ldw, code, T, V, d, _p(labels), float(scale), _p(lse), _p(dloss),
-            _p(dH), lddh, _p(dW), lddw, _p(work), _stream(stream)), "nq_vocab_loss_backward")
-    return dH, dW
+            _p(gH), lddh, _p(gW), lddw, _p(w), handle), "nq_vocab_loss_backward")
+        return gH, gW
+    return on.call(stream, run)
 
 
 class LedoitWolf:
@@ -777,11 +802,11 @@ class STERefiner:
         if not 1 <= T <= self.max_tokens:
             raise ValueError(f"a batch holds 1 .. {self.max_tokens} tokens")
         if isinstance(X, Act8):
-            with _on_device("codes exps Y rows", X.codes, X.exps, Y, rows):
-                _check(_lib.load().nq_ste_step_act8(
+            _on_device("codes exps Y rows", X.codes, X.exps, Y, rows).call(
+                stream, lambda handle: _check(_lib.load().nq_ste_step_act8(
                     C.c_void_p(self.handle), _p(X.codes), ldc, _p(X.exps), lde,
                     _ptr(Y, "Y", f32, 2, need_contig=False), _matrix(Y, "Y")[2], rp, T, float(lr),
-                    _stream(stream)), "nq_ste_step_act8")
+                    handle), "nq_ste_step_act8"))
             return
         _check(_lib.load().nq_ste_step(
             C.c_void_p(self.handle), _ptr(X, "X", f32, 2, need_contig=False), X.stride(0),

@@ -628,6 +628,38 @@ def test_calls_on_two_streams_at_once(gpu):
         assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
+def test_what_a_call_allocates_belongs_to_the_stream_it_is_given(gpu):
+    """Calls on a stream passed by its handle, while the current stream takes
+    and fills memory of the sizes that the calls have just let go."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    L = Layer(33, 300, 384, 320, 96, "float32", gpu)
+    Hd = Head(34, 300, 5000, 256, "float32", gpu)
+
+    def run(**kw):
+        loss, lse = nq.vocab_loss(Hd.H, Hd.W, Hd.labels, **kw)
+        return (loss, *nq.vocab_loss_backward(Hd.H, Hd.W, Hd.labels, lse, Hd.dl, **kw),
+                *nq.binary_matmul_backward(*L.args(), **kw),
+                nq.act8_dequantize(nq.act8_quantize(Hd.W, **kw), **kw))
+
+    want = run()
+    sizes = [nq.vocab_loss_work_bytes(300, 5000, 256, torch.float32, g) for g in (False, True)]
+    sizes.append(nq.binary_matmul_backward_work_bytes(300, 384, 320, 96))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    here = torch.cuda.current_stream()
+    for _ in range(3):
+        got = run(stream=side.cuda_stream)
+        assert torch.cuda.current_stream() == here
+        for n in sizes:
+            torch.empty(n, dtype=torch.uint8, device=gpu).fill_(255)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    got = run(stream=0)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_refinement_from_a_checkpoint_is_the_same_step(gpu):
     """STERefiner on a checkpoint of its inputs equals, bit for bit, the steps
     on the values that the checkpoint stands for."""
