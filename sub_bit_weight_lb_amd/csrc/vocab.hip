@@ -103,7 +103,8 @@ struct Mma {
   Opnd A, B;                // C (M x N), M = A.rows, N = B.rows
   int64_t K;                // a multiple of 64
   int64_t k_slice;          // k per slice (grid y), a multiple of 64
-  const float* zs;          // kStat, kGrad: the factor of the products (one float)
+  const float* zs;          // kStat, kGrad: the factor of the products (fp32: one float on the
+  float z0;                 // GPU; 16-bit: z0)
   // kStat, kGrad: rows are words v0 .., columns tokens
   int64_t v0;
   const int32_t* labels;
@@ -124,12 +125,12 @@ constexpr bool b_major(int epi) { return epi == kDw; }
 // Tile order: workgroup b runs on XCD b % 8, which takes consecutive indices;
 // indices run down bands of 4 tile rows, so that the 32 tiles an XCD holds at
 // once form a 4 x 8 block and share operands in its L2.
-__device__ __forceinline__ bool tile_of(int64_t ntm, int64_t ntn, int64_t& tm, int64_t& tn) {
-  const int64_t nt = ntm * ntn, per = (nt + 7) / 8;
-  const int64_t t = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if ((int64_t)(blockIdx.x >> 3) >= per || t >= nt) return false;
-  const int64_t band = t / (4 * ntn), idx = t - band * 4 * ntn;
-  const int64_t h = lmin(4, ntm - 4 * band);
+__device__ __forceinline__ bool tile_of(uint32_t ntm, uint32_t ntn, int64_t& tm, int64_t& tn) {
+  const uint32_t nt = ntm * ntn, per = (nt + 7) / 8;   // (< 2^31: 2^24 x 2^20 outputs at most)
+  const uint32_t t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((blockIdx.x >> 3) >= per || t >= nt) return false;
+  const uint32_t band = t / (4 * ntn), idx = t - band * 4 * ntn;
+  const uint32_t h = min(4u, ntm - 4 * band);
   tm = 4 * band + idx % h;
   tn = idx / h;
   return true;
@@ -266,24 +267,25 @@ struct Reader {
   }
 };
 
-// WM x WN waves of 16 MI x 16 NI (MI >= NI). Two stages of 64 k in LDS; a
+// WM x WN waves of 16 MI x 16 NI (MI >= NI). NS stages of 64 k in LDS; a
 // stage's copies go out as soon as everyone has read the stage that they
-// replace, a half-stage of products and more before they are waited for.
-template <int D, int EPI, int WM, int WN, int MI, int NI>
+// replace, NS - 2 stages, a half-stage of products and more before they are
+// waited for. (NS: mma_launch.)
+template <int D, int EPI, int WM, int WN, int MI, int NI, int NS>
 __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
   constexpr int BM = 16 * MI * WM, BN = 16 * NI * WN, W = WM * WN;
   constexpr int kStage = (BM + BN) * 128;
   constexpr int CA = BM / 8 / W, CB = BN / 8 / W;
   static_assert(CA * 8 * W == BM && CB * 8 * W == BN, "copies");
   constexpr bool AM = a_major(EPI), BM_ = b_major(EPI), F16 = D != kBF16;
-  __shared__ __align__(16) uint8_t lds[2 * kStage];
+  __shared__ __align__(16) uint8_t lds[NS * kStage];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, li = lane & 15;
   const int wm = wave / WN, wn = wave % WN;
   const int64_t M = a.A.rows, N = a.B.rows;
   int64_t tm, tn;
-  if (!tile_of((M + BM - 1) / BM, (N + BN - 1) / BN, tm, tn)) return;
+  if (!tile_of((uint32_t)((M + BM - 1) / BM), (uint32_t)((N + BN - 1) / BN), tm, tn)) return;
   const int64_t m0 = tm * BM, n0 = tn * BN;
   const int64_t k_lo = (int64_t)blockIdx.y * a.k_slice;
   const int nk = (int)((lmin(a.K, k_lo + a.k_slice) - k_lo) / BK);
@@ -310,13 +312,6 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
       kt = 0;
       ++pass;
     }
-  };
-  auto copy = [&](int stage) {
-    aim(stage, true);
-#pragma unroll
-    for (int c = 0; c < CA; ++c) ta.put(c);
-#pragma unroll
-    for (int c = 0; c < CB; ++c) tb.put(c);
   };
   f32x4 acc[MI][NI];
 #pragma unroll
@@ -348,37 +343,49 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // each wave waits for its own copies and reads, then for the other waves
-  auto sync = [&]() {
+  // each wave waits for its reads and for its own copies, but for those of the
+  // last `ahead` stages, then for the other waves
+  auto sync = [&](auto ahead) {
     __builtin_amdgcn_sched_barrier(0);    // (products before it stay before it)
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(decltype(ahead)::value * (CA + CB))
+                 : "memory");
     __builtin_amdgcn_sched_barrier(0);
   };
-  copy(0);
-  sync();
-  if (steps > 1) copy(1);
+  // (copies of stages past the last bring zeros and read nothing: a branch
+  // around them would cost more, and every wait counts the same)
+#pragma unroll 1
+  for (int st = 0; st < NS; ++st) {
+    aim(st, st < steps);
+#pragma unroll
+    for (int c = 0; c < CA; ++c) ta.put(c);
+#pragma unroll
+    for (int c = 0; c < CB; ++c) tb.put(c);
+  }
+  sync(std::integral_constant<int, NS - 1>{});
 #pragma unroll
   for (int j = 0; j < NI; ++j) fb[0][j] = rb.read(lds + BM * 128, j, 0);
 #pragma unroll
   for (int i = 0; i < MI; ++i) fa[0][i] = ra.read(lds, i, 0);
   typedef std::integral_constant<int, 0> H0;
   typedef std::integral_constant<int, 1> H1;
+  int cur = 0;
   for (int s = 0; s < steps; ++s) {
-    const int cur = s & 1;
+    const int next = cur + 1 == NS ? 0 : cur + 1;
     phase(H0{}, std::false_type{}, lds + cur * kStage);
-    sync();   // the other stage has landed; everyone has read this one
-    // (no branch around the last two stages' copies: they bring zeros; after
-    // the last stage this reads what is left there, for nothing)
-    aim(cur, s + 2 < steps);
-    phase(H1{}, std::true_type{}, lds + (cur ^ 1) * kStage);
+    // the next stage has landed; everyone has read this one
+    sync(std::integral_constant<int, NS - 2>{});
+    aim(cur, s + NS < steps);
+    // (after the last stage this reads what is there, for nothing)
+    phase(H1{}, std::true_type{}, lds + next * kStage);
+    cur = next;
   }
   // the last copies must land before this workgroup's LDS is given away
-  sync();
+  sync(std::integral_constant<int, 0>{});
 
   // lane (g, li), element v of tile (i, j): row 16 i + 4 g + v, column 16 j + li
   const int64_t r0 = m0 + wm * MI * 16 + 4 * g, c0 = n0 + wn * NI * 16 + li;
   if constexpr (EPI == kStat) {
-    const float zs = *a.zs;
+    const float zs = D == kF32 ? *a.zs : a.z0;
     const int64_t half = a.v0 / (16 * MI) + tm * WM + wm;
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
@@ -411,7 +418,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
       }
     }
   } else if constexpr (EPI == kGrad) {
-    const float zs = *a.zs;
+    const float zs = D == kF32 ? *a.zs : a.z0;
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const int64_t t = c0 + 16 * j;
@@ -905,15 +912,21 @@ Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad) {
   return p;
 }
 
+// Four stages where there is one workgroup per CU at most, so that its LDS has
+// no other use, and k is long enough to win their start back (301 tokens, 4999
+// words of bf16: 8 stages of k 14 us with either, 16 stages 18 v 20, 32 stages
+// 27 v 32; 4 stages 19 v 15; 128 tokens, 32000 words, 64 stages: 52 v 80).
 template <int D, int EPI>
 hipError_t mma_launch(const Mma& a, bool big, int slices, hipStream_t s) {
   const int64_t t = big ? 256 : 128;
   const int64_t tiles = ((a.A.rows + t - 1) / t) * ((a.B.rows + t - 1) / t);
   const dim3 grid((unsigned)((tiles + 7) / 8 * 8), (unsigned)slices);
   if (big)
-    hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 4, 8, 4>), grid, dim3(512), 0, s, a);
+    hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 4, 8, 4, 2>), grid, dim3(512), 0, s, a);
+  else if (tiles * slices <= 256 && std::min(a.K, a.k_slice) / BK * passes(D) >= 16)
+    hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 2, 4, 4, 4>), grid, dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 2, 4, 4>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 2, 4, 4, 2>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -926,23 +939,30 @@ hipError_t pack(const void* X, int64_t rows, int64_t k, int64_t ld, const int32_
   return hipGetLastError();
 }
 
-// The factors of a call (and wn with dloss), and H's rows with those of
-// ignored tokens zeroed.
+// The factors of a call (and wn with dloss), and H: rows with those of ignored
+// tokens zeroed, which dW's sums over the tokens need, or for the loss alone in
+// place where it can be (an ignored token's column of products is not used).
 template <int D>
 hipError_t begin(const Vocab& a, const Plan& p, const float* dloss, Opnd* H, hipStream_t s) {
   char* w = (char*)a.work;
   Factors* fac = (Factors*)(w + p.fac);
   float* amax = (float*)(w + p.amax);
   hipError_t e;
+  if (D != kF32 && !dloss && direct(a.H, a.ldh, a.d, D)) {
+    *H = Opnd{(const uint16_t*)a.H, a.ldh, 0, a.T, a.d};
+    return hipSuccess;
+  }
   if (D == kF32) {
     hipLaunchKernelGGL(amax_kernel, dim3(kAmaxParts, 2), dim3(256), 0, s, (const float*)a.H, a.T,
                        a.ldh, (const float*)a.W, a.V, a.ldw, a.d, a.labels, amax);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(factors_kernel, dim3(1), dim3(1024), 0, s, D == kF32 ? amax : nullptr, dloss,
-                     a.labels, a.T, a.V, D == kBF16 ? 1.0f : kTop16, a.scale, (float*)(w + p.wn),
-                     fac);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (D == kF32 || dloss) {
+    hipLaunchKernelGGL(factors_kernel, dim3(1), dim3(1024), 0, s, D == kF32 ? amax : nullptr,
+                       dloss, a.labels, a.T, a.V, D == kBF16 ? 1.0f : kTop16, a.scale,
+                       (float*)(w + p.wn), fac);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   uint16_t* out = (uint16_t*)(w + p.hp);
   *H = Opnd{out, p.dp * terms(D), p.dp, a.T, p.dp};
   return pack<D>(a.H, a.T, a.d, a.ldh, a.labels, &fac->mh, out, p.tp, p.dp, s);
@@ -1000,6 +1020,7 @@ hipError_t loss(const Vocab& a, hipStream_t s) {
     if ((e = begin<D>(a, p, nullptr, &m.B, s)) != hipSuccess) return e;
     m.K = m.k_slice = p.dp;
     m.zs = &((Factors*)(w + p.fac))->zs;
+    m.z0 = a.scale;
     m.labels = a.labels;
     m.top = (float*)(w + p.top); m.sum = (float*)(w + p.sum); m.hit = (float*)(w + p.hit);
     // all words at once where W is used in place
@@ -1041,6 +1062,7 @@ hipError_t backward(const Vocab& a, hipStream_t s) {
     m.A = W; m.B = H;
     m.K = m.k_slice = p.dp;
     m.zs = &fac->zs;
+    m.z0 = a.scale;
     m.v0 = v0; m.labels = a.labels; m.lse = a.lse; m.wn = (float*)(w + p.wn);
     m.G = G; m.gld = p.piece;
     if ((e = mma_launch<D, kGrad>(m, big_tiles(nv, a.T, 1), 1, s)) != hipSuccess) return e;
