@@ -62,28 +62,42 @@ constexpr int kDigit = 2048;      // bytes of a digit per 16 rows and 128 column
 constexpr int kThinMax = 64;      // rows of a thin launch
 constexpr int kThinWaves = 8;
 constexpr int kMaxSplit = 8;      // slices of the columns (wide, few tiles)
-constexpr int64_t kTeamRows = 1024;   // up to this many rows, a workgroup per row
+// Up to this many rows, a workgroup per row, else eight rows per workgroup
+// (whole calls in us, rank 1024: 200 rows of a 4096 x 4096 layer 56 v 77, 512
+// rows of 11008 x 4096 117 v 139, 1000 rows of 4096 x 4096 119 v 112).
+constexpr int64_t kTeamRows = 512;
 // the largest magnitude of ND balanced digits, 1.99215...  2^(8 ND - 2): an
 // fp32 value with a mantissa up to this is below it
 constexpr uint32_t kTopMant = 8322814;
 
 // ---------------------------------------------------------------- rows
-// Sources of four columns c, c + 8, c + 16, c + 24 of a row (of one 32-column
-// word); columns past the end are 0.
+// Sources of four columns c .. c + 3 of a row, c a multiple of 4 (past the end:
+// 0), loaded together from any address.
+template <class T>
+struct __attribute__((packed)) Four {
+  T v[4];
+};
+template <class T>
+__device__ __forceinline__ Four<T> load4(const T* p, int64_t left) {
+  Four<T> r;
+  if (left >= 4) {
+    __builtin_memcpy(&r, p, sizeof(r));
+  } else {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) r.v[d] = d < left ? p[d] : (T)0;
+  }
+  return r;
+}
 struct SrcAct {      // s2 * x^
   Act8 q;
   const float* scale;
   int64_t cols;
   __device__ __forceinline__ void load(int64_t row, int64_t c, float (&x)[4]) const {
-    if (c >= cols) {
-      x[0] = x[1] = x[2] = x[3] = 0.0f;
-      return;
-    }
-    const float st = act8_step(q.exps[row * q.lde + (c >> 5)]);
-    const int8_t* p = q.codes + row * q.ldc + c;
+    const float st = c < cols ? act8_step(q.exps[row * q.lde + (c >> 5)]) : 0.0f;
+    const Four<int8_t> v = load4(q.codes + row * q.ldc + c, cols - c);
+    const Four<float> f = load4(scale + c, cols - c);
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
-      x[b] = c + 8 * b < cols ? (float)p[8 * b] * st * scale[c + 8 * b] : 0.0f;
+    for (int d = 0; d < 4; ++d) x[d] = c + d < cols ? (float)v.v[d] * st * f.v[d] : 0.0f;
   }
 };
 template <int D>
@@ -93,10 +107,10 @@ struct SrcGrad {     // s1 * dy
   const float* scale;
   int64_t cols;
   __device__ __forceinline__ void load(int64_t row, int64_t c, float (&x)[4]) const {
-    const typename Elem<D>::type* q = p + row * ld + c;
+    const Four<typename Elem<D>::type> v = load4(p + row * ld + c, cols - c);
+    const Four<float> f = load4(scale + c, cols - c);
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
-      x[b] = c + 8 * b < cols ? Elem<D>::to(q[8 * b]) * scale[c + 8 * b] : 0.0f;
+    for (int d = 0; d < 4; ++d) x[d] = Elem<D>::to(v.v[d]) * f.v[d];
   }
 };
 struct SrcProj {     // p or dp: fp32, or the fp64 partial sums of nsum slices
@@ -106,19 +120,19 @@ struct SrcProj {     // p or dp: fp32, or the fp64 partial sums of nsum slices
   int64_t cols;
   __device__ __forceinline__ void load(int64_t row, int64_t c, float (&x)[4]) const {
     if (nsum == 1) {
-      const float* q = (const float*)p + row * ld + c;
+      const Four<float> v = load4((const float*)p + row * ld + c, cols - c);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) x[b] = c + 8 * b < cols ? q[8 * b] : 0.0f;
+      for (int d = 0; d < 4; ++d) x[d] = v.v[d];
       return;
     }
-    const double* q = (const double*)p + row * ld + c;
+    double a[4] = {0.0, 0.0, 0.0, 0.0};
+    for (int z = 0; z < nsum; ++z) {
+      const Four<double> v = load4((const double*)p + z * slice + row * ld + c, cols - c);
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      double a = 0.0;
-      if (c + 8 * b < cols)
-        for (int z = 0; z < nsum; ++z) a += q[z * slice + 8 * b];
-      x[b] = (float)a;
+      for (int d = 0; d < 4; ++d) a[d] += v.v[d];
     }
+#pragma unroll
+    for (int d = 0; d < 4; ++d) x[d] = (float)a[d];
   }
 };
 
@@ -136,15 +150,8 @@ template <int ND>
 __device__ __forceinline__ int row_exponent(uint32_t mx) {
   return max((int)(mx >> 23) - 127 - (8 * ND - 2) + ((mx & 0x7fffffu) > kTopMant), -126);
 }
-// Four values of a word as digits: out[p] holds digit p of column b in byte b.
-// With 128 added to each digit's place the bytes of an integer are its balanced
-// digits plus 128; then a 4 x 4 transpose of bytes.
-template <int ND>
-__device__ __forceinline__ void to_digits(const float (&x)[4], float inv, uint32_t (&out)[4]) {
-  constexpr uint32_t kBias = ND == 4 ? 0x80808080u : 0x00808080u;
-  uint32_t u[4];
-#pragma unroll
-  for (int b = 0; b < 4; ++b) u[b] = ((uint32_t)(int)rintf(x[b] * inv) + kBias) ^ 0x80808080u;
+// out[k] = byte k of u[0], u[1], u[2], u[3]
+__device__ __forceinline__ void transpose_bytes(const uint32_t (&u)[4], uint32_t (&out)[4]) {
   const uint32_t a = __builtin_amdgcn_perm(u[1], u[0], 0x05010400u);
   const uint32_t c = __builtin_amdgcn_perm(u[3], u[2], 0x05010400u);
   const uint32_t d = __builtin_amdgcn_perm(u[1], u[0], 0x07030602u);
@@ -154,19 +161,37 @@ __device__ __forceinline__ void to_digits(const float (&x)[4], float inv, uint32
   out[2] = __builtin_amdgcn_perm(e, d, 0x05040100u);
   out[3] = __builtin_amdgcn_perm(e, d, 0x07060302u);
 }
+// Four values as digits: out[p] holds digit p of value d in byte d. With 128
+// added to each digit's place the bytes of an integer are its balanced digits
+// plus 128.
+template <int ND>
+__device__ __forceinline__ void to_digits(const float (&x)[4], float inv, uint32_t (&out)[4]) {
+  constexpr uint32_t kBias = ND == 4 ? 0x80808080u : 0x00808080u;
+  uint32_t u[4];
+#pragma unroll
+  for (int d = 0; d < 4; ++d) u[d] = ((uint32_t)(int)rintf(x[d] * inv) + kBias) ^ 0x80808080u;
+  transpose_bytes(u, out);
+}
 
 // 128-column blocks of a row of digits: whole groups of four
 __host__ __device__ __forceinline__ int64_t blocks(int64_t cols) { return (cols + 511) / 512 * 4; }
 
-// Eight rows per workgroup, a wave each (lane = word (lane / 8) of 256
-// columns, byte position lane % 8 in it), the digits of 256 columns exchanged
-// through LDS so that whole 128-byte lines are stored. TEAM: one row per
+// A wave takes 256 columns of a row at a time, four consecutive ones per lane,
+// and exchanges digits through LDS: a lane's four columns 8 b + 4 s + d, d = 0
+// .. 3, are one byte each of half s's four dwords, so whole halves (16 bytes, b
+// = 0 .. 3) are read back and their bytes transposed. Eight rows per workgroup,
+// a wave each, so that whole 128-byte lines are stored; TEAM: one row per
 // workgroup, its waves taking 256 columns in turn (few rows). blockIdx.y picks
 // one of two jobs. Columns past the end up to a multiple of 512 get zeros.
+// Bound by its loads and stores: 8192 x 4096 fp32 and as many codes to four
+// digits (436 MB) 127 us, 3.4 TB/s (loads of single elements 8 columns apart
+// 137; two waves per row 147).
 template <int ND, bool TEAM, class S0, class S1>
 __global__ __launch_bounds__(512) void rows_kernel(S0 s0, S1 s1, int64_t T, Digits o0, Digits o1) {
-  constexpr int kRun = 8 * 16 + 16;   // eight rows of 16 bytes, padded against bank conflicts
-  __shared__ __align__(16) uint8_t buf[TEAM ? 16 : 2][TEAM ? 16 : ND * 16 * kRun];
+  constexpr int kGroup = TEAM ? 1 : 8;                // rows
+  constexpr int kRun = 16 * kGroup + (TEAM ? 0 : 16); // a half of each row, padded for the banks
+  constexpr int kBuf = ND * 16 * kRun;                // 256 columns
+  __shared__ __align__(16) uint8_t buf[TEAM ? 8 : 2][kBuf];
   __shared__ uint32_t wmax[8];
   __shared__ int wsum[8][ND];
   const int lane = threadIdx.x & 63;
@@ -178,9 +203,9 @@ __global__ __launch_bounds__(512) void rows_kernel(S0 s0, S1 s1, int64_t T, Digi
   const bool in = row < T;
   const int64_t nkb = blocks(cols), nch = nkb / 2;
   const int64_t first = TEAM ? wave : 0, stride = TEAM ? 8 : 1;
-  const int w8 = lane >> 3, sd = lane & 7;
+  const int w8 = lane >> 3, b = (lane >> 1) & 3, s = lane & 1;   // word, and where in it
   auto load = [&](int64_t ch, float (&x)[4]) {
-    const int64_t c = ch * 256 + 32 * w8 + sd;
+    const int64_t c = ch * 256 + 4 * lane;
     if (!in) {
       x[0] = x[1] = x[2] = x[3] = 0.0f;
     } else if (job) {
@@ -223,36 +248,40 @@ __global__ __launch_bounds__(512) void rows_kernel(S0 s0, S1 s1, int64_t T, Digi
   int sum[ND];
 #pragma unroll
   for (int p = 0; p < ND; ++p) sum[p] = 0;
-  uint8_t* block = o.planes + (row >> 4) * nkb * (ND * kDigit);
+  // run (digit, s, word) of LDS holds that half of the group's rows; it goes to
+  // block word % 4 of the 512 columns' four, lane group word / 4, plus two in the
+  // second 256
+  auto half_of = [&](int64_t ch, int run, int64_t r, const uint8_t* src) {
+    const int w = run & 7, h = (run >> 3) & 1, p = run >> 4;
+    const u32x4 v = *(const u32x4*)src;
+    const uint32_t u[4] = {v[0], v[1], v[2], v[3]};
+    uint32_t t[4];
+    transpose_bytes(u, t);
+    *(u32x4*)(o.planes + ((r >> 4) * nkb + (ch >> 1) * 4 + (w & 3)) * (ND * kDigit) + p * kDigit +
+              h * 1024 + (((w >> 2) + 2 * (int)(ch & 1)) * 16 + (int)(r & 15)) * 16) =
+        u32x4{t[0], t[1], t[2], t[3]};
+  };
   auto write = [&](int64_t ch, float (&x)[4]) {
     if (bad) x[0] = x[1] = x[2] = x[3] = 0.0f;
     uint32_t dig[4];
     to_digits<ND>(x, inv, dig);
 #pragma unroll
     for (int p = 0; p < ND; ++p) sum[p] = __builtin_amdgcn_sdot4((int)dig[p], 0x01010101, sum[p], false);
-    // word w8 of these 256 columns: block w8 % 4 of the 512's four, lane group
-    // w8 / 4, plus two in the second half
+    uint8_t* to = buf[TEAM ? wave : ch & 1];
+#pragma unroll
+    for (int p = 0; p < ND; ++p)
+      *(uint32_t*)(to + ((p * 2 + s) * 8 + w8) * kRun + (TEAM ? 0 : wave * 16) + 4 * b) = dig[p];
     if (TEAM) {
-      uint8_t* dst = block + ((ch >> 1) * 4 + (w8 & 3)) * (ND * kDigit) + (sd >> 2) * 1024 +
-                     (((w8 >> 2) + 2 * (int)(ch & 1)) * 16 + (int)(row & 15)) * 16 + 4 * (sd & 3);
-#pragma unroll
-      for (int p = 0; p < ND; ++p) *(uint32_t*)(dst + p * kDigit) = dig[p];
+      // a wave's own 256 columns
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (lane < ND * 16) half_of(ch, lane, row, to + lane * kRun);
+      __builtin_amdgcn_wave_barrier();
     } else {
-      // run (block, digit, s, g) of eight rows, the row's 16 bytes
-      uint8_t* b = buf[ch & 1];
-#pragma unroll
-      for (int p = 0; p < ND; ++p)
-        *(uint32_t*)(b + ((((w8 & 3) * ND + p) * 2 + (sd >> 2)) * 2 + (w8 >> 2)) * kRun + wave * 16 +
-                     4 * (sd & 3)) = dig[p];
       __syncthreads();   // (the other buffer is free: its readers passed this barrier)
       const int t = threadIdx.x;
-      if (t < ND * 128) {
-        const int run = t >> 3, g = (run & 1) + 2 * (int)(ch & 1), s = (run >> 1) & 1, q = run >> 2;
-        const int64_t kb = (ch >> 1) * 4 + q / ND;
-        *(u32x4*)(o.planes + (((int64_t)blockIdx.x >> 1) * nkb + kb) * (ND * kDigit) +
-                  (q % ND) * kDigit + s * 1024 + (g * 16 + (blockIdx.x & 1) * 8 + (t & 7)) * 16) =
-            *(const u32x4*)(b + run * kRun + (t & 7) * 16);
-      }
+      if (t < ND * 128)
+        half_of(ch, t >> 3, (int64_t)blockIdx.x * 8 + (t & 7), to + (t >> 3) * kRun + (t & 7) * 16);
     }
   };
 #pragma unroll
