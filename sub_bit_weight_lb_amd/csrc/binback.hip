@@ -41,13 +41,20 @@
 // wide_kernel (more than kThinMax rows): 256 threads, 2 x 2 waves of 16 MI
 // rows x 16 NJ signs. A wave loads its digits from memory to registers two
 // steps of 64 columns ahead (a fragment is 1 KB in a row; the two waves of a
-// row share it in the L1), without a barrier. The signs of 512 columns are
-// copied to LDS as they are, double buffered, one barrier per eight steps;
-// the digits share one expansion of them (8 NJ vector instructions against
-// MI NJ ND products per step). Workgroup b runs on XCD b % 8, and an XCD takes
+// row share it in the L1). The signs of 512 columns are copied to LDS as they
+// are, double buffered, by each wave for itself: with copies shared by the
+// workgroup and a barrier per 512 columns the waves wait for each other (8192 x
+// 4096 columns of four digits by 2 x 2048 signs' rows 575 us, so 491). The digits
+// share one expansion of the signs (8 NJ vector instructions against MI NJ ND
+// products per step). Workgroup b runs on XCD b % 8, and an XCD takes
 // consecutive tiles, which share their rows' digits in its L2.
+// Bound by how well the loads and the expansion hide behind the products: those
+// 1100 TOP in 491 us are 2.24 POP/s, kGrad's 825 TOP with their epilogue 453 us,
+// 1.82 (products and expansion alone reach 3.7 POP/s, without loads here 2.5; a
+// large int8 product of the library 2.16).
 // thin_kernel (few rows): a workgroup takes all rows and 16 signs' rows, its
-// waves split the columns and add up through LDS.
+// waves split the columns and add up through LDS. Bound by latency: two launches
+// of 7 us for one row of a 4096 x 4096 layer of rank 2048 (2 MB of signs each).
 #include "tune.h"
 
 #include <algorithm>
@@ -56,7 +63,7 @@ namespace nq {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
+typedef __attribute__((address_space(3))) uint32_t* lds_ptr_t;
 
 constexpr int kDigit = 2048;      // bytes of a digit per 16 rows and 128 columns
 constexpr int kThinMax = 64;      // rows of a thin launch
@@ -266,7 +273,8 @@ __global__ __launch_bounds__(512) void rows_kernel(S0 s0, S1 s1, int64_t T, Digi
     uint32_t dig[4];
     to_digits<ND>(x, inv, dig);
 #pragma unroll
-    for (int p = 0; p < ND; ++p) sum[p] = __builtin_amdgcn_sdot4((int)dig[p], 0x01010101, sum[p], false);
+    for (int p = 0; p < ND; ++p)
+      sum[p] = __builtin_amdgcn_sdot4((int)dig[p], 0x01010101, sum[p], false);
     uint8_t* to = buf[TEAM ? wave : ch & 1];
 #pragma unroll
     for (int p = 0; p < ND; ++p)
@@ -322,10 +330,10 @@ enum Epi : int {
   kGrad = 1,   // column sums of dy q; or dx = s2 da and column sums of da x^
 };
 constexpr int digits(int epi) { return epi == kProj ? 4 : 3; }
-// A wide wave's tile in units of 16 rows and 16 signs: 128 and 144 registers
-// of sums
+// A wide wave's tile in units of 16 rows and 16 signs: 128 and 120 registers of
+// sums (kGrad of 1 x 8 484 us where 2 x 5 takes 453)
 constexpr int row_tiles(int epi) { return epi == kProj ? 1 : 2; }
-constexpr int sign_tiles(int epi) { return epi == kProj ? 8 : 6; }
+constexpr int sign_tiles(int epi) { return epi == kProj ? 8 : 5; }
 struct Prod {
   Digits a;                   // T rows, K columns
   const uint32_t* bits;       // N x K signs
@@ -448,7 +456,11 @@ template <int EPI, int D>
 __global__ __launch_bounds__(256, 2) void wide_kernel(Prod a0, Prod a1) {
   constexpr int ND = digits(EPI), MI = row_tiles(EPI), NJ = sign_tiles(EPI);
   constexpr int kBlock = ND * kDigit, kRows = 32 * MI, kSigns = 32 * NJ;
-  __shared__ uint32_t lds[2][kSigns][16];   // signs of 512 columns
+  // a wave's own 16 NJ rows of signs of 512 columns, two of these: no wave waits
+  // for another. Four rows are 65 words apart, so that 16 rows' words 4 g lie in
+  // distinct banks.
+  constexpr int kFour = 65;
+  __shared__ uint32_t lds[4][2][4 * NJ][kFour];
   const Prod& a = blockIdx.z ? a1 : a0;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -462,37 +474,46 @@ __global__ __launch_bounds__(256, 2) void wide_kernel(Prod a0, Prod a1) {
   const int64_t tm = tile / ntn, tn = tile - tm * ntn;
   const int64_t nkb = blocks(a.K), nw = (a.K + 31) / 32;
   const int64_t kb0 = z * a.kbs, kb1 = lmin(nkb, kb0 + a.kbs);
-  // signs of the tile: rows past N are clamped (dropped at the end), words
-  // past a row's last read what follows, or nothing past the last row's (the
-  // descriptor's range, which counts the vector offset alone): they meet zero
-  // digits
-  const int64_t rows = lmin(kSigns, a.N - tn * kSigns);
-  const __amdgpu_buffer_rsrc_t br = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(a.bits + tn * kSigns * a.ldb), (short)0, (int)(((rows - 1) * a.ldb + nw) * 4),
-      0x00020000);
-  // a copy takes 4 rows x 16 words; row r keeps words 4 q .. 4 q + 3 in slot
-  // q ^ ((r >> 2) & 3)
-  auto signs = [&](int64_t sb) {
-    uint32_t* st = &lds[sb & 1][0][0];
-#pragma unroll
-    for (int c = 0; c < kSigns / 16; ++c) {
-      const int r0 = (wave * (kSigns / 16) + c) * 4, r = r0 + (lane >> 4);
-      const int w = ((((lane >> 2) & 3) ^ ((r >> 2) & 3)) << 2) | (lane & 3);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          br, (lds_ptr_t)(st + r0 * 16), 4, (int)((lmin(r, rows - 1) * a.ldb + sb * 16 + w) * 4), 0,
-          0, 0);
-    }
+  // signs of the wave: rows past N are past the descriptor's range (which counts
+  // the vector offset alone) and read as zero; words past a row's last read what
+  // follows, or nothing past the last row's: they meet zero digits
+  const int64_t n0 = tn * kSigns + wn * 16 * NJ, rows = lmin(16 * NJ, a.N - n0);
+  const uint64_t at0 = (uint64_t)(uintptr_t)(a.bits + n0 * a.ldb);
+  const int lo = scalar((int)at0), hi = scalar((int)(at0 >> 32) & 0xffff);
+  const int size = scalar(rows > 0 ? (int)(((rows - 1) * a.ldb + nw) * 4) : 0);
+  const int to = scalar((int)(uint32_t)(uintptr_t)(lds_ptr_t)&lds[wave][0][0][0]);
+  const uint32_t from = (uint32_t)((lane >> 4) * a.ldb * 4) + (lane & 15) * 4;
+  const uint32_t four = (uint32_t)(16 * a.ldb);   // bytes of four rows
+  // Copy c, 4 rows x 16 words, of the signs of 512 columns sb (!live: of zeros,
+  // which reads nothing). Written out: after a builtin's the compiler waits for
+  // all loads at the next use of one. It writes no register and keeps its place
+  // among the loads of digits and the waits.
+  auto copy = [&](int64_t sb, int c, bool live) {
+    const int st = to + (int)(sb & 1) * 16 * NJ * kFour;
+    asm volatile(
+        "s_mov_b32 s92, %0\n\t"
+        "s_mov_b32 s93, %1\n\t"
+        "s_mov_b32 s94, %2\n\t"
+        "s_mov_b32 s95, 0x20000\n\t"
+        "s_add_u32 m0, %3, %4\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dword %5, s[92:95], 0 offen lds"
+        :
+        : "s"(lo), "s"(hi), "s"(live ? size : 0), "s"(st), "i"(c * kFour * 4),
+          "v"(from + ((uint32_t)sb * 64 + c * four))
+        : "s92", "s93", "s94", "s95", "scc");
   };
   // the wave's digits: MI rows of blocks, nkb blocks apart (rows past T hold no
   // digits of the call: whatever they give is dropped at the end)
-  const uint8_t* dp = a.a.planes + (tm * 2 + wm) * MI * nkb * kBlock + lane * 16;
+  const uint8_t* dp = a.a.planes + (tm * 2 + wm) * MI * nkb * kBlock;
   i32x4 fr[2][MI][ND];
   auto digits_of = [&](int64_t kb, int s) {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int p = 0; p < ND; ++p)
-        fr[s][i][p] = *(const i32x4*)(dp + (i * nkb + kb) * kBlock + p * kDigit + s * 1024);
+        fr[s][i][p] = *(const i32x4*)((dp + (i * nkb + kb) * kBlock + p * kDigit + s * 1024) +
+                                      (uint32_t)lane * 16);
   };
   i32x4 acc[ND][MI][NJ];
 #pragma unroll
@@ -501,33 +522,40 @@ __global__ __launch_bounds__(256, 2) void wide_kernel(Prod a0, Prod a1) {
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[p][i][j] = i32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int c = 0; c < 4 * NJ; ++c) copy(kb0 >> 2, c, true);
+  __builtin_amdgcn_sched_barrier(0);
   digits_of(kb0, 0);
+  __builtin_amdgcn_sched_barrier(0);   // (in the order of the loop's, which the waits count)
   digits_of(kb0, 1);
-  signs(kb0 >> 2);
-  const int at = (wn * 16 * NJ + li) * 16 + ((g ^ (li >> 2)) << 2);
-  for (int64_t kb = kb0; kb < kb1; ++kb) {
-    if ((kb & 3) == 0) {
-      // the copies of this 512 have landed, everyone is done with the last
-      __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
-      asm volatile("s_barrier" ::: "memory");
-      if (kb + 4 < kb1) signs((kb >> 2) + 1);
-    }
-    const uint32_t* st = &lds[(kb >> 2) & 1][0][0] + at + (kb & 3);
-    uint32_t word[NJ];
+  __builtin_amdgcn_sched_barrier(0);
+  // word 4 g + q of row 16 j + li
+  const uint32_t* mine = &lds[wave][0][0][0] + (li >> 2) * kFour + (li & 3) * 16 + 4 * g;
+  // the copies issued before the last half step's digits have landed
+  auto landed = [&]() { asm volatile("s_waitcnt vmcnt(%0)" ::"i"(MI * ND) : "memory"); };
+  uint32_t word[2][NJ];
+  auto words_of = [&](int64_t sb, int q) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) word[j] = st[j * 256];
-    const int64_t ahead = lmin(kb + 1, kb1 - 1);
+    for (int j = 0; j < NJ; ++j) word[q & 1][j] = mine[((int)(sb & 1) * NJ + j) * 4 * kFour + q];
+  };
+  landed();
+  words_of(kb0 >> 2, 0);
+  for (int64_t k0 = kb0; k0 < kb1; k0 += 4) {
+    const bool more = k0 + 4 < kb1;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      i32x4 b = spread(word[0], s);
+    for (int h = 0; h < 8; ++h) {
+      const int q = h >> 1, s = h & 1;
+      const int64_t ahead = lmin(k0 + q + 1, kb1 - 1);
+      i32x4 b = spread(word[q & 1][0], s);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const i32x4 nb = spread(word[j + 1 < NJ ? j + 1 : j], s);
+        const i32x4 nb = spread(word[q & 1][j + 1 < NJ ? j + 1 : j], s);
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
           for (int p = 0; p < ND; ++p)
-            acc[p][i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fr[s][i][p], b, acc[p][i][j], 0, 0, 0);
+            acc[p][i][j] =
+                __builtin_amdgcn_mfma_i32_16x16x64_i8(fr[s][i][p], b, acc[p][i][j], 0, 0, 0);
         // the next signs are spread between the products
 #pragma unroll
         for (int q = 0; q < MI * ND; ++q) {
@@ -535,12 +563,30 @@ __global__ __launch_bounds__(256, 2) void wide_kernel(Prod a0, Prod a1) {
           __builtin_amdgcn_sched_group_barrier(0x2, 2, 0);
         }
         b = nb;
+        if (j == 0) {
+          // (after this half step's wait for its digits, which counts what is
+          // younger)
+          __builtin_amdgcn_sched_barrier(0);
+          if (s) {
+            // the next block's words (after the last block, of what is there)
+            if (q == 3) landed();
+            words_of((k0 >> 2) + (q == 3), (q + 1) & 3);
+          }
+          if (h < 4) {
+            // a quarter of the next 512's copies (of zeros at the end)
+#pragma unroll
+            for (int c = h * NJ; c < (h + 1) * NJ; ++c) copy((k0 >> 2) + 1, c, more);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
       // (kept here: the next step's products must not move above these loads)
       digits_of(ahead, s);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
+  // the last copies must land before LDS is used again or given away
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   float cs[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) cs[j] = 0.0f;

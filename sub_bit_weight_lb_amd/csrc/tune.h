@@ -19,6 +19,15 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ int64_t lmin(int64_t a, int64_t b) { return a < b ? a : b; }
 __device__ __forceinline__ int64_t lmax(int64_t a, int64_t b) { return a > b ? a : b; }
 
+// A uniform value in a scalar register, for operands of inline assembly: read
+// from a vector register that the compiler cannot see through (it drops a
+// v_readfirstlane of what it knows to be uniform, and may then hand the assembly
+// a vector register).
+__device__ __forceinline__ int scalar(int x) {
+  asm("" : "+v"(x));
+  return __builtin_amdgcn_readfirstlane(x);
+}
+
 // One element of type D as the caller stores it, and its conversions; from()
 // rounds to nearest even.
 template <int D> struct Elem;

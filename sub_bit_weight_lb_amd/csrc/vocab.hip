@@ -136,14 +136,6 @@ __device__ __forceinline__ bool tile_of(uint32_t ntm, uint32_t ntn, int64_t& tm,
   return true;
 }
 
-// A uniform value in a scalar register, for the copies below: read from a vector
-// register that the compiler cannot see through (it drops a v_readfirstlane of
-// what it knows to be uniform, and may then hand them a vector register).
-__device__ __forceinline__ int scalar(int x) {
-  asm("" : "+v"(x));
-  return __builtin_amdgcn_readfirstlane(x);
-}
-
 // One operand's tile: R rows (k-contiguous) or columns (k-major) of 64 k, R *
 // 128 bytes per stage, brought from memory to LDS by NC copies of 1 KB per
 // wave.
@@ -548,14 +540,11 @@ __device__ __forceinline__ int term_b(int s) { return (0x844 >> (2 * s)) & 3; } 
 // (64 registers or fewer: two workgroups of 1024 threads per CU)
 template <int D, int NT, bool VEC>
 __global__ __launch_bounds__(1024 / NT)
-    __attribute__((amdgpu_waves_per_eu(D != kF32 && VEC && NT == 1 ? 8 : 1))) void score_kernel(const typename Elem<D>::type* __restrict__ H,
-                                                    int64_t ldh,
-                                                    const typename Elem<D>::type* __restrict__ W,
-                                                    int64_t ldw, int64_t T, int64_t V, int64_t d,
-                                                    const int32_t* __restrict__ labels,
-                                                    float scale, float* __restrict__ top,
-                                                    float* __restrict__ sum,
-                                                    float* __restrict__ hit) {
+    __attribute__((amdgpu_waves_per_eu(D != kF32 && VEC && NT == 1 ? 8 : 1))) void score_kernel(
+        const typename Elem<D>::type* __restrict__ H, int64_t ldh,
+        const typename Elem<D>::type* __restrict__ W, int64_t ldw, int64_t T, int64_t V, int64_t d,
+        const int32_t* __restrict__ labels, float scale, float* __restrict__ top,
+        float* __restrict__ sum, float* __restrict__ hit) {
   constexpr int NW = 16 / NT;
   __shared__ f32x4 red[NW][4 * NT][64];
   __shared__ float st[2][4][16 * NT];
