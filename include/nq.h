@@ -401,13 +401,14 @@ nq_status nq_act8_steps(const uint8_t* exps, int64_t lde, int64_t rows, int64_t 
  * words): U_bits m x ldu, Ut_bits r x ldut (its transpose), V_bits n x ldv,
  * Vt_bits r x ldvt, each as nq_lbadmm_run and nq_transpose_signs write them.
  * ds1, ds2 float32, written (not added to). T == 0 writes zeros there.
- * The left factors of the products are taken in fixed point, 24 bits of each
- * row's largest value, and summed exactly; a row of X or dY with a NaN or an
+ * The left factors of the products are taken in fixed point (s2 x and s1 dY in
+ * 32 bits of each row's largest value, p and S_U^T (s1 dY) in 24) and summed
+ * exactly; a row of X or dY with a NaN or an
  * infinity gives NaN. Results do not depend on any order of summing but that
  * of ds1 and ds2 over tokens, which is fixed. All on `stream`, no allocation;
  * work: nq_binary_matmul_backward_work_bytes(T, m, n, r) bytes of device
- * scratch, 16-byte aligned. m, n, r in 1 .. 2^21, the signs' row strides at most
- * 2^20 words. */
+ * scratch, 16-byte aligned. m, n, r in 1 .. 2^21, T <= 2^24, T m, T n and T r at
+ * most 2^36, the signs' row strides at most 2^20 words. */
 nq_status nq_binary_matmul_backward(const uint32_t* U_bits, int64_t ldu, const uint32_t* Ut_bits,
                                     int64_t ldut, const uint32_t* V_bits, int64_t ldv,
                                     const uint32_t* Vt_bits, int64_t ldvt, int64_t m, int64_t n,
@@ -432,7 +433,8 @@ int64_t nq_binary_matmul_backward_work_bytes(int64_t T, int64_t m, int64_t n, in
  * a row of H gives NaN in its loss, in W in every loss it takes part in.
  * work: nq_vocab_loss_work_bytes(T, V, d, dtype, 0) bytes of device scratch,
  * 16-byte aligned. All on `stream`, no allocation; sums run in a fixed order.
- * T == 0 is a no-op. T <= 2^20, V <= 2^24, d <= 2^18, strides <= 2^21. */
+ * T == 0 is a no-op. T <= 2^20, V <= 2^24, T V <= 2^38, d <= 2^18, strides <=
+ * 2^21. */
 nq_status nq_vocab_loss(const void* H, int64_t ldh, const void* W, int64_t ldw, int32_t dtype,
                         int64_t T, int64_t V, int64_t d, const int32_t* labels, float scale,
                         float* loss, float* lse, void* work, void* stream);

@@ -16,6 +16,8 @@ namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 21;    // layer sizes
 constexpr int64_t kMaxRows = int64_t(1) << 31;   // tokens
+// of a layer's gradient: every launch stays below 2^32 threads
+constexpr int64_t kMaxTuned = int64_t(1) << 24, kMaxValues = int64_t(1) << 36;
 constexpr int64_t kMaxWords = int64_t(1) << 20;  // of a row of signs: 256 rows stay below 2^31 bytes
 
 bool dtype_ok(int32_t t) { return t == NQ_F32 || t == NQ_BF16 || t == NQ_F16; }
@@ -34,9 +36,10 @@ nq_status check_act8(const int8_t* codes, int64_t ldc, const uint8_t* exps, int6
 }
 
 // limits of the loss: byte offsets inside a 256-row tile of any operand stay
-// below 2^31
+// below 2^31, and a launch of one tile per 256 x 256 logits below 2^32 threads
 constexpr int64_t kMaxTokens = int64_t(1) << 20, kMaxVocab = int64_t(1) << 24;
 constexpr int64_t kMaxHidden = int64_t(1) << 18, kMaxLd = int64_t(1) << 21;
+constexpr int64_t kMaxLogits = int64_t(1) << 38;
 
 nq_status check_vocab(const void* H, int64_t ldh, const void* W, int64_t ldw, int32_t dtype,
                       int64_t T, int64_t V, int64_t d, const int32_t* labels, float scale,
@@ -45,6 +48,7 @@ nq_status check_vocab(const void* H, int64_t ldh, const void* W, int64_t ldw, in
   if (T < 0 || T > kMaxTokens) return bad("T must be in [0, 2^20]");
   if (V < 1 || V > kMaxVocab) return bad("V must be in [1, 2^24]");
   if (d < 1 || d > kMaxHidden) return bad("d must be in [1, 2^18]");
+  if (T * V > kMaxLogits) return bad("T V must be <= 2^38");
   if (!std::isfinite(scale)) return bad("scale must be finite");
   if (T == 0) return NQ_OK;
   if (!H || !W || !labels || !work) return bad("H, W, labels and work are required");
@@ -106,8 +110,8 @@ nq_status nq_act8_steps(const uint8_t* exps, int64_t lde, int64_t rows, int64_t 
 }
 
 int64_t nq_binary_matmul_backward_work_bytes(int64_t T, int64_t m, int64_t n, int64_t r) {
-  if (T < 0 || m < 0 || n < 0 || r < 0 || T > kMaxRows || m > kMaxDim || n > kMaxDim ||
-      r > kMaxDim)
+  if (T < 0 || m < 0 || n < 0 || r < 0 || T > kMaxTuned || m > kMaxDim || n > kMaxDim ||
+      r > kMaxDim || T * std::max(std::max(m, n), r) > kMaxValues)
     return -1;
   return T == 0 || m == 0 || n == 0 || r == 0 ? 0 : binback_work_bytes(m, n, r, T);
 }
@@ -123,7 +127,9 @@ nq_status nq_binary_matmul_backward(const uint32_t* U_bits, int64_t ldu, const u
   if (!dtype_ok(dtype)) return bad("dtype must be NQ_F32, NQ_BF16 or NQ_F16");
   if (m < 1 || n < 1 || r < 1 || m > kMaxDim || n > kMaxDim || r > kMaxDim)
     return bad("m, n and r must be in [1, 2^21]");
-  if (T < 0 || T > kMaxRows) return bad("T must be in [0, 2^31]");
+  if (T < 0 || T > kMaxTuned) return bad("T must be in [0, 2^24]");
+  if (T * std::max(std::max(m, n), r) > kMaxValues)
+    return bad("T m, T n and T r must be <= 2^36");
   if (!ds1 || !ds2) return bad("ds1 and ds2 are required");
   hipStream_t s = (hipStream_t)stream;
   if (T == 0) {   // no tokens: the sums over them are zero
@@ -160,7 +166,7 @@ nq_status nq_binary_matmul_backward(const uint32_t* U_bits, int64_t ldu, const u
 
 int64_t nq_vocab_loss_work_bytes(int64_t T, int64_t V, int64_t d, int32_t dtype, int32_t grad) {
   if (!dtype_ok(dtype) || T < 0 || V < 1 || d < 1 || T > kMaxTokens || V > kMaxVocab ||
-      d > kMaxHidden)
+      d > kMaxHidden || T * V > kMaxLogits)
     return -1;
   return T == 0 ? 0 : vocab_work_bytes(T, V, d, dtype, grad != 0);
 }

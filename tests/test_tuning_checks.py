@@ -225,6 +225,16 @@ def test_backward_workspace(lib):
     assert f(1, 4096, 4096, 2048) < f(64, 4096, 4096, 2048) < f(8192, 4096, 4096, 2048) < 1 << 30
 
 
+def test_backward_refuses_more_values_than_a_launch_covers(lib):
+    f = lib.nq_binary_matmul_backward_work_bytes
+    for T, m, n, r in [((1 << 24) + 1, 1, 1, 1), (1 << 20, 65537, 8, 8), (1 << 20, 8, 65537, 8),
+                       (1 << 20, 8, 8, 65537)]:
+        assert f(T, m, n, r) == -1
+        assert backward(lib, T=T, m=m, n=n, r=r, ldu=4096, ldut=4096, ldv=4096, ldvt=4096,
+                        ldc=n, lde=4096, lddy=m, lddx=n) == L.NQ_ERR_INVALID_ARG
+    assert f(1 << 20, 65536, 4096, 512) > 0
+
+
 def vloss(lib, **k):
     a = dict(H=PTR, ldh=20, W=PTR, ldw=20, dtype=0, T=3, V=50, d=20, labels=PTR, scale=1.0,
              loss=PTR, lse=PTR, work=PTR)
@@ -268,6 +278,14 @@ def test_vocab_workspace(lib):
     for dt in (0, 1, 2):
         for grad in (0, 1):
             assert f(300, 5000, 515, dt, grad) > 0
+
+
+def test_loss_refuses_more_logits_than_a_launch_covers(lib):
+    for call in (vloss, vback):
+        assert call(lib, T=1 << 20, V=(1 << 18) + 1) == L.NQ_ERR_INVALID_ARG
+    for grad in (0, 1):
+        assert lib.nq_vocab_loss_work_bytes(1 << 20, (1 << 18) + 1, 8, 1, grad) == -1
+        assert lib.nq_vocab_loss_work_bytes(1 << 20, 1 << 18, 8, 1, grad) > 0
 
 
 def test_ste_step_from_a_checkpoint_status(lib):
