@@ -191,14 +191,14 @@ __global__ __launch_bounds__(256) void act8_steps_kernel(const uint8_t* __restri
 }
 
 // The thread layout for rows of `units` threads' work: tx = 2^txs threads along
-// a row, 8 at least (a group's exponent) and 256 at most, and a grid of about
-// 65536 workgroups that walk the rows (8192 measured a fifth slower).
+// a row, 256 at most and 2^least at least, and a grid of about 65536 workgroups
+// that walk the rows (8192 measured a fifth slower).
 struct Shape {
   dim3 grid;
   int txs;
 };
-Shape shape_for(int64_t rows, int64_t units) {
-  int txs = 3;
+Shape shape_for(int64_t rows, int64_t units, int least) {
+  int txs = least;
   while (txs < 8 && (int64_t(1) << txs) < units) ++txs;
   const int64_t gx = (units + (int64_t(1) << txs) - 1) >> txs;
   const int64_t ty = 256 >> txs;
@@ -213,7 +213,8 @@ bool far(int64_t rows, int64_t cols, int dtype) {
 template <int D, bool FAR>
 void quantize(const void* X, int64_t rows, int64_t cols, int64_t ldx, int8_t* codes, int64_t ldc,
               uint8_t* exps, int64_t lde, hipStream_t s) {
-  const Shape p = shape_for(rows, (cols + cols_in(D) - 1) / cols_in(D));
+  // (the threads of a group lie side by side in one row: two, or eight)
+  const Shape p = shape_for(rows, (cols + cols_in(D) - 1) / cols_in(D), D == kF32 ? 3 : 1);
   hipLaunchKernelGGL((act8_quantize_kernel<D, FAR>), p.grid, dim3(256), 0, s,
                      (const typename Elem<D>::type*)X, rows, cols, ldx, codes, ldc, exps, lde,
                      p.txs);
@@ -221,7 +222,7 @@ void quantize(const void* X, int64_t rows, int64_t cols, int64_t ldx, int8_t* co
 
 template <int D, bool FAR>
 void dequantize(const Act8& q, int64_t rows, int64_t cols, void* X, int64_t ldx, hipStream_t s) {
-  const Shape p = shape_for(rows, (cols + cols_out(D) - 1) / cols_out(D));
+  const Shape p = shape_for(rows, (cols + cols_out(D) - 1) / cols_out(D), 0);
   hipLaunchKernelGGL((act8_dequantize_kernel<D, FAR>), p.grid, dim3(256), 0, s, q.codes, q.ldc,
                      q.exps, q.lde, rows, cols, (typename Elem<D>::type*)X, ldx, p.txs);
 }
@@ -254,7 +255,7 @@ hipError_t launch_act8_dequantize(const Act8& q, int64_t rows, int64_t cols, voi
 hipError_t launch_act8_steps(const uint8_t* exps, int64_t lde, int64_t rows, int64_t groups,
                              float* steps, int64_t lds, hipStream_t s) {
   if (rows <= 0 || groups <= 0) return hipSuccess;
-  const Shape p = shape_for(rows, (groups + 3) / 4);
+  const Shape p = shape_for(rows, (groups + 3) / 4, 0);
   hipLaunchKernelGGL(act8_steps_kernel, p.grid, dim3(256), 0, s, exps, lde, rows, groups, steps,
                      lds, p.txs);
   return hipGetLastError();
