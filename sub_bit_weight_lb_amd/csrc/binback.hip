@@ -68,7 +68,7 @@ typedef __attribute__((address_space(3))) uint32_t* lds_ptr_t;
 constexpr int kDigit = 2048;      // bytes of a digit per 16 rows and 128 columns
 constexpr int kThinMax = 64;      // rows of a thin launch
 constexpr int kThinWaves = 8;
-constexpr int kMaxSplit = 8;      // slices of the columns (wide, few tiles)
+constexpr int kMaxSplit = 8;      // slices of the columns (few tiles)
 // Up to this many rows, a workgroup per row, else eight rows per workgroup
 // (whole calls in us, rank 1024: 200 rows of a 4096 x 4096 layer 56 v 77, 512
 // rows of 11008 x 4096 117 v 139, 1000 rows of 4096 x 4096 119 v 112).
@@ -618,15 +618,17 @@ __global__ __launch_bounds__(64 * kThinWaves) void thin_kernel(Prod a0, Prod a1)
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, li = lane & 15;
   const int64_t n0 = (int64_t)blockIdx.x * 16;
-  if (n0 >= a.N) return;
+  const int z = blockIdx.z;
+  if (n0 >= a.N || z >= a.split) return;
   const int64_t nkb = blocks(a.K), nw = (a.K + 31) / 32;
+  const int64_t kb1 = lmin(nkb, (z + 1) * a.kbs);
   const uint32_t* bp = a.bits + lmin(n0 + li, a.N - 1) * a.ldb;
   i32x4 acc[ND][MT][1];
 #pragma unroll
   for (int p = 0; p < ND; ++p)
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[p][i][0] = i32x4{0, 0, 0, 0};
-  for (int64_t kb = wave; kb < nkb; kb += kThinWaves) {
+  for (int64_t kb = z * a.kbs + wave; kb < kb1; kb += kThinWaves) {
     const uint32_t w = bp[lmin((kb >> 2) * 16 + 4 * g + (kb & 3), nw - 1)];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -657,7 +659,7 @@ __global__ __launch_bounds__(64 * kThinWaves) void thin_kernel(Prod a0, Prod a1)
   }
   if (wave) return;
   float cs[1] = {0.0f};
-  finish<EPI, D, MT, 1>(a, 0, n0, g, li, 0, acc, cs);
+  finish<EPI, D, MT, 1>(a, 0, n0, g, li, z, acc, cs);
   if (EPI == kProj) return;
   cs[0] += __shfl_xor(cs[0], 16);
   cs[0] += __shfl_xor(cs[0], 32);
@@ -699,16 +701,15 @@ struct Work {
   int64_t bytes;
 };
 // Slices of the columns of a chain's first product: enough tiles for two
-// workgroups on each of the 256 CUs (the two chains run together), at least
-// 512 columns each.
+// workgroups on each of the 256 CUs (one of a thin launch, which has eight
+// waves; the two chains run together), at least 512 columns each.
 constexpr int64_t tiles_of(int epi, int64_t T, int64_t N) {
   const int64_t rows = 32 * row_tiles(epi), signs = 32 * sign_tiles(epi);
   return ((T + rows - 1) / rows) * ((N + signs - 1) / signs);
 }
 int proj_split(int64_t T, int64_t r, int64_t K) {
-  if (T <= kThinMax) return 1;
-  const int64_t tiles = 2 * tiles_of(kProj, T, r);
-  return (int)std::max<int64_t>(1, std::min({(int64_t)kMaxSplit, 512 / tiles, blocks(K) / 4}));
+  const int64_t most = T <= kThinMax ? 256 / (2 * ((r + 15) / 16)) : 512 / (2 * tiles_of(kProj, T, r));
+  return (int)std::max<int64_t>(1, std::min({(int64_t)kMaxSplit, most, blocks(K) / 4}));
 }
 // rows per partial column sum
 constexpr int64_t kSumRows = 32 * row_tiles(kGrad);
@@ -749,7 +750,8 @@ template <int EPI, int D>
 hipError_t products(const Prod& a, const Prod& b, hipStream_t s) {
   const int64_t N = std::max(a.N, b.N);
   if (a.T <= kThinMax) {
-    const dim3 grid((unsigned)((N + 15) / 16), 2), block(64 * kThinWaves);
+    const dim3 grid((unsigned)((N + 15) / 16), 2, (unsigned)std::max(a.split, b.split));
+    const dim3 block(64 * kThinWaves);
     if (a.T <= 16)
       hipLaunchKernelGGL((thin_kernel<EPI, D, 1>), grid, block, 0, s, a, b);
     else if (a.T <= 32)
