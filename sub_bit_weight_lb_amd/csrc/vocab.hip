@@ -50,13 +50,14 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4* lds_tr_t;
 
 constexpr int BK = 64;            // k per stage
-// Tokens of score_kernel. Above, mma_kernel reads W at a higher rate although
-// half of a tile is empty (4096 x 32000 bf16, 64 tokens: 94 us, score_kernel
-// 104; 32 tokens: 72 in score_kernel), but fp32 would be copied for it (2048 x
-// 32000, 64 tokens: 309 us, score_kernel 90).
-constexpr int score_max(int dtype) { return dtype == kF32 ? 64 : 32; }
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kTop16 = 32768.0f;   // what fp16 terms are scaled to
+
+// Whether score_kernel takes a call. With more tokens mma_kernel reads W at a
+// higher rate although half of a tile is empty (4096 x 32000 bf16, 64 tokens: 94
+// us, score_kernel 104; 32 tokens: 72 in score_kernel), but fp32 would be copied
+// for it (2048 x 32000, 64 tokens: 309 us, score_kernel 90).
+bool few(int64_t T, int64_t d, int dtype) { return d >= 8 && T <= (dtype == kF32 ? 64 : 32); }
 
 // one 16 x 16 x 32 product of 16-bit operands
 template <bool F16>
@@ -483,25 +484,14 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
 // many waves with one load per row each keep HBM busiest (4096 x 32000 bf16, 16
 // tokens, in us with the join: 16 waves 59 (4.4 TB/s), 8 waves 63, 4 waves 96;
 // 8 waves of 64 columns 71, 4 waves of 128 columns 80, of two such runs in
-// registers 84). Rows are 16-byte aligned and d % 8 == 0 (VEC), or elements are
-// loaded one by one.
+// registers 84). Eight values are loaded together from any address (rows that are
+// not 16-byte aligned: 3 tokens, 6673 x 68774 fp16 350 us, one by one 727). At the
+// end of a row the last eight are loaded, and of H those that came before are
+// zeroed (d >= 8).
 template <int D>
-struct Raw8 {
+struct __attribute__((packed)) Raw8 {
   typename Elem<D>::type e[8];
 };
-template <int D, bool VEC>
-__device__ __forceinline__ Raw8<D> load8(const typename Elem<D>::type* row, int64_t k, int64_t d) {
-  typedef typename Elem<D>::type E;
-  Raw8<D> r;
-  if constexpr (VEC) {
-    __builtin_memcpy(r.e, __builtin_assume_aligned(row + lmin(k, d - 8), 16), sizeof(r.e));
-    if (k >= d) __builtin_memset(r.e, 0, sizeof(r.e));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r.e[i] = k + i < d ? row[k + i] : (E)0;
-  }
-  return r;
-}
 // x = h + m + l in bf16, exact; not finite: the first term alone
 __device__ __forceinline__ void split3(float x, uint16_t (&t)[3]) {
   t[0] = Elem<kBF16>::from(x);
@@ -528,7 +518,7 @@ __device__ __forceinline__ Frag<D> frag_of(const Raw8<D>& r) {
       for (int i = 0; i < 4; ++i)
         f.t[p][i] = (uint32_t)q[2 * i][p] | (uint32_t)q[2 * i + 1][p] << 16;
   } else {
-    __builtin_memcpy(&f.t[0], r.e, 16);
+    __builtin_memcpy(&f.t[0], &r, 16);
   }
   return f;
 }
@@ -537,9 +527,9 @@ __device__ __forceinline__ int term_a(int s) { return (0x250 >> (2 * s)) & 3; } 
 __device__ __forceinline__ int term_b(int s) { return (0x844 >> (2 * s)) & 3; }   // 0 1 0 1 0 2
 
 // (64 registers or fewer: two workgroups of 1024 threads per CU)
-template <int D, int NT, bool VEC>
+template <int D, int NT>
 __global__ __launch_bounds__(1024 / NT)
-    __attribute__((amdgpu_waves_per_eu(D != kF32 && VEC && NT == 1 ? 8 : 1))) void score_kernel(
+    __attribute__((amdgpu_waves_per_eu(D != kF32 && NT == 1 ? 8 : 1))) void score_kernel(
         const typename Elem<D>::type* __restrict__ H, int64_t ldh,
         const typename Elem<D>::type* __restrict__ W, int64_t ldw, int64_t T, int64_t V, int64_t d,
         const int32_t* __restrict__ labels, float scale, float* __restrict__ top,
@@ -550,23 +540,36 @@ __global__ __launch_bounds__(1024 / NT)
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, li = lane & 15;
   const int64_t v0 = (int64_t)blockIdx.x * 64;
-  const typename Elem<D>::type *wr[4], *hr[NT];
+  // byte offsets of the rows (64 rows of 2^21 values at most: 32 bits)
+  constexpr int kSize = sizeof(typename Elem<D>::type);
+  const char *Wb = (const char*)(W + v0 * ldw), *Hb = (const char*)H;
+  uint32_t wr[4], hr[NT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) wr[i] = W + lmin(v0 + 16 * i + li, V - 1) * ldw;
+  for (int i = 0; i < 4; ++i)
+    wr[i] = (uint32_t)lmin(16 * i + li, V - 1 - v0) * (uint32_t)(ldw * kSize);
 #pragma unroll
-  for (int j = 0; j < NT; ++j) hr[j] = H + lmin(16 * j + li, T - 1) * ldh;
+  for (int j = 0; j < NT; ++j) hr[j] = (uint32_t)lmin(16 * j + li, T - 1) * (uint32_t)(ldh * kSize);
   f32x4 acc[4][NT];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t k0 = wave * 32; k0 < d; k0 += 32 * NW) {
+  for (int k0 = wave * 32; k0 < d; k0 += 32 * NW) {
+    const int k = min(k0 + 8 * g, (int)d - 8);
+    const uint32_t at = k * kSize;
     Raw8<D> w[4], h[NT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = load8<D, VEC>(wr[i], k0 + 8 * g, d);
+    for (int i = 0; i < 4; ++i) __builtin_memcpy(&w[i], Wb + (wr[i] + at), sizeof(w[i]));
 #pragma unroll
-    for (int j = 0; j < NT; ++j) h[j] = load8<D, VEC>(hr[j], k0 + 8 * g, d);
+    for (int j = 0; j < NT; ++j) __builtin_memcpy(&h[j], Hb + (hr[j] + at), sizeof(h[j]));
     __builtin_amdgcn_sched_barrier(0);   // (all loads before the first product)
+    if (k0 + 32 > d) {
+      const int before = k0 + 8 * g - k;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[j].e[i] = i < before ? (typename Elem<D>::type)0 : h[j].e[i];
+    }
     Frag<D> b[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) b[j] = frag_of<D>(h[j]);
@@ -592,7 +595,7 @@ __global__ __launch_bounds__(1024 / NT)
     if (wave >= 4) break;
     const int e = wave * NT + j;
     f32x4 z = red[0][e][lane];
-#pragma unroll
+#pragma unroll 4
     for (int n = 1; n < NW; ++n) z += red[n][e][lane];
     const int64_t t = 16 * j + li, w = v0 + 16 * wave + 4 * g;
     const int32_t label = t < T ? labels[t] : -1;
@@ -881,7 +884,7 @@ Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad) {
     p.top = take(4 * np * T);
     p.sum = take(4 * np * T);
     p.hit = take(4 * T);
-    if (T <= score_max(dtype)) {
+    if (few(T, d, dtype)) {
       p.bytes = off;
       return p;
     }
@@ -974,17 +977,9 @@ template <int D, int NT>
 void score(const Vocab& a, const Plan& p, hipStream_t s) {
   typedef typename Elem<D>::type E;
   char* w = (char*)a.work;
-  const bool vec = a.d % 8 == 0 && a.ldh * sizeof(E) % 16 == 0 && a.ldw * sizeof(E) % 16 == 0 &&
-                   ((uintptr_t)a.H | (uintptr_t)a.W) % 16 == 0;
-  const dim3 grid((unsigned)((a.V + 63) / 64));
-  if (vec)
-    hipLaunchKernelGGL((score_kernel<D, NT, true>), grid, dim3(1024 / NT), 0, s, (const E*)a.H, a.ldh,
-                       (const E*)a.W, a.ldw, a.T, a.V, a.d, a.labels, a.scale,
-                       (float*)(w + p.top), (float*)(w + p.sum), (float*)(w + p.hit));
-  else
-    hipLaunchKernelGGL((score_kernel<D, NT, false>), grid, dim3(1024 / NT), 0, s, (const E*)a.H, a.ldh,
-                       (const E*)a.W, a.ldw, a.T, a.V, a.d, a.labels, a.scale,
-                       (float*)(w + p.top), (float*)(w + p.sum), (float*)(w + p.hit));
+  hipLaunchKernelGGL((score_kernel<D, NT>), dim3((unsigned)((a.V + 63) / 64)), dim3(1024 / NT), 0, s,
+                     (const E*)a.H, a.ldh, (const E*)a.W, a.ldw, a.T, a.V, a.d, a.labels, a.scale,
+                     (float*)(w + p.top), (float*)(w + p.sum), (float*)(w + p.hit));
 }
 
 template <int D>
@@ -993,7 +988,7 @@ hipError_t loss(const Vocab& a, hipStream_t s) {
   char* w = (char*)a.work;
   hipError_t e;
   int64_t np;   // partials per token
-  if (a.T <= score_max(D)) {
+  if (few(a.T, a.d, D)) {
     np = (a.V + 63) / 64;
     if (a.T <= 16) {
       score<D, 1>(a, p, s);
