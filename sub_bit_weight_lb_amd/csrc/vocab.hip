@@ -143,12 +143,17 @@ __device__ __forceinline__ bool tile_of(uint32_t ntm, uint32_t ntn, int64_t& tm,
 //   keeps k-octet q in slot q ^ ((r >> 1) & 7), so that the 16 lanes that read
 //   one octet of 16 consecutive rows hit distinct banks.
 //   k-major: LDS rows of R columns (2 R bytes, 32-byte chunks); row k keeps
-//   chunk c in place c ^ ((k & 3) + 4 ((k >> 3) & 1)), so that the eight rows
-//   that half a wave reads at once hit distinct banks.
+//   chunk c in place c ^ ((k & 3) + 4 ((k >> 3) & 1)), or for R = 64, where two
+//   rows fill the banks, c ^ (((k >> 1) & 1) + 2 ((k >> 3) & 1)), so that the
+//   eight rows that half a wave reads at once hit distinct banks.
 // A fragment is 16 rows or columns of 32 k: lane (li, g) holds row li, k 8 g ..
 // 8 g + 7. In the k-major form two transposing reads of 4 k each fill it: in
 // each 16 lanes, lane i addresses row i / 4, columns 4 (i % 4) .., and receives
 // column i.
+template <int R>
+__device__ __forceinline__ int place(int k) {
+  return R == 64 ? ((k >> 1) & 1) + 2 * ((k >> 3) & 1) : (k & 3) + 4 * ((k >> 3) & 1);
+}
 template <int R, int NC, bool MAJOR>
 struct Tile {
   static constexpr int kRowsPer = MAJOR ? 512 / R : 8;   // LDS rows per copy
@@ -173,7 +178,7 @@ struct Tile {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int k = k0 + first(c) * kRowsPer + lane * 16 / (2 * R), slot = lane * 16 % (2 * R) / 16;
-        const int chunk = (slot >> 1) ^ ((k & 3) + 4 * ((k >> 3) & 1));
+        const int chunk = (slot >> 1) ^ place<R>(k);
         off[c] = (uint32_t)(((int64_t)(lane * 16 / (2 * R)) * o.ld + 16 * chunk + 8 * (slot & 1)) * 2);
       }
     } else {
@@ -237,7 +242,7 @@ struct Reader {
 
   __device__ __forceinline__ void init(int g0, int g, int li) {
     if constexpr (MAJOR) {
-      const int f = (li >> 2) + 4 * (g & 1);
+      const int f = place<R>(8 * g + (li >> 2));
 #pragma unroll
       for (int j = 0; j < N; ++j)
         at[j] = (8 * g + (li >> 2)) * 2 * R + (((g0 + j) ^ f) << 5) + (li & 3) * 8;
@@ -843,13 +848,23 @@ struct Plan {
   // byte offsets
   int64_t hp, wp, top, sum, hit, wn, fac, amax, G, part, bytes;
 };
-// Tiles of 256 x 256 (one workgroup of four waves per CU) or of 128 x 128 (two
-// per CU, which lose about a fifth of the rate to twice the copies): whichever
-// needs less time in whole rounds over the 256 CUs.
+int64_t tiles_of(int64_t M, int64_t N, int64_t tile) {
+  return ((M + tile - 1) / tile) * ((N + tile - 1) / tile);
+}
+// Tiles of 256 x 256 (one workgroup of eight waves per CU) or of 128 x 128 (two
+// of four per CU, which lose about a fifth of the rate to twice the copies):
+// whichever needs less time in whole rounds over the 256 CUs (512 tokens, 32000
+// x 2048 bf16: the loss 66 us in big tiles, 90 in small ones; 300 tokens, 20000 x
+// 1024: 42 and 32).
 bool big_tiles(int64_t M, int64_t N, int64_t slices) {
-  const int64_t big = ((M + 255) / 256) * ((N + 255) / 256) * slices;
-  const int64_t small = ((M + 127) / 128) * ((N + 127) / 128) * slices;
+  const int64_t big = tiles_of(M, N, 256) * slices, small = tiles_of(M, N, 128) * slices;
   return (big + 255) / 256 * 4.0 <= (small + 255) / 256 * 1.25;
+}
+// Of 64 x 64 where 128 x 128 leave half of the CUs idle (loss and gradient in us:
+// 128 tokens, 8192 x 4096 bf16 34 and 102, else 48 and 118; 74 tokens, 1115 x 2368
+// fp32 74 and 105, else 97 and 128).
+int tile_for(int64_t M, int64_t N) {
+  return tiles_of(M, N, 128) <= 128 ? 64 : big_tiles(M, N, 1) ? 256 : 128;
 }
 // Slices of the contraction of dH: a workgroup for every CU, in big tiles where
 // those are enough for most of the CUs, 256 words at least.
@@ -880,7 +895,10 @@ Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad) {
     return at;
   };
   if (!grad) {
-    const int64_t np = (V + 63) / 64 + 4;
+    // partials per token: one per 64 words, or two per tile's words (W in place or
+    // in pieces)
+    const bool tiny = !few(T, d, dtype) && (tile_for(V, T) == 64 || tile_for(p.piece, T) == 64);
+    const int64_t np = (tiny ? 2 : 1) * ((V + 63) / 64) + 4;
     p.top = take(4 * np * T);
     p.sum = take(4 * np * T);
     p.hit = take(4 * T);
@@ -908,16 +926,19 @@ Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad) {
 // words of bf16: 8 stages of k 14 us with either, 16 stages 18 v 20, 32 stages
 // 27 v 32; 4 stages 19 v 15; 128 tokens, 32000 words, 64 stages: 52 v 80).
 template <int D, int EPI>
-hipError_t mma_launch(const Mma& a, bool big, int slices, hipStream_t s) {
-  const int64_t t = big ? 256 : 128;
-  const int64_t tiles = ((a.A.rows + t - 1) / t) * ((a.B.rows + t - 1) / t);
+hipError_t mma_launch(const Mma& a, int tile, int slices, hipStream_t s) {
+  const int64_t tiles = tiles_of(a.A.rows, a.B.rows, tile);
   const dim3 grid((unsigned)((tiles + 7) / 8 * 8), (unsigned)slices);
-  if (big)
+  if (tile == 256) {
     hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 4, 8, 4, 2>), grid, dim3(512), 0, s, a);
-  else if (tiles * slices <= 256 && std::min(a.K, a.k_slice) / BK * passes(D) >= 16)
+  } else if (tile == 64) {
+    if constexpr (EPI != kDh)
+      hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 2, 2, 2, 4>), grid, dim3(256), 0, s, a);
+  } else if (tiles * slices <= 256 && std::min(a.K, a.k_slice) / BK * passes(D) >= 16) {
     hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 2, 4, 4, 4>), grid, dim3(256), 0, s, a);
-  else
+  } else {
     hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 2, 4, 4, 2>), grid, dim3(256), 0, s, a);
+  }
   return hipGetLastError();
 }
 
@@ -1008,12 +1029,12 @@ hipError_t loss(const Vocab& a, hipStream_t s) {
     m.top = (float*)(w + p.top); m.sum = (float*)(w + p.sum); m.hit = (float*)(w + p.hit);
     // all words at once where W is used in place
     const int64_t piece = direct(a.W, a.ldw, a.d, D) ? a.V : p.piece;
-    const bool big = big_tiles(piece, a.T, 1);
-    np = big ? 2 * ((a.V + 255) / 256) : 2 * ((a.V + 127) / 128);
+    const int tile = tile_for(piece, a.T);
+    np = 2 * ((a.V + tile - 1) / tile);
     for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
       m.v0 = v0;
       if ((e = words<D>(a, p, v0, std::min(piece, a.V - v0), &m.A, s)) != hipSuccess) return e;
-      if ((e = mma_launch<D, kStat>(m, big, 1, s)) != hipSuccess) return e;
+      if ((e = mma_launch<D, kStat>(m, tile, 1, s)) != hipSuccess) return e;
     }
   }
   hipLaunchKernelGGL(stat_kernel, dim3((unsigned)((a.T + 15) / 16)), dim3(1024), 0, s,
@@ -1048,7 +1069,7 @@ hipError_t backward(const Vocab& a, hipStream_t s) {
     m.z0 = a.scale;
     m.v0 = v0; m.labels = a.labels; m.lse = a.lse; m.wn = (float*)(w + p.wn);
     m.G = G; m.gld = p.piece;
-    if ((e = mma_launch<D, kGrad>(m, big_tiles(nv, a.T, 1), 1, s)) != hipSuccess) return e;
+    if ((e = mma_launch<D, kGrad>(m, tile_for(nv, a.T), 1, s)) != hipSuccess) return e;
     // (G is zero for words past nv and tokens past T, to the tile's end)
     if (a.dH) {
       Mma h{};
@@ -1058,7 +1079,7 @@ hipError_t backward(const Vocab& a, hipStream_t s) {
       h.k_slice = kz;
       h.part = (float*)(w + p.part); h.slice = slice; h.ldo = ldp; h.add = v0 > 0;
       const int n = (int)((h.K + kz - 1) / kz);
-      if ((e = mma_launch<D, kDh>(h, big_tiles(a.d, a.T, nz), n, s)) != hipSuccess) return e;
+      if ((e = mma_launch<D, kDh>(h, big_tiles(a.d, a.T, nz) ? 256 : 128, n, s)) != hipSuccess) return e;
     }
     if (a.dW) {
       Mma x{};
@@ -1067,7 +1088,7 @@ hipError_t backward(const Vocab& a, hipStream_t s) {
       x.K = x.k_slice = round_up(a.T, BK);
       x.post = &fac->post_w;
       x.out = (E*)a.dW + v0 * a.lddw; x.ldo = a.lddw;
-      if ((e = mma_launch<D, kDw>(x, big_tiles(a.d, nv, 1), 1, s)) != hipSuccess) return e;
+      if ((e = mma_launch<D, kDw>(x, tile_for(a.d, nv), 1, s)) != hipSuccess) return e;
     }
   }
   if (a.dH) {

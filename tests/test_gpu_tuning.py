@@ -373,6 +373,20 @@ def test_loss_and_gradient_match_oracle(gpu, name, T, V, d):
 
 
 @pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("T, V, d", [(600, 4100, 200), (600, 4100, 1100), (1100, 12100, 1100),
+                                     (70, 4100, 2052), (2, 3, 4)])
+def test_loss_and_gradient_in_tiles_of_every_size(gpu, name, T, V, d):
+    """128 x 128 tiles with few and with many k, 256 x 256 tiles in every
+    product, 64 x 64 tiles with many k, fewer columns than a load takes."""
+    import sub_bit_weight_lb_amd as nq
+    print(f"case T={T} V={V} d={d} {name}", flush=True)
+    L = Head(T + V + d, T, V, d, name, gpu)
+    loss, lse = nq.vocab_loss(L.H, L.W, L.labels)
+    L.check_loss(loss, lse)
+    L.check_grad(*nq.vocab_loss_backward(L.H, L.W, L.labels, lse, L.dl))
+
+
+@pytest.mark.parametrize("name", TYPES)
 @pytest.mark.parametrize("T, d", [(15, 200), (16, 72), (31, 136), (32, 1000), (33, 129), (48, 64),
                                   (63, 40), (64, 515)])
 def test_loss_of_few_tokens(gpu, name, T, d):
