@@ -360,7 +360,9 @@ nq_status nq_ste_destroy(nq_ste_t h);
  * The digest's stage 3 (方法步骤详情) freezes the binary factors and tunes the
  * scales of the whole model against a loss on its outputs. What follows is
  * what one layer of that needs beside nq_binary_matmul: its input kept in 8
- * bits for the backward pass, and its gradient from there. */
+ * bits for the backward pass, and its gradient from there; and the loss over
+ * the model's vocabulary with its gradient. Outputs and work must not overlap
+ * the inputs or each other. */
 
 /* Element types of tensors that are not always float32. */
 typedef enum nq_dtype { NQ_F32 = 0, NQ_BF16 = 1, NQ_F16 = 2 } nq_dtype;

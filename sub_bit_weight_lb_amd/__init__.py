@@ -546,8 +546,9 @@ def binary_matmul_backward(U_bits, Ut_bits, V_bits, Vt_bits, s1, s2, X, dY, r, w
     (n x ceil(r/32)) as lbadmm_run returns them, Ut_bits (r x ceil(m/32)) and
     Vt_bits (r x ceil(n/32)) their transposes (transpose_signs). dX (T x n) has
     dY's type (None with want_dX=False); ds1 (m) and ds2 (n) are float32 sums
-    over the tokens. work, if given, holds
-    binary_matmul_backward_work_bytes(T, m, n, r) bytes, 16-byte aligned."""
+    over the tokens. Outputs must not share memory with inputs. work, if given,
+    holds binary_matmul_backward_work_bytes(T, m, n, r) bytes, 16-byte
+    aligned."""
     torch = _torch()
     f32, i32 = torch.float32, torch.int32
     T, n, ldc, lde = _act8(X, "X")
@@ -646,8 +647,8 @@ def vocab_loss_backward(H, W, labels, lse, dloss, scale=1.0, want_dH=True, want_
     its lse: returns (dH, dW) in H's type (None where not wanted). lse and
     dloss are T float32. The logits are computed again in pieces of the
     vocabulary. Ignored tokens (negative labels) get zero rows of dH and add
-    nothing to dW. work, if given, holds
-    vocab_loss_work_bytes(T, V, d, H.dtype, grad=True) bytes."""
+    nothing to dW. Outputs must not share memory with inputs. work, if given,
+    holds vocab_loss_work_bytes(T, V, d, H.dtype, grad=True) bytes."""
     torch = _torch()
     T, V, d, code, ldh, ldw = _vocab_args(H, W, labels)
     _vector(lse, "lse", T, torch.float32)
