@@ -702,24 +702,36 @@ __global__ __launch_bounds__(256) void amax_kernel(const float* __restrict__ H, 
   const float* X = w ? W : H;
   const int64_t rows = w ? V : T, ld = w ? ldw : ldh;
   float m = 0.0f;
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-    if (!w && labels[r] < 0) continue;
-    const float* x = X + r * ld;
-    // (16 bytes at a time, which may start at any element)
-    int64_t c = 4 * threadIdx.x;
-#pragma unroll 4
-    for (; c + 4 <= d; c += 1024) {
-      struct __attribute__((packed)) { float v[4]; } q;
-      __builtin_memcpy(&q, x + c, 16);
+  auto take = [&](float x, bool on) {
+    const float v = on ? fabsf(x) : 0.0f;
+    m = v < __builtin_inff() ? fmaxf(m, v) : m;
+  };
+  // four rows at a time, 16 bytes each, from any address; rows and columns past
+  // the end are clamped (a maximum may see a value twice), so that no branch
+  // parts the loads
+  for (int64_t r0 = blockIdx.x; r0 < rows; r0 += 4 * (int64_t)gridDim.x) {
+    const float* x[4];
+    bool on[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float v = fabsf(q.v[i]);
-        m = v < __builtin_inff() ? fmaxf(m, v) : m;
-      }
+    for (int u = 0; u < 4; ++u) {
+      const int64_t r = lmin(r0 + u * (int64_t)gridDim.x, rows - 1);
+      on[u] = w || labels[r] >= 0;
+      x[u] = X + r * ld;
     }
-    for (; c < d; ++c) {
-      const float v = fabsf(x[c]);
-      m = v < __builtin_inff() ? fmaxf(m, v) : m;
+    if (d < 4) {
+      for (int64_t c = threadIdx.x; c < d; c += 256)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) take(x[u][c], on[u]);
+      continue;
+    }
+    for (int64_t c = 4 * threadIdx.x; c < d; c += 1024) {
+      struct __attribute__((packed)) { float v[4]; } q[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) __builtin_memcpy(&q[u], x[u] + lmin(c, d - 4), 16);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) take(q[u].v[i], on[u]);
     }
   }
   sm[threadIdx.x] = m;
