@@ -883,15 +883,19 @@ bool big_tiles(int64_t M, int64_t N, int64_t slices) {
 int tile_for(int64_t M, int64_t N) {
   return tiles_of(M, N, 128) <= 128 ? 64 : big_tiles(M, N, 1) ? 256 : 128;
 }
-// Slices of the contraction of dH: a workgroup for every CU, in big tiles where
-// those are enough for most of the CUs, 256 words at least.
+// Slices of the contraction of dH: a workgroup for every CU (two in small
+// tiles), 256 words at least. Big tiles need more slices, each with its share of
+// fp32 sums to write and join: taken where they fill most CUs, have 1024 words
+// each and a clear lead in products per CU (1024 tokens, 32000 x 2048 fp32: 404
+// us in 8 slices of big tiles, 550 in 4 of small ones; 1500 tokens, 4000 x 1500
+// bf16, 571 words each: dH 106 us in big tiles, 91 in small ones; 600 tokens, 10000
+// x 3000 fp16, no lead: 154 and 129).
 int dh_slices(int64_t T, int64_t d, int64_t piece) {
-  const int64_t big = ((d + 255) / 256) * ((T + 255) / 256);
-  const int64_t small = ((d + 127) / 128) * ((T + 127) / 128);
-  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(piece / 256, 64));
+  const int64_t big = tiles_of(d, T, 256), most = std::max<int64_t>(1, std::min<int64_t>(piece / 256, 64));
   const int64_t nb = std::max<int64_t>(1, std::min(256 / big, most));
-  if (big * nb >= 192) return (int)nb;
-  return (int)std::max<int64_t>(1, std::min(512 / small, most));
+  const int64_t ns = std::max<int64_t>(1, std::min(512 / tiles_of(d, T, 128), most));
+  const bool lead = 4.0 / nb <= 0.85 * 2.5 / ns;
+  return (int)(big * nb >= 192 && piece / nb >= 1024 && lead ? nb : ns);
 }
 // Words per piece: G, and a copy of W's piece where one is needed, hold at most
 // 2^26 values each (two thousand words at least), which leaves the fp32 sums of

@@ -374,6 +374,7 @@ def test_loss_and_gradient_match_oracle(gpu, name, T, V, d):
 
 @pytest.mark.parametrize("name", TYPES)
 @pytest.mark.parametrize("T, V, d", [(600, 4100, 200), (600, 4100, 1100), (1100, 12100, 1100),
+                                     (700, 10300, 2000),
                                      (70, 4100, 2052), (2, 3, 4)])
 def test_loss_and_gradient_in_tiles_of_every_size(gpu, name, T, V, d):
     """128 x 128 tiles with few and with many k, 256 x 256 tiles in every
