@@ -386,6 +386,13 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
 
   // lane (g, li), element v of tile (i, j): row 16 i + 4 g + v, column 16 j + li
   const int64_t r0 = m0 + wm * MI * 16 + 4 * g, c0 = n0 + wn * NI * 16 + li;
+  // kStat, kGrad: element (i, v) is a word if 16 i + v < left, a token's label if
+  // it is own() (-1: not one of the lane's)
+  const int left = (int)lmax(lmin(M - r0, 16 * MI), 0);
+  auto own = [&](int32_t label) {
+    const int64_t at = label - a.v0 - r0;
+    return label >= 0 && at >= 0 && at < 16 * MI && (at & 15) < 4 ? (int)at : -1;
+  };
   if constexpr (EPI == kStat) {
     const float zs = D == kF32 ? *a.zs : a.z0;
     const int64_t half = a.v0 / (16 * MI) + tm * WM + wm;
@@ -398,12 +405,18 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
       for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          const int64_t w = r0 + 16 * i + v;
-          const float z = zs * acc[i][j][v];
-          acc[i][j][v] = z;
-          if (w < M) top = fmaxf(top, z);
-          if (w < M && w + a.v0 == label) a.hit[t] = z;
+          acc[i][j][v] *= zs;
+          if (16 * i + v < left) top = fmaxf(top, acc[i][j][v]);
         }
+      const int at = own(label);
+      if (at >= 0 && at < left) {   // (one lane of all tiles: no branch per element)
+        float z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) z = 16 * i + v == at ? acc[i][j][v] : z;
+        a.hit[t] = z;
+      }
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       float sum = 0.0f;
@@ -411,7 +424,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
       for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-          sum += r0 + 16 * i + v < M ? __expf(acc[i][j][v] - top) : 0.0f;
+          sum += 16 * i + v < left ? __expf(acc[i][j][v] - top) : 0.0f;
       sum += __shfl_xor(sum, 16);
       sum += __shfl_xor(sum, 32);
       if (g == 0 && t < N) {
@@ -426,17 +439,17 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
       const int64_t t = c0 + 16 * j;
       const int32_t label = t < N ? a.labels[t] : -1;
       const float lse = label >= 0 ? a.lse[t] : 0.0f, wn_t = label >= 0 ? a.wn[t] : 0.0f;
+      const int at = own(label), used = label >= 0 ? left : 0;
       uint16_t* row = a.G + t * a.gld * terms(D);
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         uint16_t q[4][terms(D)];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          const int64_t w = r0 + 16 * i + v;
           const float y = zs * acc[i][j][v] - lse;
           float x = D == kF32 ? expf(y) : __expf(y);
-          if (w + a.v0 == label) x -= 1.0f;
-          x = label >= 0 && w < M ? x * wn_t : 0.0f;
+          if (16 * i + v == at) x -= 1.0f;
+          x = 16 * i + v < used ? x * wn_t : 0.0f;
           split<D>(x, q[v]);
         }
 #pragma unroll
