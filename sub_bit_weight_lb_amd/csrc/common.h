@@ -5,14 +5,14 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "sizes.h"
+
 namespace nq {
 
 // Padded sizes: every workspace matrix is stored zero-padded to these
 // multiples so that the tiled kernels need no bounds checks.
 constexpr int kPadMN = 256;  // m and n (rows of Wt / Wt^T / U / V)
 constexpr int kPadR = 128;   // r (rank)
-
-inline int64_t round_up(int64_t x, int64_t q) { return (x + q - 1) / q * q; }
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));

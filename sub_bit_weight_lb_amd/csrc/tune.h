@@ -7,10 +7,6 @@
 
 namespace nq {
 
-// Element types of caller tensors (nq_dtype in include/nq.h).
-enum DType : int { kF32 = 0, kBF16 = 1, kF16 = 2 };
-inline int64_t dtype_bytes(int t) { return t == kF32 ? 4 : 2; }
-
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
