@@ -59,16 +59,16 @@
 
 #include <algorithm>
 
+#include "binback_plan.h"
+
 namespace nq {
+using namespace binback;
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) uint32_t* lds_ptr_t;
 
-constexpr int kDigit = 2048;      // bytes of a digit per 16 rows and 128 columns
-constexpr int kThinMax = 64;      // rows of a thin launch
 constexpr int kThinWaves = 8;
-constexpr int kMaxSplit = 8;      // slices of the columns (few tiles)
 // Up to this many rows, a workgroup per row, else eight rows per workgroup
 // (whole calls in us, rank 1024: 200 rows of a 4096 x 4096 layer 56 v 77, 512
 // rows of 11008 x 4096 117 v 139, 1000 rows of 4096 x 4096 119 v 112).
@@ -179,9 +179,6 @@ __device__ __forceinline__ void to_digits(const float (&x)[4], float inv, uint32
   for (int d = 0; d < 4; ++d) u[d] = ((uint32_t)(int)rintf(x[d] * inv) + kBias) ^ 0x80808080u;
   transpose_bytes(u, out);
 }
-
-// 128-column blocks of a row of digits: whole groups of four
-__host__ __device__ __forceinline__ int64_t blocks(int64_t cols) { return (cols + 511) / 512 * 4; }
 
 // A wave takes 256 columns of a row at a time, four consecutive ones per lane,
 // and exchanges digits through LDS: a lane's four columns 8 b + 4 s + d, d = 0
@@ -325,15 +322,6 @@ __global__ __launch_bounds__(512) void rows_kernel(S0 s0, S1 s1, int64_t T, Digi
 }
 
 // ---------------------------------------------------------------- products
-enum Epi : int {
-  kProj = 0,   // out: p or dp (fp32, or fp64 partials when the columns are split)
-  kGrad = 1,   // column sums of dy q; or dx = s2 da and column sums of da x^
-};
-constexpr int digits(int epi) { return epi == kProj ? 4 : 3; }
-// A wide wave's tile in units of 16 rows and 16 signs: 128 and 120 registers of
-// sums (kGrad of 1 x 8 484 us where 2 x 5 takes 453)
-constexpr int row_tiles(int epi) { return epi == kProj ? 1 : 2; }
-constexpr int sign_tiles(int epi) { return epi == kProj ? 8 : 5; }
 struct Prod {
   Digits a;                   // T rows, K columns
   const uint32_t* bits;       // N x K signs
@@ -609,7 +597,8 @@ __global__ __launch_bounds__(256, 2) void wide_kernel(Prod a0, Prod a1) {
 }
 
 // All T <= 16 MT rows and 16 sign rows per workgroup; wave w takes the
-// 128-column blocks w, w + 8, ...
+// 128-column blocks w, w + 8, ... (rows past T up to 16 MT hold no digits of the
+// call, but the planes have room for them: digit_rows)
 template <int EPI, int D, int MT>
 __global__ __launch_bounds__(64 * kThinWaves) void thin_kernel(Prod a0, Prod a1) {
   constexpr int ND = digits(EPI), kBlock = ND * kDigit;
@@ -698,41 +687,16 @@ struct Work {
   Digits d[2];      // of the two chains
   void* P[2];
   float *cp1, *cp2;
-  int64_t bytes;
 };
-// Slices of the columns of a chain's first product: enough tiles for two
-// workgroups on each of the 256 CUs (one of a thin launch, which has eight
-// waves; the two chains run together), at least 512 columns each.
-constexpr int64_t tiles_of(int epi, int64_t T, int64_t N) {
-  const int64_t rows = 32 * row_tiles(epi), signs = 32 * sign_tiles(epi);
-  return ((T + rows - 1) / rows) * ((N + signs - 1) / signs);
-}
-int proj_split(int64_t T, int64_t r, int64_t K) {
-  const int64_t most = T <= kThinMax ? 256 / (2 * ((r + 15) / 16)) : 512 / (2 * tiles_of(kProj, T, r));
-  return (int)std::max<int64_t>(1, std::min({(int64_t)kMaxSplit, most, blocks(K) / 4}));
-}
-// rows per partial column sum
-constexpr int64_t kSumRows = 32 * row_tiles(kGrad);
-Work carve(char* base, int64_t m, int64_t n, int64_t r, int64_t T) {
+Work carve(char* base, const Plan& p) {
   Work w{};
-  int64_t off = 0;
-  auto take = [&](int64_t bytes) {
-    char* p = base ? base + off : nullptr;
-    off += (bytes + 255) / 256 * 256;
-    return p;
-  };
-  const int64_t Tp = round_up(T, T <= kThinMax ? 16 : kSumRows), nt = (T + kSumRows - 1) / kSumRows;
   for (int c = 0; c < 2; ++c) {
-    const int64_t K = c ? m : n;
-    const int sp = proj_split(T, r, K);
-    w.d[c].planes = (uint8_t*)take(Tp * 128 * std::max(4 * blocks(K), 3 * blocks(r)));
-    w.d[c].steps = (float*)take(4 * T);
-    w.d[c].sums = (i32x4*)take(16 * T);
-    w.P[c] = take(sp == 1 ? 4 * T * r : 8 * T * r * sp);
+    w.d[c] = Digits{(uint8_t*)base + p.planes[c], (float*)(base + p.steps[c]),
+                    (i32x4*)(base + p.sums[c])};
+    w.P[c] = base + p.P[c];
   }
-  w.cp1 = (float*)take(4 * nt * m);
-  w.cp2 = (float*)take(4 * nt * n);
-  w.bytes = off;
+  w.cp1 = (float*)(base + p.cp1);
+  w.cp2 = (float*)(base + p.cp2);
   return w;
 }
 
@@ -752,9 +716,10 @@ hipError_t products(const Prod& a, const Prod& b, hipStream_t s) {
   if (a.T <= kThinMax) {
     const dim3 grid((unsigned)((N + 15) / 16), 2, (unsigned)std::max(a.split, b.split));
     const dim3 block(64 * kThinWaves);
-    if (a.T <= 16)
+    const int tiles = thin_tiles(a.T);
+    if (tiles == 1)
       hipLaunchKernelGGL((thin_kernel<EPI, D, 1>), grid, block, 0, s, a, b);
-    else if (a.T <= 32)
+    else if (tiles == 2)
       hipLaunchKernelGGL((thin_kernel<EPI, D, 2>), grid, block, 0, s, a, b);
     else
       hipLaunchKernelGGL((thin_kernel<EPI, D, 4>), grid, block, 0, s, a, b);
@@ -773,7 +738,8 @@ hipError_t products(const Prod& a, const Prod& b, hipStream_t s) {
 template <int D>
 hipError_t run(const BinBack& a, hipStream_t s) {
   typedef typename Elem<D>::type E;
-  const Work w = carve((char*)a.work, a.m, a.n, a.r, a.T);
+  const Plan plan = plan_for(a.m, a.n, a.r, a.T);
+  const Work w = carve((char*)a.work, plan);
   const bool one = a.T <= kSumRows;   // a single row tile: its column sums are the result
   hipError_t e;
   // a and s1 dy, then p and dp
@@ -788,7 +754,7 @@ hipError_t run(const BinBack& a, hipStream_t s) {
     p[c].ldb = c ? a.ldut : a.ldvt;
     p[c].T = a.T; p[c].N = a.r; p[c].K = K;
     p[c].P = w.P[c]; p[c].ldp = a.r; p[c].slice = a.T * a.r;
-    p[c].split = proj_split(a.T, a.r, K);
+    p[c].split = plan.split[c];
     p[c].kbs = round_up((nkb + p[c].split - 1) / p[c].split, 4);
     p[c].split = (int)((nkb + p[c].kbs - 1) / p[c].kbs);   // (no empty slice)
   }
@@ -816,7 +782,7 @@ hipError_t run(const BinBack& a, hipStream_t s) {
 }  // namespace
 
 int64_t binback_work_bytes(int64_t m, int64_t n, int64_t r, int64_t T) {
-  return carve(nullptr, m, n, r, T).bytes;
+  return plan_for(m, n, r, T).bytes;
 }
 
 hipError_t launch_binback(const BinBack& a, hipStream_t s) {

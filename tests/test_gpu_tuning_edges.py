@@ -3,7 +3,7 @@ ranges have edges; bounds as in test_gpu_tuning.py."""
 import numpy as np
 import pytest
 
-from test_gpu_tuning import TYPES, Head, dt
+from test_gpu_tuning import TYPES, Head, Layer, dt
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +31,19 @@ def test_gradient_reads_nothing_that_it_did_not_write(gpu, name, T, V, d):
     L.check_grad(*nq.vocab_loss_backward(
         L.H, L.W, L.labels, lse, L.dl,
         work=dirty(nq.vocab_loss_work_bytes(T, V, d, dt(name), True), gpu)))
+
+
+# ---------------------------------------------------------------- packed layer's gradient
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("T, m, n, r", [(33, 2100, 1500, 64), (35, 8111, 1249, 147), (40, 4096, 600, 300),
+                                        (48, 700, 5000, 33), (17, 3000, 900, 90), (65, 1500, 2100, 200),
+                                        (300, 700, 1300, 150), (600, 515, 700, 70)])
+def test_layer_gradient_in_a_workspace_of_nans(gpu, name, T, m, n, r):
+    """Rows of digits past the last token are read but not used; sums and joins
+    hold nothing that the call has not written."""
+    import sub_bit_weight_lb_amd as nq
+    print(f"case T={T} {m}x{n} r={r} {name}", flush=True)
+    L = Layer(T + m, T, m, n, r, name, gpu)
+    work = dirty(nq.binary_matmul_backward_work_bytes(T, m, n, r), gpu)
+    L.check(*nq.binary_matmul_backward(*L.args(), work=work))

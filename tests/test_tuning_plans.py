@@ -78,3 +78,39 @@ def test_the_first_piece_writes_every_slice_of_dh(vocab_plan):
         assert share[0] == nz, (T, V, d, t)
         assert max(share) == nz
         assert total - part >= 4 * nz * T * (-(-d // 4) * 4)
+
+
+# ---------------------------------------------------------------- packed layer's gradient
+
+@pytest.fixture(scope="module")
+def layer_plan(tmp_path_factory):
+    return compile_plan(tmp_path_factory.mktemp("layer"), "binback_plan.h", """
+    using namespace binback;
+    const Plan p = plan_for(x[0], x[1], x[2], x[3]);
+    out = {p.planes[0], p.steps[0], p.planes[1], p.steps[1], p.bytes, thin_tiles(x[3]),
+           kThinMax, kDigit, 16 * row_tiles(kProj), 16 * row_tiles(kGrad)};""")
+
+
+def test_the_digit_planes_cover_what_the_products_read(layer_plan):
+    """A thin launch reads the digits of all 16-row tiles of its kernel, a wide
+    one those of all rows of its workgroups' two wave rows, whatever T is: both
+    must lie inside the chain's planes, in front of its steps. Blocks of 2048
+    bytes a digit hold 16 rows and 128 columns, whole groups of four blocks a
+    row; the first products have four digits of the chain's columns, the second
+    three of the rank's."""
+    rng = random.Random(2)
+    shapes = [(11008, 4096, 1536), (28672, 8192, 512), (28672, 8192, 64), (8111, 1249, 147),
+              (65, 300, 129), (1, 1, 1)]
+    shapes += [tuple(log_uniform(rng, 1, 30000) for _ in range(3)) for _ in range(60)]
+    rows = [s + (T,) for s in shapes for T in list(range(1, 130)) + [500, 513, 8191]]
+    for (m, n, r, T), v in zip(rows, layer_plan(rows)):
+        at, end, total, tiles, thin_max, digit = (v[0], v[2]), (v[1], v[3]), v[4], v[5], v[6], v[7]
+        for c, K in enumerate((n, m)):
+            for nd, cols, wave_rows in ((4, K, v[8]), (3, r, v[9])):
+                group = -(-cols // 512) * 4 * nd * digit      # bytes of 16 rows
+                if T <= thin_max:
+                    groups = tiles
+                else:
+                    groups = -(-T // (2 * wave_rows)) * 2 * wave_rows // 16
+                assert 16 * groups >= T
+                assert at[c] + groups * group <= end[c] <= total, (m, n, r, T)
