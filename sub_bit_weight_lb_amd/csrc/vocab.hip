@@ -33,9 +33,16 @@
 // over k, leaves out l l, at most 2^-24 of the product. (Three bf16 terms and
 // six passes measured 1.9 times the time at no smaller error.)
 //
-// Few tokens (up to 32, fp32 up to 64, the loss alone): score_kernel streams W
-// once, 64 words per workgroup, its waves sharing the columns; fp32 is split in
-// registers, into three bf16 terms and six products, which need no scale.
+// Few tokens (up to 32, fp32 up to 64): score_kernel takes kStat's and kGrad's
+// place. It streams W once, 64 words per workgroup, its waves sharing the
+// columns; fp32 is split in registers, into three bf16 terms and six products,
+// which need no scale.
+//
+// The gradient's z have to be the very ones that lse came from: each carries an
+// error of its sum's rounding, which exp(z - lse) keeps whole in a probability
+// near one, and the two mma_kernel epilogues, or score_kernel's two, sum in one
+// order. (fp32, 30 tokens, lse from score_kernel and z from mma_kernel: dH up to
+// ten times as far off as with the same z for both.)
 #include "tune.h"
 
 #include <algorithm>
@@ -544,17 +551,27 @@ __device__ __forceinline__ Frag<D> frag_of(const Raw8<D>& r) {
 __device__ __forceinline__ int term_a(int s) { return (0x250 >> (2 * s)) & 3; }   // 0 0 1 1 2 0
 __device__ __forceinline__ int term_b(int s) { return (0x844 >> (2 * s)) & 3; }   // 0 1 0 1 0 2
 
+// What score_kernel gives: per token and 64 words the largest z and the sum of
+// exponentials, and the label's z; or G of the words from v0 on, zero up to the
+// next multiple of 64, [token][term][gld].
+struct ScoreStat {
+  float *top, *sum, *hit;
+};
+struct ScoreGrad {
+  const float *lse, *wn;
+  uint16_t* G;
+  int64_t gld, v0;
+};
 // (64 registers or fewer: two workgroups of 1024 threads per CU)
-template <int D, int NT>
+template <int D, int NT, bool GRAD>
 __global__ __launch_bounds__(1024 / NT)
     __attribute__((amdgpu_waves_per_eu(D != kF32 && NT == 1 ? 8 : 1))) void score_kernel(
         const typename Elem<D>::type* __restrict__ H, int64_t ldh,
         const typename Elem<D>::type* __restrict__ W, int64_t ldw, int64_t T, int64_t V, int64_t d,
-        const int32_t* __restrict__ labels, float scale, float* __restrict__ top,
-        float* __restrict__ sum, float* __restrict__ hit) {
+        const int32_t* __restrict__ labels, float scale, std::conditional_t<GRAD, ScoreGrad, ScoreStat> o) {
   constexpr int NW = 16 / NT;
   __shared__ f32x4 red[NW][4 * NT][64];
-  __shared__ float st[2][4][16 * NT];
+  __shared__ float st[2][4][GRAD ? 1 : 16 * NT];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, li = lane & 15;
   const int64_t v0 = (int64_t)blockIdx.x * 64;
@@ -617,36 +634,57 @@ __global__ __launch_bounds__(1024 / NT)
     for (int n = 1; n < NW; ++n) z += red[n][e][lane];
     const int64_t t = 16 * j + li, w = v0 + 16 * wave + 4 * g;
     const int32_t label = t < T ? labels[t] : -1;
-    float m = kNegInf, x[4];
+    if constexpr (GRAD) {
+      if (t >= T) continue;
+      const float lse = label >= 0 ? o.lse[t] : 0.0f, wn = label >= 0 ? o.wn[t] : 0.0f;
+      uint16_t q[4][terms(D)];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      x[v] = scale * z[v];
-      if (w + v < V) m = fmaxf(m, x[v]);
-      if (w + v < V && w + v == label) hit[t] = x[v];
-    }
-    m = fmaxf(m, __shfl_xor(m, 16));
-    m = fmaxf(m, __shfl_xor(m, 32));
-    float s = 0.0f;
+      for (int v = 0; v < 4; ++v) {
+        const float y = scale * z[v] - lse;
+        float x = D == kF32 ? expf(y) : __expf(y);
+        if (o.v0 + w + v == label) x -= 1.0f;
+        x = label >= 0 && w + v < V ? x * wn : 0.0f;
+        split<D>(x, q[v]);
+      }
 #pragma unroll
-    for (int v = 0; v < 4; ++v) s += w + v < V ? __expf(x[v] - m) : 0.0f;
-    s += __shfl_xor(s, 16);
-    s += __shfl_xor(s, 32);
-    if (g == 0) {
-      st[0][wave][16 * j + li] = m;
-      st[1][wave][16 * j + li] = s;
+      for (int p = 0; p < terms(D); ++p)
+        *(u32x2*)(o.G + (t * terms(D) + p) * o.gld + w) =
+            u32x2{(uint32_t)q[0][p] | (uint32_t)q[1][p] << 16,
+                  (uint32_t)q[2][p] | (uint32_t)q[3][p] << 16};
+    } else {
+      float m = kNegInf, x[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        x[v] = scale * z[v];
+        if (w + v < V) m = fmaxf(m, x[v]);
+        if (w + v < V && w + v == label) o.hit[t] = x[v];
+      }
+      m = fmaxf(m, __shfl_xor(m, 16));
+      m = fmaxf(m, __shfl_xor(m, 32));
+      float s = 0.0f;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) s += w + v < V ? __expf(x[v] - m) : 0.0f;
+      s += __shfl_xor(s, 16);
+      s += __shfl_xor(s, 32);
+      if (g == 0) {
+        st[0][wave][16 * j + li] = m;
+        st[1][wave][16 * j + li] = s;
+      }
     }
   }
-  __syncthreads();
-  const int t = threadIdx.x;
-  if (t < 16 * NT && t < T) {
-    float m = kNegInf, s = 0.0f;
+  if constexpr (!GRAD) {
+    __syncthreads();
+    const int t = threadIdx.x;
+    if (t < 16 * NT && t < T) {
+      float m = kNegInf, s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = fmaxf(m, st[0][i][t]);
+      for (int i = 0; i < 4; ++i) m = fmaxf(m, st[0][i][t]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (v0 + 16 * i < V) s += st[1][i][t] * __expf(st[0][i][t] - m);
-    top[(int64_t)blockIdx.x * T + t] = m;
-    sum[(int64_t)blockIdx.x * T + t] = s;
+      for (int i = 0; i < 4; ++i)
+        if (v0 + 16 * i < V) s += st[1][i][t] * __expf(st[0][i][t] - m);
+      o.top[(int64_t)blockIdx.x * T + t] = m;
+      o.sum[(int64_t)blockIdx.x * T + t] = s;
+    }
   }
 }
 
@@ -932,13 +970,26 @@ hipError_t words(const Vocab& a, const Plan& p, int64_t v0, int64_t nv, Opnd* o,
   return pack<D>(W, nv, a.d, a.ldw, nullptr, &((Factors*)(w + p.fac))->mw, out, nv, p.dp, s);
 }
 
-template <int D, int NT>
-void score(const Vocab& a, const Plan& p, hipStream_t s) {
+// score_kernel over nv words from v0 on
+template <int D, bool GRAD>
+hipError_t score(const Vocab& a, int64_t v0, int64_t nv,
+                 const std::conditional_t<GRAD, ScoreGrad, ScoreStat>& o, hipStream_t s) {
   typedef typename Elem<D>::type E;
-  char* w = (char*)a.work;
-  hipLaunchKernelGGL((score_kernel<D, NT>), dim3((unsigned)((a.V + 63) / 64)), dim3(1024 / NT), 0, s,
-                     (const E*)a.H, a.ldh, (const E*)a.W, a.ldw, a.T, a.V, a.d, a.labels, a.scale,
-                     (float*)(w + p.top), (float*)(w + p.sum), (float*)(w + p.hit));
+  const dim3 grid((unsigned)((nv + 63) / 64));
+  const E *H = (const E*)a.H, *W = (const E*)a.W + v0 * a.ldw;
+  auto go = [&](auto tiles) {
+    constexpr int NT = decltype(tiles)::value;
+    hipLaunchKernelGGL((score_kernel<D, NT, GRAD>), grid, dim3(1024 / NT), 0, s, H, a.ldh, W, a.ldw,
+                       a.T, nv, a.d, a.labels, a.scale, o);
+  };
+  if (a.T <= 16) {
+    go(std::integral_constant<int, 1>{});
+  } else if (D != kF32 || a.T <= 32) {
+    go(std::integral_constant<int, 2>{});
+  } else if constexpr (D == kF32) {
+    go(std::integral_constant<int, 4>{});
+  }
+  return hipGetLastError();
 }
 
 template <int D>
@@ -949,14 +1000,8 @@ hipError_t loss(const Vocab& a, hipStream_t s) {
   int64_t np;   // partials per token
   if (few(a.T, a.d, D)) {
     np = (a.V + 63) / 64;
-    if (a.T <= 16) {
-      score<D, 1>(a, p, s);
-    } else if (D != kF32 || a.T <= 32) {
-      score<D, 2>(a, p, s);
-    } else if constexpr (D == kF32) {
-      score<D, 4>(a, p, s);
-    }
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const ScoreStat o{(float*)(w + p.top), (float*)(w + p.sum), (float*)(w + p.hit)};
+    if ((e = score<D, false>(a, 0, a.V, o, s)) != hipSuccess) return e;
   } else {
     Mma m{};
     if ((e = begin<D>(a, p, nullptr, &m.B, s)) != hipSuccess) return e;
@@ -999,15 +1044,22 @@ hipError_t backward(const Vocab& a, hipStream_t s) {
   for (int64_t v0 = 0; v0 < a.V; v0 += p.piece) {
     const int64_t nv = std::min(p.piece, a.V - v0), nvp = round_up(nv, 256);
     if ((e = words<D>(a, p, v0, nv, &W, s)) != hipSuccess) return e;
-    Mma m{};
-    m.A = W; m.B = H;
-    m.K = m.k_slice = p.dp;
-    m.zs = &fac->zs;
-    m.z0 = a.scale;
-    m.v0 = v0; m.labels = a.labels; m.lse = a.lse; m.wn = (float*)(w + p.wn);
-    m.G = G; m.gld = p.piece;
-    if ((e = mma_launch<D, kGrad>(m, tile_for(nv, a.T), 1, s)) != hipSuccess) return e;
-    // (G is zero for words past nv and tokens past T, to the tile's end)
+    const bool score_g = few(a.T, a.d, D);
+    if (score_g) {
+      const ScoreGrad o{a.lse, (float*)(w + p.wn), G, p.piece, v0};
+      if ((e = score<D, true>(a, v0, nv, o, s)) != hipSuccess) return e;
+    } else {
+      Mma m{};
+      m.A = W; m.B = H;
+      m.K = m.k_slice = p.dp;
+      m.zs = &fac->zs;
+      m.z0 = a.scale;
+      m.v0 = v0; m.labels = a.labels; m.lse = a.lse; m.wn = (float*)(w + p.wn);
+      m.G = G; m.gld = p.piece;
+      if ((e = mma_launch<D, kGrad>(m, tile_for(nv, a.T), 1, s)) != hipSuccess) return e;
+    }
+    // (G is zero for words past nv to the next multiple of 64, and from
+    // mma_kernel for tokens past T to the tile's end)
     if (a.dH) {
       Mma h{};
       h.A = Opnd{W.p, W.ld, W.plane, a.d, nv};
@@ -1021,7 +1073,7 @@ hipError_t backward(const Vocab& a, hipStream_t s) {
     if (a.dW) {
       Mma x{};
       x.A = Opnd{H.p, H.ld, H.plane, a.d, p.tp};
-      x.B = Opnd{G, p.piece * NTm, p.piece, nv, p.tp};
+      x.B = Opnd{G, p.piece * NTm, p.piece, nv, score_g ? a.T : p.tp};
       x.K = x.k_slice = round_up(a.T, BK);
       x.post = &fac->post_w;
       x.out = (E*)a.dW + v0 * a.lddw; x.ldo = a.lddw;

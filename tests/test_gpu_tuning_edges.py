@@ -47,3 +47,60 @@ def test_layer_gradient_in_a_workspace_of_nans(gpu, name, T, m, n, r):
     L = Layer(T + m, T, m, n, r, name, gpu)
     work = dirty(nq.binary_matmul_backward_work_bytes(T, m, n, r), gpu)
     L.check(*nq.binary_matmul_backward(*L.args(), work=work))
+
+
+# ---------------------------------------------------------------- the loss and its gradient together
+
+U = 2.0 ** -24
+
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("T", [1, 5, 16, 17, 32, 33, 64, 65, 128])
+def test_probabilities_of_the_gradient_sum_to_one(gpu, name, T):
+    """sum_v G_tv = 0: read in dH at a column where every word holds 1 and every
+    token 0. Columns that cancel in pairs make z's partial sums a thousand times
+    its value, so z is off by 1e-4 and more, and probabilities add up to one
+    only if the gradient's z are those that lse came from. With the same z, with
+    y_v = z_v - lse <= 0 and gaps a_v = max z - z_v, what is left is
+      lse: U |lse| of its last sum, 2 U log V of the logarithm, and of the sum of
+        exponentials 24 U (its depth, exp's 2 units) and 4 U sum_v p_v a_v;
+      exp in the gradient: sum_v p_v (4 U + 4 U |y_v|);
+      G: 2 U and its rounding to its type, half() or 2^-22 of fp32's terms, and
+        dH's fp32 sum over the words, (V + 40) U, of sum_v |G_v|, and dH's own
+        rounding."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    from test_gpu_tuning import H as host, half, put
+    print(f"case T={T} {name}", flush=True)
+    V, d = 300, 512
+    rng = np.random.default_rng(T)
+    W = rng.standard_normal((V, d)) * 0.1
+    X = rng.standard_normal((T, d)) * 0.3
+    labels = rng.integers(0, V, T)
+    X[:, 256:] += 4.0 * W[labels, 256:]          # most tokens are sure of their label
+    W[:, 0], X[:, 0] = 1.0, 0.0                  # where the sum is read
+    W[:, 128] = 0.0
+    W[:, 1:128] *= 100.0
+    X[:, 1:128] *= 300.0
+    W[:, 129:256], X[:, 129:256] = W[:, 1:128], -X[:, 1:128]
+    Hd, Wd = put(X, gpu, name), put(W, gpu, name)
+    lab = torch.from_numpy(labels.astype(np.int32)).to(gpu)
+    dl = put(rng.uniform(0.5, 1.0, T), gpu)
+    _, lse = nq.vocab_loss(Hd, Wd, lab)
+    dH, _ = nq.vocab_loss_backward(Hd, Wd, lab, lse, dl)
+
+    z = host(Hd) @ host(Wd).T
+    top = z.max(1, keepdims=True)
+    lse64 = (top + np.log(np.exp(z - top).sum(1, keepdims=True)))[:, 0]
+    p = np.exp(z - lse64[:, None])
+    G = p.copy()
+    G[np.arange(T), labels] -= 1.0
+    # (the z that are used differ from these by a part in a hundred at most)
+    absG, gaps, y = 1.1 * np.abs(G).sum(1), (p * (top - z)).sum(1), (p * (lse64[:, None] - z)).sum(1)
+    g_type = 2.0 ** -22 if name == "float32" else half(name)
+    tol = U * (np.abs(lse64) + 2 * np.log(V) + 24 + 4 * gaps + 4 + 4 * y)
+    tol = tol + (2 * U + g_type + (V + 40) * U) * absG
+    tol = 1.1 * host(dl) * tol * (1 + half(name))
+    got = np.abs(host(dH)[:, 0])
+    print("largest share of the bound", float((got / tol).max()), flush=True)
+    np.testing.assert_array_less(got, tol)
