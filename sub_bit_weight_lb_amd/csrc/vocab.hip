@@ -29,7 +29,7 @@
 // to 2^15 at its largest, so that probabilities down to 2^-29 keep all their
 // bits. fp32 operands are scaled by a power of two each (H, W and G to 2^15 at
 // their largest) and split into two fp16 terms x = h + l, which hold x to
-// 2^-24 of itself or 2^-39 of the largest; x y = h h + h l + l h, three passes
+// 2^-24 of itself or 2^-39 of the largest; x y = h l + l h + h h, three passes
 // over k, leaves out l l, at most 2^-24 of the product. (Three bf16 terms and
 // six passes measured 1.9 times the time at no smaller error.)
 //
@@ -303,15 +303,16 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
   Reader<BN, NI, BM_> rb;
   ra.init(wm * MI, g, li);
   rb.init(wn * NI, g, li);
-  // passes: h h, h l, l h
+  // passes: h l, l h, h h (the small ones first: what they round is 2^-11 of a
+  // sum with h h in it)
   int pass = 0, kt = 0;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   // the next stage's copies, ready to go to `stage`
   auto aim = [&](int stage, bool live) {
     const uint32_t st = lds0 + stage * kStage;
     const int64_t k = k_lo + (int64_t)kt * BK;
-    ta.aim(live, st, wave, k, D == kF32 && pass == 2 ? a.A.plane : 0);
-    tb.aim(live, st + BM * 128, wave, k, D == kF32 && pass == 1 ? a.B.plane : 0);
+    ta.aim(live, st, wave, k, D == kF32 && pass == 1 ? a.A.plane : 0);
+    tb.aim(live, st + BM * 128, wave, k, D == kF32 && pass == 0 ? a.B.plane : 0);
     if (++kt == nk) {
       kt = 0;
       ++pass;

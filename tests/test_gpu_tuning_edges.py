@@ -104,3 +104,45 @@ def test_probabilities_of_the_gradient_sum_to_one(gpu, name, T):
     got = np.abs(host(dH)[:, 0])
     print("largest share of the bound", float((got / tol).max()), flush=True)
     np.testing.assert_array_less(got, tol)
+
+
+@pytest.mark.parametrize("tokens", [(1, 2, 8, 16), (17, 24, 30, 32), (33, 40, 48, 64), (65, 80, 100, 128)])
+def test_fp32_gradients_are_as_exact_as_the_plain_form(gpu, tokens):
+    """Against float64, over some batches together, the error (relative, in the
+    norm) of dH, dW and lse is at most 1.5 times that of the same formulas in
+    fp32 torch products. Both round every partial sum once to fp32, in orders
+    of their own, so that the two errors are samples of one size: a sum in
+    three passes over k, the largest first, rounds three times as often at full
+    size and comes out at twice it; logits that differ from those of lse at ten
+    times it."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    V, d = 700, 4096
+    own, plain = np.zeros(3), np.zeros(3)
+    for T in tokens:
+        print(f"case T={T}", flush=True)
+        g = torch.Generator(device=gpu).manual_seed(T)
+        W = 0.02 * torch.randn((V, d), generator=g, device=gpu)
+        labels = torch.randint(0, V, (T,), generator=g, device=gpu)
+        lean = (torch.arange(T, device=gpu) % 2).float().unsqueeze(1) * (10.0 / (0.0004 * d))
+        X = torch.randn((T, d), generator=g, device=gpu) + lean * W[labels]
+        dl = torch.full((T,), 1.0 / T, device=gpu)
+
+        def formulas(X, W, dl):
+            z = torch.mm(X, W.t())
+            top = z.amax(1, keepdim=True)
+            lse = torch.log(torch.exp(z - top).sum(1)) + top[:, 0]
+            G = torch.exp(z - lse.unsqueeze(1))
+            G[torch.arange(T, device=gpu), labels] -= 1.0
+            G = G * dl.unsqueeze(1)
+            return torch.mm(G, W), torch.mm(G.t(), X), lse
+
+        _, lse = nq.vocab_loss(X, W, labels.int())
+        got = (*nq.vocab_loss_backward(X, W, labels.int(), lse, dl), lse)
+        want = formulas(X.double(), W.double(), dl.double())
+        for e, values in ((own, got), (plain, formulas(X, W, dl))):
+            e += [float((a.double() - b).norm() / b.norm()) ** 2 for a, b in zip(values, want)]
+    ratio = np.sqrt(own / plain)
+    print("own", np.sqrt(own), "plain", np.sqrt(plain), flush=True)
+    assert (ratio[:2] <= 1.5).all(), ratio
+    assert ratio[2] <= 2.0, ratio     # (lse adds one sum of a handful of large terms)
