@@ -27,9 +27,9 @@
 // Types: bf16 and fp16 operands are exact and sums are fp32; G is rounded to
 // the operands' type once (half a unit, like the results). fp16's G is scaled
 // to 2^15 at its largest, so that probabilities down to 2^-29 keep all their
-// bits. fp32 operands are scaled by a power of two each (H, W and G to 2^15 at
-// their largest) and split into two fp16 terms x = h + l, which hold x to
-// 2^-24 of itself or 2^-39 of the largest; x y = h l + l h + h h, three passes
+// bits. fp32 operands are scaled by powers of two (each row of H, all of H for
+// dW, W and G to 2^15 at their largest) and split into two fp16 terms x = h + l,
+// which hold x to 2^-24 of itself or 2^-39 of the largest; x y = h l + l h + h h, three passes
 // over k, leaves out l l, at most 2^-24 of the product. (Three bf16 terms and
 // six passes measured 1.9 times the time at no smaller error.)
 //
@@ -105,8 +105,8 @@ struct Mma {
   Opnd A, B;                // C (M x N), M = A.rows, N = B.rows
   int64_t K;                // a multiple of 64
   int64_t k_slice;          // k per slice (grid y), a multiple of 64
-  const float* zs;          // kStat, kGrad: the factor of the products (fp32: one float on the
-  float z0;                 // GPU; 16-bit: z0)
+  const float* zs;          // kStat, kGrad: the factor of the products (fp32: of each token;
+  float z0;                 // 16-bit: z0)
   // kStat, kGrad: rows are words v0 .., columns tokens
   int64_t v0;
   const int32_t* labels;
@@ -397,12 +397,12 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
     return label >= 0 && at >= 0 && at < 16 * MI && (at & 15) < 4 ? (int)at : -1;
   };
   if constexpr (EPI == kStat) {
-    const float zs = D == kF32 ? *a.zs : a.z0;
     const int64_t half = a.v0 / (16 * MI) + tm * WM + wm;
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const int64_t t = c0 + 16 * j;
       const int32_t label = t < N ? a.labels[t] : -1;
+      const float zs = D == kF32 ? (t < N ? a.zs[t] : 0.0f) : a.z0;
       float top = kNegInf;
 #pragma unroll
       for (int i = 0; i < MI; ++i)
@@ -436,12 +436,12 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
       }
     }
   } else if constexpr (EPI == kGrad) {
-    const float zs = D == kF32 ? *a.zs : a.z0;
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const int64_t t = c0 + 16 * j;
       const int32_t label = t < N ? a.labels[t] : -1;
       const float lse = label >= 0 ? a.lse[t] : 0.0f, wn_t = label >= 0 ? a.wn[t] : 0.0f;
+      const float zs = D == kF32 ? (label >= 0 ? a.zs[t] : 0.0f) : a.z0;
       const int at = own(label), used = label >= 0 ? left : 0;
       uint16_t* row = a.G + t * a.gld * terms(D);
 #pragma unroll
@@ -731,47 +731,77 @@ __global__ __launch_bounds__(1024) void stat_kernel(const float* __restrict__ to
   loss[t] = label < 0 ? 0.0f : l - h;
 }
 
-// parts[y][x] = the largest finite magnitude of a share of H (y = 0) or W
+// Factors of each token, read by the kernels that follow.
+struct Rows {
+  float *hz, *hw;        // powers of two that its row of H is scaled by, for z and for dW (fp32)
+  float *zs;             // scale / (hz mw): of its products (fp32)
+  float *wn;             // of G
+};
+Rows rows_of(char* work, const Plan& p, int64_t T) {
+  float* f = (float*)(work + p.rows);
+  return {f, f + T, f + 2 * T, f + 3 * T};
+}
+// The largest finite magnitudes: hm[t] of each row of H (y = 0; 0 for an ignored
+// token), parts[x] of a share of W's rows (y = 1).
 __global__ __launch_bounds__(256) void amax_kernel(const float* __restrict__ H, int64_t T,
                                                    int64_t ldh, const float* __restrict__ W,
                                                    int64_t V, int64_t ldw, int64_t d,
                                                    const int32_t* __restrict__ labels,
+                                                   float* __restrict__ hm,
                                                    float* __restrict__ parts) {
   __shared__ float sm[256];
-  const bool w = blockIdx.y;
-  const float* X = w ? W : H;
-  const int64_t rows = w ? V : T, ld = w ? ldw : ldh;
+  struct __attribute__((packed)) Four { float v[4]; };
   float m = 0.0f;
-  auto take = [&](float x, bool on) {
-    const float v = on ? fabsf(x) : 0.0f;
+  auto take = [&](float x) {
+    const float v = fabsf(x);
     m = v < __builtin_inff() ? fmaxf(m, v) : m;
   };
-  // four rows at a time, 16 bytes each, from any address; rows and columns past
-  // the end are clamped (a maximum may see a value twice), so that no branch
-  // parts the loads
-  for (int64_t r0 = blockIdx.x; r0 < rows; r0 += 4 * (int64_t)gridDim.x) {
-    const float* x[4];
-    bool on[4];
+  // four times 16 bytes at a time, from any address; rows and columns past the end
+  // are clamped (a maximum may see a value twice), so that no branch parts the loads
+  if (blockIdx.y == 0) {   // a wave per row
+    const int lane = threadIdx.x & 63;
+    for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < T; t += 4 * (int64_t)gridDim.x) {
+      const float* x = H + t * ldh;
+      m = 0.0f;
+      if (labels[t] >= 0) {
+        if (d < 4) {
+          for (int64_t c = lane; c < d; c += 64) take(x[c]);
+        } else {
+          for (int64_t c = 4 * lane; c < d; c += 1024) {
+            Four q[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t r = lmin(r0 + u * (int64_t)gridDim.x, rows - 1);
-      on[u] = w || labels[r] >= 0;
-      x[u] = X + r * ld;
+            for (int u = 0; u < 4; ++u) __builtin_memcpy(&q[u], x + lmin(c + 256 * u, d - 4), 16);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) take(q[u].v[i]);
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+      if (lane == 0) hm[t] = m;
     }
+    return;
+  }
+  for (int64_t r0 = blockIdx.x; r0 < V; r0 += 4 * (int64_t)gridDim.x) {
+    const float* x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) x[u] = W + lmin(r0 + u * (int64_t)gridDim.x, V - 1) * ldw;
     if (d < 4) {
       for (int64_t c = threadIdx.x; c < d; c += 256)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) take(x[u][c], on[u]);
+        for (int u = 0; u < 4; ++u) take(x[u][c]);
       continue;
     }
     for (int64_t c = 4 * threadIdx.x; c < d; c += 1024) {
-      struct __attribute__((packed)) { float v[4]; } q[4];
+      Four q[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) __builtin_memcpy(&q[u], x[u] + lmin(c, d - 4), 16);
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) take(q[u].v[i], on[u]);
+        for (int i = 0; i < 4; ++i) take(q[u].v[i]);
     }
   }
   sm[threadIdx.x] = m;
@@ -780,7 +810,7 @@ __global__ __launch_bounds__(256) void amax_kernel(const float* __restrict__ H, 
     if ((int)threadIdx.x < o) sm[threadIdx.x] = fmaxf(sm[threadIdx.x], sm[threadIdx.x + o]);
     __syncthreads();
   }
-  if (threadIdx.x == 0) parts[blockIdx.y * gridDim.x + blockIdx.x] = sm[0];
+  if (threadIdx.x == 0) parts[blockIdx.x] = sm[0];
 }
 // the largest of v over the workgroup's 1024 threads
 __device__ __forceinline__ float max_of(float v, float* sm) {
@@ -801,20 +831,27 @@ __device__ __forceinline__ float power_for(float m) {
 }
 // The factors, and with dloss the normalised weights: wn[t] = dloss[t] /
 // max|dloss| times gs (0 for an ignored token, NaN for a label at or past V).
-// parts (fp32 operands): the maxima of H and W. One workgroup.
-__global__ __launch_bounds__(1024) void factors_kernel(const float* __restrict__ parts,
+// hm and parts (fp32 operands): the maxima of H's rows and of W. One workgroup.
+__global__ __launch_bounds__(1024) void factors_kernel(const float* __restrict__ hm,
+                                                       const float* __restrict__ parts,
                                                        const float* __restrict__ dloss,
                                                        const int32_t* __restrict__ labels,
                                                        int64_t T, int64_t V, float gs, float scale,
-                                                       float* __restrict__ wn,
-                                                       Factors* __restrict__ out) {
+                                                       Rows rows, Factors* __restrict__ out) {
   __shared__ float sm[1024];
   float mh = 1.0f, mw = 1.0f, m = 0.0f;
   if (parts) {
-    const int t = threadIdx.x;
-    mh = power_for(max_of(parts[t], sm));
-    mw = power_for(max_of(parts[kAmaxParts + t], sm));
+    mw = power_for(max_of(parts[threadIdx.x], sm));
+    for (int64_t t = threadIdx.x; t < T; t += 1024) m = fmaxf(m, hm[t]);
+    mh = power_for(max_of(m, sm));
+    for (int64_t t = threadIdx.x; t < T; t += 1024) {
+      const float f = power_for(hm[t]);
+      rows.hz[t] = f;
+      rows.zs[t] = (float)((double)scale / f / mw);
+      if (dloss) rows.hw[t] = mh;
+    }
   }
+  m = 0.0f;
   if (dloss) {
     for (int64_t t = threadIdx.x; t < T; t += 1024)
       if (labels[t] >= 0) m = fmaxf(m, fabsf(dloss[t]));
@@ -822,12 +859,12 @@ __global__ __launch_bounds__(1024) void factors_kernel(const float* __restrict__
     for (int64_t t = threadIdx.x; t < T; t += 1024) {
       const int32_t label = labels[t];
       const float w = m == 0.0f ? dloss[t] : dloss[t] / m * gs;   // (all zero, or NaN)
-      wn[t] = label < 0 ? 0.0f : label < V ? w : __uint_as_float(0x7fc00000u);
+      rows.wn[t] = label < 0 ? 0.0f : label < V ? w : __uint_as_float(0x7fc00000u);
     }
   }
   if (threadIdx.x == 0) {
     const double f = (m == 0.0f ? 1.0 : (double)m) * (double)scale / (double)gs;
-    *out = Factors{mh, mw, (float)((double)scale / mh / mw), (float)(f / mw), (float)(f / mh)};
+    *out = Factors{mw, (float)(f / mw), (float)(f / mh)};
   }
 }
 
@@ -851,10 +888,11 @@ __global__ __launch_bounds__(256) void dh_kernel(const float* __restrict__ part,
 }
 
 // ---------------------------------------------------------------- layout
-// out [row][term][kp] = the terms of X (rows x k) times *mul (fp32), zero from
-// k to kp, for rows past the last up to rp, and for rows whose label is
-// negative (labels nullable).
-template <int D>
+// out [row][term][kp] = the terms of X (rows x k) times a factor (fp32: *mul, or
+// with PER_ROW mul[row]), zero from k to kp, for rows past the last up to rp, and
+// for rows whose label is negative (labels nullable). Form z of the grid takes
+// mul + z * rows and the z-th copy of out.
+template <int D, bool PER_ROW>
 __global__ __launch_bounds__(256) void pack_kernel(const typename Elem<D>::type* __restrict__ X,
                                                    int64_t rows, int64_t k, int64_t ld,
                                                    const int32_t* __restrict__ labels,
@@ -864,10 +902,11 @@ __global__ __launch_bounds__(256) void pack_kernel(const typename Elem<D>::type*
   typedef typename Elem<D>::type E;
   const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
   if (c >= kp) return;
-  const float f = D == kF32 ? *mul : 1.0f;
+  out += blockIdx.z * rp * kp * terms(D);
   for (int64_t r = blockIdx.y; r < rp; r += gridDim.y) {
     E e[8];
     const bool row = r < rows && (!labels || labels[r] >= 0);
+    const float f = D != kF32 ? 1.0f : !PER_ROW ? *mul : row ? mul[blockIdx.z * rows + r] : 0.0f;
     if (row && c + 8 <= k) {
       __builtin_memcpy(e, X + r * ld + c, sizeof(e));
     } else {
@@ -919,42 +958,53 @@ hipError_t mma_launch(const Mma& a, int tile, int slices, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int D>
+template <int D, bool PER_ROW>
 hipError_t pack(const void* X, int64_t rows, int64_t k, int64_t ld, const int32_t* labels,
-                const float* mul, uint16_t* out, int64_t rp, int64_t kp, hipStream_t s) {
-  const dim3 grid((unsigned)((kp / 8 + 255) / 256), (unsigned)std::min<int64_t>(rp, 16384));
-  hipLaunchKernelGGL(pack_kernel<D>, grid, dim3(256), 0, s, (const typename Elem<D>::type*)X, rows,
-                     k, ld, labels, mul, out, rp, kp);
+                const float* mul, uint16_t* out, int64_t rp, int64_t kp, int forms, hipStream_t s) {
+  const dim3 grid((unsigned)((kp / 8 + 255) / 256), (unsigned)std::min<int64_t>(rp, 16384),
+                  (unsigned)forms);
+  hipLaunchKernelGGL((pack_kernel<D, PER_ROW>), grid, dim3(256), 0, s,
+                     (const typename Elem<D>::type*)X, rows, k, ld, labels, mul, out, rp, kp);
   return hipGetLastError();
 }
 
-// The factors of a call (and wn with dloss), and H: rows with those of ignored
-// tokens zeroed, which dW's sums over the tokens need, or for the loss alone in
-// place where it can be (an ignored token's column of products is not used).
+// The factors of a call (and wn with dloss), and H twice: for z, and with dloss
+// for dW. The rows of ignored tokens are zeroed, which dW's sums over the tokens
+// need; for the loss alone H stays in place where it can (an ignored token's
+// column of products is not used). fp32 has a copy of its own for each (a token's
+// power of two does not pass through dW's sums).
 template <int D>
-hipError_t begin(const Vocab& a, const Plan& p, const float* dloss, Opnd* H, hipStream_t s) {
+hipError_t begin(const Vocab& a, const Plan& p, const float* dloss, Opnd* Hz, Opnd* Hw,
+                 hipStream_t s) {
   char* w = (char*)a.work;
   Factors* fac = (Factors*)(w + p.fac);
-  float* amax = (float*)(w + p.amax);
+  float *hm = (float*)(w + p.hm), *amax = (float*)(w + p.amax);
+  const Rows rows = rows_of(w, p, a.T);
   hipError_t e;
   if (D != kF32 && !dloss && direct(a.H, a.ldh, a.d, D)) {
-    *H = Opnd{(const uint16_t*)a.H, a.ldh, 0, a.T, a.d};
+    *Hz = Opnd{(const uint16_t*)a.H, a.ldh, 0, a.T, a.d};
     return hipSuccess;
   }
   if (D == kF32) {
     hipLaunchKernelGGL(amax_kernel, dim3(kAmaxParts, 2), dim3(256), 0, s, (const float*)a.H, a.T,
-                       a.ldh, (const float*)a.W, a.V, a.ldw, a.d, a.labels, amax);
+                       a.ldh, (const float*)a.W, a.V, a.ldw, a.d, a.labels, hm, amax);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (D == kF32 || dloss) {
-    hipLaunchKernelGGL(factors_kernel, dim3(1), dim3(1024), 0, s, D == kF32 ? amax : nullptr,
-                       dloss, a.labels, a.T, a.V, D == kBF16 ? 1.0f : kTop16, a.scale,
-                       (float*)(w + p.wn), fac);
+    hipLaunchKernelGGL(factors_kernel, dim3(1), dim3(1024), 0, s, hm, D == kF32 ? amax : nullptr,
+                       dloss, a.labels, a.T, a.V, D == kBF16 ? 1.0f : kTop16, a.scale, rows, fac);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   uint16_t* out = (uint16_t*)(w + p.hp);
-  *H = Opnd{out, p.dp * terms(D), p.dp, a.T, p.dp};
-  return pack<D>(a.H, a.T, a.d, a.ldh, a.labels, &fac->mh, out, p.tp, p.dp, s);
+  const int n = dloss ? forms(D) : 1;
+  *Hz = Opnd{out, p.dp * terms(D), p.dp, a.T, p.dp};
+  *Hw = Opnd{out + (n - 1) * p.tp * p.dp * terms(D), p.dp * terms(D), p.dp, a.d, p.tp};
+  // (the copies that the call's products read, one behind the other)
+  const bool z = !dloss || !few(a.T, a.d, D), dw = dloss && a.dW;
+  const int from = z ? 0 : n - 1, to = dw ? n - 1 : 0;
+  if ((!z && !dw) || from > to) return hipSuccess;
+  return pack<D, true>(a.H, a.T, a.d, a.ldh, a.labels, rows.hz + from * a.T,
+                       out + from * p.tp * p.dp * terms(D), p.tp, p.dp, to - from + 1, s);
 }
 // nv words of W from v0: in place, or a copy in the workspace
 template <int D>
@@ -968,7 +1018,7 @@ hipError_t words(const Vocab& a, const Plan& p, int64_t v0, int64_t nv, Opnd* o,
   char* w = (char*)a.work;
   uint16_t* out = (uint16_t*)(w + p.wp);
   *o = Opnd{out, p.dp * terms(D), p.dp, nv, p.dp};
-  return pack<D>(W, nv, a.d, a.ldw, nullptr, &((Factors*)(w + p.fac))->mw, out, nv, p.dp, s);
+  return pack<D, false>(W, nv, a.d, a.ldw, nullptr, &((Factors*)(w + p.fac))->mw, out, nv, p.dp, 1, s);
 }
 
 // score_kernel over nv words from v0 on
@@ -1005,9 +1055,10 @@ hipError_t loss(const Vocab& a, hipStream_t s) {
     if ((e = score<D, false>(a, 0, a.V, o, s)) != hipSuccess) return e;
   } else {
     Mma m{};
-    if ((e = begin<D>(a, p, nullptr, &m.B, s)) != hipSuccess) return e;
+    Opnd unused;
+    if ((e = begin<D>(a, p, nullptr, &m.B, &unused, s)) != hipSuccess) return e;
     m.K = m.k_slice = p.dp;
-    m.zs = &((Factors*)(w + p.fac))->zs;
+    m.zs = rows_of(w, p, a.T).zs;
     m.z0 = a.scale;
     m.labels = a.labels;
     m.top = (float*)(w + p.top); m.sum = (float*)(w + p.sum); m.hit = (float*)(w + p.hit);
@@ -1037,8 +1088,9 @@ hipError_t backward(const Vocab& a, hipStream_t s) {
   constexpr int NTm = terms(D);
   const int64_t ldp = round_up(a.d, 4), slice = a.T * ldp;
   hipError_t e;
-  Opnd H, W;
-  if ((e = begin<D>(a, p, a.dloss, &H, s)) != hipSuccess) return e;
+  const Rows rows = rows_of(w, p, a.T);
+  Opnd Hz, Hw, W;
+  if ((e = begin<D>(a, p, a.dloss, &Hz, &Hw, s)) != hipSuccess) return e;
   // every piece uses the same slices of its words for dH; the first writes them
   // all, the last, where it is another, may leave some as they are: those are not
   // launched
@@ -1047,15 +1099,15 @@ hipError_t backward(const Vocab& a, hipStream_t s) {
     if ((e = words<D>(a, p, v0, nv, &W, s)) != hipSuccess) return e;
     const bool score_g = few(a.T, a.d, D);
     if (score_g) {
-      const ScoreGrad o{a.lse, (float*)(w + p.wn), G, p.piece, v0};
+      const ScoreGrad o{a.lse, rows.wn, G, p.piece, v0};
       if ((e = score<D, true>(a, v0, nv, o, s)) != hipSuccess) return e;
     } else {
       Mma m{};
-      m.A = W; m.B = H;
+      m.A = W; m.B = Hz;
       m.K = m.k_slice = p.dp;
-      m.zs = &fac->zs;
+      m.zs = rows.zs;
       m.z0 = a.scale;
-      m.v0 = v0; m.labels = a.labels; m.lse = a.lse; m.wn = (float*)(w + p.wn);
+      m.v0 = v0; m.labels = a.labels; m.lse = a.lse; m.wn = rows.wn;
       m.G = G; m.gld = p.piece;
       if ((e = mma_launch<D, kGrad>(m, tile_for(nv, a.T), 1, s)) != hipSuccess) return e;
     }
@@ -1073,7 +1125,7 @@ hipError_t backward(const Vocab& a, hipStream_t s) {
     }
     if (a.dW) {
       Mma x{};
-      x.A = Opnd{H.p, H.ld, H.plane, a.d, p.tp};
+      x.A = Hw;
       x.B = Opnd{G, p.piece * NTm, p.piece, nv, score_g ? a.T : p.tp};
       x.K = x.k_slice = round_up(a.T, BK);
       x.post = &fac->post_w;

@@ -15,10 +15,11 @@ constexpr int terms(int D) { return D == kF32 ? 2 : 1; }
 constexpr int kAmaxParts = 1024;
 // Factors of a call, read by the kernels that follow.
 struct Factors {
-  float mh, mw;          // powers of two that H and W are scaled by (fp32, else 1)
-  float zs;              // scale / (mh mw)
+  float mw;              // power of two that W is scaled by (fp32, else 1)
   float post_h, post_w;  // of dH and dW
 };
+// copies of H that a gradient takes: for z and for dW
+constexpr int forms(int D) { return D == kF32 ? 2 : 1; }
 
 // Whether score_kernel takes a call. With more tokens mma_kernel reads W at a
 // higher rate although half of a tile is empty (4096 x 32000 bf16, 64 tokens: 94
@@ -32,7 +33,7 @@ struct Plan {
   int nz;                      // slices of dH, each with a share of the first piece
   int64_t kz;                  // words per slice, to 64
   // byte offsets
-  int64_t hp, wp, top, sum, hit, wn, fac, amax, G, part, bytes;
+  int64_t hp, wp, top, sum, hit, hm, rows, fac, amax, G, part, bytes;
 };
 inline int64_t tiles_of(int64_t M, int64_t N, int64_t tile) {
   return ((M + tile - 1) / tile) * ((N + tile - 1) / tile);
@@ -98,15 +99,16 @@ inline Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad) {
     }
   }
   p.fac = take(sizeof(Factors));
-  p.amax = take(4 * 2 * kAmaxParts);
-  p.hp = take(2 * nt * p.tp * p.dp);
+  p.amax = take(4 * kAmaxParts);
+  p.hm = take(4 * T);
+  p.rows = take(4 * 4 * T);
+  p.hp = take(2 * nt * p.tp * p.dp * (grad ? forms(dtype) : 1));
   p.wp = take(2 * nt * p.piece * p.dp);
   if (grad) {
     // (the first piece, which may be V itself, writes every slice that is joined)
     const int64_t words = round_up(std::min(p.piece, V), BK), nz = dh_slices(T, d, p.piece);
     p.kz = round_up((words + nz - 1) / nz, BK);
     p.nz = (int)((words + p.kz - 1) / p.kz);
-    p.wn = take(4 * T);
     p.G = take(2 * nt * p.tp * p.piece);
     p.part = take(4 * p.nz * T * round_up(d, 4));
   }

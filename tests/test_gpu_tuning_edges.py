@@ -146,3 +146,27 @@ def test_fp32_gradients_are_as_exact_as_the_plain_form(gpu, tokens):
     print("own", np.sqrt(own), "plain", np.sqrt(plain), flush=True)
     assert (ratio[:2] <= 1.5).all(), ratio
     assert ratio[2] <= 2.0, ratio     # (lse adds one sum of a handful of large terms)
+
+
+@pytest.mark.parametrize("T", [9, 64, 65, 300])
+def test_a_loud_token_costs_the_others_nothing(gpu, T):
+    """fp32 hidden states of one token 1e8 times the rest: the others' loss, lse
+    and dH keep every bit."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    L = Head(41, T, 700, 200, "float32", gpu, ignored=0.0)
+    loss, lse = nq.vocab_loss(L.H, L.W, L.labels)
+    L.check_loss(loss, lse)
+    dH, dW = nq.vocab_loss_backward(L.H, L.W, L.labels, lse, L.dl)
+    L.check_grad(dH, dW)
+    L.H[3] *= 1e8
+    loud = nq.vocab_loss(L.H, L.W, L.labels)
+    rest = [t for t in range(T) if t != 3]
+    assert torch.equal(loud[0][rest], loss[rest]) and torch.equal(loud[1][rest], lse[rest])
+    got, _ = nq.vocab_loss_backward(L.H, L.W, L.labels, loud[1], L.dl)
+    assert torch.equal(got[rest], dH[rest])
+    # ignored, it does not count for dW either
+    L.labels[3] = -1
+    without, _ = nq.vocab_loss(L.H, L.W, L.labels)
+    assert torch.equal(without[rest], loss[rest])
+    L.check_grad(*nq.vocab_loss_backward(L.H, L.W, L.labels, loud[1], L.dl))
