@@ -25,10 +25,14 @@
 // LDS to the registers, by ds_read_b64_tr_b16.
 //
 // Types: bf16 and fp16 operands are exact and sums are fp32; G is rounded to
-// the operands' type once (half a unit, like the results). fp16's G is scaled
-// to 2^15 at its largest, so that probabilities down to 2^-29 keep all their
-// bits. fp32 operands are scaled by powers of two (each row of H, all of H for
-// dW, W and G to 2^15 at their largest) and split into two fp16 terms x = h + l,
+// the operands' type once (half a unit, like the results; bf16's dH and dW are
+// then off by about a tenth more than by their own rounding). fp16 and fp32 G hold
+// (p - [label]) of each token to 2^15 at its largest whatever the others' dloss
+// are (fp16: from 2^-10 of the largest dloss on), so that probabilities down to
+// 2^-29 keep all their bits; dloss itself enters at the end of dH's row and,
+// as a power of two, in a copy of H for dW. fp32 operands are scaled by powers of
+// two (each row of H, all of H's copy for dW, W to 2^15 at their largest) and
+// split into two fp16 terms x = h + l,
 // which hold x to 2^-24 of itself or 2^-39 of the largest; x y = h l + l h + h h, three passes
 // over k, leaves out l l, at most 2^-24 of the product. (Three bf16 terms and
 // six passes measured 1.9 times the time at no smaller error.)
@@ -60,7 +64,6 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4* lds_tr_t;
 
 constexpr float kNegInf = -__builtin_inff();
-constexpr float kTop16 = 32768.0f;   // what fp16 terms are scaled to
 
 // one 16 x 16 x 32 product of 16-bit operands
 template <bool F16>
@@ -733,13 +736,13 @@ __global__ __launch_bounds__(1024) void stat_kernel(const float* __restrict__ to
 
 // Factors of each token, read by the kernels that follow.
 struct Rows {
-  float *hz, *hw;        // powers of two that its row of H is scaled by, for z and for dW (fp32)
+  float *hz, *hw;        // powers of two that its row of H is scaled by, for z (fp32) and for dW
   float *zs;             // scale / (hz mw): of its products (fp32)
-  float *wn;             // of G
+  float *wn, *pt;        // of G, of its row of dH
 };
 Rows rows_of(char* work, const Plan& p, int64_t T) {
   float* f = (float*)(work + p.rows);
-  return {f, f + T, f + 2 * T, f + 3 * T};
+  return {f, f + T, f + 2 * T, f + 3 * T, f + 4 * T};
 }
 // The largest finite magnitudes: hm[t] of each row of H (y = 0; 0 for an ignored
 // token), parts[x] of a share of W's rows (y = 1).
@@ -829,70 +832,117 @@ __device__ __forceinline__ float power_for(float m) {
   const int e = 14 - ((int)(b >> 23) - 127) + ((b & 0x7fffffu) == 0);
   return m > 0.0f ? __uint_as_float((uint32_t)(min(max(e, -126), 126) + 127) << 23) : 1.0f;
 }
-// The factors, and with dloss the normalised weights: wn[t] = dloss[t] /
-// max|dloss| times gs (0 for an ignored token, NaN for a label at or past V).
-// hm and parts (fp32 operands): the maxima of H's rows and of W. One workgroup.
+// value * 2^e, rounded once
+__device__ __forceinline__ float scaled(double value, int e) { return (float)ldexp(value, e); }
+// The factors. With dloss = f 2^x per token (1/2 <= |f| < 1; x0 of the largest),
+//   bf16:       G = (p - [label]) dloss / max|dloss|: its exponents reach far enough;
+//   fp32:       G = (p - [label]) f 2^15 whatever the others' dloss are, dH's row
+//               takes 2^(x - 15) at its end, and H's copy for dW 2^(x - x0);
+//   fp16:       as fp32, but G keeps up to kInG bits of x - x0, as H, which is not
+//               scaled to its type's top, has fewer to give.
+// (0 for an ignored token; NaN for a label at or past V.) hm and parts (fp32
+// operands): the maxima of H's rows and of W. One workgroup.
+constexpr int kInG = 10;
+template <int D>
 __global__ __launch_bounds__(1024) void factors_kernel(const float* __restrict__ hm,
                                                        const float* __restrict__ parts,
                                                        const float* __restrict__ dloss,
                                                        const int32_t* __restrict__ labels,
-                                                       int64_t T, int64_t V, float gs, float scale,
-                                                       Rows rows, Factors* __restrict__ out) {
+                                                       int64_t T, int64_t V, float scale, Rows rows,
+                                                       Factors* __restrict__ out) {
   __shared__ float sm[1024];
-  float mh = 1.0f, mw = 1.0f, m = 0.0f;
-  if (parts) {
+  float mw = 1.0f;
+  if (D == kF32) {
     mw = power_for(max_of(parts[threadIdx.x], sm));
-    for (int64_t t = threadIdx.x; t < T; t += 1024) m = fmaxf(m, hm[t]);
-    mh = power_for(max_of(m, sm));
     for (int64_t t = threadIdx.x; t < T; t += 1024) {
       const float f = power_for(hm[t]);
       rows.hz[t] = f;
       rows.zs[t] = (float)((double)scale / f / mw);
-      if (dloss) rows.hw[t] = mh;
     }
   }
-  m = 0.0f;
-  if (dloss) {
-    for (int64_t t = threadIdx.x; t < T; t += 1024)
-      if (labels[t] >= 0) m = fmaxf(m, fabsf(dloss[t]));
-    m = max_of(m, sm);
+  if (!dloss) {
+    if (threadIdx.x == 0) out->mw = mw;
+    return;
+  }
+  // the largest of the finite ones
+  float m = 0.0f;
+  for (int64_t t = threadIdx.x; t < T; t += 1024) {
+    const float v = labels[t] >= 0 ? fabsf(dloss[t]) : 0.0f;
+    m = v < __builtin_inff() ? fmaxf(m, v) : m;
+  }
+  m = max_of(m, sm);
+  int x0 = 0;
+  if (m > 0.0f) frexpf(m, &x0);
+  // f and x of a token; x = x0 where dloss is 0 or not finite
+  auto parted = [&](int64_t t, int& x) {
+    x = x0;
+    const float l = dloss[t];
+    return l != 0.0f && fabsf(l) < __builtin_inff() ? frexpf(l, &x) : l;
+  };
+  // fp32: H's copy for dW, weighted by 2^(x - x0), to 2^15 at its largest
+  float mh = 1.0f;
+  if (D == kF32) {
+    float e = 0.0f;
     for (int64_t t = threadIdx.x; t < T; t += 1024) {
-      const int32_t label = labels[t];
-      const float w = m == 0.0f ? dloss[t] : dloss[t] / m * gs;   // (all zero, or NaN)
-      rows.wn[t] = label < 0 ? 0.0f : label < V ? w : __uint_as_float(0x7fc00000u);
+      int x;
+      if (labels[t] >= 0 && parted(t, x) != 0.0f) e = fmaxf(e, ldexpf(hm[t], x - x0));
     }
+    mh = power_for(max_of(e, sm));
   }
-  if (threadIdx.x == 0) {
-    const double f = (m == 0.0f ? 1.0 : (double)m) * (double)scale / (double)gs;
-    *out = Factors{mw, (float)(f / mw), (float)(f / mh)};
+  for (int64_t t = threadIdx.x; t < T; t += 1024) {
+    const int32_t label = labels[t];
+    float wn, pt, hw = 0.0f;
+    if (D == kBF16) {
+      wn = m == 0.0f ? dloss[t] : dloss[t] / m;   // (none is finite and not zero)
+      pt = m == 0.0f ? scale : m * scale;
+    } else {
+      int x;
+      const float f = parted(t, x);
+      const int k = D == kF16 ? min(x0 - x, kInG) : 0;
+      wn = ldexpf(f, 15 - k);
+      pt = scaled((double)scale / mw, x + k - 15);
+      hw = f == 0.0f ? 0.0f : ldexpf(mh, x + k - x0);
+    }
+    rows.wn[t] = label < 0 ? 0.0f : label < V ? wn : __uint_as_float(0x7fc00000u);
+    rows.pt[t] = label < 0 ? 0.0f : pt;
+    rows.hw[t] = label < 0 ? 0.0f : hw;
   }
+  if (threadIdx.x == 0)
+    *out = Factors{mw, D == kBF16 ? (m == 0.0f ? 1.0f : m) * scale : scaled((double)scale / mh, x0 - 15)};
 }
 
-// dH = post times the sum of nz slices (in order)
+// dH = each token's factor times the sum of nz slices (in order); zero for an
+// ignored token
 template <int D>
 __global__ __launch_bounds__(256) void dh_kernel(const float* __restrict__ part, int nz,
                                                  int64_t slice, int64_t ldp, int64_t T, int64_t d,
-                                                 const float* __restrict__ post,
+                                                 const int32_t* __restrict__ labels,
+                                                 const float* __restrict__ pt,
                                                  typename Elem<D>::type* __restrict__ out,
                                                  int64_t ldo) {
   const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  const float f = *post;
   if (c >= d) return;
   for (int64_t t = blockIdx.y; t < T; t += gridDim.y) {
+    const bool used = labels[t] >= 0;
+    const float f = pt[t];
     f32x4 s = *(const f32x4*)(part + t * ldp + c);
     for (int z = 1; z < nz; ++z) s += *(const f32x4*)(part + z * slice + t * ldp + c);
 #pragma unroll
     for (int v = 0; v < 4; ++v)
-      if (c + v < d) out[t * ldo + c + v] = Elem<D>::from(s[v] * f);
+      if (c + v < d) out[t * ldo + c + v] = Elem<D>::from(used ? s[v] * f : 0.0f);
   }
 }
 
 // ---------------------------------------------------------------- layout
-// out [row][term][kp] = the terms of X (rows x k) times a factor (fp32: *mul, or
-// with PER_ROW mul[row]), zero from k to kp, for rows past the last up to rp, and
-// for rows whose label is negative (labels nullable). Form z of the grid takes
-// mul + z * rows and the z-th copy of out.
-template <int D, bool PER_ROW>
+// out [row][term][kp] = the terms of X (rows x k) times a factor, zero from k to
+// kp, for rows past the last up to rp, and for rows whose label is negative (labels
+// nullable). Form z of the grid writes the z-th copy of out.
+enum Mul : int {
+  kAsIs = 0,      // 1
+  kOne = 1,       // *mul
+  kEachRow = 2,   // mul[z * rows + row]
+};
+template <int D, int M>
 __global__ __launch_bounds__(256) void pack_kernel(const typename Elem<D>::type* __restrict__ X,
                                                    int64_t rows, int64_t k, int64_t ld,
                                                    const int32_t* __restrict__ labels,
@@ -906,7 +956,7 @@ __global__ __launch_bounds__(256) void pack_kernel(const typename Elem<D>::type*
   for (int64_t r = blockIdx.y; r < rp; r += gridDim.y) {
     E e[8];
     const bool row = r < rows && (!labels || labels[r] >= 0);
-    const float f = D != kF32 ? 1.0f : !PER_ROW ? *mul : row ? mul[blockIdx.z * rows + r] : 0.0f;
+    const float f = M == kAsIs ? 1.0f : M == kOne ? *mul : row ? mul[blockIdx.z * rows + r] : 0.0f;
     if (row && c + 8 <= k) {
       __builtin_memcpy(e, X + r * ld + c, sizeof(e));
     } else {
@@ -916,8 +966,8 @@ __global__ __launch_bounds__(256) void pack_kernel(const typename Elem<D>::type*
     uint16_t q[8][terms(D)];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if constexpr (D == kF32)
-        split<D>(e[i] * f, q[i]);
+      if constexpr (M != kAsIs)
+        split<D>(Elem<D>::to(e[i]) * f, q[i]);
       else
         q[i][0] = __builtin_bit_cast(uint16_t, e[i]);
     }
@@ -958,21 +1008,20 @@ hipError_t mma_launch(const Mma& a, int tile, int slices, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int D, bool PER_ROW>
+template <int D, int M>
 hipError_t pack(const void* X, int64_t rows, int64_t k, int64_t ld, const int32_t* labels,
                 const float* mul, uint16_t* out, int64_t rp, int64_t kp, int forms, hipStream_t s) {
   const dim3 grid((unsigned)((kp / 8 + 255) / 256), (unsigned)std::min<int64_t>(rp, 16384),
                   (unsigned)forms);
-  hipLaunchKernelGGL((pack_kernel<D, PER_ROW>), grid, dim3(256), 0, s,
+  hipLaunchKernelGGL((pack_kernel<D, M>), grid, dim3(256), 0, s,
                      (const typename Elem<D>::type*)X, rows, k, ld, labels, mul, out, rp, kp);
   return hipGetLastError();
 }
 
-// The factors of a call (and wn with dloss), and H twice: for z, and with dloss
-// for dW. The rows of ignored tokens are zeroed, which dW's sums over the tokens
-// need; for the loss alone H stays in place where it can (an ignored token's
-// column of products is not used). fp32 has a copy of its own for each (a token's
-// power of two does not pass through dW's sums).
+// The factors of a call, and H twice: for z, in place where it can be (an ignored
+// token's column of products is not used), and with dloss for dW, whose sums over
+// the tokens need the rows of ignored ones zeroed and, but for bf16, each token's
+// weight in them. Copies that no product of the call reads are not made.
 template <int D>
 hipError_t begin(const Vocab& a, const Plan& p, const float* dloss, Opnd* Hz, Opnd* Hw,
                  hipStream_t s) {
@@ -981,30 +1030,36 @@ hipError_t begin(const Vocab& a, const Plan& p, const float* dloss, Opnd* Hz, Op
   float *hm = (float*)(w + p.hm), *amax = (float*)(w + p.amax);
   const Rows rows = rows_of(w, p, a.T);
   hipError_t e;
-  if (D != kF32 && !dloss && direct(a.H, a.ldh, a.d, D)) {
-    *Hz = Opnd{(const uint16_t*)a.H, a.ldh, 0, a.T, a.d};
-    return hipSuccess;
-  }
   if (D == kF32) {
     hipLaunchKernelGGL(amax_kernel, dim3(kAmaxParts, 2), dim3(256), 0, s, (const float*)a.H, a.T,
                        a.ldh, (const float*)a.W, a.V, a.ldw, a.d, a.labels, hm, amax);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (D == kF32 || dloss) {
-    hipLaunchKernelGGL(factors_kernel, dim3(1), dim3(1024), 0, s, hm, D == kF32 ? amax : nullptr,
-                       dloss, a.labels, a.T, a.V, D == kBF16 ? 1.0f : kTop16, a.scale, rows, fac);
+    hipLaunchKernelGGL(factors_kernel<D>, dim3(1), dim3(1024), 0, s, hm, amax, dloss, a.labels, a.T,
+                       a.V, a.scale, rows, fac);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
+  const bool dw = dloss && a.dW, score = dloss && few(a.T, a.d, D);
+  // (bf16 has one copy for both)
+  const bool z = !score && (!direct(a.H, a.ldh, a.d, D) || (D == kBF16 && dw));
   uint16_t* out = (uint16_t*)(w + p.hp);
-  const int n = dloss ? forms(D) : 1;
-  *Hz = Opnd{out, p.dp * terms(D), p.dp, a.T, p.dp};
-  *Hw = Opnd{out + (n - 1) * p.tp * p.dp * terms(D), p.dp * terms(D), p.dp, a.d, p.tp};
-  // (the copies that the call's products read, one behind the other)
-  const bool z = !dloss || !few(a.T, a.d, D), dw = dloss && a.dW;
-  const int from = z ? 0 : n - 1, to = dw ? n - 1 : 0;
-  if ((!z && !dw) || from > to) return hipSuccess;
-  return pack<D, true>(a.H, a.T, a.d, a.ldh, a.labels, rows.hz + from * a.T,
-                       out + from * p.tp * p.dp * terms(D), p.tp, p.dp, to - from + 1, s);
+  const int64_t copy = p.tp * p.dp * terms(D);
+  *Hz = z ? Opnd{out, p.dp * terms(D), p.dp, a.T, p.dp}
+          : Opnd{(const uint16_t*)a.H, a.ldh, 0, a.T, a.d};
+  *Hw = Opnd{out + (forms(D) - 1) * copy, p.dp * terms(D), p.dp, a.d, p.tp};
+  if constexpr (D == kF32) {   // the two copies, and their factors, lie behind each other
+    const int from = z ? 0 : 1, n = (int)z + (int)dw;
+    if (n == 0) return hipSuccess;
+    return pack<D, kEachRow>(a.H, a.T, a.d, a.ldh, a.labels, rows.hz + from * a.T,
+                             out + from * copy, p.tp, p.dp, n, s);
+  } else {
+    if (z || (D == kBF16 && dw))
+      if ((e = pack<D, kAsIs>(a.H, a.T, a.d, a.ldh, a.labels, nullptr, out, p.tp, p.dp, 1, s)) != hipSuccess)
+        return e;
+    if (D == kBF16 || !dw) return hipSuccess;
+    return pack<D, kEachRow>(a.H, a.T, a.d, a.ldh, a.labels, rows.hw, out + copy, p.tp, p.dp, 1, s);
+  }
 }
 // nv words of W from v0: in place, or a copy in the workspace
 template <int D>
@@ -1018,7 +1073,7 @@ hipError_t words(const Vocab& a, const Plan& p, int64_t v0, int64_t nv, Opnd* o,
   char* w = (char*)a.work;
   uint16_t* out = (uint16_t*)(w + p.wp);
   *o = Opnd{out, p.dp * terms(D), p.dp, nv, p.dp};
-  return pack<D, false>(W, nv, a.d, a.ldw, nullptr, &((Factors*)(w + p.fac))->mw, out, nv, p.dp, 1, s);
+  return pack<D, D == kF32 ? kOne : kAsIs>(W, nv, a.d, a.ldw, nullptr, &((Factors*)(w + p.fac))->mw, out, nv, p.dp, 1, s);
 }
 
 // score_kernel over nv words from v0 on
@@ -1136,7 +1191,7 @@ hipError_t backward(const Vocab& a, hipStream_t s) {
   if (a.dH) {
     const dim3 grid((unsigned)((a.d + 1023) / 1024), (unsigned)std::min<int64_t>(a.T, 16384));
     hipLaunchKernelGGL(dh_kernel<D>, grid, dim3(256), 0, s, (const float*)(w + p.part), p.nz, slice,
-                       ldp, a.T, a.d, &fac->post_h, (E*)a.dH, a.lddh);
+                       ldp, a.T, a.d, a.labels, rows.pt, (E*)a.dH, a.lddh);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return hipSuccess;

@@ -16,10 +16,10 @@ constexpr int kAmaxParts = 1024;
 // Factors of a call, read by the kernels that follow.
 struct Factors {
   float mw;              // power of two that W is scaled by (fp32, else 1)
-  float post_h, post_w;  // of dH and dW
+  float post_w;          // of dW
 };
-// copies of H that a gradient takes: for z and for dW
-constexpr int forms(int D) { return D == kF32 ? 2 : 1; }
+// copies of H that a gradient takes: for z and for dW (bf16: one for both)
+constexpr int forms(int D) { return D == kBF16 ? 1 : 2; }
 
 // Whether score_kernel takes a call. With more tokens mma_kernel reads W at a
 // higher rate although half of a tile is empty (4096 x 32000 bf16, 64 tokens: 94
@@ -101,7 +101,7 @@ inline Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad) {
   p.fac = take(sizeof(Factors));
   p.amax = take(4 * kAmaxParts);
   p.hm = take(4 * T);
-  p.rows = take(4 * 4 * T);
+  p.rows = take(4 * 5 * T);
   p.hp = take(2 * nt * p.tp * p.dp * (grad ? forms(dtype) : 1));
   p.wp = take(2 * nt * p.piece * p.dp);
   if (grad) {

@@ -170,3 +170,75 @@ def test_a_loud_token_costs_the_others_nothing(gpu, T):
     without, _ = nq.vocab_loss(L.H, L.W, L.labels)
     assert torch.equal(without[rest], loss[rest])
     L.check_grad(*nq.vocab_loss_backward(L.H, L.W, L.labels, loud[1], L.dl))
+
+
+def check_rows_of_dh(L, dH):
+    """dH's rows to bounds that scale with the row's own dloss, as in
+    Head.check_grad but for what is left of G's range: fp16 terms of G hold
+    (p - [label]) f 2^15 with 1/2 <= |f| < 1, so a probability to 2^-25 of 2^14
+    at least, 2^-39; fp16 keeps up to 10 bits of the tokens' differences in it,
+    2^-29; bf16's exponents reach further than any of these. W's terms hold
+    2^-39 of its largest."""
+    from oracle import tuning as O
+    from test_gpu_tuning import H as host, half, least
+    lab, h, V = L.labels.cpu().numpy(), half(L.name), L.W.shape[0]
+    use = lab >= 0
+    Hh, W, dl = host(L.H), host(L.W), host(L.dl)
+    Hh[~use] = 0
+    want, _, G = O.vocab_loss_backward(Hh, W, lab, dl, L.scale)
+    size = np.abs(dl[use])[:, None] * abs(L.scale)
+    ez = L.zbound()[use]
+    p = np.exp(L.scale * Hh[use] @ W.T - O.vocab_loss(Hh, W, lab, L.scale)[1][use][:, None])
+    ee = ez + ez.max(1, keepdims=True) + (V + 16) * U + 16 * U * np.abs(np.log(np.maximum(p, 1e-30)))
+    eg = p * (np.expm1(ee) + 8 * U) * size + (h + 4 * U) * np.abs(G)
+    eg += {"float32": 2.0 ** -39, "float16": 2.0 ** -29, "bfloat16": 0.0}[L.name] * size
+    more = 2.0 ** -22 if L.name == "float32" else 0.0
+    tol = eg @ np.abs(W) + ((V + 40) * U + more) * ((np.abs(G) + eg) @ np.abs(W))
+    if L.name == "float32":
+        tol += V * 2.0 ** -38 * size * np.abs(W).max()
+    got = host(dH)
+    np.testing.assert_array_less(np.abs(got[use] - want[use]),
+                                 1.01 * tol + h * np.abs(want[use]) + least(L.name))
+    assert (got[~use] == 0).all()
+
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("T, V", [(9, 400), (30, 5000), (64, 700), (70, 5000), (300, 700)])
+def test_a_token_of_small_weight_keeps_its_gradient(gpu, name, T, V):
+    """dloss from 1 to 1e-7 of the largest: each row of dH is as exact as if it
+    were alone. (fp16's subnormals end at 2^-24: its dloss are 2^10 times as
+    large, so that what is asked for can be written.)"""
+    import sub_bit_weight_lb_amd as nq
+    print(f"case T={T} V={V} {name}", flush=True)
+    L = Head(51, T, V, 96, name, gpu)
+    _, lse = nq.vocab_loss(L.H, L.W, L.labels)
+    for k in range(T):
+        L.dl[k] = (-1.0) ** k * 10.0 ** -(k % 8) * (1.0 + 0.1 * (k % 5)) * (1024 if name == "float16" else 1)
+    dH, dW = nq.vocab_loss_backward(L.H, L.W, L.labels, lse, L.dl)
+    check_rows_of_dh(L, dH)
+    L.check_grad(None, dW)
+    only, none = nq.vocab_loss_backward(L.H, L.W, L.labels, lse, L.dl, want_dW=False)
+    assert none is None and (only == dH).all()
+    none, only = nq.vocab_loss_backward(L.H, L.W, L.labels, lse, L.dl, want_dH=False)
+    assert none is None and (only == dW).all()
+
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("T", [9, 70])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_a_dloss_that_is_not_finite_stays_in_its_row(gpu, name, T, bad):
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    L = Head(52, T, 400, 64, name, gpu, ignored=0.0)
+    _, lse = nq.vocab_loss(L.H, L.W, L.labels)
+    L.dl[2] = 0.0
+    want, _ = nq.vocab_loss_backward(L.H, L.W, L.labels, lse, L.dl)
+    assert (want[2] == 0).all()
+    L.dl[2] = bad
+    dH, dW = nq.vocab_loss_backward(L.H, L.W, L.labels, lse, L.dl)
+    rest = [t for t in range(T) if t != 2]
+    assert torch.equal(dH[rest], want[rest])
+    assert not torch.isfinite(dH[2]).any() and not torch.isfinite(dW).all()
+    L.dl.fill_(bad)
+    dH, _ = nq.vocab_loss_backward(L.H, L.W, L.labels, lse, L.dl)
+    assert not torch.isfinite(dH).any()
