@@ -28,7 +28,7 @@ constexpr int forms(int D) { return D == kBF16 ? 1 : 2; }
 inline bool few(int64_t T, int64_t d, int dtype) { return d >= 8 && T <= (dtype == kF32 ? 64 : 32); }
 
 struct Plan {
-  int64_t dp, tp;              // d to 64, T to 256
+  int64_t dp, tp;              // d to 64, T to 256 (few tokens: to 64)
   int64_t piece, npieces;      // words of a piece, to 256; pieces
   int nz;                      // slices of dH, each with a share of the first piece
   int64_t kz;                  // words per slice, to 64
@@ -74,8 +74,8 @@ inline Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad) {
   Plan p{};
   const int nt = terms(dtype);
   p.dp = round_up(d, BK);
-  p.tp = round_up(T, 256);
-  const int64_t most = std::max<int64_t>(2048, (int64_t(1) << 26) / std::max(T, d) / 256 * 256);
+  p.tp = round_up(T, few(T, d, dtype) ? BK : 256);
+  const int64_t most = std::max<int64_t>(2048, (int64_t(1) << 26) / std::max(p.tp, p.dp) / 256 * 256);
   p.npieces = (V + most - 1) / most;
   p.piece = round_up((V + p.npieces - 1) / p.npieces, 256);
   p.npieces = (V + p.piece - 1) / p.piece;

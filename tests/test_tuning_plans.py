@@ -55,7 +55,7 @@ def log_uniform(rng, lo, hi):
 def vocab_plan(tmp_path_factory):
     return compile_plan(tmp_path_factory.mktemp("vocab"), "vocab_plan.h", """
     const vocab::Plan p = vocab::plan_for(x[0], x[1], x[2], (int)x[3], true);
-    out = {p.piece, p.npieces, p.nz, p.kz, p.part, p.bytes};""")
+    out = {p.piece, p.npieces, p.nz, p.kz, p.part, p.bytes, p.tp, p.dp, p.wp, p.G};""")
 
 
 # (tokens, words, columns) whose last slice of dH, in a vocabulary rounded up to
@@ -71,13 +71,42 @@ def test_the_first_piece_writes_every_slice_of_dh(vocab_plan):
     shapes = SHORT + [(log_uniform(rng, 1, 8192), log_uniform(rng, 1, 1 << 18), log_uniform(rng, 1, 16384))
                       for _ in range(20000)]
     rows = [s + (t,) for s in shapes for t in range(3)]
-    for (T, V, d, t), (piece, npieces, nz, kz, part, total) in zip(rows, vocab_plan(rows)):
+    for (T, V, d, t), (piece, npieces, nz, kz, part, total, *_) in zip(rows, vocab_plan(rows)):
         assert piece % 256 == 0 and (npieces - 1) * piece < V <= npieces * piece
         assert kz % 64 == 0 and nz >= 1
         share = [-(-(-(-min(piece, V - v0) // 64) * 64) // kz) for v0 in range(0, V, piece)]
         assert share[0] == nz, (T, V, d, t)
         assert max(share) == nz
         assert total - part >= 4 * nz * T * (-(-d // 4) * 4)
+
+
+def test_pieces_of_the_vocabulary_bound_the_workspace(vocab_plan):
+    """G and the copy of W's piece, as they lie there (tokens and columns rounded
+    up), hold at most 2^26 values each per term, but for pieces of 2048 words,
+    the least; tokens are rounded up to the products' 256 rows, or 64 where
+    score_kernel writes G."""
+    rng = random.Random(3)
+    shapes = [(1, 1 << 24, 64), (1, 1 << 24, 1), (1, 1 << 24, 8), (64, 1 << 24, 64), (65, 1 << 24, 64),
+              (1, 1 << 24, 1 << 18), (1 << 14, 1 << 24, 64)]
+    shapes += [(log_uniform(rng, 1, 1 << 20), log_uniform(rng, 1, 1 << 18), log_uniform(rng, 1, 1 << 18))
+               for _ in range(5000)]
+    rows = [s + (t,) for s in shapes for t in range(3)]
+    for (T, V, d, t), (piece, _, _, _, part, _, tp, dp, wp, G) in zip(rows, vocab_plan(rows)):
+        terms = 2 if t == 0 else 1
+        few = d >= 8 and T <= (64 if t == 0 else 32)
+        assert tp == -(-T // (64 if few else 256)) * (64 if few else 256) and dp == -(-d // 64) * 64
+        assert piece <= max(2048, (1 << 26) // max(tp, dp))
+        assert G - wp >= 2 * terms * piece * dp and part - G >= 2 * terms * piece * tp
+
+
+def test_the_workspace_of_one_token_is_not_that_of_many():
+    """Documented sizes: one token and a vocabulary of 2^24 words."""
+    import sub_bit_weight_lb_amd as nq
+    import torch
+    for d in (1, 8, 64):
+        got = nq.vocab_loss_work_bytes(1, 1 << 24, d, torch.float32, True)
+        # two terms of 2 bytes for 2^26 values of G and of W; the rest is small
+        assert got <= 2 * 4 * (1 << 26) + (1 << 24), (d, got)
 
 
 # ---------------------------------------------------------------- packed layer's gradient
