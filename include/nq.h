@@ -432,7 +432,8 @@ int64_t nq_binary_matmul_backward_work_bytes(int64_t T, int64_t m, int64_t n, in
  * (device float32, T each). A negative label is ignored: its loss and lse are
  * 0 and its row of H is not used (it may hold anything); a label >= V gives
  * NaN (the library does not read labels on the host). A NaN or an infinity in
- * a row of H gives NaN in its loss, in W in every loss it takes part in.
+ * a row of H gives NaN in its loss, in W in every loss that is not ignored (so
+ * does a logit that overflows float32, to either side).
  * work: nq_vocab_loss_work_bytes(T, V, d, dtype, 0) bytes of device scratch,
  * 16-byte aligned. All on `stream`, no allocation; sums run in a fixed order.
  * T == 0 is a no-op. T <= 2^20, V <= 2^24, T V <= 2^38, d <= 2^18, strides <=

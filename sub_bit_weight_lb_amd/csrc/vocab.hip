@@ -406,13 +406,14 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
       const int64_t t = c0 + 16 * j;
       const int32_t label = t < N ? a.labels[t] : -1;
       const float zs = D == kF32 ? (t < N ? a.zs[t] : 0.0f) : a.z0;
-      float top = kNegInf;
+      float top = kNegInf, low = 0.0f;
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           acc[i][j][v] *= zs;
           if (16 * i + v < left) top = fmaxf(top, acc[i][j][v]);
+          low = fminf(low, acc[i][j][v]);   // (0 for rows past the last word)
         }
       const int at = own(label);
       if (at >= 0 && at < left) {   // (one lane of all tiles: no branch per element)
@@ -431,6 +432,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
 #pragma unroll
         for (int v = 0; v < 4; ++v)
           sum += 16 * i + v < left ? __expf(acc[i][j][v] - top) : 0.0f;
+      sum = low == kNegInf ? __uint_as_float(0x7fc00000u) : sum;   // (an infinity in W: exp makes it 0)
       sum += __shfl_xor(sum, 16);
       sum += __shfl_xor(sum, 32);
       if (g == 0 && t < N) {
@@ -667,7 +669,8 @@ __global__ __launch_bounds__(1024 / NT)
       m = fmaxf(m, __shfl_xor(m, 32));
       float s = 0.0f;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) s += w + v < V ? __expf(x[v] - m) : 0.0f;
+      for (int v = 0; v < 4; ++v)   // (-infinity, of an infinity in W, is no zero but NaN)
+        s += w + v >= V ? 0.0f : x[v] == kNegInf ? __uint_as_float(0x7fc00000u) : __expf(x[v] - m);
       s += __shfl_xor(s, 16);
       s += __shfl_xor(s, 32);
       if (g == 0) {

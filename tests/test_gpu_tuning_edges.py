@@ -242,3 +242,22 @@ def test_a_dloss_that_is_not_finite_stays_in_its_row(gpu, name, T, bad):
     L.dl.fill_(bad)
     dH, _ = nq.vocab_loss_backward(L.H, L.W, L.labels, lse, L.dl)
     assert not torch.isfinite(dH).any()
+
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("T, V, d", [(9, 300, 64), (40, 300, 129), (70, 300, 64), (300, 1200, 200)])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_a_word_that_is_not_finite_shows_in_every_loss(gpu, name, T, V, d, bad):
+    """Also where its logit is -infinity, which exp would make a zero."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    L = Head(61, T, V, d, name, gpu)
+    L.labels[L.labels == 7] = 8
+    L.W[7, 5] = bad
+    used = L.labels >= 0
+    assert (L.H[used, 5] > 0).any() and (L.H[used, 5] < 0).any()
+    loss, lse = nq.vocab_loss(L.H, L.W, L.labels)
+    assert loss[used].isnan().all() and lse[used].isnan().all()
+    assert (loss[~used] == 0).all() and (lse[~used] == 0).all()
+    dH, dW = nq.vocab_loss_backward(L.H, L.W, L.labels, lse, L.dl)
+    assert dH[used].isnan().all() and (dH[~used] == 0).all() and dW.isnan().all()
