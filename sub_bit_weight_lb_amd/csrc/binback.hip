@@ -478,6 +478,8 @@ __global__ __launch_bounds__(256, 2) void wide_kernel(Prod a0, Prod a1) {
   // among the loads of digits and the waits.
   auto copy = [&](int64_t sb, int c, bool live) {
     const int st = to + (int)(sb & 1) * 16 * NJ * kFour;
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"   // (m0 is reserved: nothing is kept in it across)
     asm volatile(
         "s_mov_b32 s92, %0\n\t"
         "s_mov_b32 s93, %1\n\t"
@@ -489,7 +491,8 @@ __global__ __launch_bounds__(256, 2) void wide_kernel(Prod a0, Prod a1) {
         :
         : "s"(lo), "s"(hi), "s"(live ? size : 0), "s"(st), "i"(c * kFour * 4),
           "v"(from + ((uint32_t)sb * 64 + c * four))
-        : "s92", "s93", "s94", "s95", "scc");
+        : "m0", "s92", "s93", "s94", "s95", "scc");
+#pragma clang diagnostic pop
   };
   // the wave's digits: MI rows of blocks, nkb blocks apart (rows past T hold no
   // digits of the call: whatever they give is dropped at the end)

@@ -227,6 +227,8 @@ struct Tile {
   // for it, though it is for the next stage. It writes no register, sync()
   // waits for it, and it keeps its place among the reads and sync()s.
   __device__ __forceinline__ void put(int c) const {
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"   // (m0 is reserved: nothing is kept in it across)
     asm volatile(
         "s_mov_b32 s92, %0\n\t"
         "s_mov_b32 s93, %1\n\t"
@@ -237,7 +239,8 @@ struct Tile {
         "buffer_load_dwordx4 %5, s[92:95], 0 offen lds"
         :
         : "s"(lo), "s"(hi), "s"(n), "s"(to), "i"(c * 1024), "v"(o[kind(c)] + c * step)
-        : "s92", "s93", "s94", "s95", "scc");
+        : "m0", "s92", "s93", "s94", "s95", "scc");
+#pragma clang diagnostic pop
   }
 };
 // Fragments of the N 16-row groups from group g0 on, half h (32 k) of a stage.

@@ -143,3 +143,25 @@ def test_the_digit_planes_cover_what_the_products_read(layer_plan):
                     groups = -(-T // (2 * wave_rows)) * 2 * wave_rows // 16
                 assert 16 * groups >= T
                 assert at[c] + groups * group <= end[c] <= total, (m, n, r, T)
+
+
+# ---------------------------------------------------------------- inline assembly
+
+def test_assembly_names_the_registers_that_it_writes():
+    """Each scalar register that a block of assembly names as a destination is
+    among its clobbers, m0 and the carry of a scalar add too."""
+    import re
+    blocks = 0
+    for name in sorted(os.listdir(CSRC)):
+        if not name.endswith((".hip", ".h")):
+            continue
+        text = open(os.path.join(CSRC, name)).read()
+        for block in re.findall(r"asm\s+volatile\s*\((.*?)\);", text, re.S):
+            code = "".join(re.findall(r'"([^"]*)"', block)).replace("\\n", " ").replace("\\t", " ")
+            writes = set(re.findall(r"\bs_(?:mov|add|sub|or|and|lsh[lr])\w*\s+(m0|s\d+)\b", code))
+            if re.search(r"\bs_(?:add|sub|or|and|lsh[lr])\w*\s", code):
+                writes.add("scc")
+            named = set(re.findall(r'"(m0|s\d+|scc)"', block))
+            assert writes <= named, (name, writes - named)
+            blocks += bool(writes)
+    assert blocks >= 2
