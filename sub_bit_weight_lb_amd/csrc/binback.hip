@@ -152,10 +152,11 @@ struct Digits {
 };
 
 // The step of a row whose largest magnitude has the bits mx:
-// max|v| = 1.f 2^(E - 127) <= 127.5 256^(ND - 1) 2^e.
+// max|v| = 1.f 2^(E - 127) <= 127.5 256^(ND - 1) 2^e; 2^-149, of which every fp32
+// value is a multiple, at least.
 template <int ND>
 __device__ __forceinline__ int row_exponent(uint32_t mx) {
-  return max((int)(mx >> 23) - 127 - (8 * ND - 2) + ((mx & 0x7fffffu) > kTopMant), -126);
+  return max((int)(mx >> 23) - 127 - (8 * ND - 2) + ((mx & 0x7fffffu) > kTopMant), -149);
 }
 // out[k] = byte k of u[0], u[1], u[2], u[3]
 __device__ __forceinline__ void transpose_bytes(const uint32_t (&u)[4], uint32_t (&out)[4]) {
@@ -172,11 +173,11 @@ __device__ __forceinline__ void transpose_bytes(const uint32_t (&u)[4], uint32_t
 // added to each digit's place the bytes of an integer are its balanced digits
 // plus 128.
 template <int ND>
-__device__ __forceinline__ void to_digits(const float (&x)[4], float inv, uint32_t (&out)[4]) {
+__device__ __forceinline__ void to_digits(const float (&x)[4], int e, uint32_t (&out)[4]) {
   constexpr uint32_t kBias = ND == 4 ? 0x80808080u : 0x00808080u;
   uint32_t u[4];
 #pragma unroll
-  for (int d = 0; d < 4; ++d) u[d] = ((uint32_t)(int)rintf(x[d] * inv) + kBias) ^ 0x80808080u;
+  for (int d = 0; d < 4; ++d) u[d] = ((uint32_t)(int)rintf(ldexpf(x[d], -e)) + kBias) ^ 0x80808080u;
   transpose_bytes(u, out);
 }
 
@@ -248,7 +249,6 @@ __global__ __launch_bounds__(512) void rows_kernel(S0 s0, S1 s1, int64_t T, Digi
   }
   const bool bad = mx >= 0x7f800000u;
   const int e = row_exponent<ND>(mx);
-  const float inv = bad ? 0.0f : __uint_as_float((uint32_t)(127 - e) << 23);
   int sum[ND];
 #pragma unroll
   for (int p = 0; p < ND; ++p) sum[p] = 0;
@@ -268,7 +268,7 @@ __global__ __launch_bounds__(512) void rows_kernel(S0 s0, S1 s1, int64_t T, Digi
   auto write = [&](int64_t ch, float (&x)[4]) {
     if (bad) x[0] = x[1] = x[2] = x[3] = 0.0f;
     uint32_t dig[4];
-    to_digits<ND>(x, inv, dig);
+    to_digits<ND>(x, e, dig);
 #pragma unroll
     for (int p = 0; p < ND; ++p)
       sum[p] = __builtin_amdgcn_sdot4((int)dig[p], 0x01010101, sum[p], false);
@@ -313,7 +313,7 @@ __global__ __launch_bounds__(512) void rows_kernel(S0 s0, S1 s1, int64_t T, Digi
       for (int p = 0; p < ND; ++p) sum[p] += wsum[w][p];
   }
   if (lane == 0 && in) {
-    o.steps[row] = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(e + 127) << 23);
+    o.steps[row] = bad ? __uint_as_float(0x7fc00000u) : ldexpf(1.0f, e);
     i32x4 v = {0, 0, 0, 0};
 #pragma unroll
     for (int p = 0; p < ND; ++p) v[p] = sum[p];

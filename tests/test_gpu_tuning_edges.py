@@ -49,6 +49,24 @@ def test_layer_gradient_in_a_workspace_of_nans(gpu, name, T, m, n, r):
     L.check(*nq.binary_matmul_backward(*L.args(), work=work))
 
 
+@pytest.mark.parametrize("T", [6, 50, 150, 600])
+@pytest.mark.parametrize("down", [60, 90, 100])
+def test_layer_gradient_of_small_numbers(gpu, T, down):
+    """fp32 gradients and activations 2^-down as large: rows keep all digits of
+    their fixed point until fp32's own subnormals, 2^-149, end them. (dY and the
+    values of X are 2^-7 and 1, s1 and s2 2^-6: at 2^-100 the products s1 dY begin
+    to be subnormal, off by 2^-150 each, 2^-37 of a row's largest.)"""
+    import sub_bit_weight_lb_amd as nq
+    print(f"case T={T} 2^-{down}", flush=True)
+    L = Layer(T, T, 200, 300, 70, "float32", gpu)
+    L.dY *= 2.0 ** -down
+    L.check(*nq.binary_matmul_backward(*L.args()))
+    L = Layer(T, T, 200, 300, 70, "float32", gpu)
+    L.q.exps -= down
+    L.x = L.x * 2.0 ** -down
+    L.check(*nq.binary_matmul_backward(*L.args()))
+
+
 # ---------------------------------------------------------------- the loss and its gradient together
 
 U = 2.0 ** -24
