@@ -742,7 +742,7 @@ __global__ __launch_bounds__(1024) void stat_kernel(const float* __restrict__ to
 
 // Factors of each token, read by the kernels that follow.
 struct Rows {
-  float *hz, *hw;        // powers of two that its row of H is scaled by, for z (fp32) and for dW
+  float *hz, *hw;        // powers of two that its row of H is scaled by, for z and for dW
   float *zs;             // scale / (hz mw): of its products (fp32)
   float *wn, *pt;        // of G, of its row of dH
 };
@@ -912,6 +912,7 @@ __global__ __launch_bounds__(1024) void factors_kernel(const float* __restrict__
     rows.wn[t] = label < 0 ? 0.0f : label < V ? wn : __uint_as_float(0x7fc00000u);
     rows.pt[t] = label < 0 ? 0.0f : pt;
     rows.hw[t] = label < 0 ? 0.0f : hw;
+    if (D == kF16) rows.hz[t] = 1.0f;
   }
   if (threadIdx.x == 0)
     *out = Factors{mw, D == kBF16 ? (m == 0.0f ? 1.0f : m) * scale : scaled((double)scale / mh, x0 - 15)};
@@ -1054,17 +1055,15 @@ hipError_t begin(const Vocab& a, const Plan& p, const float* dloss, Opnd* Hz, Op
   *Hz = z ? Opnd{out, p.dp * terms(D), p.dp, a.T, p.dp}
           : Opnd{(const uint16_t*)a.H, a.ldh, 0, a.T, a.d};
   *Hw = Opnd{out + (forms(D) - 1) * copy, p.dp * terms(D), p.dp, a.d, p.tp};
-  if constexpr (D == kF32) {   // the two copies, and their factors, lie behind each other
+  if (!z && !dw) return hipSuccess;
+  if constexpr (D != kF32) {
+    if (D == kBF16 || !dw)
+      return pack<D, kAsIs>(a.H, a.T, a.d, a.ldh, a.labels, nullptr, out, p.tp, p.dp, 1, s);
+  }
+  if constexpr (D != kBF16) {   // the two copies, and their factors, lie behind each other
     const int from = z ? 0 : 1, n = (int)z + (int)dw;
-    if (n == 0) return hipSuccess;
     return pack<D, kEachRow>(a.H, a.T, a.d, a.ldh, a.labels, rows.hz + from * a.T,
                              out + from * copy, p.tp, p.dp, n, s);
-  } else {
-    if (z || (D == kBF16 && dw))
-      if ((e = pack<D, kAsIs>(a.H, a.T, a.d, a.ldh, a.labels, nullptr, out, p.tp, p.dp, 1, s)) != hipSuccess)
-        return e;
-    if (D == kBF16 || !dw) return hipSuccess;
-    return pack<D, kEachRow>(a.H, a.T, a.d, a.ldh, a.labels, rows.hw, out + copy, p.tp, p.dp, 1, s);
   }
 }
 // nv words of W from v0: in place, or a copy in the workspace
