@@ -358,11 +358,13 @@ nq_status nq_ste_destroy(nq_ste_t h);
 
 /* ---- tuning a packed model ----
  * The digest's stage 3 (方法步骤详情) freezes the binary factors and tunes the
- * scales of the whole model against a loss on its outputs. What follows is
- * what one layer of that needs beside nq_binary_matmul: its input kept in 8
- * bits for the backward pass, and its gradient from there; and the loss over
- * the model's vocabulary with its gradient. Outputs and work must not overlap
- * the inputs or each other. */
+ * scales of the whole model. What follows is what one layer of that needs beside
+ * nq_binary_matmul: its input kept in 8 bits for the backward pass, and its
+ * gradient from there; and the cross entropy of the model's outputs against
+ * labels, by which a packed model is scored or tuned, with its gradient. (The
+ * stage's own objective, the KL divergence from the original model's outputs, takes
+ * a distribution in the labels' place and is not among them.) Outputs and work
+ * must not overlap the inputs or each other. */
 
 /* Element types of tensors that are not always float32. */
 typedef enum nq_dtype { NQ_F32 = 0, NQ_BF16 = 1, NQ_F16 = 2 } nq_dtype;
@@ -436,6 +438,9 @@ int64_t nq_binary_matmul_backward_work_bytes(int64_t T, int64_t m, int64_t n, in
  * does a logit that overflows float32, to either side).
  * work: nq_vocab_loss_work_bytes(T, V, d, dtype, 0) bytes of device scratch,
  * 16-byte aligned. All on `stream`, no allocation; sums run in a fixed order.
+ * float32 operands of more than 64 tokens are taken to 2^-24 of an element or
+ * 2^-39 of the largest of its row of H, or of all of W: a word far louder than
+ * the rest costs those bits, a token does not.
  * T == 0 is a no-op. T <= 2^20, V <= 2^24, T V <= 2^38, d <= 2^18, strides <=
  * 2^21. */
 nq_status nq_vocab_loss(const void* H, int64_t ldh, const void* W, int64_t ldw, int32_t dtype,
@@ -443,15 +448,20 @@ nq_status nq_vocab_loss(const void* H, int64_t ldh, const void* W, int64_t ldw, 
                         float* loss, float* lse, void* work, void* stream);
 
 /* Gradient of sum_t dloss_t loss_t from the lse of nq_vocab_loss on the same
- * H, W, labels and scale: with
+ * H, W, labels and scale (the same tokens in one call: with another number of them
+ * the logits can be summed in another order, and the probabilities of lse and of
+ * the gradient then differ by its rounding): with
  *   G_tv = (exp(z_tv - lse_t) - [v == labels[t]]) dloss_t scale,
  *   dH (T x d, row stride lddh) = G W,   dW (V x d, row stride lddw) = G^T H
  * in H's type, written (not added to); one of them may be NULL. The logits are
  * computed again, a piece of the vocabulary at a time; G is rounded once to
- * H's type (float32: kept whole). Ignored tokens get zero rows of dH and add
- * nothing to dW, whatever their dloss; a label >= V gives NaN in its row of
- * dH and in dW. work: nq_vocab_loss_work_bytes(T, V, d, dtype, 1) bytes,
- * 16-byte aligned. T == 0 is a no-op with dW == NULL and an error with it. */
+ * H's type (float32: to 2^-24 of itself or 2^-39 of dloss_t scale), each token's
+ * by itself, and for dW H to 2^-39 of the largest |dloss_t H_tc| in float32; in
+ * float16 tokens of a dloss below 2^-10 of the largest scale theirs down, to
+ * float16's subnormals. Ignored tokens get zero rows of dH and add nothing to dW,
+ * whatever their dloss; a label >= V gives NaN in its row of dH and in dW, a
+ * dloss that is not finite in no other row of dH. work:
+ * nq_vocab_loss_work_bytes(T, V, d, dtype, 1) bytes, 16-byte aligned. T == 0 is a no-op with dW == NULL and an error with it. */
 nq_status nq_vocab_loss_backward(const void* H, int64_t ldh, const void* W, int64_t ldw,
                                  int32_t dtype, int64_t T, int64_t V, int64_t d,
                                  const int32_t* labels, float scale, const float* lse,

@@ -4,8 +4,10 @@ from such a checkpoint, and softmax cross entropy over a vocabulary with its
 gradient. float64 NumPy; it shares no code with the GPU library.
 
 Source: the digest's section 方法步骤详情, stage 3 (the binary factors are
-frozen and the scales tuned against a loss on the model's outputs); the pages
-give no formulas, so these are the plain ones:
+frozen and the scales tuned, there by the KL divergence from the original
+model's outputs); the pages give no formula of a layer's gradient, nor of
+checkpoints and of the cross entropy against labels that a model is scored by,
+so these are the plain ones:
 
     checkpoint   e = least integer with max|x| <= 127 2^e over 32 columns of a
                  row, clamped to -126 .. 121 (9 for float16); c = x / 2^e to

@@ -644,7 +644,7 @@ def vocab_loss(H, W, labels, scale=1.0, loss=None, lse=None, work=None, stream=N
 def vocab_loss_backward(H, W, labels, lse, dloss, scale=1.0, want_dH=True, want_dW=True, dH=None,
                         dW=None, work=None, stream=None):
     """Gradient of sum(dloss * loss) for vocab_loss(H, W, labels, scale), from
-    its lse: returns (dH, dW) in H's type (None where not wanted). lse and
+    its lse (of one call with these tokens): returns (dH, dW) in H's type (None where not wanted). lse and
     dloss are T float32. The logits are computed again in pieces of the
     vocabulary. Ignored tokens (negative labels) get zero rows of dH and add
     nothing to dW. Outputs must not share memory with inputs. work, if given,

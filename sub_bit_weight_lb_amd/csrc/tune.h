@@ -105,7 +105,7 @@ struct Vocab {
   const float* dloss;                // T (gradient)
   void *dH, *dW;                     // T x d, V x d (gradient; either nullable)
   int64_t lddh, lddw;
-  void* work;                        // vocab_work_bytes, 256-byte aligned
+  void* work;                        // vocab_work_bytes, 16-byte aligned
 };
 int64_t vocab_work_bytes(int64_t T, int64_t V, int64_t d, int dtype, bool grad);
 hipError_t launch_vocab_loss(const Vocab& a, hipStream_t s);

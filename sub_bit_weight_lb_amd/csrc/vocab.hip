@@ -24,18 +24,19 @@
 // k runs down the rows (W in kDh, H and G in kDw) is transposed on its way from
 // LDS to the registers, by ds_read_b64_tr_b16.
 //
-// Types: bf16 and fp16 operands are exact and sums are fp32; G is rounded to
-// the operands' type once (half a unit, like the results; bf16's dH and dW are
-// then off by about a tenth more than by their own rounding). fp16 and fp32 G hold
-// (p - [label]) of each token to 2^15 at its largest whatever the others' dloss
-// are (fp16: from 2^-10 of the largest dloss on), so that probabilities down to
-// 2^-29 keep all their bits; dloss itself enters at the end of dH's row and,
-// as a power of two, in a copy of H for dW. fp32 operands are scaled by powers of
-// two (each row of H, all of H's copy for dW, W to 2^15 at their largest) and
-// split into two fp16 terms x = h + l,
-// which hold x to 2^-24 of itself or 2^-39 of the largest; x y = h l + l h + h h, three passes
-// over k, leaves out l l, at most 2^-24 of the product. (Three bf16 terms and
-// six passes measured 1.9 times the time at no smaller error.)
+// Types: bf16 and fp16 operands are exact and sums are fp32. G is rounded to the
+// operands' type once: half a unit, like the results, so that dH and dW are off by
+// about a tenth more than by their own rounding (relative to the exact gradient
+// 0.0017 for the plain form and 0.0018 to 0.0019 here in bf16; a second term of G
+// would double two of the four products). bf16's G holds (p - [label]) dloss of the
+// largest dloss 1; fp16's and fp32's hold p - [label] of each token to 2^15,
+// whatever the others' dloss (fp16: with dloss to 2^-10 of the largest), so that
+// probabilities down to 2^-29 keep all their bits. fp32 operands are scaled by powers
+// of two (each row of H, all of H's copy for dW, W: to 2^15 at their largest) and
+// split into two fp16 terms x = h + l, which hold x to 2^-24 of itself or 2^-39
+// of the largest; x y = h l + l h + h h, three passes over k, leaves out l l, at
+// most 2^-24 of the product. (Three bf16 terms and six passes measured 1.9 times
+// the time at no smaller error.)
 //
 // Few tokens (up to 32, fp32 up to 64): score_kernel takes kStat's and kGrad's
 // place. It streams W once, 64 words per workgroup, its waves sharing the
@@ -95,9 +96,8 @@ __device__ __forceinline__ void split(float x, uint16_t (&t)[terms(D)]) {
 
 // A 16-bit operand of the products, `ld` apart, its terms `plane` apart within
 // a row. k-contiguous: `rows` rows of k values. k-major: k runs down the rows
-// and `rows` counts the columns. kv: the k that exist (past them a
-// k-contiguous operand reads zeros, a k-major one its last row, which meets
-// zeros of the other).
+// and `rows` counts the columns. kv: the k that exist (past them
+// an operand reads zeros).
 struct Opnd {
   const uint16_t* p;
   int64_t ld, plane, rows, kv;
@@ -844,8 +844,9 @@ __device__ __forceinline__ float scaled(double value, int e) { return (float)lde
 //   bf16:       G = (p - [label]) dloss / max|dloss|: its exponents reach far enough;
 //   fp32:       G = (p - [label]) f 2^15 whatever the others' dloss are, dH's row
 //               takes 2^(x - 15) at its end, and H's copy for dW 2^(x - x0);
-//   fp16:       as fp32, but G keeps up to kInG bits of x - x0, as H, which is not
-//               scaled to its type's top, has fewer to give.
+//   fp16:       as fp32, but G keeps up to kInG bits of x - x0: it has 29 below its
+//               top, of which 11 are asked for, where H, which is not scaled to its
+//               type's top, has 14 where it is about 1.
 // (0 for an ignored token; NaN for a label at or past V.) hm and parts (fp32
 // operands): the maxima of H's rows and of W. One workgroup.
 constexpr int kInG = 10;
