@@ -455,8 +455,8 @@ nq_status nq_vocab_loss(const void* H, int64_t ldh, const void* W, int64_t ldw, 
  *   dH (T x d, row stride lddh) = G W,   dW (V x d, row stride lddw) = G^T H
  * in H's type, written (not added to); one of them may be NULL. The logits are
  * computed again, a piece of the vocabulary at a time; G is rounded once to
- * H's type (float32: to 2^-24 of itself or 2^-39 of dloss_t scale), each token's
- * by itself, and for dW H to 2^-39 of the largest |dloss_t H_tc| in float32; in
+ * H's type (of 32 tokens or fewer, where d >= 8: to 16 bits or more; float32: to
+ * 2^-24 of itself or 2^-39 of dloss_t scale), each token's by itself, and for dW H to 2^-39 of the largest |dloss_t H_tc| in float32; in
  * float16 tokens of a dloss below 2^-10 of the largest scale theirs down, to
  * float16's subnormals. Ignored tokens get zero rows of dH and add nothing to dW,
  * whatever their dloss; a label >= V gives NaN in its row of dH and in dW, a

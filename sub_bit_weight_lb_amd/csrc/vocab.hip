@@ -24,11 +24,10 @@
 // k runs down the rows (W in kDh, H and G in kDw) is transposed on its way from
 // LDS to the registers, by ds_read_b64_tr_b16.
 //
-// Types: bf16 and fp16 operands are exact and sums are fp32. G is rounded to the
-// operands' type once: half a unit, like the results, so that dH and dW are off by
-// about a tenth more than by their own rounding (relative to the exact gradient
-// 0.0017 for the plain form and 0.0018 to 0.0019 here in bf16; a second term of G
-// would double two of the four products). bf16's G holds (p - [label]) dloss of the
+// Types: bf16 and fp16 operands are exact and sums are fp32. 16-bit G of more than 32
+// tokens is rounded to the operands' type once: half a unit, like the results
+// (relative to the exact gradient 0.0017 for the plain form, 0.0018 to 0.0019 here in
+// bf16); of fewer it has two terms (kFewTerms). bf16's G holds (p - [label]) dloss of the
 // largest dloss 1; fp16's and fp32's hold p - [label] of each token to 2^15,
 // whatever the others' dloss (fp16: with dloss to 2^-10 of the largest), so that
 // probabilities down to 2^-29 keep all their bits. fp32 operands are scaled by powers
@@ -77,20 +76,23 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// Passes over k of an operand of type D
-constexpr int passes(int D) { return D == kF32 ? 3 : 1; }
+// Passes over k of a product of epilogue EPI, with GT terms of G
+enum Epi : int { kStat = 0, kGrad = 1, kDh = 2, kDw = 3 };
+constexpr int passes(int D, int epi, int GT) {
+  return D == kF32 ? 3 : epi == kDh || epi == kDw ? GT : 1;
+}
 
-// x (already scaled) as its terms of type D. Not finite: the first term alone.
-template <int D>
-__device__ __forceinline__ void split(float x, uint16_t (&t)[terms(D)]) {
-  if constexpr (D == kF32) {
-    const _Float16 h = (_Float16)x;
-    const float r = x - (float)h;
+// x (already scaled) as N terms of the 16-bit type that the products of D's take.
+// Not finite: the first term alone.
+template <int D, int N>
+__device__ __forceinline__ void split(float x, uint16_t (&t)[N]) {
+  typedef Elem<D == kBF16 ? kBF16 : kF16> E;
+  const typename E::type h = E::from(x);
+  t[0] = __builtin_bit_cast(uint16_t, h);
+  if constexpr (N == 2) {
+    const float r = x - E::to(h);
     const bool fin = (__float_as_uint(r) & 0x7fffffffu) < 0x7f800000u;
-    t[0] = __builtin_bit_cast(uint16_t, h);
-    t[1] = fin ? __builtin_bit_cast(uint16_t, (_Float16)r) : (uint16_t)0;
-  } else {
-    t[0] = __builtin_bit_cast(uint16_t, Elem<D>::from(x));
+    t[1] = fin ? __builtin_bit_cast(uint16_t, E::from(r)) : (uint16_t)0;
   }
 }
 
@@ -103,7 +105,6 @@ struct Opnd {
   int64_t ld, plane, rows, kv;
 };
 
-enum Epi : int { kStat = 0, kGrad = 1, kDh = 2, kDw = 3 };
 struct Mma {
   Opnd A, B;                // C (M x N), M = A.rows, N = B.rows
   int64_t K;                // a multiple of 64
@@ -281,7 +282,7 @@ struct Reader {
 // 3.5: 1.19 to 1.29 PFLOP/s (a large bf16 product of the library 1.27; this
 // kernel without its copies 1.5, matrix instructions alone 2.2). fp32, 1024
 // tokens, 32000 words, d = 2048: 0.40 to 0.46 ms each, 290 to 330 TFLOP/s.
-template <int D, int EPI, int WM, int WN, int MI, int NI, int NS>
+template <int D, int EPI, int GT, int WM, int WN, int MI, int NI, int NS>
 __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
   constexpr int BM = 16 * MI * WM, BN = 16 * NI * WN, W = WM * WN;
   constexpr int kStage = (BM + BN) * 128;
@@ -299,7 +300,8 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
   const int64_t m0 = tm * BM, n0 = tn * BN;
   const int64_t k_lo = (int64_t)blockIdx.y * a.k_slice;
   const int nk = (int)((lmin(a.K, k_lo + a.k_slice) - k_lo) / BK);
-  const int steps = nk * passes(D);
+  constexpr int NP = passes(D, EPI, GT);
+  const int steps = nk * NP;
 
   Tile<BM, CA, AM> ta;
   Tile<BN, CB, BM_> tb;
@@ -309,8 +311,9 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
   Reader<BN, NI, BM_> rb;
   ra.init(wm * MI, g, li);
   rb.init(wn * NI, g, li);
-  // passes: h l, l h, h h (the small ones first: what they round is 2^-11 of a
-  // sum with h h in it)
+  // fp32: passes over all k, h l, l h, h h (the small ones first: what they round is
+  // 2^-11 of a sum with h h in it). 16-bit operands with two terms of G: G's l and
+  // h in turn at each k, which the other operand is then near for.
   int pass = 0, kt = 0;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   // the next stage's copies, ready to go to `stage`
@@ -318,10 +321,15 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
     const uint32_t st = lds0 + stage * kStage;
     const int64_t k = k_lo + (int64_t)kt * BK;
     ta.aim(live, st, wave, k, D == kF32 && pass == 1 ? a.A.plane : 0);
-    tb.aim(live, st + BM * 128, wave, k, D == kF32 && pass == 0 ? a.B.plane : 0);
-    if (++kt == nk) {
-      kt = 0;
-      ++pass;
+    tb.aim(live, st + BM * 128, wave, k, NP > 1 && pass == 0 ? a.B.plane : 0);
+    if constexpr (D == kF32) {
+      if (++kt == nk) {
+        kt = 0;
+        ++pass;
+      }
+    } else if (++pass == NP) {
+      pass = 0;
+      ++kt;
     }
   };
   f32x4 acc[MI][NI];
@@ -451,10 +459,10 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
       const float lse = label >= 0 ? a.lse[t] : 0.0f, wn_t = label >= 0 ? a.wn[t] : 0.0f;
       const float zs = D == kF32 ? (label >= 0 ? a.zs[t] : 0.0f) : a.z0;
       const int at = own(label), used = label >= 0 ? left : 0;
-      uint16_t* row = a.G + t * a.gld * terms(D);
+      uint16_t* row = a.G + t * a.gld * GT;
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
-        uint16_t q[4][terms(D)];
+        uint16_t q[4][GT];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const float y = zs * acc[i][j][v] - lse;
@@ -464,7 +472,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
           split<D>(x, q[v]);
         }
 #pragma unroll
-        for (int p = 0; p < terms(D); ++p)
+        for (int p = 0; p < GT; ++p)
           *(u32x2*)(row + p * a.gld + r0 + 16 * i) =
               u32x2{(uint32_t)q[0][p] | (uint32_t)q[1][p] << 16,
                     (uint32_t)q[2][p] | (uint32_t)q[3][p] << 16};
@@ -646,7 +654,7 @@ __global__ __launch_bounds__(1024 / NT)
     if constexpr (GRAD) {
       if (t >= T) continue;
       const float lse = label >= 0 ? o.lse[t] : 0.0f, wn = label >= 0 ? o.wn[t] : 0.0f;
-      uint16_t q[4][terms(D)];
+      uint16_t q[4][kFewTerms];
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const float y = scale * z[v] - lse;
@@ -656,8 +664,8 @@ __global__ __launch_bounds__(1024 / NT)
         split<D>(x, q[v]);
       }
 #pragma unroll
-      for (int p = 0; p < terms(D); ++p)
-        *(u32x2*)(o.G + (t * terms(D) + p) * o.gld + w) =
+      for (int p = 0; p < kFewTerms; ++p)
+        *(u32x2*)(o.G + (t * kFewTerms + p) * o.gld + w) =
             u32x2{(uint32_t)q[0][p] | (uint32_t)q[1][p] << 16,
                   (uint32_t)q[2][p] | (uint32_t)q[3][p] << 16};
     } else {
@@ -999,19 +1007,20 @@ bool direct(const void* X, int64_t ld, int64_t k, int dtype) {
 // no other use, and k is long enough to win their start back (301 tokens, 4999
 // words of bf16: 8 stages of k 14 us with either, 16 stages 18 v 20, 32 stages
 // 27 v 32; 4 stages 19 v 15; 128 tokens, 32000 words, 64 stages: 52 v 80).
-template <int D, int EPI>
+template <int D, int EPI, int GT>
 hipError_t mma_launch(const Mma& a, int tile, int slices, hipStream_t s) {
   const int64_t tiles = tiles_of(a.A.rows, a.B.rows, tile);
   const dim3 grid((unsigned)((tiles + 7) / 8 * 8), (unsigned)slices);
   if (tile == 256) {
-    hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 4, 8, 4, 2>), grid, dim3(512), 0, s, a);
+    hipLaunchKernelGGL((mma_kernel<D, EPI, GT, 2, 4, 8, 4, 2>), grid, dim3(512), 0, s, a);
   } else if (tile == 64) {
     if constexpr (EPI != kDh)
-      hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 2, 2, 2, 4>), grid, dim3(256), 0, s, a);
-  } else if (tiles * slices <= 256 && std::min(a.K, a.k_slice) / BK * passes(D) >= 16) {
-    hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 2, 4, 4, 4>), grid, dim3(256), 0, s, a);
+      hipLaunchKernelGGL((mma_kernel<D, EPI, GT, 2, 2, 2, 2, 4>), grid, dim3(256), 0, s, a);
+  } else if (tiles * slices <= 256 &&
+             std::min(a.K, a.k_slice) / BK * passes(D, EPI, GT) >= 16) {
+    hipLaunchKernelGGL((mma_kernel<D, EPI, GT, 2, 2, 4, 4, 4>), grid, dim3(256), 0, s, a);
   } else {
-    hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 2, 4, 4, 2>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((mma_kernel<D, EPI, GT, 2, 2, 4, 4, 2>), grid, dim3(256), 0, s, a);
   }
   return hipGetLastError();
 }
@@ -1130,7 +1139,7 @@ hipError_t loss(const Vocab& a, hipStream_t s) {
     for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
       m.v0 = v0;
       if ((e = words<D>(a, p, v0, std::min(piece, a.V - v0), &m.A, s)) != hipSuccess) return e;
-      if ((e = mma_launch<D, kStat>(m, tile, 1, s)) != hipSuccess) return e;
+      if ((e = mma_launch<D, kStat, 1>(m, tile, 1, s)) != hipSuccess) return e;
     }
   }
   hipLaunchKernelGGL(stat_kernel, dim3((unsigned)((a.T + 15) / 16)), dim3(1024), 0, s,
@@ -1139,65 +1148,85 @@ hipError_t loss(const Vocab& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The products of nv words from v0 on, with GT terms of G
+template <int D, int GT>
+hipError_t piece(const Vocab& a, const Plan& p, int64_t v0, int64_t nv, const Opnd& Hz,
+                 const Opnd& Hw, hipStream_t s) {
+  typedef typename Elem<D>::type E;
+  char* w = (char*)a.work;
+  Factors* fac = (Factors*)(w + p.fac);
+  uint16_t* G = (uint16_t*)(w + p.G);
+  const Rows rows = rows_of(w, p, a.T);
+  const bool score_g = few(a.T, a.d, D);   // (16 bits: GT says so)
+  hipError_t e;
+  Opnd W;
+  if ((e = words<D>(a, p, v0, nv, &W, s)) != hipSuccess) return e;
+  if (score_g) {
+    if constexpr (GT == kFewTerms) {
+      const ScoreGrad o{a.lse, rows.wn, G, p.piece, v0};
+      if ((e = score<D, true>(a, v0, nv, o, s)) != hipSuccess) return e;
+    }
+  } else if constexpr (GT == terms(D)) {
+    Mma m{};
+    m.A = W; m.B = Hz;
+    m.K = m.k_slice = p.dp;
+    m.zs = rows.zs;
+    m.z0 = a.scale;
+    m.v0 = v0; m.labels = a.labels; m.lse = a.lse; m.wn = rows.wn;
+    m.G = G; m.gld = p.piece;
+    if ((e = mma_launch<D, kGrad, GT>(m, tile_for(nv, a.T), 1, s)) != hipSuccess) return e;
+  }
+  // (G is zero for words past nv to the next multiple of 64, and from
+  // mma_kernel for tokens past T to the tile's end)
+  if (a.dH) {
+    Mma h{};
+    h.A = Opnd{W.p, W.ld, W.plane, a.d, nv};
+    h.B = Opnd{G, p.piece * GT, p.piece, a.T, round_up(nv, 256)};
+    h.K = round_up(nv, BK);
+    h.k_slice = p.kz;
+    h.part = (float*)(w + p.part); h.slice = a.T * round_up(a.d, 4); h.ldo = round_up(a.d, 4);
+    h.add = v0 > 0;
+    const int n = (int)((h.K + p.kz - 1) / p.kz), tile = big_tiles(a.d, a.T, p.nz) ? 256 : 128;
+    if ((e = mma_launch<D, kDh, GT>(h, tile, n, s)) != hipSuccess) return e;
+  }
+  if (a.dW) {
+    Mma x{};
+    x.A = Hw;
+    x.B = Opnd{G, p.piece * GT, p.piece, nv, score_g ? a.T : p.tp};
+    x.K = x.k_slice = round_up(a.T, BK);
+    x.post = &fac->post_w;
+    x.out = (E*)a.dW + v0 * a.lddw; x.ldo = a.lddw;
+    if ((e = mma_launch<D, kDw, GT>(x, tile_for(a.d, nv), 1, s)) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 template <int D>
 hipError_t backward(const Vocab& a, hipStream_t s) {
   typedef typename Elem<D>::type E;
   const Plan p = plan_for(a.T, a.V, a.d, D, true);
   char* w = (char*)a.work;
-  Factors* fac = (Factors*)(w + p.fac);
-  uint16_t* G = (uint16_t*)(w + p.G);
-  constexpr int NTm = terms(D);
-  const int64_t ldp = round_up(a.d, 4), slice = a.T * ldp;
-  hipError_t e;
   const Rows rows = rows_of(w, p, a.T);
-  Opnd Hz, Hw, W;
+  hipError_t e;
+  Opnd Hz, Hw;
   if ((e = begin<D>(a, p, a.dloss, &Hz, &Hw, s)) != hipSuccess) return e;
   // every piece uses the same slices of its words for dH; the first writes them
   // all, the last, where it is another, may leave some as they are: those are not
   // launched
   for (int64_t v0 = 0; v0 < a.V; v0 += p.piece) {
-    const int64_t nv = std::min(p.piece, a.V - v0), nvp = round_up(nv, 256);
-    if ((e = words<D>(a, p, v0, nv, &W, s)) != hipSuccess) return e;
-    const bool score_g = few(a.T, a.d, D);
-    if (score_g) {
-      const ScoreGrad o{a.lse, rows.wn, G, p.piece, v0};
-      if ((e = score<D, true>(a, v0, nv, o, s)) != hipSuccess) return e;
-    } else {
-      Mma m{};
-      m.A = W; m.B = Hz;
-      m.K = m.k_slice = p.dp;
-      m.zs = rows.zs;
-      m.z0 = a.scale;
-      m.v0 = v0; m.labels = a.labels; m.lse = a.lse; m.wn = rows.wn;
-      m.G = G; m.gld = p.piece;
-      if ((e = mma_launch<D, kGrad>(m, tile_for(nv, a.T), 1, s)) != hipSuccess) return e;
-    }
-    // (G is zero for words past nv to the next multiple of 64, and from
-    // mma_kernel for tokens past T to the tile's end)
-    if (a.dH) {
-      Mma h{};
-      h.A = Opnd{W.p, W.ld, W.plane, a.d, nv};
-      h.B = Opnd{G, p.piece * NTm, p.piece, a.T, nvp};
-      h.K = round_up(nv, BK);
-      h.k_slice = p.kz;
-      h.part = (float*)(w + p.part); h.slice = slice; h.ldo = ldp; h.add = v0 > 0;
-      const int n = (int)((h.K + p.kz - 1) / p.kz);
-      if ((e = mma_launch<D, kDh>(h, big_tiles(a.d, a.T, p.nz) ? 256 : 128, n, s)) != hipSuccess) return e;
-    }
-    if (a.dW) {
-      Mma x{};
-      x.A = Hw;
-      x.B = Opnd{G, p.piece * NTm, p.piece, nv, score_g ? a.T : p.tp};
-      x.K = x.k_slice = round_up(a.T, BK);
-      x.post = &fac->post_w;
-      x.out = (E*)a.dW + v0 * a.lddw; x.ldo = a.lddw;
-      if ((e = mma_launch<D, kDw>(x, tile_for(a.d, nv), 1, s)) != hipSuccess) return e;
-    }
+    const int64_t nv = std::min(p.piece, a.V - v0);
+    if constexpr (D == kF32)
+      e = piece<D, terms(D)>(a, p, v0, nv, Hz, Hw, s);
+    else
+      e = few(a.T, a.d, D) ? piece<D, kFewTerms>(a, p, v0, nv, Hz, Hw, s)
+                           : piece<D, 1>(a, p, v0, nv, Hz, Hw, s);
+    if (e != hipSuccess) return e;
   }
   if (a.dH) {
     const dim3 grid((unsigned)((a.d + 1023) / 1024), (unsigned)std::min<int64_t>(a.T, 16384));
-    hipLaunchKernelGGL(dh_kernel<D>, grid, dim3(256), 0, s, (const float*)(w + p.part), p.nz, slice,
-                       ldp, a.T, a.d, a.labels, rows.pt, (E*)a.dH, a.lddh);
+    const int64_t ldp = round_up(a.d, 4);
+    hipLaunchKernelGGL(dh_kernel<D>, grid, dim3(256), 0, s, (const float*)(w + p.part), p.nz,
+                       a.T * ldp, ldp, a.T, a.d, a.labels, rows.pt, (E*)a.dH, a.lddh);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return hipSuccess;

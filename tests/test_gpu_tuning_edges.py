@@ -279,3 +279,40 @@ def test_a_word_that_is_not_finite_shows_in_every_loss(gpu, name, T, V, d, bad):
     assert (loss[~used] == 0).all() and (lse[~used] == 0).all()
     dH, dW = nq.vocab_loss_backward(L.H, L.W, L.labels, lse, L.dl)
     assert dH[used].isnan().all() and (dH[~used] == 0).all() and dW.isnan().all()
+
+
+@pytest.mark.parametrize("name", ["bfloat16", "float16"])
+@pytest.mark.parametrize("T, V, d", [(1, 5000, 1000), (1, 32000, 512), (2, 700, 4096), (5, 32000, 512),
+                                     (16, 5000, 1000), (32, 32000, 512), (33, 32000, 512), (300, 5000, 1000)])
+def test_16_bit_gradients_against_the_plain_form(gpu, name, T, V, d):
+    """The error of dH and dW (relative, in the norm) against that of the formulas in
+    fp32, rounded once at the end. Up to 32 tokens G has two terms, 16 bits of it
+    or more, and what is left is the outputs' rounding: 1 + 2^-8 of its square
+    and the fp32 sums, 1.05 with room. With more it is rounded to the type itself,
+    half a unit as the outputs are: two roundings of one size, 2^0.5 of one, 1.5
+    with room for their samples."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    print(f"case T={T} V={V} d={d} {name}", flush=True)
+    for seed in range(6):
+        g = torch.Generator(device=gpu).manual_seed(100 * seed + T)
+        W = 0.02 * torch.randn((V, d), generator=g, device=gpu)
+        labels = torch.randint(0, V, (T,), generator=g, device=gpu)
+        lean = (torch.rand((T, 1), generator=g, device=gpu) < 0.5) * (10.0 / (0.0004 * d))
+        X = (torch.randn((T, d), generator=g, device=gpu) + lean * W[labels]).to(dt(name))
+        W = W.to(dt(name))
+        dl = torch.full((T,), 1.0 / T, device=gpu)
+
+        def formulas(X, W, dl):
+            z = torch.mm(X, W.t())
+            G = torch.exp(z - torch.logsumexp(z, 1, keepdim=True))
+            G[torch.arange(T, device=gpu), labels] -= 1.0
+            G = G * dl.unsqueeze(1)
+            return torch.mm(G, W), torch.mm(G.t(), X)
+
+        _, lse = nq.vocab_loss(X, W, labels.int())
+        got = nq.vocab_loss_backward(X, W, labels.int(), lse, dl)
+        plain = [v.to(dt(name)) for v in formulas(X.float(), W.float(), dl)]
+        for a, p, e in zip(got, plain, formulas(X.double(), W.double(), dl.double())):
+            own, ref = (float((v.double() - e).norm() / e.norm()) for v in (a, p))
+            assert own <= (1.05 if T <= 32 else 1.5) * ref, (seed, own, ref)
