@@ -27,7 +27,7 @@
 // Types: bf16 and fp16 operands are exact and sums are fp32. 16-bit G of more than 32
 // tokens is rounded to the operands' type once: half a unit, like the results
 // (relative to the exact gradient 0.0017 for the plain form, 0.0018 to 0.0019 here in
-// bf16); of fewer it has two terms (kFewTerms). bf16's G holds (p - [label]) dloss of the
+// bf16); of fewer it has two terms (g_rows). bf16's G holds (p - [label]) dloss of the
 // largest dloss 1; fp16's and fp32's hold p - [label] of each token to 2^15,
 // whatever the others' dloss (fp16: with dloss to 2^-10 of the largest), so that
 // probabilities down to 2^-29 keep all their bits. fp32 operands are scaled by powers
@@ -76,11 +76,8 @@ __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// Passes over k of a product of epilogue EPI, with GT terms of G
-enum Epi : int { kStat = 0, kGrad = 1, kDh = 2, kDw = 3 };
-constexpr int passes(int D, int epi, int GT) {
-  return D == kF32 ? 3 : epi == kDh || epi == kDw ? GT : 1;
-}
+// Passes over k of an operand of type D
+constexpr int passes(int D) { return D == kF32 ? 3 : 1; }
 
 // x (already scaled) as N terms of the 16-bit type that the products of D's take.
 // Not finite: the first term alone.
@@ -105,6 +102,7 @@ struct Opnd {
   int64_t ld, plane, rows, kv;
 };
 
+enum Epi : int { kStat = 0, kGrad = 1, kDh = 2, kDw = 3 };
 struct Mma {
   Opnd A, B;                // C (M x N), M = A.rows, N = B.rows
   int64_t K;                // a multiple of 64
@@ -282,7 +280,7 @@ struct Reader {
 // 3.5: 1.19 to 1.29 PFLOP/s (a large bf16 product of the library 1.27; this
 // kernel without its copies 1.5, matrix instructions alone 2.2). fp32, 1024
 // tokens, 32000 words, d = 2048: 0.40 to 0.46 ms each, 290 to 330 TFLOP/s.
-template <int D, int EPI, int GT, int WM, int WN, int MI, int NI, int NS>
+template <int D, int EPI, int WM, int WN, int MI, int NI, int NS>
 __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
   constexpr int BM = 16 * MI * WM, BN = 16 * NI * WN, W = WM * WN;
   constexpr int kStage = (BM + BN) * 128;
@@ -300,8 +298,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
   const int64_t m0 = tm * BM, n0 = tn * BN;
   const int64_t k_lo = (int64_t)blockIdx.y * a.k_slice;
   const int nk = (int)((lmin(a.K, k_lo + a.k_slice) - k_lo) / BK);
-  constexpr int NP = passes(D, EPI, GT);
-  const int steps = nk * NP;
+  const int steps = nk * passes(D);
 
   Tile<BM, CA, AM> ta;
   Tile<BN, CB, BM_> tb;
@@ -311,9 +308,8 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
   Reader<BN, NI, BM_> rb;
   ra.init(wm * MI, g, li);
   rb.init(wn * NI, g, li);
-  // fp32: passes over all k, h l, l h, h h (the small ones first: what they round is
-  // 2^-11 of a sum with h h in it). 16-bit operands with two terms of G: G's l and
-  // h in turn at each k, which the other operand is then near for.
+  // passes: h l, l h, h h (the small ones first: what they round is 2^-11 of a
+  // sum with h h in it)
   int pass = 0, kt = 0;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   // the next stage's copies, ready to go to `stage`
@@ -321,15 +317,10 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
     const uint32_t st = lds0 + stage * kStage;
     const int64_t k = k_lo + (int64_t)kt * BK;
     ta.aim(live, st, wave, k, D == kF32 && pass == 1 ? a.A.plane : 0);
-    tb.aim(live, st + BM * 128, wave, k, NP > 1 && pass == 0 ? a.B.plane : 0);
-    if constexpr (D == kF32) {
-      if (++kt == nk) {
-        kt = 0;
-        ++pass;
-      }
-    } else if (++pass == NP) {
-      pass = 0;
-      ++kt;
+    tb.aim(live, st + BM * 128, wave, k, D == kF32 && pass == 0 ? a.B.plane : 0);
+    if (++kt == nk) {
+      kt = 0;
+      ++pass;
     }
   };
   f32x4 acc[MI][NI];
@@ -459,10 +450,10 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
       const float lse = label >= 0 ? a.lse[t] : 0.0f, wn_t = label >= 0 ? a.wn[t] : 0.0f;
       const float zs = D == kF32 ? (label >= 0 ? a.zs[t] : 0.0f) : a.z0;
       const int at = own(label), used = label >= 0 ? left : 0;
-      uint16_t* row = a.G + t * a.gld * GT;
+      uint16_t* row = a.G + t * a.gld * terms(D);
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
-        uint16_t q[4][GT];
+        uint16_t q[4][terms(D)];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const float y = zs * acc[i][j][v] - lse;
@@ -472,7 +463,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
           split<D>(x, q[v]);
         }
 #pragma unroll
-        for (int p = 0; p < GT; ++p)
+        for (int p = 0; p < terms(D); ++p)
           *(u32x2*)(row + p * a.gld + r0 + 16 * i) =
               u32x2{(uint32_t)q[0][p] | (uint32_t)q[1][p] << 16,
                     (uint32_t)q[2][p] | (uint32_t)q[3][p] << 16};
@@ -840,14 +831,12 @@ __device__ __forceinline__ float max_of(float v, float* sm) {
   }
   return sm[0];
 }
-// 2^e with m 2^e in (2^14, 2^15], e in -126 .. 126
-__device__ __forceinline__ float power_for(float m) {
+// e with m 2^e in (2^14, 2^15], in -126 .. 126
+__device__ __forceinline__ int power_for(float m) {
   const uint32_t b = __float_as_uint(m);
   const int e = 14 - ((int)(b >> 23) - 127) + ((b & 0x7fffffu) == 0);
-  return m > 0.0f ? __uint_as_float((uint32_t)(min(max(e, -126), 126) + 127) << 23) : 1.0f;
+  return m > 0.0f ? min(max(e, -126), 126) : 0;
 }
-// value * 2^e, rounded once
-__device__ __forceinline__ float scaled(double value, int e) { return (float)ldexp(value, e); }
 // The factors. With dloss = f 2^x per token (1/2 <= |f| < 1; x0 of the largest),
 //   bf16:       G = (p - [label]) dloss / max|dloss|: its exponents reach far enough;
 //   fp32:       G = (p - [label]) f 2^15 whatever the others' dloss are, dH's row
@@ -866,17 +855,17 @@ __global__ __launch_bounds__(1024) void factors_kernel(const float* __restrict__
                                                        int64_t T, int64_t V, float scale, Rows rows,
                                                        Factors* __restrict__ out) {
   __shared__ float sm[1024];
-  float mw = 1.0f;
+  int ew = 0;   // (scales are powers of two: factors by ldexp, rounded once at most)
   if (D == kF32) {
-    mw = power_for(max_of(parts[threadIdx.x], sm));
+    ew = power_for(max_of(parts[threadIdx.x], sm));
     for (int64_t t = threadIdx.x; t < T; t += 1024) {
-      const float f = power_for(hm[t]);
-      rows.hz[t] = f;
-      rows.zs[t] = (float)((double)scale / f / mw);
+      const int e = power_for(hm[t]);
+      rows.hz[t] = ldexpf(1.0f, e);
+      rows.zs[t] = ldexpf(scale, -(e + ew));
     }
   }
   if (!dloss) {
-    if (threadIdx.x == 0) out->mw = mw;
+    if (threadIdx.x == 0) out->mw = ldexpf(1.0f, ew);
     return;
   }
   // the largest of the finite ones
@@ -895,14 +884,14 @@ __global__ __launch_bounds__(1024) void factors_kernel(const float* __restrict__
     return l != 0.0f && fabsf(l) < __builtin_inff() ? frexpf(l, &x) : l;
   };
   // fp32: H's copy for dW, weighted by 2^(x - x0), to 2^15 at its largest
-  float mh = 1.0f;
+  int eh = 0;
   if (D == kF32) {
     float e = 0.0f;
     for (int64_t t = threadIdx.x; t < T; t += 1024) {
       int x;
       if (labels[t] >= 0 && parted(t, x) != 0.0f) e = fmaxf(e, ldexpf(hm[t], x - x0));
     }
-    mh = power_for(max_of(e, sm));
+    eh = power_for(max_of(e, sm));
   }
   for (int64_t t = threadIdx.x; t < T; t += 1024) {
     const int32_t label = labels[t];
@@ -915,8 +904,8 @@ __global__ __launch_bounds__(1024) void factors_kernel(const float* __restrict__
       const float f = parted(t, x);
       const int k = D == kF16 ? min(x0 - x, kInG) : 0;
       wn = ldexpf(f, 15 - k);
-      pt = scaled((double)scale / mw, x + k - 15);
-      hw = f == 0.0f ? 0.0f : ldexpf(mh, x + k - x0);
+      pt = ldexpf(scale, x + k - 15 - ew);
+      hw = f == 0.0f ? 0.0f : ldexpf(1.0f, x + k - x0 + eh);
     }
     rows.wn[t] = label < 0 ? 0.0f : label < V ? wn : __uint_as_float(0x7fc00000u);
     rows.pt[t] = label < 0 ? 0.0f : pt;
@@ -924,12 +913,13 @@ __global__ __launch_bounds__(1024) void factors_kernel(const float* __restrict__
     if (D == kF16) rows.hz[t] = 1.0f;
   }
   if (threadIdx.x == 0)
-    *out = Factors{mw, D == kBF16 ? (m == 0.0f ? 1.0f : m) * scale : scaled((double)scale / mh, x0 - 15)};
+    *out = Factors{ldexpf(1.0f, ew),
+                   D == kBF16 ? (m == 0.0f ? 1.0f : m) * scale : ldexpf(scale, x0 - 15 - eh)};
 }
 
-// dH = each token's factor times the sum of nz slices (in order); zero for an
-// ignored token
-template <int D>
+// dH = each token's factor times the sum of nz slices (in order) of its RT rows; zero
+// for an ignored token
+template <int D, int RT>
 __global__ __launch_bounds__(256) void dh_kernel(const float* __restrict__ part, int nz,
                                                  int64_t slice, int64_t ldp, int64_t T, int64_t d,
                                                  const int32_t* __restrict__ labels,
@@ -941,8 +931,11 @@ __global__ __launch_bounds__(256) void dh_kernel(const float* __restrict__ part,
   for (int64_t t = blockIdx.y; t < T; t += gridDim.y) {
     const bool used = labels[t] >= 0;
     const float f = pt[t];
-    f32x4 s = *(const f32x4*)(part + t * ldp + c);
-    for (int z = 1; z < nz; ++z) s += *(const f32x4*)(part + z * slice + t * ldp + c);
+    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int z = 0; z < nz; ++z)
+#pragma unroll
+      for (int p = 0; p < RT; ++p)
+        s += *(const f32x4*)(part + z * slice + (t * RT + p) * ldp + c);
 #pragma unroll
     for (int v = 0; v < 4; ++v)
       if (c + v < d) out[t * ldo + c + v] = Elem<D>::from(used ? s[v] * f : 0.0f);
@@ -952,7 +945,8 @@ __global__ __launch_bounds__(256) void dh_kernel(const float* __restrict__ part,
 // ---------------------------------------------------------------- layout
 // out [row][term][kp] = the terms of X (rows x k) times a factor, zero from k to
 // kp, for rows past the last up to rp, and for rows whose label is negative (labels
-// nullable). Form z of the grid writes the z-th copy of out.
+// nullable); with twice, each row two times. Form z of the grid writes the z-th copy
+// of out.
 enum Mul : int {
   kAsIs = 0,      // 1
   kOne = 1,       // *mul
@@ -964,20 +958,21 @@ __global__ __launch_bounds__(256) void pack_kernel(const typename Elem<D>::type*
                                                    const int32_t* __restrict__ labels,
                                                    const float* __restrict__ mul,
                                                    uint16_t* __restrict__ out, int64_t rp,
-                                                   int64_t kp) {
+                                                   int64_t kp, int twice) {
   typedef typename Elem<D>::type E;
   const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
   if (c >= kp) return;
   out += blockIdx.z * rp * kp * terms(D);
   for (int64_t r = blockIdx.y; r < rp; r += gridDim.y) {
     E e[8];
-    const bool row = r < rows && (!labels || labels[r] >= 0);
-    const float f = M == kAsIs ? 1.0f : M == kOne ? *mul : row ? mul[blockIdx.z * rows + r] : 0.0f;
+    const int64_t at = r >> twice;
+    const bool row = at < rows && (!labels || labels[at] >= 0);
+    const float f = M == kAsIs ? 1.0f : M == kOne ? *mul : row ? mul[blockIdx.z * rows + at] : 0.0f;
     if (row && c + 8 <= k) {
-      __builtin_memcpy(e, X + r * ld + c, sizeof(e));
+      __builtin_memcpy(e, X + at * ld + c, sizeof(e));
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = row && c + i < k ? X[r * ld + c + i] : (E)0;
+      for (int i = 0; i < 8; ++i) e[i] = row && c + i < k ? X[at * ld + c + i] : (E)0;
     }
     uint16_t q[8][terms(D)];
 #pragma unroll
@@ -1007,31 +1002,31 @@ bool direct(const void* X, int64_t ld, int64_t k, int dtype) {
 // no other use, and k is long enough to win their start back (301 tokens, 4999
 // words of bf16: 8 stages of k 14 us with either, 16 stages 18 v 20, 32 stages
 // 27 v 32; 4 stages 19 v 15; 128 tokens, 32000 words, 64 stages: 52 v 80).
-template <int D, int EPI, int GT>
+template <int D, int EPI>
 hipError_t mma_launch(const Mma& a, int tile, int slices, hipStream_t s) {
   const int64_t tiles = tiles_of(a.A.rows, a.B.rows, tile);
   const dim3 grid((unsigned)((tiles + 7) / 8 * 8), (unsigned)slices);
   if (tile == 256) {
-    hipLaunchKernelGGL((mma_kernel<D, EPI, GT, 2, 4, 8, 4, 2>), grid, dim3(512), 0, s, a);
+    hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 4, 8, 4, 2>), grid, dim3(512), 0, s, a);
   } else if (tile == 64) {
     if constexpr (EPI != kDh)
-      hipLaunchKernelGGL((mma_kernel<D, EPI, GT, 2, 2, 2, 2, 4>), grid, dim3(256), 0, s, a);
-  } else if (tiles * slices <= 256 &&
-             std::min(a.K, a.k_slice) / BK * passes(D, EPI, GT) >= 16) {
-    hipLaunchKernelGGL((mma_kernel<D, EPI, GT, 2, 2, 4, 4, 4>), grid, dim3(256), 0, s, a);
+      hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 2, 2, 2, 4>), grid, dim3(256), 0, s, a);
+  } else if (tiles * slices <= 256 && std::min(a.K, a.k_slice) / BK * passes(D) >= 16) {
+    hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 2, 4, 4, 4>), grid, dim3(256), 0, s, a);
   } else {
-    hipLaunchKernelGGL((mma_kernel<D, EPI, GT, 2, 2, 4, 4, 2>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((mma_kernel<D, EPI, 2, 2, 4, 4, 2>), grid, dim3(256), 0, s, a);
   }
   return hipGetLastError();
 }
 
 template <int D, int M>
 hipError_t pack(const void* X, int64_t rows, int64_t k, int64_t ld, const int32_t* labels,
-                const float* mul, uint16_t* out, int64_t rp, int64_t kp, int forms, hipStream_t s) {
+                const float* mul, uint16_t* out, int64_t rp, int64_t kp, int forms, bool twice,
+                hipStream_t s) {
   const dim3 grid((unsigned)((kp / 8 + 255) / 256), (unsigned)std::min<int64_t>(rp, 16384),
                   (unsigned)forms);
   hipLaunchKernelGGL((pack_kernel<D, M>), grid, dim3(256), 0, s,
-                     (const typename Elem<D>::type*)X, rows, k, ld, labels, mul, out, rp, kp);
+                     (const typename Elem<D>::type*)X, rows, k, ld, labels, mul, out, rp, kp, (int)twice);
   return hipGetLastError();
 }
 
@@ -1060,6 +1055,8 @@ hipError_t begin(const Vocab& a, const Plan& p, const float* dloss, Opnd* Hz, Op
   const bool dw = dloss && a.dW, score = dloss && few(a.T, a.d, D);
   // (bf16 has one copy for both)
   const bool z = !score && (!direct(a.H, a.ldh, a.d, D) || (D == kBF16 && dw));
+  // (for dW's products with two rows of G per token)
+  const bool twice = score && g_rows(a.T, a.d, D) == 2;
   uint16_t* out = (uint16_t*)(w + p.hp);
   const int64_t copy = p.tp * p.dp * terms(D);
   *Hz = z ? Opnd{out, p.dp * terms(D), p.dp, a.T, p.dp}
@@ -1068,12 +1065,12 @@ hipError_t begin(const Vocab& a, const Plan& p, const float* dloss, Opnd* Hz, Op
   if (!z && !dw) return hipSuccess;
   if constexpr (D != kF32) {
     if (D == kBF16 || !dw)
-      return pack<D, kAsIs>(a.H, a.T, a.d, a.ldh, a.labels, nullptr, out, p.tp, p.dp, 1, s);
+      return pack<D, kAsIs>(a.H, a.T, a.d, a.ldh, a.labels, nullptr, out, p.tp, p.dp, 1, twice, s);
   }
   if constexpr (D != kBF16) {   // the two copies, and their factors, lie behind each other
     const int from = z ? 0 : 1, n = (int)z + (int)dw;
     return pack<D, kEachRow>(a.H, a.T, a.d, a.ldh, a.labels, rows.hz + from * a.T,
-                             out + from * copy, p.tp, p.dp, n, s);
+                             out + from * copy, p.tp, p.dp, n, twice, s);
   }
 }
 // nv words of W from v0: in place, or a copy in the workspace
@@ -1088,7 +1085,8 @@ hipError_t words(const Vocab& a, const Plan& p, int64_t v0, int64_t nv, Opnd* o,
   char* w = (char*)a.work;
   uint16_t* out = (uint16_t*)(w + p.wp);
   *o = Opnd{out, p.dp * terms(D), p.dp, nv, p.dp};
-  return pack<D, D == kF32 ? kOne : kAsIs>(W, nv, a.d, a.ldw, nullptr, &((Factors*)(w + p.fac))->mw, out, nv, p.dp, 1, s);
+  return pack<D, D == kF32 ? kOne : kAsIs>(W, nv, a.d, a.ldw, nullptr,
+                                           &((Factors*)(w + p.fac))->mw, out, nv, p.dp, 1, false, s);
 }
 
 // score_kernel over nv words from v0 on
@@ -1139,7 +1137,7 @@ hipError_t loss(const Vocab& a, hipStream_t s) {
     for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
       m.v0 = v0;
       if ((e = words<D>(a, p, v0, std::min(piece, a.V - v0), &m.A, s)) != hipSuccess) return e;
-      if ((e = mma_launch<D, kStat, 1>(m, tile, 1, s)) != hipSuccess) return e;
+      if ((e = mma_launch<D, kStat>(m, tile, 1, s)) != hipSuccess) return e;
     }
   }
   hipLaunchKernelGGL(stat_kernel, dim3((unsigned)((a.T + 15) / 16)), dim3(1024), 0, s,
@@ -1148,85 +1146,70 @@ hipError_t loss(const Vocab& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The products of nv words from v0 on, with GT terms of G
-template <int D, int GT>
-hipError_t piece(const Vocab& a, const Plan& p, int64_t v0, int64_t nv, const Opnd& Hz,
-                 const Opnd& Hw, hipStream_t s) {
-  typedef typename Elem<D>::type E;
-  char* w = (char*)a.work;
-  Factors* fac = (Factors*)(w + p.fac);
-  uint16_t* G = (uint16_t*)(w + p.G);
-  const Rows rows = rows_of(w, p, a.T);
-  const bool score_g = few(a.T, a.d, D);   // (16 bits: GT says so)
-  hipError_t e;
-  Opnd W;
-  if ((e = words<D>(a, p, v0, nv, &W, s)) != hipSuccess) return e;
-  if (score_g) {
-    if constexpr (GT == kFewTerms) {
-      const ScoreGrad o{a.lse, rows.wn, G, p.piece, v0};
-      if ((e = score<D, true>(a, v0, nv, o, s)) != hipSuccess) return e;
-    }
-  } else if constexpr (GT == terms(D)) {
-    Mma m{};
-    m.A = W; m.B = Hz;
-    m.K = m.k_slice = p.dp;
-    m.zs = rows.zs;
-    m.z0 = a.scale;
-    m.v0 = v0; m.labels = a.labels; m.lse = a.lse; m.wn = rows.wn;
-    m.G = G; m.gld = p.piece;
-    if ((e = mma_launch<D, kGrad, GT>(m, tile_for(nv, a.T), 1, s)) != hipSuccess) return e;
-  }
-  // (G is zero for words past nv to the next multiple of 64, and from
-  // mma_kernel for tokens past T to the tile's end)
-  if (a.dH) {
-    Mma h{};
-    h.A = Opnd{W.p, W.ld, W.plane, a.d, nv};
-    h.B = Opnd{G, p.piece * GT, p.piece, a.T, round_up(nv, 256)};
-    h.K = round_up(nv, BK);
-    h.k_slice = p.kz;
-    h.part = (float*)(w + p.part); h.slice = a.T * round_up(a.d, 4); h.ldo = round_up(a.d, 4);
-    h.add = v0 > 0;
-    const int n = (int)((h.K + p.kz - 1) / p.kz), tile = big_tiles(a.d, a.T, p.nz) ? 256 : 128;
-    if ((e = mma_launch<D, kDh, GT>(h, tile, n, s)) != hipSuccess) return e;
-  }
-  if (a.dW) {
-    Mma x{};
-    x.A = Hw;
-    x.B = Opnd{G, p.piece * GT, p.piece, nv, score_g ? a.T : p.tp};
-    x.K = x.k_slice = round_up(a.T, BK);
-    x.post = &fac->post_w;
-    x.out = (E*)a.dW + v0 * a.lddw; x.ldo = a.lddw;
-    if ((e = mma_launch<D, kDw, GT>(x, tile_for(a.d, nv), 1, s)) != hipSuccess) return e;
-  }
-  return hipSuccess;
-}
-
 template <int D>
 hipError_t backward(const Vocab& a, hipStream_t s) {
   typedef typename Elem<D>::type E;
   const Plan p = plan_for(a.T, a.V, a.d, D, true);
   char* w = (char*)a.work;
-  const Rows rows = rows_of(w, p, a.T);
+  Factors* fac = (Factors*)(w + p.fac);
+  uint16_t* G = (uint16_t*)(w + p.G);
+  // rows of G, and so of dH's sums, as the products see them: the terms of 16-bit G
+  // are rows of their own
+  const int rt = g_rows(a.T, a.d, D);
+  const int64_t RT = rt * a.T, gld = p.piece * terms(D);
+  const int64_t ldp = round_up(a.d, 4), slice = RT * ldp;
+  const bool score_g = few(a.T, a.d, D);
   hipError_t e;
-  Opnd Hz, Hw;
+  const Rows rows = rows_of(w, p, a.T);
+  Opnd Hz, Hw, W;
   if ((e = begin<D>(a, p, a.dloss, &Hz, &Hw, s)) != hipSuccess) return e;
   // every piece uses the same slices of its words for dH; the first writes them
   // all, the last, where it is another, may leave some as they are: those are not
   // launched
   for (int64_t v0 = 0; v0 < a.V; v0 += p.piece) {
-    const int64_t nv = std::min(p.piece, a.V - v0);
-    if constexpr (D == kF32)
-      e = piece<D, terms(D)>(a, p, v0, nv, Hz, Hw, s);
-    else
-      e = few(a.T, a.d, D) ? piece<D, kFewTerms>(a, p, v0, nv, Hz, Hw, s)
-                           : piece<D, 1>(a, p, v0, nv, Hz, Hw, s);
-    if (e != hipSuccess) return e;
+    const int64_t nv = std::min(p.piece, a.V - v0), nvp = round_up(nv, 256);
+    if ((e = words<D>(a, p, v0, nv, &W, s)) != hipSuccess) return e;
+    if (score_g) {
+      const ScoreGrad o{a.lse, rows.wn, G, p.piece, v0};
+      if ((e = score<D, true>(a, v0, nv, o, s)) != hipSuccess) return e;
+    } else {
+      Mma m{};
+      m.A = W; m.B = Hz;
+      m.K = m.k_slice = p.dp;
+      m.zs = rows.zs;
+      m.z0 = a.scale;
+      m.v0 = v0; m.labels = a.labels; m.lse = a.lse; m.wn = rows.wn;
+      m.G = G; m.gld = p.piece;
+      if ((e = mma_launch<D, kGrad>(m, tile_for(nv, a.T), 1, s)) != hipSuccess) return e;
+    }
+    // (G is zero for words past nv to the next multiple of 64, and from
+    // mma_kernel for tokens past T to the tile's end)
+    if (a.dH) {
+      Mma h{};
+      h.A = Opnd{W.p, W.ld, W.plane, a.d, nv};
+      h.B = Opnd{G, gld, p.piece, RT, nvp};
+      h.K = round_up(nv, BK);
+      h.k_slice = p.kz;
+      h.part = (float*)(w + p.part); h.slice = slice; h.ldo = ldp; h.add = v0 > 0;
+      const int n = (int)((h.K + p.kz - 1) / p.kz), tile = big_tiles(a.d, RT, p.nz) ? 256 : 128;
+      if ((e = mma_launch<D, kDh>(h, tile, n, s)) != hipSuccess) return e;
+    }
+    if (a.dW) {
+      Mma x{};
+      x.A = Hw;
+      x.B = Opnd{G, gld, p.piece, nv, score_g ? RT : p.tp};
+      x.K = x.k_slice = round_up(RT, BK);
+      x.post = &fac->post_w;
+      x.out = (E*)a.dW + v0 * a.lddw; x.ldo = a.lddw;
+      if ((e = mma_launch<D, kDw>(x, tile_for(a.d, nv), 1, s)) != hipSuccess) return e;
+    }
   }
   if (a.dH) {
     const dim3 grid((unsigned)((a.d + 1023) / 1024), (unsigned)std::min<int64_t>(a.T, 16384));
-    const int64_t ldp = round_up(a.d, 4);
-    hipLaunchKernelGGL(dh_kernel<D>, grid, dim3(256), 0, s, (const float*)(w + p.part), p.nz,
-                       a.T * ldp, ldp, a.T, a.d, a.labels, rows.pt, (E*)a.dH, a.lddh);
+    auto* join = dh_kernel<D, 1>;
+    if constexpr (D != kF32) join = rt == 1 ? join : dh_kernel<D, kFewTerms>;
+    hipLaunchKernelGGL(join, grid, dim3(256), 0, s, (const float*)(w + p.part), p.nz, slice, ldp,
+                       a.T, a.d, a.labels, rows.pt, (E*)a.dH, a.lddh);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return hipSuccess;

@@ -30,17 +30,18 @@ constexpr int forms(int D) { return D == kBF16 ? 1 : 2; }
 // 810, 829 and 848).
 inline bool few(int64_t T, int64_t d, int dtype) { return d >= 8 && T <= (dtype == kF32 ? 64 : 32); }
 
-// Terms of G. One value of G, the label's or a likely word's, carries most of a
-// token's gradient, and a 16-bit G's rounding of it is common to the token's row of
-// dH and to dW's row of the word. Over many tokens that is a second rounding like the
-// outputs' own, 2^0.5 of their error at most (1.05 to 1.25 measured with 2048 tokens,
-// a few 1.4 with 64); the gradient of one token can be twice, of 32 tokens 1.5 times as
-// far off as rounding its results alone. So 16-bit G of few tokens has a second term,
-// as good as exact (32 tokens, 32000 x 4096 bf16: 316 us in place of 277; of all
-// tokens it would double two of the four products).
+// Rows of G per token: terms of a 16-bit G that the products take as tokens of their
+// own (fp32's two terms lie in one row, for its passes over k). One value of G, the
+// label's or a likely word's, carries most of a token's gradient, and a 16-bit G's
+// rounding of it is common to the token's row of dH and to dW's row of the word. Over
+// many tokens that is a second rounding like the outputs' own, 2^0.5 of their error
+// at most (1.05 to 1.25 measured with 2048 tokens, a few 1.4 with 64); the gradient of
+// one token can be twice, of 32 tokens 1.5 times as far off as rounding its results
+// alone. So 16-bit G of few tokens has a second term, as good as exact, in rows of the
+// products' tiles that would be empty.
 constexpr int kFewTerms = 2;
-inline int g_terms(int64_t T, int64_t d, int dtype) {
-  return few(T, d, dtype) ? kFewTerms : terms(dtype);
+inline int g_rows(int64_t T, int64_t d, int dtype) {
+  return dtype != kF32 && few(T, d, dtype) ? kFewTerms : 1;
 }
 
 struct Plan {
@@ -125,8 +126,9 @@ inline Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad) {
     const int64_t words = round_up(std::min(p.piece, V), BK), nz = dh_slices(T, d, p.piece);
     p.kz = round_up((words + nz - 1) / nz, BK);
     p.nz = (int)((words + p.kz - 1) / p.kz);
-    p.G = take(2 * g_terms(T, d, dtype) * p.tp * p.piece);
-    p.part = take(4 * p.nz * T * round_up(d, 4));
+    // (few tokens: their two rows each are 64 at most)
+    p.G = take(2 * nt * p.tp * p.piece);
+    p.part = take(4 * p.nz * T * g_rows(T, d, dtype) * round_up(d, 4));
   }
   p.bytes = off;
   return p;
