@@ -316,3 +316,75 @@ def test_16_bit_gradients_against_the_plain_form(gpu, name, T, V, d):
         for a, p, e in zip(got, plain, formulas(X.double(), W.double(), dl.double())):
             own, ref = (float((v.double() - e).norm() / e.norm()) for v in (a, p))
             assert own <= (1.05 if T <= 32 else 1.5) * ref, (seed, own, ref)
+
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("T, V, d", [(1, 1, 8), (2, 1, 40), (32, 1, 16), (33, 1, 16), (5, 3, 9), (32, 65, 8),
+                                     (64, 129, 31), (16, 63, 7)])
+@pytest.mark.parametrize("scale", [1.0, -0.7, 0.0])
+def test_smallest_vocabularies_and_scales_of_any_sign(gpu, name, T, V, d, scale):
+    import sub_bit_weight_lb_amd as nq
+    print(f"case T={T} V={V} d={d} scale={scale} {name}", flush=True)
+    L = Head(T + V, T, V, d, name, gpu, scale=scale)
+    loss, lse = nq.vocab_loss(L.H, L.W, L.labels, scale=scale,
+                              work=dirty(nq.vocab_loss_work_bytes(T, V, d, dt(name)), gpu))
+    L.check_loss(loss, lse)
+    L.check_grad(*nq.vocab_loss_backward(
+        L.H, L.W, L.labels, lse, L.dl, scale=scale,
+        work=dirty(nq.vocab_loss_work_bytes(T, V, d, dt(name), True), gpu)))
+
+
+@pytest.mark.parametrize("name, k", [("float32", 90), ("float32", -90), ("bfloat16", 90),
+                                     ("bfloat16", -90), ("float16", 3)])
+@pytest.mark.parametrize("T", [7, 40, 90])
+def test_gradients_scale_with_dloss_to_the_bit(gpu, name, k, T):
+    """All dloss times a power of two give the same gradient times it, where no
+    output leaves its type's normal numbers."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    L = Head(71, T, 300, 72, name, gpu)
+    L.labels[L.labels >= 0] %= 7          # many tokens share a label
+    _, lse = nq.vocab_loss(L.H, L.W, L.labels)
+    a = nq.vocab_loss_backward(L.H, L.W, L.labels, lse, L.dl)
+    L.check_grad(*a)
+    b = nq.vocab_loss_backward(L.H, L.W, L.labels, lse, L.dl * 2.0 ** k)
+    for x, y in zip(a, b):
+        x, y = x.float(), y.float()
+        least = 4 * torch.finfo(dt(name)).smallest_normal
+        normal = ((x.abs() > least) & (y.abs() > least)) | ((x == 0) & (y == 0))
+        assert normal.float().mean() > 0.9
+        assert torch.equal(x[normal] * 2.0 ** k, y[normal])
+
+
+@pytest.mark.parametrize("name", TYPES)
+def test_captured_gradients_of_few_tokens_replay(gpu, name):
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    T, V, d = 11, 900, 136
+    L = Head(81, T, V, d, name, gpu)
+    work = torch.empty(nq.vocab_loss_work_bytes(T, V, d, dt(name), True), dtype=torch.uint8, device=gpu)
+
+    def run():
+        loss, lse = nq.vocab_loss(L.H, L.W, L.labels, work=work)
+        return (loss, lse, *nq.vocab_loss_backward(L.H, L.W, L.labels, lse, L.dl, work=work))
+
+    run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for k in range(3):
+        gen = torch.Generator(device=gpu).manual_seed(k)
+        L.H.copy_(torch.randn(L.H.shape, generator=gen, device=gpu))
+        L.dl.copy_(torch.randn(L.dl.shape, generator=gen, device=gpu))
+        work.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        want = run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
