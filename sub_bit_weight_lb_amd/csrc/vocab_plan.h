@@ -26,8 +26,8 @@ constexpr int forms(int D) { return D == kBF16 ? 1 : 2; }
 // us, score_kernel 104; 32 tokens: 72 in score_kernel), but fp32 would be copied
 // for it (2048 x 32000, 64 tokens: 309 us, score_kernel 90). The gradient's logits
 // come from the same kernel; its time is much the same with either (4096 x 32000
-// bf16, 1 and 32 tokens: 262 and 276 us, with mma_kernel 266 and 274; fp32 790 and
-// 810, 829 and 848).
+// bf16, 1 and 32 tokens, one term of G: 262 and 276 us, with mma_kernel 266 and 274;
+// fp32 790 and 810, 829 and 848).
 inline bool few(int64_t T, int64_t d, int dtype) { return d >= 8 && T <= (dtype == kF32 ? 64 : 32); }
 
 // Rows of G per token: terms of a 16-bit G that the products take as tokens of their
