@@ -472,6 +472,85 @@ nq_status nq_vocab_loss_backward(const void* H, int64_t ldh, const void* W, int6
  * gradient). Host only; -1 for sizes out of range. */
 int64_t nq_vocab_loss_work_bytes(int64_t T, int64_t V, int64_t d, int32_t dtype, int32_t grad);
 
+/* Log probabilities over a large vocabulary, the T x V logits z = scale H W^T never
+ * kept (H, W, dtype, sizes, strides and scale as in nq_vocab_loss). Device float32
+ * unless said otherwise:
+ *   lse_t = log sum_v exp z_tv (T),
+ *   entropy_t = -sum_v p log p of p = exp(z - lse) (T),
+ *   logprobs_tg = z_t,tokens[t][g] - lse_t (T x G) for tokens (device int32, T x G,
+ *     row stride ldt): a negative one gives 0, one >= V NaN. G in 0 .. 128 (0: tokens
+ *     and logprobs may be NULL);
+ *   top_ids (int32), top_logprobs (T x k): the k words of the largest z and z - lse,
+ *     largest first, the lower word first where z are equal. k in 0 .. min(V, 128)
+ *     (0: both may be NULL).
+ * Each row has all its outputs whatever its tokens are. A row with a logit that is
+ * not finite (a NaN or an infinity in its row of H or in W, an overflow) has NaN in
+ * lse, entropy, logprobs (of words in 0 .. V - 1) and top_logprobs, -1 in top_ids.
+ * z is summed in the order that the sizes of the call give: equal calls give equal
+ * results; words whose z differ by less than its rounding may come in another
+ * order with another number of tokens.
+ * work: nq_vocab_logprobs_work_bytes(T, V, d, dtype, G, k) bytes, 16-byte aligned. All
+ * on `stream`, no allocation. T == 0 is a no-op. */
+nq_status nq_vocab_logprobs(const void* H, int64_t ldh, const void* W, int64_t ldw, int32_t dtype,
+                            int64_t T, int64_t V, int64_t d, const int32_t* tokens, int64_t ldt,
+                            int64_t G, int64_t k, float scale, float* logprobs, float* entropy,
+                            float* lse, int32_t* top_ids, float* top_logprobs, void* work,
+                            void* stream);
+
+/* Bytes of `work` for the call above. Host only; -1 for sizes out of range. */
+int64_t nq_vocab_logprobs_work_bytes(int64_t T, int64_t V, int64_t d, int32_t dtype, int64_t G,
+                                     int64_t k);
+
+/* Divergence KL(q || p) of a model's p = softmax(z), z = scale H W^T (as in
+ * nq_vocab_loss; scale: one over the temperature) from a teacher's K words per token
+ * ("方法步骤详情", stage 3: the objective that the scales are tuned by, with the teacher's
+ * distribution cut to its best words). ids (device int32, T x K, row stride ldi): words;
+ * a negative one is no entry, a token without entries is ignored. logq (device
+ * float32, T x K, row stride ldq): log probabilities, -infinity allowed. With lse_t
+ * = log sum_v exp z_tv:
+ *   tail != 0: q = exp logq, of which sum q <= 1 is expected; what is left, r = max(0,
+ *     1 - sum q), is one outcome, "another word", of probability exp(rest - lse),
+ *     rest_t = log sum exp z_tv over the words that the token does not list:
+ *     loss_t = sum_k q_k (logq_k - z_t,ids[k] + lse_t) + r (log r - rest_t + lse_t);
+ *     where every word is listed, rest is -infinity and r counts as 0;
+ *   tail == 0: q = softmax of logq over the token's entries (logq may be logits):
+ *     loss_t = sum_k q_k (log q_k - z_t,ids[k] + lse_t); rest = lse.
+ * Terms with q = 0 or r = 0 are 0. A word listed more than once has the sum of its
+ * entries' terms. loss, lse, rest (T) and hit (T x K: z of each entry, 0 for none) are
+ * device float32, lse, rest and hit for the gradient. An ignored token has 0 in all
+ * of them and its row of H is not used; one with a word >= V has NaN in loss and in
+ * that hit; a logit that is not finite gives NaN in its token's loss and lse. K in 1 ..
+ * 128. work: nq_vocab_distill_work_bytes(T, V, d, dtype, K, 0) bytes, 16-byte
+ * aligned. All on `stream`, no allocation; sums run in a fixed order. T == 0 is a no-op. */
+nq_status nq_vocab_distill(const void* H, int64_t ldh, const void* W, int64_t ldw, int32_t dtype,
+                           int64_t T, int64_t V, int64_t d, const int32_t* ids, int64_t ldi,
+                           const float* logq, int64_t ldq, int64_t K, float scale, int32_t tail,
+                           float* loss, float* lse, float* rest, float* hit, void* work,
+                           void* stream);
+
+/* Gradient of sum_t dloss_t loss_t from the lse, rest and hit of nq_vocab_distill on the
+ * same arguments (and in one call: see nq_vocab_loss_backward, whose products, types,
+ * roundings and limits these are): with Q = sum q + r (1 where tail == 0),
+ *   G_tv = (Q exp(z_tv - lse_t) - sum of q over v's entries) dloss_t scale, v listed,
+ *   G_tv = exp(z_tv - rest_t) (Q exp(rest_t - lse_t) - r) dloss_t scale, v not listed,
+ *   dH (T x d, row stride lddh) = G W,   dW (V x d, row stride lddw) = G^T H
+ * in H's type, written (not added to); one of them may be NULL. Nothing flows to logq.
+ * Ignored tokens get zero rows of dH and add nothing to dW; a word >= V gives NaN in its
+ * token's row of dH and in dW. work: nq_vocab_distill_work_bytes(T, V, d, dtype, K, 1)
+ * bytes, 16-byte aligned. T == 0 is a no-op with dW == NULL and an error with it. */
+nq_status nq_vocab_distill_backward(const void* H, int64_t ldh, const void* W, int64_t ldw,
+                                    int32_t dtype, int64_t T, int64_t V, int64_t d,
+                                    const int32_t* ids, int64_t ldi, const float* logq, int64_t ldq,
+                                    int64_t K, float scale, int32_t tail, const float* lse,
+                                    const float* rest, const float* hit, const float* dloss,
+                                    void* dH, int64_t lddh, void* dW, int64_t lddw, void* work,
+                                    void* stream);
+
+/* Bytes of `work` for the two calls above (grad: 0 for the loss, 1 for its
+ * gradient). Host only; -1 for sizes out of range. */
+int64_t nq_vocab_distill_work_bytes(int64_t T, int64_t V, int64_t d, int32_t dtype, int64_t K,
+                                    int32_t grad);
+
 /* ---- building blocks (the same kernels the run uses; for tests and tools) ----
  * These take caller buffers of any shape, copy into zero-padded temporaries
  * (hipMalloc, freed before the call returns), run the kernels on `stream`,

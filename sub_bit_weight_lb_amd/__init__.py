@@ -12,6 +12,7 @@ Functions mirror the C names without the ``nq_`` prefix:
     transpose_signs / binary_matmul / binary_matmul_noalloc / lw_* (LedoitWolf) /
     ste_* (STERefiner) / act8_quantize / act8_dequantize / act8_steps (Act8) /
     binary_matmul_backward / vocab_loss / vocab_loss_backward /
+    vocab_logprobs (VocabLogprobs) / vocab_distill / vocab_distill_backward (VocabDistill) /
     op_precondition / op_gram / op_gemm_rhs / op_cholesky_inverse / op_svid
 plus the conveniences ``LBADMM`` (a handle object) and ``lbadmm`` (one call).
 """
@@ -33,6 +34,8 @@ __all__ = [
     "Act8", "ACT8_GROUP", "act8_quantize", "act8_dequantize", "act8_steps",
     "binary_matmul_backward", "binary_matmul_backward_work_bytes",
     "vocab_loss", "vocab_loss_backward", "vocab_loss_work_bytes",
+    "VocabLogprobs", "vocab_logprobs", "vocab_logprobs_work_bytes",
+    "VocabDistill", "vocab_distill", "vocab_distill_backward", "vocab_distill_work_bytes",
     "preconditioners", "STERefiner", "cosine_lr", "op_precondition", "op_gram",
     "op_gemm_rhs", "op_sign_gemm", "op_cholesky_inverse", "op_svid", "LBADMM", "lbadmm", "Result",
     "status_string", "version",
@@ -603,15 +606,19 @@ def vocab_loss_work_bytes(T, V, d, dtype, grad=False):
                                                     _dtype_code(dtype, "dtype"), int(bool(grad))))
 
 
-def _vocab_args(H, W, labels):
-    torch = _torch()
+def _head_args(H, W):
     T, d, ldh = _matrix(H, "H")
     V, _, ldw = _matrix(W, "W", None, d, H.dtype)
     code = _dtype_code(H.dtype, "H")
-    _vector(labels, "labels", T, torch.int32)
     if V < 1 or d < 1:
         raise ValueError("the vocabulary and the hidden size must be >= 1")
     return T, V, d, code, ldh, ldw
+
+
+def _vocab_args(H, W, labels):
+    args = _head_args(H, W)
+    _vector(labels, "labels", args[0], _torch().int32)
+    return args
 
 
 def vocab_loss(H, W, labels, scale=1.0, loss=None, lse=None, work=None, stream=None):
@@ -678,6 +685,203 @@ def vocab_loss_backward(H, W, labels, lse, dloss, scale=1.0, want_dH=True, want_
         _check(lib.nq_vocab_loss_backward(
             _p(H), ldh, _p(W), ldw, code, T, V, d, _p(labels), float(scale), _p(lse), _p(dloss),
             _p(gH), lddh, _p(gW), lddw, _p(w), handle), "nq_vocab_loss_backward")
+        return gH, gW
+    return on.call(stream, run)
+
+
+# words that a token can list or be given, and its best words at most
+VOCAB_MAX_LISTED = 128
+
+
+@dataclass
+class VocabLogprobs:
+    """What vocab_logprobs finds for T rows: logprobs (the shape of tokens; None
+    without), entropy and lse (T), top_ids (T x k int32) and top_logprobs (T x k);
+    float32 unless said otherwise."""
+    logprobs: "object"
+    entropy: "object"
+    lse: "object"
+    top_ids: "object"
+    top_logprobs: "object"
+
+
+def vocab_logprobs_work_bytes(T, V, d, dtype, given=0, k=0):
+    """Bytes of workspace vocab_logprobs needs for T rows, V words, hidden size d,
+    H and W of dtype, `given` tokens per row and k best words."""
+    return int(_lib.load().nq_vocab_logprobs_work_bytes(
+        int(T), int(V), int(d), _dtype_code(dtype, "dtype"), int(given), int(k)))
+
+
+def vocab_logprobs(H, W, tokens=None, k=0, scale=1.0, out=None, work=None, stream=None):
+    """Log probabilities under softmax of z = scale H W^T, which is never kept: H
+    (T x d) and W (V x d) float32, bfloat16 or float16 with unit column stride.
+    tokens (T, or T x G with G <= 128; int32): the words whose log probability is
+    wanted, a negative one gives 0, one >= V NaN. Returns a VocabLogprobs with those,
+    each row's entropy and lse = log sum exp z, and its k best words (k <= 128) with
+    their log probabilities, best first, the lower word first among equals. out, if
+    given, is a VocabLogprobs of contiguous tensors to fill; work holds
+    vocab_logprobs_work_bytes(T, V, d, H.dtype, G, k) bytes. A row with a logit that
+    is not finite has NaN and the words -1."""
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
+    T, V, d, code, ldh, ldw = _head_args(H, W)
+    k, given, ldt = int(k), 0, 1
+    if not 0 <= k <= min(VOCAB_MAX_LISTED, V):
+        raise ValueError(f"k must be in 0 .. {min(VOCAB_MAX_LISTED, V)}")
+    if tokens is not None:
+        flat = isinstance(tokens, torch.Tensor) and tokens.dim() == 1
+        if flat:
+            _vector(tokens, "tokens", T, i32)
+            given = 1
+        else:
+            _, given, ldt = _matrix(tokens, "tokens", T, None, i32)
+        if given > VOCAB_MAX_LISTED:
+            raise ValueError(f"a row has at most {VOCAB_MAX_LISTED} tokens")
+    if out is not None:
+        if not isinstance(out, VocabLogprobs):
+            raise TypeError("out must be a VocabLogprobs")
+        if tokens is not None:
+            _vector(out.logprobs, "out.logprobs", T * given, f32)
+        _vector(out.entropy, "out.entropy", T, f32)
+        _vector(out.lse, "out.lse", T, f32)
+        if k:
+            _vector(out.top_ids, "out.top_ids", T * k, i32)
+            _vector(out.top_logprobs, "out.top_logprobs", T * k, f32)
+        on = _on_device("H W tokens logprobs entropy lse top_ids top_logprobs work", H, W, tokens,
+                        out.logprobs, out.entropy, out.lse, out.top_ids, out.top_logprobs, work)
+    else:
+        on = _on_device("H W tokens work", H, W, tokens, work)
+
+    def run(handle):
+        o = out
+        if o is None:
+            def new(shape, dtype=f32):
+                return torch.empty(shape, dtype=dtype, device=H.device)
+            o = VocabLogprobs(None if tokens is None else new(tokens.shape), new(T), new(T),
+                              new((T, k), i32), new((T, k)))
+        lib = _lib.load()
+        w = _workspace(work, lib.nq_vocab_logprobs_work_bytes(T, V, d, code, given, k), H.device)
+        _check(lib.nq_vocab_logprobs(
+            _p(H), ldh, _p(W), ldw, code, T, V, d, _p(tokens), ldt, given, k, float(scale),
+            _p(o.logprobs), _p(o.entropy), _p(o.lse), _p(o.top_ids), _p(o.top_logprobs), _p(w),
+            handle), "nq_vocab_logprobs")
+        return o
+    return on.call(stream, run)
+
+
+@dataclass
+class VocabDistill:
+    """What vocab_distill hands to its gradient for T tokens with K entries each: lse
+    and rest (T) and hit (T x K), float32."""
+    lse: "object"
+    rest: "object"
+    hit: "object"
+
+
+def vocab_distill_work_bytes(T, V, d, dtype, K, grad=False):
+    """Bytes of workspace vocab_distill (or, with grad, vocab_distill_backward) needs
+    for T tokens of K entries, V words, hidden size d and H, W of dtype."""
+    return int(_lib.load().nq_vocab_distill_work_bytes(
+        int(T), int(V), int(d), _dtype_code(dtype, "dtype"), int(K), int(bool(grad))))
+
+
+def _distill_args(H, W, ids, logq):
+    torch = _torch()
+    T, V, d, code, ldh, ldw = _head_args(H, W)
+    _, K, ldi = _matrix(ids, "ids", T, None, torch.int32)
+    _, _, ldq = _matrix(logq, "logq", T, K, torch.float32)
+    if not 1 <= K <= VOCAB_MAX_LISTED:
+        raise ValueError(f"a token lists 1 .. {VOCAB_MAX_LISTED} words")
+    return T, V, d, code, ldh, ldw, K, ldi, ldq
+
+
+def _distill_state(q, T, K):
+    f32 = _torch().float32
+    if not isinstance(q, VocabDistill):
+        raise TypeError("the loss's state must be a VocabDistill")
+    _vector(q.lse, "lse", T, f32)
+    _vector(q.rest, "rest", T, f32)
+    _vector(q.hit, "hit", T * K, f32)
+
+
+def vocab_distill(H, W, ids, logq, scale=1.0, tail=True, loss=None, state=None, work=None,
+                  stream=None):
+    """KL divergence of softmax(z), z = scale H W^T never kept, from a teacher's K <=
+    128 words per token: ids (T x K int32; a negative one is no entry, a token without
+    any is ignored) and their log probabilities logq (T x K float32), as
+    vocab_logprobs gives them for the teacher (at its own scale: one over the
+    temperature). tail: the rest of the teacher's mass, 1 - sum exp logq, is one
+    outcome more, "another word"; without it logq is normalised over a token's
+    entries (and may be logits). Returns (loss, state): T float32, 0 for an ignored
+    token, and the VocabDistill that vocab_distill_backward takes; both can be given
+    to be filled. A word >= V gives NaN; one listed twice counts with both entries.
+    work, if given, holds vocab_distill_work_bytes(T, V, d, H.dtype, K) bytes."""
+    torch = _torch()
+    f32 = torch.float32
+    T, V, d, code, ldh, ldw, K, ldi, ldq = _distill_args(H, W, ids, logq)
+    if loss is not None:
+        _vector(loss, "loss", T, f32)
+    if state is not None:
+        _distill_state(state, T, K)
+        given = (state.lse, state.rest, state.hit)
+    else:
+        given = (None, None, None)
+    on = _on_device("H W ids logq loss lse rest hit work", H, W, ids, logq, loss, *given, work)
+
+    def run(handle):
+        def new(*shape):
+            return torch.empty(shape, dtype=f32, device=H.device)
+        a = new(T) if loss is None else loss
+        q = VocabDistill(new(T), new(T), new(T, K)) if state is None else state
+        lib = _lib.load()
+        w = _workspace(work, lib.nq_vocab_distill_work_bytes(T, V, d, code, K, 0), H.device)
+        _check(lib.nq_vocab_distill(
+            _p(H), ldh, _p(W), ldw, code, T, V, d, _p(ids), ldi, _p(logq), ldq, K, float(scale),
+            int(bool(tail)), _p(a), _p(q.lse), _p(q.rest), _p(q.hit), _p(w), handle),
+            "nq_vocab_distill")
+        return a, q
+    return on.call(stream, run)
+
+
+def vocab_distill_backward(H, W, ids, logq, state, dloss, scale=1.0, tail=True, want_dH=True,
+                           want_dW=True, dH=None, dW=None, work=None, stream=None):
+    """Gradient of sum(dloss * loss) for (loss, state) = vocab_distill(H, W, ids,
+    logq, scale, tail) of one call with these tokens: returns (dH, dW) in H's type
+    (None where not wanted). dloss is T float32. The logits are computed again in
+    pieces of the vocabulary. Ignored tokens get zero rows of dH and add nothing to
+    dW. Outputs must not share memory with inputs. work, if given, holds
+    vocab_distill_work_bytes(T, V, d, H.dtype, K, grad=True) bytes."""
+    torch = _torch()
+    T, V, d, code, ldh, ldw, K, ldi, ldq = _distill_args(H, W, ids, logq)
+    _distill_state(state, T, K)
+    _vector(dloss, "dloss", T, torch.float32)
+    lddh = lddw = d
+    if dH is not None:
+        _, _, lddh = _matrix(dH, "dH", T, d, H.dtype)
+    if dW is not None:
+        _, _, lddw = _matrix(dW, "dW", V, d, H.dtype)
+    want_dH, want_dW = want_dH or dH is not None, want_dW or dW is not None
+    if not (want_dH or want_dW):
+        raise ValueError("neither dH nor dW is wanted")
+    on = _on_device("H W ids logq lse rest hit dloss dH dW work", H, W, ids, logq, state.lse,
+                    state.rest, state.hit, dloss, dH, dW, work)
+
+    def run(handle):
+        gH, gW = dH, dW
+        if want_dH and gH is None:
+            gH = torch.empty((T, d), dtype=H.dtype, device=H.device)
+        if want_dW and gW is None:
+            gW = torch.empty((V, d), dtype=H.dtype, device=H.device)
+        if T == 0:
+            if gW is not None:
+                gW.zero_()
+            return gH, gW
+        lib = _lib.load()
+        w = _workspace(work, lib.nq_vocab_distill_work_bytes(T, V, d, code, K, 1), H.device)
+        _check(lib.nq_vocab_distill_backward(
+            _p(H), ldh, _p(W), ldw, code, T, V, d, _p(ids), ldi, _p(logq), ldq, K, float(scale),
+            int(bool(tail)), _p(state.lse), _p(state.rest), _p(state.hit), _p(dloss), _p(gH), lddh,
+            _p(gW), lddw, _p(w), handle), "nq_vocab_distill_backward")
         return gH, gW
     return on.call(stream, run)
 

@@ -9,6 +9,7 @@
 
 #include "abi.h"
 #include "tune.h"
+#include "vocab_plan.h"
 
 using namespace nq;
 
@@ -41,9 +42,8 @@ constexpr int64_t kMaxTokens = int64_t(1) << 20, kMaxVocab = int64_t(1) << 24;
 constexpr int64_t kMaxHidden = int64_t(1) << 18, kMaxLd = int64_t(1) << 21;
 constexpr int64_t kMaxLogits = int64_t(1) << 38;
 
-nq_status check_vocab(const void* H, int64_t ldh, const void* W, int64_t ldw, int32_t dtype,
-                      int64_t T, int64_t V, int64_t d, const int32_t* labels, float scale,
-                      const void* work) {
+nq_status check_head(const void* H, int64_t ldh, const void* W, int64_t ldw, int32_t dtype,
+                     int64_t T, int64_t V, int64_t d, float scale, const void* work) {
   if (!dtype_ok(dtype)) return bad("dtype must be NQ_F32, NQ_BF16 or NQ_F16");
   if (T < 0 || T > kMaxTokens) return bad("T must be in [0, 2^20]");
   if (V < 1 || V > kMaxVocab) return bad("V must be in [1, 2^24]");
@@ -51,13 +51,38 @@ nq_status check_vocab(const void* H, int64_t ldh, const void* W, int64_t ldw, in
   if (T * V > kMaxLogits) return bad("T V must be <= 2^38");
   if (!std::isfinite(scale)) return bad("scale must be finite");
   if (T == 0) return NQ_OK;
-  if (!H || !W || !labels || !work) return bad("H, W, labels and work are required");
+  if (!H || !W || !work) return bad("H, W and work are required");
   if (ldh < d || ldw < d) return bad("ldh < d or ldw < d");
   if (ldh > kMaxLd || ldw > kMaxLd) return bad("ldh and ldw must be <= 2^21");
   if (misaligned(H, dtype_bytes(dtype)) || misaligned(W, dtype_bytes(dtype)))
     return bad("H or W is not aligned to its type");
   if (misaligned(work, 16)) return bad("work must be 16-byte aligned");
   return NQ_OK;
+}
+nq_status check_vocab(const void* H, int64_t ldh, const void* W, int64_t ldw, int32_t dtype,
+                      int64_t T, int64_t V, int64_t d, const int32_t* labels, float scale,
+                      const void* work) {
+  const nq_status st = check_head(H, ldh, W, ldw, dtype, T, V, d, scale, work);
+  return st == NQ_OK && T > 0 && !labels ? bad("labels are required") : st;
+}
+bool head_ok(int64_t T, int64_t V, int64_t d, int32_t dtype) {
+  return dtype_ok(dtype) && T >= 0 && V >= 1 && d >= 1 && T <= kMaxTokens && V <= kMaxVocab &&
+         d <= kMaxHidden && T * V <= kMaxLogits;
+}
+nq_status check_listed(const int32_t* ids, int64_t ldi, const float* logq, int64_t ldq, int64_t K) {
+  if (K < 1 || K > vocab::kMaxListed) return bad("K must be in [1, 128]");
+  if (!ids || !logq) return bad("ids and logq are required");
+  if (ldi < K || ldq < K) return bad("ldi < K or ldq < K");
+  if (ldi > kMaxLd || ldq > kMaxLd) return bad("ldi and ldq must be <= 2^21");
+  if (misaligned(ids, 4) || misaligned(logq, 4)) return bad("ids or logq is not aligned to its type");
+  return NQ_OK;
+}
+Vocab head(const void* H, int64_t ldh, const void* W, int64_t ldw, int32_t dtype, int64_t T, int64_t V,
+           int64_t d, float scale, void* work) {
+  Vocab a{};
+  a.H = H; a.W = W; a.dtype = dtype; a.ldh = ldh; a.ldw = ldw; a.T = T; a.V = V; a.d = d;
+  a.scale = scale; a.work = work;
+  return a;
 }
 
 }  // namespace
@@ -203,6 +228,93 @@ nq_status nq_vocab_loss_backward(const void* H, int64_t ldh, const void* W, int6
   a.labels = labels; a.scale = scale; a.lse = (float*)lse; a.dloss = dloss;
   a.dH = dH; a.lddh = lddh; a.dW = dW; a.lddw = lddw; a.work = work;
   NQ_HIPCHK(launch_vocab_loss_backward(a, (hipStream_t)stream));
+  return NQ_OK;
+}
+
+int64_t nq_vocab_logprobs_work_bytes(int64_t T, int64_t V, int64_t d, int32_t dtype, int64_t G,
+                                     int64_t k) {
+  if (!head_ok(T, V, d, dtype) || G < 0 || k < 0 || G > vocab::kMaxListed || k > vocab::kMaxListed || k > V)
+    return -1;
+  return T == 0 ? 0 : logprobs_work_bytes(T, V, d, dtype, G, k);
+}
+
+nq_status nq_vocab_logprobs(const void* H, int64_t ldh, const void* W, int64_t ldw, int32_t dtype,
+                            int64_t T, int64_t V, int64_t d, const int32_t* tokens, int64_t ldt,
+                            int64_t G, int64_t k, float scale, float* logprobs, float* entropy,
+                            float* lse, int32_t* top_ids, float* top_logprobs, void* work,
+                            void* stream) {
+  const nq_status st = check_head(H, ldh, W, ldw, dtype, T, V, d, scale, work);
+  if (st != NQ_OK) return st;
+  if (G < 0 || G > vocab::kMaxListed) return bad("G must be in [0, 128]");
+  if (k < 0 || k > vocab::kMaxListed) return bad("k must be in [0, 128]");
+  if (k > V) return bad("k > V");
+  if (T == 0) return NQ_OK;
+  if (!entropy || !lse) return bad("entropy and lse are required");
+  if (G && (!tokens || !logprobs)) return bad("tokens and logprobs are required");
+  if (G && (ldt < G || ldt > kMaxLd)) return bad("ldt must be in [G, 2^21]");
+  if (k && (!top_ids || !top_logprobs)) return bad("top_ids and top_logprobs are required");
+  if (misaligned(tokens, 4) || misaligned(logprobs, 4) || misaligned(entropy, 4) ||
+      misaligned(lse, 4) || misaligned(top_ids, 4) || misaligned(top_logprobs, 4))
+    return bad("tokens or an output is not aligned to its type");
+  Logprobs a{};
+  a.v = head(H, ldh, W, ldw, dtype, T, V, d, scale, work);
+  a.tokens = tokens; a.given = G; a.ldt = ldt; a.k = k;
+  a.logprobs = logprobs; a.entropy = entropy; a.lse = lse;
+  a.top_ids = top_ids; a.top_logprobs = top_logprobs;
+  NQ_HIPCHK(launch_vocab_logprobs(a, (hipStream_t)stream));
+  return NQ_OK;
+}
+
+int64_t nq_vocab_distill_work_bytes(int64_t T, int64_t V, int64_t d, int32_t dtype, int64_t K,
+                                    int32_t grad) {
+  if (!head_ok(T, V, d, dtype) || K < 1 || K > vocab::kMaxListed) return -1;
+  return T == 0 ? 0 : distill_work_bytes(T, V, d, dtype, K, grad != 0);
+}
+
+nq_status nq_vocab_distill(const void* H, int64_t ldh, const void* W, int64_t ldw, int32_t dtype,
+                           int64_t T, int64_t V, int64_t d, const int32_t* ids, int64_t ldi,
+                           const float* logq, int64_t ldq, int64_t K, float scale, int32_t tail,
+                           float* loss, float* lse, float* rest, float* hit, void* work,
+                           void* stream) {
+  nq_status st = check_head(H, ldh, W, ldw, dtype, T, V, d, scale, work);
+  if (st != NQ_OK || T == 0) return st;
+  if ((st = check_listed(ids, ldi, logq, ldq, K)) != NQ_OK) return st;
+  if (!loss || !lse || !rest || !hit) return bad("loss, lse, rest and hit are required");
+  if (misaligned(loss, 4) || misaligned(lse, 4) || misaligned(rest, 4) || misaligned(hit, 4))
+    return bad("an output is not aligned to its type");
+  Distill a{};
+  a.v = head(H, ldh, W, ldw, dtype, T, V, d, scale, work);
+  a.ids = ids; a.logq = logq; a.K = K; a.ldi = ldi; a.ldq = ldq; a.tail = tail != 0;
+  a.loss = loss; a.lse = lse; a.rest = rest; a.hit = hit;
+  NQ_HIPCHK(launch_vocab_distill(a, (hipStream_t)stream));
+  return NQ_OK;
+}
+
+nq_status nq_vocab_distill_backward(const void* H, int64_t ldh, const void* W, int64_t ldw,
+                                    int32_t dtype, int64_t T, int64_t V, int64_t d,
+                                    const int32_t* ids, int64_t ldi, const float* logq, int64_t ldq,
+                                    int64_t K, float scale, int32_t tail, const float* lse,
+                                    const float* rest, const float* hit, const float* dloss,
+                                    void* dH, int64_t lddh, void* dW, int64_t lddw, void* work,
+                                    void* stream) {
+  if (T == 0 && dW && V >= 1 && d >= 1)
+    return bad("T == 0: there is no gradient (dW is all zero)");
+  nq_status st = check_head(H, ldh, W, ldw, dtype, T, V, d, scale, work);
+  if (st != NQ_OK || T == 0) return st;
+  if ((st = check_listed(ids, ldi, logq, ldq, K)) != NQ_OK) return st;
+  if (!lse || !rest || !hit || !dloss) return bad("lse, rest, hit and dloss are required");
+  if (!dH && !dW) return bad("dH or dW is required");
+  if ((dH && lddh < d) || (dW && lddw < d)) return bad("lddh < d or lddw < d");
+  if (misaligned(dH, dtype_bytes(dtype)) || misaligned(dW, dtype_bytes(dtype)))
+    return bad("dH or dW is not aligned to its type");
+  if (misaligned(lse, 4) || misaligned(rest, 4) || misaligned(hit, 4) || misaligned(dloss, 4))
+    return bad("lse, rest, hit or dloss is not aligned to its type");
+  Distill a{};
+  a.v = head(H, ldh, W, ldw, dtype, T, V, d, scale, work);
+  a.v.dloss = dloss; a.v.dH = dH; a.v.lddh = lddh; a.v.dW = dW; a.v.lddw = lddw;
+  a.ids = ids; a.logq = logq; a.K = K; a.ldi = ldi; a.ldq = ldq; a.tail = tail != 0;
+  a.lse = (float*)lse; a.rest = (float*)rest; a.hit = (float*)hit;
+  NQ_HIPCHK(launch_vocab_distill_backward(a, (hipStream_t)stream));
   return NQ_OK;
 }
 

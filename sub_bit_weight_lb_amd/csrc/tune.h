@@ -106,9 +106,39 @@ struct Vocab {
   void *dH, *dW;                     // T x d, V x d (gradient; either nullable)
   int64_t lddh, lddw;
   void* work;                        // vocab_work_bytes, 16-byte aligned
+  // a gradient whose G is exp(z - lse) share dloss scale, but val dloss scale at the
+  // `listed` words of each token (0: none; a negative one: no entry); wr: T, scratch
+  const float* share;
+  float* wr;
+  const int32_t* ids;
+  int64_t listed, ldi;
+  const float* val;                  // T x listed
 };
 int64_t vocab_work_bytes(int64_t T, int64_t V, int64_t d, int dtype, bool grad);
 hipError_t launch_vocab_loss(const Vocab& a, hipStream_t s);
 hipError_t launch_vocab_loss_backward(const Vocab& a, hipStream_t s);
+
+// ---------------------------------------------------------------- single logits (vocab_top.hip)
+struct Logprobs {
+  Vocab v;                           // H, W, sizes, scale, work
+  const int32_t* tokens;             // T x given, ldt apart; negative: none
+  int64_t given, ldt, k;
+  float *logprobs, *entropy, *lse;   // T x given, T, T
+  int32_t* top_ids;                  // T x k
+  float* top_logprobs;
+};
+struct Distill {
+  Vocab v;                           // H, W, sizes, scale, dloss, dH, dW, work
+  const int32_t* ids;                // T x K, ldi apart; negative: no entry
+  const float* logq;                 // T x K, ldq apart
+  int64_t K, ldi, ldq;
+  int tail;
+  float *loss, *lse, *rest, *hit;    // T, T, T, T x K; but for loss read by the gradient
+};
+int64_t logprobs_work_bytes(int64_t T, int64_t V, int64_t d, int dtype, int64_t given, int64_t k);
+int64_t distill_work_bytes(int64_t T, int64_t V, int64_t d, int dtype, int64_t K, bool grad);
+hipError_t launch_vocab_logprobs(const Logprobs& a, hipStream_t s);
+hipError_t launch_vocab_distill(const Distill& a, hipStream_t s);
+hipError_t launch_vocab_distill_backward(const Distill& a, hipStream_t s);
 
 }  // namespace nq

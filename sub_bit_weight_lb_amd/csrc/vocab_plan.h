@@ -1,5 +1,6 @@
-// Sizes, workspace layout and launch rules of the loss over a vocabulary
-// (vocab.hip). Host code alone, without HIP: tests compile it by itself.
+// Sizes, workspace layout and launch rules of the operators over a vocabulary
+// (vocab.hip, vocab_top.hip). Host code alone, without HIP: tests compile it by
+// itself.
 #pragma once
 
 #include <algorithm>
@@ -87,7 +88,8 @@ inline int dh_slices(int64_t T, int64_t d, int64_t piece) {
 // Words per piece: G, and a copy of W's piece where one is needed, hold at most
 // 2^26 values each (two thousand words at least), which leaves the fp32 sums of
 // dH, read and written once per piece, a few percent of the piece's products.
-inline Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad) {
+// (kept: the operands of a product whose results have their place in a KeepPlan.)
+inline Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad, bool kept = false) {
   Plan p{};
   const int nt = terms(dtype);
   p.dp = round_up(d, BK);
@@ -102,7 +104,7 @@ inline Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad) {
     off += round_up(bytes, 256);
     return at;
   };
-  if (!grad) {
+  if (!grad && !kept) {
     // partials per token: one per 64 words, or two per tile's words (W in place or
     // in pieces)
     const bool tiny = !few(T, d, dtype) && (tile_for(V, T) == 64 || tile_for(p.piece, T) == 64);
@@ -132,6 +134,64 @@ inline Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad) {
   }
   p.bytes = off;
   return p;
+}
+
+// ---------------------------------------------------------------- single logits (vocab_top.hip)
+constexpr int64_t kMaxListed = 128;   // words that a token can list, and its best words
+constexpr int64_t kKeep = int64_t(1) << 27;   // values of one kind that are kept at most
+
+constexpr int64_t kFirst = 8192;              // words of the first step
+
+// What a call keeps of the logits of `block` tokens at a time: the sums of every group of
+// words; the groups of listed words in a slot each; and, to find the best words, the
+// groups that may hold one of them, of a step of the vocabulary at a time.
+struct KeepPlan {
+  Plan p;                     // of the operands
+  bool few;                   // score_kernel's: all logits are kept, in one step
+  int tile;
+  int64_t group, groups;      // words of a group, groups of a token
+  int64_t block;              // tokens at a time
+  int64_t first, step;        // words of the first step and of the largest (0: no best words)
+  int64_t lds, ldz;           // bytes of a token's slots, its row of kept logits
+  int64_t stat, slot, zslot, z, best, thr, bytes;
+};
+inline KeepPlan keep_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t listed, int64_t top) {
+  KeepPlan k{};
+  k.few = few(T, d, dtype);
+  if (!k.few) k.p = plan_for(T, V, d, dtype, false, true);
+  k.tile = k.few ? 128 : tile_for(V, T);
+  k.group = k.tile / 2;
+  k.groups = (V + k.group - 1) / k.group;
+  k.block = T;
+  if (!k.few) {
+    int64_t most = std::min(kKeep / std::max<int64_t>(listed * k.group, 1), kKeep / (4 * k.groups));
+    if (top) most = std::min(most, kKeep / std::min(round_up(V, 256), kFirst));
+    k.block = std::min(T, std::max<int64_t>(256, most / 256 * 256));
+  }
+  if (k.few) {
+    k.ldz = round_up(V, 64);
+  } else if (top) {
+    k.step = std::min(round_up(V, 256), std::max(kFirst, kKeep / k.block / 256 * 256));
+    k.first = std::min(k.step, kFirst);
+    k.ldz = k.step;
+  }
+  k.lds = round_up(k.groups, 16);
+  int64_t off = round_up(k.p.bytes, 256);
+  auto take = [&](int64_t bytes) {
+    const int64_t at = off;
+    off += round_up(bytes, 256);
+    return at;
+  };
+  k.stat = take(16 * k.block * k.groups);
+  k.z = take(4 * k.block * k.ldz);
+  if (!k.few && listed) {
+    k.slot = take(k.block * k.lds);
+    k.zslot = take(4 * k.block * listed * k.group);
+  }
+  k.best = take(8 * k.block * top);
+  k.thr = take(4 * k.block);
+  k.bytes = off;
+  return k;
 }
 
 }  // namespace vocab

@@ -1,0 +1,699 @@
+// What is asked of single logits of a large vocabulary, which are never kept as a
+// whole (z = scale H W^T, the products of vocab_product.h):
+//
+// Log probabilities, to score a model and to write down what it holds likely:
+//   lse_t = log sum_v exp z_tv,  log p = z - lse of the given words,
+//   entropy_t = -sum_v p log p = log S - U / S,  S = sum exp(z - m), U = sum
+//   exp(z - m) (z - m), m the largest z (both terms are 0 or more; S - 1 is summed by itself),
+//   the k largest z, the lower word first among equals.
+// Divergence from a teacher's K words with log probabilities logq, KL(q || p):
+//   q = exp logq, r = max(0, 1 - sum q), rest = log sum exp z over the words that are
+//   not listed, loss = sum q (logq - z + lse) + r (log r - rest + lse)
+//   (tail), or q = softmax(logq) over the token's entries, r = 0, rest = lse;
+//   its derivative by z_v, with Q = sum q + r: Q p_v - sum q of v's entries where v is
+//   listed, exp(z_v - rest) (Q exp(rest - lse) - r) where it is not (with r = 0 and rest
+//   = lse: Q p_v). Here rest is a sum of its own: what is left of exp lse without
+//   the listed words' part would be rounding where they hold all but 2^-20 of it.
+//
+// The product's epilogue kPick (up to 32 tokens, fp32 64: score_kernel) leaves, per token and
+// group of words, the largest z and the sums S and U about it, and the z of
+//   groups with a listed word: each has a slot, which slots_kernel gives;
+//   groups that may hold one of the best words: the vocabulary is taken in steps, and
+//   from the second on only groups with a z above the k-th best so far are written.
+// A workgroup per token (top_kernel, distill_kernel) then joins the groups.
+#include "vocab_product.h"
+
+namespace nq {
+namespace {
+
+constexpr int kList = (int)kMaxListed;
+const float kNaN = __builtin_nanf("");
+
+// ---------------------------------------------------------------- joins of sums
+// About the largest z of all, m: r = sum e - 1 and u = sum e (z - m), e = exp(z - m).
+// r is a sum of its own, so that log(1 + r) keeps the digits of a row that is all but certain.
+struct Sums {
+  float m, r, u;
+};
+constexpr Sums kNothing{kNegInf, -1.0f, 0.0f};   // (a sum of 0)
+__device__ __forceinline__ void join(Sums& a, Sums b) {
+  if (b.r == -1.0f) return;
+  if (a.r == -1.0f) {
+    a = b;
+    return;
+  }
+  const float n = fmaxf(a.m, b.m);
+  const float x = a.m - n, y = b.m - n;
+  const float p = __expf(x), q = __expf(y), as = 1.0f + a.r, bs = 1.0f + b.r;
+  a.r = x == 0.0f ? a.r + q * bs : b.r + p * as;
+  a.u = p * (a.u + x * as) + q * (b.u + y * bs);
+  a.m = n;
+}
+// Over the workgroup's NT threads, in a fixed order; all of them get the result. sm: three
+// floats per wave.
+template <int NT>
+__device__ __forceinline__ Sums join_all(Sums a, float* sm) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const Sums b{__shfl_xor(a.m, o), __shfl_xor(a.r, o), __shfl_xor(a.u, o)};
+    // (both sides of a pair join the lower lane's with the upper one's)
+    const bool up = threadIdx.x & o;
+    Sums l = up ? b : a;
+    join(l, up ? a : b);
+    a = l;
+  }
+  const int wave = threadIdx.x >> 6;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) {
+    sm[3 * wave] = a.m;
+    sm[3 * wave + 1] = a.r;
+    sm[3 * wave + 2] = a.u;
+  }
+  __syncthreads();
+  a = Sums{sm[0], sm[1], sm[2]};
+#pragma unroll
+  for (int w = 1; w < NT / 64; ++w) join(a, Sums{sm[3 * w], sm[3 * w + 1], sm[3 * w + 2]});
+  return a;
+}
+
+// ---------------------------------------------------------------- slots
+// slot[t][group] = the first of the token's K entries with a word in it, 255 for groups without
+// one. A workgroup per token.
+__global__ __launch_bounds__(kList) void slots_kernel(const int32_t* __restrict__ ids, int64_t ldi,
+                                                      int K, int64_t V, int group,
+                                                      uint8_t* __restrict__ slot, int64_t lds) {
+  __shared__ int gr[kList];
+  const int64_t t = blockIdx.x;
+  const int k = threadIdx.x;
+  uint8_t* row = slot + t * lds;
+  for (int64_t i = 16 * k; i < lds; i += 16 * kList)
+    *(u32x4*)(row + i) = u32x4{~0u, ~0u, ~0u, ~0u};
+  const int32_t id = k < K ? ids[t * ldi + k] : -1;
+  const int mine = id >= 0 && id < V ? id / group : -1;
+  gr[k] = mine;
+  __syncthreads();
+  if (mine < 0) return;
+  for (int j = 0; j < k; ++j)
+    if (gr[j] == mine) return;
+  row[mine] = (uint8_t)k;
+}
+
+// ---------------------------------------------------------------- log probabilities
+struct Top {
+  Kept kept;
+  int group;                 // words of a group
+  int64_t V, v0, g0, g1;     // the step's first word, its groups
+  int k, have;               // best words; whether `best` holds those of earlier steps
+  uint64_t* best;            // [token][k], best first
+  float* thr;                // [token]: the k-th best z
+  int last;                  // the last step: what follows is written
+  const int32_t* tokens;     // [token][ldt]
+  int64_t ldt;
+  int given;
+  float *logprobs, *entropy, *lse;
+  int32_t* top_ids;
+  float* top_logprobs;
+};
+// Order of the words: larger z first, then the lower word. 0: less than any.
+__device__ __forceinline__ uint32_t order_of(float z) {
+  const uint32_t b = __float_as_uint(z + 0.0f);   // (no zero below zero)
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ uint64_t key_of(float z, uint32_t word) {
+  return (uint64_t)order_of(z) << 32 | (uint32_t)~word;
+}
+
+// The best words of a step join those of earlier ones; in the last step the token's outputs
+// follow. A workgroup of NT threads per token.
+//   Bound: each thread takes the largest z of its share of the groups; the k-th largest of
+//   these is one that k words reach. Only groups that reach it are looked at: k, and few
+//   more where a thread has two.
+//   Their words above the bound go to a list in LDS, in any order (an atomic counter gives
+//   the places; keys are distinct, so that the order does not show). The list is cut to its k
+//   best, each key's place counted, where it has no room for a group, and at the end.
+template <int NT>
+__global__ __launch_bounds__(NT) void top_kernel(Top a) {
+  constexpr int kCap = 2048, NW = NT / 64;
+  __shared__ uint64_t list[kCap];
+  __shared__ uint32_t most[NT];
+  __shared__ int todo[NT];
+  __shared__ int count, left;
+  __shared__ uint32_t lim;
+  __shared__ float sm[3 * NW];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t t = blockIdx.x;
+  const f32x4* stat = a.kept.stat + t * a.kept.groups;
+  const int k = a.k;
+  if (k) {
+    uint64_t bound = 0;   // keys above it are in
+    uint32_t m = 0;
+    for (int64_t g = a.g0 + tid; g < a.g1; g += NT) m = max(m, order_of(stat[g][0]));
+    most[tid] = m;
+    if (a.have && tid < k) list[tid] = a.best[t * k + tid];
+    if (tid == 0) {
+      lim = 0;
+      count = a.have ? k : 0;
+    }
+    __syncthreads();
+    int above = 0;
+#pragma unroll 8
+    for (int j = 0; j < NT; ++j) above += most[j] > m || (most[j] == m && j < tid);
+    if (above == k - 1) lim = m;
+    __syncthreads();
+    if (lim) bound = ((uint64_t)lim << 32) - 1;
+    if (a.have && list[k - 1] > bound) bound = list[k - 1];
+    const float* z = a.kept.z + t * a.kept.ldz;
+    int n = a.have ? k : 0;
+    // cuts the list to its k best, in order
+    auto cut = [&]() {
+      uint64_t key[kCap / NT];
+      int place[kCap / NT];
+#pragma unroll
+      for (int i = 0; i < kCap / NT; ++i) {
+        key[i] = tid + i * NT < n ? list[tid + i * NT] : 0;
+        place[i] = kCap;
+      }
+#pragma unroll
+      for (int i = 0; i < kCap / NT; ++i) {
+        if (i * NT >= n) break;
+        int p = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) p += list[j] > key[i];
+        place[i] = key[i] ? p : kCap;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kCap / NT; ++i)
+        if (place[i] < k) list[place[i]] = key[i];
+      n = min(n, k);
+      if (tid == 0) count = n;
+      __syncthreads();
+      if (n == k && list[k - 1] > bound) bound = list[k - 1];
+    };
+    for (int64_t base = a.g0; base < a.g1; base += NT) {
+      if (tid == 0) left = 0;
+      __syncthreads();
+      const int64_t g = base + tid;
+      const bool in = g < a.g1 && key_of(stat[g][0], (uint32_t)(g * a.group)) > bound;
+      const uint64_t who = __ballot(in);
+      int at = 0;
+      if (lane == 0 && who) at = atomicAdd(&left, __popcll(who));
+      at = __shfl(at, 0);
+      if (in) todo[at + __popcll(who & ((uint64_t(1) << lane) - 1))] = (int)g;
+      __syncthreads();
+      const int c = left;
+      for (int b = 0; b < c;) {
+        if (n + a.group > kCap) cut();
+        const int end = min(c, b + (kCap - n) / a.group);
+        // four groups of a wave at a time, all their loads before the first use
+        for (int i = b + wave; i < end; i += 4 * NW) {
+          float x[4][2];
+          uint32_t w[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int e = i + q * NW;
+            w[q] = (uint32_t)(todo[min(e, end - 1)] * a.group) + lane;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const bool on = e < end && lane + 64 * h < a.group && w[q] + 64 * h < a.V;
+              x[q][h] = on ? z[w[q] + 64 * h - a.v0] : 0.0f;
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int e = i + q * NW;
+              const bool on = e < end && lane + 64 * h < a.group && w[q] + 64 * h < a.V;
+              const uint64_t key = key_of(x[q][h], w[q] + 64 * h);
+              const uint64_t who = __ballot(on && key > bound);
+              if (!who) continue;
+              int at = 0;
+              if (lane == 0) at = atomicAdd(&count, __popcll(who));
+              at = __shfl(at, 0);
+              if (on && key > bound) list[at + __popcll(who & ((uint64_t(1) << lane) - 1))] = key;
+            }
+        }
+        __syncthreads();
+        n = count;
+        b = end;
+        __syncthreads();   // (nobody adds to count before all have read it)
+      }
+    }
+    cut();
+    for (int i = n + tid; i < k; i += NT) list[i] = 0;   // (fewer: where z are not finite)
+    __syncthreads();
+    if (!a.last) {
+      if (tid < k) a.best[t * k + tid] = list[tid];
+      if (tid == 0) a.thr[t] = value_of((uint32_t)(list[k - 1] >> 32));
+      return;
+    }
+  }
+  Sums r = kNothing;
+  for (int64_t g = tid; g < a.kept.groups; g += NT) {
+    const f32x4 x = stat[g];
+    join(r, Sums{x[0], x[1], x[2]});
+  }
+  r = join_all<NT>(r, sm);
+  const float log_s = log1pf(r.r);
+  const bool fine = r.r == r.r;
+  if (tid == 0) {
+    a.lse[t] = r.m + log_s;
+    a.entropy[t] = log_s - r.u / (1.0f + r.r);
+  }
+  if (tid < k) {
+    const uint64_t key = list[tid];
+    a.top_ids[t * k + tid] = fine ? (int32_t)~(uint32_t)key : -1;
+    a.top_logprobs[t * k + tid] = fine ? value_of((uint32_t)(key >> 32)) - r.m - log_s : kNaN;
+  }
+  if (tid < a.given) {
+    const int32_t id = a.tokens[t * a.ldt + tid];
+    float x = id < 0 ? 0.0f : kNaN;
+    if (id >= 0 && id < a.V) {
+      const Kept& o = a.kept;
+      const float z = o.slot ? o.zslot[(t * o.slots + o.slot[t * o.lds + id / a.group]) * a.group + id % a.group]
+                             : o.z[t * o.ldz + id];
+      x = z - r.m - log_s;
+    }
+    a.logprobs[t * a.given + tid] = x;
+  }
+}
+
+// ---------------------------------------------------------------- divergence
+struct Near {
+  Kept kept;
+  int group;
+  int64_t V;
+  const int32_t* ids;
+  const float* logq;
+  int64_t ldi, ldq;
+  int K, tail;
+  float *loss, *lse, *rest, *hit;
+};
+// sum of x over a wave, in a fixed order; all lanes get it
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+  return x;
+}
+__device__ __forceinline__ double wave_max(double x) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) x = fmax(x, __shfl_xor(x, o));
+  return x;
+}
+// A teacher's probabilities of one token: entries lane and lane + 64 of a wave, in 64 bits (r is
+// what a sum near one leaves). on: whether the entry is one.
+struct Teacher {
+  double q[2], logq[2], sum, r;
+};
+__device__ __forceinline__ Teacher teacher(const float (&l)[2], const bool (&on)[2], bool tail) {
+  Teacher t;
+  double top = 0.0;
+  if (!tail) {
+    top = wave_max(fmax(on[0] ? (double)l[0] : -INFINITY, on[1] ? (double)l[1] : -INFINITY));
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    t.logq[i] = on[i] ? (double)l[i] - top : 0.0;
+    t.q[i] = on[i] ? exp(t.logq[i]) : 0.0;
+  }
+  t.sum = wave_sum(t.q[0] + t.q[1]);
+  if (!tail) {
+    const double log_sum = log(t.sum);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      t.q[i] /= t.sum;
+      t.logq[i] -= log_sum;
+    }
+    t.sum = t.sum == t.sum ? 1.0 : t.sum;
+  }
+  t.r = tail ? 1.0 - t.sum : 0.0;
+  t.r = t.r < 0.0 ? 0.0 : t.r;   // (a NaN stays)
+  return t;
+}
+
+// loss, lse, rest and hit of a token from its groups' sums and the z of its listed words. A
+// workgroup of NT threads per token.
+//   With a tail, the groups with listed words are left out of the groups' sums, and their
+//   other words are summed here from the slots.
+template <int NT>
+__global__ __launch_bounds__(NT) void distill_kernel(Near a) {
+  constexpr int NW = NT / 64;
+  __shared__ int owner[kList], grp[kList], word[kList];
+  __shared__ uint32_t out[kList][4];   // of the owner's group: the words that are listed
+  __shared__ float zs[kList];
+  __shared__ int used;
+  __shared__ float sm[3 * NW];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t t = blockIdx.x;
+  const Kept& o = a.kept;
+  f32x4* stat = o.stat + t * o.groups;
+  if (tid == 0) used = 0;
+  int32_t id = -1;
+  if (tid < kList) {
+    id = tid < a.K ? a.ids[t * a.ldi + tid] : -1;
+    word[tid] = id;
+    grp[tid] = id >= 0 && id < a.V ? id / a.group : -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[tid][i] = 0;
+  }
+  __syncthreads();
+  auto logits = [&](int own) {   // the owner's group
+    return o.slot ? o.zslot + (t * o.slots + own) * a.group : o.z + t * o.ldz + (int64_t)grp[own] * a.group;
+  };
+  if (tid < kList) {
+    int own = tid;
+    const int mine = grp[tid];
+    if (mine >= 0)
+      for (int j = tid - 1; j >= 0; --j) own = grp[j] == mine ? j : own;
+    owner[tid] = mine >= 0 ? own : -1;
+    if (id >= 0) used = 1;   // (all write the same)
+    float z = id < 0 ? 0.0f : kNaN;
+    if (mine >= 0) {
+      const int in = id - mine * a.group;
+      z = logits(own)[in];
+      atomicOr(&out[own][in >> 5], 1u << (in & 31));
+      if (a.tail && own == tid) stat[mine] = f32x4{kNegInf, -1.0f, 0.0f, 0.0f};
+    }
+    zs[tid] = z;
+  }
+  __syncthreads();
+  Sums r = kNothing;
+  for (int64_t g = tid; g < o.groups; g += NT) {
+    const f32x4 x = stat[g];
+    join(r, Sums{x[0], x[1], 0.0f});
+  }
+  if (a.tail) {
+    for (int k = wave; k < a.K; k += NW) {
+      if (owner[k] != k) continue;
+      const float* z = logits(k);
+      const int64_t w0 = (int64_t)grp[k] * a.group;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = lane + 64 * h;
+        if (i < a.group && w0 + i < a.V && !(out[k][i >> 5] >> (i & 31) & 1)) {
+          const float x = z[i];
+          // (an infinity gives NaN)
+          join(r, Sums{x, fabsf(x) == __builtin_inff() ? kNaN : 0.0f, 0.0f});
+        }
+      }
+    }
+  }
+  r = join_all<NT>(r, sm);
+  if (wave) return;
+  // entries lane and lane + 64
+  float z[2], l[2];
+  bool on[2], twice[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = lane + 64 * i;
+    on[i] = word[k] >= 0;
+    z[i] = zs[k];
+    l[i] = on[i] ? a.logq[t * a.ldq + k] : 0.0f;
+    twice[i] = false;
+    for (int j = 0; j < k; ++j) twice[i] |= word[j] == word[k];
+  }
+  const Teacher q = teacher(l, on, a.tail);
+  double m = r.m, s = 1.0 + (double)r.r;
+  const bool all = r.r == -1.0f;   // every word is listed
+  if (a.tail) {
+    // the listed words' part
+    m = wave_max(fmax(on[0] ? (double)z[0] : -INFINITY, on[1] ? (double)z[1] : -INFINITY));
+    m = fmax(m, (double)r.m);
+    double e = 0.0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) e += on[i] && !twice[i] && word[lane + 64 * i] < a.V ? exp((double)z[i] - m) : 0.0;
+    s = wave_sum(e);
+    if (!all) s += (1.0 + (double)r.r) * exp((double)r.m - m);
+  }
+  const double log_s = log(s);
+  double e = 0.0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) e += q.q[i] == 0.0 ? 0.0 : q.q[i] * (q.logq[i] - ((double)z[i] - m) + log_s);
+  double loss = wave_sum(e);
+  const double rest = a.tail ? (double)r.m + log1p((double)r.r) : m + log_s;
+  // (without a rest there is none to be off from)
+  if (!all && q.r != 0.0) loss += q.r * (log(q.r) - (rest - m) + log_s);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (lane + 64 * i < a.K) a.hit[t * a.K + lane + 64 * i] = used ? z[i] : 0.0f;
+  if (lane == 0) {
+    a.loss[t] = used ? (float)loss : 0.0f;
+    a.lse[t] = used ? (float)(m + log_s) : 0.0f;
+    a.rest[t] = used ? (float)rest : 0.0f;
+  }
+}
+
+// What the gradient's products need of a token (struct Vocab): its label (the first word
+// listed, whose G val replaces; V where one is at or past V; -1 without any), its share,
+// and val of its entries. Four tokens per workgroup, a wave each.
+__global__ __launch_bounds__(256) void shares_kernel(const int32_t* __restrict__ ids, int64_t ldi,
+                                                     const float* __restrict__ logq, int64_t ldq,
+                                                     int K, int tail, int64_t T, int64_t V,
+                                                     const float* __restrict__ lse,
+                                                     const float* __restrict__ rest,
+                                                     const float* __restrict__ hit,
+                                                     int32_t* __restrict__ labels,
+                                                     float* __restrict__ share,
+                                                     float* __restrict__ val) {
+  __shared__ int word[4][kList];
+  __shared__ double qs[4][kList];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+  const bool real = t < T;
+  float l[2];
+  bool on[2];
+  int id[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = lane + 64 * i;
+    id[i] = real && k < K ? ids[t * ldi + k] : -1;
+    on[i] = id[i] >= 0;
+    l[i] = on[i] ? logq[t * ldq + k] : 0.0f;
+    word[wave][k] = id[i];
+  }
+  const Teacher q = teacher(l, on, tail);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) qs[wave][lane + 64 * i] = q.q[i];
+  __syncthreads();
+  if (!real) return;
+  const double e = lse[t], out = tail ? (double)rest[t] : e;
+  const double r = out == -INFINITY ? 0.0 : q.r, whole = q.sum + r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = lane + 64 * i;
+    if (k >= K) continue;
+    double mine = 0.0;
+    if (on[i])
+      for (int j = 0; j < K; ++j) mine += word[wave][j] == id[i] ? qs[wave][j] : 0.0;
+    val[t * K + k] = on[i] ? (float)(whole * exp((double)hit[t * K + k] - e) - mine) : 0.0f;
+  }
+  const uint64_t some[2] = {__ballot(on[0]), __ballot(on[1])};
+  const bool past = __ballot(id[0] >= V || id[1] >= V) != 0;
+  if (lane == 0) {
+    const int first = some[0] ? __ffsll((unsigned long long)some[0]) - 1 : some[1] ? 63 + __ffsll((unsigned long long)some[1]) : -1;
+    labels[t] = first < 0 ? -1 : past ? (int32_t)V : word[wave][first];
+    share[t] = first < 0 ? 0.0f : (float)(tail ? whole * exp(out - e) - r : whole);
+  }
+}
+
+// ---------------------------------------------------------------- launches
+// The logits of tokens t0 .. t0 + n of the words v0 .. v0 + nv, as `kept` says
+template <int D>
+hipError_t pick(const Vocab& a, const KeepPlan& k, const Opnd& H, int64_t t0, int64_t n, int64_t v0,
+                int64_t nv, const Kept& kept, hipStream_t s) {
+  Mma m{};
+  m.B = H;
+  m.B.p += t0 * H.ld;
+  m.B.rows = n;
+  m.K = m.k_slice = k.p.dp;
+  m.zs = rows_of((char*)a.work, k.p, a.T).zs + t0;
+  m.z0 = a.scale;
+  m.v0 = v0;
+  m.kept = kept;
+  hipError_t e;
+  if ((e = words<D>(a, k.p, v0, nv, &m.A, s)) != hipSuccess) return e;
+  return mma_launch<D, kPick>(m, k.tile, 1, s);
+}
+
+template <int NT> void go_top(const Top& t, int64_t rows, hipStream_t s) {
+  hipLaunchKernelGGL(top_kernel<NT>, dim3((unsigned)rows), dim3(NT), 0, s, t);
+}
+// (more threads per token where there are few)
+bool wide(int64_t T) { return T <= 64; }
+
+template <int D>
+hipError_t logprobs(const Logprobs& a, hipStream_t s) {
+  const Vocab& v = a.v;
+  const KeepPlan k = keep_plan(v.T, v.V, v.d, D, a.given, a.k);
+  char* w = (char*)v.work;
+  hipError_t e;
+  Kept o{};
+  o.stat = (f32x4*)(w + k.stat);
+  o.groups = k.groups;
+  o.ldz = k.ldz;
+  Top t{};
+  t.group = (int)k.group;
+  t.V = v.V;
+  t.k = (int)a.k;
+  t.best = (uint64_t*)(w + k.best);
+  t.thr = (float*)(w + k.thr);
+  t.ldt = a.ldt;
+  t.given = (int)a.given;
+  Opnd H{}, unused;
+  if (!k.few && (e = begin<D>(v, k.p, nullptr, &H, &unused, s)) != hipSuccess) return e;
+  for (int64_t t0 = 0; t0 < v.T; t0 += k.block) {
+    const int64_t n = std::min(k.block, v.T - t0);
+    t.tokens = a.tokens ? a.tokens + t0 * a.ldt : nullptr;
+    t.logprobs = a.logprobs + t0 * a.given;
+    t.entropy = a.entropy + t0;
+    t.lse = a.lse + t0;
+    t.top_ids = a.top_ids + t0 * a.k;
+    t.top_logprobs = a.top_logprobs + t0 * a.k;
+    if (!k.few && a.given) {
+      o.slot = (uint8_t*)(w + k.slot);
+      o.lds = k.lds;
+      o.slots = a.given;
+      o.zslot = (float*)(w + k.zslot);
+      hipLaunchKernelGGL(slots_kernel, dim3((unsigned)n), dim3(kList), 0, s, t.tokens, a.ldt, t.given,
+                         v.V, t.group, (uint8_t*)(w + k.slot), k.lds);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (k.few || a.k) o.z = (float*)(w + k.z);
+    // without best words all at once, or a copy of W's at a time
+    const int64_t most = k.few ? v.V : direct(v.W, v.ldw, v.d, D) ? v.V : k.p.piece;
+    int64_t step = k.few || !a.k ? most : std::min(k.first, most);
+    for (int64_t v0 = 0, nv; v0 < v.V; v0 += nv) {
+      nv = std::min(step, v.V - v0);
+      o.thr = v0 ? t.thr : nullptr;
+      if (k.few)
+        e = score<D>(v, 0, v.V, o, s);
+      else
+        e = pick<D>(v, k, H, t0, n, v0, nv, o, s);
+      if (e != hipSuccess) return e;
+      t.last = v0 + nv >= v.V;
+      if (!a.k && !t.last) continue;
+      t.kept = o;
+      t.v0 = v0;
+      t.g0 = v0 / k.group;
+      t.g1 = (v0 + nv + k.group - 1) / k.group;
+      t.have = v0 > 0;
+      wide(n) ? go_top<1024>(t, n, s) : go_top<256>(t, n, s);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      if (a.k) step = std::min(std::min(3 * step, k.step), most);
+    }
+  }
+  return hipSuccess;
+}
+
+template <int D>
+hipError_t distill(const Distill& a, hipStream_t s) {
+  const Vocab& v = a.v;
+  const KeepPlan k = keep_plan(v.T, v.V, v.d, D, a.K, 0);
+  char* w = (char*)v.work;
+  hipError_t e;
+  Near r{};
+  r.kept.stat = (f32x4*)(w + k.stat);
+  r.kept.groups = k.groups;
+  r.kept.ldz = k.ldz;
+  if (k.few) {
+    r.kept.z = (float*)(w + k.z);
+  } else {
+    r.kept.slot = (uint8_t*)(w + k.slot);
+    r.kept.lds = k.lds;
+    r.kept.slots = a.K;
+    r.kept.zslot = (float*)(w + k.zslot);
+  }
+  r.group = (int)k.group;
+  r.V = v.V;
+  r.ldi = a.ldi;
+  r.ldq = a.ldq;
+  r.K = (int)a.K;
+  r.tail = a.tail;
+  Opnd H{}, unused;
+  if (!k.few && (e = begin<D>(v, k.p, nullptr, &H, &unused, s)) != hipSuccess) return e;
+  for (int64_t t0 = 0; t0 < v.T; t0 += k.block) {
+    const int64_t n = std::min(k.block, v.T - t0);
+    r.ids = a.ids + t0 * a.ldi;
+    r.logq = a.logq + t0 * a.ldq;
+    r.loss = a.loss + t0;
+    r.lse = a.lse + t0;
+    r.rest = a.rest + t0;
+    r.hit = a.hit + t0 * a.K;
+    if (k.few) {
+      if ((e = score<D>(v, 0, v.V, r.kept, s)) != hipSuccess) return e;
+    } else {
+      hipLaunchKernelGGL(slots_kernel, dim3((unsigned)n), dim3(kList), 0, s, r.ids, a.ldi, r.K, v.V,
+                         r.group, (uint8_t*)(w + k.slot), k.lds);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      const int64_t step = direct(v.W, v.ldw, v.d, D) ? v.V : k.p.piece;
+      for (int64_t v0 = 0; v0 < v.V; v0 += step)
+        if ((e = pick<D>(v, k, H, t0, n, v0, std::min(step, v.V - v0), r.kept, s)) != hipSuccess) return e;
+    }
+    if (wide(n))
+      hipLaunchKernelGGL(distill_kernel<1024>, dim3((unsigned)n), dim3(1024), 0, s, r);
+    else
+      hipLaunchKernelGGL(distill_kernel<256>, dim3((unsigned)n), dim3(256), 0, s, r);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// What the gradient needs beside the loss's own workspace
+struct SharePlan {
+  int64_t labels, share, wr, val, bytes;
+};
+SharePlan share_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t K) {
+  SharePlan p;
+  p.labels = round_up(plan_for(T, V, d, dtype, true).bytes, 256);
+  p.share = p.labels + round_up(4 * T, 256);
+  p.wr = p.share + round_up(4 * T, 256);
+  p.val = p.wr + round_up(4 * T, 256);
+  p.bytes = p.val + round_up(4 * T * K, 256);
+  return p;
+}
+
+}  // namespace
+
+int64_t logprobs_work_bytes(int64_t T, int64_t V, int64_t d, int dtype, int64_t given, int64_t k) {
+  return keep_plan(T, V, d, dtype, given, k).bytes;
+}
+int64_t distill_work_bytes(int64_t T, int64_t V, int64_t d, int dtype, int64_t K, bool grad) {
+  return grad ? share_plan(T, V, d, dtype, K).bytes : keep_plan(T, V, d, dtype, K, 0).bytes;
+}
+
+hipError_t launch_vocab_logprobs(const Logprobs& a, hipStream_t s) {
+  if (a.v.dtype == kF32) return logprobs<kF32>(a, s);
+  return a.v.dtype == kBF16 ? logprobs<kBF16>(a, s) : logprobs<kF16>(a, s);
+}
+
+hipError_t launch_vocab_distill(const Distill& a, hipStream_t s) {
+  if (a.v.dtype == kF32) return distill<kF32>(a, s);
+  return a.v.dtype == kBF16 ? distill<kBF16>(a, s) : distill<kF16>(a, s);
+}
+
+hipError_t launch_vocab_distill_backward(const Distill& a, hipStream_t s) {
+  Vocab v = a.v;
+  const SharePlan p = share_plan(v.T, v.V, v.d, v.dtype, a.K);
+  char* w = (char*)v.work;
+  int32_t* labels = (int32_t*)(w + p.labels);
+  float *share = (float*)(w + p.share), *val = (float*)(w + p.val);
+  hipLaunchKernelGGL(shares_kernel, dim3((unsigned)((v.T + 3) / 4)), dim3(256), 0, s, a.ids, a.ldi, a.logq,
+                     a.ldq, (int)a.K, a.tail, v.T, v.V, a.lse, a.rest, a.hit, labels, share, val);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  v.labels = labels;
+  v.lse = a.tail ? a.rest : a.lse;
+  v.share = share;
+  v.wr = (float*)(w + p.wr);
+  v.ids = a.ids;
+  v.ldi = a.ldi;
+  v.listed = a.K;
+  v.val = val;
+  return launch_vocab_loss_backward(v, s);
+}
+
+}  // namespace nq
