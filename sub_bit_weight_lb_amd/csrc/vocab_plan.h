@@ -140,7 +140,8 @@ inline Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad, bool
 constexpr int64_t kMaxListed = 128;   // words that a token can list, and its best words
 constexpr int64_t kKeep = int64_t(1) << 27;   // values of one kind that are kept at most
 
-constexpr int64_t kFirst = 8192;              // words of the first step
+constexpr int64_t kFirst = 8192;              // words of the first step at least
+constexpr int64_t kWhole = int64_t(1) << 26;  // logits of a block that are kept whole, in one step
 
 // What a call keeps of the logits of `block` tokens at a time: the sums of every group of
 // words; the groups of listed words in a slot each; and, to find the best words, the
@@ -163,16 +164,18 @@ inline KeepPlan keep_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t li
   k.group = k.tile / 2;
   k.groups = (V + k.group - 1) / k.group;
   k.block = T;
+  // (twice as many groups as best words, so that few of their words are above a group's best)
+  const int64_t all = round_up(V, 256), first = std::min(all, std::max(kFirst, round_up(2 * top * k.group, 256)));
   if (!k.few) {
     int64_t most = std::min(kKeep / std::max<int64_t>(listed * k.group, 1), kKeep / (4 * k.groups));
-    if (top) most = std::min(most, kKeep / std::min(round_up(V, 256), kFirst));
+    if (top) most = std::min(most, kKeep / first);
     k.block = std::min(T, std::max<int64_t>(256, most / 256 * 256));
   }
   if (k.few) {
     k.ldz = round_up(V, 64);
   } else if (top) {
-    k.step = std::min(round_up(V, 256), std::max(kFirst, kKeep / k.block / 256 * 256));
-    k.first = std::min(k.step, kFirst);
+    k.step = std::min(all, std::max(first, kKeep / k.block / 256 * 256));
+    k.first = k.block * all <= kWhole ? all : first;
     k.ldz = k.step;
   }
   k.lds = round_up(k.groups, 16);

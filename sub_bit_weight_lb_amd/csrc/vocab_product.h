@@ -70,6 +70,7 @@ struct Kept {
   float* z;                 // [token][ldz], nullable: z of the call's words,
   int64_t ldz;
   const float* thr;         // of groups with one above the token's thr (nullable: all)
+  int flip;                 // kPick: z's factor is below zero
 };
 
 enum Epi : int { kStat = 0, kGrad = 1, kDh = 2, kDw = 3, kPick = 4 };
@@ -414,49 +415,79 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
       }
     }
   } else if constexpr (EPI == kPick) {
+    // z = acc zs with zs made positive, so that the largest acc is the largest z, e = 2^((acc
+    // - largest) zs log2 e) without a scaled z, and dot is NaN where an acc is not finite
+    // (0 times infinity, too).
     const Kept& o = a.kept;
     const int64_t group = a.v0 / (16 * MI) + tm * WM + wm;
+    if (o.flip) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j) acc[i][j] = -acc[i][j];
+    }
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const int64_t t = c0 + 16 * j;
       const bool used = t < N && group < o.groups;
-      const float zs = D == kF32 ? (t < N ? a.zs[t] : 0.0f) : a.z0;
+      const float zs = fabsf(D == kF32 ? (t < N ? a.zs[t] : 0.0f) : a.z0);
       const float thr = used && o.thr ? o.thr[t] : kNegInf;
       const int slot = used && o.slot ? o.slot[t * o.lds + group] : 255;
-      float top = kNegInf, low = 0.0f;
+      float top = kNegInf, sum = 0.0f, dot = 0.0f, r;
+      const float by = zs * 1.44269504f;
+      auto sums = [&](auto whole) {   // (whole: no word past the last)
+        constexpr bool ALL = decltype(whole)::value;
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          acc[i][j][v] *= zs;
-          if (16 * i + v < left) top = fmaxf(top, acc[i][j][v]);
-          low = fminf(low, acc[i][j][v]);
+          for (int v = 0; v < 4; ++v)
+            if (ALL || 16 * i + v < left) top = fmaxf(top, acc[i][j][v]);
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float y = (acc[i][j][v] - top) * by;
+            const float e = __builtin_amdgcn_exp2f(y);
+            sum += ALL || 16 * i + v < left ? e : 0.0f;
+            dot = ALL || 16 * i + v < left ? fmaf(e, y, dot) : dot;
+          }
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        dot += __shfl_xor(dot, 16);
+        dot += __shfl_xor(dot, 32);
+        r = sum - 1.0f;
+        // a group that is all but one word: what r leaves out of 2^-4 of it is summed by itself
+        if (__ballot(sum < 1.0625f)) {
+          float ones = 0.0f, rest = 0.0f;
+#pragma unroll
+          for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const float y = acc[i][j][v] - top;
+              const bool on = ALL || 16 * i + v < left;
+              ones += on && y == 0.0f ? 1.0f : 0.0f;
+              rest += on && y != 0.0f ? __builtin_amdgcn_exp2f(y * by) : 0.0f;
+            }
+          ones += __shfl_xor(ones, 16);
+          ones += __shfl_xor(ones, 32);
+          rest += __shfl_xor(rest, 16);
+          rest += __shfl_xor(rest, 32);
+          r = rest + (ones - 1.0f);
         }
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      float sum = 0.0f, dot = 0.0f, ones = 0.0f;
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float y = acc[i][j][v] - top, e = __expf(y);
-          const bool on = 16 * i + v < left;
-          ones += on && y == 0.0f ? 1.0f : 0.0f;
-          sum += on && y != 0.0f ? e : 0.0f;
-          dot += on ? e * y : 0.0f;
-        }
-      sum = low == kNegInf ? __uint_as_float(0x7fc00000u) : sum;   // (as in kStat)
-      sum += __shfl_xor(sum, 16);
-      sum += __shfl_xor(sum, 32);
-      ones += __shfl_xor(ones, 16);
-      ones += __shfl_xor(ones, 32);
-      dot += __shfl_xor(dot, 16);
-      dot += __shfl_xor(dot, 32);
+      };
+      if (m0 + (wm + 1) * MI * 16 <= M)
+        sums(std::true_type{});
+      else
+        sums(std::false_type{});
       if (!used) continue;
-      if (g == 0) o.stat[t * o.groups + group] = f32x4{top, sum + (ones - 1.0f), dot, 0.0f};
+      top *= zs;
+      if (g == 0)
+        o.stat[t * o.groups + group] = f32x4{top, dot == dot ? r : __uint_as_float(0x7fc00000u), dot * 0.69314718f, 0.0f};
       auto put = [&](float* p) {   // (of words past the last too: rows and slots hold whole groups)
 #pragma unroll
-        for (int i = 0; i < MI; ++i) *(f32x4*)(p + 16 * i + 4 * g) = acc[i][j];
+        for (int i = 0; i < MI; ++i) *(f32x4*)(p + 16 * i + 4 * g) = acc[i][j] * zs;
       };
       if (slot != 255) put(o.zslot + (t * o.slots + slot) * (16 * MI));
       if (o.z && !(top <= thr)) put(o.z + t * o.ldz + (tm * WM + wm) * (16 * MI));

@@ -49,53 +49,73 @@ __device__ __forceinline__ void join(Sums& a, Sums b) {
   a.u = p * (a.u + x * as) + q * (b.u + y * bs);
   a.m = n;
 }
+// Joins a lane's sums with those of lane ^ o: both join the lower one's with the upper one's.
+__device__ __forceinline__ void pair(Sums& a, int o) {
+  const Sums b{__shfl_xor(a.m, o), __shfl_xor(a.r, o), __shfl_xor(a.u, o)};
+  const bool up = threadIdx.x & o;
+  Sums l = up ? b : a;
+  join(l, up ? a : b);
+  a = l;
+}
 // Over the workgroup's NT threads, in a fixed order; all of them get the result. sm: three
 // floats per wave.
 template <int NT>
 __device__ __forceinline__ Sums join_all(Sums a, float* sm) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const Sums b{__shfl_xor(a.m, o), __shfl_xor(a.r, o), __shfl_xor(a.u, o)};
-    // (both sides of a pair join the lower lane's with the upper one's)
-    const bool up = threadIdx.x & o;
-    Sums l = up ? b : a;
-    join(l, up ? a : b);
-    a = l;
-  }
-  const int wave = threadIdx.x >> 6;
+  for (int o = 32; o > 0; o >>= 1) pair(a, o);
+  constexpr int NW = NT / 64;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) {
+  if (lane == 0) {
     sm[3 * wave] = a.m;
     sm[3 * wave + 1] = a.r;
     sm[3 * wave + 2] = a.u;
   }
   __syncthreads();
-  a = Sums{sm[0], sm[1], sm[2]};
+  const int w = lane & (NW - 1);
+  a = Sums{sm[3 * w], sm[3 * w + 1], sm[3 * w + 2]};
 #pragma unroll
-  for (int w = 1; w < NT / 64; ++w) join(a, Sums{sm[3 * w], sm[3 * w + 1], sm[3 * w + 2]});
+  for (int o = NW / 2; o > 0; o >>= 1) pair(a, o);
   return a;
 }
 
 // ---------------------------------------------------------------- slots
+// The first of a token's K entries with the same group as entry k (its owner), and whether an
+// earlier entry has the same word. grp, word: of the entries, in LDS, -1 for none; padded to 4.
+struct Same {
+  int owner;
+  bool twice;
+};
+__device__ __forceinline__ Same same(const int* grp, const int* word, int K, int k) {
+  typedef int i32x4 __attribute__((ext_vector_type(4)));
+  const int g = grp[k], w = word[k];
+  Same r{k, false};
+#pragma unroll 4
+  for (int j = 0; j < K; j += 4) {
+    const i32x4 gs = *(const i32x4*)(grp + j), ws = *(const i32x4*)(word + j);
+#pragma unroll
+    for (int u = 3; u >= 0; --u) {
+      r.owner = gs[u] == g && j + u < r.owner ? j + u : r.owner;
+      r.twice |= ws[u] == w && j + u < k;
+    }
+  }
+  return r;
+}
 // slot[t][group] = the first of the token's K entries with a word in it, 255 for groups without
 // one. A workgroup per token.
 __global__ __launch_bounds__(kList) void slots_kernel(const int32_t* __restrict__ ids, int64_t ldi,
                                                       int K, int64_t V, int group,
                                                       uint8_t* __restrict__ slot, int64_t lds) {
-  __shared__ int gr[kList];
+  __shared__ __align__(16) int gr[kList];
   const int64_t t = blockIdx.x;
   const int k = threadIdx.x;
   uint8_t* row = slot + t * lds;
+  const int32_t id = k < K ? ids[t * ldi + k] : -1;
   for (int64_t i = 16 * k; i < lds; i += 16 * kList)
     *(u32x4*)(row + i) = u32x4{~0u, ~0u, ~0u, ~0u};
-  const int32_t id = k < K ? ids[t * ldi + k] : -1;
-  const int mine = id >= 0 && id < V ? id / group : -1;
-  gr[k] = mine;
+  gr[k] = id >= 0 && id < V ? id / group : -1;
   __syncthreads();
-  if (mine < 0) return;
-  for (int j = 0; j < k; ++j)
-    if (gr[j] == mine) return;
-  row[mine] = (uint8_t)k;
+  if (gr[k] >= 0 && same(gr, gr, K, k).owner == k) row[gr[k]] = (uint8_t)k;
 }
 
 // ---------------------------------------------------------------- log probabilities
@@ -126,19 +146,40 @@ __device__ __forceinline__ uint64_t key_of(float z, uint32_t word) {
   return (uint64_t)order_of(z) << 32 | (uint32_t)~word;
 }
 
+// The largest c of the form that bits 31 .. low can write with k of the N values of each lane at
+// or above c (0: with none); *n: how many those are. Stops where they are k.
+template <int N>
+__device__ __forceinline__ uint32_t reached(const uint32_t (&x)[N], int k, int low, int* n) {
+  uint32_t c = 0;
+  *n = 64 * N;
+  for (int b = 31; b >= low; --b) {
+    const uint32_t d = c | 1u << b;
+    int above = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) above += __popcll(__ballot(x[i] >= d));
+    if (above >= k) {
+      c = d;
+      *n = above;
+      if (above == k) break;
+    }
+  }
+  return c;
+}
+
 // The best words of a step join those of earlier ones; in the last step the token's outputs
 // follow. A workgroup of NT threads per token.
-//   Bound: each thread takes the largest z of its share of the groups; the k-th largest of
-//   these is one that k words reach. Only groups that reach it are looked at: k, and few
-//   more where a thread has two.
+//   Bound: 256 shares of the step's groups have a largest z each; one that k of these reach
+//   is one that k words reach. Only groups that reach it are looked at: k, and few more
+//   where a share has two.
 //   Their words above the bound go to a list in LDS, in any order (an atomic counter gives
-//   the places; keys are distinct, so that the order does not show). The list is cut to its k
-//   best, each key's place counted, where it has no room for a group, and at the end.
+//   the places; keys are distinct, so that the order does not show), which one wave cuts to
+//   its k best, found bit by bit. If the list is too short for them (many words of one
+//   value), as many groups at a time as it has room for.
 template <int NT>
 __global__ __launch_bounds__(NT) void top_kernel(Top a) {
-  constexpr int kCap = 2048, NW = NT / 64;
+  constexpr int kCap = 1024, NW = NT / 64, kEach = kCap / 64;
   __shared__ uint64_t list[kCap];
-  __shared__ uint32_t most[NT];
+  __shared__ __align__(16) uint32_t most[256];
   __shared__ int todo[NT];
   __shared__ int count, left;
   __shared__ uint32_t lim;
@@ -148,50 +189,111 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
   const f32x4* stat = a.kept.stat + t * a.kept.groups;
   const int k = a.k;
   if (k) {
-    uint64_t bound = 0;   // keys above it are in
     uint32_t m = 0;
     for (int64_t g = a.g0 + tid; g < a.g1; g += NT) m = max(m, order_of(stat[g][0]));
-    most[tid] = m;
-    if (a.have && tid < k) list[tid] = a.best[t * k + tid];
-    if (tid == 0) {
-      lim = 0;
-      count = a.have ? k : 0;
+    if constexpr (NT > 256) {
+#pragma unroll
+      for (int o = 1; o < NT / 256; o *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, o));
     }
+    if (tid % (NT / 256) == 0) most[tid / (NT / 256)] = m;
+    if (a.have && tid < k) list[tid] = a.best[t * k + tid];
+    if (tid == 0) count = a.have ? k : 0;
     __syncthreads();
-    int above = 0;
-#pragma unroll 8
-    for (int j = 0; j < NT; ++j) above += most[j] > m || (most[j] == m && j < tid);
-    if (above == k - 1) lim = m;
-    __syncthreads();
-    if (lim) bound = ((uint64_t)lim << 32) - 1;
-    if (a.have && list[k - 1] > bound) bound = list[k - 1];
+    uint64_t bound;   // keys above it are in
+    {
+      const u32x4 q = ((const u32x4*)most)[lane];
+      const uint32_t x[4] = {q[0], q[1], q[2], q[3]};
+      int n;
+      const uint32_t c = reached(x, k, 12, &n);
+      bound = c ? ((uint64_t)c << 32) - 1 : 0;
+      // (later words lose to earlier ones of the same z)
+      if (a.have) bound = max(bound, (uint64_t)order_of(a.thr[t]) << 32 | 0xffffffffu);
+    }
     const float* z = a.kept.z + t * a.kept.ldz;
     int n = a.have ? k : 0;
-    // cuts the list to its k best, in order
+    // cuts the list to its k best; afterwards lim is what they reach
     auto cut = [&]() {
-      uint64_t key[kCap / NT];
-      int place[kCap / NT];
+      if (wave == 0) {
+        uint32_t hi[kEach], lo[kEach];
 #pragma unroll
-      for (int i = 0; i < kCap / NT; ++i) {
-        key[i] = tid + i * NT < n ? list[tid + i * NT] : 0;
-        place[i] = kCap;
-      }
+        for (int i = 0; i < kEach; ++i) {
+          const uint64_t key = 64 * i + lane < n ? list[64 * i + lane] : 0;
+          hi[i] = (uint32_t)(key >> 32);
+          lo[i] = (uint32_t)key;
+        }
+        int got;
+        const uint32_t c = n <= 256 ? reached(reinterpret_cast<const uint32_t(&)[4]>(hi), k, 0, &got)
+                                    : reached(hi, k, 0, &got);
+        uint32_t d = 0;
+        if (got != k) {   // several of the k-th z: the lower words
+          uint32_t x[kEach];
+          int above = 0;
 #pragma unroll
-      for (int i = 0; i < kCap / NT; ++i) {
-        if (i * NT >= n) break;
-        int p = 0;
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) p += list[j] > key[i];
-        place[i] = key[i] ? p : kCap;
+          for (int i = 0; i < kEach; ++i) {
+            above += __popcll(__ballot(hi[i] > c));
+            x[i] = hi[i] == c ? lo[i] : 0;
+          }
+          d = reached(x, k - above, 0, &got);
+        }
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const bool in = 64 * i + lane < n && (hi[i] > c || (hi[i] == c && lo[i] >= d));
+          const uint64_t who = __ballot(in);
+          if (in) list[at + __popcll(who & ((uint64_t(1) << lane) - 1))] = (uint64_t)hi[i] << 32 | lo[i];
+          at += __popcll(who);
+        }
+        if (lane == 0) {
+          count = at;
+          lim = c;
+        }
       }
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kCap / NT; ++i)
-        if (place[i] < k) list[place[i]] = key[i];
-      n = min(n, k);
-      if (tid == 0) count = n;
+      n = count;
       __syncthreads();
-      if (n == k && list[k - 1] > bound) bound = list[k - 1];
+      bound = max(bound, ((uint64_t)lim << 32) - (lim != 0));
+    };
+    // words above the bound of the groups todo[b .. end); whether all had room
+    auto collect = [&](int b, int end) {
+      // four groups of a wave at a time, all their loads before the first use
+      for (int i = b + wave; i < end; i += 4 * NW) {
+        float x[4][2];
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int e = i + q * NW;
+          w[q] = (uint32_t)(todo[min(e, end - 1)] * a.group) + lane;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const bool on = e < end && lane + 64 * h < a.group && w[q] + 64 * h < a.V;
+            x[q][h] = on ? z[w[q] + 64 * h - a.v0] : 0.0f;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const bool on = i + q * NW < end && lane + 64 * h < a.group && w[q] + 64 * h < a.V;
+            const uint64_t key = key_of(x[q][h], w[q] + 64 * h);
+            const bool in = on && key > bound;
+            const uint64_t who = __ballot(in);
+            if (!who) continue;
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&count, __popcll(who));
+            at = __shfl(at, 0) + __popcll(who & ((uint64_t(1) << lane) - 1));
+            if (in && at < kCap) list[at] = key;
+          }
+      }
+      __syncthreads();
+      const int c = count;
+      __syncthreads();   // (nobody changes count before all have read it)
+      if (c > kCap) {
+        if (tid == 0) count = n;
+        __syncthreads();
+        return false;
+      }
+      n = c;
+      return true;
     };
     for (int64_t base = a.g0; base < a.g1; base += NT) {
       if (tid == 0) left = 0;
@@ -205,50 +307,19 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
       if (in) todo[at + __popcll(who & ((uint64_t(1) << lane) - 1))] = (int)g;
       __syncthreads();
       const int c = left;
-      for (int b = 0; b < c;) {
-        if (n + a.group > kCap) cut();
-        const int end = min(c, b + (kCap - n) / a.group);
-        // four groups of a wave at a time, all their loads before the first use
-        for (int i = b + wave; i < end; i += 4 * NW) {
-          float x[4][2];
-          uint32_t w[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int e = i + q * NW;
-            w[q] = (uint32_t)(todo[min(e, end - 1)] * a.group) + lane;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const bool on = e < end && lane + 64 * h < a.group && w[q] + 64 * h < a.V;
-              x[q][h] = on ? z[w[q] + 64 * h - a.v0] : 0.0f;
-            }
-          }
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int e = i + q * NW;
-              const bool on = e < end && lane + 64 * h < a.group && w[q] + 64 * h < a.V;
-              const uint64_t key = key_of(x[q][h], w[q] + 64 * h);
-              const uint64_t who = __ballot(on && key > bound);
-              if (!who) continue;
-              int at = 0;
-              if (lane == 0) at = atomicAdd(&count, __popcll(who));
-              at = __shfl(at, 0);
-              if (on && key > bound) list[at + __popcll(who & ((uint64_t(1) << lane) - 1))] = key;
-            }
+      if (c && !collect(0, c)) {
+        for (int b = 0; b < c;) {
+          if (n + a.group > kCap) cut();
+          const int end = min(c, b + (kCap - n) / a.group);
+          collect(b, end);
+          b = end;
         }
-        __syncthreads();
-        n = count;
-        b = end;
-        __syncthreads();   // (nobody adds to count before all have read it)
       }
     }
     cut();
-    for (int i = n + tid; i < k; i += NT) list[i] = 0;   // (fewer: where z are not finite)
-    __syncthreads();
     if (!a.last) {
-      if (tid < k) a.best[t * k + tid] = list[tid];
-      if (tid == 0) a.thr[t] = value_of((uint32_t)(list[k - 1] >> 32));
+      if (tid < k) a.best[t * k + tid] = tid < n ? list[tid] : 0;
+      if (tid == 0) a.thr[t] = value_of(lim);
       return;
     }
   }
@@ -265,9 +336,18 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
     a.entropy[t] = log_s - r.u / (1.0f + r.r);
   }
   if (tid < k) {
-    const uint64_t key = list[tid];
-    a.top_ids[t * k + tid] = fine ? (int32_t)~(uint32_t)key : -1;
-    a.top_logprobs[t * k + tid] = fine ? value_of((uint32_t)(key >> 32)) - r.m - log_s : kNaN;
+    int place = tid;
+    if (fine) {
+      const uint64_t key = list[tid];
+      place = 0;
+#pragma unroll 8
+      for (int j = 0; j < k; ++j) place += list[j] > key;
+      a.top_ids[t * k + place] = (int32_t)~(uint32_t)key;
+      a.top_logprobs[t * k + place] = value_of((uint32_t)(key >> 32)) - r.m - log_s;
+    } else {
+      a.top_ids[t * k + place] = -1;
+      a.top_logprobs[t * k + place] = kNaN;
+    }
   }
   if (tid < a.given) {
     const int32_t id = a.tokens[t * a.ldt + tid];
@@ -342,7 +422,9 @@ __device__ __forceinline__ Teacher teacher(const float (&l)[2], const bool (&on)
 template <int NT>
 __global__ __launch_bounds__(NT) void distill_kernel(Near a) {
   constexpr int NW = NT / 64;
-  __shared__ int owner[kList], grp[kList], word[kList];
+  __shared__ __align__(16) int grp[kList], word[kList];
+  __shared__ int owner[kList];
+  __shared__ bool again[kList];        // an earlier entry has the same word
   __shared__ uint32_t out[kList][4];   // of the owner's group: the words that are listed
   __shared__ float zs[kList];
   __shared__ int used;
@@ -365,11 +447,11 @@ __global__ __launch_bounds__(NT) void distill_kernel(Near a) {
     return o.slot ? o.zslot + (t * o.slots + own) * a.group : o.z + t * o.ldz + (int64_t)grp[own] * a.group;
   };
   if (tid < kList) {
-    int own = tid;
     const int mine = grp[tid];
-    if (mine >= 0)
-      for (int j = tid - 1; j >= 0; --j) own = grp[j] == mine ? j : own;
+    const Same first = same(grp, word, a.K, tid);
+    const int own = first.owner;
     owner[tid] = mine >= 0 ? own : -1;
+    again[tid] = first.twice;
     if (id >= 0) used = 1;   // (all write the same)
     float z = id < 0 ? 0.0f : kNaN;
     if (mine >= 0) {
@@ -387,19 +469,42 @@ __global__ __launch_bounds__(NT) void distill_kernel(Near a) {
     join(r, Sums{x[0], x[1], 0.0f});
   }
   if (a.tail) {
-    for (int k = wave; k < a.K; k += NW) {
-      if (owner[k] != k) continue;
-      const float* z = logits(k);
-      const int64_t w0 = (int64_t)grp[k] * a.group;
+    // four groups of a wave at a time, all their loads before the first use
+    for (int k0 = wave; k0 < a.K; k0 += 4 * NW) {
+      float x[4][2];
+      bool on[4][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = lane + 64 * h;
-        if (i < a.group && w0 + i < a.V && !(out[k][i >> 5] >> (i & 31) & 1)) {
-          const float x = z[i];
-          // (an infinity gives NaN)
-          join(r, Sums{x, fabsf(x) == __builtin_inff() ? kNaN : 0.0f, 0.0f});
+      for (int q = 0; q < 4; ++q) {
+        const int k = min(k0 + q * NW, a.K - 1);
+        const bool own = k0 + q * NW < a.K && owner[k] == k;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = lane + 64 * h;
+          on[q][h] = own && i < a.group && (int64_t)grp[k] * a.group + i < a.V &&
+                     !(out[k][(i >> 5) & 3] >> (i & 31) & 1);
+          x[q][h] = on[q][h] ? logits(k)[i] : 0.0f;
         }
       }
+      Sums b{kNegInf, -1.0f, 0.0f};
+      bool bad = false;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          b.m = on[q][h] ? fmaxf(b.m, x[q][h]) : b.m;
+          bad |= on[q][h] && !(fabsf(x[q][h]) < __builtin_inff());
+        }
+      float ones = -1.0f, sum = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float y = x[q][h] - b.m;
+          ones += on[q][h] && y == 0.0f ? 1.0f : 0.0f;
+          sum += on[q][h] && y != 0.0f ? __expf(y) : 0.0f;
+        }
+      b.r = bad ? kNaN : sum + ones;
+      join(r, b);
     }
   }
   r = join_all<NT>(r, sm);
@@ -413,8 +518,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(Near a) {
     on[i] = word[k] >= 0;
     z[i] = zs[k];
     l[i] = on[i] ? a.logq[t * a.ldq + k] : 0.0f;
-    twice[i] = false;
-    for (int j = 0; j < k; ++j) twice[i] |= word[j] == word[k];
+    twice[i] = again[k];
   }
   const Teacher q = teacher(l, on, a.tail);
   double m = r.m, s = 1.0 + (double)r.r;
@@ -532,6 +636,7 @@ hipError_t logprobs(const Logprobs& a, hipStream_t s) {
   char* w = (char*)v.work;
   hipError_t e;
   Kept o{};
+  o.flip = v.scale < 0.0f;
   o.stat = (f32x4*)(w + k.stat);
   o.groups = k.groups;
   o.ldz = k.ldz;
@@ -596,6 +701,7 @@ hipError_t distill(const Distill& a, hipStream_t s) {
   char* w = (char*)v.work;
   hipError_t e;
   Near r{};
+  r.kept.flip = v.scale < 0.0f;
   r.kept.stat = (f32x4*)(w + k.stat);
   r.kept.groups = k.groups;
   r.kept.ldz = k.ldz;
