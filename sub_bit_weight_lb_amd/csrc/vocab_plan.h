@@ -144,8 +144,9 @@ constexpr int64_t kFirst = 8192;              // words of the first step at leas
 constexpr int64_t kWhole = int64_t(1) << 26;  // logits of a block that are kept whole, in one step
 
 // What a call keeps of the logits of `block` tokens at a time: the sums of every group of
-// words; the groups of listed words in a slot each; and, to find the best words, the
-// groups that may hold one of them, of a step of the vocabulary at a time.
+// words; the groups of listed words in a slot each; and, to find the best words, the largest z
+// of each part of a group and the parts that may hold one of them, of a step of the
+// vocabulary at a time.
 struct KeepPlan {
   Plan p;                     // of the operands
   bool few;                   // score_kernel's: all logits are kept, in one step
@@ -154,7 +155,7 @@ struct KeepPlan {
   int64_t block;              // tokens at a time
   int64_t first, step;        // words of the first step and of the largest (0: no best words)
   int64_t lds, ldz;           // bytes of a token's slots, its row of kept logits
-  int64_t stat, slot, zslot, z, best, thr, bytes;
+  int64_t stat, tops, slot, zslot, z, best, thr, bytes;
 };
 inline KeepPlan keep_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t listed, int64_t top) {
   KeepPlan k{};
@@ -186,6 +187,7 @@ inline KeepPlan keep_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t li
     return at;
   };
   k.stat = take(16 * k.block * k.groups);
+  if (top) k.tops = take(4 * 4 * k.block * k.groups);
   k.z = take(4 * k.block * k.ldz);
   if (!k.few && listed) {
     k.slot = take(k.block * k.lds);

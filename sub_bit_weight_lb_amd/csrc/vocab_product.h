@@ -67,11 +67,24 @@ struct Kept {
   const uint8_t* slot;      // [token][lds], nullable: the slot that a group's z go to, 255: none
   int64_t lds, slots;
   float* zslot;             // [token][slots][words of a group]
+  float* tops;              // [token][subs of groups], nullable: the largest z of each part of a group
   float* z;                 // [token][ldz], nullable: z of the call's words,
   int64_t ldz;
-  const float* thr;         // of groups with one above the token's thr (nullable: all)
+  const float* thr;         // of parts with one above the token's thr (nullable: all)
   int flip;                 // kPick: z's factor is below zero
 };
+
+// Words of a part: a group has four (of 32 words two).
+constexpr int part_of(int group) { return group == 128 ? 32 : 16; }
+
+// x of the lanes l, l ^ 16, l ^ 32 and l ^ 48 joined by f, in all of them
+template <typename F>
+__device__ __forceinline__ float across(float x, F f) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = f(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return f(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
 
 enum Epi : int { kStat = 0, kGrad = 1, kDh = 2, kDw = 3, kPick = 4 };
 struct Mma {
@@ -433,17 +446,24 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
       const float zs = fabsf(D == kF32 ? (t < N ? a.zs[t] : 0.0f) : a.z0);
       const float thr = used && o.thr ? o.thr[t] : kNegInf;
       const int slot = used && o.slot ? o.slot[t * o.lds + group] : 255;
-      float top = kNegInf, sum = 0.0f, dot = 0.0f, r;
+      // parts of the group: PI row tiles each
+      constexpr int PARTS = 16 * MI / part_of(16 * MI), PI = MI / PARTS;
+      float tops[PARTS], top = kNegInf, sum = 0.0f, dot = 0.0f, r;
       const float by = zs * 1.44269504f;
+      auto add = [](float x, float y) { return x + y; };
       auto sums = [&](auto whole) {   // (whole: no word past the last)
         constexpr bool ALL = decltype(whole)::value;
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+        for (int q = 0; q < PARTS; ++q) {
+          float x = kNegInf;
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (ALL || 16 * i + v < left) top = fmaxf(top, acc[i][j][v]);
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
+          for (int i = q * PI; i < (q + 1) * PI; ++i)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              if (ALL || 16 * i + v < left) x = fmaxf(x, acc[i][j][v]);
+          tops[q] = across(x, [](float x, float y) { return fmaxf(x, y); });
+          top = fmaxf(top, tops[q]);
+        }
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -453,10 +473,8 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
             sum += ALL || 16 * i + v < left ? e : 0.0f;
             dot = ALL || 16 * i + v < left ? fmaf(e, y, dot) : dot;
           }
-        sum += __shfl_xor(sum, 16);
-        sum += __shfl_xor(sum, 32);
-        dot += __shfl_xor(dot, 16);
-        dot += __shfl_xor(dot, 32);
+        sum = across(sum, add);
+        dot = across(dot, add);
         r = sum - 1.0f;
         // a group that is all but one word: what r leaves out of 2^-4 of it is summed by itself
         if (__ballot(sum < 1.0625f)) {
@@ -470,11 +488,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
               ones += on && y == 0.0f ? 1.0f : 0.0f;
               rest += on && y != 0.0f ? __builtin_amdgcn_exp2f(y * by) : 0.0f;
             }
-          ones += __shfl_xor(ones, 16);
-          ones += __shfl_xor(ones, 32);
-          rest += __shfl_xor(rest, 16);
-          rest += __shfl_xor(rest, 32);
-          r = rest + (ones - 1.0f);
+          r = across(rest, add) + (across(ones, add) - 1.0f);
         }
       };
       if (m0 + (wm + 1) * MI * 16 <= M)
@@ -482,15 +496,31 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
       else
         sums(std::false_type{});
       if (!used) continue;
-      top *= zs;
-      if (g == 0)
-        o.stat[t * o.groups + group] = f32x4{top, dot == dot ? r : __uint_as_float(0x7fc00000u), dot * 0.69314718f, 0.0f};
-      auto put = [&](float* p) {   // (of words past the last too: rows and slots hold whole groups)
+      if (g == 0) {
+        o.stat[t * o.groups + group] = f32x4{top * zs, dot == dot ? r : __uint_as_float(0x7fc00000u), dot * 0.69314718f, 0.0f};
+        if (o.tops) {
+          float* p = o.tops + (t * o.groups + group) * PARTS;
 #pragma unroll
-        for (int i = 0; i < MI; ++i) *(f32x4*)(p + 16 * i + 4 * g) = acc[i][j] * zs;
+          for (int q = 0; q < PARTS; q += 2) *(u32x2*)(p + q) = u32x2{__float_as_uint(tops[q] * zs), __float_as_uint(tops[q + 1] * zs)};
+        }
+      }
+      auto put = [&](float* p, int i) {   // (of words past the last too: rows and slots hold whole groups)
+        *(f32x4*)(p + 16 * i + 4 * g) = acc[i][j] * zs;
       };
-      if (slot != 255) put(o.zslot + (t * o.slots + slot) * (16 * MI));
-      if (o.z && !(top <= thr)) put(o.z + t * o.ldz + (tm * WM + wm) * (16 * MI));
+      if (slot != 255) {
+        float* p = o.zslot + (t * o.slots + slot) * (16 * MI);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) put(p, i);
+      }
+      if (o.z) {
+        float* p = o.z + t * o.ldz + (tm * WM + wm) * (16 * MI);
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q)
+          if (!(tops[q] * zs <= thr)) {
+#pragma unroll
+            for (int i = q * PI; i < (q + 1) * PI; ++i) put(p, i);
+          }
+      }
     }
   } else if constexpr (EPI == kGrad) {
 #pragma unroll
@@ -774,6 +804,8 @@ __global__ __launch_bounds__(1024 / NT)
           }
         }
         o.stat[t * o.groups + blockIdx.x] = f32x4{m, s + ones, y, 0.0f};
+        if (o.tops)
+          *(f32x4*)(o.tops + (t * o.groups + blockIdx.x) * 4) = f32x4{st[0][0][t], st[0][1][t], st[0][2][t], st[0][3][t]};
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)

@@ -18,8 +18,8 @@
 // The product's epilogue kPick (up to 32 tokens, fp32 64: score_kernel) leaves, per token and
 // group of words, the largest z and the sums S and U about it, and the z of
 //   groups with a listed word: each has a slot, which slots_kernel gives;
-//   groups that may hold one of the best words: the vocabulary is taken in steps, and
-//   from the second on only groups with a z above the k-th best so far are written.
+//   parts of groups that may hold one of the best words: the vocabulary is taken in steps,
+//   and from the second on only parts with a z above the k-th best so far are written.
 // A workgroup per token (top_kernel, distill_kernel) then joins the groups.
 #include "vocab_product.h"
 
@@ -122,7 +122,7 @@ __global__ __launch_bounds__(kList) void slots_kernel(const int32_t* __restrict_
 struct Top {
   Kept kept;
   int group;                 // words of a group
-  int64_t V, v0, g0, g1;     // the step's first word, its groups
+  int64_t V, v0, p0, p1;     // the step's first word, its parts
   int k, have;               // best words; whether `best` holds those of earlier steps
   uint64_t* best;            // [token][k], best first
   float* thr;                // [token]: the k-th best z
@@ -168,19 +168,19 @@ __device__ __forceinline__ uint32_t reached(const uint32_t (&x)[N], int k, int l
 
 // The best words of a step join those of earlier ones; in the last step the token's outputs
 // follow. A workgroup of NT threads per token.
-//   Bound: 256 shares of the step's groups have a largest z each; one that k of these reach
-//   is one that k words reach. Only groups that reach it are looked at: k, and few more
+//   Bound: 256 shares of the step's parts have a largest z each; one that k of these reach
+//   is one that k words reach. Only parts that reach it are looked at: k, and few more
 //   where a share has two.
 //   Their words above the bound go to a list in LDS, in any order (an atomic counter gives
 //   the places; keys are distinct, so that the order does not show), which one wave cuts to
 //   its k best, found bit by bit. If the list is too short for them (many words of one
-//   value), as many groups at a time as it has room for.
+//   value), as many parts at a time as it has room for.
 template <int NT>
 __global__ __launch_bounds__(NT) void top_kernel(Top a) {
   constexpr int kCap = 1024, NW = NT / 64, kEach = kCap / 64;
   __shared__ uint64_t list[kCap];
   __shared__ __align__(16) uint32_t most[256];
-  __shared__ int todo[NT];
+  __shared__ int todo[4 * NT];
   __shared__ int count, left;
   __shared__ uint32_t lim;
   __shared__ float sm[3 * NW];
@@ -189,8 +189,25 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
   const f32x4* stat = a.kept.stat + t * a.kept.groups;
   const int k = a.k;
   if (k) {
+    // parts of the token, four at a time (a step's first is a multiple of 4; past its last:
+    // -infinity, which is nobody's largest unless nothing is finite)
+    const int part = part_of(a.group);
+    const float* tops = a.kept.tops + t * a.kept.groups * (a.group / part);
+    auto four = [&](int64_t p) {
+      f32x4 x;
+      if (p + 4 <= a.p1) {
+        __builtin_memcpy(&x, tops + p, 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = p + i < a.p1 ? tops[p + i] : kNegInf;
+      }
+      return x;
+    };
     uint32_t m = 0;
-    for (int64_t g = a.g0 + tid; g < a.g1; g += NT) m = max(m, order_of(stat[g][0]));
+    for (int64_t p = a.p0 + 4 * tid; p < a.p1; p += 4 * NT) {
+      const f32x4 x = four(p);
+      m = max(m, order_of(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]))));
+    }
     if constexpr (NT > 256) {
 #pragma unroll
       for (int o = 1; o < NT / 256; o *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, o));
@@ -253,36 +270,32 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
       __syncthreads();
       bound = max(bound, ((uint64_t)lim << 32) - (lim != 0));
     };
-    // words above the bound of the groups todo[b .. end); whether all had room
+    // words above the bound of the parts todo[b .. end); whether all had room
     auto collect = [&](int b, int end) {
-      // four groups of a wave at a time, all their loads before the first use
-      for (int i = b + wave; i < end; i += 4 * NW) {
-        float x[4][2];
+      // a wave reads 64 / part of them at once, four times before the first use
+      const int each = 64 / part, first = wave * each + lane / part, in = lane % part;
+      for (int i = b; i < end; i += 4 * NW * each) {
+        float x[4];
         uint32_t w[4];
+        bool on[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int e = i + q * NW;
-          w[q] = (uint32_t)(todo[min(e, end - 1)] * a.group) + lane;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const bool on = e < end && lane + 64 * h < a.group && w[q] + 64 * h < a.V;
-            x[q][h] = on ? z[w[q] + 64 * h - a.v0] : 0.0f;
-          }
+          const int e = i + q * NW * each + first;
+          w[q] = (uint32_t)(todo[min(e, end - 1)] * part + in);
+          on[q] = e < end && w[q] < a.V;
+          x[q] = on[q] ? z[w[q] - a.v0] : 0.0f;
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const bool on = i + q * NW < end && lane + 64 * h < a.group && w[q] + 64 * h < a.V;
-            const uint64_t key = key_of(x[q][h], w[q] + 64 * h);
-            const bool in = on && key > bound;
-            const uint64_t who = __ballot(in);
-            if (!who) continue;
-            int at = 0;
-            if (lane == 0) at = atomicAdd(&count, __popcll(who));
-            at = __shfl(at, 0) + __popcll(who & ((uint64_t(1) << lane) - 1));
-            if (in && at < kCap) list[at] = key;
-          }
+        for (int q = 0; q < 4; ++q) {
+          const uint64_t key = key_of(x[q], w[q]);
+          const bool up = on[q] && key > bound;
+          const uint64_t who = __ballot(up);
+          if (!who) continue;
+          int at = 0;
+          if (lane == 0) at = atomicAdd(&count, __popcll(who));
+          at = __shfl(at, 0) + __popcll(who & ((uint64_t(1) << lane) - 1));
+          if (up && at < kCap) list[at] = key;
+        }
       }
       __syncthreads();
       const int c = count;
@@ -295,22 +308,23 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
       n = c;
       return true;
     };
-    for (int64_t base = a.g0; base < a.g1; base += NT) {
+    for (int64_t base = a.p0; base < a.p1; base += 4 * NT) {
       if (tid == 0) left = 0;
       __syncthreads();
-      const int64_t g = base + tid;
-      const bool in = g < a.g1 && key_of(stat[g][0], (uint32_t)(g * a.group)) > bound;
-      const uint64_t who = __ballot(in);
-      int at = 0;
-      if (lane == 0 && who) at = atomicAdd(&left, __popcll(who));
-      at = __shfl(at, 0);
-      if (in) todo[at + __popcll(who & ((uint64_t(1) << lane) - 1))] = (int)g;
+      const int64_t p = base + 4 * tid;
+      if (p < a.p1) {
+        const f32x4 x = four(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (p + i < a.p1 && key_of(x[i], (uint32_t)((p + i) * part)) > bound)
+            todo[atomicAdd(&left, 1)] = (int)(p + i);
+      }
       __syncthreads();
       const int c = left;
       if (c && !collect(0, c)) {
         for (int b = 0; b < c;) {
-          if (n + a.group > kCap) cut();
-          const int end = min(c, b + (kCap - n) / a.group);
+          if (n + part > kCap) cut();
+          const int end = min(c, b + (kCap - n) / part);
           collect(b, end);
           b = end;
         }
@@ -668,6 +682,7 @@ hipError_t logprobs(const Logprobs& a, hipStream_t s) {
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (k.few || a.k) o.z = (float*)(w + k.z);
+    if (a.k) o.tops = (float*)(w + k.tops);
     // without best words all at once, or a copy of W's at a time
     const int64_t most = k.few ? v.V : direct(v.W, v.ldw, v.d, D) ? v.V : k.p.piece;
     int64_t step = k.few || !a.k ? most : std::min(k.first, most);
@@ -683,8 +698,8 @@ hipError_t logprobs(const Logprobs& a, hipStream_t s) {
       if (!a.k && !t.last) continue;
       t.kept = o;
       t.v0 = v0;
-      t.g0 = v0 / k.group;
-      t.g1 = (v0 + nv + k.group - 1) / k.group;
+      t.p0 = v0 / part_of(t.group);
+      t.p1 = (v0 + nv + part_of(t.group) - 1) / part_of(t.group);
       t.have = v0 > 0;
       wide(n) ? go_top<1024>(t, n, s) : go_top<256>(t, n, s);
       if ((e = hipGetLastError()) != hipSuccess) return e;

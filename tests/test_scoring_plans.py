@@ -12,7 +12,7 @@ def keep_plan(tmp_path_factory):
     return compile_plan(tmp_path_factory.mktemp("keep"), "vocab_plan.h", """
     const vocab::KeepPlan k = vocab::keep_plan(x[0], x[1], x[2], (int)x[3], x[4], x[5]);
     out = {k.few, k.tile, k.group, k.groups, k.block, k.first, k.step, k.lds, k.ldz, k.p.bytes, k.stat, k.z,
-           k.slot, k.zslot, k.best, k.thr, k.bytes, k.p.piece};""")
+           k.slot, k.zslot, k.best, k.thr, k.bytes, k.tops};""")
 
 
 def test_everything_kept_has_its_place(keep_plan):
@@ -23,14 +23,15 @@ def test_everything_kept_has_its_place(keep_plan):
     shapes += [(log_uniform(rng, 1, 1 << 20), log_uniform(rng, 1, 1 << 18), log_uniform(rng, 1, 1 << 14),
                 rng.randint(0, 2), rng.randint(0, 128), rng.randint(0, 128)) for _ in range(20000)]
     for (T, V, d, t, listed, top), got in zip(shapes, keep_plan(shapes)):
-        few, tile, group, groups, block, first, step, lds, ldz, own, stat, z, slot, zslot, best, thr, total, piece = got
+        few, tile, group, groups, block, first, step, lds, ldz, own, stat, z, slot, zslot, best, thr, total, tops = got
         assert few == (d >= 8 and T <= (64 if t == 0 else 32))
         assert group == (64 if few else tile // 2) and groups == -(-V // group) and group in (32, 64, 128)
         assert block == T or (block % 256 == 0 and block < T)
         assert lds >= groups and lds % 16 == 0
         # in order, without overlaps, aligned to whole groups of 16 bytes
         assert own <= stat and all(v % 256 == 0 for v in (stat, z, best, thr))
-        assert z - stat >= 16 * block * groups
+        assert (tops if top else z) - stat >= 16 * block * groups
+        assert not top or (tops % 256 == 0 and z - tops >= 16 * block * groups)
         if few:
             assert ldz % 64 == 0 and ldz >= V and block == T
             assert best - z >= 4 * T * ldz
