@@ -144,7 +144,7 @@ constexpr int64_t kFirst = 8192;              // words of the first step at leas
 constexpr int64_t kWhole = int64_t(1) << 26;  // logits of a block that are kept whole, in one step
 
 // What a call keeps of the logits of `block` tokens at a time: the sums of every group of
-// words; the groups of listed words in a slot each; and, to find the best words, the largest z
+// words, without listed words or with them; the z of those; and, to find the best words, the largest z
 // of each part of a group and the parts that may hold one of them, of a step of the
 // vocabulary at a time.
 struct KeepPlan {
@@ -154,10 +154,13 @@ struct KeepPlan {
   int64_t group, groups;      // words of a group, groups of a token
   int64_t block;              // tokens at a time
   int64_t first, step;        // words of the first step and of the largest (0: no best words)
+  bool marked;                // listed words have marks (else their z is found in the row of kept logits)
   int64_t lds, ldz;           // bytes of a token's slots, its row of kept logits
-  int64_t stat, tops, slot, zslot, z, best, thr, bytes;
+  int64_t stat, tops, slot, marks, places, zl, z, best, thr, bytes;
 };
-inline KeepPlan keep_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t listed, int64_t top) {
+// rows: few tokens' logits are kept whole (log probabilities).
+inline KeepPlan keep_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t listed, int64_t top,
+                          bool rows) {
   KeepPlan k{};
   k.few = few(T, d, dtype);
   if (!k.few) k.p = plan_for(T, V, d, dtype, false, true);
@@ -168,12 +171,13 @@ inline KeepPlan keep_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t li
   // (twice as many groups as best words, so that few of their words are above a group's best)
   const int64_t all = round_up(V, 256), first = std::min(all, std::max(kFirst, round_up(2 * top * k.group, 256)));
   if (!k.few) {
-    int64_t most = std::min(kKeep / std::max<int64_t>(listed * k.group, 1), kKeep / (4 * k.groups));
+    int64_t most = std::min(kKeep / std::max<int64_t>(8 * listed, 1), kKeep / (4 * k.groups));
     if (top) most = std::min(most, kKeep / first);
     k.block = std::min(T, std::max<int64_t>(256, most / 256 * 256));
   }
+  k.marked = listed && !(k.few && rows);
   if (k.few) {
-    k.ldz = round_up(V, 64);
+    k.ldz = rows ? round_up(V, 64) : 0;
   } else if (top) {
     k.step = std::min(all, std::max(first, kKeep / k.block / 256 * 256));
     k.first = k.block * all <= kWhole ? all : first;
@@ -189,9 +193,11 @@ inline KeepPlan keep_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t li
   k.stat = take(16 * k.block * k.groups);
   if (top) k.tops = take(4 * 4 * k.block * k.groups);
   k.z = take(4 * k.block * k.ldz);
-  if (!k.few && listed) {
+  if (k.marked) {
     k.slot = take(k.block * k.lds);
-    k.zslot = take(4 * k.block * listed * k.group);
+    k.marks = take(32 * k.block * listed);
+    k.places = take(k.block * listed);
+    k.zl = take(4 * k.block * listed);
   }
   k.best = take(8 * k.block * top);
   k.thr = take(4 * k.block);

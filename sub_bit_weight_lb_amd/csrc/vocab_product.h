@@ -59,20 +59,36 @@ struct Opnd {
 };
 
 // What the operators that look at single logits (vocab_top.hip) keep of them. The words
-// of a token lie in groups: half a tile's, or 64 of score_kernel's.
+// of a token lie in groups: half a tile's, or 64 of score_kernel's. The distinct words that a
+// token lists have places in its row of zl; a group with any has a mark.
+struct __attribute__((aligned(32))) Mark {
+  u32x4 words;              // which of the group's words are listed
+  uint32_t place;           // of the first of them; the others follow
+};
 struct Kept {
   f32x4* stat;              // [token][groups]: largest z; sum e - 1, e = exp(z - largest), which is
                             // summed without that 1 and so keeps the digits of a small rest; sum e (z - largest)
   int64_t groups;
-  const uint8_t* slot;      // [token][lds], nullable: the slot that a group's z go to, 255: none
-  int64_t lds, slots;
-  float* zslot;             // [token][slots][words of a group]
-  float* tops;              // [token][subs of groups], nullable: the largest z of each part of a group
+  const uint8_t* slot;      // [token][lds], nullable: a group's mark, 255: none
+  int64_t lds, listed;
+  const Mark* marks;        // [token][listed]
+  float* zl;                // [token][listed]
+  int without;              // stat leaves listed words out
+  float* tops;              // [token][parts of groups], nullable: the largest z of each part of a group
   float* z;                 // [token][ldz], nullable: z of the call's words,
   int64_t ldz;
   const float* thr;         // of parts with one above the token's thr (nullable: all)
   int flip;                 // kPick: z's factor is below zero
 };
+// The place of listed word `in` of a group
+__device__ __forceinline__ uint32_t place_of(u32x4 words, uint32_t place, int in) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = in - 32 * i;
+    place += __popc(words[i] & (n >= 32 ? ~0u : n > 0 ? (1u << n) - 1 : 0u));
+  }
+  return place;
+}
 
 // Words of a part: a group has four (of 32 words two).
 constexpr int part_of(int group) { return group == 128 ? 32 : 16; }
@@ -439,19 +455,69 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
 #pragma unroll
         for (int j = 0; j < NI; ++j) acc[i][j] = -acc[i][j];
     }
+    // what the tokens need from memory, all of it before the first use
+    float zsj[NI], thrj[NI];
+    uint32_t minej[NI];   // bit 4 i + v: a listed word
+    int slotj[NI];
+    // bit 4 i + v: past the last word
+    uint32_t past = 0;
+    if (m0 + (wm + 1) * MI * 16 > M) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) past |= (uint32_t)(16 * i + v >= left) << (4 * i + v);
+    }
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const int64_t t = c0 + 16 * j;
       const bool used = t < N && group < o.groups;
-      const float zs = fabsf(D == kF32 ? (t < N ? a.zs[t] : 0.0f) : a.z0);
-      const float thr = used && o.thr ? o.thr[t] : kNegInf;
-      const int slot = used && o.slot ? o.slot[t * o.lds + group] : 255;
+      zsj[j] = fabsf(D == kF32 ? (used ? a.zs[t] : 0.0f) : a.z0);
+      thrj[j] = used && o.thr ? o.thr[t] : kNegInf;
+      slotj[j] = used && o.slot ? o.slot[t * o.lds + group] : 255;
+    }
+    u32x4 words[NI];
+    uint32_t place[NI];
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      words[j] = u32x4{0, 0, 0, 0};
+      place[j] = 0;
+      if (slotj[j] != 255) {
+        const Mark& m = o.marks[(c0 + 16 * j) * o.listed + slotj[j]];
+        words[j] = m.words;
+        place[j] = m.place;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      minej[j] = 0;
+      if (!__ballot(slotj[j] != 255)) continue;
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const uint32_t four = words[j][i / 2] >> (16 * (i & 1) + 4 * g) & 15u;
+        minej[j] |= four << (4 * i);
+        if (__ballot(four)) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if (four >> v & 1u)
+              o.zl[(c0 + 16 * j) * o.listed + place_of(words[j], place[j], 16 * i + 4 * g + v)] = acc[i][j][v] * zsj[j];
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const int64_t t = c0 + 16 * j;
+      const bool used = t < N && group < o.groups;
+      const float zs = zsj[j], thr = thrj[j];
+      const uint32_t mine = minej[j];
+      const uint32_t off = past | (o.without ? mine : 0u);   // bits of words that are left out
+      // all ones for a word that is not
+      auto on = [&](int bit) { return (uint32_t)((int)(~off << (31 - bit)) >> 31); };
       // parts of the group: PI row tiles each
       constexpr int PARTS = 16 * MI / part_of(16 * MI), PI = MI / PARTS;
       float tops[PARTS], top = kNegInf, sum = 0.0f, dot = 0.0f, r;
       const float by = zs * 1.44269504f;
       auto add = [](float x, float y) { return x + y; };
-      auto sums = [&](auto whole) {   // (whole: no word past the last)
+      auto sums = [&](auto whole) {   // (whole: no word is left out)
         constexpr bool ALL = decltype(whole)::value;
 #pragma unroll
         for (int q = 0; q < PARTS; ++q) {
@@ -460,7 +526,9 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
           for (int i = q * PI; i < (q + 1) * PI; ++i)
 #pragma unroll
             for (int v = 0; v < 4; ++v)
-              if (ALL || 16 * i + v < left) x = fmaxf(x, acc[i][j][v]);
+              x = fmaxf(x, ALL ? acc[i][j][v]
+                               : __uint_as_float((__float_as_uint(acc[i][j][v]) & on(4 * i + v)) |
+                                                 (0xff800000u & ~on(4 * i + v))));
           tops[q] = across(x, [](float x, float y) { return fmaxf(x, y); });
           top = fmaxf(top, tops[q]);
         }
@@ -469,9 +537,10 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             const float y = (acc[i][j][v] - top) * by;
-            const float e = __builtin_amdgcn_exp2f(y);
-            sum += ALL || 16 * i + v < left ? e : 0.0f;
-            dot = ALL || 16 * i + v < left ? fmaf(e, y, dot) : dot;
+            float e = __builtin_amdgcn_exp2f(y);
+            if (!ALL) e = __uint_as_float(__float_as_uint(e) & on(4 * i + v));
+            sum += e;
+            dot = fmaf(e, y, dot);
           }
         sum = across(sum, add);
         dot = across(dot, add);
@@ -484,14 +553,17 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
               const float y = acc[i][j][v] - top;
-              const bool on = ALL || 16 * i + v < left;
-              ones += on && y == 0.0f ? 1.0f : 0.0f;
-              rest += on && y != 0.0f ? __builtin_amdgcn_exp2f(y * by) : 0.0f;
+              const bool in = ALL || !(off >> (4 * i + v) & 1u);
+              ones += in && y == 0.0f ? 1.0f : 0.0f;
+              rest += in && y != 0.0f ? __builtin_amdgcn_exp2f(y * by) : 0.0f;
             }
           r = across(rest, add) + (across(ones, add) - 1.0f);
         }
+        // (no word left: a sum of 0)
+        constexpr uint32_t every = MI == 8 ? ~0u : (1u << (4 * MI & 31)) - 1;
+        if (!ALL && across(off == every ? 0.0f : 1.0f, add) == 0.0f) dot = 0.0f;
       };
-      if (m0 + (wm + 1) * MI * 16 <= M)
+      if (!__ballot(off))
         sums(std::true_type{});
       else
         sums(std::false_type{});
@@ -504,14 +576,9 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
           for (int q = 0; q < PARTS; q += 2) *(u32x2*)(p + q) = u32x2{__float_as_uint(tops[q] * zs), __float_as_uint(tops[q + 1] * zs)};
         }
       }
-      auto put = [&](float* p, int i) {   // (of words past the last too: rows and slots hold whole groups)
+      auto put = [&](float* p, int i) {   // (of words past the last too: rows hold whole groups)
         *(f32x4*)(p + 16 * i + 4 * g) = acc[i][j] * zs;
       };
-      if (slot != 255) {
-        float* p = o.zslot + (t * o.slots + slot) * (16 * MI);
-#pragma unroll
-        for (int i = 0; i < MI; ++i) put(p, i);
-      }
       if (o.z) {
         float* p = o.z + t * o.ldz + (tm * WM + wm) * (16 * MI);
 #pragma unroll
@@ -742,15 +809,34 @@ __global__ __launch_bounds__(1024 / NT)
                   (uint32_t)q[2][p] | (uint32_t)q[3][p] << 16};
     } else {
       float m = kNegInf, x[4];
+      [[maybe_unused]] bool on[4];
+      if constexpr (PICK) {
+        const int slot = t < T && o.slot ? o.slot[t * o.lds + blockIdx.x] : 255;
+        u32x4 words = {0, 0, 0, 0};
+        uint32_t place = 0;
+        if (slot != 255) {
+          words = o.marks[t * o.listed + slot].words;
+          place = o.marks[t * o.listed + slot].place;
+        }
+        const uint32_t half = wave & 2 ? words[1] : words[0];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        x[v] = scale * z[v];
-        if (w + v < V) m = fmaxf(m, x[v]);
-        if constexpr (!PICK)
+        for (int v = 0; v < 4; ++v) {
+          const int in = 16 * wave + 4 * g + v;
+          const bool mine = half >> (in & 31) & 1u;
+          x[v] = scale * z[v];
+          on[v] = w + v < V && !(mine && o.without);
+          if (on[v]) m = fmaxf(m, x[v]);
+          if (mine) o.zl[t * o.listed + place_of(words, place, in)] = x[v];
+        }
+        if (t < T && o.z) *(f32x4*)(o.z + t * o.ldz + w) = f32x4{x[0], x[1], x[2], x[3]};
+      } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          x[v] = scale * z[v];
+          if (w + v < V) m = fmaxf(m, x[v]);
           if (w + v < V && w + v == label) o.hit[t] = x[v];
+        }
       }
-      if constexpr (PICK)
-        if (t < T) *(f32x4*)(o.z + t * o.ldz + w) = f32x4{x[0], x[1], x[2], x[3]};
       m = fmaxf(m, __shfl_xor(m, 16));
       m = fmaxf(m, __shfl_xor(m, 32));
       float s = 0.0f;
@@ -759,10 +845,9 @@ __global__ __launch_bounds__(1024 / NT)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const float a = x[v] - m, e = __expf(a);
-          const bool on = w + v < V;
-          ones += on && a == 0.0f ? 1.0f : 0.0f;
-          s += !on || a == 0.0f ? 0.0f : x[v] == kNegInf ? __uint_as_float(0x7fc00000u) : e;
-          y += on ? e * a : 0.0f;
+          ones += on[v] && a == 0.0f ? 1.0f : 0.0f;
+          s += !on[v] || a == 0.0f ? 0.0f : x[v] == kNegInf ? __uint_as_float(0x7fc00000u) : e;
+          y += on[v] ? e * a : 0.0f;
         }
         ones += __shfl_xor(ones, 16);
         ones += __shfl_xor(ones, 32);
@@ -797,7 +882,7 @@ __global__ __launch_bounds__(1024 / NT)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float a = st[0][i][t] - m, e = __expf(a), r = st[1][i][t] + st[3][i][t];
-          if (v0 + 16 * i < V) {
+          if (r != -1.0f) {   // (-1: no word, a sum of 0)
             ones += a == 0.0f ? 1.0f : 0.0f;
             s += a == 0.0f ? r : e * (1.0f + r);
             y += (st[2][i][t] + a * (1.0f + r)) * e;

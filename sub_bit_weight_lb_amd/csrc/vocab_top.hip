@@ -16,8 +16,9 @@
 //   the listed words' part would be rounding where they hold all but 2^-20 of it.
 //
 // The product's epilogue kPick (up to 32 tokens, fp32 64: score_kernel) leaves, per token and
-// group of words, the largest z and the sums S and U about it, and the z of
-//   groups with a listed word: each has a slot, which slots_kernel gives;
+// group of words, the largest z and the sums S and U about it (for a divergence with a tail
+// without the listed words), and the z of
+//   listed words: marks_kernel has told where they are;
 //   parts of groups that may hold one of the best words: the vocabulary is taken in steps,
 //   and from the second on only parts with a z above the k-th best so far are written.
 // A workgroup per token (top_kernel, distill_kernel) then joins the groups.
@@ -79,43 +80,59 @@ __device__ __forceinline__ Sums join_all(Sums a, float* sm) {
   return a;
 }
 
-// ---------------------------------------------------------------- slots
-// The first of a token's K entries with the same group as entry k (its owner), and whether an
-// earlier entry has the same word. grp, word: of the entries, in LDS, -1 for none; padded to 4.
-struct Same {
-  int owner;
-  bool twice;
+// ---------------------------------------------------------------- listed words
+// slot, marks (Kept) and the place of each of a token's K entries in its row of zl (255: a word
+// below 0 or past the last): the distinct words of its list, by groups in the order of their
+// first entries. A workgroup per token.
+struct Marks {
+  uint8_t* slot;
+  int64_t lds;
+  Mark* marks;               // [token][K]
+  uint8_t* places;           // [token][K]
 };
-__device__ __forceinline__ Same same(const int* grp, const int* word, int K, int k) {
+__global__ __launch_bounds__(kList) void marks_kernel(const int32_t* __restrict__ ids, int64_t ldi,
+                                                      int K, int64_t V, int group, Marks o) {
   typedef int i32x4 __attribute__((ext_vector_type(4)));
-  const int g = grp[k], w = word[k];
-  Same r{k, false};
-#pragma unroll 4
-  for (int j = 0; j < K; j += 4) {
-    const i32x4 gs = *(const i32x4*)(grp + j), ws = *(const i32x4*)(word + j);
-#pragma unroll
-    for (int u = 3; u >= 0; --u) {
-      r.owner = gs[u] == g && j + u < r.owner ? j + u : r.owner;
-      r.twice |= ws[u] == w && j + u < k;
-    }
-  }
-  return r;
-}
-// slot[t][group] = the first of the token's K entries with a word in it, 255 for groups without
-// one. A workgroup per token.
-__global__ __launch_bounds__(kList) void slots_kernel(const int32_t* __restrict__ ids, int64_t ldi,
-                                                      int K, int64_t V, int group,
-                                                      uint8_t* __restrict__ slot, int64_t lds) {
-  __shared__ __align__(16) int gr[kList];
+  __shared__ __align__(16) int grp[kList], sizes[kList];
+  __shared__ u32x4 words[kList];
+  __shared__ uint32_t base[kList];
   const int64_t t = blockIdx.x;
   const int k = threadIdx.x;
-  uint8_t* row = slot + t * lds;
   const int32_t id = k < K ? ids[t * ldi + k] : -1;
-  for (int64_t i = 16 * k; i < lds; i += 16 * kList)
-    *(u32x4*)(row + i) = u32x4{~0u, ~0u, ~0u, ~0u};
-  gr[k] = id >= 0 && id < V ? id / group : -1;
+  const bool real = id >= 0 && id < V;
+  const int mine = real ? id / group : -1, in = real ? id - mine * group : 0;
+  uint8_t* row = o.slot + t * o.lds;
+  for (int64_t i = 16 * k; i < o.lds; i += 16 * kList) *(u32x4*)(row + i) = u32x4{~0u, ~0u, ~0u, ~0u};
+  grp[k] = mine;
+  words[k] = u32x4{0, 0, 0, 0};
   __syncthreads();
-  if (gr[k] >= 0 && same(gr, gr, K, k).owner == k) row[gr[k]] = (uint8_t)k;
+  int owner = k;   // the first entry of the same group
+#pragma unroll 4
+  for (int j = 0; j < K; j += 4) {
+    const i32x4 g = *(const i32x4*)(grp + j);
+#pragma unroll
+    for (int u = 3; u >= 0; --u) owner = g[u] == mine && j + u < owner ? j + u : owner;
+  }
+  if (real) atomicOr((uint32_t*)&words[owner] + (in >> 5), 1u << (in & 31));
+  __syncthreads();
+  const u32x4 own = words[k];
+  sizes[k] = __popc(own[0]) + __popc(own[1]) + __popc(own[2]) + __popc(own[3]);
+  __syncthreads();
+  uint32_t place = 0;
+#pragma unroll 4
+  for (int j = 0; j < K; j += 4) {
+    const i32x4 n = *(const i32x4*)(sizes + j);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) place += j + u < k ? (uint32_t)n[u] : 0u;
+  }
+  base[k] = place;
+  if (real && owner == k) {
+    row[mine] = (uint8_t)k;
+    o.marks[t * K + k].words = own;
+    o.marks[t * K + k].place = place;
+  }
+  __syncthreads();
+  if (k < K) o.places[t * K + k] = real ? (uint8_t)place_of(words[owner], base[owner], in) : (uint8_t)255;
 }
 
 // ---------------------------------------------------------------- log probabilities
@@ -128,6 +145,7 @@ struct Top {
   float* thr;                // [token]: the k-th best z
   int last;                  // the last step: what follows is written
   const int32_t* tokens;     // [token][ldt]
+  const uint8_t* places;     // [token][given], nullable: where their z are in zl (else in z)
   int64_t ldt;
   int given;
   float *logprobs, *entropy, *lse;
@@ -177,9 +195,9 @@ __device__ __forceinline__ uint32_t reached(const uint32_t (&x)[N], int k, int l
 //   value), as many parts at a time as it has room for.
 template <int NT>
 __global__ __launch_bounds__(NT) void top_kernel(Top a) {
-  constexpr int kCap = 1024, NW = NT / 64, kEach = kCap / 64;
+  constexpr int kCap = 512, NW = NT / 64, kEach = kCap / 64;
   __shared__ uint64_t list[kCap];
-  __shared__ __align__(16) uint32_t most[256];
+  __shared__ __align__(16) uint32_t most[NT > 64 ? 256 : 4];
   __shared__ int todo[4 * NT];
   __shared__ int count, left;
   __shared__ uint32_t lim;
@@ -203,22 +221,28 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
       }
       return x;
     };
-    uint32_t m = 0;
+    uint32_t m[4] = {};
     for (int64_t p = a.p0 + 4 * tid; p < a.p1; p += 4 * NT) {
       const f32x4 x = four(p);
-      m = max(m, order_of(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]))));
-    }
-    if constexpr (NT > 256) {
+      if constexpr (NT > 64) {
+        m[0] = max(m[0], order_of(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]))));
+      } else {
 #pragma unroll
-      for (int o = 1; o < NT / 256; o *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, o));
+        for (int i = 0; i < 4; ++i) m[i] = max(m[i], order_of(x[i]));
+      }
     }
-    if (tid % (NT / 256) == 0) most[tid / (NT / 256)] = m;
-    if (a.have && tid < k) list[tid] = a.best[t * k + tid];
+    if constexpr (NT > 64) {
+#pragma unroll
+      for (int o = 1; o < NT / 256; o *= 2) m[0] = max(m[0], (uint32_t)__shfl_xor((int)m[0], o));
+      if (tid % (NT / 256) == 0) most[tid / (NT / 256)] = m[0];
+    }
+    if (a.have)
+      for (int i = tid; i < k; i += NT) list[i] = a.best[t * k + i];
     if (tid == 0) count = a.have ? k : 0;
     __syncthreads();
     uint64_t bound;   // keys above it are in
     {
-      const u32x4 q = ((const u32x4*)most)[lane];
+      const u32x4 q = NT > 64 ? ((const u32x4*)most)[lane] : u32x4{m[0], m[1], m[2], m[3]};
       const uint32_t x[4] = {q[0], q[1], q[2], q[3]};
       int n;
       const uint32_t c = reached(x, k, 12, &n);
@@ -332,7 +356,7 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
     }
     cut();
     if (!a.last) {
-      if (tid < k) a.best[t * k + tid] = tid < n ? list[tid] : 0;
+      for (int i = tid; i < k; i += NT) a.best[t * k + i] = i < n ? list[i] : 0;
       if (tid == 0) a.thr[t] = value_of(lim);
       return;
     }
@@ -349,10 +373,10 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
     a.lse[t] = r.m + log_s;
     a.entropy[t] = log_s - r.u / (1.0f + r.r);
   }
-  if (tid < k) {
-    int place = tid;
+  for (int i = tid; i < k; i += NT) {
+    int place = i;
     if (fine) {
-      const uint64_t key = list[tid];
+      const uint64_t key = list[i];
       place = 0;
 #pragma unroll 8
       for (int j = 0; j < k; ++j) place += list[j] > key;
@@ -363,27 +387,25 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
       a.top_logprobs[t * k + place] = kNaN;
     }
   }
-  if (tid < a.given) {
-    const int32_t id = a.tokens[t * a.ldt + tid];
+  for (int i = tid; i < a.given; i += NT) {
+    const int32_t id = a.tokens[t * a.ldt + i];
     float x = id < 0 ? 0.0f : kNaN;
     if (id >= 0 && id < a.V) {
       const Kept& o = a.kept;
-      const float z = o.slot ? o.zslot[(t * o.slots + o.slot[t * o.lds + id / a.group]) * a.group + id % a.group]
-                             : o.z[t * o.ldz + id];
+      const float z = a.places ? o.zl[t * a.given + a.places[t * a.given + i]] : o.z[t * o.ldz + id];
       x = z - r.m - log_s;
     }
-    a.logprobs[t * a.given + tid] = x;
+    a.logprobs[t * a.given + i] = x;
   }
 }
 
 // ---------------------------------------------------------------- divergence
 struct Near {
   Kept kept;
-  int group;
-  int64_t V;
   const int32_t* ids;
   const float* logq;
   int64_t ldi, ldq;
+  const uint8_t* places;     // [token][K]
   int K, tail;
   float *loss, *lse, *rest, *hit;
 };
@@ -429,121 +451,52 @@ __device__ __forceinline__ Teacher teacher(const float (&l)[2], const bool (&on)
   return t;
 }
 
-// loss, lse, rest and hit of a token from its groups' sums and the z of its listed words. A
-// workgroup of NT threads per token.
-//   With a tail, the groups with listed words are left out of the groups' sums, and their
-//   other words are summed here from the slots.
+// loss, lse, rest and hit of a token from its groups' sums (with a tail: without the listed
+// words) and the z of its listed words. A workgroup of NT threads per token.
 template <int NT>
 __global__ __launch_bounds__(NT) void distill_kernel(Near a) {
-  constexpr int NW = NT / 64;
-  __shared__ __align__(16) int grp[kList], word[kList];
-  __shared__ int owner[kList];
-  __shared__ bool again[kList];        // an earlier entry has the same word
-  __shared__ uint32_t out[kList][4];   // of the owner's group: the words that are listed
-  __shared__ float zs[kList];
-  __shared__ int used;
-  __shared__ float sm[3 * NW];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ float sm[3 * (NT / 64)];
+  const int tid = threadIdx.x, lane = tid & 63;
   const int64_t t = blockIdx.x;
   const Kept& o = a.kept;
-  f32x4* stat = o.stat + t * o.groups;
-  if (tid == 0) used = 0;
-  int32_t id = -1;
-  if (tid < kList) {
-    id = tid < a.K ? a.ids[t * a.ldi + tid] : -1;
-    word[tid] = id;
-    grp[tid] = id >= 0 && id < a.V ? id / a.group : -1;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) out[tid][i] = 0;
-  }
-  __syncthreads();
-  auto logits = [&](int own) {   // the owner's group
-    return o.slot ? o.zslot + (t * o.slots + own) * a.group : o.z + t * o.ldz + (int64_t)grp[own] * a.group;
-  };
-  if (tid < kList) {
-    const int mine = grp[tid];
-    const Same first = same(grp, word, a.K, tid);
-    const int own = first.owner;
-    owner[tid] = mine >= 0 ? own : -1;
-    again[tid] = first.twice;
-    if (id >= 0) used = 1;   // (all write the same)
-    float z = id < 0 ? 0.0f : kNaN;
-    if (mine >= 0) {
-      const int in = id - mine * a.group;
-      z = logits(own)[in];
-      atomicOr(&out[own][in >> 5], 1u << (in & 31));
-      if (a.tail && own == tid) stat[mine] = f32x4{kNegInf, -1.0f, 0.0f, 0.0f};
-    }
-    zs[tid] = z;
-  }
-  __syncthreads();
-  Sums r = kNothing;
-  for (int64_t g = tid; g < o.groups; g += NT) {
-    const f32x4 x = stat[g];
-    join(r, Sums{x[0], x[1], 0.0f});
-  }
-  if (a.tail) {
-    // four groups of a wave at a time, all their loads before the first use
-    for (int k0 = wave; k0 < a.K; k0 += 4 * NW) {
-      float x[4][2];
-      bool on[4][2];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int k = min(k0 + q * NW, a.K - 1);
-        const bool own = k0 + q * NW < a.K && owner[k] == k;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int i = lane + 64 * h;
-          on[q][h] = own && i < a.group && (int64_t)grp[k] * a.group + i < a.V &&
-                     !(out[k][(i >> 5) & 3] >> (i & 31) & 1);
-          x[q][h] = on[q][h] ? logits(k)[i] : 0.0f;
-        }
-      }
-      Sums b{kNegInf, -1.0f, 0.0f};
-      bool bad = false;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          b.m = on[q][h] ? fmaxf(b.m, x[q][h]) : b.m;
-          bad |= on[q][h] && !(fabsf(x[q][h]) < __builtin_inff());
-        }
-      float ones = -1.0f, sum = 0.0f;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float y = x[q][h] - b.m;
-          ones += on[q][h] && y == 0.0f ? 1.0f : 0.0f;
-          sum += on[q][h] && y != 0.0f ? __expf(y) : 0.0f;
-        }
-      b.r = bad ? kNaN : sum + ones;
-      join(r, b);
-    }
-  }
-  r = join_all<NT>(r, sm);
-  if (wave) return;
-  // entries lane and lane + 64
-  float z[2], l[2];
-  bool on[2], twice[2];
+  const f32x4* stat = o.stat + t * o.groups;
+  const float* zl = o.zl + t * a.K;
+  // entries lane and lane + 64 of the token
+  float z[2], l[2], x[2];
+  bool on[2];
+  int place[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int k = lane + 64 * i;
-    on[i] = word[k] >= 0;
-    z[i] = zs[k];
+    const int32_t id = k < a.K ? a.ids[t * a.ldi + k] : -1;
+    on[i] = id >= 0;
+    place[i] = on[i] ? a.places[t * a.K + k] : 255;
     l[i] = on[i] ? a.logq[t * a.ldq + k] : 0.0f;
-    twice[i] = again[k];
+    z[i] = !on[i] ? 0.0f : place[i] == 255 ? kNaN : zl[place[i]];
   }
+  Sums r = kNothing;
+  for (int64_t g = tid; g < o.groups; g += NT) {
+    const f32x4 q = stat[g];
+    join(r, Sums{q[0], q[1], 0.0f});
+  }
+  r = join_all<NT>(r, sm);
+  if (tid >= 64) return;
+  const bool used = __ballot(on[0] || on[1]) != 0;
   const Teacher q = teacher(l, on, a.tail);
   double m = r.m, s = 1.0 + (double)r.r;
   const bool all = r.r == -1.0f;   // every word is listed
   if (a.tail) {
-    // the listed words' part
-    m = wave_max(fmax(on[0] ? (double)z[0] : -INFINITY, on[1] ? (double)z[1] : -INFINITY));
+    // the part of the listed words, which have the places 0 .. n - 1
+    int n = max(place[0] == 255 ? 0 : place[0] + 1, place[1] == 255 ? 0 : place[1] + 1);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) n = max(n, __shfl_xor(n, o));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x[i] = lane + 64 * i < n ? zl[lane + 64 * i] : kNegInf;
+    m = wave_max(fmax((double)x[0], (double)x[1]));
     m = fmax(m, (double)r.m);
     double e = 0.0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) e += on[i] && !twice[i] && word[lane + 64 * i] < a.V ? exp((double)z[i] - m) : 0.0;
+    for (int i = 0; i < 2; ++i) e += lane + 64 * i < n ? exp((double)x[i] - m) : 0.0;
     s = wave_sum(e);
     if (!all) s += (1.0 + (double)r.r) * exp((double)r.m - m);
   }
@@ -557,7 +510,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(Near a) {
   if (!all && q.r != 0.0) loss += q.r * (log(q.r) - (rest - m) + log_s);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    if (lane + 64 * i < a.K) a.hit[t * a.K + lane + 64 * i] = used ? z[i] : 0.0f;
+    if (lane + 64 * i < a.K) a.hit[t * a.K + lane + 64 * i] = z[i];
   if (lane == 0) {
     a.loss[t] = used ? (float)loss : 0.0f;
     a.lse[t] = used ? (float)(m + log_s) : 0.0f;
@@ -637,16 +590,28 @@ hipError_t pick(const Vocab& a, const KeepPlan& k, const Opnd& H, int64_t t0, in
   return mma_launch<D, kPick>(m, k.tile, 1, s);
 }
 
+// Where what is kept of listed words lies, and the marks of n tokens
+hipError_t mark(char* w, const KeepPlan& k, const int32_t* ids, int64_t ldi, int64_t K, int64_t n, int64_t V,
+                Kept* o, const uint8_t** places, hipStream_t s) {
+  const Marks m{(uint8_t*)(w + k.slot), k.lds, (Mark*)(w + k.marks), (uint8_t*)(w + k.places)};
+  o->slot = m.slot;
+  o->lds = k.lds;
+  o->listed = K;
+  o->marks = m.marks;
+  o->zl = (float*)(w + k.zl);
+  *places = m.places;
+  hipLaunchKernelGGL(marks_kernel, dim3((unsigned)n), dim3(kList), 0, s, ids, ldi, (int)K, V, (int)k.group, m);
+  return hipGetLastError();
+}
+
 template <int NT> void go_top(const Top& t, int64_t rows, hipStream_t s) {
   hipLaunchKernelGGL(top_kernel<NT>, dim3((unsigned)rows), dim3(NT), 0, s, t);
 }
-// (more threads per token where there are few)
-bool wide(int64_t T) { return T <= 64; }
 
 template <int D>
 hipError_t logprobs(const Logprobs& a, hipStream_t s) {
   const Vocab& v = a.v;
-  const KeepPlan k = keep_plan(v.T, v.V, v.d, D, a.given, a.k);
+  const KeepPlan k = keep_plan(v.T, v.V, v.d, D, a.given, a.k, true);
   char* w = (char*)v.work;
   hipError_t e;
   Kept o{};
@@ -672,15 +637,7 @@ hipError_t logprobs(const Logprobs& a, hipStream_t s) {
     t.lse = a.lse + t0;
     t.top_ids = a.top_ids + t0 * a.k;
     t.top_logprobs = a.top_logprobs + t0 * a.k;
-    if (!k.few && a.given) {
-      o.slot = (uint8_t*)(w + k.slot);
-      o.lds = k.lds;
-      o.slots = a.given;
-      o.zslot = (float*)(w + k.zslot);
-      hipLaunchKernelGGL(slots_kernel, dim3((unsigned)n), dim3(kList), 0, s, t.tokens, a.ldt, t.given,
-                         v.V, t.group, (uint8_t*)(w + k.slot), k.lds);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
+    if (k.marked && (e = mark(w, k, t.tokens, a.ldt, a.given, n, v.V, &o, &t.places, s)) != hipSuccess) return e;
     if (k.few || a.k) o.z = (float*)(w + k.z);
     if (a.k) o.tops = (float*)(w + k.tops);
     // without best words all at once, or a copy of W's at a time
@@ -701,7 +658,7 @@ hipError_t logprobs(const Logprobs& a, hipStream_t s) {
       t.p0 = v0 / part_of(t.group);
       t.p1 = (v0 + nv + part_of(t.group) - 1) / part_of(t.group);
       t.have = v0 > 0;
-      wide(n) ? go_top<1024>(t, n, s) : go_top<256>(t, n, s);
+      n <= 64 ? go_top<512>(t, n, s) : go_top<256>(t, n, s);
       if ((e = hipGetLastError()) != hipSuccess) return e;
       if (a.k) step = std::min(std::min(3 * step, k.step), most);
     }
@@ -712,24 +669,14 @@ hipError_t logprobs(const Logprobs& a, hipStream_t s) {
 template <int D>
 hipError_t distill(const Distill& a, hipStream_t s) {
   const Vocab& v = a.v;
-  const KeepPlan k = keep_plan(v.T, v.V, v.d, D, a.K, 0);
+  const KeepPlan k = keep_plan(v.T, v.V, v.d, D, a.K, 0, false);
   char* w = (char*)v.work;
   hipError_t e;
   Near r{};
   r.kept.flip = v.scale < 0.0f;
   r.kept.stat = (f32x4*)(w + k.stat);
   r.kept.groups = k.groups;
-  r.kept.ldz = k.ldz;
-  if (k.few) {
-    r.kept.z = (float*)(w + k.z);
-  } else {
-    r.kept.slot = (uint8_t*)(w + k.slot);
-    r.kept.lds = k.lds;
-    r.kept.slots = a.K;
-    r.kept.zslot = (float*)(w + k.zslot);
-  }
-  r.group = (int)k.group;
-  r.V = v.V;
+  r.kept.without = a.tail;
   r.ldi = a.ldi;
   r.ldq = a.ldq;
   r.K = (int)a.K;
@@ -744,20 +691,15 @@ hipError_t distill(const Distill& a, hipStream_t s) {
     r.lse = a.lse + t0;
     r.rest = a.rest + t0;
     r.hit = a.hit + t0 * a.K;
+    if ((e = mark(w, k, r.ids, a.ldi, a.K, n, v.V, &r.kept, &r.places, s)) != hipSuccess) return e;
     if (k.few) {
       if ((e = score<D>(v, 0, v.V, r.kept, s)) != hipSuccess) return e;
     } else {
-      hipLaunchKernelGGL(slots_kernel, dim3((unsigned)n), dim3(kList), 0, s, r.ids, a.ldi, r.K, v.V,
-                         r.group, (uint8_t*)(w + k.slot), k.lds);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
       const int64_t step = direct(v.W, v.ldw, v.d, D) ? v.V : k.p.piece;
       for (int64_t v0 = 0; v0 < v.V; v0 += step)
         if ((e = pick<D>(v, k, H, t0, n, v0, std::min(step, v.V - v0), r.kept, s)) != hipSuccess) return e;
     }
-    if (wide(n))
-      hipLaunchKernelGGL(distill_kernel<1024>, dim3((unsigned)n), dim3(1024), 0, s, r);
-    else
-      hipLaunchKernelGGL(distill_kernel<256>, dim3((unsigned)n), dim3(256), 0, s, r);
+    hipLaunchKernelGGL(distill_kernel<256>, dim3((unsigned)n), dim3(256), 0, s, r);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return hipSuccess;
@@ -780,10 +722,10 @@ SharePlan share_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t K) {
 }  // namespace
 
 int64_t logprobs_work_bytes(int64_t T, int64_t V, int64_t d, int dtype, int64_t given, int64_t k) {
-  return keep_plan(T, V, d, dtype, given, k).bytes;
+  return keep_plan(T, V, d, dtype, given, k, true).bytes;
 }
 int64_t distill_work_bytes(int64_t T, int64_t V, int64_t d, int dtype, int64_t K, bool grad) {
-  return grad ? share_plan(T, V, d, dtype, K).bytes : keep_plan(T, V, d, dtype, K, 0).bytes;
+  return grad ? share_plan(T, V, d, dtype, K).bytes : keep_plan(T, V, d, dtype, K, 0, false).bytes;
 }
 
 hipError_t launch_vocab_logprobs(const Logprobs& a, hipStream_t s) {
