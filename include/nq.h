@@ -525,12 +525,18 @@ int64_t nq_vocab_logprobs_work_bytes(int64_t T, int64_t V, int64_t d, int32_t dt
 nq_status nq_vocab_distill(const void* H, int64_t ldh, const void* W, int64_t ldw, int32_t dtype,
                            int64_t T, int64_t V, int64_t d, const int32_t* ids, int64_t ldi,
                            const float* logq, int64_t ldq, int64_t K, float scale, int32_t tail,
-                           float* loss, float* lse, float* rest, float* hit, void* work,
-                           void* stream);
+                           float* loss, float* lse, float* rest, float* hit, float* logits,
+                           void* work, void* stream);
+
+/* Number of float32 in `logits` of the call above, which the gradient of few tokens can take to
+ * read W once less: nq_vocab_distill_logits(T, V, d, dtype) device floats, 16-byte aligned, or
+ * NULL (0 floats, of more tokens: ignored). Host only; -1 for sizes out of range. */
+int64_t nq_vocab_distill_logits(int64_t T, int64_t V, int64_t d, int32_t dtype);
 
 /* Gradient of sum_t dloss_t loss_t from the lse, rest and hit of nq_vocab_distill on the
- * same arguments (and in one call: see nq_vocab_loss_backward, whose products, types,
- * roundings and limits these are): with Q = sum q + r (1 where tail == 0),
+ * same arguments and in one call, and its logits where they were kept (NULL: computed
+ * again). Of more than 32 tokens (float32: 64), or d < 8, the products, roundings and limits
+ * are those of nq_vocab_loss_backward; fewer have all but the results in float32. With Q = sum q + r (1 where tail == 0),
  *   G_tv = (Q exp(z_tv - lse_t) - sum of q over v's entries) dloss_t scale, v listed,
  *   G_tv = exp(z_tv - rest_t) (Q exp(rest_t - lse_t) - r) dloss_t scale, v not listed,
  *   dH (T x d, row stride lddh) = G W,   dW (V x d, row stride lddw) = G^T H
@@ -542,9 +548,9 @@ nq_status nq_vocab_distill_backward(const void* H, int64_t ldh, const void* W, i
                                     int32_t dtype, int64_t T, int64_t V, int64_t d,
                                     const int32_t* ids, int64_t ldi, const float* logq, int64_t ldq,
                                     int64_t K, float scale, int32_t tail, const float* lse,
-                                    const float* rest, const float* hit, const float* dloss,
-                                    void* dH, int64_t lddh, void* dW, int64_t lddw, void* work,
-                                    void* stream);
+                                    const float* rest, const float* hit, const float* logits,
+                                    const float* dloss, void* dH, int64_t lddh, void* dW,
+                                    int64_t lddw, void* work, void* stream);
 
 /* Bytes of `work` for the two calls above (grad: 0 for the loss, 1 for its
  * gradient). Host only; -1 for sizes out of range. */

@@ -772,10 +772,13 @@ def vocab_logprobs(H, W, tokens=None, k=0, scale=1.0, out=None, work=None, strea
 @dataclass
 class VocabDistill:
     """What vocab_distill hands to its gradient for T tokens with K entries each: lse
-    and rest (T) and hit (T x K), float32."""
+    and rest (T) and hit (T x K), float32; of few tokens also their logits (T x V to
+    the next multiple of 64), which save the gradient a pass over W (None: they are
+    computed again)."""
     lse: "object"
     rest: "object"
     hit: "object"
+    logits: "object" = None
 
 
 def vocab_distill_work_bytes(T, V, d, dtype, K, grad=False):
@@ -795,13 +798,17 @@ def _distill_args(H, W, ids, logq):
     return T, V, d, code, ldh, ldw, K, ldi, ldq
 
 
-def _distill_state(q, T, K):
+def _distill_state(q, T, V, K):
     f32 = _torch().float32
     if not isinstance(q, VocabDistill):
         raise TypeError("the loss's state must be a VocabDistill")
     _vector(q.lse, "lse", T, f32)
     _vector(q.rest, "rest", T, f32)
     _vector(q.hit, "hit", T * K, f32)
+    if q.logits is not None:
+        _vector(q.logits, "logits", T * -(-V // 64) * 64, f32)
+        if q.logits.data_ptr() % 16:
+            raise ValueError("logits must be 16-byte aligned")
 
 
 def vocab_distill(H, W, ids, logq, scale=1.0, tail=True, loss=None, state=None, work=None,
@@ -822,22 +829,25 @@ def vocab_distill(H, W, ids, logq, scale=1.0, tail=True, loss=None, state=None, 
     if loss is not None:
         _vector(loss, "loss", T, f32)
     if state is not None:
-        _distill_state(state, T, K)
-        given = (state.lse, state.rest, state.hit)
+        _distill_state(state, T, V, K)
+        given = (state.lse, state.rest, state.hit, state.logits)
     else:
-        given = (None, None, None)
-    on = _on_device("H W ids logq loss lse rest hit work", H, W, ids, logq, loss, *given, work)
+        given = (None, None, None, None)
+    on = _on_device("H W ids logq loss lse rest hit logits work", H, W, ids, logq, loss, *given, work)
 
     def run(handle):
         def new(*shape):
             return torch.empty(shape, dtype=f32, device=H.device)
         a = new(T) if loss is None else loss
-        q = VocabDistill(new(T), new(T), new(T, K)) if state is None else state
         lib = _lib.load()
+        q = state
+        if q is None:
+            kept = lib.nq_vocab_distill_logits(T, V, d, code)
+            q = VocabDistill(new(T), new(T), new(T, K), new(T, kept // T) if kept > 0 else None)
         w = _workspace(work, lib.nq_vocab_distill_work_bytes(T, V, d, code, K, 0), H.device)
         _check(lib.nq_vocab_distill(
             _p(H), ldh, _p(W), ldw, code, T, V, d, _p(ids), ldi, _p(logq), ldq, K, float(scale),
-            int(bool(tail)), _p(a), _p(q.lse), _p(q.rest), _p(q.hit), _p(w), handle),
+            int(bool(tail)), _p(a), _p(q.lse), _p(q.rest), _p(q.hit), _p(q.logits), _p(w), handle),
             "nq_vocab_distill")
         return a, q
     return on.call(stream, run)
@@ -853,7 +863,7 @@ def vocab_distill_backward(H, W, ids, logq, state, dloss, scale=1.0, tail=True, 
     vocab_distill_work_bytes(T, V, d, H.dtype, K, grad=True) bytes."""
     torch = _torch()
     T, V, d, code, ldh, ldw, K, ldi, ldq = _distill_args(H, W, ids, logq)
-    _distill_state(state, T, K)
+    _distill_state(state, T, V, K)
     _vector(dloss, "dloss", T, torch.float32)
     lddh = lddw = d
     if dH is not None:
@@ -863,8 +873,8 @@ def vocab_distill_backward(H, W, ids, logq, state, dloss, scale=1.0, tail=True, 
     want_dH, want_dW = want_dH or dH is not None, want_dW or dW is not None
     if not (want_dH or want_dW):
         raise ValueError("neither dH nor dW is wanted")
-    on = _on_device("H W ids logq lse rest hit dloss dH dW work", H, W, ids, logq, state.lse,
-                    state.rest, state.hit, dloss, dH, dW, work)
+    on = _on_device("H W ids logq lse rest hit logits dloss dH dW work", H, W, ids, logq, state.lse,
+                    state.rest, state.hit, state.logits, dloss, dH, dW, work)
 
     def run(handle):
         gH, gW = dH, dW
@@ -880,8 +890,8 @@ def vocab_distill_backward(H, W, ids, logq, state, dloss, scale=1.0, tail=True, 
         w = _workspace(work, lib.nq_vocab_distill_work_bytes(T, V, d, code, K, 1), H.device)
         _check(lib.nq_vocab_distill_backward(
             _p(H), ldh, _p(W), ldw, code, T, V, d, _p(ids), ldi, _p(logq), ldq, K, float(scale),
-            int(bool(tail)), _p(state.lse), _p(state.rest), _p(state.hit), _p(dloss), _p(gH), lddh,
-            _p(gW), lddw, _p(w), handle), "nq_vocab_distill_backward")
+            int(bool(tail)), _p(state.lse), _p(state.rest), _p(state.hit), _p(state.logits), _p(dloss),
+            _p(gH), lddh, _p(gW), lddw, _p(w), handle), "nq_vocab_distill_backward")
         return gH, gW
     return on.call(stream, run)
 

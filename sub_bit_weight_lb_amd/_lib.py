@@ -93,9 +93,10 @@ SIGNATURES = {
                                P, P, P, P]),
     "nq_vocab_logprobs_work_bytes": (I64, [I64, I64, I64, I32, I64, I64]),
     "nq_vocab_distill": (ST, [P, I64, P, I64, I32, I64, I64, I64, P, I64, P, I64, I64, F32, I32, P,
-                              P, P, P, P, P]),
+                              P, P, P, P, P, P]),
+    "nq_vocab_distill_logits": (I64, [I64, I64, I64, I32]),
     "nq_vocab_distill_backward": (ST, [P, I64, P, I64, I32, I64, I64, I64, P, I64, P, I64, I64, F32,
-                                       I32, P, P, P, P, P, I64, P, I64, P, P]),
+                                       I32, P, P, P, P, P, P, I64, P, I64, P, P]),
     "nq_vocab_distill_work_bytes": (I64, [I64, I64, I64, I32, I64, I32]),
     "nq_op_precondition": (ST, [P, I64, I64, I64, P, P, P, I64, P]),
     "nq_op_gram": (ST, [P, I64, I64, I64, F32, P, I64, P]),

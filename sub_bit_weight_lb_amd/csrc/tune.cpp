@@ -271,21 +271,27 @@ int64_t nq_vocab_distill_work_bytes(int64_t T, int64_t V, int64_t d, int32_t dty
   return T == 0 ? 0 : distill_work_bytes(T, V, d, dtype, K, grad != 0);
 }
 
+int64_t nq_vocab_distill_logits(int64_t T, int64_t V, int64_t d, int32_t dtype) {
+  if (!head_ok(T, V, d, dtype)) return -1;
+  return T > 0 && vocab::keeps(T, V, d, dtype) ? T * round_up(V, 64) : 0;
+}
+
 nq_status nq_vocab_distill(const void* H, int64_t ldh, const void* W, int64_t ldw, int32_t dtype,
                            int64_t T, int64_t V, int64_t d, const int32_t* ids, int64_t ldi,
                            const float* logq, int64_t ldq, int64_t K, float scale, int32_t tail,
-                           float* loss, float* lse, float* rest, float* hit, void* work,
-                           void* stream) {
+                           float* loss, float* lse, float* rest, float* hit, float* logits,
+                           void* work, void* stream) {
   nq_status st = check_head(H, ldh, W, ldw, dtype, T, V, d, scale, work);
   if (st != NQ_OK || T == 0) return st;
   if ((st = check_listed(ids, ldi, logq, ldq, K)) != NQ_OK) return st;
   if (!loss || !lse || !rest || !hit) return bad("loss, lse, rest and hit are required");
   if (misaligned(loss, 4) || misaligned(lse, 4) || misaligned(rest, 4) || misaligned(hit, 4))
     return bad("an output is not aligned to its type");
+  if (misaligned(logits, 16)) return bad("logits must be 16-byte aligned");
   Distill a{};
   a.v = head(H, ldh, W, ldw, dtype, T, V, d, scale, work);
   a.ids = ids; a.logq = logq; a.K = K; a.ldi = ldi; a.ldq = ldq; a.tail = tail != 0;
-  a.loss = loss; a.lse = lse; a.rest = rest; a.hit = hit;
+  a.loss = loss; a.lse = lse; a.rest = rest; a.hit = hit; a.z = logits;
   NQ_HIPCHK(launch_vocab_distill(a, (hipStream_t)stream));
   return NQ_OK;
 }
@@ -294,9 +300,9 @@ nq_status nq_vocab_distill_backward(const void* H, int64_t ldh, const void* W, i
                                     int32_t dtype, int64_t T, int64_t V, int64_t d,
                                     const int32_t* ids, int64_t ldi, const float* logq, int64_t ldq,
                                     int64_t K, float scale, int32_t tail, const float* lse,
-                                    const float* rest, const float* hit, const float* dloss,
-                                    void* dH, int64_t lddh, void* dW, int64_t lddw, void* work,
-                                    void* stream) {
+                                    const float* rest, const float* hit, const float* logits,
+                                    const float* dloss, void* dH, int64_t lddh, void* dW,
+                                    int64_t lddw, void* work, void* stream) {
   if (T == 0 && dW && V >= 1 && d >= 1)
     return bad("T == 0: there is no gradient (dW is all zero)");
   nq_status st = check_head(H, ldh, W, ldw, dtype, T, V, d, scale, work);
@@ -309,11 +315,12 @@ nq_status nq_vocab_distill_backward(const void* H, int64_t ldh, const void* W, i
     return bad("dH or dW is not aligned to its type");
   if (misaligned(lse, 4) || misaligned(rest, 4) || misaligned(hit, 4) || misaligned(dloss, 4))
     return bad("lse, rest, hit or dloss is not aligned to its type");
+  if (misaligned(logits, 16)) return bad("logits must be 16-byte aligned");
   Distill a{};
   a.v = head(H, ldh, W, ldw, dtype, T, V, d, scale, work);
   a.v.dloss = dloss; a.v.dH = dH; a.v.lddh = lddh; a.v.dW = dW; a.v.lddw = lddw;
   a.ids = ids; a.logq = logq; a.K = K; a.ldi = ldi; a.ldq = ldq; a.tail = tail != 0;
-  a.lse = (float*)lse; a.rest = (float*)rest; a.hit = (float*)hit;
+  a.lse = (float*)lse; a.rest = (float*)rest; a.hit = (float*)hit; a.z = (float*)logits;
   NQ_HIPCHK(launch_vocab_distill_backward(a, (hipStream_t)stream));
   return NQ_OK;
 }

@@ -134,7 +134,16 @@ struct Distill {
   int64_t K, ldi, ldq;
   int tail;
   float *loss, *lse, *rest, *hit;    // T, T, T, T x K; but for loss read by the gradient
+  float* z;                          // T x (V to 64), nullable: logits that few tokens keep for it
 };
+// few tokens' gradient: v with labels, lse, share, ids, val as above; z, G (T rows of FewPlan's ldz),
+// part: FewPlan's
+struct Few {
+  Vocab v;
+  const float* z;
+  float *G, *part;
+};
+hipError_t launch_few_gradient(const Few& a, hipStream_t s);
 int64_t logprobs_work_bytes(int64_t T, int64_t V, int64_t d, int dtype, int64_t given, int64_t k);
 int64_t distill_work_bytes(int64_t T, int64_t V, int64_t d, int dtype, int64_t K, bool grad);
 hipError_t launch_vocab_logprobs(const Logprobs& a, hipStream_t s);

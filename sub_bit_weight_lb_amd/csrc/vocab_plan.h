@@ -205,5 +205,34 @@ inline KeepPlan keep_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t li
   return k;
 }
 
+// ---------------------------------------------------------------- few tokens' gradient (vocab_few.hip)
+struct FewPlan {
+  int64_t ldz;               // of a token's row of z and of G
+  int64_t columns;           // workgroups that share a slice of dH
+  int64_t blocks, slices;    // of dH: blocks of 16 words in a slice
+  int64_t G, z, part, bytes;
+};
+// Slices of dH: a round of workgroups of four waves, four per CU (three where a wave has 17 or more
+// tokens' sums of a 16-bit W, 33 of an fp32 one), with 64 words or more each.
+inline FewPlan few_plan(int64_t T, int64_t V, int64_t d, int dtype) {
+  FewPlan p{};
+  const int64_t all = (V + 15) / 16;
+  p.ldz = round_up(V, 64);
+  p.columns = (d * dtype_bytes(dtype) + 255) / 256;
+  const int64_t want = std::min(std::max<int64_t>(1, (T <= (dtype == kF32 ? 32 : 16) ? 1024 : 768) / p.columns), (all + 3) / 4);
+  p.blocks = round_up((all + want - 1) / want, 4);
+  p.slices = (all + p.blocks - 1) / p.blocks;
+  p.G = 0;
+  p.z = round_up(4 * T * p.ldz, 256);
+  p.part = 2 * p.z;
+  p.bytes = p.part + round_up(4 * p.slices * T * round_up(d, 4), 256);
+  return p;
+}
+// Whether the loss of few tokens keeps its logits for the gradient, which need not read W for them
+// once more.
+inline bool keeps(int64_t T, int64_t V, int64_t d, int dtype) {
+  return few(T, d, dtype) && T * round_up(V, 64) <= int64_t(1) << 24;
+}
+
 }  // namespace vocab
 }  // namespace nq

@@ -888,7 +888,7 @@ __global__ __launch_bounds__(1024 / NT)
             y += (st[2][i][t] + a * (1.0f + r)) * e;
           }
         }
-        o.stat[t * o.groups + blockIdx.x] = f32x4{m, s + ones, y, 0.0f};
+        if (o.stat) o.stat[t * o.groups + blockIdx.x] = f32x4{m, s + ones, y, 0.0f};
         if (o.tops)
           *(f32x4*)(o.tops + (t * o.groups + blockIdx.x) * 4) = f32x4{st[0][0][t], st[0][1][t], st[0][2][t], st[0][3][t]};
       } else {

@@ -693,6 +693,8 @@ hipError_t distill(const Distill& a, hipStream_t s) {
     r.hit = a.hit + t0 * a.K;
     if ((e = mark(w, k, r.ids, a.ldi, a.K, n, v.V, &r.kept, &r.places, s)) != hipSuccess) return e;
     if (k.few) {
+      r.kept.z = keeps(v.T, v.V, v.d, D) ? a.z : nullptr;
+      r.kept.ldz = round_up(v.V, 64);
       if ((e = score<D>(v, 0, v.V, r.kept, s)) != hipSuccess) return e;
     } else {
       const int64_t step = direct(v.W, v.ldw, v.d, D) ? v.V : k.p.piece;
@@ -705,13 +707,13 @@ hipError_t distill(const Distill& a, hipStream_t s) {
   return hipSuccess;
 }
 
-// What the gradient needs beside the loss's own workspace
+// What the gradient needs beside its products' workspace
 struct SharePlan {
   int64_t labels, share, wr, val, bytes;
 };
 SharePlan share_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t K) {
   SharePlan p;
-  p.labels = round_up(plan_for(T, V, d, dtype, true).bytes, 256);
+  p.labels = round_up(few(T, d, dtype) ? few_plan(T, V, d, dtype).bytes : plan_for(T, V, d, dtype, true).bytes, 256);
   p.share = p.labels + round_up(4 * T, 256);
   p.wr = p.share + round_up(4 * T, 256);
   p.val = p.wr + round_up(4 * T, 256);
@@ -756,7 +758,20 @@ hipError_t launch_vocab_distill_backward(const Distill& a, hipStream_t s) {
   v.ldi = a.ldi;
   v.listed = a.K;
   v.val = val;
-  return launch_vocab_loss_backward(v, s);
+  if (!few(v.T, v.d, v.dtype)) return launch_vocab_loss_backward(v, s);
+  const FewPlan f = few_plan(v.T, v.V, v.d, v.dtype);
+  Few g{v, keeps(v.T, v.V, v.d, v.dtype) ? a.z : nullptr, (float*)(w + f.G), (float*)(w + f.part)};
+  if (!g.z) {
+    Kept o{};
+    o.z = (float*)(w + f.z);
+    o.ldz = f.ldz;
+    const hipError_t e = v.dtype == kF32    ? score<kF32>(v, 0, v.V, o, s)
+                         : v.dtype == kBF16 ? score<kBF16>(v, 0, v.V, o, s)
+                                            : score<kF16>(v, 0, v.V, o, s);
+    if (e != hipSuccess) return e;
+    g.z = o.z;
+  }
+  return launch_few_gradient(g, s);
 }
 
 }  // namespace nq

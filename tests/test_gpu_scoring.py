@@ -551,6 +551,28 @@ def test_a_rest_that_is_next_to_nothing(gpu, T):
         L.check_grad(*L.grad(q))
 
 
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("T, V, d", [(1, 5000, 4100), (3, 70000, 64), (7, 333, 8), (16, 900, 1000), (19, 2100, 130),
+                                     (32, 4099, 515)])
+def test_gradient_of_few_tokens(gpu, name, T, V, d):
+    """With the loss's logits and without them; slices of the words, columns and words
+    past whole blocks, one output alone."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    print(f"case T={T} V={V} d={d} {name}", flush=True)
+    L = Taught(T + V, T, V, d, 17, name, gpu)
+    loss, q = L.loss()
+    assert q.logits.shape == (T, -(-V // 64) * 64)
+    L.check_loss(loss, q)
+    dH, dW = L.grad(q)
+    L.check_grad(dH, dW)
+    bare = nq.VocabDistill(q.lse, q.rest, q.hit)
+    l2, _ = L.loss(state=bare)
+    assert torch.equal(loss, l2)
+    assert all(torch.equal(a, b) for a, b in zip((dH, dW), L.grad(bare)))
+    assert torch.equal(L.grad(q, want_dW=False)[0], dH) and torch.equal(L.grad(q, want_dH=False)[1], dW)
+
+
 def test_several_pieces_of_the_vocabulary(gpu):
     """A hidden size so large that W is copied and taken in pieces: against float64 on
     the GPU."""

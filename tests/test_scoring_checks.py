@@ -95,6 +95,7 @@ def test_distill_refuses(no_library, change):
 @pytest.mark.parametrize("change", [
     dict(state=None), dict(state=state(lse=torch.zeros(4))), dict(state=state(hit=torch.zeros((3, 5)))),
     dict(state=state(rest=torch.zeros(3, dtype=torch.float64))), dict(dloss=torch.zeros(2)),
+    dict(state=state(logits=torch.zeros((3, 50)))), dict(state=state(logits=torch.zeros(193)[1:])),
     dict(dloss=torch.zeros(3, dtype=torch.bfloat16)), dict(dH=torch.zeros((3, 21))),
     dict(dW=torch.zeros((50, 20), dtype=torch.float16)), dict(want_dH=False, want_dW=False),
 ])
@@ -134,15 +135,15 @@ def logprobs(lib, **k):
 
 def distill(lib, **k):
     a = dict(H=PTR, ldh=20, W=PTR, ldw=20, dtype=0, T=3, V=50, d=20, ids=PTR, ldi=4, logq=PTR, ldq=4,
-             K=4, scale=1.0, tail=1, loss=PTR, lse=PTR, rest=PTR, hit=PTR, work=PTR)
+             K=4, scale=1.0, tail=1, loss=PTR, lse=PTR, rest=PTR, hit=PTR, logits=None, work=PTR)
     a.update(k)
     return lib.nq_vocab_distill(*a.values(), None)
 
 
 def backward(lib, **k):
     a = dict(H=PTR, ldh=20, W=PTR, ldw=20, dtype=0, T=3, V=50, d=20, ids=PTR, ldi=4, logq=PTR, ldq=4,
-             K=4, scale=1.0, tail=1, lse=PTR, rest=PTR, hit=PTR, dloss=PTR, dH=PTR, lddh=20, dW=PTR,
-             lddw=20, work=PTR)
+             K=4, scale=1.0, tail=1, lse=PTR, rest=PTR, hit=PTR, logits=None, dloss=PTR, dH=PTR,
+             lddh=20, dW=PTR, lddw=20, work=PTR)
     a.update(k)
     return lib.nq_vocab_distill_backward(*a.values(), None)
 
@@ -171,7 +172,8 @@ def test_logprobs_status(lib, bad):
 @pytest.mark.parametrize("call", [distill, backward])
 @pytest.mark.parametrize("bad", [dict(ids=None), dict(logq=None), dict(K=0), dict(K=129, ldi=129, ldq=129),
                                  dict(ldi=3), dict(ldq=3), dict(ldi=BIG), dict(ids=ODD), dict(logq=ODD),
-                                 dict(rest=None), dict(hit=None), dict(hit=ODD)])
+                                 dict(rest=None), dict(hit=None), dict(hit=ODD),
+                                 dict(logits=C.c_void_p(4104))])
 def test_distill_status(lib, call, bad):
     assert call(lib, **bad) == L.NQ_ERR_INVALID_ARG
 
@@ -199,6 +201,11 @@ def test_workspaces(lib):
         assert f(300, 5000, 515, dt, 4, 20) > 0 and g(300, 5000, 515, dt, 20, 0) > 0
         # the loss's own gradient is a part of it
         assert g(300, 5000, 515, dt, 20, 1) > lib.nq_vocab_loss_work_bytes(300, 5000, 515, dt, 1)
+    # logits that few tokens keep
+    h = lib.nq_vocab_distill_logits
+    assert h(3, 50, 20, 0) == 3 * 64 and h(64, 1000, 8, 0) == 64 * 1024 and h(32, 1000, 8, 1) == 32 * 1024
+    assert h(65, 1000, 8, 0) == h(33, 1000, 8, 2) == h(3, 1000, 7, 0) == h(0, 5, 8, 0) == h(32, 1 << 20, 8, 1) == 0
+    assert h(1, 0, 8, 0) == h(1, 5, 8, 3) == -1
     # of any number of tokens and words: three kinds of 2^27 values, beside the operands' copies
     for T, V in ((1 << 20, 1 << 18), (1 << 14, 1 << 24), (8192, 131072)):
         own = f(T, V, 64, 1, 128, 128)
