@@ -156,6 +156,7 @@ struct KeepPlan {
   int64_t first, step;        // words of the first step and of the largest (0: no best words)
   bool marked;                // listed words have marks (else their z is found in the row of kept logits)
   int64_t lds, ldz;           // bytes of a token's slots, its row of kept logits
+  int64_t zs, ws;             // fp32: factors of tokens and of a piece's words
   int64_t stat, tops, slot, marks, places, zl, z, best, thr, bytes;
 };
 // rows: few tokens' logits are kept whole (log probabilities).
@@ -190,6 +191,10 @@ inline KeepPlan keep_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t li
     off += round_up(bytes, 256);
     return at;
   };
+  if (dtype == kF32 && !k.few) {
+    k.zs = take(4 * T);
+    k.ws = take(4 * k.p.piece);
+  }
   k.stat = take(16 * k.block * k.groups);
   if (top) k.tops = take(4 * 4 * k.block * k.groups);
   k.z = take(4 * k.block * k.ldz);

@@ -78,7 +78,7 @@ struct Kept {
   float* z;                 // [token][ldz], nullable: z of the call's words,
   int64_t ldz;
   const float* thr;         // of parts with one above the token's thr (nullable: all)
-  int flip;                 // kPick: z's factor is below zero
+  int flip;                 // kPick, 16-bit: z's factor is below zero
 };
 // The place of listed word `in` of a group
 __device__ __forceinline__ uint32_t place_of(u32x4 words, uint32_t place, int in) {
@@ -107,8 +107,9 @@ struct Mma {
   Opnd A, B;                // C (M x N), M = A.rows, N = B.rows
   int64_t K;                // a multiple of 64
   int64_t k_slice;          // k per slice (grid y), a multiple of 64
-  const float* zs;          // kStat, kGrad: the factor of the products (fp32: of each token;
+  const float* zs;          // kStat, kGrad, kPick: the factor of the products (fp32: of each token;
   float z0;                 // 16-bit: z0)
+  const float* ws;          // kPick, fp32: and of each word (to the next multiple of 256)
   // kStat, kGrad: rows are words v0 .., columns tokens
   int64_t v0;
   const int32_t* labels;
@@ -449,7 +450,17 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
     // (0 times infinity, too).
     const Kept& o = a.kept;
     const int64_t group = a.v0 / (16 * MI) + tm * WM + wm;
-    if (o.flip) {
+    if constexpr (D == kF32) {   // (factors of words differ: z itself)
+      float zs[NI];
+#pragma unroll
+      for (int j = 0; j < NI; ++j) zs[j] = c0 + 16 * j < N ? a.zs[c0 + 16 * j] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const f32x4 ws = *(const f32x4*)(a.ws + r0 + 16 * i);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) acc[i][j] *= ws * zs[j];
+      }
+    } else if (o.flip) {
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -471,7 +482,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
     for (int j = 0; j < NI; ++j) {
       const int64_t t = c0 + 16 * j;
       const bool used = t < N && group < o.groups;
-      zsj[j] = fabsf(D == kF32 ? (used ? a.zs[t] : 0.0f) : a.z0);
+      zsj[j] = D == kF32 ? 1.0f : fabsf(a.z0);
       thrj[j] = used && o.thr ? o.thr[t] : kNegInf;
       slotj[j] = used && o.slot ? o.slot[t * o.lds + group] : 255;
     }
@@ -1135,6 +1146,72 @@ __global__ __launch_bounds__(256) void pack_kernel(const typename Elem<D>::type*
   }
 }
 
+// The two terms of each row of fp32 X (rows x k), scaled by a power of two of its own to 2^15 at
+// their largest, zero from k to kp: out [row][term][kp]; unscale[row] = mul over the power, 0 from
+// the last row to unscale[full]. A workgroup per row, which it reads twice where it is long.
+__global__ __launch_bounds__(256) void rowpack_kernel(const float* __restrict__ X, int64_t rows, int64_t k,
+                                                      int64_t ld, float mul, uint16_t* __restrict__ out,
+                                                      int64_t kp, float* __restrict__ unscale, int64_t full) {
+  __shared__ float sm[4];
+  if (blockIdx.x == 0)
+    for (int64_t i = rows + threadIdx.x; i < full; i += 256) unscale[i] = 0.0f;
+  struct __attribute__((packed)) Eight { float v[8]; };
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const float* x = X + r * ld;
+    float m = 0.0f;
+    auto load = [&](int64_t c, float (&e)[8]) {
+      if (c + 8 <= k) {
+        Eight q;
+        __builtin_memcpy(&q, x + c, 32);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = q.v[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = c + i < k ? x[c + i] : 0.0f;
+      }
+    };
+    float first[8];
+    for (int64_t c = 8 * threadIdx.x; c < kp; c += 2048) {
+      float e[8];
+      load(c, e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float v = fabsf(e[i]);
+        m = v < __builtin_inff() ? fmaxf(m, v) : m;
+        if (c < 2048) first[i] = e[i];
+      }
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    __syncthreads();   // (sm of the row before has been read)
+    if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+    const int p = power_for(m);
+    if (threadIdx.x == 0) unscale[r] = ldexpf(mul, -p);
+    const float f = ldexpf(1.0f, p);
+    for (int64_t c = 8 * threadIdx.x; c < kp; c += 2048) {
+      float e[8];
+      if (c < 2048) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = first[i];
+      } else {
+        load(c, e);
+      }
+      uint16_t q[8][2];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) split<kF32>(e[i] * f, q[i]);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = (uint32_t)q[2 * i][n] | (uint32_t)q[2 * i + 1][n] << 16;
+        *(u32x4*)(out + (r * 2 + n) * kp + c) = w;
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------- plan
 // Whether X's rows can be copied as they are: 16-bit, 16-byte aligned.
 bool direct(const void* X, int64_t ld, int64_t k, int dtype) {
@@ -1162,6 +1239,12 @@ hipError_t mma_launch(const Mma& a, int tile, int slices, hipStream_t s) {
   return hipGetLastError();
 }
 
+inline hipError_t rowpack(const void* X, int64_t rows, int64_t k, int64_t ld, float mul, uint16_t* out, int64_t kp,
+                          float* unscale, int64_t full, hipStream_t s) {
+  hipLaunchKernelGGL(rowpack_kernel, dim3((unsigned)std::min<int64_t>(rows, 65536)), dim3(256), 0, s, (const float*)X,
+                     rows, k, ld, mul, out, kp, unscale, full);
+  return hipGetLastError();
+}
 template <int D, int M>
 hipError_t pack(const void* X, int64_t rows, int64_t k, int64_t ld, const int32_t* labels,
                 const float* mul, uint16_t* out, int64_t rp, int64_t kp, int forms, bool twice,

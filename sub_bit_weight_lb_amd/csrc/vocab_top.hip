@@ -572,6 +572,19 @@ __global__ __launch_bounds__(256) void shares_kernel(const int32_t* __restrict__
 }
 
 // ---------------------------------------------------------------- launches
+// H as the products take it
+template <int D>
+hipError_t tokens(const Vocab& a, const KeepPlan& k, Opnd* H, hipStream_t s) {
+  Opnd unused;
+  if constexpr (D != kF32) {
+    return begin<D>(a, k.p, nullptr, H, &unused, s);
+  } else {
+    char* w = (char*)a.work;
+    uint16_t* out = (uint16_t*)(w + k.p.hp);
+    *H = Opnd{out, 2 * k.p.dp, k.p.dp, a.T, k.p.dp};
+    return rowpack(a.H, a.T, a.d, a.ldh, a.scale, out, k.p.dp, (float*)(w + k.zs), a.T, s);
+  }
+}
 // The logits of tokens t0 .. t0 + n of the words v0 .. v0 + nv, as `kept` says
 template <int D>
 hipError_t pick(const Vocab& a, const KeepPlan& k, const Opnd& H, int64_t t0, int64_t n, int64_t v0,
@@ -581,12 +594,22 @@ hipError_t pick(const Vocab& a, const KeepPlan& k, const Opnd& H, int64_t t0, in
   m.B.p += t0 * H.ld;
   m.B.rows = n;
   m.K = m.k_slice = k.p.dp;
-  m.zs = rows_of((char*)a.work, k.p, a.T).zs + t0;
+  char* w = (char*)a.work;
+  m.zs = (float*)(w + k.zs) + t0;
+  m.ws = (float*)(w + k.ws);
   m.z0 = a.scale;
   m.v0 = v0;
   m.kept = kept;
   hipError_t e;
-  if ((e = words<D>(a, k.p, v0, nv, &m.A, s)) != hipSuccess) return e;
+  if constexpr (D != kF32) {
+    e = words<D>(a, k.p, v0, nv, &m.A, s);
+  } else {   // (every word to the top of the terms' range by itself: no pass over W for its largest)
+    uint16_t* out = (uint16_t*)(w + k.p.wp);
+    m.A = Opnd{out, 2 * k.p.dp, k.p.dp, nv, k.p.dp};
+    e = rowpack((const float*)a.W + v0 * a.ldw, nv, a.d, a.ldw, 1.0f, out, k.p.dp, (float*)(w + k.ws),
+                round_up(nv, 256), s);
+  }
+  if (e != hipSuccess) return e;
   return mma_launch<D, kPick>(m, k.tile, 1, s);
 }
 
@@ -627,8 +650,8 @@ hipError_t logprobs(const Logprobs& a, hipStream_t s) {
   t.thr = (float*)(w + k.thr);
   t.ldt = a.ldt;
   t.given = (int)a.given;
-  Opnd H{}, unused;
-  if (!k.few && (e = begin<D>(v, k.p, nullptr, &H, &unused, s)) != hipSuccess) return e;
+  Opnd H{};
+  if (!k.few && (e = tokens<D>(v, k, &H, s)) != hipSuccess) return e;
   for (int64_t t0 = 0; t0 < v.T; t0 += k.block) {
     const int64_t n = std::min(k.block, v.T - t0);
     t.tokens = a.tokens ? a.tokens + t0 * a.ldt : nullptr;
@@ -681,8 +704,8 @@ hipError_t distill(const Distill& a, hipStream_t s) {
   r.ldq = a.ldq;
   r.K = (int)a.K;
   r.tail = a.tail;
-  Opnd H{}, unused;
-  if (!k.few && (e = begin<D>(v, k.p, nullptr, &H, &unused, s)) != hipSuccess) return e;
+  Opnd H{};
+  if (!k.few && (e = tokens<D>(v, k, &H, s)) != hipSuccess) return e;
   for (int64_t t0 = 0; t0 < v.T; t0 += k.block) {
     const int64_t n = std::min(k.block, v.T - t0);
     r.ids = a.ids + t0 * a.ldi;

@@ -7,7 +7,7 @@ import pytest
 from test_tuning_plans import compile_plan, log_uniform
 
 
-FIELDS = ("few tile group groups block first step marked lds ldz own stat tops z slot marks places zl best thr "
+FIELDS = ("few tile group groups block first step marked lds ldz own piece zs ws stat tops z slot marks places zl best thr "
           "bytes").split()
 
 
@@ -15,7 +15,8 @@ FIELDS = ("few tile group groups block first step marked lds ldz own stat tops z
 def keep_plan(tmp_path_factory):
     ask = compile_plan(tmp_path_factory.mktemp("keep"), "vocab_plan.h", """
     const vocab::KeepPlan k = vocab::keep_plan(x[0], x[1], x[2], (int)x[3], x[4], x[5], x[6] != 0);
-    out = {k.few, k.tile, k.group, k.groups, k.block, k.first, k.step, k.marked, k.lds, k.ldz, k.p.bytes, k.stat,
+    out = {k.few, k.tile, k.group, k.groups, k.block, k.first, k.step, k.marked, k.lds, k.ldz, k.p.bytes, k.p.piece, k.zs,
+           k.ws, k.stat,
            k.tops, k.z, k.slot, k.marks, k.places, k.zl, k.best, k.thr, k.bytes};""")
     return lambda rows: [dict(zip(FIELDS, got)) for got in ask(rows)]
 
@@ -45,6 +46,9 @@ def test_everything_kept_has_its_place(keep_plan):
             assert k["first"] >= min(whole, 2 * top * group)
         # what is kept, in order and without overlaps
         need = [("own", None)]
+        if t == 0 and not few:
+            need += [("zs", 4 * T), ("ws", 4 * k["piece"])]
+            assert k["piece"] % 256 == 0
         need.append(("stat", 16 * block * k["groups"]))
         if top:
             need.append(("tops", 16 * block * k["groups"]))
