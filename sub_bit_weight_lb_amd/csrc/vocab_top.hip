@@ -164,6 +164,10 @@ __device__ __forceinline__ uint64_t key_of(float z, uint32_t word) {
   return (uint64_t)order_of(z) << 32 | (uint32_t)~word;
 }
 
+// how many lanes of `who` come before this one
+__device__ __forceinline__ int rank_in(uint64_t who) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+}
 // The largest c of the form that bits 31 .. low can write with k of the N values of each lane at
 // or above c (0: with none); *n: how many those are. Stops where they are k.
 template <int N>
@@ -206,6 +210,17 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
   const int64_t t = blockIdx.x;
   const f32x4* stat = a.kept.stat + t * a.kept.groups;
   const int k = a.k;
+  int n = 0;   // words in the list
+  // what the outputs need, on its way while the best words are found
+  f32x4 mine = {kNegInf, -1.0f, 0.0f, 0.0f};
+  if (a.last && tid < a.kept.groups) mine = stat[tid];
+  int32_t id = -1;
+  float zid = kNaN;
+  if (a.last && tid < a.given) {
+    id = a.tokens[t * a.ldt + tid];
+    if (id >= 0 && id < a.V)
+      zid = a.places ? a.kept.zl[t * a.given + a.places[t * a.given + tid]] : a.kept.z[t * a.kept.ldz + id];
+  }
   if (k) {
     // parts of the token, four at a time (a step's first is a multiple of 4; past its last:
     // -infinity, which is nobody's largest unless nothing is finite)
@@ -251,7 +266,7 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
       if (a.have) bound = max(bound, (uint64_t)order_of(a.thr[t]) << 32 | 0xffffffffu);
     }
     const float* z = a.kept.z + t * a.kept.ldz;
-    int n = a.have ? k : 0;
+    n = a.have ? k : 0;
     // cuts the list to its k best; afterwards lim is what they reach
     auto cut = [&]() {
       if (wave == 0) {
@@ -281,7 +296,7 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
         for (int i = 0; i < kEach; ++i) {
           const bool in = 64 * i + lane < n && (hi[i] > c || (hi[i] == c && lo[i] >= d));
           const uint64_t who = __ballot(in);
-          if (in) list[at + __popcll(who & ((uint64_t(1) << lane) - 1))] = (uint64_t)hi[i] << 32 | lo[i];
+          if (in) list[at + rank_in(who)] = (uint64_t)hi[i] << 32 | lo[i];
           at += __popcll(who);
         }
         if (lane == 0) {
@@ -296,29 +311,36 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
     };
     // words above the bound of the parts todo[b .. end); whether all had room
     auto collect = [&](int b, int end) {
-      // a wave reads 64 / part of them at once, four times before the first use
+      // a wave reads 64 / part of them at once, eight times before the first use
+      constexpr int Q = 8;
       const int each = 64 / part, first = wave * each + lane / part, in = lane % part;
-      for (int i = b; i < end; i += 4 * NW * each) {
-        float x[4];
-        uint32_t w[4];
-        bool on[4];
+      for (int i = b; i < end; i += Q * NW * each) {
+        float x[Q];
+        uint32_t w[Q];
+        bool on[Q];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < Q; ++q) {
           const int e = i + q * NW * each + first;
           w[q] = (uint32_t)(todo[min(e, end - 1)] * part + in);
           on[q] = e < end && w[q] < a.V;
           x[q] = on[q] ? z[w[q] - a.v0] : 0.0f;
         }
+        uint64_t who[Q];
+        int some = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint64_t key = key_of(x[q], w[q]);
-          const bool up = on[q] && key > bound;
-          const uint64_t who = __ballot(up);
-          if (!who) continue;
-          int at = 0;
-          if (lane == 0) at = atomicAdd(&count, __popcll(who));
-          at = __shfl(at, 0) + __popcll(who & ((uint64_t(1) << lane) - 1));
-          if (up && at < kCap) list[at] = key;
+        for (int q = 0; q < Q; ++q) {
+          who[q] = __ballot(on[q] && key_of(x[q], w[q]) > bound);
+          some += __popcll(who[q]);
+        }
+        if (!some) continue;
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&count, some);
+        at = __builtin_amdgcn_readfirstlane(at);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const int place = at + rank_in(who[q]);
+          if (who[q] >> lane & 1 && place < kCap) list[place] = key_of(x[q], w[q]);
+          at += __popcll(who[q]);
         }
       }
       __syncthreads();
@@ -354,15 +376,16 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
         }
       }
     }
-    cut();
+    // (a short list is put in order as it is)
+    if (!a.last || n > NT) cut();
     if (!a.last) {
       for (int i = tid; i < k; i += NT) a.best[t * k + i] = i < n ? list[i] : 0;
       if (tid == 0) a.thr[t] = value_of(lim);
       return;
     }
   }
-  Sums r = kNothing;
-  for (int64_t g = tid; g < a.kept.groups; g += NT) {
+  Sums r{mine[0], mine[1], mine[2]};
+  for (int64_t g = tid + NT; g < a.kept.groups; g += NT) {
     const f32x4 x = stat[g];
     join(r, Sums{x[0], x[1], x[2]});
   }
@@ -373,30 +396,22 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
     a.lse[t] = r.m + log_s;
     a.entropy[t] = log_s - r.u / (1.0f + r.r);
   }
-  for (int i = tid; i < k; i += NT) {
-    int place = i;
-    if (fine) {
-      const uint64_t key = list[i];
-      place = 0;
+  if (!fine) {
+    for (int i = tid; i < k; i += NT) {
+      a.top_ids[t * k + i] = -1;
+      a.top_logprobs[t * k + i] = kNaN;
+    }
+  } else if (tid < n) {   // (n <= NT; k of them are at least as good as the others)
+    const uint64_t key = list[tid];
+    int place = 0;
 #pragma unroll 8
-      for (int j = 0; j < k; ++j) place += list[j] > key;
+    for (int j = 0; j < n; ++j) place += list[j] > key;
+    if (place < k) {
       a.top_ids[t * k + place] = (int32_t)~(uint32_t)key;
       a.top_logprobs[t * k + place] = value_of((uint32_t)(key >> 32)) - r.m - log_s;
-    } else {
-      a.top_ids[t * k + place] = -1;
-      a.top_logprobs[t * k + place] = kNaN;
     }
   }
-  for (int i = tid; i < a.given; i += NT) {
-    const int32_t id = a.tokens[t * a.ldt + i];
-    float x = id < 0 ? 0.0f : kNaN;
-    if (id >= 0 && id < a.V) {
-      const Kept& o = a.kept;
-      const float z = a.places ? o.zl[t * a.given + a.places[t * a.given + i]] : o.z[t * o.ldz + id];
-      x = z - r.m - log_s;
-    }
-    a.logprobs[t * a.given + i] = x;
-  }
+  if (tid < a.given) a.logprobs[t * a.given + tid] = id < 0 ? 0.0f : zid - r.m - log_s;
 }
 
 // ---------------------------------------------------------------- divergence
