@@ -528,9 +528,11 @@ nq_status nq_vocab_distill(const void* H, int64_t ldh, const void* W, int64_t ld
                            float* loss, float* lse, float* rest, float* hit, float* logits,
                            void* work, void* stream);
 
-/* Number of float32 in `logits` of the call above, which the gradient of few tokens can take to
- * read W once less: nq_vocab_distill_logits(T, V, d, dtype) device floats, 16-byte aligned, or
- * NULL (0 floats, of more tokens: ignored). Host only; -1 for sizes out of range. */
+/* Number of float32 in `logits` of the call above, which the gradient can take to compute them
+ * only once: T rows of V to the next multiple of 128, 16-byte aligned (what lies behind V is
+ * written too), or NULL for none. 0 where they are not kept (a hidden size so small that they cost
+ * more than they save, or more than 2^30 of them: a pointer given is ignored). Host only; -1 for
+ * sizes out of range. */
 int64_t nq_vocab_distill_logits(int64_t T, int64_t V, int64_t d, int32_t dtype);
 
 /* Gradient of sum_t dloss_t loss_t from the lse, rest and hit of nq_vocab_distill on the

@@ -772,9 +772,9 @@ def vocab_logprobs(H, W, tokens=None, k=0, scale=1.0, out=None, work=None, strea
 @dataclass
 class VocabDistill:
     """What vocab_distill hands to its gradient for T tokens with K entries each: lse
-    and rest (T) and hit (T x K), float32; of few tokens also their logits (T x V to
-    the next multiple of 64), which save the gradient a pass over W (None: they are
-    computed again)."""
+    and rest (T) and hit (T x K), float32; and, where it pays (up to 4 GiB), the
+    logits (T x V to the next multiple of 128), which the gradient then need not
+    compute again. They can be left out (None)."""
     lse: "object"
     rest: "object"
     hit: "object"
@@ -806,12 +806,12 @@ def _distill_state(q, T, V, K):
     _vector(q.rest, "rest", T, f32)
     _vector(q.hit, "hit", T * K, f32)
     if q.logits is not None:
-        _vector(q.logits, "logits", T * -(-V // 64) * 64, f32)
+        _vector(q.logits, "logits", T * -(-V // 128) * 128, f32)
         if q.logits.data_ptr() % 16:
             raise ValueError("logits must be 16-byte aligned")
 
 
-def vocab_distill(H, W, ids, logq, scale=1.0, tail=True, loss=None, state=None, work=None,
+def vocab_distill(H, W, ids, logq, scale=1.0, tail=True, keep=True, loss=None, state=None, work=None,
                   stream=None):
     """KL divergence of softmax(z), z = scale H W^T never kept, from a teacher's K <=
     128 words per token: ids (T x K int32; a negative one is no entry, a token without
@@ -820,8 +820,8 @@ def vocab_distill(H, W, ids, logq, scale=1.0, tail=True, loss=None, state=None, 
     temperature). tail: the rest of the teacher's mass, 1 - sum exp logq, is one
     outcome more, "another word"; without it logq is normalised over a token's
     entries (and may be logits). Returns (loss, state): T float32, 0 for an ignored
-    token, and the VocabDistill that vocab_distill_backward takes; both can be given
-    to be filled. A word >= V gives NaN; one listed twice counts with both entries.
+    token, and the VocabDistill that vocab_distill_backward takes (keep: with the
+    logits, where it pays); both can be given to be filled. A word >= V gives NaN; one listed twice counts with both entries.
     work, if given, holds vocab_distill_work_bytes(T, V, d, H.dtype, K) bytes."""
     torch = _torch()
     f32 = torch.float32
@@ -842,7 +842,7 @@ def vocab_distill(H, W, ids, logq, scale=1.0, tail=True, loss=None, state=None, 
         lib = _lib.load()
         q = state
         if q is None:
-            kept = lib.nq_vocab_distill_logits(T, V, d, code)
+            kept = lib.nq_vocab_distill_logits(T, V, d, code) if keep else 0
             q = VocabDistill(new(T), new(T), new(T, K), new(T, kept // T) if kept > 0 else None)
         w = _workspace(work, lib.nq_vocab_distill_work_bytes(T, V, d, code, K, 0), H.device)
         _check(lib.nq_vocab_distill(

@@ -273,7 +273,7 @@ int64_t nq_vocab_distill_work_bytes(int64_t T, int64_t V, int64_t d, int32_t dty
 
 int64_t nq_vocab_distill_logits(int64_t T, int64_t V, int64_t d, int32_t dtype) {
   if (!head_ok(T, V, d, dtype)) return -1;
-  return T > 0 && vocab::keeps(T, V, d, dtype) ? T * round_up(V, 64) : 0;
+  return T > 0 && vocab::keeps(T, V, d, dtype) ? T * vocab::row_of(V) : 0;
 }
 
 nq_status nq_vocab_distill(const void* H, int64_t ldh, const void* W, int64_t ldw, int32_t dtype,

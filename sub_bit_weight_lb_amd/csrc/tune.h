@@ -113,6 +113,8 @@ struct Vocab {
   const int32_t* ids;
   int64_t listed, ldi;
   const float* val;                  // T x listed
+  const float* z;                    // nullable: the logits, ldz apart
+  int64_t ldz;
 };
 int64_t vocab_work_bytes(int64_t T, int64_t V, int64_t d, int dtype, bool grad);
 hipError_t launch_vocab_loss(const Vocab& a, hipStream_t s);
@@ -134,7 +136,7 @@ struct Distill {
   int64_t K, ldi, ldq;
   int tail;
   float *loss, *lse, *rest, *hit;    // T, T, T, T x K; but for loss read by the gradient
-  float* z;                          // T x (V to 64), nullable: logits that few tokens keep for it
+  float* z;                          // T x (V to 128), nullable: logits that are kept for it
 };
 // few tokens' gradient: v with labels, lse, share, ids, val as above; z, G (T rows of FewPlan's ldz),
 // part: FewPlan's

@@ -119,6 +119,55 @@ __global__ __launch_bounds__(256) void dh_kernel(const float* __restrict__ part,
   }
 }
 
+// G of 2048 words of a token per workgroup from kept logits (z: of the piece's words): what kGrad
+// makes of them, and val at the words that the token lists; zero to the next multiple of 64 words
+// and for tokens past T.
+template <int D>
+__global__ __launch_bounds__(256) void kept_kernel(const float* __restrict__ z, int64_t ldz, int64_t T,
+                                                   int64_t v0, int64_t nv, const int32_t* __restrict__ ids,
+                                                   int64_t ldi, int K, const float* __restrict__ val,
+                                                   const int32_t* __restrict__ labels,
+                                                   const float* __restrict__ lse,
+                                                   const float* __restrict__ wr,
+                                                   const float* __restrict__ wn, uint16_t* __restrict__ G,
+                                                   int64_t gld) {
+  constexpr int N = terms(D);
+  const int64_t t = blockIdx.x, w0 = (int64_t)blockIdx.y * 2048, w = w0 + 8 * threadIdx.x;
+  const bool used = t < T && labels[t] >= 0;
+  uint16_t* row = G + t * N * gld;
+  if (w < (nv + 63) / 64 * 64) {
+    uint16_t q[8][N];
+    const float ref = used ? lse[t] : 0.0f, s = used ? wr[t] : 0.0f;
+    f32x4 x[2] = {};
+    if (used) {   // (rows hold whole groups of 128 words)
+      x[0] = *(const f32x4*)(z + t * ldz + w);
+      x[1] = *(const f32x4*)(z + t * ldz + w + 4);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = x[i / 4][i % 4] - ref;
+      split<D>(used && w + i < nv ? (D == kF32 ? expf(y) : __expf(y)) * s : 0.0f, q[i]);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      u32x4 o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = (uint32_t)q[2 * i][n] | (uint32_t)q[2 * i + 1][n] << 16;
+      *(u32x4*)(row + n * gld + w) = o;
+    }
+  }
+  if (t >= T) return;
+  __syncthreads();
+  for (int k = threadIdx.x; k < K; k += 256) {
+    const int64_t id = ids[t * ldi + k], at = id - v0;
+    if (id < 0 || at < w0 || at >= w0 + 2048 || at >= nv) continue;
+    uint16_t q[N];
+    split<D>(val[t * K + k] * wn[t], q);
+#pragma unroll
+    for (int n = 0; n < N; ++n) row[n * gld + at] = q[n];
+  }
+}
+
 // G of the words that a token lists, in its N terms: val, before dloss, in place of what the
 // products' epilogue left there (a word listed twice has the same val twice).
 template <int D, int N>
@@ -197,7 +246,12 @@ hipError_t backward(const Vocab& a, hipStream_t s) {
   for (int64_t v0 = 0; v0 < a.V; v0 += p.piece) {
     const int64_t nv = std::min(p.piece, a.V - v0), nvp = round_up(nv, 256);
     if ((e = words<D>(a, p, v0, nv, &W, s)) != hipSuccess) return e;
-    if (score_g) {
+    if (a.z) {
+      const dim3 grid((unsigned)round_up(a.T, BK), (unsigned)((nv + 2047) / 2048));
+      hipLaunchKernelGGL(kept_kernel<D>, grid, dim3(256), 0, s, a.z + v0, a.ldz, a.T, v0, nv, a.ids, a.ldi,
+                         (int)a.listed, a.val, a.labels, a.lse, wn, rows.wn, G, p.piece);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    } else if (score_g) {
       const ScoreGrad o{a.lse, wn, G, p.piece, v0};
       if ((e = score<D>(a, v0, nv, o, s)) != hipSuccess) return e;
     } else {
@@ -210,7 +264,7 @@ hipError_t backward(const Vocab& a, hipStream_t s) {
       m.G = G; m.gld = p.piece;
       if ((e = mma_launch<D, kGrad>(m, tile_for(nv, a.T), 1, s)) != hipSuccess) return e;
     }
-    if (a.listed) {
+    if (a.listed && !a.z) {
       const dim3 grid((unsigned)((a.T * a.listed + 255) / 256));
       auto* put = listed_kernel<D, terms(D)>;
       if constexpr (D != kF32) put = rt == 1 ? put : listed_kernel<D, kFewTerms>;

@@ -211,6 +211,8 @@ inline KeepPlan keep_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t li
 }
 
 // ---------------------------------------------------------------- few tokens' gradient (vocab_few.hip)
+// Words of a token's row of logits that are kept for a gradient: whole groups
+inline int64_t row_of(int64_t V) { return round_up(V, 128); }
 struct FewPlan {
   int64_t ldz;               // of a token's row of z and of G
   int64_t columns;           // workgroups that share a slice of dH
@@ -222,7 +224,7 @@ struct FewPlan {
 inline FewPlan few_plan(int64_t T, int64_t V, int64_t d, int dtype) {
   FewPlan p{};
   const int64_t all = (V + 15) / 16;
-  p.ldz = round_up(V, 64);
+  p.ldz = row_of(V);
   p.columns = (d * dtype_bytes(dtype) + 255) / 256;
   const int64_t want = std::min(std::max<int64_t>(1, (T <= (dtype == kF32 ? 32 : 16) ? 1024 : 768) / p.columns), (all + 3) / 4);
   p.blocks = round_up((all + want - 1) / want, 4);
@@ -233,10 +235,16 @@ inline FewPlan few_plan(int64_t T, int64_t V, int64_t d, int dtype) {
   p.bytes = p.part + round_up(4 * p.slices * T * round_up(d, 4), 256);
   return p;
 }
-// Whether the loss of few tokens keeps its logits for the gradient, which need not read W for them
-// once more.
+// Whether a divergence keeps its logits for the gradient, which need not compute them once more: 4
+// GiB of them at most, and where the hidden size is so large that computing costs more than a store
+// and a load (loss and gradient in us, kept and not: 4096 tokens, 131072 words of bf16, d = 4096
+// 11634 and 14254, 1024 4137 and 4245, 512 3092 and 2724; logits that stay in the last-level cache,
+// 1024 tokens, 32000 words, d = 1024 323 and 328, 512 220 and 223, 128 164 and 157; fp32, 4096
+// tokens, 32000 words, d = 512 1652 and 1845, 256 1198 and 1239).
 inline bool keeps(int64_t T, int64_t V, int64_t d, int dtype) {
-  return few(T, d, dtype) && T * round_up(V, 64) <= int64_t(1) << 24;
+  const int64_t n = T * row_of(V);
+  const bool pays = d >= (n <= int64_t(1) << 25 || dtype == kF32 ? 256 : 1024);
+  return (few(T, d, dtype) || pays) && n <= int64_t(1) << 30;
 }
 
 }  // namespace vocab

@@ -594,7 +594,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
         float* p = o.z + t * o.ldz + (tm * WM + wm) * (16 * MI);
 #pragma unroll
         for (int q = 0; q < PARTS; ++q)
-          if (!(tops[q] * zs <= thr)) {
+          if (!o.thr || !(tops[q] * zs <= thr)) {
 #pragma unroll
             for (int i = q * PI; i < (q + 1) * PI; ++i) put(p, i);
           }
@@ -1279,7 +1279,8 @@ hipError_t begin(const Vocab& a, const Plan& p, const float* dloss, Opnd* Hz, Op
                        a.T, a.V, a.scale, rows, fac);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  const bool dw = dloss && a.dW, score = dloss && few(a.T, a.d, D);
+  // (score: z comes from score_kernel, or has been kept)
+  const bool dw = dloss && a.dW, score = dloss && (few(a.T, a.d, D) || a.z);
   // (bf16 has one copy for both)
   const bool z = !score && (!direct(a.H, a.ldh, a.d, D) || (D == kBF16 && dw));
   // (for dW's products with two rows of G per token)

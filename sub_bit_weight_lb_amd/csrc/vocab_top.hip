@@ -730,14 +730,17 @@ hipError_t distill(const Distill& a, hipStream_t s) {
     r.rest = a.rest + t0;
     r.hit = a.hit + t0 * a.K;
     if ((e = mark(w, k, r.ids, a.ldi, a.K, n, v.V, &r.kept, &r.places, s)) != hipSuccess) return e;
+    float* z = a.z && keeps(v.T, v.V, v.d, D) ? a.z + t0 * row_of(v.V) : nullptr;
+    r.kept.z = z;
+    r.kept.ldz = row_of(v.V);
     if (k.few) {
-      r.kept.z = keeps(v.T, v.V, v.d, D) ? a.z : nullptr;
-      r.kept.ldz = round_up(v.V, 64);
       if ((e = score<D>(v, 0, v.V, r.kept, s)) != hipSuccess) return e;
     } else {
       const int64_t step = direct(v.W, v.ldw, v.d, D) ? v.V : k.p.piece;
-      for (int64_t v0 = 0; v0 < v.V; v0 += step)
+      for (int64_t v0 = 0; v0 < v.V; v0 += step) {
+        r.kept.z = z ? z + v0 : nullptr;
         if ((e = pick<D>(v, k, H, t0, n, v0, std::min(step, v.V - v0), r.kept, s)) != hipSuccess) return e;
+      }
     }
     hipLaunchKernelGGL(distill_kernel<256>, dim3((unsigned)n), dim3(256), 0, s, r);
     if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -796,9 +799,14 @@ hipError_t launch_vocab_distill_backward(const Distill& a, hipStream_t s) {
   v.ldi = a.ldi;
   v.listed = a.K;
   v.val = val;
-  if (!few(v.T, v.d, v.dtype)) return launch_vocab_loss_backward(v, s);
+  const float* z = keeps(v.T, v.V, v.d, v.dtype) ? a.z : nullptr;
+  if (!few(v.T, v.d, v.dtype)) {
+    v.z = z;
+    v.ldz = row_of(v.V);
+    return launch_vocab_loss_backward(v, s);
+  }
   const FewPlan f = few_plan(v.T, v.V, v.d, v.dtype);
-  Few g{v, keeps(v.T, v.V, v.d, v.dtype) ? a.z : nullptr, (float*)(w + f.G), (float*)(w + f.part)};
+  Few g{v, z, (float*)(w + f.G), (float*)(w + f.part)};
   if (!g.z) {
     Kept o{};
     o.z = (float*)(w + f.z);

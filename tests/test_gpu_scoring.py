@@ -420,6 +420,29 @@ def test_divergence_in_tiles_of_every_size(gpu, name, T, V, d, K):
 
 
 @pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("T, V, d, K", [(70, 4100, 800, 100), (300, 2049, 1100, 33), (513, 300, 900, 128),
+                                        (65, 40, 768, 64), (129, 70000, 770, 5)])
+def test_gradient_with_and_without_the_logits(gpu, name, T, V, d, K):
+    """Logits that the loss kept, and computed again: the same bits of z, so gradients
+    that differ by the rounding of its exponential alone."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    print(f"case T={T} V={V} d={d} K={K} {name}", flush=True)
+    L = Taught(T + V, T, V, d, K, name, gpu)
+    loss, q = L.loss()
+    assert q.logits.shape == (T, -(-V // 128) * 128)
+    L.check_loss(loss, q)
+    L.exact()
+    less(np.abs(H64(q.logits)[L.used, :V] - L.z[L.used]), (L.ez + 2 * U * np.abs(L.z).max(1))[L.used, None])
+    dH, dW = L.grad(q)
+    L.check_grad(dH, dW)
+    l2, bare = L.loss(keep=False)
+    assert bare.logits is None and torch.equal(loss, l2)
+    assert all(torch.equal(getattr(q, f), getattr(bare, f)) for f in ("lse", "rest", "hit"))
+    L.check_grad(*L.grad(bare))
+
+
+@pytest.mark.parametrize("name", TYPES)
 @pytest.mark.parametrize("T", [9, 40, 140])
 def test_divergence_of_views(gpu, name, T):
     import torch
@@ -562,7 +585,7 @@ def test_gradient_of_few_tokens(gpu, name, T, V, d):
     print(f"case T={T} V={V} d={d} {name}", flush=True)
     L = Taught(T + V, T, V, d, 17, name, gpu)
     loss, q = L.loss()
-    assert q.logits.shape == (T, -(-V // 64) * 64)
+    assert q.logits.shape == (T, -(-V // 128) * 128)
     L.check_loss(loss, q)
     dH, dW = L.grad(q)
     L.check_grad(dH, dW)

@@ -95,7 +95,7 @@ def test_distill_refuses(no_library, change):
 @pytest.mark.parametrize("change", [
     dict(state=None), dict(state=state(lse=torch.zeros(4))), dict(state=state(hit=torch.zeros((3, 5)))),
     dict(state=state(rest=torch.zeros(3, dtype=torch.float64))), dict(dloss=torch.zeros(2)),
-    dict(state=state(logits=torch.zeros((3, 50)))), dict(state=state(logits=torch.zeros(193)[1:])),
+    dict(state=state(logits=torch.zeros((3, 50)))), dict(state=state(logits=torch.zeros(385)[1:])),
     dict(dloss=torch.zeros(3, dtype=torch.bfloat16)), dict(dH=torch.zeros((3, 21))),
     dict(dW=torch.zeros((50, 20), dtype=torch.float16)), dict(want_dH=False, want_dW=False),
 ])
@@ -201,10 +201,12 @@ def test_workspaces(lib):
         assert f(300, 5000, 515, dt, 4, 20) > 0 and g(300, 5000, 515, dt, 20, 0) > 0
         # the loss's own gradient is a part of it
         assert g(300, 5000, 515, dt, 20, 1) > lib.nq_vocab_loss_work_bytes(300, 5000, 515, dt, 1)
-    # logits that few tokens keep
+    # logits that are kept
     h = lib.nq_vocab_distill_logits
-    assert h(3, 50, 20, 0) == 3 * 64 and h(64, 1000, 8, 0) == 64 * 1024 and h(32, 1000, 8, 1) == 32 * 1024
-    assert h(65, 1000, 8, 0) == h(33, 1000, 8, 2) == h(3, 1000, 7, 0) == h(0, 5, 8, 0) == h(32, 1 << 20, 8, 1) == 0
+    assert h(3, 50, 20, 0) == 3 * 128 and h(64, 1000, 8, 0) == 64 * 1024 and h(32, 1000, 8, 1) == 32 * 1024
+    assert h(8192, 131072, 4096, 1) == 1 << 30 and h(8193, 131072, 4096, 1) == 0
+    assert h(4096, 131072, 1000, 1) == 0 and h(4096, 131072, 1000, 0) == 1 << 29
+    assert h(65, 1000, 8, 0) == h(33, 1000, 8, 2) == h(3, 1000, 7, 0) == h(0, 5, 8, 0) == 0
     assert h(1, 0, 8, 0) == h(1, 5, 8, 3) == -1
     # of any number of tokens and words: three kinds of 2^27 values, beside the operands' copies
     for T, V in ((1 << 20, 1 << 18), (1 << 14, 1 << 24), (8192, 131072)):
