@@ -109,6 +109,7 @@ __global__ __launch_bounds__(256) void dh_kernel(const float* __restrict__ part,
     const bool used = labels[t] >= 0;
     const float f = pt[t];
     f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
     for (int z = 0; z < nz; ++z)
 #pragma unroll
       for (int p = 0; p < RT; ++p)
@@ -120,9 +121,9 @@ __global__ __launch_bounds__(256) void dh_kernel(const float* __restrict__ part,
 }
 
 // G of 2048 words of a token per workgroup from kept logits (z: of the piece's words): what kGrad
-// makes of them, and val at the words that the token lists; zero to the next multiple of 64 words
-// and for tokens past T.
-template <int D>
+// makes of them, in N terms, and val at the words that the token lists; zero to the next multiple
+// of 64 words and for tokens past T.
+template <int D, int N>
 __global__ __launch_bounds__(256) void kept_kernel(const float* __restrict__ z, int64_t ldz, int64_t T,
                                                    int64_t v0, int64_t nv, const int32_t* __restrict__ ids,
                                                    int64_t ldi, int K, const float* __restrict__ val,
@@ -131,7 +132,6 @@ __global__ __launch_bounds__(256) void kept_kernel(const float* __restrict__ z, 
                                                    const float* __restrict__ wr,
                                                    const float* __restrict__ wn, uint16_t* __restrict__ G,
                                                    int64_t gld) {
-  constexpr int N = terms(D);
   const int64_t t = blockIdx.x, w0 = (int64_t)blockIdx.y * 2048, w = w0 + 8 * threadIdx.x;
   const bool used = t < T && labels[t] >= 0;
   uint16_t* row = G + t * N * gld;
@@ -200,7 +200,7 @@ hipError_t loss(const Vocab& a, hipStream_t s) {
   } else {
     Mma m{};
     Opnd unused;
-    if ((e = begin<D>(a, p, nullptr, &m.B, &unused, s)) != hipSuccess) return e;
+    if ((e = begin<D>(a, p, nullptr, 1, &m.B, &unused, s)) != hipSuccess) return e;
     m.K = m.k_slice = p.dp;
     m.zs = rows_of(w, p, a.T).zs;
     m.z0 = a.scale;
@@ -225,13 +225,13 @@ hipError_t loss(const Vocab& a, hipStream_t s) {
 template <int D>
 hipError_t backward(const Vocab& a, hipStream_t s) {
   typedef typename Elem<D>::type E;
-  const Plan p = plan_for(a.T, a.V, a.d, D, true);
+  const Plan p = grad_plan(a.T, a.V, a.d, D, a.z);
   char* w = (char*)a.work;
   Factors* fac = (Factors*)(w + p.fac);
   uint16_t* G = (uint16_t*)(w + p.G);
   // rows of G, and so of dH's sums, as the products see them: the terms of 16-bit G
   // are rows of their own
-  const int rt = g_rows(a.T, a.d, D);
+  const int rt = a.z ? kept_rows(a.T, a.V, a.d, D) : g_rows(a.T, a.d, D);
   const int64_t RT = rt * a.T, gld = p.piece * terms(D);
   const int64_t ldp = round_up(a.d, 4), slice = RT * ldp;
   const bool score_g = few(a.T, a.d, D);
@@ -239,7 +239,7 @@ hipError_t backward(const Vocab& a, hipStream_t s) {
   const Rows rows = rows_of(w, p, a.T);
   const float* wn = a.share ? a.wr : rows.wn;
   Opnd Hz, Hw, W;
-  if ((e = begin<D>(a, p, a.dloss, &Hz, &Hw, s)) != hipSuccess) return e;
+  if ((e = begin<D>(a, p, a.dloss, rt, &Hz, &Hw, s)) != hipSuccess) return e;
   // every piece uses the same slices of its words for dH; the first writes them
   // all, the last, where it is another, may leave some as they are: those are not
   // launched
@@ -247,8 +247,10 @@ hipError_t backward(const Vocab& a, hipStream_t s) {
     const int64_t nv = std::min(p.piece, a.V - v0), nvp = round_up(nv, 256);
     if ((e = words<D>(a, p, v0, nv, &W, s)) != hipSuccess) return e;
     if (a.z) {
-      const dim3 grid((unsigned)round_up(a.T, BK), (unsigned)((nv + 2047) / 2048));
-      hipLaunchKernelGGL(kept_kernel<D>, grid, dim3(256), 0, s, a.z + v0, a.ldz, a.T, v0, nv, a.ids, a.ldi,
+      const dim3 grid((unsigned)(round_up(RT, BK) / rt), (unsigned)((nv + 2047) / 2048));
+      auto* fill = kept_kernel<D, terms(D)>;
+      if constexpr (D != kF32) fill = rt == 1 ? fill : kept_kernel<D, kFewTerms>;
+      hipLaunchKernelGGL(fill, grid, dim3(256), 0, s, a.z + v0, a.ldz, a.T, v0, nv, a.ids, a.ldi,
                          (int)a.listed, a.val, a.labels, a.lse, wn, rows.wn, G, p.piece);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     } else if (score_g) {

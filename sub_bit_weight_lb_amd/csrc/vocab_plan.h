@@ -45,8 +45,15 @@ inline int g_rows(int64_t T, int64_t d, int dtype) {
   return dtype != kF32 && few(T, d, dtype) ? kFewTerms : 1;
 }
 
+// From kept logits: of up to 128 tokens, whose rows of G still fit one tile of dH, where W is what
+// takes the time; and where the products are short. (One term's error of dH and dW, over that of
+// rounding the exact ones: up to 1.7 with 33 to 65 tokens, 1.56 with 200; with more it nears 2^0.5.)
+inline int kept_rows(int64_t T, int64_t V, int64_t d, int dtype) {
+  return dtype != kF32 && (T <= 128 || (double)T * V * d <= 4294967296.0) ? kFewTerms : 1;
+}
+
 struct Plan {
-  int64_t dp, tp;              // d to 64, T to 256 (few tokens: to 64)
+  int64_t dp, tp;              // d to 64, rows of G to 256 (few tokens: T to 64)
   int64_t piece, npieces;      // words of a piece, to 256; pieces
   int nz;                      // slices of dH, each with a share of the first piece
   int64_t kz;                  // words per slice, to 64
@@ -88,12 +95,13 @@ inline int dh_slices(int64_t T, int64_t d, int64_t piece) {
 // Words per piece: G, and a copy of W's piece where one is needed, hold at most
 // 2^26 values each (two thousand words at least), which leaves the fp32 sums of
 // dH, read and written once per piece, a few percent of the piece's products.
-// (kept: the operands of a product whose results have their place in a KeepPlan.)
-inline Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad, bool kept = false) {
+// (kept: the operands of a product whose results have their place in a KeepPlan; rows: of G per
+// token.)
+inline Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad, bool kept, int rows) {
   Plan p{};
   const int nt = terms(dtype);
   p.dp = round_up(d, BK);
-  p.tp = round_up(T, few(T, d, dtype) ? BK : 256);
+  p.tp = few(T, d, dtype) ? round_up(T, BK) : round_up(rows * T, 256);
   const int64_t most = std::max<int64_t>(2048, (int64_t(1) << 26) / std::max(p.tp, p.dp) / 256 * 256);
   p.npieces = (V + most - 1) / most;
   p.piece = round_up((V + p.npieces - 1) / p.npieces, 256);
@@ -130,10 +138,14 @@ inline Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad, bool
     p.nz = (int)((words + p.kz - 1) / p.kz);
     // (few tokens: their two rows each are 64 at most)
     p.G = take(2 * nt * p.tp * p.piece);
-    p.part = take(4 * p.nz * T * g_rows(T, d, dtype) * round_up(d, 4));
+    p.part = take(4 * p.nz * T * rows * round_up(d, 4));
   }
   p.bytes = off;
   return p;
+}
+
+inline Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad) {
+  return plan_for(T, V, d, dtype, grad, false, g_rows(T, d, dtype));
 }
 
 // ---------------------------------------------------------------- single logits (vocab_top.hip)
@@ -164,7 +176,7 @@ inline KeepPlan keep_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t li
                           bool rows) {
   KeepPlan k{};
   k.few = few(T, d, dtype);
-  if (!k.few) k.p = plan_for(T, V, d, dtype, false, true);
+  if (!k.few) k.p = plan_for(T, V, d, dtype, false, true, 1);
   k.tile = k.few ? 128 : tile_for(V, T);
   k.group = k.tile / 2;
   k.groups = (V + k.group - 1) / k.group;
@@ -240,11 +252,16 @@ inline FewPlan few_plan(int64_t T, int64_t V, int64_t d, int dtype) {
 // and a load (loss and gradient in us, kept and not: 4096 tokens, 131072 words of bf16, d = 4096
 // 11634 and 14254, 1024 4137 and 4245, 512 3092 and 2724; logits that stay in the last-level cache,
 // 1024 tokens, 32000 words, d = 1024 323 and 328, 512 220 and 223, 128 164 and 157; fp32, 4096
-// tokens, 32000 words, d = 512 1652 and 1845, 256 1198 and 1239).
+// tokens, 32000 words, d = 512 1652 and 1845, 256 1198 and 1239), or G has two terms.
 inline bool keeps(int64_t T, int64_t V, int64_t d, int dtype) {
   const int64_t n = T * row_of(V);
   const bool pays = d >= (n <= int64_t(1) << 25 || dtype == kF32 ? 256 : 1024);
-  return (few(T, d, dtype) || pays) && n <= int64_t(1) << 30;
+  return (few(T, d, dtype) || kept_rows(T, V, d, dtype) > 1 || pays) && n <= int64_t(1) << 30;
+}
+
+// Of a gradient from kept logits, or without.
+inline Plan grad_plan(int64_t T, int64_t V, int64_t d, int dtype, bool z) {
+  return plan_for(T, V, d, dtype, true, false, z ? kept_rows(T, V, d, dtype) : g_rows(T, d, dtype));
 }
 
 }  // namespace vocab

@@ -1259,9 +1259,9 @@ hipError_t pack(const void* X, int64_t rows, int64_t k, int64_t ld, const int32_
 // The factors of a call, and H twice: for z, in place where it can be (an ignored
 // token's column of products is not used), and with dloss for dW, whose sums over
 // the tokens need the rows of ignored ones zeroed and, but for bf16, each token's
-// weight in them. Copies that no product of the call reads are not made.
+// weight in them. Copies that no product of the call reads are not made. rt: rows of G per token.
 template <int D>
-hipError_t begin(const Vocab& a, const Plan& p, const float* dloss, Opnd* Hz, Opnd* Hw,
+hipError_t begin(const Vocab& a, const Plan& p, const float* dloss, int rt, Opnd* Hz, Opnd* Hw,
                  hipStream_t s) {
   char* w = (char*)a.work;
   Factors* fac = (Factors*)(w + p.fac);
@@ -1284,7 +1284,7 @@ hipError_t begin(const Vocab& a, const Plan& p, const float* dloss, Opnd* Hz, Op
   // (bf16 has one copy for both)
   const bool z = !score && (!direct(a.H, a.ldh, a.d, D) || (D == kBF16 && dw));
   // (for dW's products with two rows of G per token)
-  const bool twice = score && g_rows(a.T, a.d, D) == 2;
+  const bool twice = score && rt == 2;
   uint16_t* out = (uint16_t*)(w + p.hp);
   const int64_t copy = p.tp * p.dp * terms(D);
   *Hz = z ? Opnd{out, p.dp * terms(D), p.dp, a.T, p.dp}

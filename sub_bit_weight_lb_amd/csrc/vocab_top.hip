@@ -592,7 +592,7 @@ template <int D>
 hipError_t tokens(const Vocab& a, const KeepPlan& k, Opnd* H, hipStream_t s) {
   Opnd unused;
   if constexpr (D != kF32) {
-    return begin<D>(a, k.p, nullptr, H, &unused, s);
+    return begin<D>(a, k.p, nullptr, 1, H, &unused, s);
   } else {
     char* w = (char*)a.work;
     uint16_t* out = (uint16_t*)(w + k.p.hp);
@@ -754,7 +754,9 @@ struct SharePlan {
 };
 SharePlan share_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t K) {
   SharePlan p;
-  p.labels = round_up(few(T, d, dtype) ? few_plan(T, V, d, dtype).bytes : plan_for(T, V, d, dtype, true).bytes, 256);
+  p.labels = few(T, d, dtype) ? few_plan(T, V, d, dtype).bytes
+                              : grad_plan(T, V, d, dtype, keeps(T, V, d, dtype)).bytes;
+  p.labels = round_up(p.labels, 256);
   p.share = p.labels + round_up(4 * T, 256);
   p.wr = p.share + round_up(4 * T, 256);
   p.val = p.wr + round_up(4 * T, 256);

@@ -206,7 +206,8 @@ def test_workspaces(lib):
     assert h(3, 50, 20, 0) == 3 * 128 and h(64, 1000, 8, 0) == 64 * 1024 and h(32, 1000, 8, 1) == 32 * 1024
     assert h(8192, 131072, 4096, 1) == 1 << 30 and h(8193, 131072, 4096, 1) == 0
     assert h(4096, 131072, 1000, 1) == 0 and h(4096, 131072, 1000, 0) == 1 << 29
-    assert h(65, 1000, 8, 0) == h(33, 1000, 8, 2) == h(3, 1000, 7, 0) == h(0, 5, 8, 0) == 0
+    assert h(128, 1000, 8, 2) == 128 * 1024 and h(3, 1000, 7, 1) == 3 * 1024
+    assert h(65, 1000, 8, 0) == h(8192, 131072, 8, 2) == h(3, 1000, 7, 0) == h(0, 5, 8, 0) == 0
     assert h(1, 0, 8, 0) == h(1, 5, 8, 3) == -1
     # of any number of tokens and words: three kinds of 2^27 values, beside the operands' copies
     for T, V in ((1 << 20, 1 << 18), (1 << 14, 1 << 24), (8192, 131072)):
