@@ -149,6 +149,8 @@ inline Plan plan_for(int64_t T, int64_t V, int64_t d, int dtype, bool grad) {
 }
 
 // ---------------------------------------------------------------- single logits (vocab_top.hip)
+// Words of a token's row of logits that are kept for a gradient: whole groups
+inline int64_t row_of(int64_t V) { return round_up(V, 128); }
 constexpr int64_t kMaxListed = 128;   // words that a token can list, and its best words
 constexpr int64_t kKeep = int64_t(1) << 27;   // values of one kind that are kept at most
 
@@ -171,9 +173,7 @@ struct KeepPlan {
   int64_t zs, ws;             // fp32: factors of tokens and of a piece's words
   int64_t stat, tops, slot, marks, places, zl, z, best, thr, bytes;
 };
-// rows: few tokens' logits are kept whole (log probabilities).
-inline KeepPlan keep_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t listed, int64_t top,
-                          bool rows) {
+inline KeepPlan keep_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t listed, int64_t top) {
   KeepPlan k{};
   k.few = few(T, d, dtype);
   if (!k.few) k.p = plan_for(T, V, d, dtype, false, true, 1);
@@ -188,9 +188,9 @@ inline KeepPlan keep_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t li
     if (top) most = std::min(most, kKeep / first);
     k.block = std::min(T, std::max<int64_t>(256, most / 256 * 256));
   }
-  k.marked = listed && !(k.few && rows);
+  k.marked = listed && !k.few;
   if (k.few) {
-    k.ldz = rows ? round_up(V, 64) : 0;
+    k.ldz = row_of(V);
   } else if (top) {
     k.step = std::min(all, std::max(first, kKeep / k.block / 256 * 256));
     k.first = k.block * all <= kWhole ? all : first;
@@ -223,8 +223,6 @@ inline KeepPlan keep_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t li
 }
 
 // ---------------------------------------------------------------- few tokens' gradient (vocab_few.hip)
-// Words of a token's row of logits that are kept for a gradient: whole groups
-inline int64_t row_of(int64_t V) { return round_up(V, 128); }
 struct FewPlan {
   int64_t ldz;               // of a token's row of z and of G
   int64_t columns;           // workgroups that share a slice of dH

@@ -820,34 +820,15 @@ __global__ __launch_bounds__(1024 / NT)
                   (uint32_t)q[2][p] | (uint32_t)q[3][p] << 16};
     } else {
       float m = kNegInf, x[4];
-      [[maybe_unused]] bool on[4];
-      if constexpr (PICK) {
-        const int slot = t < T && o.slot ? o.slot[t * o.lds + blockIdx.x] : 255;
-        u32x4 words = {0, 0, 0, 0};
-        uint32_t place = 0;
-        if (slot != 255) {
-          words = o.marks[t * o.listed + slot].words;
-          place = o.marks[t * o.listed + slot].place;
-        }
-        const uint32_t half = wave & 2 ? words[1] : words[0];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int in = 16 * wave + 4 * g + v;
-          const bool mine = half >> (in & 31) & 1u;
-          x[v] = scale * z[v];
-          on[v] = w + v < V && !(mine && o.without);
-          if (on[v]) m = fmaxf(m, x[v]);
-          if (mine) o.zl[t * o.listed + place_of(words, place, in)] = x[v];
-        }
-        if (t < T && o.z) *(f32x4*)(o.z + t * o.ldz + w) = f32x4{x[0], x[1], x[2], x[3]};
-      } else {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          x[v] = scale * z[v];
-          if (w + v < V) m = fmaxf(m, x[v]);
+      for (int v = 0; v < 4; ++v) {
+        x[v] = scale * z[v];
+        if (w + v < V) m = fmaxf(m, x[v]);
+        if constexpr (!PICK)
           if (w + v < V && w + v == label) o.hit[t] = x[v];
-        }
       }
+      if constexpr (PICK)
+        if (t < T) *(f32x4*)(o.z + t * o.ldz + w) = f32x4{x[0], x[1], x[2], x[3]};
       m = fmaxf(m, __shfl_xor(m, 16));
       m = fmaxf(m, __shfl_xor(m, 32));
       float s = 0.0f;
@@ -856,9 +837,10 @@ __global__ __launch_bounds__(1024 / NT)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const float a = x[v] - m, e = __expf(a);
-          ones += on[v] && a == 0.0f ? 1.0f : 0.0f;
-          s += !on[v] || a == 0.0f ? 0.0f : x[v] == kNegInf ? __uint_as_float(0x7fc00000u) : e;
-          y += on[v] ? e * a : 0.0f;
+          const bool on = w + v < V;
+          ones += on && a == 0.0f ? 1.0f : 0.0f;
+          s += !on || a == 0.0f ? 0.0f : x[v] == kNegInf ? __uint_as_float(0x7fc00000u) : e;
+          y += on ? e * a : 0.0f;
         }
         ones += __shfl_xor(ones, 16);
         ones += __shfl_xor(ones, 32);
@@ -893,7 +875,7 @@ __global__ __launch_bounds__(1024 / NT)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float a = st[0][i][t] - m, e = __expf(a), r = st[1][i][t] + st[3][i][t];
-          if (r != -1.0f) {   // (-1: no word, a sum of 0)
+          if (v0 + 16 * i < V) {
             ones += a == 0.0f ? 1.0f : 0.0f;
             s += a == 0.0f ? r : e * (1.0f + r);
             y += (st[2][i][t] + a * (1.0f + r)) * e;

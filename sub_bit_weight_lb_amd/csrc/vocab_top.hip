@@ -417,6 +417,7 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
 // ---------------------------------------------------------------- divergence
 struct Near {
   Kept kept;
+  int64_t V;
   const int32_t* ids;
   const float* logq;
   int64_t ldi, ldq;
@@ -466,53 +467,22 @@ __device__ __forceinline__ Teacher teacher(const float (&l)[2], const bool (&on)
   return t;
 }
 
-// loss, lse, rest and hit of a token from its groups' sums (with a tail: without the listed
-// words) and the z of its listed words. A workgroup of NT threads per token.
-template <int NT>
-__global__ __launch_bounds__(NT) void distill_kernel(Near a) {
-  __shared__ float sm[3 * (NT / 64)];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int64_t t = blockIdx.x;
-  const Kept& o = a.kept;
-  const f32x4* stat = o.stat + t * o.groups;
-  const float* zl = o.zl + t * a.K;
-  // entries lane and lane + 64 of the token
-  float z[2], l[2], x[2];
-  bool on[2];
-  int place[2];
+// loss, lse, rest and hit of token t, by one wave: r joins the groups' sums (with a tail: without the
+// listed words); of entries lane and lane + 64 on: whether they are one, z (NaN for a word past the
+// last); the distinct listed words' z are those x that are `part`.
+__device__ __forceinline__ void finish(const Near& a, int64_t t, int lane, Sums r, const bool (&on)[2],
+                                       const float (&z)[2], const float (&x)[2], const bool (&part)[2]) {
+  float l[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int k = lane + 64 * i;
-    const int32_t id = k < a.K ? a.ids[t * a.ldi + k] : -1;
-    on[i] = id >= 0;
-    place[i] = on[i] ? a.places[t * a.K + k] : 255;
-    l[i] = on[i] ? a.logq[t * a.ldq + k] : 0.0f;
-    z[i] = !on[i] ? 0.0f : place[i] == 255 ? kNaN : zl[place[i]];
-  }
-  Sums r = kNothing;
-  for (int64_t g = tid; g < o.groups; g += NT) {
-    const f32x4 q = stat[g];
-    join(r, Sums{q[0], q[1], 0.0f});
-  }
-  r = join_all<NT>(r, sm);
-  if (tid >= 64) return;
+  for (int i = 0; i < 2; ++i) l[i] = on[i] ? a.logq[t * a.ldq + lane + 64 * i] : 0.0f;
   const bool used = __ballot(on[0] || on[1]) != 0;
   const Teacher q = teacher(l, on, a.tail);
   double m = r.m, s = 1.0 + (double)r.r;
   const bool all = r.r == -1.0f;   // every word is listed
   if (a.tail) {
-    // the part of the listed words, which have the places 0 .. n - 1
-    int n = max(place[0] == 255 ? 0 : place[0] + 1, place[1] == 255 ? 0 : place[1] + 1);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) n = max(n, __shfl_xor(n, o));
-#pragma unroll
-    for (int i = 0; i < 2; ++i) x[i] = lane + 64 * i < n ? zl[lane + 64 * i] : kNegInf;
-    m = wave_max(fmax((double)x[0], (double)x[1]));
+    m = wave_max(fmax(part[0] ? (double)x[0] : -INFINITY, part[1] ? (double)x[1] : -INFINITY));
     m = fmax(m, (double)r.m);
-    double e = 0.0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) e += lane + 64 * i < n ? exp((double)x[i] - m) : 0.0;
-    s = wave_sum(e);
+    s = wave_sum((part[0] ? exp((double)x[0] - m) : 0.0) + (part[1] ? exp((double)x[1] - m) : 0.0));
     if (!all) s += (1.0 + (double)r.r) * exp((double)r.m - m);
   }
   const double log_s = log(s);
@@ -531,6 +501,127 @@ __global__ __launch_bounds__(NT) void distill_kernel(Near a) {
     a.lse[t] = used ? (float)(m + log_s) : 0.0f;
     a.rest[t] = used ? (float)rest : 0.0f;
   }
+}
+
+// A workgroup of NT threads per token.
+template <int NT>
+__global__ __launch_bounds__(NT) void distill_kernel(Near a) {
+  __shared__ float sm[3 * (NT / 64)];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int64_t t = blockIdx.x;
+  const Kept& o = a.kept;
+  const f32x4* stat = o.stat + t * o.groups;
+  const float* zl = o.zl + t * a.K;
+  float z[2], x[2];
+  bool on[2], part[2];
+  int place[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = lane + 64 * i;
+    on[i] = k < a.K && a.ids[t * a.ldi + k] >= 0;
+    place[i] = on[i] ? a.places[t * a.K + k] : 255;
+    z[i] = !on[i] ? 0.0f : place[i] == 255 ? kNaN : zl[place[i]];
+  }
+  Sums r = kNothing;
+  for (int64_t g = tid; g < o.groups; g += NT) {
+    const f32x4 q = stat[g];
+    join(r, Sums{q[0], q[1], 0.0f});
+  }
+  r = join_all<NT>(r, sm);
+  if (tid >= 64) return;
+  // the listed words have the places 0 .. n - 1
+  int n = max(place[0] == 255 ? 0 : place[0] + 1, place[1] == 255 ? 0 : place[1] + 1);
+#pragma unroll
+  for (int i = 32; i > 0; i >>= 1) n = max(n, __shfl_xor(n, i));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    part[i] = lane + 64 * i < n;
+    x[i] = part[i] && a.tail ? zl[lane + 64 * i] : 0.0f;
+  }
+  finish(a, t, lane, r, on, z, x, part);
+}
+
+// The same of few tokens, whose logits are all there (without marks: a launch less). With a tail,
+// groups of 64 words with a listed one are summed again, from those logits.
+template <int NT>
+__global__ __launch_bounds__(NT) void distill_few_kernel(Near a) {
+  typedef int i32x4 __attribute__((ext_vector_type(4)));
+  constexpr int NW = NT / 64;
+  __shared__ __align__(16) int word[kList];
+  __shared__ int owner[kList];          // the first entry of the same group; -1: none
+  __shared__ bool again[kList];         // an earlier entry has the same word
+  __shared__ uint32_t out[kList][2];    // of the owner's group: the words that are listed
+  __shared__ float sm[3 * NW];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t t = blockIdx.x;
+  const Kept& o = a.kept;
+  f32x4* stat = o.stat + t * o.groups;
+  const float* row = o.z + t * o.ldz;
+  float z[2], x[2];
+  bool on[2], part[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = lane + 64 * i;
+    const int32_t id = k < a.K ? a.ids[t * a.ldi + k] : -1;
+    on[i] = id >= 0;
+    z[i] = !on[i] ? 0.0f : id < a.V ? row[id] : kNaN;
+    if (wave == 0) {
+      word[k] = id < a.V ? id : -1;
+      out[k][0] = out[k][1] = 0;
+    }
+  }
+  __syncthreads();
+  if (a.tail && tid < kList) {
+    const int id = word[tid], g = id >> 6;   // (-1 of none: no group's)
+    int own = tid;
+    bool twice = false;
+#pragma unroll 4
+    for (int j = 0; j < a.K; j += 4) {
+      const i32x4 w = *(const i32x4*)(word + j);
+#pragma unroll
+      for (int u = 3; u >= 0; --u) {
+        own = (w[u] >> 6) == g && j + u < own ? j + u : own;
+        twice |= w[u] == id && j + u < tid;
+      }
+    }
+    owner[tid] = id >= 0 ? own : -1;
+    again[tid] = twice;
+    if (id >= 0) {
+      atomicOr(&out[own][id >> 5 & 1], 1u << (id & 31));
+      if (own == tid) stat[g] = f32x4{kNegInf, -1.0f, 0.0f, 0.0f};
+    }
+  }
+  __syncthreads();
+  Sums r = kNothing;
+  for (int64_t g = tid; g < o.groups; g += NT) {
+    const f32x4 q = stat[g];
+    join(r, Sums{q[0], q[1], 0.0f});
+  }
+  if (a.tail) {
+    // four groups of a wave at a time, all their loads before the first use
+    for (int k0 = wave; k0 < a.K; k0 += 4 * NW) {
+      float y[4];
+      bool in[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int k = min(k0 + q * NW, a.K - 1);
+        const int64_t w = (int64_t)(word[k] >> 6) * 64 + lane;
+        in[q] = k0 + q * NW < a.K && owner[k] == k && w < a.V && !(out[k][lane >> 5] >> (lane & 31) & 1);
+        y[q] = in[q] ? row[w] : 0.0f;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (in[q]) join(r, Sums{y[q], fabsf(y[q]) < __builtin_inff() ? 0.0f : kNaN, 0.0f});
+    }
+  }
+  r = join_all<NT>(r, sm);
+  if (wave) return;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    part[i] = a.tail && word[lane + 64 * i] >= 0 && !again[lane + 64 * i];
+    x[i] = z[i];
+  }
+  finish(a, t, lane, r, on, z, x, part);
 }
 
 // What the gradient's products need of a token (struct Vocab): its label (the first word
@@ -649,7 +740,7 @@ template <int NT> void go_top(const Top& t, int64_t rows, hipStream_t s) {
 template <int D>
 hipError_t logprobs(const Logprobs& a, hipStream_t s) {
   const Vocab& v = a.v;
-  const KeepPlan k = keep_plan(v.T, v.V, v.d, D, a.given, a.k, true);
+  const KeepPlan k = keep_plan(v.T, v.V, v.d, D, a.given, a.k);
   char* w = (char*)v.work;
   hipError_t e;
   Kept o{};
@@ -707,7 +798,7 @@ hipError_t logprobs(const Logprobs& a, hipStream_t s) {
 template <int D>
 hipError_t distill(const Distill& a, hipStream_t s) {
   const Vocab& v = a.v;
-  const KeepPlan k = keep_plan(v.T, v.V, v.d, D, a.K, 0, false);
+  const KeepPlan k = keep_plan(v.T, v.V, v.d, D, a.K, 0);
   char* w = (char*)v.work;
   hipError_t e;
   Near r{};
@@ -715,6 +806,7 @@ hipError_t distill(const Distill& a, hipStream_t s) {
   r.kept.stat = (f32x4*)(w + k.stat);
   r.kept.groups = k.groups;
   r.kept.without = a.tail;
+  r.V = v.V;
   r.ldi = a.ldi;
   r.ldq = a.ldq;
   r.K = (int)a.K;
@@ -729,18 +821,21 @@ hipError_t distill(const Distill& a, hipStream_t s) {
     r.lse = a.lse + t0;
     r.rest = a.rest + t0;
     r.hit = a.hit + t0 * a.K;
-    if ((e = mark(w, k, r.ids, a.ldi, a.K, n, v.V, &r.kept, &r.places, s)) != hipSuccess) return e;
     float* z = a.z && keeps(v.T, v.V, v.d, D) ? a.z + t0 * row_of(v.V) : nullptr;
     r.kept.z = z;
     r.kept.ldz = row_of(v.V);
     if (k.few) {
+      if (!z) r.kept.z = (float*)(w + k.z);
       if ((e = score<D>(v, 0, v.V, r.kept, s)) != hipSuccess) return e;
-    } else {
-      const int64_t step = direct(v.W, v.ldw, v.d, D) ? v.V : k.p.piece;
-      for (int64_t v0 = 0; v0 < v.V; v0 += step) {
-        r.kept.z = z ? z + v0 : nullptr;
-        if ((e = pick<D>(v, k, H, t0, n, v0, std::min(step, v.V - v0), r.kept, s)) != hipSuccess) return e;
-      }
+      hipLaunchKernelGGL(distill_few_kernel<512>, dim3((unsigned)n), dim3(512), 0, s, r);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      continue;
+    }
+    if ((e = mark(w, k, r.ids, a.ldi, a.K, n, v.V, &r.kept, &r.places, s)) != hipSuccess) return e;
+    const int64_t step = direct(v.W, v.ldw, v.d, D) ? v.V : k.p.piece;
+    for (int64_t v0 = 0; v0 < v.V; v0 += step) {
+      r.kept.z = z ? z + v0 : nullptr;
+      if ((e = pick<D>(v, k, H, t0, n, v0, std::min(step, v.V - v0), r.kept, s)) != hipSuccess) return e;
     }
     hipLaunchKernelGGL(distill_kernel<256>, dim3((unsigned)n), dim3(256), 0, s, r);
     if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -767,10 +862,10 @@ SharePlan share_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t K) {
 }  // namespace
 
 int64_t logprobs_work_bytes(int64_t T, int64_t V, int64_t d, int dtype, int64_t given, int64_t k) {
-  return keep_plan(T, V, d, dtype, given, k, true).bytes;
+  return keep_plan(T, V, d, dtype, given, k).bytes;
 }
 int64_t distill_work_bytes(int64_t T, int64_t V, int64_t d, int dtype, int64_t K, bool grad) {
-  return grad ? share_plan(T, V, d, dtype, K).bytes : keep_plan(T, V, d, dtype, K, 0, false).bytes;
+  return grad ? share_plan(T, V, d, dtype, K).bytes : keep_plan(T, V, d, dtype, K, 0).bytes;
 }
 
 hipError_t launch_vocab_logprobs(const Logprobs& a, hipStream_t s) {
