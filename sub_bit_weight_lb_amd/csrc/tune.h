@@ -138,12 +138,12 @@ struct Distill {
   float *loss, *lse, *rest, *hit;    // T, T, T, T x K; but for loss read by the gradient
   float* z;                          // T x (V to 128), nullable: logits that are kept for it
 };
-// few tokens' gradient: v with labels, lse, share, ids, val as above; z, G (T rows of FewPlan's ldz),
-// part: FewPlan's
+// few tokens' gradient: z, G (T rows of FewPlan's ldz), part: FewPlan's; labels: T, scratch
 struct Few {
-  Vocab v;
+  Distill a;
   const float* z;
   float *G, *part;
+  int32_t* labels;
 };
 hipError_t launch_few_gradient(const Few& a, hipStream_t s);
 int64_t logprobs_work_bytes(int64_t T, int64_t V, int64_t d, int dtype, int64_t given, int64_t k);

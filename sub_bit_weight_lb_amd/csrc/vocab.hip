@@ -276,25 +276,31 @@ hipError_t backward(const Vocab& a, hipStream_t s) {
     }
     // (G is zero for words past nv to the next multiple of 64, and from
     // mma_kernel for tokens past T to the tile's end)
+    Mma h{}, x{};
+    int slices = 0, tile_h = 0, tile_x = 0;
     if (a.dH) {
-      Mma h{};
       h.A = Opnd{W.p, W.ld, W.plane, a.d, nv};
       h.B = Opnd{G, gld, p.piece, RT, nvp};
       h.K = round_up(nv, BK);
       h.k_slice = p.kz;
       h.part = (float*)(w + p.part); h.slice = slice; h.ldo = ldp; h.add = v0 > 0;
-      const int n = (int)((h.K + p.kz - 1) / p.kz), tile = big_tiles(a.d, RT, p.nz) ? 256 : 128;
-      if ((e = mma_launch<D, kDh>(h, tile, n, s)) != hipSuccess) return e;
+      slices = (int)((h.K + p.kz - 1) / p.kz);
+      tile_h = big_tiles(a.d, RT, p.nz) ? 256 : 128;
     }
     if (a.dW) {
-      Mma x{};
       x.A = Hw;
       x.B = Opnd{G, gld, p.piece, nv, score_g ? RT : p.tp};
       x.K = x.k_slice = round_up(RT, BK);
       x.post = &fac->post_w;
       x.out = (E*)a.dW + v0 * a.lddw; x.ldo = a.lddw;
-      if ((e = mma_launch<D, kDw>(x, tile_for(a.d, nv), 1, s)) != hipSuccess) return e;
+      tile_x = tile_for(a.d, nv);
     }
+    if (a.dH && a.dW && pairs(tile_h, tiles_of(a.d, RT, 128) * slices, tile_x, tiles_of(a.d, nv, 128))) {
+      if ((e = pair_launch<D>(h, slices, x, s)) != hipSuccess) return e;
+      continue;
+    }
+    if (a.dH && (e = mma_launch<D, kDh>(h, tile_h, slices, s)) != hipSuccess) return e;
+    if (a.dW && (e = mma_launch<D, kDw>(x, tile_x, 1, s)) != hipSuccess) return e;
   }
   if (a.dH) {
     const dim3 grid((unsigned)((a.d + 1023) / 1024), (unsigned)std::min<int64_t>(a.T, 16384));

@@ -12,7 +12,7 @@
 
 #include <algorithm>
 
-#include "vocab_plan.h"
+#include "vocab_share.h"
 
 namespace nq {
 using namespace vocab;
@@ -25,33 +25,48 @@ struct __attribute__((packed)) Raw {
   typename Elem<D>::type e[N];
 };
 
-// G of 1024 words of a token per workgroup, zero past the last word to the next multiple of 64.
-__global__ __launch_bounds__(256) void few_g_kernel(const float* __restrict__ z, int64_t ldz,
-                                                    int64_t V, const int32_t* __restrict__ ids,
-                                                    int64_t ldi, int K, const float* __restrict__ val,
-                                                    const int32_t* __restrict__ labels,
-                                                    const float* __restrict__ ref,
-                                                    const float* __restrict__ share,
+// G of 1024 words of a token per workgroup, zero past the last word to the next multiple of 64, and
+// the token's label. Each workgroup finds the token's share and its entries' val for itself: that is
+// a launch less.
+__global__ __launch_bounds__(256) void few_g_kernel(Taught a, const float* __restrict__ z, int64_t ldz,
                                                     const float* __restrict__ dloss, float scale,
-                                                    float* __restrict__ G) {
+                                                    int32_t* __restrict__ labels, float* __restrict__ G) {
+  __shared__ int word[kList];
+  __shared__ double q[kList];
+  __shared__ float val[kList], shared;
+  __shared__ int32_t tag;
   const int64_t t = blockIdx.y, v0 = (int64_t)blockIdx.x * 1024, v = v0 + 4 * threadIdx.x;
-  const int32_t label = labels[t];
-  const float dl = label < 0 ? 0.0f : label < V ? dloss[t] * scale : __builtin_nanf("");
+  f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (v < ldz) x = *(const f32x4*)(z + t * ldz + v);
+  const float ref = a.tail ? a.rest[t] : a.lse[t], dt = dloss[t];
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    const Share s = share_of(a, t, lane, word, q);
+    val[lane] = s.val[0];
+    val[lane + 64] = s.val[1];
+    if (lane == 0) {
+      tag = s.label;
+      shared = s.share;
+      if (blockIdx.x == 0) labels[t] = s.label;
+    }
+  }
+  __syncthreads();
+  const int32_t label = tag;
+  const float dl = label < 0 ? 0.0f : label < a.V ? dt * scale : __builtin_nanf("");
   if (v < ldz) {
     f32x4 g = {0.0f, 0.0f, 0.0f, 0.0f};
     if (label >= 0) {
-      const f32x4 x = *(const f32x4*)(z + t * ldz + v);
-      const float r = ref[t], s = share[t] * dl;
+      const float s = shared * dl;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) g[i] = v + i < V ? expf(x[i] - r) * s : 0.0f;
+      for (int i = 0; i < 4; ++i) g[i] = v + i < a.V ? expf(x[i] - ref) * s : 0.0f;
     }
     *(f32x4*)(G + t * ldz + v) = g;
   }
   __syncthreads();
   // (a word listed twice has the same val twice)
-  for (int k = threadIdx.x; k < K; k += 256) {
-    const int64_t id = ids[t * ldi + k];
-    if (id >= v0 && id < v0 + 1024 && id < V) G[t * ldz + id] = val[t * K + k] * dl;
+  for (int k = threadIdx.x; k < a.K; k += 256) {
+    const int64_t id = word[k];
+    if (id >= v0 && id < v0 + 1024 && id < a.V) G[t * ldz + id] = val[k] * dl;
   }
 }
 
@@ -245,13 +260,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(NS == 16 ? 
 template <int D>
 hipError_t gradient(const Few& a, hipStream_t s) {
   typedef typename Elem<D>::type E;
-  const Vocab& v = a.v;
+  const Vocab& v = a.a.v;
   const FewPlan p = few_plan(v.T, v.V, v.d, D);
   const int T = (int)v.T;
   hipError_t e;
-  hipLaunchKernelGGL(few_g_kernel, dim3((unsigned)((p.ldz + 1023) / 1024), (unsigned)T), dim3(256), 0, s, a.z,
-                     p.ldz, v.V, v.ids, v.ldi, (int)v.listed, v.val, v.labels, v.lse, v.share, v.dloss, v.scale,
-                     a.G);
+  const Taught of{a.a.ids, a.a.logq, a.a.lse, a.a.rest, a.a.hit, a.a.ldi, a.a.ldq, v.V, (int)a.a.K, a.a.tail};
+  hipLaunchKernelGGL(few_g_kernel, dim3((unsigned)((p.ldz + 1023) / 1024), (unsigned)T), dim3(256), 0, s, of, a.z,
+                     p.ldz, v.dloss, v.scale, a.labels, a.G);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (v.dH) {
     const int64_t ldp = round_up(v.d, 4), slice = v.T * ldp;
@@ -266,7 +281,7 @@ hipError_t gradient(const Few& a, hipStream_t s) {
     else if constexpr (D == kF32) go(std::integral_constant<int, 4>{});
     if ((e = hipGetLastError()) != hipSuccess) return e;
     hipLaunchKernelGGL(few_join_kernel<D>, dim3((unsigned)((v.d + 255) / 256), (unsigned)T), dim3(256), 0, s,
-                       a.part, (int)p.slices, slice, ldp, v.d, v.labels, (E*)v.dH, v.lddh);
+                       a.part, (int)p.slices, slice, ldp, v.d, a.labels, (E*)v.dH, v.lddh);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (v.dW) {
@@ -276,7 +291,7 @@ hipError_t gradient(const Few& a, hipStream_t s) {
     const dim3 grid((unsigned)x, (unsigned)((all + blocks - 1) / blocks));
     auto go = [&](auto steps) {
       constexpr int NS = decltype(steps)::value;
-      hipLaunchKernelGGL((few_dw_kernel<D, NS>), grid, dim3(256), 0, s, (const E*)v.H, v.ldh, T, v.V, v.d, v.labels,
+      hipLaunchKernelGGL((few_dw_kernel<D, NS>), grid, dim3(256), 0, s, (const E*)v.H, v.ldh, T, v.V, v.d, a.labels,
                          a.G, p.ldz, blocks, (E*)v.dW, v.lddw);
     };
     if (T <= 4) go(std::integral_constant<int, 1>{});
@@ -292,8 +307,8 @@ hipError_t gradient(const Few& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_few_gradient(const Few& a, hipStream_t s) {
-  if (a.v.dtype == kF32) return gradient<kF32>(a, s);
-  return a.v.dtype == kBF16 ? gradient<kBF16>(a, s) : gradient<kF16>(a, s);
+  if (a.a.v.dtype == kF32) return gradient<kF32>(a, s);
+  return a.a.v.dtype == kBF16 ? gradient<kBF16>(a, s) : gradient<kF16>(a, s);
 }
 
 }  // namespace nq

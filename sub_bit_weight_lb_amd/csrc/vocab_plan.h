@@ -45,11 +45,12 @@ inline int g_rows(int64_t T, int64_t d, int dtype) {
   return dtype != kF32 && few(T, d, dtype) ? kFewTerms : 1;
 }
 
-// From kept logits: of up to 128 tokens, whose rows of G still fit one tile of dH, where W is what
-// takes the time; and where the products are short. (One term's error of dH and dW, over that of
+// From kept logits: of up to 192 tokens, where W is most of what takes the
+// time; and where the products are so short that it does not matter (301 tokens, 4999 x 515:
+// two terms take 10 us more of 88). (One term's error of dH and dW, over that of
 // rounding the exact ones: up to 1.7 with 33 to 65 tokens, 1.56 with 200; with more it nears 2^0.5.)
 inline int kept_rows(int64_t T, int64_t V, int64_t d, int dtype) {
-  return dtype != kF32 && (T <= 128 || (double)T * V * d <= 4294967296.0) ? kFewTerms : 1;
+  return dtype != kF32 && (T <= 192 || (double)T * V * d <= 536870912.0) ? kFewTerms : 1;
 }
 
 struct Plan {
@@ -91,6 +92,13 @@ inline int dh_slices(int64_t T, int64_t d, int64_t piece) {
   const int64_t ns = std::max<int64_t>(1, std::min(512 / tiles_of(d, T, 128), most));
   const bool lead = 4.0 / nb <= 0.85 * 2.5 / ns;
   return (int)(big * nb >= 192 && piece / nb >= 1024 && lead ? nb : ns);
+}
+// Whether dH's and dW's products, of so many 128 x 128 tiles (slices counted), go in one launch: where
+// both are taken in such tiles, or dW in smaller ones, and two rounds of two per CU hold them (the
+// loss's gradient of 700 tokens, 3000 x 512 bf16: 51 -> 44 us; 300 tokens, 5000 x 300 fp32: 80 -> 66).
+// The results are the same.
+inline bool pairs(int tile_h, int64_t nh, int tile_w, int64_t nw) {
+  return tile_h == 128 && tile_w <= 128 && nh + nw <= 1024;
 }
 // Words per piece: G, and a copy of W's piece where one is needed, hold at most
 // 2^26 values each (two thousand words at least), which leaves the fp32 sums of

@@ -131,10 +131,10 @@ constexpr bool b_major(int epi) { return epi == kDw; }
 // Tile order: workgroup b runs on XCD b % 8, which takes consecutive indices;
 // indices run down bands of 4 tile rows, so that the 32 tiles an XCD holds at
 // once form a 4 x 8 block and share operands in its L2.
-__device__ __forceinline__ bool tile_of(uint32_t ntm, uint32_t ntn, int64_t& tm, int64_t& tn) {
+__device__ __forceinline__ bool tile_of(uint32_t bx, uint32_t ntm, uint32_t ntn, int64_t& tm, int64_t& tn) {
   const uint32_t nt = ntm * ntn, per = (nt + 7) / 8;   // (< 2^31: 2^24 x 2^20 outputs at most)
-  const uint32_t t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if ((blockIdx.x >> 3) >= per || t >= nt) return false;
+  const uint32_t t = (bx & 7) * per + (bx >> 3);
+  if ((bx >> 3) >= per || t >= nt) return false;
   const uint32_t band = t / (4 * ntn), idx = t - band * 4 * ntn;
   const uint32_t h = min(4u, ntm - 4 * band);
   tm = 4 * band + idx % h;
@@ -283,22 +283,21 @@ struct Reader {
 // kernel without its copies 1.5, matrix instructions alone 2.2). fp32, 1024
 // tokens, 32000 words, d = 2048: 0.40 to 0.46 ms each, 290 to 330 TFLOP/s.
 template <int D, int EPI, int WM, int WN, int MI, int NI, int NS>
-__global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
+__device__ __forceinline__ void mma_body(const Mma a, uint32_t bx, uint32_t by, uint8_t* lds) {
   constexpr int BM = 16 * MI * WM, BN = 16 * NI * WN, W = WM * WN;
   constexpr int kStage = (BM + BN) * 128;
   constexpr int CA = BM / 8 / W, CB = BN / 8 / W;
   static_assert(CA * 8 * W == BM && CB * 8 * W == BN, "copies");
   constexpr bool AM = a_major(EPI), BM_ = b_major(EPI), F16 = D != kBF16;
-  __shared__ __align__(16) uint8_t lds[NS * kStage];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, li = lane & 15;
   const int wm = wave / WN, wn = wave % WN;
   const int64_t M = a.A.rows, N = a.B.rows;
   int64_t tm, tn;
-  if (!tile_of((uint32_t)((M + BM - 1) / BM), (uint32_t)((N + BN - 1) / BN), tm, tn)) return;
+  if (!tile_of(bx, (uint32_t)((M + BM - 1) / BM), (uint32_t)((N + BN - 1) / BN), tm, tn)) return;
   const int64_t m0 = tm * BM, n0 = tn * BN;
-  const int64_t k_lo = (int64_t)blockIdx.y * a.k_slice;
+  const int64_t k_lo = (int64_t)by * a.k_slice;
   const int nk = (int)((lmin(a.K, k_lo + a.k_slice) - k_lo) / BK);
   const int steps = nk * passes(D);
 
@@ -628,7 +627,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
       }
     }
   } else if constexpr (EPI == kDh) {
-    float* part = a.part + (int64_t)blockIdx.y * a.slice;
+    float* part = a.part + (int64_t)by * a.slice;
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const int64_t t = c0 + 16 * j;
@@ -667,6 +666,22 @@ __global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
       }
     }
   }
+}
+
+template <int D, int EPI, int WM, int WN, int MI, int NI, int NS>
+__global__ __launch_bounds__(64 * WM * WN) void mma_kernel(Mma a) {
+  __shared__ __align__(16) uint8_t lds[NS * 16 * (MI * WM + NI * WN) * 128];
+  mma_body<D, EPI, WM, WN, MI, NI, NS>(a, blockIdx.x, blockIdx.y, lds);
+}
+// Two products in one launch, dH's and dW's, in 128 x 128 tiles: where neither fills the chip. nh
+// workgroups are dH's, nx to a slice.
+template <int D, int NS>
+__global__ __launch_bounds__(256) void pair_kernel(Mma h, Mma w, uint32_t nh, uint32_t nx) {
+  __shared__ __align__(16) uint8_t lds[NS * 256 * 128];
+  if (blockIdx.x < nh)
+    mma_body<D, kDh, 2, 2, 4, 4, NS>(h, blockIdx.x % nx, blockIdx.x / nx, lds);
+  else
+    mma_body<D, kDw, 2, 2, 4, 4, NS>(w, blockIdx.x - nh, 0, lds);
 }
 
 // ---------------------------------------------------------------- few tokens
@@ -1225,6 +1240,14 @@ inline hipError_t rowpack(const void* X, int64_t rows, int64_t k, int64_t ld, fl
                           float* unscale, int64_t full, hipStream_t s) {
   hipLaunchKernelGGL(rowpack_kernel, dim3((unsigned)std::min<int64_t>(rows, 65536)), dim3(256), 0, s, (const float*)X,
                      rows, k, ld, mul, out, kp, unscale, full);
+  return hipGetLastError();
+}
+// dH's and dW's products at once, in 128 x 128 tiles
+template <int D>
+hipError_t pair_launch(const Mma& h, int slices, const Mma& w, hipStream_t s) {
+  const int64_t nx = (tiles_of(h.A.rows, h.B.rows, 128) + 7) / 8 * 8, nw = (tiles_of(w.A.rows, w.B.rows, 128) + 7) / 8 * 8;
+  hipLaunchKernelGGL((pair_kernel<D, 2>), dim3((unsigned)(nx * slices + nw)), dim3(256), 0, s, h, w,
+                     (uint32_t)(nx * slices), (uint32_t)nx);
   return hipGetLastError();
 }
 template <int D, int M>

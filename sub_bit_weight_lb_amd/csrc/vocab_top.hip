@@ -23,11 +23,11 @@
 //   and from the second on only parts with a z above the k-th best so far are written.
 // A workgroup per token (top_kernel, distill_kernel) then joins the groups.
 #include "vocab_product.h"
+#include "vocab_share.h"
 
 namespace nq {
 namespace {
 
-constexpr int kList = (int)kMaxListed;
 const float kNaN = __builtin_nanf("");
 
 // ---------------------------------------------------------------- joins of sums
@@ -425,48 +425,6 @@ struct Near {
   int K, tail;
   float *loss, *lse, *rest, *hit;
 };
-// sum of x over a wave, in a fixed order; all lanes get it
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
-  return x;
-}
-__device__ __forceinline__ double wave_max(double x) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x = fmax(x, __shfl_xor(x, o));
-  return x;
-}
-// A teacher's probabilities of one token: entries lane and lane + 64 of a wave, in 64 bits (r is
-// what a sum near one leaves). on: whether the entry is one.
-struct Teacher {
-  double q[2], logq[2], sum, r;
-};
-__device__ __forceinline__ Teacher teacher(const float (&l)[2], const bool (&on)[2], bool tail) {
-  Teacher t;
-  double top = 0.0;
-  if (!tail) {
-    top = wave_max(fmax(on[0] ? (double)l[0] : -INFINITY, on[1] ? (double)l[1] : -INFINITY));
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    t.logq[i] = on[i] ? (double)l[i] - top : 0.0;
-    t.q[i] = on[i] ? exp(t.logq[i]) : 0.0;
-  }
-  t.sum = wave_sum(t.q[0] + t.q[1]);
-  if (!tail) {
-    const double log_sum = log(t.sum);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      t.q[i] /= t.sum;
-      t.logq[i] -= log_sum;
-    }
-    t.sum = t.sum == t.sum ? 1.0 : t.sum;
-  }
-  t.r = tail ? 1.0 - t.sum : 0.0;
-  t.r = t.r < 0.0 ? 0.0 : t.r;   // (a NaN stays)
-  return t;
-}
-
 // loss, lse, rest and hit of token t, by one wave: r joins the groups' sums (with a tail: without the
 // listed words); of entries lane and lane + 64 on: whether they are one, z (NaN for a word past the
 // last); the distinct listed words' z are those x that are `part`.
@@ -624,56 +582,21 @@ __global__ __launch_bounds__(NT) void distill_few_kernel(Near a) {
   finish(a, t, lane, r, on, z, x, part);
 }
 
-// What the gradient's products need of a token (struct Vocab): its label (the first word
-// listed, whose G val replaces; V where one is at or past V; -1 without any), its share,
-// and val of its entries. Four tokens per workgroup, a wave each.
-__global__ __launch_bounds__(256) void shares_kernel(const int32_t* __restrict__ ids, int64_t ldi,
-                                                     const float* __restrict__ logq, int64_t ldq,
-                                                     int K, int tail, int64_t T, int64_t V,
-                                                     const float* __restrict__ lse,
-                                                     const float* __restrict__ rest,
-                                                     const float* __restrict__ hit,
-                                                     int32_t* __restrict__ labels,
-                                                     float* __restrict__ share,
-                                                     float* __restrict__ val) {
+// Labels, shares and val (struct Vocab) of the gradient. Four tokens per workgroup, a wave each.
+__global__ __launch_bounds__(256) void shares_kernel(Taught a, int64_t T, int32_t* __restrict__ labels,
+                                                     float* __restrict__ share, float* __restrict__ val) {
   __shared__ int word[4][kList];
-  __shared__ double qs[4][kList];
+  __shared__ double q[4][kList];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = (int64_t)blockIdx.x * 4 + wave;
-  const bool real = t < T;
-  float l[2];
-  bool on[2];
-  int id[2];
+  if (t >= T) return;
+  const Share s = share_of(a, t, lane, word[wave], q[wave]);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int k = lane + 64 * i;
-    id[i] = real && k < K ? ids[t * ldi + k] : -1;
-    on[i] = id[i] >= 0;
-    l[i] = on[i] ? logq[t * ldq + k] : 0.0f;
-    word[wave][k] = id[i];
-  }
-  const Teacher q = teacher(l, on, tail);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) qs[wave][lane + 64 * i] = q.q[i];
-  __syncthreads();
-  if (!real) return;
-  const double e = lse[t], out = tail ? (double)rest[t] : e;
-  const double r = out == -INFINITY ? 0.0 : q.r, whole = q.sum + r;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int k = lane + 64 * i;
-    if (k >= K) continue;
-    double mine = 0.0;
-    if (on[i])
-      for (int j = 0; j < K; ++j) mine += word[wave][j] == id[i] ? qs[wave][j] : 0.0;
-    val[t * K + k] = on[i] ? (float)(whole * exp((double)hit[t * K + k] - e) - mine) : 0.0f;
-  }
-  const uint64_t some[2] = {__ballot(on[0]), __ballot(on[1])};
-  const bool past = __ballot(id[0] >= V || id[1] >= V) != 0;
+  for (int i = 0; i < 2; ++i)
+    if (lane + 64 * i < a.K) val[t * a.K + lane + 64 * i] = s.val[i];
   if (lane == 0) {
-    const int first = some[0] ? __ffsll((unsigned long long)some[0]) - 1 : some[1] ? 63 + __ffsll((unsigned long long)some[1]) : -1;
-    labels[t] = first < 0 ? -1 : past ? (int32_t)V : word[wave][first];
-    share[t] = first < 0 ? 0.0f : (float)(tail ? whole * exp(out - e) - r : whole);
+    labels[t] = s.label;
+    share[t] = s.share;
   }
 }
 
@@ -883,38 +806,38 @@ hipError_t launch_vocab_distill_backward(const Distill& a, hipStream_t s) {
   const SharePlan p = share_plan(v.T, v.V, v.d, v.dtype, a.K);
   char* w = (char*)v.work;
   int32_t* labels = (int32_t*)(w + p.labels);
-  float *share = (float*)(w + p.share), *val = (float*)(w + p.val);
-  hipLaunchKernelGGL(shares_kernel, dim3((unsigned)((v.T + 3) / 4)), dim3(256), 0, s, a.ids, a.ldi, a.logq,
-                     a.ldq, (int)a.K, a.tail, v.T, v.V, a.lse, a.rest, a.hit, labels, share, val);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  const Taught of{a.ids, a.logq, a.lse, a.rest, a.hit, a.ldi, a.ldq, v.V, (int)a.K, a.tail};
+  const float* z = keeps(v.T, v.V, v.d, v.dtype) ? a.z : nullptr;
   v.labels = labels;
   v.lse = a.tail ? a.rest : a.lse;
+  if (few(v.T, v.d, v.dtype)) {
+    const FewPlan f = few_plan(v.T, v.V, v.d, v.dtype);
+    Few g{a, z, (float*)(w + f.G), (float*)(w + f.part), labels};
+    if (!g.z) {
+      Kept o{};
+      o.z = (float*)(w + f.z);
+      o.ldz = f.ldz;
+      const hipError_t e = v.dtype == kF32    ? score<kF32>(v, 0, v.V, o, s)
+                           : v.dtype == kBF16 ? score<kBF16>(v, 0, v.V, o, s)
+                                              : score<kF16>(v, 0, v.V, o, s);
+      if (e != hipSuccess) return e;
+      g.z = o.z;
+    }
+    return launch_few_gradient(g, s);
+  }
+  float *share = (float*)(w + p.share), *val = (float*)(w + p.val);
+  hipLaunchKernelGGL(shares_kernel, dim3((unsigned)((v.T + 3) / 4)), dim3(256), 0, s, of, v.T, labels, share, val);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   v.share = share;
   v.wr = (float*)(w + p.wr);
   v.ids = a.ids;
   v.ldi = a.ldi;
   v.listed = a.K;
   v.val = val;
-  const float* z = keeps(v.T, v.V, v.d, v.dtype) ? a.z : nullptr;
-  if (!few(v.T, v.d, v.dtype)) {
-    v.z = z;
-    v.ldz = row_of(v.V);
-    return launch_vocab_loss_backward(v, s);
-  }
-  const FewPlan f = few_plan(v.T, v.V, v.d, v.dtype);
-  Few g{v, z, (float*)(w + f.G), (float*)(w + f.part)};
-  if (!g.z) {
-    Kept o{};
-    o.z = (float*)(w + f.z);
-    o.ldz = f.ldz;
-    const hipError_t e = v.dtype == kF32    ? score<kF32>(v, 0, v.V, o, s)
-                         : v.dtype == kBF16 ? score<kBF16>(v, 0, v.V, o, s)
-                                            : score<kF16>(v, 0, v.V, o, s);
-    if (e != hipSuccess) return e;
-    g.z = o.z;
-  }
-  return launch_few_gradient(g, s);
+  v.z = z;
+  v.ldz = row_of(v.V);
+  return launch_vocab_loss_backward(v, s);
 }
 
 }  // namespace nq
