@@ -122,7 +122,9 @@ __global__ __launch_bounds__(256) void dh_kernel(const float* __restrict__ part,
 
 // G of 2048 words of a token per workgroup from kept logits (z: of the piece's words): what kGrad
 // makes of them, in N terms, and val at the words that the token lists; zero to the next multiple
-// of 64 words and for tokens past T.
+// of 64 words and for tokens past T. Bound by HBM: a piece of 4096 tokens and 16384 words of bf16 72
+// us, 5.6 TB/s. (z is read once more and never again: past the caches, loss and gradient of 1024
+// tokens, 32000 x 2048, 508 -> 497 us.)
 template <int D, int N>
 __global__ __launch_bounds__(256) void kept_kernel(const float* __restrict__ z, int64_t ldz, int64_t T,
                                                    int64_t v0, int64_t nv, const int32_t* __restrict__ ids,
@@ -140,8 +142,8 @@ __global__ __launch_bounds__(256) void kept_kernel(const float* __restrict__ z, 
     const float ref = used ? lse[t] : 0.0f, s = used ? wr[t] : 0.0f;
     f32x4 x[2] = {};
     if (used) {   // (rows hold whole groups of 128 words)
-      x[0] = *(const f32x4*)(z + t * ldz + w);
-      x[1] = *(const f32x4*)(z + t * ldz + w + 4);
+      x[0] = __builtin_nontemporal_load((const f32x4*)(z + t * ldz + w));
+      x[1] = __builtin_nontemporal_load((const f32x4*)(z + t * ldz + w + 4));
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

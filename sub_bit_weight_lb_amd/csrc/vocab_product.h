@@ -61,7 +61,7 @@ struct Opnd {
 // What the operators that look at single logits (vocab_top.hip) keep of them. The words
 // of a token lie in groups: half a tile's, or 64 of score_kernel's. The distinct words that a
 // token lists have places in its row of zl; a group with any has a mark.
-struct __attribute__((aligned(32))) Mark {
+struct Mark {
   u32x4 words;              // which of the group's words are listed
   uint32_t place;           // of the first of them; the others follow
 };

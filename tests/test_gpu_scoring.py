@@ -280,12 +280,43 @@ def test_logprobs_of_no_rows(gpu):
     assert r.logprobs.shape == (10, 0) and abs(float(r.lse[0]) - np.log(10)) < 8 * U * 3
 
 
+@pytest.mark.parametrize("name", ["bfloat16", "float32"])
+@pytest.mark.parametrize("k", [1, 20, 64, 128])
+def test_vocabularies_in_several_steps(gpu, name, k):
+    """More logits than are kept whole: the best words of a step at a time. Values on a
+    grid, whose logits are exact in any order of summing, so that equal ones are many;
+    rows of one value, and rows that rise or fall along the vocabulary."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    T, V, d = 520, 130003, 64
+    assert T * V > 1 << 26
+    g = torch.Generator(device=gpu).manual_seed(k)
+    W = torch.randint(-3, 4, (V, d), generator=g, device=gpu).float()
+    W[:, 0] = (torch.arange(V, device=gpu) // 512 - 127).float()
+    Hh = torch.randint(-3, 4, (T, d), generator=g, device=gpu).float() / 8
+    Hh[:, 0] = 0
+    Hh[0] = 0
+    Hh[1], Hh[2], Hh[1, 0], Hh[2, 0] = 0, 0, 0.125, -0.125
+    tokens = torch.randint(0, V, (T, 2), generator=g, device=gpu, dtype=torch.int32)
+    r = nq.vocab_logprobs(Hh.to(dt(name)), W.to(dt(name)), tokens, k)
+    z = torch.mm(Hh.double(), W.double().t())
+    lse = torch.logsumexp(z, 1)
+    for a in range(0, T, 130):
+        best, ids = torch.sort(z[a:a + 130], dim=1, descending=True, stable=True)
+        assert torch.equal(r.top_ids[a:a + 130].long(), ids[:, :k])
+        tol = (V + 64) * U + 8 * U * best.abs().max()
+        assert ((r.top_logprobs[a:a + 130].double() - (best[:, :k] - lse[a:a + 130, None])).abs() <= tol).all()
+    tol = (V + 64) * U + 8 * U * z.abs().max()
+    assert ((r.lse.double() - lse).abs() <= tol).all()
+    assert ((r.logprobs.double() - (z.gather(1, tokens.long()) - lse[:, None])).abs() <= tol).all()
+
+
 def test_steps_and_blocks_are_one_result(gpu):
     """More tokens than a block holds, with a list so long that blocks are short: the rows'
     results are those of calls on parts of them."""
     import torch
     import sub_bit_weight_lb_amd as nq
-    T, V, d, k, G = 20000, 3000, 32, 20, 128
+    T, V, d, k, G = 50000, 3000, 32, 20, 128
     g = torch.Generator(device=gpu).manual_seed(4)
     Hh = torch.randn((T, d), generator=g, device=gpu).bfloat16()
     W = torch.randn((V, d), generator=g, device=gpu).bfloat16()
@@ -293,7 +324,7 @@ def test_steps_and_blocks_are_one_result(gpu):
     logq = torch.log_softmax(torch.randn((T, G), generator=g, device=gpu), 1) - 0.1
     r = nq.vocab_logprobs(Hh, W, tokens, k)
     loss, q = nq.vocab_distill(Hh, W, tokens, logq)
-    for rows in (slice(0, 2000), slice(8000, 9000), slice(19000, T)):
+    for rows in (slice(0, 2000), slice(43000, 45000), slice(49000, T)):
         p = nq.vocab_logprobs(Hh[rows], W, tokens[rows], k)
         # (tiles of another size join the words in another order: lse to rounding, z the same)
         assert torch.equal(p.top_ids, r.top_ids[rows])
@@ -596,16 +627,21 @@ def test_gradient_of_few_tokens(gpu, name, T, V, d):
     assert torch.equal(L.grad(q, want_dW=False)[0], dH) and torch.equal(L.grad(q, want_dH=False)[1], dW)
 
 
-def test_several_pieces_of_the_vocabulary(gpu):
+@pytest.mark.parametrize("name, T, keep", [("bfloat16", 40, True), ("bfloat16", 40, False), ("float16", 200, True),
+                                           ("float32", 70, True), ("float32", 70, False), ("float32", 5, True)])
+def test_several_pieces_of_the_vocabulary(gpu, name, T, keep):
     """A hidden size so large that W is copied and taken in pieces: against float64 on
     the GPU."""
     import torch
-    T, V, d, K = 40, 5000, 33001, 30
-    L = Taught(11, T, V, d, K, "bfloat16", gpu)
-    loss, q = L.loss()
+    V, d, K = 5000, 33001, 30
+    L = Taught(11, T, V, d, K, name, gpu)
+    loss, q = L.loss(keep=keep)
+    assert (q.logits is None) == (not keep)
     dH, dW = L.grad(q)
     z = torch.mm(L.H.double(), L.W.double().t())
-    zb = (d + 2) * U * float(torch.mm(L.H.double().abs(), L.W.double().abs().t()).max())
+    more = 2.0 ** -22 if name == "float32" else 0.0
+    zb = ((d + 2) * U + more) * float(torch.mm(L.H.double().abs(), L.W.double().abs().t()).max())
+    h = half(name)
     ids = L.ids.long()
     on = ids >= 0
     used = on.any(1)
@@ -624,11 +660,12 @@ def test_several_pieces_of_the_vocabulary(gpu):
     f = (L.dl.double() * used).unsqueeze(1)
     mag = ((qk.sum(1) + r).unsqueeze(1) * torch.softmax(z, 1) + target + part) * f.abs()
     G = (G - part) * f
-    rel = 2.0 ** -8 + float(np.expm1(3 * tol)) + (V + 64) * U
+    # (G's rounding, or its second term's end)
+    rel = h + 2.0 ** -21 + more + float(np.expm1(3 * tol)) + (V + 64) * U
     for got, ref, m in ((dH, torch.mm(G, L.W.double()), torch.mm(mag, L.W.double().abs())),
                         (dW, torch.mm(G.t().contiguous(), L.H.double()),
                          torch.mm(mag.t().contiguous(), L.H.double().abs()))):
-        assert ((got.double() - ref).abs() <= rel * m + 2.0 ** -8 * ref.abs() + 1e-30).all()
+        assert ((got.double() - ref).abs() <= rel * m + h * ref.abs() + V * 2.0 ** -38 + least(name)).all()
 
 
 # ---------------------------------------------------------------- together
