@@ -472,8 +472,8 @@ nq_status nq_vocab_loss_backward(const void* H, int64_t ldh, const void* W, int6
  * gradient). Host only; -1 for sizes out of range. */
 int64_t nq_vocab_loss_work_bytes(int64_t T, int64_t V, int64_t d, int32_t dtype, int32_t grad);
 
-/* Log probabilities over a large vocabulary, the T x V logits z = scale H W^T never
- * kept (H, W, dtype, sizes, strides and scale as in nq_vocab_loss). Device float32
+/* Log probabilities over a large vocabulary, of whose logits z = scale H W^T work holds a
+ * part at a time (H, W, dtype, sizes, strides and scale as in nq_vocab_loss). Device float32
  * unless said otherwise:
  *   lse_t = log sum_v exp z_tv (T),
  *   entropy_t = -sum_v p log p of p = exp(z - lse) (T),
@@ -515,7 +515,8 @@ int64_t nq_vocab_logprobs_work_bytes(int64_t T, int64_t V, int64_t d, int32_t dt
  *     where every word is listed, rest is -infinity and r counts as 0;
  *   tail == 0: q = softmax of logq over the token's entries (logq may be logits):
  *     loss_t = sum_k q_k (log q_k - z_t,ids[k] + lse_t); rest = lse.
- * Terms with q = 0 or r = 0 are 0. A word listed more than once has the sum of its
+ * Terms with q = 0 or r = 0 are 0 (tail == 0 and logq -infinity in all of a token's entries:
+ * NaN). A word listed more than once has the sum of its
  * entries' terms. loss, lse, rest (T) and hit (T x K: z of each entry, 0 for none) are
  * device float32, lse, rest and hit for the gradient. An ignored token has 0 in all
  * of them and its row of H is not used; one with a word >= V has NaN in loss and in

@@ -713,7 +713,7 @@ def vocab_logprobs_work_bytes(T, V, d, dtype, given=0, k=0):
 
 
 def vocab_logprobs(H, W, tokens=None, k=0, scale=1.0, out=None, work=None, stream=None):
-    """Log probabilities under softmax of z = scale H W^T, which is never kept: H
+    """Log probabilities under softmax of z = scale H W^T, which never leaves the call: H
     (T x d) and W (V x d) float32, bfloat16 or float16 with unit column stride.
     tokens (T, or T x G with G <= 128; int32): the words whose log probability is
     wanted, a negative one gives 0, one >= V NaN. Returns a VocabLogprobs with those,
@@ -813,16 +813,17 @@ def _distill_state(q, T, V, K):
 
 def vocab_distill(H, W, ids, logq, scale=1.0, tail=True, keep=True, loss=None, state=None, work=None,
                   stream=None):
-    """KL divergence of softmax(z), z = scale H W^T never kept, from a teacher's K <=
-    128 words per token: ids (T x K int32; a negative one is no entry, a token without
+    """KL divergence of softmax(z), z = scale H W^T, from a teacher's K <= 128
+    words per token: ids (T x K int32; a negative one is no entry, a token without
     any is ignored) and their log probabilities logq (T x K float32), as
     vocab_logprobs gives them for the teacher (at its own scale: one over the
     temperature). tail: the rest of the teacher's mass, 1 - sum exp logq, is one
     outcome more, "another word"; without it logq is normalised over a token's
     entries (and may be logits). Returns (loss, state): T float32, 0 for an ignored
     token, and the VocabDistill that vocab_distill_backward takes (keep: with the
-    logits, where it pays); both can be given to be filled. A word >= V gives NaN; one listed twice counts with both entries.
-    work, if given, holds vocab_distill_work_bytes(T, V, d, H.dtype, K) bytes."""
+    logits, where it pays); both can be given to be filled. A word >= V gives NaN;
+    one listed twice counts with both entries; without tail, a row of nothing but
+    -infinity has no softmax and gives NaN. work, if given, holds vocab_distill_work_bytes(T, V, d, H.dtype, K) bytes."""
     torch = _torch()
     f32 = torch.float32
     T, V, d, code, ldh, ldw, K, ldi, ldq = _distill_args(H, W, ids, logq)
@@ -857,8 +858,8 @@ def vocab_distill_backward(H, W, ids, logq, state, dloss, scale=1.0, tail=True, 
                            want_dW=True, dH=None, dW=None, work=None, stream=None):
     """Gradient of sum(dloss * loss) for (loss, state) = vocab_distill(H, W, ids,
     logq, scale, tail) of one call with these tokens: returns (dH, dW) in H's type
-    (None where not wanted). dloss is T float32. The logits are computed again in
-    pieces of the vocabulary. Ignored tokens get zero rows of dH and add nothing to
+    (None where not wanted). dloss is T float32. Where state has no logits they are
+    computed again, in pieces of the vocabulary. Ignored tokens get zero rows of dH and add nothing to
     dW. Outputs must not share memory with inputs. work, if given, holds
     vocab_distill_work_bytes(T, V, d, H.dtype, K, grad=True) bytes."""
     torch = _torch()

@@ -1,5 +1,5 @@
-// What is asked of single logits of a large vocabulary, which are never kept as a
-// whole (z = scale H W^T, the products of vocab_product.h):
+// What is asked of single logits of a large vocabulary (z = scale H W^T, the products of
+// vocab_product.h; of many tokens they are kept only where a gradient will read them):
 //
 // Log probabilities, to score a model and to write down what it holds likely:
 //   lse_t = log sum_v exp z_tv,  log p = z - lse of the given words,
@@ -199,9 +199,10 @@ __device__ __forceinline__ uint32_t reached(const uint32_t (&x)[N], int k, int l
 //   value), as many parts at a time as it has room for.
 template <int NT>
 __global__ __launch_bounds__(NT) void top_kernel(Top a) {
+  static_assert(NT % 256 == 0, "256 shares");
   constexpr int kCap = 512, NW = NT / 64, kEach = kCap / 64;
   __shared__ uint64_t list[kCap];
-  __shared__ __align__(16) uint32_t most[NT > 64 ? 256 : 4];
+  __shared__ __align__(16) uint32_t most[256];
   __shared__ int todo[4 * NT];
   __shared__ int count, left;
   __shared__ uint32_t lim;
@@ -236,28 +237,21 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
       }
       return x;
     };
-    uint32_t m[4] = {};
+    uint32_t m = 0;
     for (int64_t p = a.p0 + 4 * tid; p < a.p1; p += 4 * NT) {
       const f32x4 x = four(p);
-      if constexpr (NT > 64) {
-        m[0] = max(m[0], order_of(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]))));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m[i] = max(m[i], order_of(x[i]));
-      }
+      m = max(m, order_of(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]))));
     }
-    if constexpr (NT > 64) {
 #pragma unroll
-      for (int o = 1; o < NT / 256; o *= 2) m[0] = max(m[0], (uint32_t)__shfl_xor((int)m[0], o));
-      if (tid % (NT / 256) == 0) most[tid / (NT / 256)] = m[0];
-    }
+    for (int o = 1; o < NT / 256; o *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, o));
+    if (tid % (NT / 256) == 0) most[tid / (NT / 256)] = m;
     if (a.have)
       for (int i = tid; i < k; i += NT) list[i] = a.best[t * k + i];
     if (tid == 0) count = a.have ? k : 0;
     __syncthreads();
     uint64_t bound;   // keys above it are in
     {
-      const u32x4 q = NT > 64 ? ((const u32x4*)most)[lane] : u32x4{m[0], m[1], m[2], m[3]};
+      const u32x4 q = ((const u32x4*)most)[lane];
       const uint32_t x[4] = {q[0], q[1], q[2], q[3]};
       int n;
       const uint32_t c = reached(x, k, 12, &n);

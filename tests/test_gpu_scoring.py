@@ -801,3 +801,164 @@ def test_calls_on_other_streams(gpu):
     torch.cuda.synchronize()
     for out in got:
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+# ---------------------------------------------------------------- ends of the ranges
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("T", [3, 70, 300])
+def test_a_scale_of_zero(gpu, name, T):
+    """All logits 0: p = 1 / V, the lowest words first, no gradient."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    V, d, K = 5003, 72, 9
+    L = Taught(41, T, V, d, K, name, gpu, scale=0.0)
+    r = nq.vocab_logprobs(L.H, L.W, L.ids, K, scale=0.0)
+    # (V terms of 1: exact; log rounds by an ulp of 8.5 at most, and is exact to 4 u elsewhere)
+    tol = 4 * U * np.log(V)
+    assert (np.abs(H64(r.lse) - np.log(V)) <= tol).all() and (np.abs(H64(r.entropy) - np.log(V)) <= tol).all()
+    assert (r.top_ids == torch.arange(K, device=gpu, dtype=torch.int32)).all()
+    assert (np.abs(H64(r.top_logprobs) + np.log(V)) <= 2 * tol).all()
+    loss, q = L.loss()
+    dH, dW = L.grad(q)
+    assert (q.hit == 0).all() and (dH == 0).all() and (dW == 0).all()
+
+
+def softmaxed(z, ids, logq):
+    """Divergence without a tail and its gradient by z, in float64 on the GPU."""
+    import torch
+    lse = torch.logsumexp(z, 1, keepdim=True)
+    lq = torch.log_softmax(logq.double(), 1)
+    loss = (lq.exp() * (lq - z.gather(1, ids.long()) + lse)).sum(1)
+    return loss, lse[:, 0], torch.exp(z - lse).scatter_add_(1, ids.long(), -lq.exp())
+
+
+@pytest.mark.parametrize("name", ["bfloat16", "float32"])
+def test_very_many_tokens(gpu, name):
+    """More tokens than the second axis of a grid holds."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    T, V, d, K = 100001, 130, 24, 5
+    g = torch.Generator(device=gpu).manual_seed(5)
+    Hh = torch.randn((T, d), generator=g, device=gpu).to(dt(name))
+    W = torch.randn((V, d), generator=g, device=gpu).to(dt(name))
+    ids = torch.randint(0, V, (T, K), generator=g, device=gpu, dtype=torch.int32)
+    logq = torch.randn((T, K), generator=g, device=gpu)
+    dl = torch.randn(T, generator=g, device=gpu)
+    z = Hh.double() @ W.double().t()
+    loss, lse, G = softmaxed(z, ids, logq)
+    more = 2.0 ** -22 if name == "float32" else 0.0
+    zb = ((d + 2) * U + more) * float((Hh.double().abs() @ W.double().abs().t()).max()) + 2 * U * float(z.abs().max())
+    tol = 2 * zb + 2 * (V + 64) * U + 4 * U * float(loss.abs().max())
+    r = nq.vocab_logprobs(Hh, W, ids, K)
+    assert ((r.lse.double() - lse).abs() <= tol).all()
+    assert ((r.logprobs.double() - (z.gather(1, ids.long()) - lse[:, None])).abs() <= tol).all()
+    best = torch.topk(z, K, 1).values
+    assert ((z.gather(1, r.top_ids.long()) - best).abs() <= 2 * zb).all()
+    got, q = nq.vocab_distill(Hh, W, ids, logq, tail=False)
+    assert ((got.double() - loss).abs() <= tol).all()
+    dH, dW = nq.vocab_distill_backward(Hh, W, ids, logq, q, dl, tail=False)
+    G *= dl.double()[:, None]
+    mag = G.abs() + torch.exp(z - lse[:, None]) * dl.double().abs()[:, None]
+    h = half(name)
+    for out, ref, m, n in ((dH, G @ W.double(), mag @ W.double().abs(), V),
+                           (dW, G.t() @ Hh.double(), mag.t() @ Hh.double().abs(), T)):
+        rel = h + more + float(np.expm1(3 * tol)) + (n + 64) * U
+        assert ((out.double() - ref).abs() <= rel * m + h * ref.abs() + n * 2.0 ** -38 + least(name)).all()
+
+
+@pytest.mark.parametrize("T", [3, 70])
+def test_a_vocabulary_past_32_bits(gpu, T):
+    """W of more than 2^32 bytes: the last words and columns."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    V, d, K = 140001, 16384, 4
+    assert 2 * V * d > 1 << 32
+    g = torch.Generator(device=gpu).manual_seed(6)
+    W = torch.empty((V, d), dtype=torch.bfloat16, device=gpu)
+    W.normal_(0.0, 1 / 64, generator=g)
+    Hh = torch.randn((T, d), generator=g, device=gpu).bfloat16()
+    z = torch.cat([Hh.double() @ W[a:a + 20000].double().t() for a in range(0, V, 20000)], 1)
+    ids = torch.cat([torch.randint(0, V, (T, K - 1), generator=g, device=gpu, dtype=torch.int32),
+                     torch.full((T, 1), V - 1, dtype=torch.int32, device=gpu)], 1)
+    logq = torch.randn((T, K), generator=g, device=gpu)
+    dl = torch.randn(T, generator=g, device=gpu)
+    loss, lse, G = softmaxed(z, ids, logq)
+    size = max(float((Hh.double().abs() @ W[a:a + 20000].double().abs().t()).max()) for a in range(0, V, 20000))
+    zb = (d + 2) * U * size
+    tol = 2 * zb + 2 * (V + 64) * U
+    r = nq.vocab_logprobs(Hh, W, ids, K)
+    assert ((r.lse.double() - lse).abs() <= tol).all()
+    assert ((r.logprobs.double() - (z.gather(1, ids.long()) - lse[:, None])).abs() <= tol).all()
+    assert ((z.gather(1, r.top_ids.long()) - torch.topk(z, K, 1).values).abs() <= 2 * zb).all()
+    got, q = nq.vocab_distill(Hh, W, ids, logq, tail=False)
+    assert ((got.double() - loss).abs() <= tol).all()
+    dH, dW = nq.vocab_distill_backward(Hh, W, ids, logq, q, dl, tail=False)
+    G *= dl.double()[:, None]
+    mag = G.abs() + torch.exp(z - lse[:, None]) * dl.double().abs()[:, None]
+    h = half("bfloat16")
+    rel = h + float(np.expm1(3 * tol)) + (V + 64) * U
+    cols = torch.cat([torch.arange(64, device=gpu), torch.arange(d - 64, d, device=gpu)])
+    near = W[:, cols].double()
+    assert ((dH[:, cols].double() - G @ near).abs() <= rel * (mag @ near.abs()) + h * (G @ near).abs()).all()
+    for rows in (slice(0, 200), slice(V - 200, V)):
+        ref, m = G[:, rows].t() @ Hh.double(), mag[:, rows].t() @ Hh.double().abs()
+        assert ((dW[rows].double() - ref).abs() <= rel * m + h * ref.abs() + least("bfloat16")).all()
+
+
+def test_kept_logits_past_31_bits(gpu):
+    """Kept logits of more than 2^31 bytes, in several pieces for the gradient."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    T, V, d, K = 4100, 140001, 1024, 3
+    g = torch.Generator(device=gpu).manual_seed(7)
+    W = torch.randn((V, d), generator=g, device=gpu).mul_(1 / 16).bfloat16()
+    Hh = torch.randn((T, d), generator=g, device=gpu).bfloat16()
+    ids = torch.randint(0, V, (T, K), generator=g, device=gpu, dtype=torch.int32)
+    logq = torch.randn((T, K), generator=g, device=gpu)
+    dl = torch.randn(T, generator=g, device=gpu)
+    got, q = nq.vocab_distill(Hh, W, ids, logq, tail=False)
+    assert q.logits is not None and 4 * q.logits.numel() > 1 << 31
+    dH, dW = nq.vocab_distill_backward(Hh, W, ids, logq, q, dl, tail=False)
+    z = Hh.double() @ W.double().t()
+    loss, lse, G = softmaxed(z, ids, logq)
+    zb = (d + 2) * U * float((Hh[:256].double().abs() @ W.double().abs().t()).max()) * 1.5
+    tol = 2 * zb + 2 * (V + 64) * U
+    assert ((got.double() - loss).abs() <= tol).all()
+    G *= dl.double()[:, None]
+    mag = torch.exp(z - lse[:, None]).mul_(dl.double().abs()[:, None]).add_(G.abs())
+    h = half("bfloat16")
+    rel = h + float(np.expm1(3 * tol)) + (V + 64) * U
+    w, x = W.double(), Hh.double()
+    assert ((dH.double() - G @ w).abs() <= rel * (mag @ w.abs()) + h * (G @ w).abs()).all()
+    for rows in (slice(0, 300), slice(V // 2, V // 2 + 300), slice(V - 300, V)):
+        ref, m = G[:, rows].t() @ x, mag[:, rows].t() @ x.abs()
+        assert ((dW[rows].double() - ref).abs() <= rel * m + h * ref.abs() + least("bfloat16")).all()
+
+
+@pytest.mark.parametrize("T", [5, 140])
+def test_lists_with_entries_of_no_mass(gpu, T):
+    """Log probabilities of -infinity: in a part of a list they add nothing; as all of it they
+    leave the rest alone (with a tail) or no softmax (without)."""
+    import torch
+    V, d, K = 700, 40, 6
+    for tail in (True, False):
+        L = Taught(43, T, V, d, K, "float32", gpu, tail=tail)
+        L.logq[:, 1::2] = -float("inf")
+        L.logq[2] = -float("inf")
+        ids = L.ids.cpu().numpy()
+        loss, q = L.loss()
+        dH, dW = L.grad(q)
+        z = H64(L.H) @ H64(L.W).T
+        lse = O.lse_of(z)
+        if tail:
+            rest = np.array([O.lse_of(np.delete(z[t], np.unique(ids[t][ids[t] >= 0]))[None])[0] for t in range(T)])
+            # (z's sums of 40 products, lse, rest: (d + 2) u |h| |w|, (V + 64) u of each sum)
+            tol = 4 * ((d + 2) * U + 2.0 ** -22) * (np.abs(H64(L.H)) @ np.abs(H64(L.W)).T).max() + 2 * (V + 64) * U
+            if (ids[2] >= 0).any():
+                assert abs(float(loss[2]) - (lse[2] - rest[2])) <= tol
+            assert torch.isfinite(loss).all() and torch.isfinite(dH).all() and torch.isfinite(dW).all()
+        else:
+            some = torch.arange(T, device=gpu) != 2
+            assert (ids[2] < 0).all() or (loss[2].isnan() and dH[2].isnan().all())
+            assert torch.isfinite(loss[some]).all() and torch.isfinite(dH[some]).all()
