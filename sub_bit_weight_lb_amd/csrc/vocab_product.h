@@ -199,48 +199,56 @@ struct Tile {
       }
     }
   }
-  // The copies of the 64 k from k on, of the term `plane` elements into the
-  // rows, to LDS offset st: made ready here, sent one at a time by put(). What
-  // lies past the operand's end reads as zero (the descriptor's range, which
+  // The copies of a stage of 64 k: start() and next() say which, aim() makes them ready, put()
+  // sends one. What lies past the operand's end reads as zero (the descriptor's range, which
   // counts the vector offset alone: all of an address below its base is in it).
-  int lo, hi, n, to;
+  uint64_t at;            // address of the stage
+  int64_t rest;           // bytes from there to the operand's end
+  int more;               // k from there to kv
+  // the stage from k on, of the term `plane` elements into the rows
+  __device__ __forceinline__ void start(int64_t k, int64_t plane) {
+    const int64_t skip = 2 * ((MAJOR ? k * ld : k) + plane);
+    at = (uint64_t)(uintptr_t)base + skip;
+    rest = left - skip;
+    more = (int)(kv - k);
+  }
+  __device__ __forceinline__ void next() {
+    const int64_t skip = 2 * (MAJOR ? BK * ld : BK);
+    at += skip;
+    rest -= skip;
+    more -= BK;
+  }
+  typedef int i32x4 __attribute__((ext_vector_type(4)));
+  i32x4 range;            // the descriptor
+  int to;
   uint32_t o[2], step;
-  // (!live: copies of zeros, which read nothing.)
-  __device__ __forceinline__ void aim(bool live, uint32_t st, int wave, int64_t k, int64_t plane) {
-    const int64_t skip = (MAJOR ? k * ld : k) + plane;
-    const uint64_t p = (uint64_t)(uintptr_t)(base + skip);
-    lo = scalar((int)p);
-    hi = scalar((int)(p >> 32) & 0xffff);
-    n = scalar(live ? (int)lmin(lmax(left - 2 * skip, 0), 0x7fffffff) : 0);
-    to = scalar((int)(st + wave * NC * 1024));
+  // To LDS offset st. (!live: copies of zeros, which read nothing.) In 32-bit steps and without a
+  // branch: it runs between products.
+  __device__ __forceinline__ void aim(bool live, uint32_t st, int wave) {
+    const int high = (int)(rest >> 32);
+    const uint32_t low = (uint32_t)rest;
+    const int n = high < 0 ? 0 : high > 0 || low > 0x7fffffffu ? 0x7fffffff : (int)low;
+    range = i32x4{(int)at, (int)(at >> 32) & 0xffff, live ? n : 0, 0x20000};
+    to = (int)st + wave * NC * 1024;
     step = (uint32_t)(kRowsPer * ld * 2);
-    o[0] = off[0];
-    o[1] = off[1];
-    if constexpr (!MAJOR) {
-      if (k + BK > kv) {
-        // octets past kv: past any descriptor's range
+    // (octets past kv: past any descriptor's range)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) o[c] = k + 8 * koct[c] >= kv ? 0x80000000u : o[c];
-      }
-    }
+    for (int c = 0; c < 2; ++c) o[c] = !MAJOR && 8 * koct[c] >= more ? 0x80000000u : off[c];
   }
   // Copy c. Written out: after a builtin's every transposing read would wait
   // for it, though it is for the next stage. It writes no register, sync()
-  // waits for it, and it keeps its place among the reads and sync()s.
+  // waits for it, and it keeps its place among the reads and sync()s. (Five states from
+  // whatever wrote the descriptor, as a vector instruction's result would need.)
   __device__ __forceinline__ void put(int c) const {
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"   // (m0 is reserved: nothing is kept in it across)
     asm volatile(
-        "s_mov_b32 s92, %0\n\t"
-        "s_mov_b32 s93, %1\n\t"
-        "s_mov_b32 s94, %2\n\t"
-        "s_mov_b32 s95, 0x20000\n\t"
-        "s_add_u32 m0, %3, %4\n\t"
-        "s_nop 0\n\t"
-        "buffer_load_dwordx4 %5, s[92:95], 0 offen lds"
+        "s_add_u32 m0, %1, %2\n\t"
+        "s_nop 3\n\t"
+        "buffer_load_dwordx4 %3, %0, 0 offen lds"
         :
-        : "s"(lo), "s"(hi), "s"(n), "s"(to), "i"(c * 1024), "v"(o[kind(c)] + c * step)
-        : "m0", "s92", "s93", "s94", "s95", "scc");
+        : "s"(range), "s"(to), "i"(c * 1024), "v"(o[kind(c)] + c * step)
+        : "m0", "scc");
 #pragma clang diagnostic pop
   }
 };
@@ -278,10 +286,16 @@ struct Reader {
 // replace, NS - 2 stages, a half-stage of products and more before they are
 // waited for. (NS: mma_launch.)
 // Bound by how the copies and the products share a CU: 4096 tokens, 131072 words,
-// d = 4096 in bf16, kStat 3.65 ms and, in eight pieces, kGrad 3.7, kDh 3.4, kDw
-// 3.5: 1.19 to 1.29 PFLOP/s (a large bf16 product of the library 1.27; this
-// kernel without its copies 1.5, matrix instructions alone 2.2). fp32, 1024
-// tokens, 32000 words, d = 2048: 0.40 to 0.46 ms each, 290 to 330 TFLOP/s.
+// d = 4096 in bf16, kStat 3.26 ms and, in eight pieces, kGrad, kDh and kDw 3.3 to
+// 3.5: 1.25 to 1.35 PFLOP/s (a large bf16 product of the library 1.27, one of 8192^3
+// 1.62; matrix instructions alone 2.2; under this load the clock is 1.94 GHz, at
+// which the matrix cores work 63 to 68 % of the time). fp32, 1024 tokens, 32000
+// words, d = 2048: 0.37 to 0.44 ms each, 305 to 360 TFLOP/s. What a stage needs beside
+// products, reads and copies is kept off their way: its addresses go on by steps, in
+// 32-bit scalar operations between the products of the half before, and the compiler knows
+// which reads have come (all of it after the barrier, and a wait for every read at the
+// loop's head: kStat 3.56 ms, fp32 0.49 for 0.46). Four waves of 128 x 128, which read a
+// third less from LDS but have nobody to work while they wait: 3.8.
 template <int D, int EPI, int WM, int WN, int MI, int NI, int NS>
 __device__ __forceinline__ void mma_body(const Mma a, uint32_t bx, uint32_t by, uint8_t* lds) {
   constexpr int BM = 16 * MI * WM, BN = 16 * NI * WN, W = WM * WN;
@@ -312,16 +326,24 @@ __device__ __forceinline__ void mma_body(const Mma a, uint32_t bx, uint32_t by, 
   // passes: h l, l h, h h (the small ones first: what they round is 2^-11 of a
   // sum with h h in it)
   int pass = 0, kt = 0;
+  ta.start(k_lo, 0);
+  tb.start(k_lo, D == kF32 ? a.B.plane : 0);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
   // the next stage's copies, ready to go to `stage`
-  auto aim = [&](int stage, bool live) {
-    const uint32_t st = lds0 + stage * kStage;
-    const int64_t k = k_lo + (int64_t)kt * BK;
-    ta.aim(live, st, wave, k, D == kF32 && pass == 1 ? a.A.plane : 0);
-    tb.aim(live, st + BM * 128, wave, k, D == kF32 && pass == 0 ? a.B.plane : 0);
-    if (++kt == nk) {
-      kt = 0;
-      ++pass;
+  auto aim_a = [&](int stage, bool live) {
+    ta.aim(live, lds0 + stage * kStage, wave);
+    ta.next();
+  };
+  auto aim_b = [&](int stage, bool live) {
+    tb.aim(live, lds0 + stage * kStage + BM * 128, wave);
+    tb.next();
+    if constexpr (D == kF32) {
+      if (++kt == nk) {
+        kt = 0;
+        ++pass;
+        ta.start(k_lo, pass == 1 ? a.A.plane : 0);
+        tb.start(k_lo, 0);
+      }
     }
   };
   f32x4 acc[MI][NI];
@@ -332,14 +354,15 @@ __device__ __forceinline__ void mma_body(const Mma a, uint32_t bx, uint32_t by, 
   u32x4 fa[2][MI], fb[2][NI];
   // Multiplies half h while the other half's fragments come from stage st, and
   // with COPY the copies made ready go out: a row of products, its reads and
-  // copies at a time (a run of copies would hold up the products behind it).
-  auto phase = [&](auto half, auto copies, uint8_t* st) {
+  // copies at a time (a run of copies would hold up the products behind it), and with(row).
+  auto phase = [&](auto half, auto copies, uint8_t* st, auto with) {
     constexpr int h = decltype(half)::value;
     constexpr bool COPY = decltype(copies)::value;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       if (i < NI) fb[h ^ 1][i] = rb.read(st + BM * 128, i, h ^ 1);
       fa[h ^ 1][i] = ra.read(st, i, h ^ 1);
+      with(i);
 #pragma unroll
       for (int j = 0; j < NI; ++j) acc[i][j] = mma<F16>(fa[h][i], fb[h][j], acc[i][j]);
       if constexpr (COPY) {
@@ -358,6 +381,7 @@ __device__ __forceinline__ void mma_body(const Mma a, uint32_t bx, uint32_t by, 
   // last `ahead` stages, then for the other waves
   auto sync = [&](auto ahead) {
     __builtin_amdgcn_sched_barrier(0);    // (products before it stay before it)
+    __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0) once more, for the compiler's own count of reads
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(decltype(ahead)::value * (CA + CB))
                  : "memory");
     __builtin_amdgcn_sched_barrier(0);
@@ -366,7 +390,8 @@ __device__ __forceinline__ void mma_body(const Mma a, uint32_t bx, uint32_t by, 
   // around them would cost more, and every wait counts the same)
 #pragma unroll 1
   for (int st = 0; st < NS; ++st) {
-    aim(st, st < steps);
+    aim_a(st, st < steps);
+    aim_b(st, st < steps);
 #pragma unroll
     for (int c = 0; c < CA; ++c) ta.put(c);
 #pragma unroll
@@ -382,12 +407,14 @@ __device__ __forceinline__ void mma_body(const Mma a, uint32_t bx, uint32_t by, 
   int cur = 0;
   for (int s = 0; s < steps; ++s) {
     const int next = cur + 1 == NS ? 0 : cur + 1;
-    phase(H0{}, std::false_type{}, lds + cur * kStage);
+    phase(H0{}, std::false_type{}, lds + cur * kStage, [&](int i) {
+      if (i == MI / 2 - 1) aim_a(cur, s + NS < steps);
+      if (i == MI / 2) aim_b(cur, s + NS < steps);
+    });
     // the next stage has landed; everyone has read this one
     sync(std::integral_constant<int, NS - 2>{});
-    aim(cur, s + NS < steps);
     // (after the last stage this reads what is there, for nothing)
-    phase(H1{}, std::true_type{}, lds + next * kStage);
+    phase(H1{}, std::true_type{}, lds + next * kStage, [](int) {});
     cur = next;
   }
   // the last copies must land before this workgroup's LDS is given away
