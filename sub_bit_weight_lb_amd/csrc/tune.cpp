@@ -1,7 +1,8 @@
 // C ABI of the operators that tune a packed model (declared in include/nq.h):
 // 8-bit activation checkpoints (act8.hip), the gradient of a packed layer from
-// such a checkpoint (binback.hip) and the loss over a large vocabulary with its
-// gradient (vocab.hip). Each call only checks its arguments and enqueues
+// such a checkpoint (binback.hip), the loss over a large vocabulary with its
+// gradient (vocab.hip), log probabilities and the divergence from a teacher's words
+// with its gradient (vocab_top.hip, vocab_few.hip). Each call only checks its arguments and enqueues
 // kernels on the caller's stream: no allocation, no wait.
 #include <algorithm>
 #include <cmath>

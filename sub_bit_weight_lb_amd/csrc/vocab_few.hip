@@ -7,7 +7,8 @@
 // terms (the 16-bit products of vocab_product.h would need W's columns gathered and G in two
 // terms), and G keeps all its bits. Its rate, 256 operations per CU and cycle, is the
 // bandwidth's with 32 tokens of a 16-bit W or 64 of an fp32 one.
-//   32000 x 4096 bf16, 1 token, loss and gradient: 333 us with the 16-bit products.
+//   32000 x 4096 bf16, 1 token, loss and gradient: 214 us, 333 with the 16-bit products. dH 54 us and
+//   dW 51, 262 MB each: 4.9 and 5.1 TB/s.
 #include "tune.h"
 
 #include <algorithm>

@@ -473,7 +473,8 @@ __device__ __forceinline__ void mma_body(const Mma a, uint32_t bx, uint32_t by, 
   } else if constexpr (EPI == kPick) {
     // z = acc zs with zs made positive, so that the largest acc is the largest z, e = 2^((acc
     // - largest) zs log2 e) without a scaled z, and dot is NaN where an acc is not finite
-    // (0 times infinity, too).
+    // (0 times infinity, too). 777 tokens, 50021 x 1000 fp16, in us: with kStat the kernel takes 142,
+    // with this 147 to 151, with 100 listed words of each token 164.
     const Kept& o = a.kept;
     const int64_t group = a.v0 / (16 * MI) + tm * WM + wm;
     if constexpr (D == kF32) {   // (factors of words differ: z itself)
@@ -1172,7 +1173,9 @@ __global__ __launch_bounds__(256) void pack_kernel(const typename Elem<D>::type*
 
 // The two terms of each row of fp32 X (rows x k), scaled by a power of two of its own to 2^15 at
 // their largest, zero from k to kp: out [row][term][kp]; unscale[row] = mul over the power, 0 from
-// the last row to unscale[full]. A workgroup per row, which it reads twice where it is long.
+// the last row to unscale[full]. A workgroup per row, which it reads twice where it is long. (512
+// tokens, 32000 x 2048: a call of 336 us with a pass for W's largest value and pack_kernel, 295 with
+// this, which takes 82: 6.4 TB/s.)
 __global__ __launch_bounds__(256) void rowpack_kernel(const float* __restrict__ X, int64_t rows, int64_t k,
                                                       int64_t ld, float mul, uint16_t* __restrict__ out,
                                                       int64_t kp, float* __restrict__ unscale, int64_t full) {

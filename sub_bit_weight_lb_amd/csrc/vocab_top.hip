@@ -83,7 +83,10 @@ __device__ __forceinline__ Sums join_all(Sums a, float* sm) {
 // ---------------------------------------------------------------- listed words
 // slot, marks (Kept) and the place of each of a token's K entries in its row of zl (255: a word
 // below 0 or past the last): the distinct words of its list, by groups in the order of their
-// first entries. A workgroup per token.
+// first entries. A workgroup per token, a thread per entry, which all look through the whole
+// list in LDS (K^2 / 4 reads of 16 bytes: 5 us for 4096 tokens of one word, 11 for 64; 777 tokens
+// of 100 words 6). So that the products' epilogue reads a byte per token and group, and a bit
+// map where it says so: 12 us of 164 with 100 words of each token (777 tokens, 50021 x 1000 fp16).
 struct Marks {
   uint8_t* slot;
   int64_t lds;
@@ -197,12 +200,14 @@ __device__ __forceinline__ uint32_t reached(const uint32_t (&x)[N], int k, int l
 //   the places; keys are distinct, so that the order does not show), which one wave cuts to
 //   its k best, found bit by bit. If the list is too short for them (many words of one
 //   value), as many parts at a time as it has room for.
+// Bound by a token's chain of dependent loads and barriers: 9 us for one token of 32000 words, 20
+// best; 4096 tokens of 131072 words, 64 best, five steps of 35 to 47 us each (0.23 ms of 3.3).
 template <int NT>
 __global__ __launch_bounds__(NT) void top_kernel(Top a) {
   static_assert(NT % 256 == 0, "256 shares");
   constexpr int kCap = 512, NW = NT / 64, kEach = kCap / 64;
   __shared__ uint64_t list[kCap];
-  __shared__ __align__(16) uint32_t most[256];
+  __shared__ uint32_t most[NT];
   __shared__ int todo[4 * NT];
   __shared__ int count, left;
   __shared__ uint32_t lim;
@@ -237,22 +242,32 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
       }
       return x;
     };
+    // (one at a time where four would leave threads without any: fewer shares than best words
+    // bound nothing; 500 tokens of 1000 parts, 128 best: 513 us, else 20)
     uint32_t m = 0;
-    for (int64_t p = a.p0 + 4 * tid; p < a.p1; p += 4 * NT) {
-      const f32x4 x = four(p);
-      m = max(m, order_of(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]))));
+    if (a.p1 - a.p0 >= 4 * NT) {
+      for (int64_t p = a.p0 + 4 * tid; p < a.p1; p += 4 * NT) {
+        const f32x4 x = four(p);
+        m = max(m, order_of(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]))));
+      }
+    } else {
+#pragma unroll 4
+      for (int64_t p = a.p0 + tid; p < a.p1; p += NT) m = max(m, order_of(tops[p]));
     }
-#pragma unroll
-    for (int o = 1; o < NT / 256; o *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, o));
-    if (tid % (NT / 256) == 0) most[tid / (NT / 256)] = m;
+    most[tid] = m;
     if (a.have)
       for (int i = tid; i < k; i += NT) list[i] = a.best[t * k + i];
     if (tid == 0) count = a.have ? k : 0;
     __syncthreads();
     uint64_t bound;   // keys above it are in
     {
-      const u32x4 q = ((const u32x4*)most)[lane];
-      const uint32_t x[4] = {q[0], q[1], q[2], q[3]};
+      uint32_t x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = most[64 * i + lane];
+#pragma unroll
+        for (int o = 256; o < NT; o += 256) x[i] = max(x[i], most[o + 64 * i + lane]);
+      }
       int n;
       const uint32_t c = reached(x, k, 12, &n);
       bound = c ? ((uint64_t)c << 32) - 1 : 0;
@@ -371,7 +386,7 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
       }
     }
     // (a short list is put in order as it is)
-    if (!a.last || n > NT) cut();
+    if (!a.last || n > 256) cut();
     if (!a.last) {
       for (int i = tid; i < k; i += NT) a.best[t * k + i] = i < n ? list[i] : 0;
       if (tid == 0) a.thr[t] = value_of(lim);
@@ -455,7 +470,8 @@ __device__ __forceinline__ void finish(const Near& a, int64_t t, int lane, Sums 
   }
 }
 
-// A workgroup of NT threads per token.
+// A workgroup of NT threads per token; all of it but the join in one wave, in 64 bits. 777 tokens of
+// 782 groups 10 us, 4096 tokens of 1024 28 (67 MB of sums: 2.4 TB/s).
 template <int NT>
 __global__ __launch_bounds__(NT) void distill_kernel(Near a) {
   __shared__ float sm[3 * (NT / 64)];
@@ -493,8 +509,9 @@ __global__ __launch_bounds__(NT) void distill_kernel(Near a) {
   finish(a, t, lane, r, on, z, x, part);
 }
 
-// The same of few tokens, whose logits are all there (without marks: a launch less). With a tail,
-// groups of 64 words with a listed one are summed again, from those logits.
+// The same of few tokens, whose logits are all there (without marks: a launch less, 7 tokens, 32000 x
+// 4096 bf16 66 -> 62 us). With a tail, groups of 64 words with a listed one are summed again, from
+// those logits. 9 us: dependent loads.
 template <int NT>
 __global__ __launch_bounds__(NT) void distill_few_kernel(Near a) {
   typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -577,6 +594,7 @@ __global__ __launch_bounds__(NT) void distill_few_kernel(Near a) {
 }
 
 // Labels, shares and val (struct Vocab) of the gradient. Four tokens per workgroup, a wave each.
+// 4096 tokens of 64 words: 9 us.
 __global__ __launch_bounds__(256) void shares_kernel(Taught a, int64_t T, int32_t* __restrict__ labels,
                                                      float* __restrict__ share, float* __restrict__ val) {
   __shared__ int word[4][kList];
@@ -704,7 +722,10 @@ hipError_t logprobs(const Logprobs& a, hipStream_t s) {
       t.p0 = v0 / part_of(t.group);
       t.p1 = (v0 + nv + part_of(t.group) - 1) / part_of(t.group);
       t.have = v0 > 0;
-      n <= 64 ? go_top<512>(t, n, s) : go_top<256>(t, n, s);
+      // (512 threads and 256, us a launch: one token of 32000 words 10 and 11, 256 tokens of 131072, 64
+      // best, 15 and 21, 509 of 50021 12.8 and 13.1; 1000 of 32000 20 and 14, 4096 80 and 57: more
+      // tokens share a CU)
+      n <= 512 ? go_top<512>(t, n, s) : go_top<256>(t, n, s);
       if ((e = hipGetLastError()) != hipSuccess) return e;
       if (a.k) step = std::min(std::min(3 * step, k.step), most);
     }
