@@ -242,10 +242,17 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
       }
       return x;
     };
-    // (one at a time where four would leave threads without any: fewer shares than best words
-    // bound nothing; 500 tokens of 1000 parts, 128 best: 513 us, else 20)
+    // (one part at a time where four would leave threads without any, and words where the parts are
+    // few for the best words: fewer shares than those bound nothing. 500 tokens of 1000 parts, 128
+    // best: 513 us by fours, 20; 2000 tokens, 128 best: of 125 parts 89 us, by words 26, of 250 30
+    // and 32)
+    const float* z = a.kept.z + t * a.kept.ldz;
     uint32_t m = 0;
-    if (a.p1 - a.p0 >= 4 * NT) {
+    if (2 * (a.p1 - a.p0) < 3 * k && !a.have) {   // (the first step's z are all there)
+      const int64_t end = lmin(a.V, a.p1 * part);
+#pragma unroll 4
+      for (int64_t w = a.v0 + tid; w < end; w += NT) m = max(m, order_of(z[w - a.v0]));
+    } else if (a.p1 - a.p0 >= 4 * NT) {
       for (int64_t p = a.p0 + 4 * tid; p < a.p1; p += 4 * NT) {
         const f32x4 x = four(p);
         m = max(m, order_of(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]))));
@@ -274,7 +281,6 @@ __global__ __launch_bounds__(NT) void top_kernel(Top a) {
       // (later words lose to earlier ones of the same z)
       if (a.have) bound = max(bound, (uint64_t)order_of(a.thr[t]) << 32 | 0xffffffffu);
     }
-    const float* z = a.kept.z + t * a.kept.ldz;
     n = a.have ? k : 0;
     // cuts the list to its k best; afterwards lim is what they reach
     auto cut = [&]() {

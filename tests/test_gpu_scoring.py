@@ -962,3 +962,25 @@ def test_lists_with_entries_of_no_mass(gpu, T):
             some = torch.arange(T, device=gpu) != 2
             assert (ids[2] < 0).all() or (loss[2].isnan() and dH[2].isnan().all())
             assert torch.isfinite(loss[some]).all() and torch.isfinite(dH[some]).all()
+
+
+@pytest.mark.parametrize("name", ["bfloat16", "float32"])
+@pytest.mark.parametrize("T", [7, 90, 700])
+@pytest.mark.parametrize("V", [128, 129, 700, 1000, 1700, 2100, 3000, 3300, 6000, 9000, 33000])
+def test_best_words_of_short_and_long_vocabularies(gpu, name, T, V):
+    """128 and 100 best words where the vocabulary has fewer parts than that, about as many, and
+    more: words, single parts and four parts at a time bound them. Logits on a grid, exact in any
+    order of summing."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    g = torch.Generator(device=gpu).manual_seed(V)
+    W = torch.randint(-3, 4, (V, 64), generator=g, device=gpu).float()
+    Hh = torch.randint(-3, 4, (T, 64), generator=g, device=gpu).float() / 8
+    Hh[0] = 0
+    z = torch.mm(Hh.double(), W.double().t())
+    best, ids = torch.sort(z, dim=1, descending=True, stable=True)
+    for k in (100, 128):
+        r = nq.vocab_logprobs(Hh.to(dt(name)), W.to(dt(name)), k=k)
+        assert torch.equal(r.top_ids.long(), ids[:, :k])
+        want = best[:, :k] - torch.logsumexp(z, 1)[:, None]
+        assert ((r.top_logprobs.double() - want).abs() <= (V + 64) * U + 8 * U * best.abs().max()).all()
