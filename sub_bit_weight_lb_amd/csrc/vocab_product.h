@@ -719,7 +719,7 @@ __global__ __launch_bounds__(256) void pair_kernel(Mma h, Mma w, uint32_t nh, ui
 // tokens, in us with the join: 16 waves 59 (4.4 TB/s), 8 waves 63, 4 waves 96;
 // 8 waves of 64 columns 71, 4 waves of 128 columns 80, of two such runs in
 // registers 84). Eight values are loaded together from any address (rows that are
-// not 16-byte aligned: 3 tokens, 6673 x 68774 fp16 350 us, one by one 727). At the
+// not 16-byte aligned: 3 tokens, 6673 x 68774 fp16 296 us, one by one 727). At the
 // end of a row the last eight are loaded, and of H those that came before are
 // zeroed (d >= 8).
 template <int D>
@@ -771,8 +771,28 @@ struct ScoreGrad {
   uint16_t* G;
   int64_t gld, v0;
 };
-// (64 registers or fewer: two workgroups of 1024 threads per CU)
-template <int D, int NT, typename OUT>
+// Eight 16-bit values from an address that may not be a multiple of 4: words of 4 bytes are loaded
+// and shifted (`at`: bytes from `base`, which is such a multiple). Each word loaded holds a byte
+// that is asked for. Loads of 16 bytes from such addresses take twice the time where a row has 64 bytes
+// of a load (4 tokens, 34797 x 5825 bf16: 239 us, shifted 151; 20 tokens 294 and 233; rows of 5826,
+// at multiples of 4, 115 as they are). The values are the same.
+template <int D>
+__device__ __forceinline__ Raw8<D> shifted(const char* base, uint32_t at) {
+  struct __attribute__((packed, aligned(4))) Words { uint32_t v[4]; } w;
+  const char* p = base + (at & ~3u);
+  __builtin_memcpy(&w, __builtin_assume_aligned(p, 4), 16);
+  const uint32_t by = (at & 2u) * 8;
+  const uint32_t more = *(const uint32_t*)(p + (by ? 16 : 12));
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = __builtin_amdgcn_alignbit(i < 3 ? w.v[i + 1] : more, w.v[i], by);
+  Raw8<D> r;
+  __builtin_memcpy(&r, o, 16);
+  return r;
+}
+// (64 registers or fewer: two workgroups of 1024 threads per CU. ODD: rows of W, or of H, that do not
+// start at multiples of 4 bytes)
+template <int D, int NT, bool ODD, typename OUT>
 __global__ __launch_bounds__(1024 / NT)
     __attribute__((amdgpu_waves_per_eu(D != kF32 && NT == 1 ? 8 : 1))) void score_kernel(
         const typename Elem<D>::type* __restrict__ H, int64_t ldh,
@@ -788,6 +808,9 @@ __global__ __launch_bounds__(1024 / NT)
   // byte offsets of the rows (64 rows of 2^21 values at most: 32 bits)
   constexpr int kSize = sizeof(typename Elem<D>::type);
   const char *Wb = (const char*)(W + v0 * ldw), *Hb = (const char*)H;
+  const uint32_t in = ODD ? (uint32_t)(uintptr_t)Wb & 2u : 0u, inh = ODD ? (uint32_t)(uintptr_t)Hb & 2u : 0u;
+  Wb -= in;
+  Hb -= inh;
   uint32_t wr[4], hr[NT];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -804,9 +827,19 @@ __global__ __launch_bounds__(1024 / NT)
     const uint32_t at = k * kSize;
     Raw8<D> w[4], h[NT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) __builtin_memcpy(&w[i], Wb + (wr[i] + at), sizeof(w[i]));
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (ODD)
+        w[i] = shifted<D>(Wb, wr[i] + at + in);
+      else
+        __builtin_memcpy(&w[i], Wb + (wr[i] + at), sizeof(w[i]));
+    }
 #pragma unroll
-    for (int j = 0; j < NT; ++j) __builtin_memcpy(&h[j], Hb + (hr[j] + at), sizeof(h[j]));
+    for (int j = 0; j < NT; ++j) {
+      if constexpr (ODD)
+        h[j] = shifted<D>(Hb, hr[j] + at + inh);
+      else
+        __builtin_memcpy(&h[j], Hb + (hr[j] + at), sizeof(h[j]));
+    }
     __builtin_amdgcn_sched_barrier(0);   // (all loads before the first product)
     if (k0 + 32 > d) {
       const int before = k0 + 8 * g - k;
@@ -1360,8 +1393,11 @@ hipError_t score(const Vocab& a, int64_t v0, int64_t nv, const OUT& o, hipStream
   const E *H = (const E*)a.H, *W = (const E*)a.W + v0 * a.ldw;
   auto go = [&](auto tiles) {
     constexpr int NT = decltype(tiles)::value;
-    hipLaunchKernelGGL((score_kernel<D, NT, OUT>), grid, dim3(1024 / NT), 0, s, H, a.ldh, W, a.ldw,
-                       a.T, nv, a.d, a.labels, a.scale, o);
+    auto* kernel = score_kernel<D, NT, false, OUT>;
+    if constexpr (D != kF32)
+      if (a.ldw % 2 || a.ldh % 2 || ((uintptr_t)W | (uintptr_t)H) % 4) kernel = score_kernel<D, NT, true, OUT>;
+    hipLaunchKernelGGL(kernel, grid, dim3(1024 / NT), 0, s, H, a.ldh, W, a.ldw, a.T, nv, a.d, a.labels,
+                       a.scale, o);
   };
   if (a.T <= 16) {
     go(std::integral_constant<int, 1>{});

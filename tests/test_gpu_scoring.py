@@ -984,3 +984,25 @@ def test_best_words_of_short_and_long_vocabularies(gpu, name, T, V):
         assert torch.equal(r.top_ids.long(), ids[:, :k])
         want = best[:, :k] - torch.logsumexp(z, 1)[:, None]
         assert ((r.top_logprobs.double() - want).abs() <= (V + 64) * U + 8 * U * best.abs().max()).all()
+
+
+@pytest.mark.parametrize("name", ["bfloat16", "float16"])
+@pytest.mark.parametrize("T", [1, 4, 17, 32])
+@pytest.mark.parametrize("d, lead", [(8, 1), (9, 0), (33, 1), (333, 0), (514, 1), (515, 1)])
+def test_rows_at_odd_addresses(gpu, name, T, d, lead):
+    """Rows of W and H at every address that 16-bit values can have: the results are those of
+    aligned copies."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    V, K = 777, 9
+    L = Taught(61, T, V, d, K, name, gpu)
+    pad = 8 - d % 8
+    H1, W1 = (strided(x, pad) for x in (L.H, L.W))
+    want = nq.vocab_logprobs(H1, W1, L.ids, K)
+    loss, q = nq.vocab_distill(H1, W1, L.ids, L.logq)
+    for h, w in ((strided(L.H, 0, lead), strided(L.W, 0, lead)), (strided(L.H, 1, 1), W1), (H1, strided(L.W, 1, 1)),
+                 (strided(L.H, 2, 1), strided(L.W, 3, 2))):
+        r = nq.vocab_logprobs(h, w, L.ids, K)
+        assert all(torch.equal(getattr(r, f), getattr(want, f)) for f in ("logprobs", "lse", "entropy", "top_ids"))
+        l2, q2 = nq.vocab_distill(h, w, L.ids, L.logq)
+        assert torch.equal(l2, loss) and torch.equal(q2.hit, q.hit)
