@@ -25,7 +25,7 @@ constexpr int forms(int D) { return D == kBF16 ? 1 : 2; }
 // Whether score_kernel takes a call. With more tokens mma_kernel reads W at a
 // higher rate although half of a tile is empty (4096 x 32000 bf16, 64 tokens: 94
 // us, score_kernel 104; 32 tokens: 72 in score_kernel), but fp32 would be copied
-// for it (2048 x 32000, 64 tokens: 309 us, score_kernel 90). The gradient's logits
+// for it (2048 x 32000, 64 tokens: 309 us, score_kernel 79). The gradient's logits
 // come from the same kernel; its time is much the same with either (4096 x 32000
 // bf16, 1 and 32 tokens, one term of G: 262 and 276 us, with mma_kernel 266 and 274;
 // fp32 790 and 810, 829 and 848).

@@ -726,13 +726,22 @@ template <int D>
 struct __attribute__((packed)) Raw8 {
   typename Elem<D>::type e[8];
 };
-// x = h + m + l in bf16, exact; not finite: the first term alone
-__device__ __forceinline__ void split3(float x, uint16_t (&t)[3]) {
-  t[0] = Elem<kBF16>::from(x);
-  const float r = x - Elem<kBF16>::to(t[0]);
-  const bool fin = (__float_as_uint(r) & 0x7fffffffu) < 0x7f800000u;
-  t[1] = fin ? Elem<kBF16>::from(r) : (uint16_t)0;
-  t[2] = fin ? Elem<kBF16>::from(r - Elem<kBF16>::to(t[1])) : (uint16_t)0;
+// x = h + m + l in bf16, exact, of two values at a time (which is how they are converted: 7.5
+// operations a value, 13 one by one: 33 tokens, 27271 x 7872, 244 us and 293); not finite: the first term alone
+__device__ __forceinline__ void split3(float x, float y, uint32_t (&t)[3]) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    t[p] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{x, y}), bf16x2));
+    if (p == 2) break;
+    x -= __uint_as_float(t[p] << 16);
+    y -= __uint_as_float(t[p] & 0xffff0000u);
+    if (p == 0) {
+      x = fabsf(x) < __builtin_inff() ? x : 0.0f;
+      y = fabsf(y) < __builtin_inff() ? y : 0.0f;
+    }
+  }
 }
 constexpr int score_terms(int D) { return D == kF32 ? 3 : 1; }
 template <int D>
@@ -743,14 +752,13 @@ template <int D>
 __device__ __forceinline__ Frag<D> frag_of(const Raw8<D>& r) {
   Frag<D> f;
   if constexpr (D == kF32) {
-    uint16_t q[8][3];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) split3(r.e[i], q[i]);
+    for (int i = 0; i < 4; ++i) {
+      uint32_t q[3];
+      split3(r.e[2 * i], r.e[2 * i + 1], q);
 #pragma unroll
-    for (int p = 0; p < 3; ++p)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        f.t[p][i] = (uint32_t)q[2 * i][p] | (uint32_t)q[2 * i + 1][p] << 16;
+      for (int p = 0; p < 3; ++p) f.t[p][i] = q[p];
+    }
   } else {
     __builtin_memcpy(&f.t[0], &r, 16);
   }
