@@ -15,7 +15,7 @@
 //   kStat  z of a tile of words x tokens -> per token the largest and the sum
 //          of exponentials over each half of the tile; stat_kernel joins them;
 //   kGrad  z again, G = exp(z - lse) - [label] rounded to the operands' type,
-//          [token][word];
+//          [token][word] (kGradTwo: with a second term in a row of its own);
 //   kDh    dH += G W over the piece (fp32 sums, slices of the piece when
 //          there are few tiles; dh_kernel adds the slices at the end);
 //   kDw    dW = G^T H, the piece's rows.
@@ -227,13 +227,13 @@ hipError_t loss(const Vocab& a, hipStream_t s) {
 template <int D>
 hipError_t backward(const Vocab& a, hipStream_t s) {
   typedef typename Elem<D>::type E;
-  const Plan p = grad_plan(a.T, a.V, a.d, D, a.z);
+  const Plan p = a.share ? distill_plan(a.T, a.V, a.d, D) : plan_for(a.T, a.V, a.d, D, true);
   char* w = (char*)a.work;
   Factors* fac = (Factors*)(w + p.fac);
   uint16_t* G = (uint16_t*)(w + p.G);
   // rows of G, and so of dH's sums, as the products see them: the terms of 16-bit G
   // are rows of their own
-  const int rt = a.z ? kept_rows(a.T, a.V, a.d, D) : g_rows(a.T, a.d, D);
+  const int rt = a.share ? distill_rows(a.T, a.V, a.d, D) : g_rows(a.T, a.d, D);
   const int64_t RT = rt * a.T, gld = p.piece * terms(D);
   const int64_t ldp = round_up(a.d, 4), slice = RT * ldp;
   const bool score_g = few(a.T, a.d, D);
@@ -266,7 +266,13 @@ hipError_t backward(const Vocab& a, hipStream_t s) {
       m.z0 = a.scale;
       m.v0 = v0; m.labels = a.labels; m.lse = a.lse; m.wn = wn;
       m.G = G; m.gld = p.piece;
-      if ((e = mma_launch<D, kGrad>(m, tile_for(nv, a.T), 1, s)) != hipSuccess) return e;
+      m.lines = round_up(RT, BK) / rt;
+      const int tile = tile_for(nv, a.T);
+      if constexpr (D != kF32)
+        e = rt == 1 ? mma_launch<D, kGrad>(m, tile, 1, s) : mma_launch<D, kGradTwo>(m, tile, 1, s);
+      else
+        e = mma_launch<D, kGrad>(m, tile, 1, s);
+      if (e != hipSuccess) return e;
     }
     if (a.listed && !a.z) {
       const dim3 grid((unsigned)((a.T * a.listed + 255) / 256));
@@ -277,7 +283,7 @@ hipError_t backward(const Vocab& a, hipStream_t s) {
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     // (G is zero for words past nv to the next multiple of 64, and from
-    // mma_kernel for tokens past T to the tile's end)
+    // mma_kernel for tokens past T to the tile's end, or to the products' last 64 rows)
     Mma h{}, x{};
     int slices = 0, tile_h = 0, tile_x = 0;
     if (a.dH) {

@@ -45,11 +45,11 @@ inline int g_rows(int64_t T, int64_t d, int dtype) {
   return dtype != kF32 && few(T, d, dtype) ? kFewTerms : 1;
 }
 
-// From kept logits: of up to 192 tokens, where W is most of what takes the
-// time; and where the products are so short that it does not matter (301 tokens, 4999 x 515:
-// two terms take 10 us more of 88). (One term's error of dH and dW, over that of
+// Of a divergence's gradient, from kept logits or from its own: of up to 192 tokens, where W is
+// most of what takes the time; and where the products are so short that it does not matter (301
+// tokens, 4999 x 515: two terms take 10 us more of 88). (One term's error of dH and dW, over that of
 // rounding the exact ones: up to 1.7 with 33 to 65 tokens, 1.56 with 200; with more it nears 2^0.5.)
-inline int kept_rows(int64_t T, int64_t V, int64_t d, int dtype) {
+inline int distill_rows(int64_t T, int64_t V, int64_t d, int dtype) {
   return dtype != kF32 && (T <= 192 || (double)T * V * d <= 536870912.0) ? kFewTerms : 1;
 }
 
@@ -262,12 +262,26 @@ inline FewPlan few_plan(int64_t T, int64_t V, int64_t d, int dtype) {
 inline bool keeps(int64_t T, int64_t V, int64_t d, int dtype) {
   const int64_t n = T * row_of(V);
   const bool pays = d >= (n <= int64_t(1) << 25 || dtype == kF32 ? 256 : 1024);
-  return (few(T, d, dtype) || kept_rows(T, V, d, dtype) > 1 || pays) && n <= int64_t(1) << 30;
+  return (few(T, d, dtype) || distill_rows(T, V, d, dtype) > 1 || pays) && n <= int64_t(1) << 30;
 }
 
-// Of a gradient from kept logits, or without.
-inline Plan grad_plan(int64_t T, int64_t V, int64_t d, int dtype, bool z) {
-  return plan_for(T, V, d, dtype, true, false, z ? kept_rows(T, V, d, dtype) : g_rows(T, d, dtype));
+// Of a divergence's gradient. One plan with and without kept logits: its pieces, and so its bytes,
+// depend on the rows of G, of which more can need less (shorter pieces of W).
+inline Plan distill_plan(int64_t T, int64_t V, int64_t d, int dtype) {
+  return plan_for(T, V, d, dtype, true, false, distill_rows(T, V, d, dtype));
+}
+// What such a gradient needs beside its products' workspace
+struct SharePlan {
+  int64_t labels, share, wr, val, bytes;
+};
+inline SharePlan share_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t K) {
+  SharePlan p;
+  p.labels = round_up(few(T, d, dtype) ? few_plan(T, V, d, dtype).bytes : distill_plan(T, V, d, dtype).bytes, 256);
+  p.share = p.labels + round_up(4 * T, 256);
+  p.wr = p.share + round_up(4 * T, 256);
+  p.val = p.wr + round_up(4 * T, 256);
+  p.bytes = p.val + round_up(4 * T * K, 256);
+  return p;
 }
 
 }  // namespace vocab

@@ -102,7 +102,7 @@ __device__ __forceinline__ float across(float x, F f) {
   return f(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
-enum Epi : int { kStat = 0, kGrad = 1, kDh = 2, kDw = 3, kPick = 4 };
+enum Epi : int { kStat = 0, kGrad = 1, kDh = 2, kDw = 3, kPick = 4, kGradTwo = 5 };
 struct Mma {
   Opnd A, B;                // C (M x N), M = A.rows, N = B.rows
   int64_t K;                // a multiple of 64
@@ -110,13 +110,13 @@ struct Mma {
   const float* zs;          // kStat, kGrad, kPick: the factor of the products (fp32: of each token;
   float z0;                 // 16-bit: z0)
   const float* ws;          // kPick, fp32: and of each word (to the next multiple of 256)
-  // kStat, kGrad: rows are words v0 .., columns tokens
+  // kStat, kGrad, kGradTwo: rows are words v0 .., columns tokens
   int64_t v0;
   const int32_t* labels;
   float *top, *sum, *hit;   // kStat: partials [half tiles of words][N], target logits
   const float *lse, *wn;    // kGrad: lse and normalised dloss per token
-  uint16_t* G;              // kGrad: [token][term][gld]
-  int64_t gld;
+  uint16_t* G;              // kGrad: [token][term][gld]; kGradTwo: two terms of 16 bits, for
+  int64_t gld, lines;       // tokens below lines
   // kDh, kDw: rows are the d columns, columns tokens or words
   float* part;              // kDh: slices of N x ldo fp32
   int64_t slice, ldo;
@@ -627,7 +627,8 @@ __device__ __forceinline__ void mma_body(const Mma a, uint32_t bx, uint32_t by, 
           }
       }
     }
-  } else if constexpr (EPI == kGrad) {
+  } else if constexpr (EPI == kGrad || EPI == kGradTwo) {
+    constexpr int P = EPI == kGradTwo ? kFewTerms : terms(D);
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const int64_t t = c0 + 16 * j;
@@ -635,10 +636,11 @@ __device__ __forceinline__ void mma_body(const Mma a, uint32_t bx, uint32_t by, 
       const float lse = label >= 0 ? a.lse[t] : 0.0f, wn_t = label >= 0 ? a.wn[t] : 0.0f;
       const float zs = D == kF32 ? (label >= 0 ? a.zs[t] : 0.0f) : a.z0;
       const int at = own(label), used = label >= 0 ? left : 0;
-      uint16_t* row = a.G + t * a.gld * terms(D);
+      uint16_t* row = a.G + t * a.gld * P;
+      if (EPI == kGradTwo && t >= a.lines) continue;
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
-        uint16_t q[4][terms(D)];
+        uint16_t q[4][P];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const float y = zs * acc[i][j][v] - lse;
@@ -648,7 +650,7 @@ __device__ __forceinline__ void mma_body(const Mma a, uint32_t bx, uint32_t by, 
           split<D>(x, q[v]);
         }
 #pragma unroll
-        for (int p = 0; p < terms(D); ++p)
+        for (int p = 0; p < P; ++p)
           *(u32x2*)(row + p * a.gld + r0 + 16 * i) =
               u32x2{(uint32_t)q[0][p] | (uint32_t)q[1][p] << 16,
                     (uint32_t)q[2][p] | (uint32_t)q[3][p] << 16};
@@ -1359,11 +1361,11 @@ hipError_t begin(const Vocab& a, const Plan& p, const float* dloss, int rt, Opnd
   const bool dw = dloss && a.dW, score = dloss && (few(a.T, a.d, D) || a.z);
   // (bf16 has one copy for both)
   const bool z = !score && (!direct(a.H, a.ldh, a.d, D) || (D == kBF16 && dw));
-  // (for dW's products with two rows of G per token)
-  const bool twice = score && rt == 2;
+  // (for dW's products with two rows of G per token; z's take every other row)
+  const bool twice = dloss && rt == 2;
   uint16_t* out = (uint16_t*)(w + p.hp);
   const int64_t copy = p.tp * p.dp * terms(D);
-  *Hz = z ? Opnd{out, p.dp * terms(D), p.dp, a.T, p.dp}
+  *Hz = z ? Opnd{out, p.dp * terms(D) << (int)twice, p.dp, a.T, p.dp}
           : Opnd{(const uint16_t*)a.H, a.ldh, 0, a.T, a.d};
   *Hw = Opnd{out + (forms(D) - 1) * copy, p.dp * terms(D), p.dp, a.d, p.tp};
   if (!z && !dw) return hipSuccess;

@@ -787,22 +787,6 @@ hipError_t distill(const Distill& a, hipStream_t s) {
   return hipSuccess;
 }
 
-// What the gradient needs beside its products' workspace
-struct SharePlan {
-  int64_t labels, share, wr, val, bytes;
-};
-SharePlan share_plan(int64_t T, int64_t V, int64_t d, int dtype, int64_t K) {
-  SharePlan p;
-  p.labels = few(T, d, dtype) ? few_plan(T, V, d, dtype).bytes
-                              : grad_plan(T, V, d, dtype, keeps(T, V, d, dtype)).bytes;
-  p.labels = round_up(p.labels, 256);
-  p.share = p.labels + round_up(4 * T, 256);
-  p.wr = p.share + round_up(4 * T, 256);
-  p.val = p.wr + round_up(4 * T, 256);
-  p.bytes = p.val + round_up(4 * T * K, 256);
-  return p;
-}
-
 }  // namespace
 
 int64_t logprobs_work_bytes(int64_t T, int64_t V, int64_t d, int dtype, int64_t given, int64_t k) {
