@@ -46,11 +46,12 @@ inline int g_rows(int64_t T, int64_t d, int dtype) {
 }
 
 // Of a divergence's gradient, from kept logits or from its own: of up to 192 tokens, where W is
-// most of what takes the time; and where the products are so short that it does not matter (301
-// tokens, 4999 x 515: two terms take 10 us more of 88). (One term's error of dH and dW, over that of
+// most of what takes the time; and of short products, whose second term costs tens of microseconds
+// (loss and gradient in us, two terms and one: 301 tokens, 4999 x 515 92 and 81; 1024 tokens, 8000 x 512
+// 128 and 98; at most 300 tokens, 8000 x 1024 122 and 86). (One term's error of dH and dW, over that of
 // rounding the exact ones: up to 1.7 with 33 to 65 tokens, 1.56 with 200; with more it nears 2^0.5.)
 inline int distill_rows(int64_t T, int64_t V, int64_t d, int dtype) {
-  return dtype != kF32 && (T <= 192 || (double)T * V * d <= 536870912.0) ? kFewTerms : 1;
+  return dtype != kF32 && (T <= 192 || (double)T * V * d <= 4294967296.0) ? kFewTerms : 1;
 }
 
 struct Plan {
@@ -258,11 +259,11 @@ inline FewPlan few_plan(int64_t T, int64_t V, int64_t d, int dtype) {
 // and a load (loss and gradient in us, kept and not: 4096 tokens, 131072 words of bf16, d = 4096
 // 11634 and 14254, 1024 4137 and 4245, 512 3092 and 2724; logits that stay in the last-level cache,
 // 1024 tokens, 32000 words, d = 1024 323 and 328, 512 220 and 223, 128 164 and 157; fp32, 4096
-// tokens, 32000 words, d = 512 1652 and 1845, 256 1198 and 1239), or G has two terms.
+// tokens, 32000 words, d = 512 1652 and 1845, 256 1198 and 1239).
 inline bool keeps(int64_t T, int64_t V, int64_t d, int dtype) {
   const int64_t n = T * row_of(V);
   const bool pays = d >= (n <= int64_t(1) << 25 || dtype == kF32 ? 256 : 1024);
-  return (few(T, d, dtype) || distill_rows(T, V, d, dtype) > 1 || pays) && n <= int64_t(1) << 30;
+  return (few(T, d, dtype) || pays) && n <= int64_t(1) << 30;
 }
 
 // Of a divergence's gradient. One plan with and without kept logits: its pieces, and so its bytes,

@@ -180,15 +180,27 @@ def test_a_gradient_that_computes_its_logits_keeps_to_its_workspace(gpu, name, T
 
 @pytest.mark.parametrize("keep", [True, False])
 @pytest.mark.parametrize("name", ["bfloat16", "float16"])
-@pytest.mark.parametrize("T, V, d", [(33, 700, 72), (40, 500, 515), (65, 300, 128), (129, 257, 77), (192, 400, 64)])
+@pytest.mark.parametrize("T, V, d", [(33, 700, 72), (40, 500, 515), (65, 300, 328), (129, 257, 77), (192, 400, 264)])
 def test_16_bit_gradients_have_both_terms_with_and_without_the_logits(gpu, name, T, V, d, keep):
     """33 to 192 tokens, rows in place and copied (d = 77, 515), either result alone: the same bounds."""
     import torch
     print(f"case T={T} V={V} d={d} {name} keep={keep}", flush=True)
     L = Exact(T + V + d, T, V, d, 9, name, gpu).exact()
     loss, q = L.loss(keep=keep)
-    assert (q.logits is None) == (not keep)
+    assert (q.logits is not None) == (keep and d >= 256)
     dH, dW = L.grad(q)
     L.check(dH, dW, 2)
     assert torch.equal(L.grad(q, want_dW=False)[0], dH)
     assert torch.equal(L.grad(q, want_dH=False)[1], dW)
+
+
+@pytest.mark.parametrize("name", ["bfloat16", "float16"])
+@pytest.mark.parametrize("T, V, d", [(300, 500, 4000), (800, 700, 1000), (301, 4999, 515), (2000, 300, 72)])
+def test_short_products_have_both_terms(gpu, name, T, V, d):
+    """More tokens, where T V d is 2^32 at most: what a second term costs is little there."""
+    print(f"case T={T} V={V} d={d} {name}", flush=True)
+    assert T > 192 and T * V * d <= 1 << 32
+    L = Exact(T + V + d, T, V, d, 9, name, gpu).exact()
+    for keep in (True, False):
+        _, q = L.loss(keep=keep)
+        L.check(*L.grad(q), 2)
