@@ -259,11 +259,12 @@ inline FewPlan few_plan(int64_t T, int64_t V, int64_t d, int dtype) {
 // and a load (loss and gradient in us, kept and not: 4096 tokens, 131072 words of bf16, d = 4096
 // 11634 and 14254, 1024 4137 and 4245, 512 3092 and 2724; logits that stay in the last-level cache,
 // 1024 tokens, 32000 words, d = 1024 323 and 328, 512 220 and 223, 128 164 and 157; fp32, 4096
-// tokens, 32000 words, d = 512 1652 and 1845, 256 1198 and 1239).
+// tokens, 32000 words, d = 512 1652 and 1845, 256 1198 and 1239); or, of 16 bits, where there are few of
+// them (150 tokens, 32000 words, d = 128 88 and 93).
 inline bool keeps(int64_t T, int64_t V, int64_t d, int dtype) {
   const int64_t n = T * row_of(V);
   const bool pays = d >= (n <= int64_t(1) << 25 || dtype == kF32 ? 256 : 1024);
-  return (few(T, d, dtype) || pays) && n <= int64_t(1) << 30;
+  return (few(T, d, dtype) || (dtype != kF32 && (T <= 192 || (double)T * V * d <= 536870912.0)) || pays) && n <= int64_t(1) << 30;
 }
 
 // Of a divergence's gradient. One plan with and without kept logits: its pieces, and so its bytes,
