@@ -461,7 +461,8 @@ __device__ __forceinline__ void finish(const Near& a, int64_t t, int lane, Sums 
   const double log_s = log(s);
   double e = 0.0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) e += q.q[i] == 0.0 ? 0.0 : q.q[i] * (q.logq[i] - ((double)z[i] - m) + log_s);
+  for (int i = 0; i < 2; ++i)   // (a word past the last has its NaN without any mass, too)
+    e += q.q[i] == 0.0 ? (z[i] == z[i] ? 0.0 : (double)kNaN) : q.q[i] * (q.logq[i] - ((double)z[i] - m) + log_s);
   double loss = wave_sum(e);
   const double rest = a.tail ? (double)r.m + log1p((double)r.r) : m + log_s;
   // (without a rest there is none to be off from)
