@@ -455,7 +455,9 @@ __device__ __forceinline__ void finish(const Near& a, int64_t t, int lane, Sums 
   if (a.tail) {
     m = wave_max(fmax(part[0] ? (double)x[0] : -INFINITY, part[1] ? (double)x[1] : -INFINITY));
     m = fmax(m, (double)r.m);
-    s = wave_sum((part[0] ? exp((double)x[0] - m) : 0.0) + (part[1] ? exp((double)x[1] - m) : 0.0));
+    // (a listed z of -infinity is no zero but NaN, as in the groups' sums)
+    auto e = [&](int i) { return !part[i] ? 0.0 : x[i] == kNegInf ? (double)kNaN : exp((double)x[i] - m); };
+    s = wave_sum(e(0) + e(1));
     if (!all) s += (1.0 + (double)r.r) * exp((double)r.m - m);
   }
   const double log_s = log(s);
@@ -471,7 +473,7 @@ __device__ __forceinline__ void finish(const Near& a, int64_t t, int lane, Sums 
   for (int i = 0; i < 2; ++i)
     if (lane + 64 * i < a.K) a.hit[t * a.K + lane + 64 * i] = z[i];
   if (lane == 0) {
-    a.loss[t] = used ? (float)loss : 0.0f;
+    a.loss[t] = !used ? 0.0f : log_s == log_s ? (float)loss : kNaN;
     a.lse[t] = used ? (float)(m + log_s) : 0.0f;
     a.rest[t] = used ? (float)rest : 0.0f;
   }
