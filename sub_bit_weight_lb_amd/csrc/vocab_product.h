@@ -607,7 +607,9 @@ __device__ __forceinline__ void mma_body(const Mma a, uint32_t bx, uint32_t by, 
         sums(std::false_type{});
       if (!used) continue;
       if (g == 0) {
-        o.stat[t * o.groups + group] = f32x4{top * zs, dot == dot ? r : __uint_as_float(0x7fc00000u), dot * 0.69314718f, 0.0f};
+        // (the largest z past fp32's range, of a finite acc: not finite either, unless there is no word)
+        const bool fine = dot == dot && (fabsf(top * zs) < __builtin_inff() || r == -1.0f);
+        o.stat[t * o.groups + group] = f32x4{top * zs, fine ? r : __uint_as_float(0x7fc00000u), dot * 0.69314718f, 0.0f};
         if (o.tops) {
           float* p = o.tops + (t * o.groups + group) * PARTS;
 #pragma unroll

@@ -62,3 +62,30 @@ def test_a_listed_logit_of_minus_infinity(gpu, name, T, mass, tail):
     assert q.lse.isnan().all() and loss.isnan().all()
     dH, dW = L.grad(q)
     assert dH.isnan().all() and dW.isnan().all()
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("T", [4, 70, 300])
+def test_logits_that_their_scale_takes_past_fp32(gpu, T, sign):
+    """Sums that are finite, and not after their scale: a vocabulary of one group, and one of several of
+    which one is past the type's lowest value."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    for V, first in ((20, 0), (300, 0), (300, 256)):
+        W = torch.zeros((V, 64), device=gpu)
+        W[first:first + 128, 0] = sign * 2.0 ** 20
+        W[0, 1] = 1.0
+        Hh = torch.zeros((T, 64), device=gpu)
+        Hh[0, 0] = 2.0 ** 20
+        Hh[1, 1] = 2.0 ** -100
+        Hh, W = Hh.bfloat16(), W.bfloat16()
+        ids = torch.full((T, 2), V - 1, dtype=torch.int32, device=gpu)
+        r = nq.vocab_logprobs(Hh, W, ids, 3, scale=2.0 ** 100)
+        assert r.lse[0].isnan() and r.entropy[0].isnan() and r.logprobs[0].isnan().all()
+        assert r.top_logprobs[0].isnan().all() and (r.top_ids[0] == -1).all()
+        assert torch.isfinite(r.lse[1:]).all() and torch.isfinite(r.entropy[1:]).all() and (r.top_ids[1:] >= 0).all()
+        for tail in (True, False):
+            for keep in (True, False):
+                logq = torch.full((T, 2), -2.0, device=gpu)
+                loss, q = nq.vocab_distill(Hh, W, ids, logq, scale=2.0 ** 100, tail=tail, keep=keep)
+                assert loss[0].isnan() and q.lse[0].isnan() and torch.isfinite(loss[1:]).all()
