@@ -107,7 +107,8 @@ struct Vocab {
   int64_t lddh, lddw;
   void* work;                        // vocab_work_bytes, 16-byte aligned
   // a gradient whose G is exp(z - lse) share dloss scale, but val dloss scale at the
-  // `listed` words of each token (0: none; a negative one: no entry); wr: T, scratch
+  // `listed` words of each token (0: none; a negative one: no entry); |G| <= wr dloss scale, wr: T,
+  // overwritten
   const float* share;
   float* wr;
   const int32_t* ids;

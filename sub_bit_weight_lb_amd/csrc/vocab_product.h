@@ -1090,6 +1090,8 @@ __device__ __forceinline__ int power_for(float m) {
 //   fp16:       as fp32, but G keeps up to kInG bits of x - x0: it has 29 below its
 //               top, of which 11 are asked for, where H, which is not scaled to its
 //               type's top, has 14 where it is about 1.
+// Where G is a divergence's, of up to Q in place of 1 (rows.wr; 1 for a teacher's probabilities), a
+// token of Q >= 1.5 has the power of two above Q in its dloss, not in G.
 // (0 for an ignored token; NaN for a label at or past V.) hm and parts (fp32
 // operands): the maxima of H's rows and of W. One workgroup.
 constexpr int kInG = 10;
@@ -1115,10 +1117,19 @@ __global__ __launch_bounds__(1024) void factors_kernel(const float* __restrict__
     if (threadIdx.x == 0) out->mw = ldexpf(1.0f, ew);
     return;
   }
+  // the power of two that token t's G is taken down by
+  auto down = [&](int64_t t) {
+    int x = 0;
+    if (D != kBF16 && share) {
+      const float q = rows.wr[t];
+      if (q >= 1.5f && q < __builtin_inff()) frexpf(q, &x);
+    }
+    return x;
+  };
   // the largest of the finite ones
   float m = 0.0f;
   for (int64_t t = threadIdx.x; t < T; t += 1024) {
-    const float v = labels[t] >= 0 ? fabsf(dloss[t]) : 0.0f;
+    const float v = labels[t] >= 0 ? ldexpf(fabsf(dloss[t]), down(t)) : 0.0f;
     m = v < __builtin_inff() ? fmaxf(m, v) : m;
   }
   m = max_of(m, sm);
@@ -1128,7 +1139,10 @@ __global__ __launch_bounds__(1024) void factors_kernel(const float* __restrict__
   auto parted = [&](int64_t t, int& x) {
     x = x0;
     const float l = dloss[t];
-    return l != 0.0f && fabsf(l) < __builtin_inff() ? frexpf(l, &x) : l;
+    if (l == 0.0f || !(fabsf(l) < __builtin_inff())) return l;
+    const float f = frexpf(l, &x);
+    x += down(t);
+    return f;
   };
   // fp32: H's copy for dW, weighted by 2^(x - x0), to 2^15 at its largest
   int eh = 0;
@@ -1150,7 +1164,7 @@ __global__ __launch_bounds__(1024) void factors_kernel(const float* __restrict__
       int x;
       const float f = parted(t, x);
       const int k = D == kF16 ? min(x0 - x, kInG) : 0;
-      wn = ldexpf(f, 15 - k);
+      wn = ldexpf(f, 15 - k - down(t));
       pt = ldexpf(scale, x + k - 15 - ew);
       hw = f == 0.0f ? 0.0f : ldexpf(1.0f, x + k - x0 + eh);
     }

@@ -53,11 +53,11 @@ __device__ __forceinline__ Teacher teacher(const float (&l)[2], const bool (&on)
 }
 
 // What the gradient needs of token t: its label (the first word listed; V where one is at or past V;
-// -1 without any), its share, its entries' words and val (struct Vocab). By one wave, entries lane and
+// -1 without any), its share, its entries' words and val (struct Vocab), Q = sum q + r. By one wave, entries lane and
 // lane + 64; word, q: kList each in LDS, of this wave alone.
 struct Share {
   int32_t label;
-  float share, val[2];
+  float share, val[2], whole;   // whole: Q
 };
 struct Taught {
   const int32_t* ids;
@@ -97,6 +97,7 @@ __device__ __forceinline__ Share share_of(const Taught& a, int64_t t, int lane, 
   const int first = some[0] ? __ffsll((unsigned long long)some[0]) - 1 : 63 + __ffsll((unsigned long long)some[1]);
   const bool used = some[0] || some[1];
   s.label = !used ? -1 : past ? (int32_t)a.V : word[first];
+  s.whole = (float)whole;
   s.share = used ? (float)(a.tail ? whole * exp(out - e) - r : whole) : 0.0f;
   return s;
 }

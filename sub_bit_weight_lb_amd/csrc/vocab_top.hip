@@ -602,10 +602,11 @@ __global__ __launch_bounds__(NT) void distill_few_kernel(Near a) {
   finish(a, t, lane, r, on, z, x, part);
 }
 
-// Labels, shares and val (struct Vocab) of the gradient. Four tokens per workgroup, a wave each.
+// Labels, shares, val (struct Vocab) and Q of the gradient. Four tokens per workgroup, a wave each.
 // 4096 tokens of 64 words: 9 us.
 __global__ __launch_bounds__(256) void shares_kernel(Taught a, int64_t T, int32_t* __restrict__ labels,
-                                                     float* __restrict__ share, float* __restrict__ val) {
+                                                     float* __restrict__ share, float* __restrict__ whole,
+                                                     float* __restrict__ val) {
   __shared__ int word[4][kList];
   __shared__ double q[4][kList];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -618,6 +619,7 @@ __global__ __launch_bounds__(256) void shares_kernel(Taught a, int64_t T, int32_
   if (lane == 0) {
     labels[t] = s.label;
     share[t] = s.share;
+    whole[t] = s.whole;
   }
 }
 
@@ -834,7 +836,8 @@ hipError_t launch_vocab_distill_backward(const Distill& a, hipStream_t s) {
     return launch_few_gradient(g, s);
   }
   float *share = (float*)(w + p.share), *val = (float*)(w + p.val);
-  hipLaunchKernelGGL(shares_kernel, dim3((unsigned)((v.T + 3) / 4)), dim3(256), 0, s, of, v.T, labels, share, val);
+  hipLaunchKernelGGL(shares_kernel, dim3((unsigned)((v.T + 3) / 4)), dim3(256), 0, s, of, v.T, labels, share,
+                     (float*)(w + p.wr), val);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   v.share = share;

@@ -130,7 +130,8 @@ class Exact:
         import torch
         h = half(self.name)
         more = 2.0 ** -21 if self.name == "float32" else h if terms == 1 else 2 * h * h
-        big = float((self.dl.abs() * self.used).max()) * abs(self.scale)
+        whole = self.q.sum(1) + self.r        # (G is scaled by it where it is more than 1)
+        big = float((self.dl.double().abs() * self.used * torch.where(whole < 1.5, 1.0, 2 * whole)).max()) * abs(self.scale)
         eG = self.eG + (more + 2 * U) * self.G.abs()
         if self.name != "bfloat16":
             eG = eG + 2.0 ** -38 * big

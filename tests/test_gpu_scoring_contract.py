@@ -89,3 +89,22 @@ def test_logits_that_their_scale_takes_past_fp32(gpu, T, sign):
                 logq = torch.full((T, 2), -2.0, device=gpu)
                 loss, q = nq.vocab_distill(Hh, W, ids, logq, scale=2.0 ** 100, tail=tail, keep=keep)
                 assert loss[0].isnan() and q.lse[0].isnan() and torch.isfinite(loss[1:]).all()
+
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("T, V, d", [(5, 500, 72), (70, 500, 72), (300, 2049, 136), (1100, 3000, 40)])
+def test_lists_of_more_than_all_mass(gpu, name, T, V, d):
+    """Log probabilities whose sum is far above one, with a tail: there is no rest of them, and the gradient is
+    the formula's, beside tokens whose lists are ordinary."""
+    import torch
+    L = Exact(T + 1, T, V, d, 9, name, gpu)
+    L.logq[::2] += 5.0
+    L.logq[1::4] += 0.5
+    if T > 5:
+        L.logq[7] += 11.0
+    L.dl[5::7] *= 2.0 ** -6
+    L.exact()
+    loss, q = L.loss()
+    L.check_loss(loss, q)
+    for state in (q, L.loss(keep=False)[1]):
+        L.check(*L.grad(state), 2)
