@@ -205,3 +205,20 @@ def test_short_products_have_both_terms(gpu, name, T, V, d):
     for keep in (True, False):
         _, q = L.loss(keep=keep)
         L.check(*L.grad(q), 2)
+
+
+# ---------------------------------------------------------------- large sizes
+
+@pytest.mark.parametrize("name, T, keep", [("bfloat16", 40, True), ("bfloat16", 40, False), ("float16", 200, True),
+                                           ("float16", 200, False), ("float32", 70, True), ("float32", 70, False),
+                                           ("float32", 5, True)])
+def test_a_hidden_size_that_takes_the_vocabulary_in_pieces(gpu, name, T, keep):
+    """Each of the pieces in which W is copied shows in dH, and words of all of them in dW."""
+    V, d = 5000, 33001
+    print(f"case T={T} {name} keep={keep}", flush=True)
+    L = Exact(11, T, V, d, 30, name, gpu).exact()
+    loss, q = L.loss(keep=keep)
+    assert (q.logits is not None) == keep
+    L.check_loss(loss, q)
+    dH, dW = L.grad(q)
+    L.check(dH, dW, 1 if T == 200 else 2, pieces=[(0, 1792), (1792, 3584), (3584, V)])
