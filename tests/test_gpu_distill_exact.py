@@ -222,3 +222,24 @@ def test_a_hidden_size_that_takes_the_vocabulary_in_pieces(gpu, name, T, keep):
     L.check_loss(loss, q)
     dH, dW = L.grad(q)
     L.check(dH, dW, 1 if T == 200 else 2, pieces=[(0, 1792), (1792, 3584), (3584, V)])
+
+
+@pytest.mark.parametrize("T, tail", [(3, True), (3, False), (70, True), (70, False), (300, True)])
+def test_gradients_of_a_vocabulary_past_32_bits(gpu, T, tail):
+    """W of more than 2^32 bytes: dW's first and last words, the first and last columns of both, and the
+    words past 2^31 and 2^32 bytes in dH."""
+    V, d = 140001, 16384
+    first = [(1 << n) // (2 * d) for n in (31, 32)]
+    print(f"case T={T} tail={tail}", flush=True)
+    L = Exact(6, T, V, d, 4, "bfloat16", gpu, tail=tail)
+    L.ids[1, 1:3] = L.ids.new_tensor(first) + 7
+    L.exact()
+    loss, q = L.loss()
+    L.check_loss(loss, q)
+    terms = 2 if T <= 192 else 1
+    for state, cols in ((q, slice(0, 64)), (q, slice(d - 64, d)), (L.loss(keep=False)[1], slice(d - 64, d))):
+        dH, dW = L.grad(state)
+        for rows in (slice(0, 200), slice(first[0] - 100, first[0] + 100), slice(first[1] - 100, first[1] + 100),
+                     slice(V - 200, V)):
+            L.check(None, dW, terms, rows=rows, cols=cols)
+        L.check(dH, None, terms, cols=cols, pieces=[(0, first[0]), (first[0], first[1]), (first[1], V)])
