@@ -108,3 +108,64 @@ def test_lists_of_more_than_all_mass(gpu, name, T, V, d):
     L.check_loss(loss, q)
     for state in (q, L.loss(keep=False)[1]):
         L.check(*L.grad(state), 2)
+
+
+def tied(V, T, gpu):
+    """W and hidden states on a grid: rows whose logits are all equal, equal but for a few better ones at either
+    end or all over, in two, three and nine values, rising and falling in long runs."""
+    import torch
+    W = torch.zeros((V, 64), device=gpu)
+    v = torch.arange(V, device=gpu)
+    W[:, 0] = (v % 2).float()
+    W[:, 1] = (v % 3).float()
+    W[:, 2] = (v * 7919 % 9).float()
+    W[:, 3] = (v // 1024 % 128).float()
+    W[:11, 4] = 1.0
+    W[-11:, 5] = 1.0
+    W[::997, 6] = 1.0
+    W[V // 2:, 7] = 1.0
+    Hh = torch.zeros((T, 64), device=gpu)
+    for t in range(T):
+        n = t % 17
+        if n:
+            Hh[t, (n - 1) // 2] = 1.0 if n % 2 else -1.0
+    return Hh, W
+
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("T, V", [(17, 131072), (40, 131072), (90, 50021), (600, 130001)])
+def test_best_words_of_rows_with_many_equal_logits(gpu, name, T, V):
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    Hh, W = tied(V, T, gpu)
+    z = Hh[:17].double() @ W.double().t()
+    ids = torch.sort(z, dim=1, descending=True, stable=True).indices
+    for k in (1, 20, 128):
+        r = nq.vocab_logprobs(Hh.to(dt(name)), W.to(dt(name)), k=k)
+        for a in range(0, T, 17):
+            assert torch.equal(r.top_ids[a:a + 17].long(), ids[:len(r.top_ids[a:a + 17]), :k])
+
+
+def test_rows_of_padding_take_no_longer(gpu):
+    """Hidden states of zeros, whose logits are all equal, against random ones: a few rounds of the search more,
+    not one for every few hundred words (8 times the time allowed; 45 were taken)."""
+    import torch
+    import sub_bit_weight_lb_amd as nq
+    g = torch.Generator(device=gpu).manual_seed(8)
+    W = torch.randn((131072, 1024), generator=g, device=gpu).bfloat16()
+    Hh = torch.randn((1, 1024), generator=g, device=gpu).bfloat16()
+
+    def least(h):
+        out = []
+        for _ in range(8):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(5):
+                nq.vocab_logprobs(h, W, k=20)
+            b.record()
+            torch.cuda.synchronize()
+            out.append(a.elapsed_time(b))
+        return min(out)
+
+    random = least(Hh)
+    assert least(torch.zeros_like(Hh)) <= 8 * random
