@@ -48,10 +48,13 @@ inline int g_rows(int64_t T, int64_t d, int dtype) {
 // Of a divergence's gradient, from kept logits or from its own: of up to 192 tokens, where W is
 // most of what takes the time; and of short products, whose second term costs tens of microseconds
 // (loss and gradient in us, two terms and one: 301 tokens, 4999 x 515 92 and 81; 1024 tokens, 8000 x 512
-// 128 and 98; at most 300 tokens, 8000 x 1024 122 and 86). (One term's error of dH and dW, over that of
-// rounding the exact ones: up to 1.7 with 33 to 65 tokens, 1.56 with 200; with more it nears 2^0.5.)
+// 128 and 98; 300 tokens, 8000 x 1024 122 and 86; 1000 tokens, 32000 x 128 194 and 146). (One term's error
+// of dH and dW, over that of rounding the exact ones: up to 1.7 with 33 to 65 tokens, 1.56 with 200; with
+// more it nears 2^0.5, so very many tokens have two only where that is next to nothing: 131072 tokens,
+// 128 x 256 2200 and 1500.)
 inline int distill_rows(int64_t T, int64_t V, int64_t d, int dtype) {
-  return dtype != kF32 && (T <= 192 || (double)T * V * d <= 4294967296.0) ? kFewTerms : 1;
+  const double n = (double)T * V * d;
+  return dtype != kF32 && (T <= 192 || n <= (T <= 4096 ? 4294967296.0 : 536870912.0)) ? kFewTerms : 1;
 }
 
 struct Plan {
