@@ -508,8 +508,8 @@ int64_t nq_vocab_logprobs_work_bytes(int64_t T, int64_t V, int64_t d, int32_t dt
  * a negative one is no entry, a token without entries is ignored. logq (device
  * float32, T x K, row stride ldq): log probabilities, -infinity allowed. With lse_t
  * = log sum_v exp z_tv:
- *   tail != 0: q = exp logq, of which sum q <= 1 is expected; what is left, r = max(0,
- *     1 - sum q), is one outcome, "another word", of probability exp(rest - lse),
+ *   tail != 0: q = exp logq, of which sum q <= 1 is expected (of more, loss and gradient are
+ *     the formulas' with r = 0); what is left, r = max(0, 1 - sum q), is one outcome, "another word", of probability exp(rest - lse),
  *     rest_t = log sum exp z_tv over the words that the token does not list:
  *     loss_t = sum_k q_k (logq_k - z_t,ids[k] + lse_t) + r (log r - rest_t + lse_t);
  *     where every word is listed, rest is -infinity and r counts as 0;
@@ -520,8 +520,8 @@ int64_t nq_vocab_logprobs_work_bytes(int64_t T, int64_t V, int64_t d, int32_t dt
  * entries' terms. loss, lse, rest (T) and hit (T x K: z of each entry, 0 for none) are
  * device float32, lse, rest and hit for the gradient. An ignored token has 0 in all
  * of them and its row of H is not used; one with a word >= V has NaN in loss and in
- * that hit; a logit that is not finite gives NaN in its token's loss and lse. K in 1 ..
- * 128. work: nq_vocab_distill_work_bytes(T, V, d, dtype, K, 0) bytes, 16-byte
+ * that hit, whatever its logq; a logit that is not finite gives NaN in its token's loss and lse,
+ * listed or not. K in 1 .. 128. work: nq_vocab_distill_work_bytes(T, V, d, dtype, K, 0) bytes, 16-byte
  * aligned. All on `stream`, no allocation; sums run in a fixed order. T == 0 is a no-op. */
 nq_status nq_vocab_distill(const void* H, int64_t ldh, const void* W, int64_t ldw, int32_t dtype,
                            int64_t T, int64_t V, int64_t d, const int32_t* ids, int64_t ldi,
@@ -531,7 +531,8 @@ nq_status nq_vocab_distill(const void* H, int64_t ldh, const void* W, int64_t ld
 
 /* Number of float32 in `logits` of the call above, which the gradient can take to compute them
  * only once: T rows of V to the next multiple of 128, 16-byte aligned (what lies behind V is
- * written too), or NULL for none. 0 where they are not kept (a hidden size so small that they cost
+ * written too), or NULL for none, as for a loss without a gradient; a gradient has the same roundings
+ * without them. 0 where they are not kept (a hidden size so small that they cost
  * more than they save, or more than 2^30 of them: a pointer given is ignored). Host only; -1 for
  * sizes out of range. */
 int64_t nq_vocab_distill_logits(int64_t T, int64_t V, int64_t d, int32_t dtype);
@@ -539,7 +540,9 @@ int64_t nq_vocab_distill_logits(int64_t T, int64_t V, int64_t d, int32_t dtype);
 /* Gradient of sum_t dloss_t loss_t from the lse, rest and hit of nq_vocab_distill on the
  * same arguments and in one call, and its logits where they were kept (NULL: computed
  * again). Of more than 32 tokens (float32: 64), or d < 8, the products, roundings and limits
- * are those of nq_vocab_loss_backward; fewer have all but the results in float32. With Q = sum q + r (1 where tail == 0),
+ * are those of nq_vocab_loss_backward, but that a 16-bit G has two terms, as good as exact, of up to 192
+ * tokens and of short products (T V d <= 2^32, of more than 4096 tokens 2^29); fewer tokens have
+ * all but the results in float32. With Q = sum q + r (1 where tail == 0),
  *   G_tv = (Q exp(z_tv - lse_t) - sum of q over v's entries) dloss_t scale, v listed,
  *   G_tv = exp(z_tv - rest_t) (Q exp(rest_t - lse_t) - r) dloss_t scale, v not listed,
  *   dH (T x d, row stride lddh) = G W,   dW (V x d, row stride lddw) = G^T H

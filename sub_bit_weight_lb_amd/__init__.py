@@ -821,9 +821,10 @@ def vocab_distill(H, W, ids, logq, scale=1.0, tail=True, keep=True, loss=None, s
     outcome more, "another word"; without it logq is normalised over a token's
     entries (and may be logits). Returns (loss, state): T float32, 0 for an ignored
     token, and the VocabDistill that vocab_distill_backward takes (keep: with the
-    logits, where it pays); both can be given to be filled. A word >= V gives NaN;
-    one listed twice counts with both entries; without tail, a row of nothing but
-    -infinity has no softmax and gives NaN. work, if given, holds vocab_distill_work_bytes(T, V, d, H.dtype, K) bytes."""
+    logits, up to 4 GiB, where that saves the gradient more time than their store costs;
+    keep=False for a loss without a gradient); both can be given to be filled. A word
+    >= V gives NaN; one listed twice counts with both entries; without tail, a row of
+    nothing but -infinity has no softmax and gives NaN. work, if given, holds vocab_distill_work_bytes(T, V, d, H.dtype, K) bytes."""
     torch = _torch()
     f32 = torch.float32
     T, V, d, code, ldh, ldw, K, ldi, ldq = _distill_args(H, W, ids, logq)
@@ -859,7 +860,7 @@ def vocab_distill_backward(H, W, ids, logq, state, dloss, scale=1.0, tail=True, 
     """Gradient of sum(dloss * loss) for (loss, state) = vocab_distill(H, W, ids,
     logq, scale, tail) of one call with these tokens: returns (dH, dW) in H's type
     (None where not wanted). dloss is T float32. Where state has no logits they are
-    computed again, in pieces of the vocabulary. Ignored tokens get zero rows of dH and add nothing to
+    computed again, in pieces of the vocabulary, with the same roundings. Ignored tokens get zero rows of dH and add nothing to
     dW. Outputs must not share memory with inputs. work, if given, holds
     vocab_distill_work_bytes(T, V, d, H.dtype, K, grad=True) bytes."""
     torch = _torch()

@@ -27,7 +27,7 @@
 // Types: bf16 and fp16 operands are exact and sums are fp32. 16-bit G of more than 32
 // tokens is rounded to the operands' type once: half a unit, like the results
 // (relative to the exact gradient 0.0017 for the plain form, 0.0018 to 0.0019 here in
-// bf16); of fewer it has two terms (g_rows). bf16's G holds (p - [label]) dloss of the
+// bf16); of fewer it has two terms (g_rows), and a divergence's of more (distill_rows). bf16's G holds (p - [label]) dloss of the
 // largest dloss 1; fp16's and fp32's hold p - [label] of each token to 2^15,
 // whatever the others' dloss (fp16: with dloss to 2^-10 of the largest), so that
 // probabilities down to 2^-29 keep all their bits. fp32 operands are scaled by powers

@@ -6,7 +6,9 @@
 // four tokens, which are loads of whole lines from row-major W, G and H. So no copies, scales or
 // terms (the 16-bit products of vocab_product.h would need W's columns gathered and G in two
 // terms), and G keeps all its bits. Its rate, 256 operations per CU and cycle, is the
-// bandwidth's with 32 tokens of a 16-bit W or 64 of an fp32 one.
+// bandwidth's with 32 tokens of a 16-bit W or 64 of an fp32 one; there both take their share:
+//   32000 x 2048 fp32, us, dH and dW (262 MB each, 53): 16 tokens 44 and 48, 64 tokens 131 and 166
+//   (the products alone 55 at the library's fp32 rate).
 //   32000 x 4096 bf16, 1 token, loss and gradient: 214 us, 333 with the 16-bit products. dH 54 us and
 //   dW 51, 262 MB each: 4.9 and 5.1 TB/s.
 #include "tune.h"
